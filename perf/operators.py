@@ -154,7 +154,8 @@ def _values(dev):
 def _quantise(x, descale):
     """Codes, one a byte, and e4m3 scales of fp32 x [..., d]."""
     b = x.unflatten(-1, (-1, 16))
-    s = (b.abs().amax(-1) / (6.0 * descale)).clamp(max=448.0).to(torch.float8_e4m3fn)
+    # a tensor as the divisor: by a plain number torch multiplies with the reciprocal, one rounding more
+    s = (b.abs().amax(-1) / torch.full((), 6.0 * descale, device=x.device)).clamp(max=448.0).to(torch.float8_e4m3fn)
     f = s.float().unsqueeze(-1) * descale
     y = torch.where(f > 0, b.abs() / f, torch.zeros_like(b))
     code = ((y > .25).to(torch.uint8) + (y >= .75) + (y > 1.25) + (y >= 1.75) + (y > 2.5) + (y >= 3.5) + (y > 5.0))
