@@ -524,6 +524,245 @@ fa_status_t fa_decode_paged(const fa_bf16_t* q, const fa_bf16_t* k_cache,
   return FA_OK;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Shape and pages of the paged-cache calls.  ``granule``: the block size must be a multiple of it.
+fa_status_t check_paged(int n_seqs, int H, int H_kv, int d, int max_blocks_per_seq, int block_size,
+                        int num_blocks, int granule) {
+  if (n_seqs < 1 || H_kv < 1 || H < 0)
+    return fail(FA_ERR_INVALID_ARG, "n_seqs and H_kv must be >= 1 and H >= 0 (got %d, %d, %d)", n_seqs, H_kv, H);
+  if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED, "head dim d=%d not supported (64 or 128)", d);
+  if (num_blocks < 1 || max_blocks_per_seq < 1)
+    return fail(FA_ERR_INVALID_ARG, "num_blocks and max_blocks_per_seq must be >= 1 (got %d, %d)",
+                num_blocks, max_blocks_per_seq);
+  if (block_size < granule || block_size % granule != 0)
+    return fail(FA_ERR_UNSUPPORTED, "block_size must be a positive multiple of %d (got %d)", granule, block_size);
+  const long long rows = static_cast<long long>(num_blocks) * block_size;
+  if (rows >= (1LL << 31) || rows * H_kv >= (1LL << 31))
+    return fail(FA_ERR_UNSUPPORTED, "num_blocks * block_size * H_kv must be < 2^31");
+  if (static_cast<long long>(max_blocks_per_seq) * block_size >= (1LL << 31))
+    return fail(FA_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size must be < 2^31");
+  return FA_OK;
+}
+
+fa_status_t check_descale(float descale) {
+  // 6 * descale and 448 * descale are formed in fp32
+  if (!std::isfinite(descale) || !(descale >= 1e-30f) || !(descale <= 1e30f))
+    return fail(FA_ERR_INVALID_ARG, "descale factors must be in [1e-30, 1e30] (got %g)", static_cast<double>(descale));
+  return FA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+fa_status_t check_index_arrays(const int* a, const int* b, const int* c) {
+  if (!a || !b || !c) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned4(a) || !aligned4(b) || !aligned4(c))
+    return fail(FA_ERR_INVALID_ARG, "block_table, seqlens_k and cu_seqlens must be 4-byte aligned");
+  return FA_OK;
+}
+
+fa_status_t append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* k_scales,
+                   void* v_cache, void* v_scales, bool q4, const float* cos, const float* sin, const int* cu,
+                   const int* seqlens, const int* table, int n_seqs, int H, int H_kv, int total,
+                   long long q_stride, long long k_stride, long long v_stride, int max_blocks, int block_size,
+                   int num_blocks, int d, int rotary, int interleaved, int n_positions, float descale_k,
+                   float descale_v, void* stream, const char* name) {
+  fa_status_t st = check_paged(n_seqs, H, H_kv, d, max_blocks, block_size, num_blocks, q4 ? 16 : 1);
+  if (st != FA_OK) return st;
+  if (total < 0) return fail(FA_ERR_INVALID_ARG, "total must be >= 0 (got %d)", total);
+  if (rotary < 0 || rotary > d || rotary % 32 != 0)
+    return fail(FA_ERR_UNSUPPORTED, "rotary_dim must be a multiple of 32 in [0, d] (got %d)", rotary);
+  if (interleaved != 0 && interleaved != 1)
+    return fail(FA_ERR_INVALID_ARG, "interleaved must be 0 or 1 (got %d)", interleaved);
+  if (q && H < 1) return fail(FA_ERR_INVALID_ARG, "H must be >= 1 with queries (got %d)", H);
+  if (!q) H = 0;
+  if (q4) {
+    if ((st = check_descale(descale_k)) != FA_OK || (st = check_descale(descale_v)) != FA_OK) return st;
+  }
+  // one warp per 32 lanes of a token's heads: the warps are counted in an int
+  const long long warps = (static_cast<long long>(H) + 2LL * H_kv + 1) * total;
+  if (warps >= (1LL << 31)) return fail(FA_ERR_UNSUPPORTED, "total * (H + 2 H_kv) must be < 2^31");
+  if (total == 0) return FA_OK;
+  if (!k || !v || !k_cache || !v_cache || (q4 && (!k_scales || !v_scales)) || (q && !q_out) ||
+      (rotary > 0 && (!cos || !sin)))
+    return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  if ((st = check_index_arrays(cu, seqlens, table)) != FA_OK) return st;
+  if (rotary > 0 && n_positions < 1) return fail(FA_ERR_INVALID_ARG, "n_positions must be >= 1 (got %d)", n_positions);
+  for (const void* x : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
+                        static_cast<const void*>(v_cache), static_cast<const void*>(k_scales),
+                        static_cast<const void*>(v_scales), static_cast<const void*>(rotary ? cos : nullptr),
+                        static_cast<const void*>(rotary ? sin : nullptr)})
+    if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  const long long need[3] = {static_cast<long long>(H) * d, static_cast<long long>(H_kv) * d, static_cast<long long>(H_kv) * d};
+  const long long have[3] = {q_stride, k_stride, v_stride};
+  for (int i = q ? 0 : 1; i < 3; ++i)
+    if ((total > 1 && have[i] < need[i]) || have[i] < 0 || have[i] % 8 != 0 || have[i] >= (1LL << 40))
+      return fail(FA_ERR_INVALID_ARG, "token strides must be multiples of 8 elements of at least a token's heads (got %lld)", have[i]);
+  fa::AppendArgs a{};
+  a.q = q; a.k = k; a.v = v; a.q_out = q_out; a.k_cache = k_cache; a.v_cache = v_cache;
+  a.k_scales = static_cast<uint8_t*>(k_scales); a.v_scales = static_cast<uint8_t*>(v_scales);
+  a.cos = cos; a.sin = sin; a.cu = cu; a.seqlens = seqlens; a.block_table = table;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.n_seqs = n_seqs; a.H = H; a.H_kv = H_kv; a.total = total; a.max_blocks = max_blocks;
+  a.block_size = block_size; a.num_blocks = num_blocks; a.d = d; a.rotary = rotary;
+  a.interleaved = interleaved; a.n_positions = n_positions; a.descale_k = descale_k; a.descale_v = descale_v;
+  cudaError_t e = fa::launch_append(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
+}
+
+// Split count of a 4-bit attention call (n_splits <= 0: the library's choice), or an error.
+fa_status_t q4_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int* n_splits) {
+  const long long items = static_cast<long long>(n_seqs) * H_kv * fa::q4_row_blocks(H, H_kv, max_seqlen_q);
+  if (*n_splits > fa::kDecodeMaxSplits)
+    return fail(FA_ERR_UNSUPPORTED, "n_splits=%d exceeds %d", *n_splits, fa::kDecodeMaxSplits);
+  if (*n_splits <= 0) *n_splits = fa::q4_auto_splits(items, max_seqlen_k);
+  if (items >= (1LL << 31) || items * 2 * *n_splits >= (1LL << 31))
+    return fail(FA_ERR_UNSUPPORTED, "too many (sequence, key head, row block, split) items");
+  return FA_OK;
+}
+
+size_t q4_workspace(int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q, int max_seqlen_k, int d, int n_splits) {
+  if (n_seqs < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
+      (d != 64 && d != 128) || static_cast<long long>(total_q) * H >= (1LL << 31))
+    return 0;
+  if (q4_splits(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k, &n_splits) != FA_OK) return 0;
+  return n_splits == 1 ? 16 : fa::decode_part_bytes(total_q, H, d, n_splits);
+}
+
+fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, const void* v_codes,
+                      const void* v_scales, void* o, float* lse, const int* cu_q, const int* seqlens,
+                      const int* table, int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q,
+                      int max_blocks, int block_size, int num_blocks, int max_seqlen_k, int d, float scale,
+                      float descale_k, float descale_v, int causal, int n_splits, void* ws, size_t ws_bytes,
+                      void* stream, const char* name) {
+  fa_status_t st = check_paged(n_seqs, H, H_kv, d, max_blocks, block_size, num_blocks, 16);
+  if (st != FA_OK) return st;
+  if (H < 1 || H % H_kv != 0) return fail(FA_ERR_INVALID_ARG, "H must be a positive multiple of H_kv (got %d, %d)", H, H_kv);
+  if (total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "totals and max sequence lengths must be >= 0");
+  if (max_seqlen_q > total_q) return fail(FA_ERR_INVALID_ARG, "max_seqlen exceeds the total token count");
+  if (static_cast<long long>(max_seqlen_k) > static_cast<long long>(max_blocks) * block_size)
+    return fail(FA_ERR_INVALID_ARG, "max_seqlen_k=%d exceeds max_blocks_per_seq * block_size", max_seqlen_k);
+  if (max_seqlen_k >= (1LL << 31) / d) return fail(FA_ERR_UNSUPPORTED, "max_seqlen_k too large for d=%d", d);
+  if (static_cast<long long>(total_q) * H >= (1LL << 31)) return fail(FA_ERR_UNSUPPORTED, "total_q * H must be < 2^31");
+  if (!std::isfinite(scale) || !(scale > 0.f))
+    return fail(FA_ERR_INVALID_ARG, "scale must be finite and > 0 (got %g)", static_cast<double>(scale));
+  if ((st = check_descale(descale_k)) != FA_OK || (st = check_descale(descale_v)) != FA_OK) return st;
+  const float score = scale * 1.4426950408889634f * descale_k;
+  if (!(score >= 1e-34f) || !(score <= 1e34f))
+    return fail(FA_ERR_INVALID_ARG, "scale * descale_k must be in about [1e-34, 1e34] (got %g)", static_cast<double>(score));
+  if ((st = q4_splits(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k, &n_splits)) != FA_OK) return st;
+  if (total_q == 0 || max_seqlen_q == 0) return FA_OK;
+  if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !o || !lse)
+    return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  for (const void* x : {q, k_codes, k_scales, v_codes, v_scales, static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  if ((st = check_index_arrays(cu_q ? cu_q : seqlens, seqlens, table)) != FA_OK) return st;
+  if (n_splits > 1) {
+    const size_t need = fa::decode_part_bytes(total_q, H, d, n_splits);
+    if (!ws || ws_bytes < need || !aligned16(ws))
+      return fail(FA_ERR_WORKSPACE, "workspace must be >= %zu bytes and 16-byte aligned (got %zu)", need, ws_bytes);
+  }
+  fa::PagedQ4Args a{};
+  a.q = q; a.o = o; a.lse = lse; a.part = static_cast<float*>(ws);
+  a.k_codes = static_cast<const uint8_t*>(k_codes); a.k_scales = static_cast<const uint8_t*>(k_scales);
+  a.v_codes = static_cast<const uint8_t*>(v_codes); a.v_scales = static_cast<const uint8_t*>(v_scales);
+  a.cu_q = cu_q; a.seqlens = seqlens; a.block_table = table;
+  a.n_seqs = n_seqs; a.H = H; a.H_kv = H_kv; a.total_q = total_q; a.max_seqlen_q = max_seqlen_q; a.d = d;
+  a.num_blocks = num_blocks; a.block_size = block_size; a.max_blocks = max_blocks; a.max_seqlen_k = max_seqlen_k;
+  a.causal = causal ? 1 : 0; a.scale = scale; a.descale_k = descale_k; a.descale_v = descale_v;
+  a.n_splits = n_splits; a.chunk = fa::decode_chunk(max_seqlen_k, n_splits);
+  cudaError_t e = fa::launch_attend_q4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
+}
+
+}  // namespace
+
+extern "C" {
+
+fa_status_t fa_append_paged(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                            fa_bf16_t* k_cache, fa_bf16_t* v_cache, const float* cos, const float* sin,
+                            const int* cu_seqlens, const int* seqlens_k, const int* block_table, int n_seqs,
+                            int H, int H_kv, int total, long long q_stride, long long k_stride,
+                            long long v_stride, int max_blocks_per_seq, int block_size, int num_blocks, int d,
+                            int rotary_dim, int interleaved, int n_positions, void* stream) {
+  return append(q, k, v, q_out, k_cache, nullptr, v_cache, nullptr, false, cos, sin, cu_seqlens, seqlens_k,
+                block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq,
+                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, 1.f, 1.f, stream,
+                "fa_append_paged launch");
+}
+
+fa_status_t fa_append_paged_q4(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                               fa_e2m1x2_t* k_codes, fa_e4m3_t* k_scales, fa_e2m1x2_t* v_codes,
+                               fa_e4m3_t* v_scales, const float* cos, const float* sin, const int* cu_seqlens,
+                               const int* seqlens_k, const int* block_table, int n_seqs, int H, int H_kv,
+                               int total, long long q_stride, long long k_stride, long long v_stride,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int d, int rotary_dim,
+                               int interleaved, int n_positions, float descale_k, float descale_v, void* stream) {
+  return append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, true, cos, sin, cu_seqlens, seqlens_k,
+                block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq,
+                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, descale_k, descale_v, stream,
+                "fa_append_paged_q4 launch");
+}
+
+fa_status_t fa_gather_paged_q4(const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales, const fa_e2m1x2_t* v_codes,
+                               const fa_e4m3_t* v_scales, fa_bf16_t* k, fa_bf16_t* v, const int* cu_seqlens,
+                               const int* seqlens_k, const int* block_table, int n_seqs, int H_kv, int total,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int d, float descale_k,
+                               float descale_v, void* stream) {
+  fa_status_t st = check_paged(n_seqs, 0, H_kv, d, max_blocks_per_seq, block_size, num_blocks, 16);
+  if (st != FA_OK) return st;
+  if (total < 0) return fail(FA_ERR_INVALID_ARG, "total must be >= 0 (got %d)", total);
+  if ((st = check_descale(descale_k)) != FA_OK || (st = check_descale(descale_v)) != FA_OK) return st;
+  if ((2LL * H_kv + 1) * total >= (1LL << 31)) return fail(FA_ERR_UNSUPPORTED, "total * H_kv too large");
+  if (total == 0) return FA_OK;
+  if (!k_codes || !k_scales || !v_codes || !v_scales || !k || !v) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
+  for (const void* x : {static_cast<const void*>(k_codes), static_cast<const void*>(k_scales),
+                        static_cast<const void*>(v_codes), static_cast<const void*>(v_scales),
+                        static_cast<const void*>(k), static_cast<const void*>(v)})
+    if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  fa::GatherArgs a{k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table,
+                   n_seqs, H_kv, total, max_blocks_per_seq, block_size, num_blocks, d, descale_k, descale_v};
+  cudaError_t e = fa::launch_gather_q4(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_gather_paged_q4 launch");
+}
+
+size_t fa_decode_paged_q4_workspace_size(int B, int H, int H_kv, int max_seqlen_k, int d, int n_splits) {
+  return q4_workspace(B, H, H_kv, B, 1, max_seqlen_k, d, n_splits);
+}
+
+fa_status_t fa_decode_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales,
+                               const fa_e2m1x2_t* v_codes, const fa_e4m3_t* v_scales, fa_bf16_t* o, float* lse,
+                               const int* block_table, const int* seqlens_k, int B, int H, int H_kv,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int max_seqlen_k, int d,
+                               float scale, float descale_k, float descale_v, int n_splits, void* ws,
+                               size_t ws_bytes, void* stream) {
+  return attend_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, nullptr, seqlens_k, block_table, B, H, H_kv,
+                   B, 1, max_blocks_per_seq, block_size, num_blocks, max_seqlen_k, d, scale, descale_k, descale_v,
+                   0, n_splits, ws, ws_bytes, stream, "fa_decode_paged_q4 launch");
+}
+
+size_t fa_fwd_paged_q4_workspace_size(int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q,
+                                      int max_seqlen_k, int d, int n_splits) {
+  return q4_workspace(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d, n_splits);
+}
+
+fa_status_t fa_fwd_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales,
+                            const fa_e2m1x2_t* v_codes, const fa_e4m3_t* v_scales, fa_bf16_t* o, float* lse,
+                            const int* cu_seqlens_q, const int* seqlens_k, const int* block_table, int n_seqs,
+                            int H, int H_kv, int total_q, int max_seqlen_q, int max_blocks_per_seq,
+                            int block_size, int num_blocks, int max_seqlen_k, int d, float scale,
+                            float descale_k, float descale_v, int causal, int n_splits, void* ws,
+                            size_t ws_bytes, void* stream) {
+  if (!cu_seqlens_q) return fail(FA_ERR_INVALID_ARG, "null cu_seqlens_q");
+  return attend_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table, n_seqs,
+                   H, H_kv, total_q, max_seqlen_q, max_blocks_per_seq, block_size, num_blocks, max_seqlen_k, d,
+                   scale, descale_k, descale_v, causal, n_splits, ws, ws_bytes, stream, "fa_fwd_paged_q4 launch");
+}
+
 fa_status_t fa_debug_counters(unsigned long long* device_counters) {
   fa::g_debug_counters = device_counters;
   return FA_OK;
@@ -544,7 +783,7 @@ fa_status_t fa_sync_status(void* stream) {
   int where = 0, w = 0;
   cudaError_t (*fetch[])(cudaStream_t, unsigned int*, int*) = {
       fa::status_fetch_fwd, fa::status_fetch_bwd, fa::status_fetch_decode,
-      fa::status_fetch_selftest};
+      fa::status_fetch_selftest, fa::status_fetch_paged, fa::status_fetch_attend_q4};
   for (auto f : fetch) {
     cudaError_t e = f(s, &c, &w);
     if (e != cudaSuccess) return cuda_fail(e, "fa_sync_status");
@@ -554,7 +793,8 @@ fa_status_t fa_sync_status(void* stream) {
     return fail(FA_ERR_DEVICE_TIMEOUT, "a kernel's bounded wait ran out (site %d)", where);
   if (code & fa::FA_DEV_BAD_CONFIG)
     return fail(FA_ERR_INVALID_ARG,
-                "a kernel found invalid sequence boundaries (cu_seqlens / max_seqlen) (site %d)",
+                "a kernel found invalid sequence boundaries (cu_seqlens / max_seqlen), lengths or cache "
+                "blocks (site %d)",
                 where);
   if (code) return fail(FA_ERR_CUDA, "device reported error code %u (site %d)", code, where);
   return FA_OK;

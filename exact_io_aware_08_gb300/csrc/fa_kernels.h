@@ -146,6 +146,47 @@ struct DecodePagedArgs {
   int n_splits, chunk;
 };
 
+// Append to a paged cache: bf16 (k_scales null) or 4 bits.
+struct AppendArgs {
+  const void *q, *k, *v;        // [total, H | H_kv, d], tokens *_stride elements apart; q may be null
+  void* q_out;                  // [total, H, d]
+  void *k_cache, *v_cache;      // bf16 [num_blocks, block_size, H_kv, d], or codes [num_blocks, H_kv, block_size, d/2]
+  uint8_t *k_scales, *v_scales; // [num_blocks, H_kv, block_size, d/16]
+  const float *cos, *sin;       // [n_positions, rotary/2]
+  const int *cu, *seqlens, *block_table;
+  long long q_stride, k_stride, v_stride;
+  int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, d, rotary, interleaved, n_positions;
+  float descale_k, descale_v;
+};
+
+struct GatherArgs {
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  void *k, *v;                  // [total, H_kv, d] bf16
+  const int *cu, *seqlens, *block_table;
+  int n_seqs, H_kv, total, max_blocks, block_size, num_blocks, d;
+  float descale_k, descale_v;
+};
+
+// Attention over a 4-bit paged cache.  cu_q null: one query a sequence, q/o [B, H, d], lse [B, H];
+// else packed queries [total_q, H, d], lse [H, total_q].
+struct PagedQ4Args {
+  const void* q;
+  const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
+  void* o;
+  float* lse;
+  float* part;                  // [total_q * H, n_splits, d + 2], used when n_splits > 1
+  const int *cu_q, *seqlens, *block_table;
+  int n_seqs, H, H_kv, total_q, max_seqlen_q, d, num_blocks, block_size, max_blocks, max_seqlen_k, causal;
+  float scale, descale_k, descale_v;
+  int n_splits, chunk;
+};
+
+cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
+cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream);
+cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream);
+cudaError_t status_fetch_paged(cudaStream_t, unsigned int*, int*);
+cudaError_t status_fetch_attend_q4(cudaStream_t, unsigned int*, int*);
+
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_fp8(const FwdArgs& a, cudaStream_t stream);   // d = 128 only
 cudaError_t launch_fwd_varlen(const FwdVarlenArgs& a, cudaStream_t stream);
@@ -194,6 +235,23 @@ inline int decode_chunk(int n_kv, int n_splits) {
 }
 inline size_t decode_part_bytes(int B, int H, int d, int n_splits) {
   return static_cast<size_t>(B) * H * n_splits * (d + 2) * sizeof(float);
+}
+
+// Query rows (query heads that share a key head, times query tokens) that a CTA of the 4-bit
+// attention computes together.
+constexpr int kQ4Rows = 16;
+// Split count of the 4-bit attention when the caller leaves it open: enough chunks for four CTAs
+// on every SM twice over, of at least 256 keys.
+inline int q4_auto_splits(long long items, int n_kv) {
+  long long s = (152LL * 8 + items - 1) / items;
+  const long long max_by_len = (static_cast<long long>(n_kv) + 255) / 256;
+  if (s > max_by_len) s = max_by_len;
+  if (s < 1) s = 1;
+  if (s > kDecodeMaxSplits) s = kDecodeMaxSplits;
+  return static_cast<int>(s);
+}
+inline long long q4_row_blocks(int H, int H_kv, int max_seqlen_q) {
+  return (static_cast<long long>(H / H_kv) * max_seqlen_q + kQ4Rows - 1) / kQ4Rows;
 }
 
 // Size of the fixed device scratch behind fa_decode_splitkv_noalloc (decode.cu).

@@ -59,6 +59,21 @@ inline bool make_map_u8_3d(CUtensorMap* map, const void* base, uint64_t inner, u
   return r == CUDA_SUCCESS;
 }
 
+// 8-bit rows {inner, rows}, dense; box {inner, box_rows}.
+inline bool make_map_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows,
+                           uint32_t box_rows, CUtensorMapSwizzle swizzle) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {inner, rows};
+  const cuuint64_t strides[1] = {inner};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(inner), box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides,
+                   box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // Packed token-major bf16 tensor [total, H, d] as {d, H, total}: box {box_inner, 1, box_rows}
 // covers box_rows consecutive tokens of one head and lands in shared memory exactly like the
 // [B, H, N, d] box above.

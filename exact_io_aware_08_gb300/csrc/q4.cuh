@@ -1,0 +1,113 @@
+// The 4-bit cache's number formats on the device, and the places of tokens in a paged cache.
+//
+// A row of d elements is d/2 code bytes (element 2i in the low four bits of byte i, 2i + 1 in the
+// high four) and d/16 scale bytes.  A code is e2m1 (sign, 2 exponent bits, 1 mantissa bit: 0, 0.5,
+// 1, 1.5, 2, 3, 4, 6 and their negatives), a scale e4m3.  A code has 2 significant bits and a scale
+// 4, so code * scale has at most 6 and lies in [2^-10, 2688]: every product is an exact fp16 number.
+#pragma once
+
+#include "sm103.cuh"
+
+namespace fa {
+
+// Four code bytes -> eight fp16 values, byte j's pair in out[j] (low half = low four bits).
+__device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t (&out)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(out[0]), "=r"(out[1]), "=r"(out[2]), "=r"(out[3]) : "r"(w));
+}
+
+// Two scale bytes (in the low half of ``w``) -> two fp16 values (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// Eight fp32 values rounded (to nearest even, saturating at +-6) to e2m1, element i in bits 4i..4i+3.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* y) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+      : "=r"(r)
+      : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+  return r;
+}
+
+// fp32 -> e4m3 (to nearest even, saturating at 448), in the low byte.
+__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
+  return pack_e4m3x4(x, 0.f, 0.f, 0.f) & 0xffu;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(w));
+  return f;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// The sequence that owns packed token ``t``: the b with cu[b] <= t < cu[b+1], found by the whole
+// warp, 32 boundaries a step.  Returns -1 for a token at or behind cu[n_seqs] (a padding row), and
+// for boundaries that do not enclose it (which are reported).  Whatever the boundaries hold, b stays
+// in [0, n_seqs) and the search ends, since each step shrinks the range.
+__device__ __forceinline__ int owner_of_token(const int* __restrict__ cu, int n_seqs, int total, int t,
+                                              int* first, int* count, int where) {
+  const int lane = threadIdx.x & 31;
+  const int end = __ldg(cu + n_seqs);
+  int lo = 0, hi = n_seqs;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int at = lo + step * (lane + 1);
+    const bool before = at < hi && __ldg(cu + at) <= t;
+    lo += __popc(__ballot_sync(0xffffffffu, before)) * step;
+    hi = min(hi, lo + step);
+  }
+  const int a = __ldg(cu + lo), b = __ldg(cu + lo + 1);
+  const bool padding = t >= end;
+  if ((t == 0 && (end > total || end < 0)) || (!padding && (a > t || b <= t || a < 0 || b > total))) {
+    if (lane == 0) report_device_error(FA_DEV_BAD_CONFIG, where);
+    return -1;
+  }
+  *first = a;
+  *count = b - a;
+  return padding ? -1 : lo;
+}
+
+// Page and row of logical token ``pos`` of sequence b; false (reported) where the position or the
+// page lies outside the cache.
+__device__ __forceinline__ bool place_of_token(const int* __restrict__ table, int max_blocks,
+                                               int block_size, int num_blocks, int b, int len, int pos,
+                                               int* page, int* row, int where) {
+  const int blk = pos / block_size;
+  bool ok = pos >= 0 && pos < len && blk < max_blocks;
+  *row = pos - blk * block_size;
+  *page = ok ? __ldg(table + static_cast<size_t>(b) * max_blocks + blk) : -1;
+  ok = ok && *page >= 0 && *page < num_blocks;
+  if (!ok && (threadIdx.x & 31) == 0) report_device_error(FA_DEV_BAD_CONFIG, where);
+  return ok;
+}
+
+}  // namespace fa

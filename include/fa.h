@@ -39,6 +39,9 @@ extern "C" {
 typedef uint16_t fa_bf16_t; /* raw bfloat16 bits */
 typedef uint8_t fa_e4m3_t;  /* raw 8-bit float code: 1 sign, 4 exponent (bias 7), 3 mantissa bits */
 
+typedef uint8_t fa_e2m1x2_t; /* two raw 4-bit float codes (1 sign, 2 exponent (bias 1), 1 mantissa bit:
+                                0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives), the first in the low bits */
+
 typedef enum {
   FA_OK = 0,
   FA_ERR_INVALID_ARG = 1,    /* null pointer, negative size, misaligned pointer, bad scale */
@@ -311,6 +314,112 @@ fa_status_t fa_decode_paged(const fa_bf16_t* q, const fa_bf16_t* k_cache,
 fa_status_t fa_decode_splitkv_noalloc(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v,
                                       fa_bf16_t* o, float* lse, int B, int H, int N_kv, int d,
                                       float scale, int n_splits, void* stream);
+
+/*
+ * fa_append_paged / fa_append_paged_q4 -- put a step's keys and values into a paged cache, rotated
+ * by their positions on the way, and rotate the step's queries (a serving step's other half beside
+ * fa_decode_paged and the 4-bit attention below; the pages describe neither paging nor rotation).
+ *
+ * Tokens of the step are packed: q [total, H, d], k and v [total, H_kv, d] bf16, consecutive tokens
+ * q_stride / k_stride / v_stride elements apart (a multiple of 8; heads of a token dense), so slices
+ * of one fused projection do.  cu_seqlens [n_seqs + 1]: sequence b owns tokens [cu[b], cu[b+1]);
+ * seqlens_k [n_seqs]: its tokens in the cache counting these.  Token cu[b] + i has position
+ *   p = seqlens_k[b] - (cu[b+1] - cu[b]) + i
+ * and goes to row p % block_size of block block_table[b * max_blocks_per_seq + p / block_size].
+ * Tokens at and behind cu[n_seqs] are padding: nothing of them is written anywhere.
+ *
+ * Rotation: the first rotary_dim (a multiple of 32, 0 to d) elements of each query and key head, in
+ * pairs (i, i + rotary_dim/2), or (2i, 2i + 1) with ``interleaved``, become
+ *   (x1 cos - x2 sin, x2 cos + x1 sin),  cos, sin: fp32 [n_positions, rotary_dim/2], row p, column i,
+ * in fp32 (each product and sum rounded), elements behind them and all values stay.  cos and sin may
+ * be null with rotary_dim 0.  q may be null (no queries; H is then not looked at); q_out [total, H, d]
+ * is dense and may be q itself where q is dense.
+ *
+ * bf16 cache: k_cache, v_cache [num_blocks, block_size, H_kv, d], rounded to nearest, as
+ * fa_decode_paged reads them (which wants block_size a multiple of 64; any will do here).
+ *
+ * 4-bit cache: codes [num_blocks, H_kv, block_size, d/2], scales [num_blocks, H_kv, block_size, d/16]:
+ * a head's rows of a block are consecutive, so that the attention reads them in long runs.
+ * block_size is a multiple of 16.  16 consecutive elements x (after rotation, in fp32) are held as
+ *   scale = e4m3(max |x| / (6 descale)),  code_i = e2m1(x_i / (scale descale)),
+ * both to nearest, ties to even, saturating at 448 and 6; a scale of 0 gives codes of 0.  The value
+ * is code * scale * descale (descale_k for keys, descale_v for values, in [1e-30, 1e30]; commonly
+ * the largest magnitude expected over 6 * 448).  What is not finite is held as some finite value.
+ *
+ * Device-side checks: boundaries outside [0, total] or not ascending, seqlens_k[b] below the step's
+ * tokens of b, a position outside the block table or the cos/sin tables, or a block id outside
+ * [0, num_blocks) skip the token's queries, keys and values and make fa_sync_status report
+ * FA_ERR_INVALID_ARG.  Two sequences that write one row of one block race.
+ * num_blocks * block_size * H_kv and total * (H + 2 H_kv) must be < 2^31 (else FA_ERR_UNSUPPORTED).
+ */
+fa_status_t fa_append_paged(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                            fa_bf16_t* k_cache, fa_bf16_t* v_cache, const float* cos, const float* sin,
+                            const int* cu_seqlens, const int* seqlens_k, const int* block_table, int n_seqs,
+                            int H, int H_kv, int total, long long q_stride, long long k_stride,
+                            long long v_stride, int max_blocks_per_seq, int block_size, int num_blocks, int d,
+                            int rotary_dim, int interleaved, int n_positions, void* stream);
+fa_status_t fa_append_paged_q4(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                               fa_e2m1x2_t* k_codes, fa_e4m3_t* k_scales, fa_e2m1x2_t* v_codes,
+                               fa_e4m3_t* v_scales, const float* cos, const float* sin, const int* cu_seqlens,
+                               const int* seqlens_k, const int* block_table, int n_seqs, int H, int H_kv,
+                               int total, long long q_stride, long long k_stride, long long v_stride,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int d, int rotary_dim,
+                               int interleaved, int n_positions, float descale_k, float descale_v, void* stream);
+
+/*
+ * fa_gather_paged_q4 -- read tokens of a 4-bit paged cache back as packed bf16: k, v [total, H_kv, d]
+ * (written), row cu[b] + i = bf16(code * scale * descale) of the token that fa_append_paged_q4 with
+ * the same cu_seqlens, seqlens_k and block_table put there, that is the last cu[b+1] - cu[b] of the
+ * sequence (all of it where that is seqlens_k[b]).  Hands a cache to the calls that take bf16 keys,
+ * fa_fwd_varlen for instance.  Rows at and behind cu[n_seqs] are left as they are; device-side checks as
+ * for the append (a rejected token's rows are left as they are).
+ */
+fa_status_t fa_gather_paged_q4(const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales, const fa_e2m1x2_t* v_codes,
+                               const fa_e4m3_t* v_scales, fa_bf16_t* k, fa_bf16_t* v, const int* cu_seqlens,
+                               const int* seqlens_k, const int* block_table, int n_seqs, int H_kv, int total,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int d, float descale_k,
+                               float descale_v, void* stream);
+
+/*
+ * fa_decode_paged_q4 -- fa_decode_paged over a 4-bit cache (layout and values as above), for grouped
+ * heads: query head h reads key head h / (H / H_kv); H_kv divides H.
+ *
+ *   O, lse = attention of q over the first seqlens_k[b] cached tokens       q, o: [B,H,1,d], lse: [B,H,1]
+ *
+ * Scores accumulate in fp32 from exact products of codes and scales with q; the attention weights are
+ * rounded to 16 bits for the product with the values.  block_size is a positive multiple of 16;
+ * seqlens_k, block_table, max_seqlen_k, n_splits and the device-side checks as for fa_decode_paged.
+ * A row with no tokens gets O = 0, lse = -inf.  ws: at least the size call's bytes, 16-byte aligned
+ * (not looked at where the call runs with one split).
+ */
+size_t fa_decode_paged_q4_workspace_size(int B, int H, int H_kv, int max_seqlen_k, int d, int n_splits);
+fa_status_t fa_decode_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales,
+                               const fa_e2m1x2_t* v_codes, const fa_e4m3_t* v_scales, fa_bf16_t* o, float* lse,
+                               const int* block_table, const int* seqlens_k, int B, int H, int H_kv,
+                               int max_blocks_per_seq, int block_size, int num_blocks, int max_seqlen_k, int d,
+                               float scale, float descale_k, float descale_v, int n_splits, void* ws,
+                               size_t ws_bytes, void* stream);
+
+/*
+ * fa_fwd_paged_q4 -- attention of several query tokens a sequence over a 4-bit paged cache: the next
+ * part of a prompt, or drafted tokens that are checked together.
+ *
+ * q, o: [total_q, H, d] packed, sequence b's n = cu_q[b+1] - cu_q[b] tokens at [cu_q[b], cu_q[b+1]);
+ * lse: [H, total_q].  The keys are the sequence's seqlens_k[b] cached tokens, the step's own among them
+ * (append them first).  causal: query i sees keys j <= seqlens_k[b] - n + i, that is the tokens up to
+ * its own; else all.  A query that sees no key (n > seqlens_k[b]) gets O = 0, lse = -inf.  Rows at and
+ * behind cu_q[n_seqs] are left as they are.  max_seqlen_q bounds the n (and sizes the launch); other
+ * arguments and checks as for fa_decode_paged_q4, boundaries as for fa_fwd_varlen.
+ */
+size_t fa_fwd_paged_q4_workspace_size(int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q,
+                                      int max_seqlen_k, int d, int n_splits);
+fa_status_t fa_fwd_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales,
+                            const fa_e2m1x2_t* v_codes, const fa_e4m3_t* v_scales, fa_bf16_t* o, float* lse,
+                            const int* cu_seqlens_q, const int* seqlens_k, const int* block_table, int n_seqs,
+                            int H, int H_kv, int total_q, int max_seqlen_q, int max_blocks_per_seq,
+                            int block_size, int num_blocks, int max_seqlen_k, int d, float scale,
+                            float descale_k, float descale_v, int causal, int n_splits, void* ws,
+                            size_t ws_bytes, void* stream);
 
 /*
  * fa_sync_status -- synchronise ``stream`` and report device-side failures recorded by any
