@@ -23,6 +23,9 @@ __all__ = [
     "fa_fwd_window", "fa_bwd_window", "forward_window", "backward_window",
     "fa_fwd_block_sparse", "fa_bwd_block_sparse", "forward_block_sparse", "backward_block_sparse",
     "BLOCK_SIZE", "fa_debug_counters",
+    "fa_append_paged", "fa_append_paged_q4", "fa_gather_paged_q4", "fa_decode_paged_q4", "fa_fwd_paged_q4",
+    "fa_decode_paged_q4_workspace_size", "fa_fwd_paged_q4_workspace_size",
+    "append_paged", "append_paged_q4", "gather_paged_q4", "decode_paged_q4", "forward_paged_q4", "rotary_tables",
 ]
 
 BLOCK_SIZE = 128   # block-sparse attention: blocks of 128 queries x 128 keys
@@ -51,6 +54,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
 _S = ctypes.c_size_t
+_L = ctypes.c_longlong
 
 _SIGNATURES = {
     "fa_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _I, _P]),
@@ -73,6 +77,13 @@ _SIGNATURES = {
     "fa_fwd_fp8": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _F, _F, _F, _F, _I, _P]),
     "fa_decode_paged": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _S,
                              _P]),
+    "fa_append_paged": (_I, [_P] * 11 + [_I] * 4 + [_L] * 3 + [_I] * 7 + [_P]),
+    "fa_append_paged_q4": (_I, [_P] * 13 + [_I] * 4 + [_L] * 3 + [_I] * 7 + [_F] * 2 + [_P]),
+    "fa_gather_paged_q4": (_I, [_P] * 9 + [_I] * 7 + [_F] * 2 + [_P]),
+    "fa_decode_paged_q4_workspace_size": (_S, [_I] * 6),
+    "fa_decode_paged_q4": (_I, [_P] * 9 + [_I] * 8 + [_F] * 3 + [_I, _P, _S, _P]),
+    "fa_fwd_paged_q4_workspace_size": (_S, [_I] * 8),
+    "fa_fwd_paged_q4": (_I, [_P] * 10 + [_I] * 10 + [_F] * 3 + [_I] * 2 + [_P, _S, _P]),
     "fa_sync_status": (_I, [_P]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
     "fa_debug_counters": (_I, [_P]),
@@ -313,6 +324,197 @@ def fa_decode_paged(q, k_cache, v_cache, o, lse, block_table, seqlens_k, max_seq
                                           _ptr(ws), ws_bytes, _stream(stream)))
 
 
+# The paged-cache calls look their tensors over before they pass pointers on: one device, the types
+# and shapes of include/fa.h, dense (the packed q, k, v of an append may be slices of a wider matrix).
+
+def _bad(message):
+    raise FaError(1, message)
+
+
+def _expect(name, t, dtypes, shape, device, strided=False):
+    """``shape``: None for a free extent.  ``strided``: only the last two dimensions are dense."""
+    if t.device != device or not t.is_cuda:
+        _bad(f"{name} must be a CUDA tensor on {device}, is on {t.device}")
+    if t.dtype not in dtypes:
+        _bad(f"{name} must be {' or '.join(str(x) for x in dtypes)}, is {t.dtype}")
+    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        _bad(f"{name} must be {list(shape)}, is {list(t.shape)}")
+    if not t.is_contiguous():
+        if not strided or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+            _bad(f"{name} must be dense" + (" in its last two dimensions" if strided else ""))
+
+
+def _types():
+    import torch
+    return (torch.bfloat16,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+
+
+def _launch(device, stream, name, *args):
+    """Calls ``name`` with the stream as its last argument, with ``device`` the current one."""
+    import torch
+    fn = getattr(load_library(), name)
+    if device.index == torch.cuda.current_device():
+        return _check(fn(*args, _stream(stream)))
+    with torch.cuda.device(device):
+        return _check(fn(*args, _stream(stream)))
+
+
+def _expect_q4(k_codes, k_scales, v_codes, v_scales, H_kv, d):
+    """Checks a 4-bit cache; (device, num_blocks, H_kv, block_size, d)."""
+    _, _, u8, e4m3, _ = _types()
+    device = k_codes.device
+    if k_codes.dim() != 4:
+        _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
+    shape = k_codes.shape
+    if (H_kv is not None and shape[1] != H_kv) or (d is not None and shape[3] * 2 != d):
+        _bad(f"k_codes must be [num_blocks, {H_kv}, block_size, {d}/2], is {list(shape)}")
+    scales = (*shape[:3], shape[3] // 8)
+    _expect("k_codes", k_codes, u8, shape, device)
+    _expect("v_codes", v_codes, u8, shape, device)
+    _expect("k_scales", k_scales, e4m3, scales, device)
+    _expect("v_scales", v_scales, e4m3, scales, device)
+    return device, shape[0], shape[1], shape[2], shape[3] * 2
+
+
+def _token_stride(t):
+    return 0 if t is None else t.stride(0)
+
+
+def _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, device):
+    """Checks what both appends share; (n_seqs, H, H_kv, total, d, rotary_dim, n_positions)."""
+    bf16, i32, _, _, f32 = _types()
+    if k.dim() != 3 or block_table.dim() != 2:
+        _bad("k must be [total, H_kv, d] and block_table [n_seqs, max_blocks]")
+    total, H_kv, d = k.shape
+    n_seqs = block_table.shape[0]
+    _expect("k", k, bf16, k.shape, device, True)
+    _expect("v", v, bf16, k.shape, device, True)
+    H = 0
+    if (q is None) != (q_out is None):
+        _bad("q and q_out go together")
+    if q is not None:
+        _expect("q", q, bf16, (total, None, d), device, True)
+        H = q.shape[1]
+        _expect("q_out", q_out, bf16, (total, H, d), device)
+    _expect("block_table", block_table, i32, block_table.shape, device)
+    _expect("cu_seqlens", cu_seqlens, i32, (n_seqs + 1,), device)
+    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
+    if (cos is None) != (sin is None):
+        _bad("cos and sin go together")
+    rotary, n_positions = 0, 0
+    if cos is not None:
+        _expect("cos", cos, f32, (None, None), device)
+        _expect("sin", sin, f32, cos.shape, device)
+        rotary, n_positions = 2 * cos.shape[1], cos.shape[0]
+    return n_seqs, H, H_kv, total, d, rotary, n_positions
+
+
+def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seqlens_k, block_table,
+                    interleaved: bool = False, stream=None):
+    """q, q_out [total, H, d] or None; k, v [total, H_kv, d]; k/v cache [num_blocks, block_size, H_kv, d];
+    cos, sin fp32 [n_positions, rotary_dim/2] or None; cu_seqlens [n_seqs + 1], seqlens_k [n_seqs] and
+    block_table [n_seqs, max_blocks] int32, all on the device."""
+    device = k_cache.device
+    n_seqs, H, H_kv, total, d, rotary, n_positions = _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k,
+                                                                  block_table, device)
+    _expect("k_cache", k_cache, _types()[0], (None, None, H_kv, d), device)
+    _expect("v_cache", v_cache, _types()[0], k_cache.shape, device)
+    _launch(device, stream, "fa_append_paged", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
+            _ptr(cos), _ptr(sin), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table), n_seqs, H, H_kv, total,
+            _token_stride(q), _token_stride(k), _token_stride(v), block_table.shape[1], k_cache.shape[1],
+            k_cache.shape[0], d, rotary, int(bool(interleaved)), n_positions)
+
+
+def fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
+                       block_table, descale_k: float, descale_v: float, interleaved: bool = False, stream=None):
+    """As fa_append_paged, with codes uint8 [num_blocks, H_kv, block_size, d/2] and scales (uint8 or
+    float8_e4m3fn) [num_blocks, H_kv, block_size, d/16]."""
+    device = k_codes.device
+    n_seqs, H, H_kv, total, d, rotary, n_positions = _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k,
+                                                                  block_table, device)
+    _, num_blocks, _, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, H_kv, d)
+    _launch(device, stream, "fa_append_paged_q4", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_codes), _ptr(k_scales),
+            _ptr(v_codes), _ptr(v_scales), _ptr(cos), _ptr(sin), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table),
+            n_seqs, H, H_kv, total, _token_stride(q), _token_stride(k), _token_stride(v), block_table.shape[1],
+            block_size, num_blocks, d, rotary, int(bool(interleaved)), n_positions, float(descale_k), float(descale_v))
+
+
+def fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table,
+                       descale_k: float, descale_v: float, stream=None):
+    """k, v [total, H_kv, d] bf16 are written."""
+    bf16, i32, _, _, _ = _types()
+    device, num_blocks, H_kv, block_size, d = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, None)
+    _expect("k", k, bf16, (None, H_kv, d), device)
+    _expect("v", v, bf16, k.shape, device)
+    _expect("block_table", block_table, i32, (None, None), device)
+    n_seqs = block_table.shape[0]
+    _expect("cu_seqlens", cu_seqlens, i32, (n_seqs + 1,), device)
+    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
+    _launch(device, stream, "fa_gather_paged_q4", _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k),
+            _ptr(v), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table), n_seqs, H_kv, k.shape[0],
+            block_table.shape[1], block_size, num_blocks, d, float(descale_k), float(descale_v))
+
+
+def fa_decode_paged_q4_workspace_size(B: int, H: int, H_kv: int, max_seqlen_k: int, d: int, n_splits: int) -> int:
+    return int(load_library().fa_decode_paged_q4_workspace_size(B, H, H_kv, max_seqlen_k, d, n_splits))
+
+
+def fa_fwd_paged_q4_workspace_size(n_seqs: int, H: int, H_kv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
+                                   d: int, n_splits: int) -> int:
+    return int(load_library().fa_fwd_paged_q4_workspace_size(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d,
+                                                             n_splits))
+
+
+def _expect_ws(ws, device):
+    if ws is not None and (ws.device != device or not ws.is_contiguous()):
+        _bad(f"the workspace must be dense and on {device}")
+
+
+def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k: int,
+                       scale: float, descale_k: float, descale_v: float, n_splits: int, ws, stream=None):
+    """q, o [B,H,1,d]; lse [B,H,1]; a 4-bit cache as fa_append_paged_q4 writes it; block_table
+    [B, max_blocks] int32; seqlens_k [B] int32.  H_kv (of the cache) divides H."""
+    bf16, i32, _, _, f32 = _types()
+    if q.dim() != 4:
+        _bad(f"q must be [B, H, 1, d], is {list(q.shape)}")
+    B, H, _, d = q.shape
+    device, num_blocks, H_kv, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, d)
+    _expect("q", q, bf16, (B, H, 1, d), device)
+    _expect("o", o, bf16, (B, H, 1, d), device)
+    _expect("lse", lse, f32, (B, H, 1), device)
+    _expect("block_table", block_table, i32, (B, None), device)
+    _expect("seqlens_k", seqlens_k, i32, (B,), device)
+    _expect_ws(ws, device)
+    _launch(device, stream, "fa_decode_paged_q4", _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+            _ptr(o), _ptr(lse), _ptr(block_table), _ptr(seqlens_k), B, H, H_kv, block_table.shape[1], block_size,
+            num_blocks, int(max_seqlen_k), d, float(scale), float(descale_k), float(descale_v), int(n_splits), _ptr(ws),
+            _nbytes(ws))
+
+
+def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table,
+                    max_seqlen_q: int, max_seqlen_k: int, scale: float, descale_k: float, descale_v: float, causal: bool,
+                    n_splits: int, ws, stream=None):
+    """q, o [total_q, H, d]; lse [H, total_q]; cu_seqlens_q [n_seqs + 1] int32; the rest as for
+    fa_decode_paged_q4."""
+    bf16, i32, _, _, f32 = _types()
+    if q.dim() != 3 or block_table.dim() != 2:
+        _bad("q must be [total_q, H, d] and block_table [n_seqs, max_blocks]")
+    total_q, H, d = q.shape
+    n_seqs = block_table.shape[0]
+    device, num_blocks, H_kv, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, d)
+    _expect("q", q, bf16, q.shape, device)
+    _expect("o", o, bf16, q.shape, device)
+    _expect("lse", lse, f32, (H, total_q), device)
+    _expect("block_table", block_table, i32, block_table.shape, device)
+    _expect("cu_seqlens_q", cu_seqlens_q, i32, (n_seqs + 1,), device)
+    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
+    _expect_ws(ws, device)
+    _launch(device, stream, "fa_fwd_paged_q4", _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
+            _ptr(o), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(block_table), n_seqs, H, H_kv, total_q,
+            int(max_seqlen_q), block_table.shape[1], block_size, num_blocks, int(max_seqlen_k), d, float(scale),
+            float(descale_k), float(descale_v), int(bool(causal)), int(n_splits), _ptr(ws), _nbytes(ws))
+
+
 def fa_debug_counters(counters):
     """Point the diagnostic tile counters at ``counters`` (a uint64/int64 device tensor of >= 2
     entries), or turn them off with None (see include/fa.h)."""
@@ -459,3 +661,91 @@ def backward_block_sparse(q, k, v, o, lse, do, block_mask, causal: bool = False,
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fa_bwd_block_sparse(q, k, v, o, lse, do, dq, dk, dv, workspace, scale, block_mask, causal, stream)
     return dq, dk, dv
+
+
+def rotary_tables(n_positions: int, rotary_dim: int, base: float = 10000.0, device=None):
+    """(cos, sin) fp32 [n_positions, rotary_dim/2] of the angles p * base^(-2i / rotary_dim), which are
+    formed in 64 bits: at position 10^5 a 32-bit angle is off by 4e-3."""
+    import torch
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * base ** (-i / rotary_dim)
+    return angle.cos().float(), angle.sin().float()
+
+
+def _rotated(q, k, q_out):
+    import torch
+    return torch.empty(q.shape, dtype=q.dtype, device=k.device) if q is not None and q_out is None else q_out
+
+
+def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, q=None, cos=None, sin=None,
+                 interleaved: bool = False, q_out=None, stream=None):
+    """Rotates a step's packed keys by their positions, puts keys and values into the bf16 paged cache
+    that decode_paged reads, and returns the rotated queries (None without q)."""
+    q_out = _rotated(q, k, q_out)
+    fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seqlens_k, block_table, interleaved, stream)
+    return q_out
+
+
+def append_paged_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, q=None, cos=None,
+                    sin=None, descale_k: float = 1.0, descale_v: float = 1.0, interleaved: bool = False, q_out=None,
+                    stream=None):
+    """append_paged into a 4-bit cache (see fa_append_paged_q4)."""
+    q_out = _rotated(q, k, q_out)
+    fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k, block_table,
+                       descale_k, descale_v, interleaved, stream)
+    return q_out
+
+
+def gather_paged_q4(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, total: int,
+                    descale_k: float = 1.0, descale_v: float = 1.0, stream=None):
+    """The last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence of a 4-bit cache as packed bf16
+    (k, v [total, H_kv, d])."""
+    import torch
+    if k_codes.dim() != 4:
+        _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
+    k = torch.empty((total, k_codes.shape[1], 2 * k_codes.shape[3]), dtype=torch.bfloat16, device=k_codes.device)
+    v = torch.empty_like(k)
+    fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table, descale_k,
+                       descale_v, stream)
+    return k, v
+
+
+def _workspace(workspace, need, device):
+    import torch
+    if workspace is None or _nbytes(workspace) < need:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    return workspace
+
+
+def decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seqlens_k, max_seqlen_k: int,
+                    n_splits: int = 0, scale: float | None = None, descale_k: float = 1.0, descale_v: float = 1.0,
+                    stream=None, workspace=None):
+    """Single-query decode over a 4-bit paged cache, grouped heads -> (O [B,H,1,d], lse [B,H,1])."""
+    import torch
+    B, H, _, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    need = fa_decode_paged_q4_workspace_size(B, H, k_codes.shape[1], max_seqlen_k, d, n_splits)
+    workspace = _workspace(workspace, need, q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((B, H, 1), dtype=torch.float32, device=q.device)
+    fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k, scale,
+                       descale_k, descale_v, n_splits, workspace, stream)
+    return o, lse
+
+
+def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
+                     max_seqlen_k: int, causal: bool = True, n_splits: int = 0, scale: float | None = None,
+                     descale_k: float = 1.0, descale_v: float = 1.0, stream=None, workspace=None):
+    """Packed queries [total_q, H, d] over a 4-bit paged cache, causal up to each one's own token
+    -> (O [total_q, H, d], lse [H, total_q])."""
+    import torch
+    total_q, H, d = q.shape
+    scale = d ** -0.5 if scale is None else scale
+    need = fa_fwd_paged_q4_workspace_size(block_table.shape[0], H, k_codes.shape[1], total_q, max_seqlen_q, max_seqlen_k,
+                                          d, n_splits)
+    workspace = _workspace(workspace, need, q.device)
+    o = torch.empty_like(q)
+    lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+    fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q,
+                    max_seqlen_k, scale, descale_k, descale_v, causal, n_splits, workspace, stream)
+    return o, lse
