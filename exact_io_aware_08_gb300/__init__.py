@@ -326,87 +326,128 @@ def fa_decode_paged(q, k_cache, v_cache, o, lse, block_table, seqlens_k, max_seq
 
 # The paged-cache calls look their tensors over before they pass pointers on: one device, the types
 # and shapes of include/fa.h, dense (the packed q, k, v of an append may be slices of a wider matrix).
+# Small calls are bound by this side, so a tensor is checked with as few calls into torch as will do,
+# and what is wrong with it is worked out only when something is.
+
+class _Torch:
+    """torch's names that every call needs, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.empty, self.empty_like = torch.empty, torch.empty_like
+        self.bf16, self.i32, self.u8 = torch.bfloat16, torch.int32, torch.uint8
+        self.e4m3, self.f32 = torch.float8_e4m3fn, torch.float32
+        self.device, self.current_device = torch.cuda.device, torch.cuda.current_device
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_names = None
+
+
+def _torch():
+    global _names
+    if _names is None:
+        _names = _Torch()
+    return _names
+
 
 def _bad(message):
     raise FaError(1, message)
 
 
-def _expect(name, t, dtypes, shape, device, strided=False):
-    """``shape``: None for a free extent.  ``strided``: only the last two dimensions are dense."""
-    if t.device != device or not t.is_cuda:
-        _bad(f"{name} must be a CUDA tensor on {device}, is on {t.device}")
-    if t.dtype not in dtypes:
-        _bad(f"{name} must be {' or '.join(str(x) for x in dtypes)}, is {t.dtype}")
-    if len(t.shape) != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+def _explain(name, t, dtype, shape, device, dense):
+    import torch
+    if not isinstance(t, torch.Tensor):
+        _bad(f"{name} must be a tensor, is {type(t).__name__}")
+    if not t.is_cuda or t.get_device() != device:
+        _bad(f"{name} must be a CUDA tensor on the cache's device, is on {t.device}")
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
         _bad(f"{name} must be {list(shape)}, is {list(t.shape)}")
-    if not t.is_contiguous():
-        if not strided or t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
-            _bad(f"{name} must be dense" + (" in its last two dimensions" if strided else ""))
+    _bad(f"{name} must be dense{dense}")
 
 
-def _types():
-    import torch
-    return (torch.bfloat16,), (torch.int32,), (torch.uint8,), (torch.uint8, torch.float8_e4m3fn), (torch.float32,)
+def _tensor(name, t, dtype, shape, device):
+    """The address of a dense tensor of this type, shape and device."""
+    if (t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        _explain(name, t, dtype, shape, device, "")
+    return t.data_ptr()
 
 
-def _launch(device, stream, name, *args):
-    """Calls ``name`` with the stream as its last argument, with ``device`` the current one."""
-    import torch
-    fn = getattr(load_library(), name)
-    if device.index == torch.cuda.current_device():
-        return _check(fn(*args, _stream(stream)))
-    with torch.cuda.device(device):
-        return _check(fn(*args, _stream(stream)))
+def _tokens(name, t, dtype, shape, device):
+    """(address, token stride) of packed tokens whose heads are dense."""
+    if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
+        _explain(name, t, dtype, shape, device, "")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 or (s1 != shape[2] and shape[1] > 1)) and t.numel():
+        _explain(name, t, dtype, shape, device, " in its last two dimensions")
+    return t.data_ptr(), s0
 
 
-def _expect_q4(k_codes, k_scales, v_codes, v_scales, H_kv, d):
-    """Checks a 4-bit cache; (device, num_blocks, H_kv, block_size, d)."""
-    _, _, u8, e4m3, _ = _types()
-    device = k_codes.device
+def _launch(device, stream, fn, *args):
+    """Calls ``fn`` with the stream as its last argument and ``device`` the current one."""
+    T = _torch()
+    if stream is None:
+        stream = T.raw_stream(device)
+    else:
+        stream = getattr(stream, "cuda_stream", stream)
+    if device == T.current_device():
+        status = fn(*args, stream)
+    else:
+        with T.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
+
+
+def _q4_cache(T, k_codes, k_scales, v_codes, v_scales):
+    """Checks a 4-bit cache; (device, addresses, num_blocks, H_kv, block_size, d)."""
     if k_codes.dim() != 4:
         _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
-    shape = k_codes.shape
-    if (H_kv is not None and shape[1] != H_kv) or (d is not None and shape[3] * 2 != d):
-        _bad(f"k_codes must be [num_blocks, {H_kv}, block_size, {d}/2], is {list(shape)}")
-    scales = (*shape[:3], shape[3] // 8)
-    _expect("k_codes", k_codes, u8, shape, device)
-    _expect("v_codes", v_codes, u8, shape, device)
-    _expect("k_scales", k_scales, e4m3, scales, device)
-    _expect("v_scales", v_scales, e4m3, scales, device)
-    return device, shape[0], shape[1], shape[2], shape[3] * 2
+    device, shape = k_codes.get_device(), k_codes.shape
+    nb, H_kv, bs, half = shape
+    scales = (nb, H_kv, bs, half // 8)
+    e4m3 = T.u8 if k_scales.dtype is T.u8 else T.e4m3
+    return (device, _tensor("k_codes", k_codes, T.u8, shape, device), _tensor("k_scales", k_scales, e4m3, scales, device),
+            _tensor("v_codes", v_codes, T.u8, shape, device), _tensor("v_scales", v_scales, e4m3, scales, device),
+            nb, H_kv, bs, 2 * half)
 
 
-def _token_stride(t):
-    return 0 if t is None else t.stride(0)
-
-
-def _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, device):
-    """Checks what both appends share; (n_seqs, H, H_kv, total, d, rotary_dim, n_positions)."""
-    bf16, i32, _, _, f32 = _types()
+def _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device):
+    """Checks what both appends share: (pointers before the cache's, after it, sizes, strides, blocks a sequence,
+    rotary_dim, n_positions)."""
     if k.dim() != 3 or block_table.dim() != 2:
         _bad("k must be [total, H_kv, d] and block_table [n_seqs, max_blocks]")
-    total, H_kv, d = k.shape
-    n_seqs = block_table.shape[0]
-    _expect("k", k, bf16, k.shape, device, True)
-    _expect("v", v, bf16, k.shape, device, True)
-    H = 0
+    total = k.shape[0]
+    n_seqs, max_blocks = block_table.shape
+    shape = (total, H_kv, d)
+    pk, sk = _tokens("k", k, T.bf16, shape, device)
+    pv, sv = _tokens("v", v, T.bf16, shape, device)
+    H, pq, po, sq = 0, None, None, 0
     if (q is None) != (q_out is None):
         _bad("q and q_out go together")
     if q is not None:
-        _expect("q", q, bf16, (total, None, d), device, True)
+        if q.dim() != 3:
+            _bad(f"q must be [total, H, d], is {list(q.shape)}")
         H = q.shape[1]
-        _expect("q_out", q_out, bf16, (total, H, d), device)
-    _expect("block_table", block_table, i32, block_table.shape, device)
-    _expect("cu_seqlens", cu_seqlens, i32, (n_seqs + 1,), device)
-    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
+        shape = (total, H, d)
+        pq, sq = _tokens("q", q, T.bf16, shape, device)
+        po = _tensor("q_out", q_out, T.bf16, shape, device)
     if (cos is None) != (sin is None):
         _bad("cos and sin go together")
-    rotary, n_positions = 0, 0
+    rotary, n_positions, pc, ps = 0, 0, None, None
     if cos is not None:
-        _expect("cos", cos, f32, (None, None), device)
-        _expect("sin", sin, f32, cos.shape, device)
-        rotary, n_positions = 2 * cos.shape[1], cos.shape[0]
-    return n_seqs, H, H_kv, total, d, rotary, n_positions
+        if cos.dim() != 2:
+            _bad(f"cos must be [n_positions, rotary_dim/2], is {list(cos.shape)}")
+        shape = cos.shape
+        n_positions, rotary = shape
+        pc, ps = _tensor("cos", cos, T.f32, shape, device), _tensor("sin", sin, T.f32, shape, device)
+    return ((pq, pk, pv, po),
+            (pc, ps, _tensor("cu_seqlens", cu_seqlens, T.i32, (n_seqs + 1,), device),
+             _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
+             _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device),
+             n_seqs, H, H_kv, total, sq, sk, sv, max_blocks), 2 * rotary, n_positions)
 
 
 def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seqlens_k, block_table,
@@ -414,81 +455,79 @@ def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seql
     """q, q_out [total, H, d] or None; k, v [total, H_kv, d]; k/v cache [num_blocks, block_size, H_kv, d];
     cos, sin fp32 [n_positions, rotary_dim/2] or None; cu_seqlens [n_seqs + 1], seqlens_k [n_seqs] and
     block_table [n_seqs, max_blocks] int32, all on the device."""
-    device = k_cache.device
-    n_seqs, H, H_kv, total, d, rotary, n_positions = _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k,
-                                                                  block_table, device)
-    _expect("k_cache", k_cache, _types()[0], (None, None, H_kv, d), device)
-    _expect("v_cache", v_cache, _types()[0], k_cache.shape, device)
-    _launch(device, stream, "fa_append_paged", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_cache), _ptr(v_cache),
-            _ptr(cos), _ptr(sin), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table), n_seqs, H, H_kv, total,
-            _token_stride(q), _token_stride(k), _token_stride(v), block_table.shape[1], k_cache.shape[1],
-            k_cache.shape[0], d, rotary, int(bool(interleaved)), n_positions)
+    T = _torch()
+    device = k_cache.get_device()
+    if k_cache.dim() != 4:
+        _bad(f"k_cache must be [num_blocks, block_size, H_kv, d], is {list(k_cache.shape)}")
+    shape = k_cache.shape
+    nb, bs, H_kv, d = shape
+    pkc, pvc = _tensor("k_cache", k_cache, T.bf16, shape, device), _tensor("v_cache", v_cache, T.bf16, shape, device)
+    head, tail, rotary, n_positions = _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device)
+    _launch(device, stream, (_lib or load_library()).fa_append_paged, *head, pkc, pvc, *tail, bs, nb, d, rotary,
+            1 if interleaved else 0, n_positions)
 
 
 def fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
                        block_table, descale_k: float, descale_v: float, interleaved: bool = False, stream=None):
-    """As fa_append_paged, with codes uint8 [num_blocks, H_kv, block_size, d/2] and scales (uint8 or
-    float8_e4m3fn) [num_blocks, H_kv, block_size, d/16]."""
-    device = k_codes.device
-    n_seqs, H, H_kv, total, d, rotary, n_positions = _append_args(q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k,
-                                                                  block_table, device)
-    _, num_blocks, _, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, H_kv, d)
-    _launch(device, stream, "fa_append_paged_q4", _ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_codes), _ptr(k_scales),
-            _ptr(v_codes), _ptr(v_scales), _ptr(cos), _ptr(sin), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table),
-            n_seqs, H, H_kv, total, _token_stride(q), _token_stride(k), _token_stride(v), block_table.shape[1],
-            block_size, num_blocks, d, rotary, int(bool(interleaved)), n_positions, float(descale_k), float(descale_v))
+    """As fa_append_paged, with codes uint8 [num_blocks, H_kv, block_size, d/2] and scales (both uint8 or
+    both float8_e4m3fn) [num_blocks, H_kv, block_size, d/16]."""
+    T = _torch()
+    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
+    head, tail, rotary, n_positions = _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device)
+    _launch(device, stream, (_lib or load_library()).fa_append_paged_q4, *head, kc, ks, vc, vs, *tail, bs, nb, d, rotary,
+            1 if interleaved else 0, n_positions, descale_k, descale_v)
 
 
 def fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table,
                        descale_k: float, descale_v: float, stream=None):
     """k, v [total, H_kv, d] bf16 are written."""
-    bf16, i32, _, _, _ = _types()
-    device, num_blocks, H_kv, block_size, d = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, None)
-    _expect("k", k, bf16, (None, H_kv, d), device)
-    _expect("v", v, bf16, k.shape, device)
-    _expect("block_table", block_table, i32, (None, None), device)
-    n_seqs = block_table.shape[0]
-    _expect("cu_seqlens", cu_seqlens, i32, (n_seqs + 1,), device)
-    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
-    _launch(device, stream, "fa_gather_paged_q4", _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(k),
-            _ptr(v), _ptr(cu_seqlens), _ptr(seqlens_k), _ptr(block_table), n_seqs, H_kv, k.shape[0],
-            block_table.shape[1], block_size, num_blocks, d, float(descale_k), float(descale_v))
+    T = _torch()
+    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
+    if k.dim() != 3 or block_table.dim() != 2:
+        _bad("k must be [total, H_kv, d] and block_table [n_seqs, max_blocks]")
+    shape = (k.shape[0], H_kv, d)
+    n_seqs, max_blocks = block_table.shape
+    _launch(device, stream, (_lib or load_library()).fa_gather_paged_q4, kc, ks, vc, vs, _tensor("k", k, T.bf16, shape, device),
+            _tensor("v", v, T.bf16, shape, device), _tensor("cu_seqlens", cu_seqlens, T.i32, (n_seqs + 1,), device),
+            _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
+            _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device), n_seqs, H_kv, shape[0], max_blocks,
+            bs, nb, d, descale_k, descale_v)
 
 
 def fa_decode_paged_q4_workspace_size(B: int, H: int, H_kv: int, max_seqlen_k: int, d: int, n_splits: int) -> int:
-    return int(load_library().fa_decode_paged_q4_workspace_size(B, H, H_kv, max_seqlen_k, d, n_splits))
+    return (_lib or load_library()).fa_decode_paged_q4_workspace_size(B, H, H_kv, max_seqlen_k, d, n_splits)
 
 
 def fa_fwd_paged_q4_workspace_size(n_seqs: int, H: int, H_kv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
                                    d: int, n_splits: int) -> int:
-    return int(load_library().fa_fwd_paged_q4_workspace_size(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d,
-                                                             n_splits))
+    return (_lib or load_library()).fa_fwd_paged_q4_workspace_size(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d, n_splits)
 
 
-def _expect_ws(ws, device):
-    if ws is not None and (ws.device != device or not ws.is_contiguous()):
-        _bad(f"the workspace must be dense and on {device}")
+def _scratch(ws, device):
+    """(address, bytes) of a workspace."""
+    if ws is None:
+        return None, 0
+    if ws.get_device() != device or not ws.is_contiguous():
+        _bad("the workspace must be dense and on the cache's device")
+    return ws.data_ptr(), ws.nbytes
 
 
 def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k: int,
                        scale: float, descale_k: float, descale_v: float, n_splits: int, ws, stream=None):
     """q, o [B,H,1,d]; lse [B,H,1]; a 4-bit cache as fa_append_paged_q4 writes it; block_table
     [B, max_blocks] int32; seqlens_k [B] int32.  H_kv (of the cache) divides H."""
-    bf16, i32, _, _, f32 = _types()
-    if q.dim() != 4:
-        _bad(f"q must be [B, H, 1, d], is {list(q.shape)}")
-    B, H, _, d = q.shape
-    device, num_blocks, H_kv, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, d)
-    _expect("q", q, bf16, (B, H, 1, d), device)
-    _expect("o", o, bf16, (B, H, 1, d), device)
-    _expect("lse", lse, f32, (B, H, 1), device)
-    _expect("block_table", block_table, i32, (B, None), device)
-    _expect("seqlens_k", seqlens_k, i32, (B,), device)
-    _expect_ws(ws, device)
-    _launch(device, stream, "fa_decode_paged_q4", _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
-            _ptr(o), _ptr(lse), _ptr(block_table), _ptr(seqlens_k), B, H, H_kv, block_table.shape[1], block_size,
-            num_blocks, int(max_seqlen_k), d, float(scale), float(descale_k), float(descale_v), int(n_splits), _ptr(ws),
-            _nbytes(ws))
+    T = _torch()
+    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
+    if q.dim() != 4 or block_table.dim() != 2:
+        _bad("q must be [B, H, 1, d] and block_table [B, max_blocks]")
+    B, H = q.shape[:2]
+    shape, max_blocks = (B, H, 1, d), block_table.shape[1]
+    pw, nw = _scratch(ws, device)
+    _launch(device, stream, (_lib or load_library()).fa_decode_paged_q4, _tensor("q", q, T.bf16, shape, device), kc, ks, vc, vs,
+            _tensor("o", o, T.bf16, shape, device), _tensor("lse", lse, T.f32, (B, H, 1), device),
+            _tensor("block_table", block_table, T.i32, (B, max_blocks), device),
+            _tensor("seqlens_k", seqlens_k, T.i32, (B,), device), B, H, H_kv, max_blocks, bs, nb, max_seqlen_k, d, scale,
+            descale_k, descale_v, n_splits, pw, nw)
 
 
 def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table,
@@ -496,23 +535,20 @@ def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_
                     n_splits: int, ws, stream=None):
     """q, o [total_q, H, d]; lse [H, total_q]; cu_seqlens_q [n_seqs + 1] int32; the rest as for
     fa_decode_paged_q4."""
-    bf16, i32, _, _, f32 = _types()
+    T = _torch()
+    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
     if q.dim() != 3 or block_table.dim() != 2:
         _bad("q must be [total_q, H, d] and block_table [n_seqs, max_blocks]")
-    total_q, H, d = q.shape
-    n_seqs = block_table.shape[0]
-    device, num_blocks, H_kv, block_size, _ = _expect_q4(k_codes, k_scales, v_codes, v_scales, None, d)
-    _expect("q", q, bf16, q.shape, device)
-    _expect("o", o, bf16, q.shape, device)
-    _expect("lse", lse, f32, (H, total_q), device)
-    _expect("block_table", block_table, i32, block_table.shape, device)
-    _expect("cu_seqlens_q", cu_seqlens_q, i32, (n_seqs + 1,), device)
-    _expect("seqlens_k", seqlens_k, i32, (n_seqs,), device)
-    _expect_ws(ws, device)
-    _launch(device, stream, "fa_fwd_paged_q4", _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales),
-            _ptr(o), _ptr(lse), _ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(block_table), n_seqs, H, H_kv, total_q,
-            int(max_seqlen_q), block_table.shape[1], block_size, num_blocks, int(max_seqlen_k), d, float(scale),
-            float(descale_k), float(descale_v), int(bool(causal)), int(n_splits), _ptr(ws), _nbytes(ws))
+    total_q, H = q.shape[:2]
+    shape = (total_q, H, d)
+    n_seqs, max_blocks = block_table.shape
+    pw, nw = _scratch(ws, device)
+    _launch(device, stream, (_lib or load_library()).fa_fwd_paged_q4, _tensor("q", q, T.bf16, shape, device), kc, ks, vc, vs,
+            _tensor("o", o, T.bf16, shape, device), _tensor("lse", lse, T.f32, (H, total_q), device),
+            _tensor("cu_seqlens_q", cu_seqlens_q, T.i32, (n_seqs + 1,), device),
+            _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
+            _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device), n_seqs, H, H_kv, total_q, max_seqlen_q,
+            max_blocks, bs, nb, max_seqlen_k, d, scale, descale_k, descale_v, 1 if causal else 0, n_splits, pw, nw)
 
 
 def fa_debug_counters(counters):
@@ -673,8 +709,7 @@ def rotary_tables(n_positions: int, rotary_dim: int, base: float = 10000.0, devi
 
 
 def _rotated(q, k, q_out):
-    import torch
-    return torch.empty(q.shape, dtype=q.dtype, device=k.device) if q is not None and q_out is None else q_out
+    return _torch().empty(q.shape, dtype=q.dtype, device=k.device) if q is not None and q_out is None else q_out
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, q=None, cos=None, sin=None,
@@ -700,20 +735,21 @@ def gather_paged_q4(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlen
                     descale_k: float = 1.0, descale_v: float = 1.0, stream=None):
     """The last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence of a 4-bit cache as packed bf16
     (k, v [total, H_kv, d])."""
-    import torch
     if k_codes.dim() != 4:
         _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
-    k = torch.empty((total, k_codes.shape[1], 2 * k_codes.shape[3]), dtype=torch.bfloat16, device=k_codes.device)
-    v = torch.empty_like(k)
+    T = _torch()
+    _, H_kv, _, half = k_codes.shape
+    k = T.empty((total, H_kv, 2 * half), dtype=T.bf16, device=k_codes.device)
+    v = T.empty_like(k)
     fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table, descale_k,
                        descale_v, stream)
     return k, v
 
 
-def _workspace(workspace, need, device):
-    import torch
-    if workspace is None or _nbytes(workspace) < need:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+def _q4_workspace(T, workspace, need, device):
+    """The caller's workspace where it is large enough; none where the call needs none."""
+    if need > 16 and (workspace is None or workspace.nbytes < need):
+        return T.empty(need, dtype=T.u8, device=device)
     return workspace
 
 
@@ -721,15 +757,15 @@ def decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seqlen
                     n_splits: int = 0, scale: float | None = None, descale_k: float = 1.0, descale_v: float = 1.0,
                     stream=None, workspace=None):
     """Single-query decode over a 4-bit paged cache, grouped heads -> (O [B,H,1,d], lse [B,H,1])."""
-    import torch
+    T = _torch()
     B, H, _, d = q.shape
-    scale = d ** -0.5 if scale is None else scale
-    need = fa_decode_paged_q4_workspace_size(B, H, k_codes.shape[1], max_seqlen_k, d, n_splits)
-    workspace = _workspace(workspace, need, q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, 1), dtype=torch.float32, device=q.device)
-    fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k, scale,
-                       descale_k, descale_v, n_splits, workspace, stream)
+    device = q.device
+    need = (_lib or load_library()).fa_decode_paged_q4_workspace_size(B, H, k_codes.shape[1], max_seqlen_k, d, n_splits)
+    workspace = _q4_workspace(T, workspace, need, device)
+    o = T.empty_like(q)
+    lse = T.empty((B, H, 1), dtype=T.f32, device=device)
+    fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k,
+                       d ** -0.5 if scale is None else scale, descale_k, descale_v, n_splits, workspace, stream)
     return o, lse
 
 
@@ -738,14 +774,15 @@ def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
                      descale_k: float = 1.0, descale_v: float = 1.0, stream=None, workspace=None):
     """Packed queries [total_q, H, d] over a 4-bit paged cache, causal up to each one's own token
     -> (O [total_q, H, d], lse [H, total_q])."""
-    import torch
+    T = _torch()
     total_q, H, d = q.shape
-    scale = d ** -0.5 if scale is None else scale
-    need = fa_fwd_paged_q4_workspace_size(block_table.shape[0], H, k_codes.shape[1], total_q, max_seqlen_q, max_seqlen_k,
-                                          d, n_splits)
-    workspace = _workspace(workspace, need, q.device)
-    o = torch.empty_like(q)
-    lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
+    device = q.device
+    need = (_lib or load_library()).fa_fwd_paged_q4_workspace_size(block_table.shape[0], H, k_codes.shape[1], total_q, max_seqlen_q,
+                                                         max_seqlen_k, d, n_splits)
+    workspace = _q4_workspace(T, workspace, need, device)
+    o = T.empty_like(q)
+    lse = T.empty((H, total_q), dtype=T.f32, device=device)
     fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q,
-                    max_seqlen_k, scale, descale_k, descale_v, causal, n_splits, workspace, stream)
+                    max_seqlen_k, d ** -0.5 if scale is None else scale, descale_k, descale_v, causal, n_splits, workspace,
+                    stream)
     return o, lse

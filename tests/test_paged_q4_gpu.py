@@ -241,7 +241,8 @@ def check_attention(o, lse, want):
     none = np.isneginf(rl)
     assert (np.isneginf(lse) == none).all() and (o[none] == 0).all()
     assert (np.abs(o - ro) <= bo).all(), float((np.abs(o - ro) / bo)[~none].max())
-    assert (np.abs(lse - rl)[~none] <= bl[~none]).all(), float((np.abs(lse - rl)[~none] / bl[~none]).max())
+    off = np.abs(lse[~none] - rl[~none]) / bl[~none]
+    assert (off <= 1).all(), float(off.max())
 
 
 # (lens, H, H_kv, d, block, n_splits)
