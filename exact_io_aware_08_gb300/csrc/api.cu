@@ -614,10 +614,10 @@ fa_status_t append(const void* q, const void* k, const void* v, void* q_out, voi
 
 // Split count of a 4-bit attention call (n_splits <= 0: the library's choice), or an error.
 fa_status_t q4_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int max_seqlen_k, int* n_splits) {
-  const long long items = static_cast<long long>(n_seqs) * H_kv * fa::q4_row_blocks(H, H_kv, max_seqlen_q);
+  const long long items = fa::q4_items(n_seqs, H, H_kv, max_seqlen_q);
   if (*n_splits > fa::kDecodeMaxSplits)
     return fail(FA_ERR_UNSUPPORTED, "n_splits=%d exceeds %d", *n_splits, fa::kDecodeMaxSplits);
-  if (*n_splits <= 0) *n_splits = fa::q4_auto_splits(items, max_seqlen_k);
+  if (*n_splits <= 0) *n_splits = fa::q4_auto_splits(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k);
   if (items >= (1LL << 31) || items * 2 * *n_splits >= (1LL << 31))
     return fail(FA_ERR_UNSUPPORTED, "too many (sequence, key head, row block, split) items");
   return FA_OK;
@@ -673,7 +673,8 @@ fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, 
   a.n_seqs = n_seqs; a.H = H; a.H_kv = H_kv; a.total_q = total_q; a.max_seqlen_q = max_seqlen_q; a.d = d;
   a.num_blocks = num_blocks; a.block_size = block_size; a.max_blocks = max_blocks; a.max_seqlen_k = max_seqlen_k;
   a.causal = causal ? 1 : 0; a.scale = scale; a.descale_k = descale_k; a.descale_v = descale_v;
-  a.n_splits = n_splits; a.chunk = fa::decode_chunk(max_seqlen_k, n_splits);
+  a.n_splits = n_splits;
+  a.chunk = fa::q4_chunk(max_seqlen_k, n_splits, fa::q4_use_tiles(H, H_kv, max_seqlen_q));
   cudaError_t e = fa::launch_attend_q4(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
 }
@@ -783,7 +784,8 @@ fa_status_t fa_sync_status(void* stream) {
   int where = 0, w = 0;
   cudaError_t (*fetch[])(cudaStream_t, unsigned int*, int*) = {
       fa::status_fetch_fwd, fa::status_fetch_bwd, fa::status_fetch_decode,
-      fa::status_fetch_selftest, fa::status_fetch_paged, fa::status_fetch_attend_q4};
+      fa::status_fetch_selftest, fa::status_fetch_paged, fa::status_fetch_attend_q4,
+      fa::status_fetch_attend_q4_tile};
   for (auto f : fetch) {
     cudaError_t e = f(s, &c, &w);
     if (e != cudaSuccess) return cuda_fail(e, "fa_sync_status");

@@ -542,20 +542,31 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   const int grid = min(p.n_items, C::MIN_CTAS * q4_sm_count());
   log_launch("attend_q4_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_splits == 1) return e;
+  return cudaGetLastError();
+}
+
+template <int D>
+static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t stream) {
   const long long warps = static_cast<long long>(a.total_q) * a.H;
   const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
   log_launch("attend_q4_merge_kernel<D>", blocks, 128, 0ull);
-  attend_q4_merge_kernel<D><<<blocks, 128, 0, stream>>>(a.part, p.o, a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.n_splits, a.descale_v);
+  attend_q4_merge_kernel<D><<<blocks, 128, 0, stream>>>(a.part, static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H,
+                                                        a.total_q, a.n_splits, a.descale_v);
   return cudaGetLastError();
 }
 
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
-  // 8 rows suffice for up to 8 query heads a key head at one token; else 16 share the unpacked keys
-  const bool small = static_cast<long long>(a.H / a.H_kv) * a.max_seqlen_q <= 8;
-  if (a.d == 64) return small ? launch_attend_q4_d<64, 1>(a, stream) : launch_attend_q4_d<64, 2>(a, stream);
-  return small ? launch_attend_q4_d<128, 1>(a, stream) : launch_attend_q4_d<128, 2>(a, stream);
+  cudaError_t e;
+  if (q4_use_tiles(a.H, a.H_kv, a.max_seqlen_q)) {
+    e = launch_attend_q4_tile(a, stream);
+  } else {
+    // 8 rows suffice for up to 8 query heads a key head at one token; else 16 share the unpacked keys
+    const bool small = q4_rows(a.H, a.H_kv, a.max_seqlen_q) <= 8;
+    if (a.d == 64) e = small ? launch_attend_q4_d<64, 1>(a, stream) : launch_attend_q4_d<64, 2>(a, stream);
+    else e = small ? launch_attend_q4_d<128, 1>(a, stream) : launch_attend_q4_d<128, 2>(a, stream);
+  }
+  if (e != cudaSuccess || a.n_splits == 1) return e;
+  return a.d == 64 ? launch_attend_q4_merge<64>(a, stream) : launch_attend_q4_merge<128>(a, stream);
 }
 
 }  // namespace fa

@@ -1,0 +1,546 @@
+// Attention of many query rows over a paged cache held in 4 bits, on the tensor core that reads
+// shared memory (the form for parts of prompts; attend_q4.cu has the one for single tokens).
+//
+// A CTA owns 256 rows of one key head, in two tiles of 128.  Rows are (query token, query head of the
+// group) pairs, token by token, so that a tile is full whatever the group's size, and the rows of a
+// token lie side by side in memory.  The mathematics is attend_q4.cu's: codes * scales are exact fp16
+// numbers, query rows are brought to fp16 by a power of two, weights 2^(s - m) <= 2^8 are rounded to
+// fp16, sums are fp32.
+//
+// Roles (512 threads, one CTA an SM):
+//   warp 0       copies codes and scales, 64 keys a stage, by bulk copies.
+//   warp 1       issues the products (the whole warp converged, one elected lane):
+//                  S_t = Q_t K_j^T   both operands from shared memory
+//                  O_t += P_t V_j    P_t from tensor memory
+//                in the order PV_0(j), S_0(j+1), PV_1(j), S_1(j+1).
+//   warp 2       joins the hand-off of P_t once V_j and K_(j+1) are there (warp 3 idles).
+//   warps 4-11   softmax, thread = row; they also bring the rows of Q in and write those of O out.
+//   warps 12-15  unpack: a lane takes 16 elements (8 code bytes, one scale), and writes 32 bytes of
+//                fp16 into the 128-byte-swizzled tile, from where K is read K-major and V MN-major.
+// Tensor memory: S_0, S_1 (P_t over the first half of S_t), O_0, O_1.
+//
+// Unpacking costs about 1.6 instructions an element and is shared by 256 rows: some 400 issue slots of
+// each SM quarter a 128-key tile, beside some 1300 of the softmax and 2048 clocks of products.
+#include "fa_kernels.h"
+#include "q4.cuh"
+
+namespace fa {
+
+template <int D>
+struct Q4TCfg {
+  static constexpr int BM = 128, BN = 128;
+  static constexpr int CH = D / 64;                           // 64-column chunks of a tile
+  static constexpr int CHUNK = 128 * 128;
+  static constexpr int TILE = 128 * D * 2;                    // fp16 tile of Q, K or V
+  static constexpr int NS = 2;                                // K and V tiles each
+  static constexpr int CB = D / 2, SB = D / 16;
+  static constexpr int CKEYS = 64;                            // keys of a code stage
+  static constexpr int OFF_CV = CKEYS * CB;                   // inside a code stage
+  static constexpr int OFF_CKS = 2 * CKEYS * CB;
+  static constexpr int OFF_CVS = OFF_CKS + CKEYS * SB;
+  static constexpr int CSTAGE = OFF_CVS + CKEYS * SB;
+  static constexpr int NC = D == 128 ? 3 : 6;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + NS * TILE;
+  static constexpr int OFF_C = OFF_V + NS * TILE;
+  static constexpr int OFF_BAR = OFF_C + NC * CSTAGE;
+  // q_full, k_full[NS], k_empty[NS], v_full[NS], v_empty[NS], s_full[2], o_done[2], c_full[NC], c_empty[NC]
+  static constexpr int NBAR = 1 + 4 * NS + 4 + 2 * NC;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t T_S = 0, T_O = 256;
+  static constexpr int THREADS = 512;
+  static constexpr int UNPACK_WARPS = 4;
+  // launched with 128 registers a thread; 128 * 64 + 256 * 168 + 128 * 96 = 63488 = 512 * 124
+  static constexpr uint32_t REG_CTRL = 64, REG_SOFTMAX = 168, REG_UNPACK = 96;
+  static constexpr int REG_NEED = 128 * 64 + 256 * 168 + 128 * 96;
+  static constexpr float RESCALE = 8.f;
+  static constexpr uint32_t BAR_P = 3, BAR_P_THREADS = 128 + 32 + 32;
+};
+
+struct Q4TParams {
+  const uint16_t* q;
+  const uint8_t *kc, *ks, *vc, *vs;
+  uint16_t* o;
+  float *lse, *part;
+  const int *cu_q, *seqlens, *table;
+  int n_seqs, H, H_kv, G, total_q, max_q, max_k, causal, num_blocks, block_size, max_blocks, piece;
+  int n_splits, chunk, row_blocks;
+  float score, descale_v;
+};
+
+// fp16 A and B, fp32 accumulator
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
+  return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+template <int D>
+__global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(const __grid_constant__ Q4TParams p) {
+  using C = Q4TCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1k(smem_raw);
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sC = smem + C::OFF_C;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* k_empty = k_full + C::NS;
+  uint64_t* v_full = k_empty + C::NS;
+  uint64_t* v_empty = v_full + C::NS;
+  uint64_t* s_full = v_empty + C::NS;
+  uint64_t* o_done = s_full + 2;
+  uint64_t* c_full = o_done + 2;
+  uint64_t* c_empty = c_full + C::NC;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  // Item: row blocks with the most keys first over all sequences and heads, then the next.
+  const int per_rb = p.n_seqs * p.H_kv * p.n_splits;
+  const int rb = p.row_blocks - 1 - static_cast<int>(blockIdx.x) / per_rb;
+  int w = static_cast<int>(blockIdx.x) % per_rb;
+  const int split = w % p.n_splits;
+  w /= p.n_splits;
+  const int hkv = w % p.H_kv;
+  const int b = w / p.H_kv;
+  int first = b, nq = 1;
+  if (p.cu_q) {
+    first = __ldg(p.cu_q + b);
+    const int end = __ldg(p.cu_q + b + 1);
+    nq = end - first;
+    if (first < 0 || end < first || end > p.total_q || nq > p.max_q) {
+      if (threadIdx.x == 0 && rb == 0) report_device_error(FA_DEV_BAD_CONFIG, 440);
+      return;
+    }
+  }
+  int len = __ldg(p.seqlens + b);
+  if (len < 0 || len > p.max_k) {
+    if (threadIdx.x == 0 && rb == 0) report_device_error(FA_DEV_BAD_CONFIG, 441);
+    len = 0;
+  }
+  const int rows = nq * p.G;
+  const int row0 = rb * 2 * C::BM;
+  if (row0 >= rows) return;                                   // whole CTA, before any shared state
+  // Row r of the sequence sees its first seen(r) keys; the item's keys are [key0, key_end), tile t
+  // runs n_t[t] key tiles of 128.
+  auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
+  const int key0 = split * p.chunk;
+  int n_t[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(key0 + p.chunk, seen(row0 + (t + 1) * C::BM - 1));
+    n_t[t] = (row0 + t * C::BM >= rows || last <= key0) ? 0 : (last - key0 + C::BN - 1) / C::BN;
+  }
+  const int n_max = max(n_t[0], n_t[1]);
+  const int key_end = min(key0 + p.chunk, seen(rows - 1 < row0 + 2 * C::BM - 1 ? rows - 1 : row0 + 2 * C::BM - 1));
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 256);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&k_full[s], C::UNPACK_WARPS);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_full[s], C::UNPACK_WARPS);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&s_full[t], 1);
+      mbar_init(&o_done[t], 1);
+    }
+    for (int s = 0; s < C::NC; ++s) {
+      mbar_init(&c_full[s], 1);
+      mbar_init(&c_empty[s], C::UNPACK_WARPS);
+    }
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < 4) {
+    setmaxnreg_dec<C::REG_CTRL>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- copies of codes and scales
+      const int pieces = C::CKEYS / p.piece;
+      bool ok = true;
+      int window = -1, tab = 0, g = 0;
+      const int n_st = 2 * n_max;                             // code stages (the last may hold no key)
+      for (; ok && g < n_st; ++g) {
+        const int s = g % C::NC, u = g / C::NC;
+        const int kk = key0 + g * C::CKEYS;
+        const int last = (min(kk + C::CKEYS, key_end) - 1) / p.block_size;
+        if (kk < key_end && (window < 0 || last >= window + 32)) {
+          window = kk / p.block_size;
+          const int blk = window + lane;
+          tab = blk <= (key_end - 1) / p.block_size ? __ldg(p.table + static_cast<size_t>(b) * p.max_blocks + blk) : 0;
+        }
+        const int key = kk + (lane < pieces ? lane : 0) * p.piece;
+        const int blk = key / p.block_size;
+        int page = __shfl_sync(0xffffffffu, tab, (blk - window) & 31);
+        const bool mine = lane < pieces && key < key_end;
+        if (mine && (page < 0 || page >= p.num_blocks)) {
+          report_device_error(FA_DEV_BAD_CONFIG, 442);
+          page = 0;                                           // stays in bounds; the result is reported invalid
+        }
+        if (u > 0 && !(ok = mbar_wait_warp(&c_empty[s], (u - 1) & 1, abort_flag, 450))) break;
+        const int live = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&c_full[s], live * p.piece * 2 * (C::CB + C::SB));
+        __syncwarp();
+        if (mine) {
+          uint8_t* st = sC + s * C::CSTAGE;
+          const size_t row = (static_cast<size_t>(page) * p.H_kv + hkv) * p.block_size + (key - blk * p.block_size);
+          const int at = lane * p.piece;
+          bulk_load(st + at * C::CB, p.kc + row * C::CB, p.piece * C::CB, &c_full[s]);
+          bulk_load(st + C::OFF_CKS + at * C::SB, p.ks + row * C::SB, p.piece * C::SB, &c_full[s]);
+          bulk_load(st + C::OFF_CV + at * C::CB, p.vc + row * C::CB, p.piece * C::CB, &c_full[s]);
+          bulk_load(st + C::OFF_CVS + at * C::SB, p.vs + row * C::SB, p.piece * C::SB, &c_full[s]);
+        }
+        __syncwarp();
+      }
+      // After an abort: let every copy land that was started.
+      if (!ok)
+        for (int x = max(0, g - C::NC); x < g; ++x) mbar_wait_warp(&c_full[x % C::NC], (x / C::NC) & 1, nullptr, 451);
+    } else if (warp == 1) {
+      // -------------------------------------------------------------- products
+      // After a failed wait the warp keeps joining every hand-off, issuing nothing.
+      if (n_max > 0) {
+        const uint32_t idesc_s = idesc_f16_f32(128, 128, 0, 0);
+        const uint32_t idesc_o = idesc_f16_f32(128, D, 0, 1);
+        const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 0, 1024);
+        const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 0, 1024);
+        const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), C::CHUNK, 1024);
+        auto issue_s = [&](int t, int j) {
+          const uint64_t a = desc_advance(dq0, t * C::TILE);
+          const uint64_t bd = desc_advance(dk0, (j % C::NS) * C::TILE);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = (ks >> 2) * C::CHUNK + (ks & 3) * 32;
+            umma_ss_w(tbase + C::T_S + t * 128, desc_advance(a, off), desc_advance(bd, off), idesc_s, ks > 0);
+          }
+          umma_commit_w(&s_full[t]);
+        };
+        auto issue_pv = [&](int t, int j, bool fresh) {
+          const uint64_t bd = desc_advance(dv0, (j % C::NS) * C::TILE);
+#pragma unroll
+          for (int ks = 0; ks < C::BN / 16; ++ks)
+            umma_ts_w(tbase + C::T_O + t * 128, tbase + C::T_S + t * 128 + ks * 8, desc_advance(bd, ks * 16 * 128), idesc_o,
+                      (!fresh || ks > 0) ? 1u : 0u);
+        };
+        bool ok = mbar_wait_warp(q_full, 0, abort_flag, 452) && mbar_wait_warp(&k_full[0], 0, abort_flag, 453);
+        if (ok) {
+          tc_fence_after();
+          if (n_t[0] > 0) issue_s(0, 0);
+          if (n_t[1] > 0) issue_s(1, 0);
+          umma_commit_w(&k_empty[0]);
+        }
+        for (int j = 0; j < n_max; ++j) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (j < n_t[t]) {
+              __syncwarp();
+              named_bar_sync(C::BAR_P + t, C::BAR_P_THREADS);
+              if (ok) {
+                tc_fence_after();
+                issue_pv(t, j, j == 0);
+                if (j + 1 == n_t[t]) umma_commit_w(&o_done[t]);
+              }
+            }
+            if (ok && j + 1 < n_t[t]) issue_s(t, j + 1);
+          }
+          if (ok) {
+            umma_commit_w(&v_empty[j % C::NS]);
+            if (j + 1 < n_max) umma_commit_w(&k_empty[(j + 1) % C::NS]);
+          }
+        }
+      }
+    } else if (warp == 2) {
+      // -------------------------------------------------------------- joins P's hand-off once V_j, K_(j+1) are there
+      bool ok = true;
+      for (int j = 0; j < n_max; ++j) {
+        if (ok) ok = mbar_wait_warp(&v_full[j % C::NS], (j / C::NS) & 1, abort_flag, 454);
+        if (ok && j + 1 < n_max) ok = mbar_wait_warp(&k_full[(j + 1) % C::NS], ((j + 1) / C::NS) & 1, abort_flag, 455);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (j < n_t[t]) {
+            __syncwarp();
+            named_bar_sync(C::BAR_P + t, C::BAR_P_THREADS);
+          }
+      }
+    }
+  } else if (warp >= 12) {
+    // ---------------------------------------------------------------- unpacking
+    setmaxnreg_dec<C::REG_UNPACK>();
+    constexpr int BLK = D / 16;                               // scale blocks of a row
+    constexpr int RPW = 32 / BLK;                             // rows a warp takes at once
+    const int blk = lane % BLK, rsub = lane / BLK;
+    // D = 128: the blocks of the second chunk write their two 16-byte units the other way round, so
+    // that the eight lanes of a row reach eight different bank groups
+    const int flip = (D == 128 && blk >= 4) ? 1 : 0;
+    auto unpack = [&](const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int key_base, int row_base) {
+#pragma unroll
+      for (int i = 0; i < C::CKEYS / (RPW * C::UNPACK_WARPS); ++i) {
+        const int r = ((warp - 12) * (C::CKEYS / (RPW * C::UNPACK_WARPS)) + i) * RPW + rsub;
+        const uint2 cd = *reinterpret_cast<const uint2*>(codes + r * C::CB + blk * 8);
+        uint32_t e = scales[r * C::SB + blk];
+        // behind the item's keys lies anything, a scale that is no number among it
+        if (key_base + r >= key_end) e = 0;
+        const uint32_t s = e4m3x2_to_f16(e * 0x0101u);
+        uint32_t h[2][4];
+        e2m1x8_to_f16(cd.x, h[0]);
+        e2m1x8_to_f16(cd.y, h[1]);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) h[k >> 2][k & 3] = hmul2(h[k >> 2][k & 3], s);
+        uint8_t* dst = tile + (blk >> 2) * C::CHUNK;
+        const int row = row_base + r;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int un = k ^ flip;
+          const uint4 v = un ? make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]) : make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]);
+          *reinterpret_cast<uint4*>(dst + sw128_offset(row, ((blk & 3) * 2 + un) * 8)) = v;
+        }
+      }
+    };
+    auto done = [&](uint64_t* bar) {                          // this warp's part is written: hand it to the tensor core
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    bool ok = true;
+    for (int j = 0; ok && j < n_max; ++j) {
+      const int s = j % C::NS, u = j / C::NS;
+      const int g0 = 2 * j, g1 = 2 * j + 1;
+      uint8_t* c0 = sC + (g0 % C::NC) * C::CSTAGE;
+      uint8_t* c1 = sC + (g1 % C::NC) * C::CSTAGE;
+      const int kk = key0 + j * C::BN;
+      if (!(ok = mbar_wait_warp(&c_full[g0 % C::NC], (g0 / C::NC) & 1, abort_flag, 456))) break;
+      if (u > 0 && !(ok = mbar_wait_warp(&k_empty[s], (u - 1) & 1, abort_flag, 457))) break;
+      unpack(c0, c0 + C::OFF_CKS, sK + s * C::TILE, kk, 0);
+      if (!(ok = mbar_wait_warp(&c_full[g1 % C::NC], (g1 / C::NC) & 1, abort_flag, 458))) break;
+      unpack(c1, c1 + C::OFF_CKS, sK + s * C::TILE, kk + C::CKEYS, C::CKEYS);
+      done(&k_full[s]);
+      if (u > 0 && !(ok = mbar_wait_warp(&v_empty[s], (u - 1) & 1, abort_flag, 459))) break;
+      unpack(c0 + C::OFF_CV, c0 + C::OFF_CVS, sV + s * C::TILE, kk, 0);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c_empty[g0 % C::NC]);
+      unpack(c1 + C::OFF_CV, c1 + C::OFF_CVS, sV + s * C::TILE, kk + C::CKEYS, C::CKEYS);
+      done(&v_full[s]);
+      if (lane == 0) mbar_arrive(&c_empty[g1 % C::NC]);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax, thread = row
+    setmaxnreg_inc<C::REG_SOFTMAX>();
+    const int t = (warp - 4) >> 2;
+    const int sub = warp & 3;                                 // TMEM lane quarter this warp may access
+    const int row = sub * 32 + lane;
+    const int r = row0 + t * C::BM + row;
+    const uint32_t t_lane = static_cast<uint32_t>(sub * 32) << 16;
+    const uint32_t t_s = tbase + t_lane + C::T_S + t * 128;
+    const uint32_t t_o = tbase + t_lane + C::T_O + t * 128;
+    const int n = t == 0 ? n_t[0] : n_t[1];
+    const int tok = first + r / p.G, head = hkv * p.G + r % p.G;
+    const size_t th = static_cast<size_t>(tok) * p.H + head;
+    float c2;                                                 // score factor of the row
+    {
+      uint4 x[D / 8];
+      float big = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + th * D) + i);
+        const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(ww[k])), fabsf(bf16_hi(ww[k]))));
+      }
+      // the largest element goes to [2^14, 2^15); exponents such that the power and its inverse are normal
+      const int ex = big == 0.f ? 14 : max(-100, static_cast<int>(__float_as_uint(big) >> 23) - 127);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+      c2 = p.score * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        uint32_t h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(ww[k]) * up, bf16_hi(ww[k]) * up);
+        *reinterpret_cast<uint4*>(sQ + t * C::TILE + (i >> 3) * C::CHUNK + sw128_offset(row, (i & 7) * 8)) =
+            make_uint4(h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(q_full);
+    }
+    const int lim = min(key_end, seen(r));                    // keys below it are this row's
+    float m = -INFINITY, l = 0.f;                             // reference (raw units) and sum of the weights
+    bool ok = true;
+    int handed = 0;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t rr[32];
+        tmem_ld32(t_s + k * 32, rr);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
+      }
+      tmem_wait_ld();
+      const int k0 = key0 + j * C::BN;
+      if (__any_sync(0xffffffffu, k0 + C::BN > lim)) {
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if (k0 + k >= lim) s[k] = -INFINITY;
+      }
+      float mq[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        mq[g] = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
+#pragma unroll
+        for (int k = 3; k < 31; k += 2) mq[g] = fmax3(mq[g], s[32 * g + k], s[32 * g + k + 1]);
+        mq[g] = fmaxf(mq[g], s[32 * g + 31]);
+      }
+      const float cand = fmaxf(m, fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]));
+      // a row that sees none of the tile's keys has nothing to move
+      const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > C::RESCALE);
+      if (__any_sync(0xffffffffu, move)) {
+        const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
+        if (move) {
+          l *= alpha;
+          m = cand;
+        }
+        if (j > 0) {
+          // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order)
+#pragma unroll
+          for (int k = 0; k < D / 32; ++k) {
+            uint32_t rr[32];
+            tmem_ld32(t_o + k * 32, rr);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float2 v = fmul2(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), make_float2(alpha, alpha));
+              rr[i] = __float_as_uint(v.x);
+              rr[i + 1] = __float_as_uint(v.y);
+            }
+            tmem_st32(t_o + k * 32, rr);
+          }
+        }
+      }
+      const float ms = (m == -INFINITY) ? 0.f : m * c2;
+      const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
+      float2 rs[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) rs[g] = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float2 x = ffma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2v, nms);
+          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+          pk[k] = pack_f16x2(e.x, e.y);
+          rs[k & 3] = fadd2(rs[k & 3], e);
+        }
+        tmem_st32(t_s + h * 32, pk);
+      }
+      const float2 rs01 = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
+      l += rs01.x + rs01.y;
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      named_bar_arrive(C::BAR_P + t, C::BAR_P_THREADS);
+      ++handed;
+    }
+    // after an abort: keep joining (blocking) the remaining hand-offs
+    for (; handed < n; ++handed) {
+      __syncwarp();
+      named_bar_sync(C::BAR_P + t, C::BAR_P_THREADS);
+    }
+    if (ok && n > 0) {
+      ok = mbar_wait_warp(&o_done[t], 0, abort_flag, 461);
+      tc_fence_after();
+    }
+    if (ok && row0 + t * C::BM < rows) {
+      const bool none = l == 0.f;                             // a row that sees no key (of the chunk)
+      const float inv = none ? 0.f : p.descale_v / l;
+      float* dst = p.n_splits > 1 ? p.part + (th * p.n_splits + split) * (D + 2) : nullptr;
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t rr[32];
+        if (n > 0) {
+          tmem_ld32(t_o + k * 32, rr);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) rr[i] = 0u;
+        }
+        if (r < rows) {
+          if (dst) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              *reinterpret_cast<float2*>(dst + k * 32 + i) = make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              uint32_t h[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                h[e] = none ? 0u : pack_bf16x2(__uint_as_float(rr[i + 2 * e]) * inv, __uint_as_float(rr[i + 2 * e + 1]) * inv);
+              *reinterpret_cast<uint4*>(p.o + th * D + k * 32 + i) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+        }
+      }
+      if (r < rows) {
+        if (dst)
+          *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : m * c2, l);
+        else
+          p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
+              none ? -INFINITY : (fmaf(m, c2, log2f(l))) * 0.6931471805599453f;
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, C::TMEM_COLS);
+  }
+}
+
+template <int D>
+static cudaError_t launch_attend_q4_tile_d(const PagedQ4Args& a, cudaStream_t stream) {
+  using C = Q4TCfg<D>;
+  Q4TParams p{};
+  p.q = static_cast<const uint16_t*>(a.q);
+  p.kc = a.k_codes; p.ks = a.k_scales; p.vc = a.v_codes; p.vs = a.v_scales;
+  p.o = static_cast<uint16_t*>(a.o); p.lse = a.lse; p.part = a.part;
+  p.cu_q = a.cu_q; p.seqlens = a.seqlens; p.table = a.block_table;
+  p.n_seqs = a.n_seqs; p.H = a.H; p.H_kv = a.H_kv; p.G = a.H / a.H_kv; p.total_q = a.total_q;
+  p.max_q = a.max_seqlen_q; p.max_k = a.max_seqlen_k; p.causal = a.causal;
+  p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.max_blocks = a.max_blocks;
+  p.piece = a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;
+  p.n_splits = a.n_splits; p.chunk = a.chunk;
+  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 2 * C::BM - 1) / (2 * C::BM));
+  p.score = a.scale * 1.4426950408889634f * a.descale_k;
+  p.descale_v = a.descale_v;
+  static int attr_done[64] = {0};
+  cudaError_t e = ensure_smem_attr(attend_q4_tile_kernel<D>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.n_seqs) * a.H_kv * p.row_blocks * a.n_splits);
+  log_launch("attend_q4_tile_kernel<D>", grid, C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
+  attend_q4_tile_kernel<D><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_attend_q4_tile(const PagedQ4Args& a, cudaStream_t stream) {
+  return a.d == 64 ? launch_attend_q4_tile_d<64>(a, stream) : launch_attend_q4_tile_d<128>(a, stream);
+}
+
+}  // namespace fa
+
+FA_DEFINE_STATUS_FETCH(status_fetch_attend_q4_tile)

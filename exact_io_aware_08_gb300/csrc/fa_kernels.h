@@ -184,8 +184,10 @@ struct PagedQ4Args {
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream);
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream);
+cudaError_t launch_attend_q4_tile(const PagedQ4Args& a, cudaStream_t stream);   // without the join of chunks
 cudaError_t status_fetch_paged(cudaStream_t, unsigned int*, int*);
 cudaError_t status_fetch_attend_q4(cudaStream_t, unsigned int*, int*);
+cudaError_t status_fetch_attend_q4_tile(cudaStream_t, unsigned int*, int*);
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_fp8(const FwdArgs& a, cudaStream_t stream);   // d = 128 only
@@ -237,21 +239,36 @@ inline size_t decode_part_bytes(int B, int H, int d, int n_splits) {
   return static_cast<size_t>(B) * H * n_splits * (d + 2) * sizeof(float);
 }
 
-// Query rows (query heads that share a key head, times query tokens) that a CTA of the 4-bit
-// attention computes together.
+// 4-bit attention: query rows of a key head (the query heads that share it, times a sequence's query
+// tokens) are computed 8 or 16 a CTA (attend_q4.cu), or 256 (attend_q4_tile.cu).
 constexpr int kQ4Rows = 16;
-// Split count of the 4-bit attention when the caller leaves it open: enough chunks for four CTAs
-// on every SM twice over, of at least 256 keys.
-inline int q4_auto_splits(long long items, int n_kv) {
-  long long s = (152LL * 8 + items - 1) / items;
-  const long long max_by_len = (static_cast<long long>(n_kv) + 255) / 256;
+constexpr int kQ4TileRows = 256;
+constexpr int kQ4TileMin = 64;
+inline long long q4_rows(int H, int H_kv, int max_seqlen_q) { return static_cast<long long>(H / H_kv) * max_seqlen_q; }
+inline bool q4_use_tiles(int H, int H_kv, int max_seqlen_q) { return q4_rows(H, H_kv, max_seqlen_q) >= kQ4TileMin; }
+// (sequence, key head, row block) items of a call
+inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q) {
+  const int per = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4TileRows : kQ4Rows;
+  return static_cast<long long>(n_seqs) * H_kv * ((q4_rows(H, H_kv, max_seqlen_q) + per - 1) / per);
+}
+// Split count when the caller leaves it open.  Few rows: enough chunks for four CTAs on every SM twice
+// over, of at least 256 keys.  Tiles: one CTA on every SM, of at least 512 keys.
+inline int q4_auto_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int n_kv) {
+  const bool tiles = q4_use_tiles(H, H_kv, max_seqlen_q);
+  const long long items = q4_items(n_seqs, H, H_kv, max_seqlen_q);
+  long long s = items < 1 ? 1 : tiles ? 152 / items : (152LL * 8 + items - 1) / items;
+  const int least = tiles ? 512 : 256;
+  const long long max_by_len = (static_cast<long long>(n_kv) + least - 1) / least;
   if (s > max_by_len) s = max_by_len;
   if (s < 1) s = 1;
   if (s > kDecodeMaxSplits) s = kDecodeMaxSplits;
   return static_cast<int>(s);
 }
-inline long long q4_row_blocks(int H, int H_kv, int max_seqlen_q) {
-  return (static_cast<long long>(H / H_kv) * max_seqlen_q + kQ4Rows - 1) / kQ4Rows;
+// Keys of a chunk: whole key tiles.
+inline int q4_chunk(int n_kv, int n_splits, bool tiles) {
+  const int step = tiles ? 128 : kDecodeKeyStep;
+  const int c = (n_kv + n_splits - 1) / n_splits;
+  return c < step ? step : (c + step - 1) / step * step;
 }
 
 // Size of the fixed device scratch behind fa_decode_splitkv_noalloc (decode.cu).
