@@ -429,7 +429,15 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
           }
         }
       }
-      const float ms = (m == -INFINITY) ? 0.f : m * c2;
+      float ms = (m == -INFINITY) ? 0.f : m * c2;
+      // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
+      // taken off first
+      if (__any_sync(0xffffffffu, fabsf(ms) > 4096.f)) {
+        const float ref = (m == -INFINITY) ? 0.f : m;
+#pragma unroll
+        for (int k = 0; k < 128; ++k) s[k] -= ref;
+        ms = 0.f;
+      }
       const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
       float2 rs[4];
 #pragma unroll
