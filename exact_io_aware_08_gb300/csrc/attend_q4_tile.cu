@@ -380,30 +380,45 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
       tc_fence_after();
-      float s[128];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        uint32_t rr[32];
-        tmem_ld32(t_s + k * 32, rr);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
-      }
-      tmem_wait_ld();
+      // S in four quarters of 32 columns.  The row maximum needs all four; the first two then stay in
+      // registers and the others are loaded a second time when their turn comes, so that a thread
+      // holds 96 scores at most beside P's words (all 128 made the compiler spill 450 bytes a thread:
+      // 1558 us instead of SPILLTIME us for 4x1024 tokens over 16384 keys).
       const int k0 = key0 + j * C::BN;
-      if (__any_sync(0xffffffffu, k0 + C::BN > lim)) {
+      const bool edge = __any_sync(0xffffffffu, k0 + C::BN > lim);
+      uint32_t s0[32], s1[32], s2[32];
+      auto mask = [&](uint32_t (&v)[32], int q) {
+        if (edge) {
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if (k0 + k >= lim) s[k] = -INFINITY;
+          for (int k = 0; k < 32; ++k)
+            if (k0 + 32 * q + k >= lim) v[k] = 0xff800000u;
+        }
+      };
+      auto top = [&](uint32_t (&v)[32]) {
+        float x = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+        float y = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+        for (int k = 6; k < 30; k += 4) {
+          x = fmax3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+          y = fmax3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+        }
+        return fmax3(fmaxf(x, y), __uint_as_float(v[30]), __uint_as_float(v[31]));
+      };
+      float mq;
+      {
+        uint32_t s3[32];
+        tmem_ld32(t_s + 64, s2);
+        tmem_ld32(t_s + 96, s3);
+        tmem_ld32(t_s, s0);
+        tmem_ld32(t_s + 32, s1);
+        tmem_wait_ld();
+        mask(s2, 2);
+        mask(s3, 3);
+        mask(s0, 0);
+        mask(s1, 1);
+        mq = fmaxf(fmaxf(top(s0), top(s1)), fmaxf(top(s2), top(s3)));
       }
-      float mq[4];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        mq[g] = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
-#pragma unroll
-        for (int k = 3; k < 31; k += 2) mq[g] = fmax3(mq[g], s[32 * g + k], s[32 * g + k + 1]);
-        mq[g] = fmaxf(mq[g], s[32 * g + 31]);
-      }
-      const float cand = fmaxf(m, fmaxf(fmax3(mq[0], mq[1], mq[2]), mq[3]));
+      const float cand = fmaxf(m, mq);
       // a row that sees none of the tile's keys has nothing to move
       const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > C::RESCALE);
       if (__any_sync(0xffffffffu, move)) {
@@ -432,29 +447,37 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       float ms = (m == -INFINITY) ? 0.f : m * c2;
       // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
       // taken off first
-      if (__any_sync(0xffffffffu, fabsf(ms) > 4096.f)) {
-        const float ref = (m == -INFINITY) ? 0.f : m;
-#pragma unroll
-        for (int k = 0; k < 128; ++k) s[k] -= ref;
-        ms = 0.f;
-      }
+      const bool far = __any_sync(0xffffffffu, fabsf(ms) > 4096.f);
+      const float ref = (m == -INFINITY) ? 0.f : m;
+      if (far) ms = 0.f;
       const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
-      float2 rs[4];
+      float2 rs[2];
+      rs[0] = rs[1] = make_float2(0.f, 0.f);
+      auto weigh = [&](uint32_t (&v)[32], int q) {            // P's columns 16 q .. 16 q + 15
+        if (far) {
 #pragma unroll
-      for (int g = 0; g < 4; ++g) rs[g] = make_float2(0.f, 0.f);
+          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) - ref);
+        }
+        uint32_t pk[16];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const float2 x = ffma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2v, nms);
+        for (int k = 0; k < 16; ++k) {
+          const float2 x = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2v, nms);
           const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
           pk[k] = pack_f16x2(e.x, e.y);
-          rs[k & 3] = fadd2(rs[k & 3], e);
+          rs[k & 1] = fadd2(rs[k & 1], e);
         }
-        tmem_st32(t_s + h * 32, pk);
-      }
-      const float2 rs01 = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
+        tmem_st16(t_s + q * 16, pk);
+      };
+      tmem_ld32(t_s + 64, s2);                                // (P covers columns 0 to 63 only)
+      weigh(s0, 0);
+      weigh(s1, 1);
+      tmem_ld32(t_s + 96, s0);
+      tmem_wait_ld();
+      mask(s2, 2);
+      weigh(s2, 2);
+      mask(s0, 3);
+      weigh(s0, 3);
+      const float2 rs01 = fadd2(rs[0], rs[1]);
       l += rs01.x + rs01.y;
       tmem_wait_st();
       tc_fence_before();
