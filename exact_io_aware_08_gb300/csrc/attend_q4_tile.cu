@@ -282,28 +282,36 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     // D = 128: the blocks of the second chunk write their two 16-byte units the other way round, so
     // that the eight lanes of a row reach eight different bank groups
     const int flip = (D == 128 && blk >= 4) ? 1 : 0;
-    auto unpack = [&](const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int key_base, int row_base) {
+    // A lane's rows are RSTEP apart, a multiple of 8: one swizzle, and constant strides.
+    constexpr int RSTEP = RPW * C::UNPACK_WARPS;
+    static_assert(RSTEP % 8 == 0, "rows of a lane share their swizzle");
+    const int r0 = (warp - 12) * RPW + rsub;
+    const uint32_t u0 = (blk >> 2) * C::CHUNK + sw128_offset(r0, ((blk & 3) * 2 + flip) * 8);
+    const uint32_t u1 = (blk >> 2) * C::CHUNK + sw128_offset(r0, ((blk & 3) * 2 + (flip ^ 1)) * 8);
+    auto unpack = [&](const uint8_t* codes, const uint8_t* scales, uint8_t* tile, int key_base) {
+      uint2 cd[C::CKEYS / RSTEP];
+      uint32_t e[C::CKEYS / RSTEP];
 #pragma unroll
-      for (int i = 0; i < C::CKEYS / (RPW * C::UNPACK_WARPS); ++i) {
-        const int r = ((warp - 12) * (C::CKEYS / (RPW * C::UNPACK_WARPS)) + i) * RPW + rsub;
-        const uint2 cd = *reinterpret_cast<const uint2*>(codes + r * C::CB + blk * 8);
-        uint32_t e = scales[r * C::SB + blk];
+      for (int i = 0; i < C::CKEYS / RSTEP; ++i) {
+        cd[i] = *reinterpret_cast<const uint2*>(codes + (r0 + i * RSTEP) * C::CB + blk * 8);
+        e[i] = scales[(r0 + i * RSTEP) * C::SB + blk];
+      }
+      if (key_base + C::CKEYS > key_end) {
         // behind the item's keys lies anything, a scale that is no number among it
-        if (key_base + r >= key_end) e = 0;
-        const uint32_t s = e4m3x2_to_f16(e * 0x0101u);
+#pragma unroll
+        for (int i = 0; i < C::CKEYS / RSTEP; ++i)
+          if (key_base + r0 + i * RSTEP >= key_end) e[i] = 0;
+      }
+#pragma unroll
+      for (int i = 0; i < C::CKEYS / RSTEP; ++i) {
+        const uint32_t s = e4m3x2_to_f16(e[i] * 0x0101u);
         uint32_t h[2][4];
-        e2m1x8_to_f16(cd.x, h[0]);
-        e2m1x8_to_f16(cd.y, h[1]);
+        e2m1x8_to_f16(flip ? cd[i].y : cd[i].x, h[0]);
+        e2m1x8_to_f16(flip ? cd[i].x : cd[i].y, h[1]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) h[k >> 2][k & 3] = hmul2(h[k >> 2][k & 3], s);
-        uint8_t* dst = tile + (blk >> 2) * C::CHUNK;
-        const int row = row_base + r;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int un = k ^ flip;
-          const uint4 v = un ? make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]) : make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]);
-          *reinterpret_cast<uint4*>(dst + sw128_offset(row, ((blk & 3) * 2 + un) * 8)) = v;
-        }
+        *reinterpret_cast<uint4*>(tile + u0 + i * RSTEP * 128) = make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]);
+        *reinterpret_cast<uint4*>(tile + u1 + i * RSTEP * 128) = make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]);
       }
     };
     auto done = [&](uint64_t* bar) {                          // this warp's part is written: hand it to the tensor core
@@ -320,15 +328,15 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       const int kk = key0 + j * C::BN;
       if (!(ok = mbar_wait_warp(&c_full[g0 % C::NC], (g0 / C::NC) & 1, abort_flag, 456))) break;
       if (u > 0 && !(ok = mbar_wait_warp(&k_empty[s], (u - 1) & 1, abort_flag, 457))) break;
-      unpack(c0, c0 + C::OFF_CKS, sK + s * C::TILE, kk, 0);
+      unpack(c0, c0 + C::OFF_CKS, sK + s * C::TILE, kk);
       if (!(ok = mbar_wait_warp(&c_full[g1 % C::NC], (g1 / C::NC) & 1, abort_flag, 458))) break;
-      unpack(c1, c1 + C::OFF_CKS, sK + s * C::TILE, kk + C::CKEYS, C::CKEYS);
+      unpack(c1, c1 + C::OFF_CKS, sK + s * C::TILE + C::CKEYS * 128, kk + C::CKEYS);
       done(&k_full[s]);
       if (u > 0 && !(ok = mbar_wait_warp(&v_empty[s], (u - 1) & 1, abort_flag, 459))) break;
-      unpack(c0 + C::OFF_CV, c0 + C::OFF_CVS, sV + s * C::TILE, kk, 0);
+      unpack(c0 + C::OFF_CV, c0 + C::OFF_CVS, sV + s * C::TILE, kk);
       __syncwarp();
       if (lane == 0) mbar_arrive(&c_empty[g0 % C::NC]);
-      unpack(c1 + C::OFF_CV, c1 + C::OFF_CVS, sV + s * C::TILE, kk + C::CKEYS, C::CKEYS);
+      unpack(c1 + C::OFF_CV, c1 + C::OFF_CVS, sV + s * C::TILE + C::CKEYS * 128, kk + C::CKEYS);
       done(&v_full[s]);
       if (lane == 0) mbar_arrive(&c_empty[g1 % C::NC]);
     }
@@ -383,7 +391,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       // S in four quarters of 32 columns.  The row maximum needs all four; the first two then stay in
       // registers and the others are loaded a second time when their turn comes, so that a thread
       // holds 96 scores at most beside P's words (all 128 made the compiler spill 450 bytes a thread:
-      // 1558 us instead of SPILLTIME us for 4x1024 tokens over 16384 keys).
+      // 1558 instead of 1200 us for 4x1024 tokens over 16384 keys).
       const int k0 = key0 + j * C::BN;
       const bool edge = __any_sync(0xffffffffu, k0 + C::BN > lim);
       uint32_t s0[32], s1[32], s2[32];
