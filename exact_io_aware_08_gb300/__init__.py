@@ -748,6 +748,8 @@ def gather_paged_q4(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlen
 
 def _q4_workspace(T, workspace, need, device):
     """The caller's workspace where it is large enough; none where the call needs none."""
+    if workspace is not None and workspace.device != device:
+        _bad("the workspace must be on the queries' device")
     if need > 16 and (workspace is None or workspace.nbytes < need):
         return T.empty(need, dtype=T.u8, device=device)
     return workspace

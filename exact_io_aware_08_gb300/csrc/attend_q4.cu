@@ -24,12 +24,15 @@
 // Keys sit in the S^T tile in the order kappa(r), which spreads the V loads over all banks.
 //
 // Layout.  Four warps compute, 16 keys each of a 64-key stage; a fifth copies stages by TMA (codes,
-// swizzled) and bulk copies (scales) into a ring that runs on across work items.  Items are
-// (sequence, key head, row block, chunk).
+// swizzled) and bulk copies (scales) into a ring that runs on across work items.  Each CTA gets an
+// equal share of all sequences' key steps (Q4Share), whatever their lengths; with an explicit split
+// count the items are (sequence, key head, row block, chunk).
 #include "fa_kernels.h"
 #include "q4.cuh"
 
 namespace fa {
+
+constexpr float kNone = -1e38f;                               // a reference below every score
 
 template <int D, int NT>
 struct Q4Cfg {
@@ -43,7 +46,7 @@ struct Q4Cfg {
   static constexpr int OFF_KS = 2 * CODES;
   static constexpr int OFF_VS = OFF_KS + SCALES;
   static constexpr int STAGE = (OFF_VS + SCALES + 1023) / 1024 * 1024;
-  static constexpr int NST = 4;
+  static constexpr int NST = D == 128 && NT == 2 ? 6 : 4;
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int MROW = D + 4;                          // floats of a merge row (bank spread)
@@ -53,7 +56,7 @@ struct Q4Cfg {
   static constexpr int SMEM_BYTES = OFF_BAR + (2 * NST + 2) * 8 + 16 + 1024;
   static constexpr int KS = D / 16;                           // k-steps of S^T
   static constexpr int MT = D / 16;                           // element tiles of O^T
-  static constexpr int MIN_CTAS = NT == 1 ? 4 : 3;
+  static constexpr int MIN_CTAS = NT == 1 ? 4 : D == 64 ? 3 : 2;
 };
 
 struct Q4Params {
@@ -64,7 +67,7 @@ struct Q4Params {
   float *lse, *part;
   const int *cu_q, *seqlens, *table;
   int n_seqs, H, H_kv, G, total_q, max_q, max_k, causal, num_blocks, block_size, max_blocks, piece;
-  int n_splits, chunk, row_blocks, n_items;
+  int n_splits, chunk, row_blocks, n_items;                   // n_splits 0: shares of equal length
   float score, descale_v;                                     // scale * log2 e * descale_k
 };
 
@@ -82,27 +85,24 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Work of one item, the same for every thread that asks.
-struct Q4Item {
-  int b, hkv, rb, split, first, nq, len, key0, key_end;   // key_end: keys any row of the block sees
-  bool write;                                             // rows to write (false: no rows, or reported)
+// What a sequence brings: its query tokens [first, first + nq), its keys, and its work in units of
+// one key step (64 keys) of one row block of one key head.  A sequence without keys still has one
+// (empty) unit a row block, which writes O = 0 and lse = -inf.
+struct Q4Seq {
+  int first, nq, len, blocks, steps;                          // row blocks a key head, units a row block
+  __device__ __forceinline__ long long units(int H_kv) const { return static_cast<long long>(blocks) * H_kv * steps; }
 };
 
-__device__ __forceinline__ Q4Item q4_item(const Q4Params& p, int item, int rows_per_block, bool report) {
-  Q4Item x;
-  x.split = item % p.n_splits;
-  item /= p.n_splits;
-  x.rb = item % p.row_blocks;
-  item /= p.row_blocks;
-  x.hkv = item % p.H_kv;
-  x.b = item / p.H_kv;
-  x.first = x.b;
+// Bad contents are reported where ``report`` is set and leave the sequence without rows (boundaries)
+// or without keys (lengths).
+__device__ __forceinline__ Q4Seq q4_seq(const Q4Params& p, int b, int rows_per_block, bool report) {
+  Q4Seq x;
+  x.first = b;
   x.nq = 1;
-  x.write = true;
-  x.len = __ldg(p.seqlens + x.b);
+  x.len = __ldg(p.seqlens + b);
   if (p.cu_q) {
-    x.first = __ldg(p.cu_q + x.b);
-    const int end = __ldg(p.cu_q + x.b + 1);
+    x.first = __ldg(p.cu_q + b);
+    const int end = __ldg(p.cu_q + b + 1);
     x.nq = end - x.first;
     if (x.first < 0 || end < x.first || end > p.total_q || x.nq > p.max_q) {
       if (report) report_device_error(FA_DEV_BAD_CONFIG, 420);
@@ -113,15 +113,133 @@ __device__ __forceinline__ Q4Item q4_item(const Q4Params& p, int item, int rows_
     if (report) report_device_error(FA_DEV_BAD_CONFIG, 421);
     x.len = 0;
   }
-  const int rows = x.nq * p.G;
-  const int row0 = x.rb * rows_per_block;
-  x.write = row0 < rows;
-  int seen = x.len;
-  if (p.causal) seen = max(0, x.len - x.nq + (min(rows, row0 + rows_per_block) - 1) / p.G + 1);
-  x.key0 = x.split * p.chunk;
-  x.key_end = x.write ? min(x.key0 + p.chunk, seen) : 0;
+  x.blocks = (x.nq * p.G + rows_per_block - 1) / rows_per_block;
+  x.steps = max(1, (x.len + kDecodeKeyStep - 1) / kDecodeKeyStep);
   return x;
 }
+
+// The shares of equal length: CTA i of N takes units [T i / N, T (i + 1) / N) of the T units of all
+// sequences, key heads and row blocks in order, however long each sequence is.  N is the grid, or less
+// where a share would fall under kQ4MinUnits.
+constexpr int kQ4MinUnits = 2;
+struct Q4Share {
+  long long total;                                            // T
+  int n;                                                      // N
+  __device__ __forceinline__ long long begin(int i) const { return total * i / n; }
+  // the CTA that has unit u
+  __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * n - 1) / total); }
+};
+
+// By a whole warp: the total, and the sequence that holds unit ``u_of(share)`` with the units before
+// it (b = -1 where there is none).
+template <typename F>
+__device__ __forceinline__ Q4Share q4_share(const Q4Params& p, int rows_per_block, int grid, bool report, F u_of, int* b,
+                                            long long* before) {
+  const int lane = threadIdx.x & 31;
+  Q4Share sh;
+  long long mine = 0;
+  for (int i = lane; i < p.n_seqs; i += 32) mine += q4_seq(p, i, rows_per_block, report).units(p.H_kv);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
+  sh.total = mine;
+  sh.n = static_cast<int>(max(1LL, min(static_cast<long long>(grid), sh.total / kQ4MinUnits)));
+  const long long u = u_of(sh);
+  long long sum = 0;
+  *b = -1;
+  for (int base = 0; base < p.n_seqs && u >= 0; base += 32) {
+    const long long v = base + lane < p.n_seqs ? q4_seq(p, base + lane, rows_per_block, false).units(p.H_kv) : 0;
+    long long inc = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, off);
+      if (lane >= off) inc += x;
+    }
+    const uint32_t beyond = __ballot_sync(0xffffffffu, sum + inc > u);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      *b = base + l;
+      *before = sum + __shfl_sync(0xffffffffu, inc - v, l);
+      break;
+    }
+    sum += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return sh;
+}
+
+// One stretch of work: rows [row0, row0 + rows_per_block) of a key head of a sequence over the keys
+// [key0, key_end); every row sees the keys below ``full``.
+struct Q4Item {
+  int b, hkv, rb, first, nq, len, key0, key_end, full;
+  int out;                                                    // -1: results; else the place of the state
+};
+
+struct Q4Walk {
+  const Q4Params& p;
+  int rows_per_block, item;                                   // chunks: the next item
+  int b;                                                      // shares: sequence, unit in it, units left
+  int off, left;
+  bool report;
+  Q4Seq seq;
+
+  __device__ __forceinline__ void finish(Q4Item& x, int step0, int steps) const {
+    const int row0 = x.rb * rows_per_block;
+    int seen = x.len;
+    x.full = x.len;
+    if (p.causal) {
+      seen = max(0, x.len - x.nq + (min(x.nq * p.G, row0 + rows_per_block) - 1) / p.G + 1);
+      x.full = x.len - x.nq + row0 / p.G + 1;
+    }
+    x.key0 = step0 * kDecodeKeyStep;
+    x.key_end = min(x.key0 + steps * kDecodeKeyStep, seen);
+    x.full = min(x.full, x.key_end);
+  }
+
+  __device__ __forceinline__ bool next(Q4Item& x) {
+    if (p.n_splits) {
+      for (; item < p.n_items; item += gridDim.x) {
+        int i = item;
+        const int split = i % p.n_splits;
+        i /= p.n_splits;
+        x.rb = i % p.row_blocks;
+        i /= p.row_blocks;
+        x.hkv = i % p.H_kv;
+        x.b = i / p.H_kv;
+        seq = q4_seq(p, x.b, rows_per_block, report);
+        if (x.rb >= seq.blocks) continue;
+        x.first = seq.first;
+        x.nq = seq.nq;
+        x.len = seq.len;
+        finish(x, split * (p.chunk / kDecodeKeyStep), p.chunk / kDecodeKeyStep);
+        x.out = p.n_splits == 1 ? -1 : split;
+        item += gridDim.x;
+        return true;
+      }
+      return false;
+    }
+    if (left <= 0) return false;
+    while (off >= seq.blocks * p.H_kv * seq.steps) {          // (a sequence with work follows: left > 0)
+      if (++b >= p.n_seqs) return false;
+      off = 0;
+      seq = q4_seq(p, b, rows_per_block, false);
+    }
+    const int pair = off / seq.steps;
+    const int step0 = off - pair * seq.steps;
+    const int steps = min(left, seq.steps - step0);
+    x.b = b;
+    x.hkv = pair % p.H_kv;
+    x.rb = pair / p.H_kv;
+    x.first = seq.first;
+    x.nq = seq.nq;
+    x.len = seq.len;
+    finish(x, step0, steps);
+    // a row block that a CTA has from its first to its last key is done; else the CTA keeps one state
+    // of a row block that began before its share (0) and one of one that goes on behind it (1)
+    x.out = steps == seq.steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
+    off += steps;
+    left -= steps;
+    return true;
+  }
+};
 
 template <int D>
 __device__ __forceinline__ uint32_t code_offset(int row, int chunk) {   // 16-byte chunk of a row, swizzled
@@ -139,7 +257,8 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NST;
   uint64_t* mrg = empty + C::NST;
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_BAR + (2 * C::NST + 2) * 8);
+  int* start = reinterpret_cast<int*>(mrg + 2);               // sequence, unit in it, units of the share
+  volatile int* abort_flag = start + 3;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -152,44 +271,62 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
     *abort_flag = 0;
     fence_mbarrier_init();
   }
+  if (warp == C::WARPS && p.n_splits == 0) {
+    int b;
+    long long before = 0;
+    const int cta = blockIdx.x;
+    const Q4Share sh = q4_share(p, C::ROWS, gridDim.x, cta == 0,
+                                [&](const Q4Share& x) { return cta < x.n && x.total > 0 ? x.begin(cta) : -1LL; }, &b, &before);
+    if (lane == 0) {
+      start[0] = b;
+      start[1] = b < 0 ? 0 : static_cast<int>(sh.begin(cta) - before);
+      start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(cta + 1) - sh.begin(cta));
+    }
+  }
+  pdl_launch_dependents();
   __syncthreads();
+  Q4Walk walk{p, C::ROWS, static_cast<int>(blockIdx.x), 0, 0, 0, warp == C::WARPS && lane == 0, {}};
+  if (p.n_splits == 0) {
+    walk.b = start[0];
+    walk.off = start[1];
+    walk.left = start[2];
+    if (walk.left > 0) walk.seq = q4_seq(p, walk.b, C::ROWS, false);
+  }
+  Q4Item x;
 
   if (warp == C::WARPS) {
     // ---------------------------------------------------------------- copies
     // Lane j copies piece j (``piece`` keys of one page) of a stage.
     const int pieces = C::KEYS / p.piece;
-    uint32_t g = 0;
+    int s = 0;
+    uint32_t phase = 1, g = 0;                               // the first pass over the ring waits for nothing
     bool ok = true;
-    for (int item = blockIdx.x; ok && item < p.n_items; item += gridDim.x) {
-      const Q4Item x = q4_item(p, item, C::ROWS, lane == 0);
+    while (ok && walk.next(x)) {
       int window = -1, tab = 0;                              // 32 table entries from block ``window`` on
+      const int last_blk = (x.key_end - 1) / p.block_size;
+      int key = x.key0 + (lane < pieces ? lane : 0) * p.piece;
+      int blk = key / p.block_size, in = key - blk * p.block_size;
       for (int kk = x.key0; kk < x.key_end; kk += C::KEYS, ++g) {
-        const int s = g % C::NST;
-        const uint32_t n = g / C::NST;
-        // the stage's pages: at most four table entries, kept 32 at a time
-        const int blk0 = kk / p.block_size;
-        const int last = (min(kk + C::KEYS, x.key_end) - 1) / p.block_size;
-        if (window < 0 || last >= window + 32) {
+        // the stage's pages, at most four: all in the window that begins with the first of them
+        const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
+        if (window < 0 || blk0 + 4 > window + 32) {
           window = blk0;
-          const int blk = window + lane;
           // entries that hold the item's keys only
-          tab = blk <= (x.key_end - 1) / p.block_size ? __ldg(p.table + static_cast<size_t>(x.b) * p.max_blocks + blk) : 0;
+          tab = window + lane <= last_blk ? __ldg(p.table + static_cast<size_t>(x.b) * p.max_blocks + window + lane) : 0;
         }
-        const int key = kk + (lane < pieces ? lane : 0) * p.piece;
-        const int blk = key / p.block_size;
         int page = __shfl_sync(0xffffffffu, tab, (blk - window) & 31);
         const bool mine = lane < pieces && key < x.key_end;
         if (mine && (page < 0 || page >= p.num_blocks)) {
           report_device_error(FA_DEV_BAD_CONFIG, 422);
           page = 0;                                          // stays in bounds; the result is reported invalid
         }
-        if (n > 0 && !(ok = mbar_wait_warp(&empty[s], (n - 1) & 1, abort_flag, 430))) break;
+        if (g >= C::NST && !(ok = mbar_wait_warp(&empty[s], phase, abort_flag, 430))) break;
         const int live = __popc(__ballot_sync(0xffffffffu, mine));
         if (lane == 0) mbar_arrive_expect_tx(&full[s], live * p.piece * 2 * (C::CB + C::SB));
         __syncwarp();
         if (mine) {
           uint8_t* st = smem + s * C::STAGE;
-          const int row = (page * p.H_kv + x.hkv) * p.block_size + (key - blk * p.block_size);
+          const int row = (page * p.H_kv + x.hkv) * p.block_size + in;
           const int at = lane * p.piece;
           tma_load_2d(st + at * C::CB, &p.tk, &full[s], 0, row);
           tma_load_2d(st + C::OFF_V + at * C::CB, &p.tv, &full[s], 0, row);
@@ -197,11 +334,21 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
           bulk_load(st + C::OFF_VS + at * C::SB, p.vs + static_cast<size_t>(row) * C::SB, p.piece * C::SB, &full[s]);
         }
         __syncwarp();
+        key += C::KEYS;
+        in += C::KEYS;
+        while (in >= p.block_size) {
+          in -= p.block_size;
+          ++blk;
+        }
+        if (++s == C::NST) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
     }
     if (!ok) {
       // drain the copies already issued (at most NST stages outstanding)
-      for (uint32_t x = (g > C::NST ? g - C::NST : 0); x < g; ++x) mbar_wait_warp(&full[x % C::NST], (x / C::NST) & 1, nullptr, 431);
+      for (uint32_t y = (g > C::NST ? g - C::NST : 0); y < g; ++y) mbar_wait_warp(&full[y % C::NST], (y / C::NST) & 1, nullptr, 431);
     }
   } else {
     // ---------------------------------------------------------------- products
@@ -210,16 +357,23 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
     const int e = 2 * c;
     const int v0 = warp * 16 + (e ^ (((e >> 1) ^ (e >> 2)) & 1));     // keys kappa(2c) and kappa(2c + 1)
     const int v1 = v0 ^ 1;
-    uint32_t g = 0, it = 0;
+    // Places in a stage; 8 rows on is 8 CB bytes on, under the swizzle too.
+    constexpr int SR = D == 128 ? 1 : 2;                              // lanes' rows that share a scale block (V)
+    const uint8_t* const pk = smem + (D == 128 ? code_offset<D>(ra, c) : code_offset<D>(ra, c >> 1) + (c & 1) * 8);
+    const uint8_t* const pks = smem + C::OFF_KS + ra * C::SB + (D == 128 ? 2 * c : c);
+    const uint8_t* const pv0 = smem + C::OFF_V + (D == 128 ? code_offset<D>(v0, r >> 1) + (r & 1) * 8 : code_offset<D>(v0, r >> 2) + (r & 3) * 4);
+    const uint8_t* const pv1 = smem + C::OFF_V + (D == 128 ? code_offset<D>(v1, r >> 1) + (r & 1) * 8 : code_offset<D>(v1, r >> 2) + (r & 3) * 4);
+    const uint8_t* const pvs0 = smem + C::OFF_VS + v0 * C::SB + r / SR;
+    const uint8_t* const pvs1 = smem + C::OFF_VS + v1 * C::SB + r / SR;
+    int s = 0;
+    uint32_t phase = 0, it = 0;
     bool ok = true;
-    for (int item = blockIdx.x; item < p.n_items; item += gridDim.x) {
-      const Q4Item x = q4_item(p, item, C::ROWS, false);
-      if (!x.write) continue;
+    while (walk.next(x)) {
       const int rows = x.nq * p.G;
       // Queries: lane (r, c) holds row r's elements [c d/4, (c+1) d/4) as B operands; the factors and
       // key limits of rows 2c and 2c + 1, whose scores the lane gets, come from the lanes that hold them.
       uint32_t qb[NT][C::KS][2];
-      float fac[NT][2];
+      float2 fac[NT];
       int vis[NT][2];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -252,25 +406,25 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
             qb[n][2 * j + (k >> 1)][k & 1] = pack_f16x2(bf16_lo(ww[k]) * up, bf16_hi(ww[k]) * up);
         }
         const int seen = p.causal ? x.len - x.nq + min(i, x.nq - 1) + 1 : x.len;
+        fac[n].x = __shfl_sync(0xffffffffu, f, 8 * c);
+        fac[n].y = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          fac[n][k] = __shfl_sync(0xffffffffu, f, (2 * c + k) * 4);
-          vis[n][k] = __shfl_sync(0xffffffffu, seen, (2 * c + k) * 4);
-        }
+        for (int k = 0; k < 2; ++k) vis[n][k] = min(x.key_end, __shfl_sync(0xffffffffu, seen, (2 * c + k) * 4));
       }
-      float m[NT][2], l[NT][2], o[NT][C::MT][4];
+      // m: reference, some number below every score before the first
+      float2 m[NT], l[NT];
+      float o[NT][C::MT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
+        m[n] = make_float2(kNone, kNone);
+        l[n] = make_float2(0.f, 0.f);
 #pragma unroll
         for (int t = 0; t < C::MT; ++t) o[n][t][0] = o[n][t][1] = o[n][t][2] = o[n][t][3] = 0.f;
       }
 
-      for (int kk = x.key0; ok && kk < x.key_end; kk += C::KEYS, ++g) {
-        const int s = g % C::NST;
-        if (!(ok = mbar_wait_warp(&full[s], (g / C::NST) & 1, abort_flag, 432))) break;
-        const uint8_t* st = smem + s * C::STAGE;
+      for (int kk = x.key0; kk < x.key_end; kk += C::KEYS) {
+        if (!(ok = mbar_wait_warp(&full[s], phase, abort_flag, 432))) break;
+        const int so = s * C::STAGE;
         // S^T: this warp's 16 keys against the rows
         float sc[NT][4];
 #pragma unroll
@@ -279,21 +433,21 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
           uint32_t wa[D / 32], wb[D / 32];                     // the two keys' codes, 8 a word
           uint32_t sa[2], sb[2];                               // scales of their blocks, doubled
           if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(st + code_offset<D>(ra, c));
-            const uint4 b = *reinterpret_cast<const uint4*>(st + code_offset<D>(ra + 8, c));
+            const uint4 a = *reinterpret_cast<const uint4*>(pk + so);
+            const uint4 b = *reinterpret_cast<const uint4*>(pk + so + 8 * C::CB);
             wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
             wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
-            const uint32_t ea = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(st + C::OFF_KS + ra * C::SB + 2 * c));
-            const uint32_t eb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(st + C::OFF_KS + (ra + 8) * C::SB + 2 * c));
+            const uint32_t ea = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + so));
+            const uint32_t eb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + so + 8 * C::SB));
             sa[0] = __byte_perm(ea, ea, 0x1010); sa[1] = __byte_perm(ea, ea, 0x3232);
             sb[0] = __byte_perm(eb, eb, 0x1010); sb[1] = __byte_perm(eb, eb, 0x3232);
           } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(st + code_offset<D>(ra, c >> 1) + (c & 1) * 8);
-            const uint2 b = *reinterpret_cast<const uint2*>(st + code_offset<D>(ra + 8, c >> 1) + (c & 1) * 8);
+            const uint2 a = *reinterpret_cast<const uint2*>(pk + so);
+            const uint2 b = *reinterpret_cast<const uint2*>(pk + so + 8 * C::CB);
             wa[0] = a.x; wa[1] = a.y;
             wb[0] = b.x; wb[1] = b.y;
-            sa[0] = e4m3x2_to_f16(st[C::OFF_KS + ra * C::SB + c] * 0x0101u);
-            sb[0] = e4m3x2_to_f16(st[C::OFF_KS + (ra + 8) * C::SB + c] * 0x0101u);
+            sa[0] = e4m3x2_to_f16(pks[so] * 0x0101u);
+            sb[0] = e4m3x2_to_f16(pks[so + 8 * C::SB] * 0x0101u);
           }
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
@@ -316,64 +470,65 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
         uint32_t pb[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float t[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            t[k] = sc[n][k] * fac[n][k & 1];
-            if (kk + ra + 8 * (k >> 1) >= min(x.key_end, vis[n][k & 1])) t[k] = -INFINITY;
+          float2 ta = fmul2(make_float2(sc[n][0], sc[n][1]), fac[n]);
+          float2 tb = fmul2(make_float2(sc[n][2], sc[n][3]), fac[n]);
+          if (kk + C::KEYS > x.full) {
+            if (kk + ra >= vis[n][0]) ta.x = -INFINITY;
+            if (kk + ra >= vis[n][1]) ta.y = -INFINITY;
+            if (kk + ra + 8 >= vis[n][0]) tb.x = -INFINITY;
+            if (kk + ra + 8 >= vis[n][1]) tb.y = -INFINITY;
           }
-          const float t0 = fmaxf(t[0], t[2]), t1 = fmaxf(t[1], t[3]);
-          if (__any_sync(0xffffffffu, t0 > m[n][0] + 8.f || t1 > m[n][1] + 8.f)) {
+          const float t0 = fmaxf(ta.x, tb.x), t1 = fmaxf(ta.y, tb.y);
+          if (__any_sync(0xffffffffu, t0 > m[n].x + 8.f || t1 > m[n].y + 8.f)) {
             // a row's maximum grew by more than 2^8: move its reference
+            float2 top = make_float2(fmaxf(m[n].x, t0), fmaxf(m[n].y, t1));
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              float top = k ? t1 : t0;
+            for (int off = 4; off <= 16; off <<= 1) {
+              top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, off));
+              top.y = fmaxf(top.y, __shfl_xor_sync(0xffffffffu, top.y, off));
+            }
+            const float2 alpha = make_float2(fast_exp2(m[n].x - top.x), fast_exp2(m[n].y - top.y));
+            m[n] = top;
+            l[n] = fmul2(l[n], alpha);
 #pragma unroll
-              for (int off = 4; off <= 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-              const float m_new = fmaxf(m[n][k], top);
-              const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m[n][k] - m_new);
-              m[n][k] = m_new;
-              l[n][k] *= alpha;
-#pragma unroll
-              for (int i = 0; i < C::MT; ++i) {
-                o[n][i][k] *= alpha;
-                o[n][i][2 + k] *= alpha;
-              }
+            for (int i = 0; i < C::MT; ++i) {
+              o[n][i][0] *= alpha.x;
+              o[n][i][1] *= alpha.y;
+              o[n][i][2] *= alpha.x;
+              o[n][i][3] *= alpha.y;
             }
           }
-          const float m0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
-          const float m1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
-          const float p0 = fast_exp2(t[0] - m0), p1 = fast_exp2(t[1] - m1);
-          const float p2 = fast_exp2(t[2] - m0), p3 = fast_exp2(t[3] - m1);
-          l[n][0] += p0 + p2;
-          l[n][1] += p1 + p3;
-          pb[n][0] = transpose8x8(pack_f16x2(p0, p1));
-          pb[n][1] = transpose8x8(pack_f16x2(p2, p3));
+          const float2 nm = make_float2(-m[n].x, -m[n].y);
+          ta = fadd2(ta, nm);
+          tb = fadd2(tb, nm);
+          const float2 pa = make_float2(fast_exp2(ta.x), fast_exp2(ta.y));
+          const float2 pc = make_float2(fast_exp2(tb.x), fast_exp2(tb.y));
+          l[n] = fadd2(l[n], fadd2(pa, pc));
+          pb[n][0] = transpose8x8(pack_f16x2(pa.x, pa.y));
+          pb[n][1] = transpose8x8(pack_f16x2(pc.x, pc.y));
         }
         // O^T += V^T P^T
         {
-          const uint8_t* sv = st + C::OFF_V;
-          const uint8_t* vs = st + C::OFF_VS;
           constexpr int W = D / 64;                            // words of a row's d/8 elements
-          constexpr int SR = D == 128 ? 1 : 2;                 // lanes' rows that share a scale block
           uint32_t lo[2][W], hi[2][W], sl[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int k0 = v0 + 8 * h, k1 = v1 + 8 * h;
             uint32_t a[W], b[W];
             if constexpr (D == 128) {
-              const uint2 x0 = *reinterpret_cast<const uint2*>(sv + code_offset<D>(k0, r >> 1) + (r & 1) * 8);
-              const uint2 x1 = *reinterpret_cast<const uint2*>(sv + code_offset<D>(k1, r >> 1) + (r & 1) * 8);
+              const uint2 x0 = *reinterpret_cast<const uint2*>(pv0 + so + 8 * h * C::CB);
+              const uint2 x1 = *reinterpret_cast<const uint2*>(pv1 + so + 8 * h * C::CB);
               a[0] = x0.x; a[1] = x0.y; b[0] = x1.x; b[1] = x1.y;
             } else {
-              a[0] = *reinterpret_cast<const uint32_t*>(sv + code_offset<D>(k0, r >> 2) + (r & 3) * 4);
-              b[0] = *reinterpret_cast<const uint32_t*>(sv + code_offset<D>(k1, r >> 2) + (r & 3) * 4);
+              a[0] = *reinterpret_cast<const uint32_t*>(pv0 + so + 8 * h * C::CB);
+              b[0] = *reinterpret_cast<const uint32_t*>(pv1 + so + 8 * h * C::CB);
             }
-            uint32_t e0 = vs[k0 * C::SB + r / SR], e1 = vs[k1 * C::SB + r / SR];
-            // rows past the end hold anything, a scale that is no number among it: 0 * NaN is NaN
-            if (kk + k0 >= x.key_end) e0 = 0;
-            if (kk + k1 >= x.key_end) e1 = 0;
-            sl[h] = e4m3x2_to_f16(e0 | (e1 << 8));
+            uint32_t e0 = pvs0[so + 8 * h * C::SB], e1 = pvs1[so + 8 * h * C::SB];
+            if (kk + C::KEYS > x.key_end) {
+              // rows past the end hold anything, a scale that is no number among it: 0 * NaN is NaN
+              if (kk + v0 + 8 * h >= x.key_end) e0 = 0;
+              if (kk + v1 + 8 * h >= x.key_end) e1 = 0;
+            }
+            sl[h] = e4m3x2_to_f16(__byte_perm(e0, e1, 0x0040));
 #pragma unroll
             for (int j = 0; j < W; ++j) {
               // byte i: the two keys' even (lo) or odd (hi) elements 2i (+1) of the word
@@ -399,22 +554,29 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&empty[s]);
+        if (++s == C::NST) {
+          s = 0;
+          phase ^= 1u;
+        }
       }
       if (!ok) break;
 
-      // The warps' states of this chunk.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1), kept at
+      // The warps' states of this stretch.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1), kept at
       // position 16 t + 2 r (+1) of the merge row.
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int off = 4; off <= 16; off <<= 1) {
+          l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, off);
+          l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, off);
+        }
 #pragma unroll
-          for (int off = 4; off <= 16; off <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], off);
+        for (int k = 0; k < 2; ++k) {
           float* dst = merge + (warp * C::ROWS + 8 * n + 2 * c + k) * C::MROW;
 #pragma unroll
           for (int t = 0; t < C::MT; ++t)
             *reinterpret_cast<float2*>(dst + 16 * t + 2 * r) = make_float2(o[n][t][k], o[n][t][2 + k]);
-          if (r == 0) ml[warp * C::ROWS + 8 * n + 2 * c + k] = make_float2(m[n][k], l[n][k]);
+          if (r == 0) ml[warp * C::ROWS + 8 * n + 2 * c + k] = k ? make_float2(m[n].y, l[n].y) : make_float2(m[n].x, l[n].x);
         }
       }
       if (!(ok = warps_sync(&mrg[0], it & 1, abort_flag, 433))) break;
@@ -423,34 +585,33 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
         const int row = x.rb * C::ROWS + n;
         if (row >= rows) break;
         const int pos = D == 128 ? ((dd >> 1) & 7) * 16 + (dd >> 4) * 2 : ((dd >> 1) & 3) * 16 + (dd >> 3) * 2;
-        float M = -INFINITY;
+        float M = kNone;
 #pragma unroll
         for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, ml[w * C::ROWS + n].x);
         float a0 = 0.f, a1 = 0.f, L = 0.f;
-        if (M != -INFINITY) {
 #pragma unroll
-          for (int w = 0; w < C::WARPS; ++w) {
-            const float2 st = ml[w * C::ROWS + n];
-            const float wt = fast_exp2(st.x - M);
-            const float2 v = *reinterpret_cast<const float2*>(merge + (w * C::ROWS + n) * C::MROW + pos);
-            a0 = fmaf(wt, v.x, a0);
-            a1 = fmaf(wt, v.y, a1);
-            L = fmaf(wt, st.y, L);
-          }
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float2 st = ml[w * C::ROWS + n];
+          const float wt = fast_exp2(st.x - M);
+          const float2 v = *reinterpret_cast<const float2*>(merge + (w * C::ROWS + n) * C::MROW + pos);
+          a0 = fmaf(wt, v.x, a0);
+          a1 = fmaf(wt, v.y, a1);
+          L = fmaf(wt, st.y, L);
         }
         const int i = row / p.G;
         const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
         const size_t th = static_cast<size_t>(tok) * p.H + head;
-        if (p.n_splits == 1) {
-          const bool none = M == -INFINITY;                    // a row that sees no key
+        if (x.out < 0) {
+          const bool none = M == kNone;                        // a row that sees no key
           const float inv = none ? 0.f : p.descale_v / L;
-          *reinterpret_cast<uint32_t*>(p.o + th * D + dd) = pack_bf16x2(none ? 0.f : a0 * inv, none ? 0.f : a1 * inv);
+          *reinterpret_cast<uint32_t*>(p.o + th * D + dd) = none ? 0u : pack_bf16x2(a0 * inv, a1 * inv);
           if (dd == 0)
             p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         } else {
-          float* dst = p.part + (th * p.n_splits + x.split) * (D + 2);
+          const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + n;
+          float* dst = p.part + at * (D + 2);
           *reinterpret_cast<float2*>(dst + dd) = make_float2(a0, a1);
-          if (dd == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M, L);
+          if (dd == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M == kNone ? -INFINITY : M, L);
         }
       }
       if (!(ok = warps_sync(&mrg[1], it & 1, abort_flag, 434))) break;
@@ -461,47 +622,88 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
   __syncthreads();
 }
 
-// Joins a row's chunk states: one warp a row.
-template <int D>
-__global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ o,
-                                                             float* __restrict__ lse, const int* __restrict__ cu_q,
-                                                             int n_seqs, int H, int total_q, int n_splits, float descale_v) {
-  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+// Writes a row's result from its chunks' states, which ``state(i)`` gives for i < n: one warp.
+template <int D, typename F>
+__device__ __forceinline__ void q4_join(F state, int n, uint16_t* o, float* lse, float descale_v) {
   const int lane = threadIdx.x & 31;
-  if (th >= static_cast<long long>(total_q) * H) return;
-  const int tok = static_cast<int>(th / H), head = static_cast<int>(th - static_cast<long long>(tok) * H);
-  if (cu_q && tok >= __ldg(cu_q + n_seqs)) return;             // rows behind the last sequence stay as they are
-  const float* base = part + static_cast<size_t>(th) * n_splits * (D + 2);
   float M = -INFINITY;
-  for (int c = lane; c < n_splits; c += 32) M = fmaxf(M, base[static_cast<size_t>(c) * (D + 2) + D]);
+  for (int i = lane; i < n; i += 32) {
+    const float* st = state(i);
+    if (st) M = fmaxf(M, st[D]);
+  }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
   constexpr int V = D / 32;
   float acc[V], L = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  for (int c = 0; c < n_splits; ++c) {
-    const float* st = base + static_cast<size_t>(c) * (D + 2);
-    const float mc = st[D];
-    if (mc == -INFINITY) continue;                             // empty chunk: weight 0
-    const float wt = fast_exp2(mc - M);
-    L = fmaf(wt, st[D + 1], L);
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* st = state(i);
+    if (!st) continue;
+    const float2 s = *reinterpret_cast<const float2*>(st + D);
+    if (s.x == -INFINITY) continue;                            // no keys: weight 0
+    const float wt = fast_exp2(s.x - M);
+    L = fmaf(wt, s.y, L);
 #pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      const float2 v = *reinterpret_cast<const float2*>(st + 64 * i + 2 * lane);
-      acc[2 * i] = fmaf(wt, v.x, acc[2 * i]);
-      acc[2 * i + 1] = fmaf(wt, v.y, acc[2 * i + 1]);
+    for (int k = 0; k < V / 2; ++k) {
+      const float2 v = *reinterpret_cast<const float2*>(st + 64 * k + 2 * lane);
+      acc[2 * k] = fmaf(wt, v.x, acc[2 * k]);
+      acc[2 * k + 1] = fmaf(wt, v.y, acc[2 * k + 1]);
     }
   }
   const bool none = M == -INFINITY;
   const float inv = none ? 0.f : descale_v / L;
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i)
-    *reinterpret_cast<uint32_t*>(o + static_cast<size_t>(th) * D + 64 * i + 2 * lane) =
-        pack_bf16x2(none ? 0.f : acc[2 * i] * inv, none ? 0.f : acc[2 * i + 1] * inv);
-  if (lane == 0)
-    lse[cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)] =
-        none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  for (int k = 0; k < V / 2; ++k)
+    *reinterpret_cast<uint32_t*>(o + 64 * k + 2 * lane) = none ? 0u : pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  if (lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// Joins a row's chunks where the caller gave their count (part: [row][chunk]): one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ o,
+                                                             float* __restrict__ lse, const int* __restrict__ cu_q,
+                                                             int n_seqs, int H, int total_q, int n_splits, float descale_v) {
+  pdl_wait();
+  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (th >= static_cast<long long>(total_q) * H) return;
+  const int tok = static_cast<int>(th / H), head = static_cast<int>(th - static_cast<long long>(tok) * H);
+  if (cu_q && tok >= __ldg(cu_q + n_seqs)) return;             // rows behind the last sequence stay as they are
+  const float* base = part + static_cast<size_t>(th) * n_splits * (D + 2);
+  q4_join<D>([&](int i) { return base + static_cast<size_t>(i) * (D + 2); }, n_splits, o + static_cast<size_t>(th) * D,
+             lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
+}
+
+// Joins the states of the row blocks that lie in several CTAs' shares: one warp a row.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int grid) {
+  constexpr int ROWS = 8 * NT;
+  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const bool some = th < static_cast<long long>(p.total_q) * p.H;
+  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
+  int b = tok, first, count;
+  if (p.cu_q) b = some ? owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423) : -1;
+  int none;
+  long long before = 0;
+  // (the search is asked for nothing: the units before sequence b are counted here)
+  const Q4Share sh = q4_share(p, ROWS, grid, false, [](const Q4Share&) { return -1LL; }, &none, &before);
+  for (int i = threadIdx.x & 31; i < b; i += 32) before += q4_seq(p, i, ROWS, false).units(p.H_kv);
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+  pdl_wait();
+  if (!some || b < 0) return;                                  // behind the last sequence: stays as it is
+  const Q4Seq seq = q4_seq(p, b, ROWS, false);
+  if (seq.blocks == 0) return;                                 // reported
+  const int row = (tok - seq.first) * p.G + head % p.G;
+  const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
+  const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
+  if (c0 == c1) return;                                        // its CTA wrote the result
+  q4_join<D>([&](int i) -> const float* {
+        const int c = c0 + i;
+        return p.part + (static_cast<size_t>(2 * c + (i == 0 ? 1 : 0)) * ROWS + row % ROWS) * (D + 2);
+      }, c1 - c0 + 1, p.o + static_cast<size_t>(th) * D,
+      p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)), p.descale_v);
 }
 
 static int q4_sm_count() {
@@ -513,6 +715,26 @@ static int q4_sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
   if (dev < 64) cached[dev] = n;
   return n;
+}
+
+// The join runs behind the chunks on the stream, but may start while their last CTAs run
+// (programmatic dependent launch): it reads lengths and boundaries, then waits for the states.
+template <typename... P, typename... A>
+static cudaError_t launch_join(void (*kernel)(P...), unsigned blocks, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(128);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+static unsigned join_blocks(const PagedQ4Args& a) {
+  return static_cast<unsigned>((static_cast<long long>(a.total_q) * a.H + 3) / 4);
 }
 
 template <int D, int NT>
@@ -532,27 +754,32 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   p.max_q = a.max_seqlen_q; p.max_k = a.max_seqlen_k; p.causal = a.causal;
   p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.max_blocks = a.max_blocks;
   p.n_splits = a.n_splits; p.chunk = a.chunk;
-  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + C::ROWS - 1) / C::ROWS);
-  p.n_items = static_cast<int>(static_cast<long long>(a.n_seqs) * a.H_kv * p.row_blocks * a.n_splits);
+  p.row_blocks = static_cast<int>((q4_rows(a.H, a.H_kv, a.max_seqlen_q) + C::ROWS - 1) / C::ROWS);
+  const long long pairs = static_cast<long long>(a.n_seqs) * a.H_kv * p.row_blocks;
+  p.n_items = static_cast<int>(pairs * a.n_splits);
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;
-  const int grid = min(p.n_items, C::MIN_CTAS * q4_sm_count());
+  const long long most = min(C::MIN_CTAS * q4_sm_count(), kQ4MaxShares);
+  const long long steps = (static_cast<long long>(a.max_seqlen_k) + kDecodeKeyStep - 1) / kDecodeKeyStep;
+  // (a share is kQ4MinUnits long at least, and there are pairs * steps units at most)
+  const long long want = a.n_splits ? p.n_items : pairs * max(1LL, steps) / kQ4MinUnits;
+  const int grid = static_cast<int>(max(1LL, min(most, want)));
   log_launch("attend_q4_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  if (e != cudaSuccess || a.n_splits || grid == 1) return e;
+  log_launch("attend_q4_join_kernel<D, NT>", join_blocks(a), 128, 0ull);
+  return launch_join(attend_q4_join_kernel<D, NT>, join_blocks(a), stream, p, grid);
 }
 
 template <int D>
 static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t stream) {
-  const long long warps = static_cast<long long>(a.total_q) * a.H;
-  const unsigned blocks = static_cast<unsigned>((warps + 3) / 4);
-  log_launch("attend_q4_merge_kernel<D>", blocks, 128, 0ull);
-  attend_q4_merge_kernel<D><<<blocks, 128, 0, stream>>>(a.part, static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H,
-                                                        a.total_q, a.n_splits, a.descale_v);
-  return cudaGetLastError();
+  log_launch("attend_q4_merge_kernel<D>", join_blocks(a), 128, 0ull);
+  return launch_join(attend_q4_merge_kernel<D>, join_blocks(a), stream, static_cast<const float*>(a.part),
+                     static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.n_splits, a.descale_v);
 }
 
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
@@ -565,7 +792,7 @@ cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
     if (a.d == 64) e = small ? launch_attend_q4_d<64, 1>(a, stream) : launch_attend_q4_d<64, 2>(a, stream);
     else e = small ? launch_attend_q4_d<128, 1>(a, stream) : launch_attend_q4_d<128, 2>(a, stream);
   }
-  if (e != cudaSuccess || a.n_splits == 1) return e;
+  if (e != cudaSuccess || a.n_splits <= 1) return e;
   return a.d == 64 ? launch_attend_q4_merge<64>(a, stream) : launch_attend_q4_merge<128>(a, stream);
 }
 

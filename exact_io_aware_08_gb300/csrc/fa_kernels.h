@@ -251,14 +251,17 @@ inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q) {
   const int per = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4TileRows : kQ4Rows;
   return static_cast<long long>(n_seqs) * H_kv * ((q4_rows(H, H_kv, max_seqlen_q) + per - 1) / per);
 }
-// Split count when the caller leaves it open.  Few rows: enough chunks for four CTAs on every SM twice
-// over, of at least 256 keys.  Tiles: one CTA on every SM, of at least 512 keys.
+// Few rows without a split count: at most this many CTAs share the work, and each keeps at most two
+// states of kQ4Rows rows.
+constexpr int kQ4MaxShares = 4 * 152;
+inline size_t q4_share_bytes(int d) { return static_cast<size_t>(kQ4MaxShares) * 2 * kQ4Rows * (d + 2) * sizeof(float); }
+// Split count when the caller leaves it open.  Few rows: 0, shares of equal length.  Tiles: one CTA on
+// every SM, of at least 512 keys.
 inline int q4_auto_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int n_kv) {
-  const bool tiles = q4_use_tiles(H, H_kv, max_seqlen_q);
+  if (!q4_use_tiles(H, H_kv, max_seqlen_q)) return 0;
   const long long items = q4_items(n_seqs, H, H_kv, max_seqlen_q);
-  long long s = items < 1 ? 1 : tiles ? 152 / items : (152LL * 8 + items - 1) / items;
-  const int least = tiles ? 512 : 256;
-  const long long max_by_len = (static_cast<long long>(n_kv) + least - 1) / least;
+  long long s = items < 1 ? 1 : 152 / items;
+  const long long max_by_len = (static_cast<long long>(n_kv) + 511) / 512;
   if (s > max_by_len) s = max_by_len;
   if (s < 1) s = 1;
   if (s > kDecodeMaxSplits) s = kDecodeMaxSplits;
