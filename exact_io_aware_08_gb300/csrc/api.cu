@@ -660,8 +660,8 @@ fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, 
     return fail(FA_ERR_INVALID_ARG, "scale * descale_k must be in about [1e-34, 1e34] (got %g)", static_cast<double>(score));
   if ((st = q4_splits(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k, &n_splits)) != FA_OK) return st;
   // key steps of a sequence are counted in an int, those of all of them over the shares too
-  if (fa::q4_items(1, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kDecodeKeyStep + 1) >= (1LL << 31) ||
-      fa::q4_items(n_seqs, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kDecodeKeyStep + 1) >= (1LL << 38))
+  if (fa::q4_items(1, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 31) ||
+      fa::q4_items(n_seqs, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 38))
     return fail(FA_ERR_UNSUPPORTED, "too many (key head, row block, key step) units");
   if (total_q == 0 || max_seqlen_q == 0) return FA_OK;
   if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !o || !lse)
@@ -683,7 +683,7 @@ fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, 
   a.num_blocks = num_blocks; a.block_size = block_size; a.max_blocks = max_blocks; a.max_seqlen_k = max_seqlen_k;
   a.causal = causal ? 1 : 0; a.scale = scale; a.descale_k = descale_k; a.descale_v = descale_v;
   a.n_splits = n_splits;
-  a.chunk = n_splits ? fa::q4_chunk(max_seqlen_k, n_splits, fa::q4_use_tiles(H, H_kv, max_seqlen_q)) : 0;
+  a.chunk = n_splits ? fa::q4_chunk(max_seqlen_k, n_splits) : 0;
   cudaError_t e = fa::launch_attend_q4(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
 }

@@ -23,7 +23,7 @@
 //                 P^T comes from the S^T accumulators by an 8x8 transpose in registers.
 // Keys sit in the S^T tile in the order kappa(r), which spreads the V loads over all banks.
 //
-// Layout.  Four warps compute, 16 keys each of a 64-key stage; a fifth copies stages by TMA (codes,
+// Layout.  Four warps compute, 32 keys each of a 128-key stage, 16 at a time; a fifth copies stages by TMA (codes,
 // swizzled) and bulk copies (scales) into a ring that runs on across work items.  Each CTA gets an
 // equal share of all sequences' key steps (Q4Share), whatever their lengths; with an explicit split
 // count the items are (sequence, key head, row block, chunk).
@@ -36,7 +36,7 @@ constexpr float kNone = -1e38f;                               // a reference bel
 
 template <int D, int NT>
 struct Q4Cfg {
-  static constexpr int KEYS = kDecodeKeyStep;                 // 64
+  static constexpr int KEYS = kQ4Step;                        // 128: 32 a warp, in two halves
   static constexpr int ROWS = 8 * NT;
   static constexpr int CB = D / 2;                            // code bytes of a row
   static constexpr int SB = D / 16;                           // scale bytes of a row
@@ -46,7 +46,7 @@ struct Q4Cfg {
   static constexpr int OFF_KS = 2 * CODES;
   static constexpr int OFF_VS = OFF_KS + SCALES;
   static constexpr int STAGE = (OFF_VS + SCALES + 1023) / 1024 * 1024;
-  static constexpr int NST = D == 128 && NT == 2 ? 6 : 4;
+  static constexpr int NST = D == 128 && NT == 1 ? 2 : 3;
   static constexpr int WARPS = 4;
   static constexpr int THREADS = 32 * (WARPS + 1);
   static constexpr int MROW = D + 4;                          // floats of a merge row (bank spread)
@@ -86,7 +86,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // What a sequence brings: its query tokens [first, first + nq), its keys, and its work in units of
-// one key step (64 keys) of one row block of one key head.  A sequence without keys still has one
+// one key step of one row block of one key head.  A sequence without keys still has one
 // (empty) unit a row block, which writes O = 0 and lse = -inf.
 struct Q4Seq {
   int first, nq, len, blocks, steps;                          // row blocks a key head, units a row block
@@ -114,14 +114,14 @@ __device__ __forceinline__ Q4Seq q4_seq(const Q4Params& p, int b, int rows_per_b
     x.len = 0;
   }
   x.blocks = (x.nq * p.G + rows_per_block - 1) / rows_per_block;
-  x.steps = max(1, (x.len + kDecodeKeyStep - 1) / kDecodeKeyStep);
+  x.steps = max(1, (x.len + kQ4Step - 1) / kQ4Step);
   return x;
 }
 
 // The shares of equal length: CTA i of N takes units [T i / N, T (i + 1) / N) of the T units of all
 // sequences, key heads and row blocks in order, however long each sequence is.  N is the grid, or less
 // where a share would fall under kQ4MinUnits.
-constexpr int kQ4MinUnits = 2;
+constexpr int kQ4MinUnits = 1;
 struct Q4Share {
   long long total;                                            // T
   int n;                                                      // N
@@ -189,8 +189,8 @@ struct Q4Walk {
       seen = max(0, x.len - x.nq + (min(x.nq * p.G, row0 + rows_per_block) - 1) / p.G + 1);
       x.full = x.len - x.nq + row0 / p.G + 1;
     }
-    x.key0 = step0 * kDecodeKeyStep;
-    x.key_end = min(x.key0 + steps * kDecodeKeyStep, seen);
+    x.key0 = step0 * kQ4Step;
+    x.key_end = min(x.key0 + steps * kQ4Step, seen);
     x.full = min(x.full, x.key_end);
   }
 
@@ -209,7 +209,7 @@ struct Q4Walk {
         x.first = seq.first;
         x.nq = seq.nq;
         x.len = seq.len;
-        finish(x, split * (p.chunk / kDecodeKeyStep), p.chunk / kDecodeKeyStep);
+        finish(x, split * (p.chunk / kQ4Step), p.chunk / kQ4Step);
         x.out = p.n_splits == 1 ? -1 : split;
         item += gridDim.x;
         return true;
@@ -307,9 +307,9 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
       int key = x.key0 + (lane < pieces ? lane : 0) * p.piece;
       int blk = key / p.block_size, in = key - blk * p.block_size;
       for (int kk = x.key0; kk < x.key_end; kk += C::KEYS, ++g) {
-        // the stage's pages, at most four: all in the window that begins with the first of them
+        // the stage's pages, at most eight: all in the window that begins with the first of them
         const int blk0 = __shfl_sync(0xffffffffu, blk, 0);
-        if (window < 0 || blk0 + 4 > window + 32) {
+        if (window < 0 || blk0 + 8 > window + 32) {
           window = blk0;
           // entries that hold the item's keys only
           tab = window + lane <= last_blk ? __ldg(p.table + static_cast<size_t>(x.b) * p.max_blocks + window + lane) : 0;
@@ -353,9 +353,9 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
   } else {
     // ---------------------------------------------------------------- products
     const int r = lane >> 2, c = lane & 3;
-    const int ra = warp * 16 + (r ^ (((r >> 1) ^ (r >> 2)) & 1));     // key kappa(r) of the warp's 16; + 8
+    const int ra = warp * 32 + (r ^ (((r >> 1) ^ (r >> 2)) & 1));     // key kappa(r) of the warp's first 8
     const int e = 2 * c;
-    const int v0 = warp * 16 + (e ^ (((e >> 1) ^ (e >> 2)) & 1));     // keys kappa(2c) and kappa(2c + 1)
+    const int v0 = warp * 32 + (e ^ (((e >> 1) ^ (e >> 2)) & 1));     // keys kappa(2c) and kappa(2c + 1)
     const int v1 = v0 ^ 1;
     // Places in a stage; 8 rows on is 8 CB bytes on, under the swizzle too.
     constexpr int SR = D == 128 ? 1 : 2;                              // lanes' rows that share a scale block (V)
@@ -425,29 +425,31 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
       for (int kk = x.key0; kk < x.key_end; kk += C::KEYS) {
         if (!(ok = mbar_wait_warp(&full[s], phase, abort_flag, 432))) break;
         const int so = s * C::STAGE;
-        // S^T: this warp's 16 keys against the rows
-        float sc[NT][4];
+        // S^T: this warp's 32 keys against the rows
+        float sc[2][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
-        {
+        for (int g = 0; g < 2; ++g) {
+          const int sg = so + g * 16 * C::CB, ss = so + g * 16 * C::SB;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) sc[g][n][0] = sc[g][n][1] = sc[g][n][2] = sc[g][n][3] = 0.f;
           uint32_t wa[D / 32], wb[D / 32];                     // the two keys' codes, 8 a word
           uint32_t sa[2], sb[2];                               // scales of their blocks, doubled
           if constexpr (D == 128) {
-            const uint4 a = *reinterpret_cast<const uint4*>(pk + so);
-            const uint4 b = *reinterpret_cast<const uint4*>(pk + so + 8 * C::CB);
+            const uint4 a = *reinterpret_cast<const uint4*>(pk + sg);
+            const uint4 b = *reinterpret_cast<const uint4*>(pk + sg + 8 * C::CB);
             wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
             wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
-            const uint32_t ea = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + so));
-            const uint32_t eb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + so + 8 * C::SB));
+            const uint32_t ea = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + ss));
+            const uint32_t eb = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(pks + ss + 8 * C::SB));
             sa[0] = __byte_perm(ea, ea, 0x1010); sa[1] = __byte_perm(ea, ea, 0x3232);
             sb[0] = __byte_perm(eb, eb, 0x1010); sb[1] = __byte_perm(eb, eb, 0x3232);
           } else {
-            const uint2 a = *reinterpret_cast<const uint2*>(pk + so);
-            const uint2 b = *reinterpret_cast<const uint2*>(pk + so + 8 * C::CB);
+            const uint2 a = *reinterpret_cast<const uint2*>(pk + sg);
+            const uint2 b = *reinterpret_cast<const uint2*>(pk + sg + 8 * C::CB);
             wa[0] = a.x; wa[1] = a.y;
             wb[0] = b.x; wb[1] = b.y;
-            sa[0] = e4m3x2_to_f16(pks[so] * 0x0101u);
-            sb[0] = e4m3x2_to_f16(pks[so + 8 * C::SB] * 0x0101u);
+            sa[0] = e4m3x2_to_f16(pks[ss] * 0x0101u);
+            sb[0] = e4m3x2_to_f16(pks[ss + 8 * C::SB] * 0x0101u);
           }
 #pragma unroll
           for (int j = 0; j < D / 32; ++j) {
@@ -461,24 +463,26 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-              mma_f16(sc[n], a[0], b[0], a[1], b[1], qb[n][2 * j][0], qb[n][2 * j][1]);
-              mma_f16(sc[n], a[2], b[2], a[3], b[3], qb[n][2 * j + 1][0], qb[n][2 * j + 1][1]);
+              mma_f16(sc[g][n], a[0], b[0], a[1], b[1], qb[n][2 * j][0], qb[n][2 * j][1]);
+              mma_f16(sc[g][n], a[2], b[2], a[3], b[3], qb[n][2 * j + 1][0], qb[n][2 * j + 1][1]);
             }
           }
         }
-        // scores of keys kk + ra and kk + ra + 8 for rows 2c, 2c + 1, in the log2 domain
-        uint32_t pb[NT][2];
+        // scores of keys kk + ra + 8 i for rows 2c, 2c + 1, in the log2 domain
+        uint32_t pb[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-          float2 ta = fmul2(make_float2(sc[n][0], sc[n][1]), fac[n]);
-          float2 tb = fmul2(make_float2(sc[n][2], sc[n][3]), fac[n]);
+          float2 t[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) t[i] = fmul2(make_float2(sc[i >> 1][n][2 * (i & 1)], sc[i >> 1][n][2 * (i & 1) + 1]), fac[n]);
           if (kk + C::KEYS > x.full) {
-            if (kk + ra >= vis[n][0]) ta.x = -INFINITY;
-            if (kk + ra >= vis[n][1]) ta.y = -INFINITY;
-            if (kk + ra + 8 >= vis[n][0]) tb.x = -INFINITY;
-            if (kk + ra + 8 >= vis[n][1]) tb.y = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (kk + ra + 8 * i >= vis[n][0]) t[i].x = -INFINITY;
+              if (kk + ra + 8 * i >= vis[n][1]) t[i].y = -INFINITY;
+            }
           }
-          const float t0 = fmaxf(ta.x, tb.x), t1 = fmaxf(ta.y, tb.y);
+          const float t0 = fmaxf(fmax3(t[0].x, t[1].x, t[2].x), t[3].x), t1 = fmaxf(fmax3(t[0].y, t[1].y, t[2].y), t[3].y);
           if (__any_sync(0xffffffffu, t0 > m[n].x + 8.f || t1 > m[n].y + 8.f)) {
             // a row's maximum grew by more than 2^8: move its reference
             float2 top = make_float2(fmaxf(m[n].x, t0), fmaxf(m[n].y, t1));
@@ -499,34 +503,37 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
             }
           }
           const float2 nm = make_float2(-m[n].x, -m[n].y);
-          ta = fadd2(ta, nm);
-          tb = fadd2(tb, nm);
-          const float2 pa = make_float2(fast_exp2(ta.x), fast_exp2(ta.y));
-          const float2 pc = make_float2(fast_exp2(tb.x), fast_exp2(tb.y));
-          l[n] = fadd2(l[n], fadd2(pa, pc));
-          pb[n][0] = transpose8x8(pack_f16x2(pa.x, pa.y));
-          pb[n][1] = transpose8x8(pack_f16x2(pc.x, pc.y));
+          float2 w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 y = fadd2(t[i], nm);
+            w[i] = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            pb[i >> 1][n][i & 1] = transpose8x8(pack_f16x2(w[i].x, w[i].y));
+          }
+          l[n] = fadd2(l[n], fadd2(fadd2(w[0], w[1]), fadd2(w[2], w[3])));
         }
         // O^T += V^T P^T
-        {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          const int sg = so + g * 16 * C::CB, ss = so + g * 16 * C::SB;
           constexpr int W = D / 64;                            // words of a row's d/8 elements
           uint32_t lo[2][W], hi[2][W], sl[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t a[W], b[W];
             if constexpr (D == 128) {
-              const uint2 x0 = *reinterpret_cast<const uint2*>(pv0 + so + 8 * h * C::CB);
-              const uint2 x1 = *reinterpret_cast<const uint2*>(pv1 + so + 8 * h * C::CB);
+              const uint2 x0 = *reinterpret_cast<const uint2*>(pv0 + sg + 8 * h * C::CB);
+              const uint2 x1 = *reinterpret_cast<const uint2*>(pv1 + sg + 8 * h * C::CB);
               a[0] = x0.x; a[1] = x0.y; b[0] = x1.x; b[1] = x1.y;
             } else {
-              a[0] = *reinterpret_cast<const uint32_t*>(pv0 + so + 8 * h * C::CB);
-              b[0] = *reinterpret_cast<const uint32_t*>(pv1 + so + 8 * h * C::CB);
+              a[0] = *reinterpret_cast<const uint32_t*>(pv0 + sg + 8 * h * C::CB);
+              b[0] = *reinterpret_cast<const uint32_t*>(pv1 + sg + 8 * h * C::CB);
             }
-            uint32_t e0 = pvs0[so + 8 * h * C::SB], e1 = pvs1[so + 8 * h * C::SB];
+            uint32_t e0 = pvs0[ss + 8 * h * C::SB], e1 = pvs1[ss + 8 * h * C::SB];
             if (kk + C::KEYS > x.key_end) {
               // rows past the end hold anything, a scale that is no number among it: 0 * NaN is NaN
-              if (kk + v0 + 8 * h >= x.key_end) e0 = 0;
-              if (kk + v1 + 8 * h >= x.key_end) e1 = 0;
+              if (kk + v0 + 16 * g + 8 * h >= x.key_end) e0 = 0;
+              if (kk + v1 + 16 * g + 8 * h >= x.key_end) e1 = 0;
             }
             sl[h] = e4m3x2_to_f16(__byte_perm(e0, e1, 0x0040));
 #pragma unroll
@@ -548,7 +555,7 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
               const uint32_t w0 = hmul2(a0[i], sl[0]), w1 = hmul2(a1[i], sl[0]);
               const uint32_t w2 = hmul2(a2[i], sl[1]), w3 = hmul2(a3[i], sl[1]);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i], w0, w1, w2, w3, pb[n][0], pb[n][1]);
+              for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * j + i], w0, w1, w2, w3, pb[g][n][0], pb[g][n][1]);
             }
           }
         }
@@ -742,7 +749,7 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   using C = Q4Cfg<D, NT>;
   Q4Params p{};
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.H_kv * a.block_size;
-  // a stage's 64 keys in pieces that never cross a page
+  // a stage's keys in pieces that never cross a page
   p.piece = a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;
   const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B;
   if (!make_map_u8_2d(&p.tk, a.k_codes, C::CB, rows, p.piece, sw) || !make_map_u8_2d(&p.tv, a.v_codes, C::CB, rows, p.piece, sw))
@@ -763,7 +770,7 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;
   const long long most = min(C::MIN_CTAS * q4_sm_count(), kQ4MaxShares);
-  const long long steps = (static_cast<long long>(a.max_seqlen_k) + kDecodeKeyStep - 1) / kDecodeKeyStep;
+  const long long steps = (static_cast<long long>(a.max_seqlen_k) + kQ4Step - 1) / kQ4Step;
   // (a share is kQ4MinUnits long at least, and there are pairs * steps units at most)
   const long long want = a.n_splits ? p.n_items : pairs * max(1LL, steps) / kQ4MinUnits;
   const int grid = static_cast<int>(max(1LL, min(most, want)));

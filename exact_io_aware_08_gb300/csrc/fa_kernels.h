@@ -267,11 +267,11 @@ inline int q4_auto_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int n_k
   if (s > kDecodeMaxSplits) s = kDecodeMaxSplits;
   return static_cast<int>(s);
 }
-// Keys of a chunk: whole key tiles.
-inline int q4_chunk(int n_kv, int n_splits, bool tiles) {
-  const int step = tiles ? 128 : kDecodeKeyStep;
+// Keys of a step, and of a chunk: whole steps.
+constexpr int kQ4Step = 128;
+inline int q4_chunk(int n_kv, int n_splits) {
   const int c = (n_kv + n_splits - 1) / n_splits;
-  return c < step ? step : (c + step - 1) / step * step;
+  return c < kQ4Step ? kQ4Step : (c + kQ4Step - 1) / kQ4Step * kQ4Step;
 }
 
 // Size of the fixed device scratch behind fa_decode_splitkv_noalloc (decode.cu).
