@@ -23,9 +23,10 @@
 //                 P^T comes from the S^T accumulators by an 8x8 transpose in registers.
 // Keys sit in the S^T tile in the order kappa(r), which spreads the V loads over all banks.
 //
-// Layout.  Four warps compute, 32 keys each of a 128-key stage, 16 at a time; a fifth copies stages by TMA (codes,
-// swizzled) and bulk copies (scales) into a ring that runs on across work items.  Each CTA gets an
-// equal share of all sequences' key steps (Q4Share), whatever their lengths; with an explicit split
+// Layout.  One CTA an SM, of three or four teams.  A team's four warps compute, 32 keys each of a
+// 128-key stage, 16 at a time; a fifth copies stages by TMA (codes, swizzled) and bulk copies (scales,
+// query rows) into a ring that runs on across work items, and its registers go to the others.  Each
+// team gets an equal share of all sequences' key steps (Q4Share), whatever their lengths; with an explicit split
 // count the items are (sequence, key head, row block, chunk).
 #include "fa_kernels.h"
 #include "q4.cuh"
@@ -46,17 +47,27 @@ struct Q4Cfg {
   static constexpr int OFF_KS = 2 * CODES;
   static constexpr int OFF_VS = OFF_KS + SCALES;
   static constexpr int STAGE = (OFF_VS + SCALES + 1023) / 1024 * 1024;
-  static constexpr int NST = D == 128 && NT == 1 ? 2 : 3;
-  static constexpr int WARPS = 4;
-  static constexpr int THREADS = 32 * (WARPS + 1);
+  static constexpr int NST = D == 128 ? 2 : 3;
+  static constexpr int WARPS = 4;                             // computing warps of a team
+  static constexpr int TEAMS = NT == 1 ? 4 : 3;
+  static constexpr int THREADS = 128 * (TEAMS + 1);           // a warpgroup a team, and one that copies
+  static constexpr int QBUF = ROWS * D * 2;
+  static constexpr int OFF_Q = NST * STAGE;                   // two items' query rows
   static constexpr int MROW = D + 4;                          // floats of a merge row (bank spread)
-  static constexpr int OFF_MERGE = NST * STAGE;               // WARPS x ROWS x MROW
-  static constexpr int OFF_ML = OFF_MERGE + WARPS * ROWS * MROW * 4;   // WARPS x ROWS x (m, l)
-  static constexpr int OFF_BAR = OFF_ML + WARPS * ROWS * 8;
-  static constexpr int SMEM_BYTES = OFF_BAR + (2 * NST + 2) * 8 + 16 + 1024;
+  static constexpr int OFF_MERGE = OFF_Q + 2 * QBUF;          // (WARPS - 1) x ROWS x MROW
+  static constexpr int OFF_ML = OFF_MERGE + (WARPS - 1) * ROWS * MROW * 4;   // (WARPS - 1) x ROWS x (m, l)
+  static constexpr int OFF_BAR = OFF_ML + (WARPS - 1) * ROWS * 8;
+  // full[NST], empty[NST], q_full[2], q_empty[2], merge written, merge read; then start[3], abort flag
+  static constexpr int NBAR = 2 * NST + 6;
+  static constexpr int TEAM_BYTES = (OFF_BAR + NBAR * 8 + 16 + 1023) / 1024 * 1024;
+  static constexpr int SMEM_BYTES = TEAMS * TEAM_BYTES + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
   static constexpr int KS = D / 16;                           // k-steps of S^T
   static constexpr int MT = D / 16;                           // element tiles of O^T
-  static constexpr int MIN_CTAS = NT == 1 ? 4 : D == 64 ? 3 : 2;
+  // Launched with 96 (640 threads) or 128 (512) registers a thread, moved from the copying warps.
+  static constexpr uint32_t REG_COPY = NT == 1 ? 32 : 40;
+  static constexpr uint32_t REG_TEAM = NT == 1 ? 112 : 152;
+  static constexpr int REG_NEED = 128 * (static_cast<int>(REG_COPY) + TEAMS * static_cast<int>(REG_TEAM));
 };
 
 struct Q4Params {
@@ -118,15 +129,15 @@ __device__ __forceinline__ Q4Seq q4_seq(const Q4Params& p, int b, int rows_per_b
   return x;
 }
 
-// The shares of equal length: CTA i of N takes units [T i / N, T (i + 1) / N) of the T units of all
-// sequences, key heads and row blocks in order, however long each sequence is.  N is the grid, or less
+// The shares of equal length: team i of N takes units [T i / N, T (i + 1) / N) of the T units of all
+// sequences, key heads and row blocks in order, however long each sequence is.  N is all teams, or less
 // where a share would fall under kQ4MinUnits.
 constexpr int kQ4MinUnits = 1;
 struct Q4Share {
   long long total;                                            // T
   int n;                                                      // N
   __device__ __forceinline__ long long begin(int i) const { return total * i / n; }
-  // the CTA that has unit u
+  // the team that has unit u
   __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * n - 1) / total); }
 };
 
@@ -175,7 +186,7 @@ struct Q4Item {
 
 struct Q4Walk {
   const Q4Params& p;
-  int rows_per_block, item;                                   // chunks: the next item
+  int rows_per_block, id, stride, item;                       // this team, all teams; chunks: the next item
   int b;                                                      // shares: sequence, unit in it, units left
   int off, left;
   bool report;
@@ -196,7 +207,7 @@ struct Q4Walk {
 
   __device__ __forceinline__ bool next(Q4Item& x) {
     if (p.n_splits) {
-      for (; item < p.n_items; item += gridDim.x) {
+      for (; item < p.n_items; item += stride) {
         int i = item;
         const int split = i % p.n_splits;
         i /= p.n_splits;
@@ -211,7 +222,7 @@ struct Q4Walk {
         x.len = seq.len;
         finish(x, split * (p.chunk / kQ4Step), p.chunk / kQ4Step);
         x.out = p.n_splits == 1 ? -1 : split;
-        item += gridDim.x;
+        item += stride;
         return true;
       }
       return false;
@@ -232,9 +243,9 @@ struct Q4Walk {
     x.nq = seq.nq;
     x.len = seq.len;
     finish(x, step0, steps);
-    // a row block that a CTA has from its first to its last key is done; else the CTA keeps one state
+    // a row block that a team has from its first to its last key is done; else the team keeps one state
     // of a row block that began before its share (0) and one of one that goes on behind it (1)
-    x.out = steps == seq.steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
+    x.out = steps == seq.steps ? -1 : 2 * id + (step0 == 0 ? 1 : 0);
     off += steps;
     left -= steps;
     return true;
@@ -247,45 +258,56 @@ __device__ __forceinline__ uint32_t code_offset(int row, int chunk) {   // 16-by
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, Q4Cfg<D, NT>::MIN_CTAS)
-attend_q4_kernel(const __grid_constant__ Q4Params p) {
+__global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(const __grid_constant__ Q4Params p) {
   using C = Q4Cfg<D, NT>;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = align_smem_1k(smem_raw);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  // Warps 4 t to 4 t + 3 compute for team t, warp 4 TEAMS + t copies for it (others of that group idle).
+  const bool copies = warp >= 4 * C::TEAMS;
+  const int team = min(copies ? warp - 4 * C::TEAMS : warp >> 2, C::TEAMS - 1);
+  const bool idle = copies && warp - 4 * C::TEAMS >= C::TEAMS;
+  uint8_t* smem = align_smem_1k(smem_raw) + team * C::TEAM_BYTES;
   float* merge = reinterpret_cast<float*>(smem + C::OFF_MERGE);
   float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NST;
-  uint64_t* mrg = empty + C::NST;
+  uint64_t* q_full = empty + C::NST;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* mrg = q_empty + 2;                                // [0]: warps 1 to 3 wrote, [1]: warp 0 read
   int* start = reinterpret_cast<int*>(mrg + 2);               // sequence, unit in it, units of the share
   volatile int* abort_flag = start + 3;
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < C::NST; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], C::WARPS);
-    }
-    mbar_init(&mrg[0], C::WARPS);
-    mbar_init(&mrg[1], C::WARPS);
-    *abort_flag = 0;
-    fence_mbarrier_init();
-  }
-  if (warp == C::WARPS && p.n_splits == 0) {
-    int b;
-    long long before = 0;
-    const int cta = blockIdx.x;
-    const Q4Share sh = q4_share(p, C::ROWS, gridDim.x, cta == 0,
-                                [&](const Q4Share& x) { return cta < x.n && x.total > 0 ? x.begin(cta) : -1LL; }, &b, &before);
+  const int id = team * gridDim.x + blockIdx.x, teams = C::TEAMS * gridDim.x;   // few shares: one an SM first
+  if (copies && !idle) {
     if (lane == 0) {
-      start[0] = b;
-      start[1] = b < 0 ? 0 : static_cast<int>(sh.begin(cta) - before);
-      start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(cta + 1) - sh.begin(cta));
+      for (int s = 0; s < C::NST; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], C::WARPS);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&q_full[s], 1);
+        mbar_init(&q_empty[s], C::WARPS);
+      }
+      mbar_init(&mrg[0], C::WARPS - 1);
+      mbar_init(&mrg[1], 1);
+      *abort_flag = 0;
+      fence_mbarrier_init();
+    }
+    if (p.n_splits == 0) {
+      int b;
+      long long before = 0;
+      const Q4Share sh = q4_share(p, C::ROWS, teams, id == 0,
+                                  [&](const Q4Share& y) { return id < y.n && y.total > 0 ? y.begin(id) : -1LL; }, &b, &before);
+      if (lane == 0) {
+        start[0] = b;
+        start[1] = b < 0 ? 0 : static_cast<int>(sh.begin(id) - before);
+        start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(id + 1) - sh.begin(id));
+      }
     }
   }
   pdl_launch_dependents();
   __syncthreads();
-  Q4Walk walk{p, C::ROWS, static_cast<int>(blockIdx.x), 0, 0, 0, warp == C::WARPS && lane == 0, {}};
+  Q4Walk walk{p, C::ROWS, id, teams, id, 0, 0, 0, copies && lane == 0, {}};
   if (p.n_splits == 0) {
     walk.b = start[0];
     walk.off = start[1];
@@ -294,14 +316,29 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
   }
   Q4Item x;
 
-  if (warp == C::WARPS) {
+  if (copies) {
+    setmaxnreg_dec<C::REG_COPY>();
     // ---------------------------------------------------------------- copies
     // Lane j copies piece j (``piece`` keys of one page) of a stage.
     const int pieces = C::KEYS / p.piece;
     int s = 0;
-    uint32_t phase = 1, g = 0;                               // the first pass over the ring waits for nothing
+    uint32_t phase = 1, g = 0, it = 0;                       // the first pass over the ring waits for nothing
     bool ok = true;
-    while (ok && walk.next(x)) {
+    while (!idle && ok && walk.next(x)) {
+      // the item's query rows: those of a token lie side by side, lane j copies token j of the block
+      {
+        const int qi = it & 1;
+        if (it >= 2 && !(ok = mbar_wait_warp(&q_empty[qi], ((it >> 1) - 1) & 1, abort_flag, 435))) break;
+        const int row0 = x.rb * C::ROWS, row1 = min(x.nq * p.G, row0 + C::ROWS);
+        if (lane == 0) mbar_arrive_expect_tx(&q_full[qi], (row1 - row0) * D * 2);
+        __syncwarp();
+        const int i = row0 / p.G + lane;
+        const int a = max(row0, i * p.G), e = min(row1, (i + 1) * p.G);
+        if (a < e)
+          bulk_load(smem + C::OFF_Q + qi * C::QBUF + (a - row0) * D * 2,
+                    p.q + (static_cast<size_t>(x.first + i) * p.H + x.hkv * p.G + (a - i * p.G)) * D, (e - a) * D * 2, &q_full[qi]);
+        ++it;
+      }
       int window = -1, tab = 0;                              // 32 table entries from block ``window`` on
       const int last_blk = (x.key_end - 1) / p.block_size;
       int key = x.key0 + (lane < pieces ? lane : 0) * p.piece;
@@ -347,15 +384,18 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
       }
     }
     if (!ok) {
-      // drain the copies already issued (at most NST stages outstanding)
+      // drain the copies already issued (at most NST stages and two items' queries outstanding)
+      for (uint32_t y = (it > 2 ? it - 2 : 0); y < it; ++y) mbar_wait_warp(&q_full[y & 1], (y >> 1) & 1, nullptr, 436);
       for (uint32_t y = (g > C::NST ? g - C::NST : 0); y < g; ++y) mbar_wait_warp(&full[y % C::NST], (y / C::NST) & 1, nullptr, 431);
     }
   } else {
+    setmaxnreg_inc<C::REG_TEAM>();
     // ---------------------------------------------------------------- products
+    const int tw = warp & 3;                                          // warp of the team
     const int r = lane >> 2, c = lane & 3;
-    const int ra = warp * 32 + (r ^ (((r >> 1) ^ (r >> 2)) & 1));     // key kappa(r) of the warp's first 8
+    const int ra = tw * 32 + (r ^ (((r >> 1) ^ (r >> 2)) & 1));       // key kappa(r) of the warp's first 8
     const int e = 2 * c;
-    const int v0 = warp * 32 + (e ^ (((e >> 1) ^ (e >> 2)) & 1));     // keys kappa(2c) and kappa(2c + 1)
+    const int v0 = tw * 32 + (e ^ (((e >> 1) ^ (e >> 2)) & 1));       // keys kappa(2c) and kappa(2c + 1)
     const int v1 = v0 ^ 1;
     // Places in a stage; 8 rows on is 8 CB bytes on, under the swizzle too.
     constexpr int SR = D == 128 ? 1 : 2;                              // lanes' rows that share a scale block (V)
@@ -375,19 +415,18 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
       uint32_t qb[NT][C::KS][2];
       float2 fac[NT];
       int vis[NT][2];
+      if (!(ok = mbar_wait_warp(&q_full[it & 1], (it >> 1) & 1, abort_flag, 437))) break;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = x.rb * C::ROWS + 8 * n + r;
         const int i = row / p.G;
+        const uint8_t* src = smem + C::OFF_Q + (it & 1) * C::QBUF + (8 * n + r) * D * 2 + c * (D / 2);
         uint4 w[D / 32];
         float big = 0.f;
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
           w[j] = make_uint4(0u, 0u, 0u, 0u);
-          if (row < rows) {
-            const size_t at = (static_cast<size_t>(x.first + i) * p.H + x.hkv * p.G + (row - i * p.G)) * D;
-            w[j] = __ldg(reinterpret_cast<const uint4*>(p.q + at + c * (D / 4)) + j);
-          }
+          if (row < rows) w[j] = *(reinterpret_cast<const uint4*>(src) + j);
           const uint32_t ww[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(ww[k])), fabsf(bf16_hi(ww[k]))));
@@ -411,6 +450,8 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) vis[n][k] = min(x.key_end, __shfl_sync(0xffffffffu, seen, (2 * c + k) * 4));
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_empty[it & 1]);
       // m: reference, some number below every score before the first
       float2 m[NT], l[NT];
       float o[NT][C::MT][4];
@@ -568,8 +609,9 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
       }
       if (!ok) break;
 
-      // The warps' states of this stretch.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1), kept at
-      // position 16 t + 2 r (+1) of the merge row.
+      // The warps' states of this stretch.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1).  Warps 1
+      // to 3 leave theirs in shared memory (position 16 t + 2 r (+1) of the merge row) and go on; warp 0
+      // adds them to its own and writes.
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -577,51 +619,78 @@ attend_q4_kernel(const __grid_constant__ Q4Params p) {
           l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, off);
           l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, off);
         }
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float* dst = merge + (warp * C::ROWS + 8 * n + 2 * c + k) * C::MROW;
-#pragma unroll
-          for (int t = 0; t < C::MT; ++t)
-            *reinterpret_cast<float2*>(dst + 16 * t + 2 * r) = make_float2(o[n][t][k], o[n][t][2 + k]);
-          if (r == 0) ml[warp * C::ROWS + 8 * n + 2 * c + k] = k ? make_float2(m[n].y, l[n].y) : make_float2(m[n].x, l[n].x);
-        }
       }
-      if (!(ok = warps_sync(&mrg[0], it & 1, abort_flag, 433))) break;
-      for (int idx = threadIdx.x; idx < C::ROWS * (D / 2); idx += 32 * C::WARPS) {
-        const int n = idx / (D / 2), dd = 2 * (idx % (D / 2));
-        const int row = x.rb * C::ROWS + n;
-        if (row >= rows) break;
-        const int pos = D == 128 ? ((dd >> 1) & 7) * 16 + (dd >> 4) * 2 : ((dd >> 1) & 3) * 16 + (dd >> 3) * 2;
-        float M = kNone;
+      if (tw > 0) {
+        if (it > 0 && !(ok = mbar_wait_warp(&mrg[1], (it - 1) & 1, abort_flag, 434))) break;
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) M = fmaxf(M, ml[w * C::ROWS + n].x);
-        float a0 = 0.f, a1 = 0.f, L = 0.f;
+        for (int n = 0; n < NT; ++n) {
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-          const float2 st = ml[w * C::ROWS + n];
-          const float wt = fast_exp2(st.x - M);
-          const float2 v = *reinterpret_cast<const float2*>(merge + (w * C::ROWS + n) * C::MROW + pos);
-          a0 = fmaf(wt, v.x, a0);
-          a1 = fmaf(wt, v.y, a1);
-          L = fmaf(wt, st.y, L);
+          for (int k = 0; k < 2; ++k) {
+            const int at = (tw - 1) * C::ROWS + 8 * n + 2 * c + k;
+#pragma unroll
+            for (int t = 0; t < C::MT; ++t)
+              *reinterpret_cast<float2*>(merge + at * C::MROW + 16 * t + 2 * r) = make_float2(o[n][t][k], o[n][t][2 + k]);
+            if (r == 0) ml[at] = k ? make_float2(m[n].y, l[n].y) : make_float2(m[n].x, l[n].x);
+          }
         }
-        const int i = row / p.G;
-        const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
-        const size_t th = static_cast<size_t>(tok) * p.H + head;
-        if (x.out < 0) {
-          const bool none = M == kNone;                        // a row that sees no key
-          const float inv = none ? 0.f : p.descale_v / L;
-          *reinterpret_cast<uint32_t*>(p.o + th * D + dd) = none ? 0u : pack_bf16x2(a0 * inv, a1 * inv);
-          if (dd == 0)
-            p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-        } else {
-          const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + n;
-          float* dst = p.part + at * (D + 2);
-          *reinterpret_cast<float2*>(dst + dd) = make_float2(a0, a1);
-          if (dd == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(M == kNone ? -INFINITY : M, L);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mrg[0]);
+      } else {
+        if (!(ok = mbar_wait_warp(&mrg[0], it & 1, abort_flag, 433))) break;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int row = x.rb * C::ROWS + 8 * n + 2 * c + k;
+            float M = k ? m[n].y : m[n].x;
+            float2 st[C::WARPS - 1];
+#pragma unroll
+            for (int w = 0; w < C::WARPS - 1; ++w) {
+              st[w] = ml[w * C::ROWS + 8 * n + 2 * c + k];
+              M = fmaxf(M, st[w].x);
+            }
+            const float wt = fast_exp2((k ? m[n].y : m[n].x) - M);
+            float L = (k ? l[n].y : l[n].x) * wt;
+            float2 acc[C::MT];
+#pragma unroll
+            for (int t = 0; t < C::MT; ++t) acc[t] = make_float2(o[n][t][k] * wt, o[n][t][2 + k] * wt);
+#pragma unroll
+            for (int w = 0; w < C::WARPS - 1; ++w) {
+              const float wv = fast_exp2(st[w].x - M);
+              L = fmaf(wv, st[w].y, L);
+              const float* src = merge + (w * C::ROWS + 8 * n + 2 * c + k) * C::MROW + 2 * r;
+#pragma unroll
+              for (int t = 0; t < C::MT; ++t)
+                acc[t] = ffma2(make_float2(wv, wv), *reinterpret_cast<const float2*>(src + 16 * t), acc[t]);
+            }
+            if (row >= rows) continue;
+            const int i = row / p.G;
+            const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
+            const size_t th = static_cast<size_t>(tok) * p.H + head;
+            const bool none = M == kNone;                      // a row that sees no key
+            if (x.out < 0) {
+              const float inv = none ? 0.f : p.descale_v / L;
+              uint32_t h[C::MT];
+#pragma unroll
+              for (int t = 0; t < C::MT; ++t) h[t] = none ? 0u : pack_bf16x2(acc[t].x * inv, acc[t].y * inv);
+              uint4* dst = reinterpret_cast<uint4*>(p.o + th * D + r * (D / 8));
+#pragma unroll
+              for (int t = 0; t < C::MT / 4; ++t) dst[t] = make_uint4(h[4 * t], h[4 * t + 1], h[4 * t + 2], h[4 * t + 3]);
+              if (r == 0)
+                p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
+                    none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            } else {
+              const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + 8 * n + 2 * c + k;
+              float* dst = p.part + at * (D + 2);
+#pragma unroll
+              for (int t = 0; t < C::MT; ++t) *reinterpret_cast<float2*>(dst + r * (D / 8) + 2 * t) = acc[t];
+              if (r == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : M, L);
+            }
+          }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mrg[1]);
       }
-      if (!(ok = warps_sync(&mrg[1], it & 1, abort_flag, 434))) break;
       ++it;
     }
   }
@@ -682,7 +751,7 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
              lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
-// Joins the states of the row blocks that lie in several CTAs' shares: one warp a row.
+// Joins the states of the row blocks that lie in several teams' shares: one warp a row.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int grid) {
   constexpr int ROWS = 8 * NT;
@@ -705,7 +774,7 @@ __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_consta
   const int row = (tok - seq.first) * p.G + head % p.G;
   const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
   const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
-  if (c0 == c1) return;                                        // its CTA wrote the result
+  if (c0 == c1) return;                                        // its team wrote the result
   q4_join<D>([&](int i) -> const float* {
         const int c = c0 + i;
         return p.part + (static_cast<size_t>(2 * c + (i == 0 ? 1 : 0)) * ROWS + row % ROWS) * (D + 2);
@@ -767,9 +836,9 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done);
+  cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
-  const long long most = min(C::MIN_CTAS * q4_sm_count(), kQ4MaxShares);
+  const long long most = min(q4_sm_count(), kQ4MaxShares / C::TEAMS);
   const long long steps = (static_cast<long long>(a.max_seqlen_k) + kQ4Step - 1) / kQ4Step;
   // (a share is kQ4MinUnits long at least, and there are pairs * steps units at most)
   const long long want = a.n_splits ? p.n_items : pairs * max(1LL, steps) / kQ4MinUnits;
@@ -777,9 +846,9 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   log_launch("attend_q4_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_splits || grid == 1) return e;
+  if (e != cudaSuccess || a.n_splits) return e;
   log_launch("attend_q4_join_kernel<D, NT>", join_blocks(a), 128, 0ull);
-  return launch_join(attend_q4_join_kernel<D, NT>, join_blocks(a), stream, p, grid);
+  return launch_join(attend_q4_join_kernel<D, NT>, join_blocks(a), stream, p, C::TEAMS * grid);
 }
 
 template <int D>
