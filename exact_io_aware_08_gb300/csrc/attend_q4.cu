@@ -65,8 +65,8 @@ struct Q4Cfg {
   static constexpr int KS = D / 16;                           // k-steps of S^T
   static constexpr int MT = D / 16;                           // element tiles of O^T
   // Launched with 96 (640 threads) or 128 (512) registers a thread, moved from the copying warps.
-  static constexpr uint32_t REG_COPY = NT == 1 ? 32 : 40;
-  static constexpr uint32_t REG_TEAM = NT == 1 ? 112 : 152;
+  static constexpr uint32_t REG_COPY = 32;
+  static constexpr uint32_t REG_TEAM = NT == 1 ? 112 : 160;
   static constexpr int REG_NEED = 128 * (static_cast<int>(REG_COPY) + TEAMS * static_cast<int>(REG_TEAM));
 };
 

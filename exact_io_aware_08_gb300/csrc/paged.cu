@@ -30,6 +30,7 @@ struct AppendParams {
 };
 
 constexpr int kPagedThreads = 256;
+constexpr float kUp = 1.f + 0x1p-20f, kDown = 1.f - 0x1p-20f;
 
 // The 4-bit form of 16 values: the lane's vector 0 (f[0..7]) and 1 (f[8..15]).  ``split``: they
 // belong to two blocks, each completed by the neighbouring lane's vector; else to one block.
@@ -46,17 +47,33 @@ __device__ __forceinline__ void quantise16(const float (&f)[16], bool split, flo
   const float both = fmaxf(a[0], a[1]);
   a[0] = split ? fmaxf(a[0], o0) : both;
   a[1] = split ? fmaxf(a[1], o1) : both;
+  // A quotient decides only between neighbouring codes.  The product with the reciprocal is within
+  // 2^-22 of it; where the codes of that product 2^-20 up and down agree, so does the quotient's
+  // (rounding is monotone), and the division, some ten instructions, is made only where they differ.
+  const float six = __fmul_rn(6.f, descale), inv6 = __frcp_rn(six);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    scale[h] = f32_to_e4m3(__fdiv_rn(a[h], __fmul_rn(6.f, descale)));
+    const float2 near = fmul2(make_float2(__fmul_rn(a[h], inv6), __fmul_rn(a[h], inv6)), make_float2(kUp, kDown));
+    const uint32_t two = f32x2_to_e4m3(near.x, near.y);
+    scale[h] = two & 0xffu;
+    if (scale[h] != two >> 8) scale[h] = f32x2_to_e4m3(__fdiv_rn(a[h], six), 0.f) & 0xffu;
     const float sd = __fmul_rn(f16x2_to_f32(e4m3x2_to_f16(scale[h])).x, descale);
-    float y[8];
+    const float inv = sd > 0.f ? __frcp_rn(sd) : 0.f;        // (a scale of 0: codes of 0 with x's signs)
+    const float2 up = make_float2(kUp, kUp), down = make_float2(kDown, kDown);
+    float y[8], z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = f[8 * h + i];
-      y[i] = sd > 0.f ? __fdiv_rn(x, sd) : copysignf(0.f, x);
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = fmul2(make_float2(f[8 * h + 2 * i], f[8 * h + 2 * i + 1]), make_float2(inv, inv));
+      const float2 u = fmul2(q, up), v = fmul2(q, down);
+      y[2 * i] = u.x; y[2 * i + 1] = u.y;
+      z[2 * i] = v.x; z[2 * i + 1] = v.y;
     }
     code[h] = f32x8_to_e2m1(y);
+    if (code[h] != f32x8_to_e2m1(z)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = sd > 0.f ? __fdiv_rn(f[8 * h + i], sd) : copysignf(0.f, f[8 * h + i]);
+      code[h] = f32x8_to_e2m1(y);
+    }
   }
 }
 
@@ -140,7 +157,8 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
       }
     }
     const int v0 = sp ? u : 2 * u, v1 = sp ? u + r16 : 2 * u + 1;
-    if (Q4) {
+    // (a pass of query heads only, the same for the whole warp, has nothing to quantise)
+    if (Q4 && (part * U + j) * SPW + SPW > p.H) {
       uint32_t code[2], scale[2];
       quantise16(f, sp, is_v ? p.descale_v : p.descale_k, code, scale);
       if (slot < slots && !is_q) {
@@ -157,9 +175,8 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
           sc[u] = static_cast<uint8_t>(scale[0]);
         }
       }
-      if (!is_q) continue;
     }
-    if (slot < slots) {
+    if (slot < slots && (!Q4 || is_q)) {
       uint32_t out[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) out[i] = rot ? pack_bf16x2(f[2 * i], f[2 * i + 1]) : in[i];
@@ -234,6 +251,21 @@ __global__ void __launch_bounds__(kPagedThreads) gather_q4_kernel(const GatherPa
   }
 }
 
+// A warp takes U passes of a token.  One where the passes are too few to fill the GPU twice over,
+// so that they spread; else four, so that the search for the token's place (four dependent loads) is
+// shared and four times the bytes are in flight behind it.
+static bool few_passes(long long passes) { return passes < 152LL * 64; }
+
+template <int D, bool Q4, int U>
+static cudaError_t launch_append_u(AppendParams& p, long long passes, cudaStream_t stream) {
+  p.warps_per_token = static_cast<int>((passes + U - 1) / U);
+  const long long warps = static_cast<long long>(p.total) * p.warps_per_token;
+  const long long grid = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
+  log_launch(Q4 ? "append_kernel<D, true, U>" : "append_kernel<D, false, U>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
+  append_kernel<D, Q4, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <int D, bool Q4>
 static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   AppendParams p{};
@@ -254,18 +286,23 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const int per_pass = 32 / (D / 16);
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;
-  constexpr int U = 1;
-  p.warps_per_token = static_cast<int>((passes + U - 1) / U);
-  const long long warps = static_cast<long long>(p.total) * p.warps_per_token;
-  const long long grid = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
-  log_launch(Q4 ? "append_kernel<D, true>" : "append_kernel<D, false>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
-  append_kernel<D, Q4, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (few_passes(passes * p.total)) return launch_append_u<D, Q4, 1>(p, passes, stream);
+  return launch_append_u<D, Q4, 4>(p, passes, stream);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
   if (a.k_scales) return a.d == 64 ? launch_append_d<64, true>(a, stream) : launch_append_d<128, true>(a, stream);
   return a.d == 64 ? launch_append_d<64, false>(a, stream) : launch_append_d<128, false>(a, stream);
+}
+
+template <int D, int U>
+static cudaError_t launch_gather_u(GatherParams& p, long long passes, cudaStream_t stream) {
+  p.warps_per_token = static_cast<int>((passes + U - 1) / U);
+  const long long warps = static_cast<long long>(p.total) * p.warps_per_token;
+  const long long grid = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
+  log_launch("gather_q4_kernel<D, U>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
+  gather_q4_kernel<D, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -279,13 +316,8 @@ static cudaError_t launch_gather_d(const GatherArgs& a, cudaStream_t stream) {
   p.descale_k = a.descale_k; p.descale_v = a.descale_v;
   const int per_pass = 32 / (D / 16);
   const long long passes = (2LL * p.H_kv + per_pass - 1) / per_pass;
-  constexpr int U = 1;
-  p.warps_per_token = static_cast<int>((passes + U - 1) / U);
-  const long long warps = static_cast<long long>(p.total) * p.warps_per_token;
-  const long long grid = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
-  log_launch("gather_q4_kernel<D>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
-  gather_q4_kernel<D, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if (few_passes(passes * p.total)) return launch_gather_u<D, 1>(p, passes, stream);
+  return launch_gather_u<D, 4>(p, passes, stream);
 }
 
 cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream) {

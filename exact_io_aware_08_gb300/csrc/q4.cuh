@@ -42,9 +42,11 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* y) {
   return r;
 }
 
-// fp32 -> e4m3 (to nearest even, saturating at 448), in the low byte.
-__device__ __forceinline__ uint32_t f32_to_e4m3(float x) {
-  return pack_e4m3x4(x, 0.f, 0.f, 0.f) & 0xffu;
+// Two fp32 values -> e4m3 (to nearest even, saturating at 448), ``lo`` in the low byte of 16 bits.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3(float lo, float hi) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 h;\n\tcvt.rn.satfinite.e4m3x2.f32 h, %2, %1;\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
