@@ -29,7 +29,7 @@ struct AppendParams {
   float descale_k, descale_v;
 };
 
-constexpr int kPagedThreads = 256;
+constexpr int kPagedThreads = 128;
 constexpr float kUp = 1.f + 0x1p-20f, kDown = 1.f - 0x1p-20f;
 
 // The 4-bit form of 16 values: the lane's vector 0 (f[0..7]) and 1 (f[8..15]).  ``split``: they
@@ -251,9 +251,12 @@ __global__ void __launch_bounds__(kPagedThreads) gather_q4_kernel(const GatherPa
   }
 }
 
-// A warp takes U passes of a token.  One where the passes are too few to fill the GPU twice over,
-// so that they spread; else four, so that the search for the token's place (four dependent loads) is
-// shared and four times the bytes are in flight behind it.
+// A warp takes U passes of a token.  One where the passes are too few to fill the GPU twice over, so
+// that they spread (4 x 16 tokens of 96 heads: 3.3 against 4.2 us); else more, so that the search for
+// the token's place (four dependent loads) is shared and more bytes are in flight behind it.  How
+// many: 6, or 3 where that leaves fewer passes empty, or, in bf16 only, 8 where none is empty then.
+// Measured with 1, 3, 6 and 8: 4 x 4096 tokens of 24 passes in bf16 204, 141, 141, 134 us; 12 passes
+// in 4 bits (with the reading back) 437, 291, 274, 354; 3 passes in 4 bits 66, 54, 83, 104.
 static bool few_passes(long long passes) { return passes < 152LL * 64; }
 
 template <int D, bool Q4, int U>
@@ -287,7 +290,10 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;
   if (few_passes(passes * p.total)) return launch_append_u<D, Q4, 1>(p, passes, stream);
-  return launch_append_u<D, Q4, 4>(p, passes, stream);
+  if constexpr (!Q4)
+    if (passes % 8 == 0) return launch_append_u<D, Q4, 8>(p, passes, stream);
+  if ((passes + 5) / 6 * 6 <= (passes + 2) / 3 * 3) return launch_append_u<D, Q4, 6>(p, passes, stream);
+  return launch_append_u<D, Q4, 3>(p, passes, stream);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
@@ -316,8 +322,9 @@ static cudaError_t launch_gather_d(const GatherArgs& a, cudaStream_t stream) {
   p.descale_k = a.descale_k; p.descale_v = a.descale_v;
   const int per_pass = 32 / (D / 16);
   const long long passes = (2LL * p.H_kv + per_pass - 1) / per_pass;
-  if (few_passes(passes * p.total)) return launch_gather_u<D, 1>(p, passes, stream);
-  return launch_gather_u<D, 4>(p, passes, stream);
+  // two passes a warp where there are (8 x 16384 tokens of 4 passes, with 1, 2 and 4: 146, 124, 174 us)
+  if (passes == 1 || few_passes(passes * p.total)) return launch_gather_u<D, 1>(p, passes, stream);
+  return launch_gather_u<D, 2>(p, passes, stream);
 }
 
 cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream) {
