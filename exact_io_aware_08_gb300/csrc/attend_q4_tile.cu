@@ -77,6 +77,182 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
 }
 
+// Brings query row ``th`` (none: zeros) as row ``row`` of the tile, in fp16, and returns its score factor.
+template <int D>
+__device__ __forceinline__ float q4_query_row(const Q4TParams& p, bool has, size_t th, uint8_t* tile, int row) {
+  uint4 x[D / 8];
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    x[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (has) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + th * D) + i);
+    const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(ww[k])), fabsf(bf16_hi(ww[k]))));
+  }
+  // the largest element goes to [2^14, 2^15); exponents such that the power and its inverse are normal
+  const int ex = big == 0.f ? 14 : max(-100, static_cast<int>(__float_as_uint(big) >> 23) - 127);
+  const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
+  const float c2 = p.score * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    uint32_t h[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(ww[k]) * up, bf16_hi(ww[k]) * up);
+    *reinterpret_cast<uint4*>(tile + (i >> 3) * Q4TCfg<D>::CHUNK + sw128_offset(row, (i & 7) * 8)) =
+        make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  return c2;
+}
+
+// One key tile of a row: S in tensor memory (columns t_s) becomes P over its first half, O (t_o) is
+// rescaled where the row's reference moves.  Keys from ``lim`` on are not the row's.
+template <int D>
+__device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int k0, int lim, bool first, float c2, float& m, float& l) {
+  // S in four quarters of 32 columns.  The row maximum needs all four; the first two then stay in
+  // registers and the others are loaded a second time when their turn comes, so that a thread
+  // holds 96 scores at most beside P's words (all 128 made the compiler spill 450 bytes a thread:
+  // 1558 instead of 1200 us for 4x1024 tokens over 16384 keys).
+  const bool edge = __any_sync(0xffffffffu, k0 + Q4TCfg<D>::BN > lim);
+  uint32_t s0[32], s1[32], s2[32];
+  auto mask = [&](uint32_t (&v)[32], int q) {
+    if (edge) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k)
+        if (k0 + 32 * q + k >= lim) v[k] = 0xff800000u;
+    }
+  };
+  auto top = [&](uint32_t (&v)[32]) {
+    float x = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
+    float y = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+#pragma unroll
+    for (int k = 6; k < 30; k += 4) {
+      x = fmax3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
+      y = fmax3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
+    }
+    return fmax3(fmaxf(x, y), __uint_as_float(v[30]), __uint_as_float(v[31]));
+  };
+  float mq;
+  {
+    uint32_t s3[32];
+    tmem_ld32(t_s + 64, s2);
+    tmem_ld32(t_s + 96, s3);
+    tmem_ld32(t_s, s0);
+    tmem_ld32(t_s + 32, s1);
+    tmem_wait_ld();
+    mask(s2, 2);
+    mask(s3, 3);
+    mask(s0, 0);
+    mask(s1, 1);
+    mq = fmaxf(fmaxf(top(s0), top(s1)), fmaxf(top(s2), top(s3)));
+  }
+  const float cand = fmaxf(m, mq);
+  // a row that sees none of the tile's keys has nothing to move
+  const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > Q4TCfg<D>::RESCALE);
+  if (__any_sync(0xffffffffu, move)) {
+    const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
+    if (move) {
+      l *= alpha;
+      m = cand;
+    }
+    if (!first) {
+      // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order)
+#pragma unroll
+      for (int k = 0; k < D / 32; ++k) {
+        uint32_t rr[32];
+        tmem_ld32(t_o + k * 32, rr);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          const float2 v = fmul2(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), make_float2(alpha, alpha));
+          rr[i] = __float_as_uint(v.x);
+          rr[i + 1] = __float_as_uint(v.y);
+        }
+        tmem_st32(t_o + k * 32, rr);
+      }
+    }
+  }
+  float ms = (m == -INFINITY) ? 0.f : m * c2;
+  // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
+  // taken off first
+  const bool far = __any_sync(0xffffffffu, fabsf(ms) > 4096.f);
+  const float ref = (m == -INFINITY) ? 0.f : m;
+  if (far) ms = 0.f;
+  const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
+  float2 rs[2];
+  rs[0] = rs[1] = make_float2(0.f, 0.f);
+  auto weigh = [&](uint32_t (&v)[32], int q) {            // P's columns 16 q .. 16 q + 15
+    if (far) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) - ref);
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float2 x = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2v, nms);
+      const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+      pk[k] = pack_f16x2(e.x, e.y);
+      rs[k & 1] = fadd2(rs[k & 1], e);
+    }
+    tmem_st16(t_s + q * 16, pk);
+  };
+  tmem_ld32(t_s + 64, s2);                                // (P covers columns 0 to 63 only)
+  weigh(s0, 0);
+  weigh(s1, 1);
+  tmem_ld32(t_s + 96, s0);
+  tmem_wait_ld();
+  mask(s2, 2);
+  weigh(s2, 2);
+  mask(s0, 3);
+  weigh(s0, 3);
+  const float2 rs01 = fadd2(rs[0], rs[1]);
+  l += rs01.x + rs01.y;
+}
+
+// The row's result, or its chunk's state: O of columns t_o over l (``any``: some key tile was run).
+template <int D>
+__device__ __forceinline__ void q4_store_row(const Q4TParams& p, uint32_t t_o, bool any, bool has, size_t th, int tok, int head, int split,
+                                             float c2, float m, float l) {
+  const bool none = l == 0.f;                             // a row that sees no key (of the chunk)
+  const float inv = none ? 0.f : p.descale_v / l;
+  float* dst = p.n_splits > 1 ? p.part + (th * p.n_splits + split) * (D + 2) : nullptr;
+#pragma unroll
+  for (int k = 0; k < D / 32; ++k) {
+    uint32_t rr[32];
+    if (any) {
+      tmem_ld32(t_o + k * 32, rr);
+      tmem_wait_ld();
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) rr[i] = 0u;
+    }
+    if (has) {
+      if (dst) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+          *reinterpret_cast<float2*>(dst + k * 32 + i) = make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8) {
+          uint32_t h[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            h[e] = none ? 0u : pack_bf16x2(__uint_as_float(rr[i + 2 * e]) * inv, __uint_as_float(rr[i + 2 * e + 1]) * inv);
+          *reinterpret_cast<uint4*>(p.o + th * D + k * 32 + i) = make_uint4(h[0], h[1], h[2], h[3]);
+        }
+      }
+    }
+  }
+  if (has) {
+    if (dst)
+      *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : m * c2, l);
+    else
+      p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
+          none ? -INFINITY : (fmaf(m, c2, log2f(l))) * 0.6931471805599453f;
+  }
+}
+
 template <int D>
 __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(const __grid_constant__ Q4TParams p) {
   using C = Q4TCfg<D>;
@@ -353,34 +529,10 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     const int n = t == 0 ? n_t[0] : n_t[1];
     const int tok = first + r / p.G, head = hkv * p.G + r % p.G;
     const size_t th = static_cast<size_t>(tok) * p.H + head;
-    float c2;                                                 // score factor of the row
-    {
-      uint4 x[D / 8];
-      float big = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < rows) x[i] = __ldg(reinterpret_cast<const uint4*>(p.q + th * D) + i);
-        const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) big = fmaxf(big, fmaxf(fabsf(bf16_lo(ww[k])), fabsf(bf16_hi(ww[k]))));
-      }
-      // the largest element goes to [2^14, 2^15); exponents such that the power and its inverse are normal
-      const int ex = big == 0.f ? 14 : max(-100, static_cast<int>(__float_as_uint(big) >> 23) - 127);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
-      c2 = p.score * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h[k] = pack_f16x2(bf16_lo(ww[k]) * up, bf16_hi(ww[k]) * up);
-        *reinterpret_cast<uint4*>(sQ + t * C::TILE + (i >> 3) * C::CHUNK + sw128_offset(row, (i & 7) * 8)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(q_full);
-    }
+    const bool has = r < rows;
+    const float c2 = q4_query_row<D>(p, has, th, sQ + t * C::TILE, row);
+    fence_proxy_async_smem();
+    mbar_arrive(q_full);
     const int lim = min(key_end, seen(r));                    // keys below it are this row's
     float m = -INFINITY, l = 0.f;                             // reference (raw units) and sum of the weights
     bool ok = true;
@@ -388,105 +540,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
       tc_fence_after();
-      // S in four quarters of 32 columns.  The row maximum needs all four; the first two then stay in
-      // registers and the others are loaded a second time when their turn comes, so that a thread
-      // holds 96 scores at most beside P's words (all 128 made the compiler spill 450 bytes a thread:
-      // 1558 instead of 1200 us for 4x1024 tokens over 16384 keys).
-      const int k0 = key0 + j * C::BN;
-      const bool edge = __any_sync(0xffffffffu, k0 + C::BN > lim);
-      uint32_t s0[32], s1[32], s2[32];
-      auto mask = [&](uint32_t (&v)[32], int q) {
-        if (edge) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k)
-            if (k0 + 32 * q + k >= lim) v[k] = 0xff800000u;
-        }
-      };
-      auto top = [&](uint32_t (&v)[32]) {
-        float x = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-        float y = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
-#pragma unroll
-        for (int k = 6; k < 30; k += 4) {
-          x = fmax3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-          y = fmax3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-        }
-        return fmax3(fmaxf(x, y), __uint_as_float(v[30]), __uint_as_float(v[31]));
-      };
-      float mq;
-      {
-        uint32_t s3[32];
-        tmem_ld32(t_s + 64, s2);
-        tmem_ld32(t_s + 96, s3);
-        tmem_ld32(t_s, s0);
-        tmem_ld32(t_s + 32, s1);
-        tmem_wait_ld();
-        mask(s2, 2);
-        mask(s3, 3);
-        mask(s0, 0);
-        mask(s1, 1);
-        mq = fmaxf(fmaxf(top(s0), top(s1)), fmaxf(top(s2), top(s3)));
-      }
-      const float cand = fmaxf(m, mq);
-      // a row that sees none of the tile's keys has nothing to move
-      const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > C::RESCALE);
-      if (__any_sync(0xffffffffu, move)) {
-        const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
-        if (move) {
-          l *= alpha;
-          m = cand;
-        }
-        if (j > 0) {
-          // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order)
-#pragma unroll
-          for (int k = 0; k < D / 32; ++k) {
-            uint32_t rr[32];
-            tmem_ld32(t_o + k * 32, rr);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 v = fmul2(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), make_float2(alpha, alpha));
-              rr[i] = __float_as_uint(v.x);
-              rr[i + 1] = __float_as_uint(v.y);
-            }
-            tmem_st32(t_o + k * 32, rr);
-          }
-        }
-      }
-      float ms = (m == -INFINITY) ? 0.f : m * c2;
-      // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
-      // taken off first
-      const bool far = __any_sync(0xffffffffu, fabsf(ms) > 4096.f);
-      const float ref = (m == -INFINITY) ? 0.f : m;
-      if (far) ms = 0.f;
-      const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
-      float2 rs[2];
-      rs[0] = rs[1] = make_float2(0.f, 0.f);
-      auto weigh = [&](uint32_t (&v)[32], int q) {            // P's columns 16 q .. 16 q + 15
-        if (far) {
-#pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) - ref);
-        }
-        uint32_t pk[16];
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float2 x = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2v, nms);
-          const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
-          pk[k] = pack_f16x2(e.x, e.y);
-          rs[k & 1] = fadd2(rs[k & 1], e);
-        }
-        tmem_st16(t_s + q * 16, pk);
-      };
-      tmem_ld32(t_s + 64, s2);                                // (P covers columns 0 to 63 only)
-      weigh(s0, 0);
-      weigh(s1, 1);
-      tmem_ld32(t_s + 96, s0);
-      tmem_wait_ld();
-      mask(s2, 2);
-      weigh(s2, 2);
-      mask(s0, 3);
-      weigh(s0, 3);
-      const float2 rs01 = fadd2(rs[0], rs[1]);
-      l += rs01.x + rs01.y;
+      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -503,43 +557,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       tc_fence_after();
     }
     if (ok && row0 + t * C::BM < rows) {
-      const bool none = l == 0.f;                             // a row that sees no key (of the chunk)
-      const float inv = none ? 0.f : p.descale_v / l;
-      float* dst = p.n_splits > 1 ? p.part + (th * p.n_splits + split) * (D + 2) : nullptr;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t rr[32];
-        if (n > 0) {
-          tmem_ld32(t_o + k * 32, rr);
-          tmem_wait_ld();
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) rr[i] = 0u;
-        }
-        if (r < rows) {
-          if (dst) {
-#pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              *reinterpret_cast<float2*>(dst + k * 32 + i) = make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                h[e] = none ? 0u : pack_bf16x2(__uint_as_float(rr[i + 2 * e]) * inv, __uint_as_float(rr[i + 2 * e + 1]) * inv);
-              *reinterpret_cast<uint4*>(p.o + th * D + k * 32 + i) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          }
-        }
-      }
-      if (r < rows) {
-        if (dst)
-          *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : m * c2, l);
-        else
-          p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
-              none ? -INFINITY : (fmaf(m, c2, log2f(l))) * 0.6931471805599453f;
-      }
+      q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, split, c2, m, l);
     }
   }
   __syncwarp();
@@ -549,6 +567,374 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
+}
+
+// ------------------------------------------------------------------------------------------
+// The same for 512 rows of a key head on a pair of SMs (d = 128): a cluster of two CTAs whose tensor
+// cores work on one product.  Tile t is 256 rows, 128 in each CTA, and each CTA holds half of the
+// other operand: 64 of a key tile's 128 keys for S, 64 of the 128 columns of V for O.  So each
+// unpacks half as much a row (K: its 64 keys whole, V: its half of every key), and the tensor core
+// reads half as much of it from each shared memory.
+//
+// The even CTA's warp 1 issues all products; the barriers it waits on are its own and both CTAs arrive
+// there, and a product's completion is signalled to both.
+// ------------------------------------------------------------------------------------------
+struct Q4PCfg {
+  static constexpr int D = 128, BN = 128;
+  static constexpr int CHUNK = 128 * 128;                     // 64 columns of a Q tile, or V's half
+  static constexpr int QTILE = 2 * CHUNK;
+  static constexpr int HALF = 16384;                          // half a K tile [2 chunks][64 keys], or of V [128 keys]
+  static constexpr int NS = 3;
+  static constexpr int CB = 64, SB = 8;
+  static constexpr int OFF_CV = 64 * CB;                      // inside a code stage: K of 64 keys, V of 128, scales
+  static constexpr int OFF_CKS = OFF_CV + 128 * CB;
+  static constexpr int OFF_CVS = OFF_CKS + 64 * SB;
+  static constexpr int CSTAGE = OFF_CVS + 128 * SB;
+  static constexpr int NC = 3;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = 2 * QTILE;
+  static constexpr int OFF_V = OFF_K + NS * HALF;
+  static constexpr int OFF_C = OFF_V + NS * HALF;
+  static constexpr int OFF_BAR = OFF_C + NC * CSTAGE;
+  // q_full, k_full[NS], v_full[NS], p_full[2] (of the even CTA); k_empty[NS], v_empty[NS], s_full[2],
+  // o_done[2], c_full[NC], c_empty[NC]
+  static constexpr int NBAR = 1 + 4 * NS + 6 + 2 * NC;
+  static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+  static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t T_S = 0, T_O = 256;
+  static constexpr int THREADS = 512;
+  static constexpr int UNPACK_WARPS = 4;
+  static constexpr uint32_t REG_CTRL = 64, REG_SOFTMAX = 168, REG_UNPACK = 96;
+  static constexpr int REG_NEED = 128 * 64 + 256 * 168 + 128 * 96;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q4PCfg::THREADS, 1)
+attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
+  using C = Q4PCfg;
+  constexpr int D = C::D;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = align_smem_1k(smem_raw);                    // (the same address in both CTAs)
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sK = smem + C::OFF_K;
+  uint8_t* sV = smem + C::OFF_V;
+  uint8_t* sC = smem + C::OFF_C;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* k_full = q_full + 1;
+  uint64_t* v_full = k_full + C::NS;
+  uint64_t* p_full = v_full + C::NS;
+  uint64_t* k_empty = p_full + 2;
+  uint64_t* v_empty = k_empty + C::NS;
+  uint64_t* s_full = v_empty + C::NS;
+  uint64_t* o_done = s_full + 2;
+  uint64_t* c_full = o_done + 2;
+  uint64_t* c_empty = c_full + C::NC;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+
+  // Item, as in the kernel above, of 512 rows.
+  const int pair = static_cast<int>(blockIdx.x) >> 1;
+  const int per_rb = p.n_seqs * p.H_kv * p.n_splits;
+  const int rb = p.row_blocks - 1 - pair / per_rb;
+  int w = pair % per_rb;
+  const int split = w % p.n_splits;
+  w /= p.n_splits;
+  const int hkv = w % p.H_kv;
+  const int b = w / p.H_kv;
+  int first = b, nq = 1;
+  if (p.cu_q) {
+    first = __ldg(p.cu_q + b);
+    const int end = __ldg(p.cu_q + b + 1);
+    nq = end - first;
+    if (first < 0 || end < first || end > p.total_q || nq > p.max_q) {
+      if (threadIdx.x == 0 && rb == 0) report_device_error(FA_DEV_BAD_CONFIG, 470);
+      return;
+    }
+  }
+  int len = __ldg(p.seqlens + b);
+  if (len < 0 || len > p.max_k) {
+    if (threadIdx.x == 0 && rb == 0) report_device_error(FA_DEV_BAD_CONFIG, 471);
+    len = 0;
+  }
+  const int rows = nq * p.G;
+  const int row0 = rb * 512;
+  if (row0 >= rows) return;                                   // both CTAs, before any shared state
+  auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
+  const int key0 = split * p.chunk;
+  int n_t[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int last = min(key0 + p.chunk, seen(row0 + t * 256 + 255));
+    n_t[t] = (row0 + t * 256 >= rows || last <= key0) ? 0 : (last - key0 + C::BN - 1) / C::BN;
+  }
+  const int n_max = max(n_t[0], n_t[1]);
+  const int key_end = min(key0 + p.chunk, seen(row0 + 511));
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 16);                                    // softmax warps of both CTAs
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&k_full[s], 2 * C::UNPACK_WARPS);
+      mbar_init(&v_full[s], 2 * C::UNPACK_WARPS);
+      mbar_init(&k_empty[s], 1);
+      mbar_init(&v_empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&p_full[t], 8 + 1);                           // the tile's softmax warps of both CTAs, and the helper
+      mbar_init(&s_full[t], 1);
+      mbar_init(&o_done[t], 1);
+    }
+    for (int s = 0; s < C::NC; ++s) {
+      mbar_init(&c_full[s], 1);
+      mbar_init(&c_empty[s], C::UNPACK_WARPS);
+    }
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  __syncthreads();
+  cluster_sync();                                             // barriers and tensor memory of both are there
+  tc_fence_after();
+  const uint32_t tbase = *tmem_slot;
+
+  if (warp < 4) {
+    setmaxnreg_dec<C::REG_CTRL>();
+    if (warp == 0) {
+      // -------------------------------------------------------------- copies: K of this CTA's 64 keys, V of all 128
+      const int kp = 64 / p.piece, vp = 128 / p.piece;        // at most 4 and 8 pieces: lanes 8 to 11, 0 to 7
+      bool ok = true;
+      int window = -1, tab = 0, g = 0;
+      for (; ok && g < n_max; ++g) {
+        const int s = g % C::NC, u = g / C::NC;
+        const int kk = key0 + g * C::BN;                      // (< key_end)
+        const int blk0 = kk / p.block_size;
+        if (window < 0 || blk0 + 8 >= window + 32) {
+          window = blk0;
+          tab = window + lane <= (key_end - 1) / p.block_size
+                    ? __ldg(p.table + static_cast<size_t>(b) * p.max_blocks + window + lane) : 0;
+        }
+        const bool is_v = lane < 8;
+        const int piece = is_v ? lane : lane - 8;
+        const bool role = is_v ? piece < vp : (lane < 12 && piece < kp);
+        const int at = role ? piece * p.piece : 0;            // key of the stage's part
+        const int key = kk + (is_v ? 0 : rank * 64) + at;
+        const int blk = key / p.block_size;
+        int page = __shfl_sync(0xffffffffu, tab, (blk - window) & 31);
+        const bool mine = role && key < key_end;
+        if (mine && (page < 0 || page >= p.num_blocks)) {
+          report_device_error(FA_DEV_BAD_CONFIG, 472);
+          page = 0;                                           // stays in bounds; the result is reported invalid
+        }
+        if (u > 0 && !(ok = mbar_wait_warp(&c_empty[s], (u - 1) & 1, abort_flag, 480))) break;
+        const int live = __popc(__ballot_sync(0xffffffffu, mine));
+        if (lane == 0) mbar_arrive_expect_tx(&c_full[s], live * p.piece * (C::CB + C::SB));
+        __syncwarp();
+        if (mine) {
+          uint8_t* st = sC + s * C::CSTAGE;
+          const size_t row = (static_cast<size_t>(page) * p.H_kv + hkv) * p.block_size + (key - blk * p.block_size);
+          bulk_load(st + (is_v ? C::OFF_CV : 0) + at * C::CB, (is_v ? p.vc : p.kc) + row * C::CB, p.piece * C::CB, &c_full[s]);
+          bulk_load(st + (is_v ? C::OFF_CVS : C::OFF_CKS) + at * C::SB, (is_v ? p.vs : p.ks) + row * C::SB, p.piece * C::SB,
+                    &c_full[s]);
+        }
+        __syncwarp();
+      }
+      if (!ok)
+        for (int x = max(0, g - C::NC); x < g; ++x) mbar_wait_warp(&c_full[x % C::NC], (x / C::NC) & 1, nullptr, 481);
+    } else if (warp == 1 && rank == 0) {
+      // -------------------------------------------------------------- products of the pair
+      const uint32_t idesc = idesc_f16_f32(256, 128, 0, 0), idesc_o = idesc_f16_f32(256, 128, 0, 1);
+      const uint64_t dq0 = smem_desc_sw128(smem_u32(sQ), 0, 1024);
+      const uint64_t dk0 = smem_desc_sw128(smem_u32(sK), 0, 1024);
+      const uint64_t dv0 = smem_desc_sw128(smem_u32(sV), C::CHUNK, 1024);
+      auto issue_s = [&](int t, int j) {
+        const uint64_t a = desc_advance(dq0, t * C::QTILE);
+        const uint64_t bd = desc_advance(dk0, (j % C::NS) * C::HALF);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          umma_ss_pair(tbase + C::T_S + t * 128, desc_advance(a, (ks >> 2) * C::CHUNK + (ks & 3) * 32),
+                       desc_advance(bd, (ks >> 2) * (C::HALF / 2) + (ks & 3) * 32), idesc, ks > 0);
+        umma_commit_pair(&s_full[t]);
+      };
+      auto issue_pv = [&](int t, int j) {
+        const uint64_t bd = desc_advance(dv0, (j % C::NS) * C::HALF);
+#pragma unroll
+        for (int ks = 0; ks < C::BN / 16; ++ks)
+          umma_ts_pair(tbase + C::T_O + t * 128, tbase + C::T_S + t * 128 + ks * 8, desc_advance(bd, ks * 16 * 128), idesc_o,
+                       (j > 0 || ks > 0) ? 1u : 0u);
+      };
+      bool ok = n_max > 0 && mbar_wait_warp_cluster(q_full, 0, abort_flag, 482) &&
+                mbar_wait_warp_cluster(&k_full[0], 0, abort_flag, 483);
+      if (ok) {
+        tc_fence_after();
+        if (n_t[0] > 0) issue_s(0, 0);
+        if (n_t[1] > 0) issue_s(1, 0);
+        // (a tile is given back only where another follows in its place: no signal stays unawaited)
+        if (C::NS < n_max) umma_commit_pair(&k_empty[0]);
+      }
+      for (int j = 0; ok && j < n_max; ++j) {
+        // V_j and K_(j+1) are there: the helper waited for them before its arrival
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (j < n_t[t]) {
+            if (!(ok = mbar_wait_warp_cluster(&p_full[t], j & 1, abort_flag, 484))) break;
+            tc_fence_after();
+            issue_pv(t, j);
+            if (j + 1 == n_t[t]) umma_commit_pair(&o_done[t]);
+          }
+          if (j + 1 < n_t[t]) issue_s(t, j + 1);
+        }
+        if (!ok) break;
+        if (j + C::NS < n_max) umma_commit_pair(&v_empty[j % C::NS]);
+        if (j + 1 + C::NS < n_max) umma_commit_pair(&k_empty[(j + 1) % C::NS]);
+      }
+    } else if (warp == 2 && rank == 0) {
+      // -------------------------------------------------------------- arrives for P_t once V_j, K_(j+1) are there
+      bool ok = true;
+      for (int j = 0; ok && j < n_max; ++j) {
+        if (!(ok = mbar_wait_warp_cluster(&v_full[j % C::NS], (j / C::NS) & 1, abort_flag, 485))) break;
+        if (j + 1 < n_max && !(ok = mbar_wait_warp_cluster(&k_full[(j + 1) % C::NS], ((j + 1) / C::NS) & 1, abort_flag, 486))) break;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if (j < n_t[t]) {
+            // one arrival a phase: wait for the last one's end first
+            if (j > 0 && !(ok = mbar_wait_warp_cluster(&p_full[t], (j - 1) & 1, abort_flag, 487))) break;
+            if (lane == 0) mbar_arrive(&p_full[t]);
+            __syncwarp();
+          }
+      }
+    }
+  } else if (warp >= 12) {
+    // ---------------------------------------------------------------- unpacking
+    setmaxnreg_dec<C::REG_UNPACK>();
+    const int uw = warp - 12;
+    auto expand = [&](uint2 cd, uint32_t e, uint8_t* d0, uint8_t* d1, bool flip) {
+      const uint32_t s = e4m3x2_to_f16(e * 0x0101u);
+      uint32_t h[2][4];
+      e2m1x8_to_f16(flip ? cd.y : cd.x, h[0]);
+      e2m1x8_to_f16(flip ? cd.x : cd.y, h[1]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) h[k >> 2][k & 3] = hmul2(h[k >> 2][k & 3], s);
+      *reinterpret_cast<uint4*>(d0) = make_uint4(h[0][0], h[0][1], h[0][2], h[0][3]);
+      *reinterpret_cast<uint4*>(d1) = make_uint4(h[1][0], h[1][1], h[1][2], h[1][3]);
+    };
+    // K: a lane takes block lane % 8 of rows 16 apart; V: block lane % 4 of this CTA's half of rows 32 apart
+    const int kb = lane & 7, kr = uw * 4 + (lane >> 3), kf = kb >> 2;
+    const uint32_t k0 = kf * (C::HALF / 2) + sw128_offset(kr, ((kb & 3) * 2 + kf) * 8);
+    const uint32_t k1 = kf * (C::HALF / 2) + sw128_offset(kr, ((kb & 3) * 2 + (kf ^ 1)) * 8);
+    const int vb = lane & 3, vr = uw * 8 + (lane >> 2);
+    const uint32_t v0 = sw128_offset(vr, vb * 16), v1 = sw128_offset(vr, vb * 16 + 8);
+    auto done = [&](uint64_t* bar) {                          // this warp's part is written: tell the issuing CTA
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(bar, 0));
+    };
+    bool ok = true;
+    for (int j = 0; ok && j < n_max; ++j) {
+      const int s = j % C::NS, u = j / C::NS;
+      const uint8_t* st = sC + (j % C::NC) * C::CSTAGE;
+      const int kk = key0 + j * C::BN;
+      if (!(ok = mbar_wait_warp(&c_full[j % C::NC], (j / C::NC) & 1, abort_flag, 488))) break;
+      if (u > 0 && !(ok = mbar_wait_warp(&k_empty[s], (u - 1) & 1, abort_flag, 489))) break;
+      {
+        uint2 cd[4];
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cd[i] = *reinterpret_cast<const uint2*>(st + (kr + 16 * i) * C::CB + kb * 8);
+          e[i] = st[C::OFF_CKS + (kr + 16 * i) * C::SB + kb];
+        }
+        // behind the item's keys lies anything, a scale that is no number among it
+        if (kk + C::BN > key_end) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (kk + rank * 64 + kr + 16 * i >= key_end) e[i] = 0;
+        }
+        uint8_t* tile = sK + s * C::HALF;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) expand(cd[i], e[i], tile + k0 + i * 16 * 128, tile + k1 + i * 16 * 128, kf != 0);
+      }
+      done(&k_full[s]);
+      if (u > 0 && !(ok = mbar_wait_warp(&v_empty[s], (u - 1) & 1, abort_flag, 490))) break;
+      {
+        uint2 cd[4];
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cd[i] = *reinterpret_cast<const uint2*>(st + C::OFF_CV + (vr + 32 * i) * C::CB + rank * 32 + vb * 8);
+          e[i] = st[C::OFF_CVS + (vr + 32 * i) * C::SB + rank * 4 + vb];
+        }
+        if (kk + C::BN > key_end) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (kk + vr + 32 * i >= key_end) e[i] = 0;
+        }
+        uint8_t* tile = sV + s * C::HALF;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) expand(cd[i], e[i], tile + v0 + i * 32 * 128, tile + v1 + i * 32 * 128, false);
+      }
+      done(&v_full[s]);
+      if (lane == 0) mbar_arrive(&c_empty[j % C::NC]);
+    }
+  } else {
+    // ---------------------------------------------------------------- softmax, thread = row
+    setmaxnreg_inc<C::REG_SOFTMAX>();
+    const int t = (warp - 4) >> 2;
+    const int sub = warp & 3;
+    const int row = sub * 32 + lane;
+    const int r = row0 + t * 256 + rank * 128 + row;
+    const uint32_t t_lane = static_cast<uint32_t>(sub * 32) << 16;
+    const uint32_t t_s = tbase + t_lane + C::T_S + t * 128;
+    const uint32_t t_o = tbase + t_lane + C::T_O + t * 128;
+    const int n = t == 0 ? n_t[0] : n_t[1];
+    const int tok = first + r / p.G, head = hkv * p.G + r % p.G;
+    const size_t th = static_cast<size_t>(tok) * p.H + head;
+    const bool has = r < rows;
+    const float c2 = q4_query_row<D>(p, has, th, sQ + t * C::QTILE, row);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(cluster_addr(q_full, 0));
+    const uint32_t hand = cluster_addr(&p_full[t], 0);
+    const int lim = min(key_end, seen(r));
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    for (int j = 0; j < n; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;
+      tc_fence_after();
+      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l);
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(hand);
+    }
+    if (ok && n > 0) {
+      ok = mbar_wait_warp(&o_done[t], 0, abort_flag, 492);
+      tc_fence_after();
+    }
+    if (ok && row0 + t * 256 < rows) q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, split, c2, m, l);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                                             // nothing of the other CTA reaches here any more
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tbase, C::TMEM_COLS);
+  }
+}
+
+static cudaError_t launch_attend_q4_pair(Q4TParams& p, const PagedQ4Args& a, cudaStream_t stream) {
+  using C = Q4PCfg;
+  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 511) / 512);
+  static int attr_done[64] = {0};
+  cudaError_t e = ensure_smem_attr(attend_q4_pair_kernel, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = static_cast<unsigned>(2LL * a.n_seqs * a.H_kv * p.row_blocks * a.n_splits);
+  log_launch("attend_q4_pair_kernel", grid, C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
+  attend_q4_pair_kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  return cudaGetLastError();
 }
 
 template <int D>
@@ -564,9 +950,10 @@ static cudaError_t launch_attend_q4_tile_d(const PagedQ4Args& a, cudaStream_t st
   p.num_blocks = a.num_blocks; p.block_size = a.block_size; p.max_blocks = a.max_blocks;
   p.piece = a.block_size % 64 == 0 ? 64 : a.block_size % 32 == 0 ? 32 : 16;
   p.n_splits = a.n_splits; p.chunk = a.chunk;
-  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 2 * C::BM - 1) / (2 * C::BM));
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
+  if (D == 128 && q4_rows(a.H, a.H_kv, a.max_seqlen_q) > kQ4TileRows) return launch_attend_q4_pair(p, a, stream);
+  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 2 * C::BM - 1) / (2 * C::BM));
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_tile_kernel<D>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
