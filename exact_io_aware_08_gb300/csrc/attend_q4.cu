@@ -698,44 +698,6 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
   __syncthreads();
 }
 
-// Writes a row's result from its chunks' states, which ``state(i)`` gives for i < n: one warp.
-template <int D, typename F>
-__device__ __forceinline__ void q4_join(F state, int n, uint16_t* o, float* lse, float descale_v) {
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const float* st = state(i);
-    if (st) M = fmaxf(M, st[D]);
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  constexpr int V = D / 32;
-  float acc[V], L = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* st = state(i);
-    if (!st) continue;
-    const float2 s = *reinterpret_cast<const float2*>(st + D);
-    if (s.x == -INFINITY) continue;                            // no keys: weight 0
-    const float wt = fast_exp2(s.x - M);
-    L = fmaf(wt, s.y, L);
-#pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      const float2 v = *reinterpret_cast<const float2*>(st + 64 * k + 2 * lane);
-      acc[2 * k] = fmaf(wt, v.x, acc[2 * k]);
-      acc[2 * k + 1] = fmaf(wt, v.y, acc[2 * k + 1]);
-    }
-  }
-  const bool none = M == -INFINITY;
-  const float inv = none ? 0.f : descale_v / L;
-#pragma unroll
-  for (int k = 0; k < V / 2; ++k)
-    *reinterpret_cast<uint32_t*>(o + 64 * k + 2 * lane) = none ? 0u : pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if (lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-}
-
 // Joins a row's chunks where the caller gave their count (part: [row][chunk]): one warp a row.
 template <int D>
 __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ o,
@@ -791,22 +753,6 @@ static int q4_sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
   if (dev < 64) cached[dev] = n;
   return n;
-}
-
-// The join runs behind the chunks on the stream, but may start while their last CTAs run
-// (programmatic dependent launch): it reads lengths and boundaries, then waits for the states.
-template <typename... P, typename... A>
-static cudaError_t launch_join(void (*kernel)(P...), unsigned blocks, cudaStream_t stream, A... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 static unsigned join_blocks(const PagedQ4Args& a) {

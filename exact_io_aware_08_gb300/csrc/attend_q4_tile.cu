@@ -68,13 +68,48 @@ struct Q4TParams {
   float *lse, *part;
   const int *cu_q, *seqlens, *table;
   int n_seqs, H, H_kv, G, total_q, max_q, max_k, causal, num_blocks, block_size, max_blocks, piece;
-  int n_splits, chunk, row_blocks;
+  int n_splits, chunk, row_blocks;                            // n_splits 0: the items from ``whole`` on in
+  int whole, tail_splits, block_rows;                         // tail_splits parts; rows of an item
   float score, descale_v;
 };
 
 // fp16 A and B, fp32 accumulator
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int a_mn, int b_mn) {
   return idesc_bf16_f32(M, N, a_mn, b_mn) & ~((1u << 7) | (1u << 10));
+}
+
+// Item of a CTA (or pair) by its index: row blocks with the most keys first over all sequences and
+// heads, then the next.  ``parts``: chunks of the item's keys; ``state``: place of its first row's state.
+struct Q4TItem {
+  int b, hkv, rb, split, parts, chunk;
+  size_t state;
+};
+
+__device__ __forceinline__ Q4TItem q4_tile_item(const Q4TParams& p, int index) {
+  Q4TItem x;
+  int item = index;
+  x.split = 0;
+  x.parts = 1;
+  x.chunk = p.chunk;
+  x.state = 0;
+  if (p.n_splits) {
+    x.parts = p.n_splits;
+    item = index / p.n_splits;
+    x.split = index - item * p.n_splits;
+  } else if (index >= p.whole) {
+    const int q = index - p.whole;
+    x.parts = p.tail_splits;
+    item = p.whole + q / p.tail_splits;
+    x.split = q % p.tail_splits;
+    x.state = static_cast<size_t>(q) * p.block_rows;
+  }
+  if (x.parts == 1) x.chunk = 1 << 30;                        // (all keys)
+  const int per_rb = p.n_seqs * p.H_kv;
+  x.rb = p.row_blocks - 1 - item / per_rb;
+  const int w = item % per_rb;
+  x.hkv = w % p.H_kv;
+  x.b = w / p.H_kv;
+  return x;
 }
 
 // Brings query row ``th`` (none: zeros) as row ``row`` of the tile, in fp16, and returns its score factor.
@@ -212,11 +247,12 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
 
 // The row's result, or its chunk's state: O of columns t_o over l (``any``: some key tile was run).
 template <int D>
-__device__ __forceinline__ void q4_store_row(const Q4TParams& p, uint32_t t_o, bool any, bool has, size_t th, int tok, int head, int split,
-                                             float c2, float m, float l) {
+__device__ __forceinline__ void q4_store_row(const Q4TParams& p, uint32_t t_o, bool any, bool has, size_t th, int tok, int head, const Q4TItem& item,
+                                             int row, float c2, float m, float l) {
   const bool none = l == 0.f;                             // a row that sees no key (of the chunk)
   const float inv = none ? 0.f : p.descale_v / l;
-  float* dst = p.n_splits > 1 ? p.part + (th * p.n_splits + split) * (D + 2) : nullptr;
+  float* dst = nullptr;                                   // the chunk's state: [row][chunk], or [part][row of the block]
+  if (item.parts > 1) dst = p.part + (p.n_splits ? th * p.n_splits + item.split : item.state + row) * (D + 2);
 #pragma unroll
   for (int k = 0; k < D / 32; ++k) {
     uint32_t rr[32];
@@ -276,14 +312,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  // Item: row blocks with the most keys first over all sequences and heads, then the next.
-  const int per_rb = p.n_seqs * p.H_kv * p.n_splits;
-  const int rb = p.row_blocks - 1 - static_cast<int>(blockIdx.x) / per_rb;
-  int w = static_cast<int>(blockIdx.x) % per_rb;
-  const int split = w % p.n_splits;
-  w /= p.n_splits;
-  const int hkv = w % p.H_kv;
-  const int b = w / p.H_kv;
+  const Q4TItem item = q4_tile_item(p, blockIdx.x);
+  const int rb = item.rb, hkv = item.hkv, b = item.b;
   int first = b, nq = 1;
   if (p.cu_q) {
     first = __ldg(p.cu_q + b);
@@ -305,15 +335,15 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
   // Row r of the sequence sees its first seen(r) keys; the item's keys are [key0, key_end), tile t
   // runs n_t[t] key tiles of 128.
   auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
-  const int key0 = split * p.chunk;
+  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
   int n_t[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int last = min(key0 + p.chunk, seen(row0 + (t + 1) * C::BM - 1));
+    const int last = min(key0 + item.chunk, seen(row0 + (t + 1) * C::BM - 1));
     n_t[t] = (row0 + t * C::BM >= rows || last <= key0) ? 0 : (last - key0 + C::BN - 1) / C::BN;
   }
   const int n_max = max(n_t[0], n_t[1]);
-  const int key_end = min(key0 + p.chunk, seen(rows - 1 < row0 + 2 * C::BM - 1 ? rows - 1 : row0 + 2 * C::BM - 1));
+  const int key_end = min(key0 + item.chunk, seen(rows - 1 < row0 + 2 * C::BM - 1 ? rows - 1 : row0 + 2 * C::BM - 1));
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 256);
@@ -335,6 +365,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+  pdl_launch_dependents();
   __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
@@ -557,7 +588,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       tc_fence_after();
     }
     if (ok && row0 + t * C::BM < rows) {
-      q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, split, c2, m, l);
+      q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, item, r - row0, c2, m, l);
     }
   }
   __syncwarp();
@@ -636,15 +667,8 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   const int lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank());
 
-  // Item, as in the kernel above, of 512 rows.
-  const int pair = static_cast<int>(blockIdx.x) >> 1;
-  const int per_rb = p.n_seqs * p.H_kv * p.n_splits;
-  const int rb = p.row_blocks - 1 - pair / per_rb;
-  int w = pair % per_rb;
-  const int split = w % p.n_splits;
-  w /= p.n_splits;
-  const int hkv = w % p.H_kv;
-  const int b = w / p.H_kv;
+  const Q4TItem item = q4_tile_item(p, blockIdx.x >> 1);      // of 512 rows
+  const int rb = item.rb, hkv = item.hkv, b = item.b;
   int first = b, nq = 1;
   if (p.cu_q) {
     first = __ldg(p.cu_q + b);
@@ -664,15 +688,15 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   const int row0 = rb * 512;
   if (row0 >= rows) return;                                   // both CTAs, before any shared state
   auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
-  const int key0 = split * p.chunk;
+  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
   int n_t[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int last = min(key0 + p.chunk, seen(row0 + t * 256 + 255));
+    const int last = min(key0 + item.chunk, seen(row0 + t * 256 + 255));
     n_t[t] = (row0 + t * 256 >= rows || last <= key0) ? 0 : (last - key0 + C::BN - 1) / C::BN;
   }
   const int n_max = max(n_t[0], n_t[1]);
-  const int key_end = min(key0 + p.chunk, seen(row0 + 511));
+  const int key_end = min(key0 + item.chunk, seen(row0 + 511));
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 16);                                    // softmax warps of both CTAs
@@ -695,6 +719,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     fence_mbarrier_init();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+  pdl_launch_dependents();
   __syncthreads();
   cluster_sync();                                             // barriers and tensor memory of both are there
   tc_fence_after();
@@ -913,7 +938,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
       ok = mbar_wait_warp(&o_done[t], 0, abort_flag, 492);
       tc_fence_after();
     }
-    if (ok && row0 + t * 256 < rows) q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, split, c2, m, l);
+    if (ok && row0 + t * 256 < rows) q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, item, r - row0, c2, m, l);
   }
   __syncwarp();
   tc_fence_before();
@@ -925,16 +950,68 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   }
 }
 
+// Joins the parts of the items from ``whole`` on: one warp a row.
+template <int D>
+__global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_constant__ Q4TParams p, int n_rows) {
+  pdl_wait();
+  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (i >= n_rows) return;
+  const int n = i / p.block_rows, row = i - n * p.block_rows;
+  const Q4TItem x = q4_tile_item(p, p.whole + n * p.tail_splits);
+  int first = x.b, nq = 1;
+  if (p.cu_q) {
+    first = __ldg(p.cu_q + x.b);
+    const int end = __ldg(p.cu_q + x.b + 1);
+    nq = end - first;
+    if (first < 0 || end < first || end > p.total_q || nq > p.max_q) return;   // reported
+  }
+  const int r = x.rb * p.block_rows + row;
+  if (r >= nq * p.G) return;
+  const int tok = first + r / p.G, head = x.hkv * p.G + r % p.G;
+  const size_t th = static_cast<size_t>(tok) * p.H + head;
+  q4_join<D>([&](int k) { return p.part + (x.state + static_cast<size_t>(k) * p.block_rows + row) * (D + 2); }, p.tail_splits,
+             p.o + th * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th), p.descale_v);
+}
+
+// Shares the items out to ``places`` (SMs, or pairs of them) at a time: all that fill them a whole
+// number of times run whole, what is left over is split so that it fills them once more, in parts of
+// at least 512 keys (4x1024 tokens over 16384 keys, 256 items on 76 pairs: 1010 us whole, 957 us
+// with the last 28 in two parts).  Returns the grid.
+static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int block_rows) {
+  p.block_rows = block_rows;
+  p.row_blocks = static_cast<int>((q4_rows(a.H, a.H_kv, a.max_seqlen_q) + block_rows - 1) / block_rows);
+  const long long items = static_cast<long long>(a.n_seqs) * a.H_kv * p.row_blocks;
+  p.whole = static_cast<int>(items);
+  p.tail_splits = 1;
+  if (a.n_splits) return items * a.n_splits;
+  const int tail = static_cast<int>(items % places);
+  const int s = tail ? min(places / tail, a.max_seqlen_k / 512) : 1;
+  if (s < 2) return items;
+  p.whole = static_cast<int>(items - tail);
+  p.tail_splits = s;
+  p.chunk = q4_chunk(a.max_seqlen_k, s);
+  return p.whole + static_cast<long long>(tail) * s;
+}
+
+template <int D>
+static cudaError_t launch_tail(const Q4TParams& p, long long grid, cudaStream_t stream) {
+  if (p.tail_splits == 1) return cudaSuccess;
+  const int rows = static_cast<int>((grid - p.whole) / p.tail_splits) * p.block_rows;
+  log_launch("attend_q4_tail_kernel<D>", rows / 4, 128, 0ull);
+  return launch_join(attend_q4_tail_kernel<D>, rows / 4, stream, p, rows);
+}
+
 static cudaError_t launch_attend_q4_pair(Q4TParams& p, const PagedQ4Args& a, cudaStream_t stream) {
   using C = Q4PCfg;
-  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 511) / 512);
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_pair_kernel, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(2LL * a.n_seqs * a.H_kv * p.row_blocks * a.n_splits);
+  const long long pairs = share_tiles(p, a, kQ4MaxTailRows / (2 * kQ4TileRows), 2 * kQ4TileRows);
+  const unsigned grid = static_cast<unsigned>(2 * pairs);
   log_launch("attend_q4_pair_kernel", grid, C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_pair_kernel<<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_tail<C::D>(p, pairs, stream) : e;
 }
 
 template <int D>
@@ -953,14 +1030,14 @@ static cudaError_t launch_attend_q4_tile_d(const PagedQ4Args& a, cudaStream_t st
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
   if (D == 128 && q4_rows(a.H, a.H_kv, a.max_seqlen_q) > kQ4TileRows) return launch_attend_q4_pair(p, a, stream);
-  p.row_blocks = static_cast<int>((static_cast<long long>(p.G) * a.max_seqlen_q + 2 * C::BM - 1) / (2 * C::BM));
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_tile_kernel<D>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
-  const unsigned grid = static_cast<unsigned>(static_cast<long long>(a.n_seqs) * a.H_kv * p.row_blocks * a.n_splits);
+  const long long grid = share_tiles(p, a, kQ4MaxTailRows / kQ4TileRows, kQ4TileRows);
   log_launch("attend_q4_tile_kernel<D>", grid, C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
-  attend_q4_tile_kernel<D><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
-  return cudaGetLastError();
+  attend_q4_tile_kernel<D><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(p);
+  e = cudaGetLastError();
+  return e == cudaSuccess ? launch_tail<D>(p, grid, stream) : e;
 }
 
 cudaError_t launch_attend_q4_tile(const PagedQ4Args& a, cudaStream_t stream) {

@@ -251,21 +251,14 @@ inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q) {
   const int per = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4TileRows : kQ4Rows;
   return static_cast<long long>(n_seqs) * H_kv * ((q4_rows(H, H_kv, max_seqlen_q) + per - 1) / per);
 }
-// Few rows without a split count: at most this many CTAs share the work, and each keeps at most two
-// states of kQ4Rows rows.
+// Without a split count (0): few rows are shared out to at most this many teams, and each keeps at most
+// two states of kQ4Rows rows; of tiles, the row blocks that do not fill all SMs once more are split,
+// into at most as many parts as there are SMs, each with a state a row.
 constexpr int kQ4MaxShares = 4 * 152;
-inline size_t q4_share_bytes(int d) { return static_cast<size_t>(kQ4MaxShares) * 2 * kQ4Rows * (d + 2) * sizeof(float); }
-// Split count when the caller leaves it open.  Few rows: 0, shares of equal length.  Tiles: one CTA on
-// every SM, of at least 512 keys.
-inline int q4_auto_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int n_kv) {
-  if (!q4_use_tiles(H, H_kv, max_seqlen_q)) return 0;
-  const long long items = q4_items(n_seqs, H, H_kv, max_seqlen_q);
-  long long s = items < 1 ? 1 : 152 / items;
-  const long long max_by_len = (static_cast<long long>(n_kv) + 511) / 512;
-  if (s > max_by_len) s = max_by_len;
-  if (s < 1) s = 1;
-  if (s > kDecodeMaxSplits) s = kDecodeMaxSplits;
-  return static_cast<int>(s);
+constexpr int kQ4MaxTailRows = 152 * kQ4TileRows;
+inline size_t q4_auto_bytes(int H, int H_kv, int max_seqlen_q, int d) {
+  const size_t rows = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4MaxTailRows : 2 * kQ4MaxShares * kQ4Rows;
+  return rows * (d + 2) * sizeof(float);
 }
 // Keys of a step, and of a chunk: whole steps.
 constexpr int kQ4Step = 128;

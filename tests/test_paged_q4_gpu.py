@@ -282,6 +282,8 @@ FORWARDS = [
     ([129, 260], [129, 1000], 5, 1, 128, 32, True, 2, 5), ([150], [450], 12, 12, 128, 256, False, 1, 0),
     ([256], [256], 4, 4, 128, 128, True, 1, 0), ([300, 20], [900, 20], 10, 2, 64, 64, True, 1, 0),
     ([1, 600], [3, 600], 4, 1, 128, 16, True, 0, 1), ([520], [1500], 8, 1, 64, 48, True, 5, 0),
+    # row blocks that are split because they do not fill the SMs
+    ([300], [2500], 4, 1, 128, 64, True, 0, 1), ([200, 90], [2200, 1100], 4, 2, 64, 32, True, 0, 2), ([70, 0, 3], [3100, 40, 1030], 4, 2, 128, 48, False, 0, 0),
 ]
 
 
