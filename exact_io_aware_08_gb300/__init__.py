@@ -324,130 +324,29 @@ def fa_decode_paged(q, k_cache, v_cache, o, lse, block_table, seqlens_k, max_seq
                                           _ptr(ws), ws_bytes, _stream(stream)))
 
 
-# The paged-cache calls look their tensors over before they pass pointers on: one device, the types
-# and shapes of include/fa.h, dense (the packed q, k, v of an append may be slices of a wider matrix).
-# Small calls are bound by this side, so a tensor is checked with as few calls into torch as will do,
-# and what is wrong with it is worked out only when something is.
+# The paged-cache calls (a serving step's) look their tensors over and marshal them in a small extension
+# module, csrc/binding.cpp: short steps are bound by the host.
 
-class _Torch:
-    """torch's names that every call needs, looked up once."""
-
-    def __init__(self):
-        import torch
-        self.empty, self.empty_like = torch.empty, torch.empty_like
-        self.bf16, self.i32, self.u8 = torch.bfloat16, torch.int32, torch.uint8
-        self.e4m3, self.f32 = torch.float8_e4m3fn, torch.float32
-        self.device, self.current_device = torch.cuda.device, torch.cuda.current_device
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
+_native = None
 
 
-_names = None
-
-
-def _torch():
-    global _names
-    if _names is None:
-        _names = _Torch()
-    return _names
-
-
-def _bad(message):
-    raise FaError(1, message)
-
-
-def _explain(name, t, dtype, shape, device, dense):
-    import torch
-    if not isinstance(t, torch.Tensor):
-        _bad(f"{name} must be a tensor, is {type(t).__name__}")
-    if not t.is_cuda or t.get_device() != device:
-        _bad(f"{name} must be a CUDA tensor on the cache's device, is on {t.device}")
-    if t.dtype != dtype:
-        _bad(f"{name} must be {dtype}, is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        _bad(f"{name} must be {list(shape)}, is {list(t.shape)}")
-    _bad(f"{name} must be dense{dense}")
-
-
-def _tensor(name, t, dtype, shape, device):
-    """The address of a dense tensor of this type, shape and device."""
-    if (t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
-        _explain(name, t, dtype, shape, device, "")
-    return t.data_ptr()
-
-
-def _tokens(name, t, dtype, shape, device):
-    """(address, token stride) of packed tokens whose heads are dense."""
-    if t.get_device() != device or device < 0 or t.dtype is not dtype or t.shape != shape:
-        _explain(name, t, dtype, shape, device, "")
-    s0, s1, s2 = t.stride()
-    if (s2 != 1 or (s1 != shape[2] and shape[1] > 1)) and t.numel():
-        _explain(name, t, dtype, shape, device, " in its last two dimensions")
-    return t.data_ptr(), s0
-
-
-def _launch(device, stream, fn, *args):
-    """Calls ``fn`` with the stream as its last argument and ``device`` the current one."""
-    T = _torch()
-    if stream is None:
-        stream = T.raw_stream(device)
-    else:
-        stream = getattr(stream, "cuda_stream", stream)
-    if device == T.current_device():
-        status = fn(*args, stream)
-    else:
-        with T.device(device):
-            status = fn(*args, stream)
-    if status:
-        _check(status)
-
-
-def _q4_cache(T, k_codes, k_scales, v_codes, v_scales):
-    """Checks a 4-bit cache; (device, addresses, num_blocks, H_kv, block_size, d)."""
-    if k_codes.dim() != 4:
-        _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
-    device, shape = k_codes.get_device(), k_codes.shape
-    nb, H_kv, bs, half = shape
-    scales = (nb, H_kv, bs, half // 8)
-    e4m3 = T.u8 if k_scales.dtype is T.u8 else T.e4m3
-    return (device, _tensor("k_codes", k_codes, T.u8, shape, device), _tensor("k_scales", k_scales, e4m3, scales, device),
-            _tensor("v_codes", v_codes, T.u8, shape, device), _tensor("v_scales", v_scales, e4m3, scales, device),
-            nb, H_kv, bs, 2 * half)
-
-
-def _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device):
-    """Checks what both appends share: (pointers before the cache's, after it, sizes, strides, blocks a sequence,
-    rotary_dim, n_positions)."""
-    if k.dim() != 3 or block_table.dim() != 2:
-        _bad("k must be [total, H_kv, d] and block_table [n_seqs, max_blocks]")
-    total = k.shape[0]
-    n_seqs, max_blocks = block_table.shape
-    shape = (total, H_kv, d)
-    pk, sk = _tokens("k", k, T.bf16, shape, device)
-    pv, sv = _tokens("v", v, T.bf16, shape, device)
-    H, pq, po, sq = 0, None, None, 0
-    if (q is None) != (q_out is None):
-        _bad("q and q_out go together")
-    if q is not None:
-        if q.dim() != 3:
-            _bad(f"q must be [total, H, d], is {list(q.shape)}")
-        H = q.shape[1]
-        shape = (total, H, d)
-        pq, sq = _tokens("q", q, T.bf16, shape, device)
-        po = _tensor("q_out", q_out, T.bf16, shape, device)
-    if (cos is None) != (sin is None):
-        _bad("cos and sin go together")
-    rotary, n_positions, pc, ps = 0, 0, None, None
-    if cos is not None:
-        if cos.dim() != 2:
-            _bad(f"cos must be [n_positions, rotary_dim/2], is {list(cos.shape)}")
-        shape = cos.shape
-        n_positions, rotary = shape
-        pc, ps = _tensor("cos", cos, T.f32, shape, device), _tensor("sin", sin, T.f32, shape, device)
-    return ((pq, pk, pv, po),
-            (pc, ps, _tensor("cu_seqlens", cu_seqlens, T.i32, (n_seqs + 1,), device),
-             _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
-             _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device),
-             n_seqs, H, H_kv, total, sq, sk, sv, max_blocks), 2 * rotary, n_positions)
+def _binding():
+    """The extension module, bound to the loaded library (raises FaError if it has not been built)."""
+    global _native
+    if _native is None:
+        import importlib.machinery
+        import importlib.util
+        import torch  # noqa: F401  (the module needs its libraries)
+        lib = load_library()
+        path = os.path.join(_HERE, "_binding.so")
+        if not os.path.exists(path):
+            raise FaError(4, f"{path} not found: build it with `python -m exact_io_aware_08_gb300.build`")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
+        loader.exec_module(module)
+        module.bind(FaError, lib._handle)
+        _native = module
+    return _native
 
 
 def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seqlens_k, block_table,
@@ -455,79 +354,48 @@ def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seql
     """q, q_out [total, H, d] or None; k, v [total, H_kv, d]; k/v cache [num_blocks, block_size, H_kv, d];
     cos, sin fp32 [n_positions, rotary_dim/2] or None; cu_seqlens [n_seqs + 1], seqlens_k [n_seqs] and
     block_table [n_seqs, max_blocks] int32, all on the device."""
-    T = _torch()
-    device = k_cache.get_device()
-    if k_cache.dim() != 4:
-        _bad(f"k_cache must be [num_blocks, block_size, H_kv, d], is {list(k_cache.shape)}")
-    shape = k_cache.shape
-    nb, bs, H_kv, d = shape
-    pkc, pvc = _tensor("k_cache", k_cache, T.bf16, shape, device), _tensor("v_cache", v_cache, T.bf16, shape, device)
-    head, tail, rotary, n_positions = _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device)
-    _launch(device, stream, (_lib or load_library()).fa_append_paged, *head, pkc, pvc, *tail, bs, nb, d, rotary,
-            1 if interleaved else 0, n_positions)
+    if q is not None and q_out is None:
+        raise FaError(1, "q and q_out go together")
+    (_native or _binding()).append(q, k, v, q_out, k_cache, None, v_cache, None, cos, sin, cu_seqlens, seqlens_k, block_table,
+                                   1.0, 1.0, interleaved, stream)
 
 
 def fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
                        block_table, descale_k: float, descale_v: float, interleaved: bool = False, stream=None):
     """As fa_append_paged, with codes uint8 [num_blocks, H_kv, block_size, d/2] and scales (both uint8 or
     both float8_e4m3fn) [num_blocks, H_kv, block_size, d/16]."""
-    T = _torch()
-    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
-    head, tail, rotary, n_positions = _step(T, q, k, v, q_out, cos, sin, cu_seqlens, seqlens_k, block_table, H_kv, d, device)
-    _launch(device, stream, (_lib or load_library()).fa_append_paged_q4, *head, kc, ks, vc, vs, *tail, bs, nb, d, rotary,
-            1 if interleaved else 0, n_positions, descale_k, descale_v)
+    if q is not None and q_out is None:
+        raise FaError(1, "q and q_out go together")
+    if k_scales is None:
+        raise FaError(1, "k_scales must be a tensor")
+    (_native or _binding()).append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
+                                   block_table, descale_k, descale_v, interleaved, stream)
 
 
 def fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table,
                        descale_k: float, descale_v: float, stream=None):
     """k, v [total, H_kv, d] bf16 are written."""
-    T = _torch()
-    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
-    if k.dim() != 3 or block_table.dim() != 2:
-        _bad("k must be [total, H_kv, d] and block_table [n_seqs, max_blocks]")
-    shape = (k.shape[0], H_kv, d)
-    n_seqs, max_blocks = block_table.shape
-    _launch(device, stream, (_lib or load_library()).fa_gather_paged_q4, kc, ks, vc, vs, _tensor("k", k, T.bf16, shape, device),
-            _tensor("v", v, T.bf16, shape, device), _tensor("cu_seqlens", cu_seqlens, T.i32, (n_seqs + 1,), device),
-            _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
-            _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device), n_seqs, H_kv, shape[0], max_blocks,
-            bs, nb, d, descale_k, descale_v)
+    if k is None or v is None:
+        raise FaError(1, "k and v must be tensors")
+    (_native or _binding()).gather(k_codes, k_scales, v_codes, v_scales, k, v, None, cu_seqlens, seqlens_k, block_table,
+                                   descale_k, descale_v, stream)
 
 
 def fa_decode_paged_q4_workspace_size(B: int, H: int, H_kv: int, max_seqlen_k: int, d: int, n_splits: int) -> int:
-    return (_lib or load_library()).fa_decode_paged_q4_workspace_size(B, H, H_kv, max_seqlen_k, d, n_splits)
+    return load_library().fa_decode_paged_q4_workspace_size(B, H, H_kv, max_seqlen_k, d, n_splits)
 
 
 def fa_fwd_paged_q4_workspace_size(n_seqs: int, H: int, H_kv: int, total_q: int, max_seqlen_q: int, max_seqlen_k: int,
                                    d: int, n_splits: int) -> int:
-    return (_lib or load_library()).fa_fwd_paged_q4_workspace_size(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d, n_splits)
-
-
-def _scratch(ws, device):
-    """(address, bytes) of a workspace."""
-    if ws is None:
-        return None, 0
-    if ws.get_device() != device or not ws.is_contiguous():
-        _bad("the workspace must be dense and on the cache's device")
-    return ws.data_ptr(), ws.nbytes
+    return load_library().fa_fwd_paged_q4_workspace_size(n_seqs, H, H_kv, total_q, max_seqlen_q, max_seqlen_k, d, n_splits)
 
 
 def fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k: int,
                        scale: float, descale_k: float, descale_v: float, n_splits: int, ws, stream=None):
     """q, o [B,H,1,d]; lse [B,H,1]; a 4-bit cache as fa_append_paged_q4 writes it; block_table
     [B, max_blocks] int32; seqlens_k [B] int32.  H_kv (of the cache) divides H."""
-    T = _torch()
-    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
-    if q.dim() != 4 or block_table.dim() != 2:
-        _bad("q must be [B, H, 1, d] and block_table [B, max_blocks]")
-    B, H = q.shape[:2]
-    shape, max_blocks = (B, H, 1, d), block_table.shape[1]
-    pw, nw = _scratch(ws, device)
-    _launch(device, stream, (_lib or load_library()).fa_decode_paged_q4, _tensor("q", q, T.bf16, shape, device), kc, ks, vc, vs,
-            _tensor("o", o, T.bf16, shape, device), _tensor("lse", lse, T.f32, (B, H, 1), device),
-            _tensor("block_table", block_table, T.i32, (B, max_blocks), device),
-            _tensor("seqlens_k", seqlens_k, T.i32, (B,), device), B, H, H_kv, max_blocks, bs, nb, max_seqlen_k, d, scale,
-            descale_k, descale_v, n_splits, pw, nw)
+    (_native or _binding()).decode(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k,
+                                   scale, descale_k, descale_v, n_splits, ws, stream, False)
 
 
 def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table,
@@ -535,20 +403,9 @@ def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_
                     n_splits: int, ws, stream=None):
     """q, o [total_q, H, d]; lse [H, total_q]; cu_seqlens_q [n_seqs + 1] int32; the rest as for
     fa_decode_paged_q4."""
-    T = _torch()
-    device, kc, ks, vc, vs, nb, H_kv, bs, d = _q4_cache(T, k_codes, k_scales, v_codes, v_scales)
-    if q.dim() != 3 or block_table.dim() != 2:
-        _bad("q must be [total_q, H, d] and block_table [n_seqs, max_blocks]")
-    total_q, H = q.shape[:2]
-    shape = (total_q, H, d)
-    n_seqs, max_blocks = block_table.shape
-    pw, nw = _scratch(ws, device)
-    _launch(device, stream, (_lib or load_library()).fa_fwd_paged_q4, _tensor("q", q, T.bf16, shape, device), kc, ks, vc, vs,
-            _tensor("o", o, T.bf16, shape, device), _tensor("lse", lse, T.f32, (H, total_q), device),
-            _tensor("cu_seqlens_q", cu_seqlens_q, T.i32, (n_seqs + 1,), device),
-            _tensor("seqlens_k", seqlens_k, T.i32, (n_seqs,), device),
-            _tensor("block_table", block_table, T.i32, (n_seqs, max_blocks), device), n_seqs, H, H_kv, total_q, max_seqlen_q,
-            max_blocks, bs, nb, max_seqlen_k, d, scale, descale_k, descale_v, 1 if causal else 0, n_splits, pw, nw)
+    (_native or _binding()).forward(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table,
+                                    max_seqlen_q, max_seqlen_k, scale, descale_k, descale_v, causal, n_splits, ws, stream,
+                                    False)
 
 
 def fa_debug_counters(counters):
@@ -708,67 +565,38 @@ def rotary_tables(n_positions: int, rotary_dim: int, base: float = 10000.0, devi
     return angle.cos().float(), angle.sin().float()
 
 
-def _rotated(q, k, q_out):
-    return _torch().empty(q.shape, dtype=q.dtype, device=k.device) if q is not None and q_out is None else q_out
-
-
 def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, q=None, cos=None, sin=None,
                  interleaved: bool = False, q_out=None, stream=None):
     """Rotates a step's packed keys by their positions, puts keys and values into the bf16 paged cache
     that decode_paged reads, and returns the rotated queries (None without q)."""
-    q_out = _rotated(q, k, q_out)
-    fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seqlens_k, block_table, interleaved, stream)
-    return q_out
+    return (_native or _binding()).append(q, k, v, q_out, k_cache, None, v_cache, None, cos, sin, cu_seqlens, seqlens_k,
+                                          block_table, 1.0, 1.0, interleaved, stream)
 
 
 def append_paged_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, q=None, cos=None,
                     sin=None, descale_k: float = 1.0, descale_v: float = 1.0, interleaved: bool = False, q_out=None,
                     stream=None):
     """append_paged into a 4-bit cache (see fa_append_paged_q4)."""
-    q_out = _rotated(q, k, q_out)
-    fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k, block_table,
-                       descale_k, descale_v, interleaved, stream)
-    return q_out
+    if k_scales is None:
+        raise FaError(1, "k_scales must be a tensor")
+    return (_native or _binding()).append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens,
+                                          seqlens_k, block_table, descale_k, descale_v, interleaved, stream)
 
 
 def gather_paged_q4(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, total: int,
                     descale_k: float = 1.0, descale_v: float = 1.0, stream=None):
     """The last cu_seqlens[b+1] - cu_seqlens[b] tokens of each sequence of a 4-bit cache as packed bf16
     (k, v [total, H_kv, d])."""
-    if k_codes.dim() != 4:
-        _bad(f"k_codes must be [num_blocks, H_kv, block_size, d/2], is {list(k_codes.shape)}")
-    T = _torch()
-    _, H_kv, _, half = k_codes.shape
-    k = T.empty((total, H_kv, 2 * half), dtype=T.bf16, device=k_codes.device)
-    v = T.empty_like(k)
-    fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table, descale_k,
-                       descale_v, stream)
-    return k, v
-
-
-def _q4_workspace(T, workspace, need, device):
-    """The caller's workspace where it is large enough; none where the call needs none."""
-    if workspace is not None and workspace.device != device:
-        _bad("the workspace must be on the queries' device")
-    if need > 16 and (workspace is None or workspace.nbytes < need):
-        return T.empty(need, dtype=T.u8, device=device)
-    return workspace
+    return (_native or _binding()).gather(k_codes, k_scales, v_codes, v_scales, None, None, total, cu_seqlens, seqlens_k,
+                                          block_table, descale_k, descale_v, stream)
 
 
 def decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, seqlens_k, max_seqlen_k: int,
                     n_splits: int = 0, scale: float | None = None, descale_k: float = 1.0, descale_v: float = 1.0,
                     stream=None, workspace=None):
     """Single-query decode over a 4-bit paged cache, grouped heads -> (O [B,H,1,d], lse [B,H,1])."""
-    T = _torch()
-    B, H, _, d = q.shape
-    device = q.device
-    need = (_lib or load_library()).fa_decode_paged_q4_workspace_size(B, H, k_codes.shape[1], max_seqlen_k, d, n_splits)
-    workspace = _q4_workspace(T, workspace, need, device)
-    o = T.empty_like(q)
-    lse = T.empty((B, H, 1), dtype=T.f32, device=device)
-    fa_decode_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, block_table, seqlens_k, max_seqlen_k,
-                       d ** -0.5 if scale is None else scale, descale_k, descale_v, n_splits, workspace, stream)
-    return o, lse
+    return (_native or _binding()).decode(q, k_codes, k_scales, v_codes, v_scales, None, None, block_table, seqlens_k,
+                                          max_seqlen_k, scale, descale_k, descale_v, n_splits, workspace, stream, True)
 
 
 def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens_q, seqlens_k, max_seqlen_q: int,
@@ -776,15 +604,6 @@ def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
                      descale_k: float = 1.0, descale_v: float = 1.0, stream=None, workspace=None):
     """Packed queries [total_q, H, d] over a 4-bit paged cache, causal up to each one's own token
     -> (O [total_q, H, d], lse [H, total_q])."""
-    T = _torch()
-    total_q, H, d = q.shape
-    device = q.device
-    need = (_lib or load_library()).fa_fwd_paged_q4_workspace_size(block_table.shape[0], H, k_codes.shape[1], total_q, max_seqlen_q,
-                                                         max_seqlen_k, d, n_splits)
-    workspace = _q4_workspace(T, workspace, need, device)
-    o = T.empty_like(q)
-    lse = T.empty((H, total_q), dtype=T.f32, device=device)
-    fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table, max_seqlen_q,
-                    max_seqlen_k, d ** -0.5 if scale is None else scale, descale_k, descale_v, causal, n_splits, workspace,
-                    stream)
-    return o, lse
+    return (_native or _binding()).forward(q, k_codes, k_scales, v_codes, v_scales, None, None, cu_seqlens_q, seqlens_k,
+                                           block_table, max_seqlen_q, max_seqlen_k, scale, descale_k, descale_v, causal,
+                                           n_splits, workspace, stream, True)

@@ -1,8 +1,9 @@
-"""Build libfa.so in-tree from csrc/*.cu for sm_103a.
+"""Build libfa.so in-tree from csrc/*.cu for sm_103a, and _binding.so from csrc/binding.cpp.
 
 Each translation unit is compiled in parallel with nvcc, then linked into
-``exact_io_aware_08_gb300/libfa.so`` (git-ignored).  Rebuilds only when a source or header is
-newer than the library.  Usage: ``python -m exact_io_aware_08_gb300.build [--force] [-v]``.
+``exact_io_aware_08_gb300/libfa.so`` (git-ignored); the extension module is compiled beside them with
+g++ against the installed torch's headers.  Rebuilds only when a source or header is newer than what
+it makes.  Usage: ``python -m exact_io_aware_08_gb300.build [--force] [-v]``.
 """
 from __future__ import annotations
 
@@ -18,6 +19,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
+BINDING = os.path.join(HERE, "_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
@@ -40,15 +43,41 @@ def _deps():
             + [os.path.join(ROOT, "include", "fa.h"), os.path.abspath(__file__)])
 
 
+def _newer(made, deps) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(p) <= os.path.getmtime(made) for p in deps)
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
-        return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    return _newer(LIB, _deps())
+
+
+def binding_up_to_date() -> bool:
+    return _newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.abspath(__file__)])
+
+
+def build_binding() -> str:
+    """Compile the extension module."""
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
+    lib = os.path.join(home, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-o", tmp, BINDING_SOURCE,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in include), "-L" + lib,
+           "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+    if not force and up_to_date() and binding_up_to_date():
         return LIB
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -64,8 +93,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        objs = list(ex.map(compile_one, srcs))
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = None if not force and binding_up_to_date() else ex.submit(build_binding)
+        objs = [] if not force and up_to_date() else list(ex.map(compile_one, srcs))
+        if binding is not None:
+            binding.result()
+    if not objs:
+        return LIB
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
