@@ -974,9 +974,11 @@ __global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_consta
 }
 
 // Shares the items out to ``places`` (SMs, or pairs of them) at a time: all that fill them a whole
-// number of times run whole, what is left over is split so that it fills them once more, in parts of
-// at least 512 keys (4x1024 tokens over 16384 keys, 256 items on 76 pairs: 1010 us whole, 957 us
-// with the last 28 in two parts).  Returns the grid.
+// number of times run whole, what is left over is split so that it fills them once more (4x1024 tokens
+// over 16384 keys, 256 items on 76 pairs: 1010 us whole, 950 us with the last 28 in two parts).  A part
+// has at least 512 keys where nothing else runs (1x128 tokens over 8128 keys: 41 us against 45 with
+// 1024), else 1024 (8 prompts of up to 1024 tokens, 64 wide: 51 us whole, 62 us in parts of 640).
+// Returns the grid.
 static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int block_rows) {
   p.block_rows = block_rows;
   p.row_blocks = static_cast<int>((q4_rows(a.H, a.H_kv, a.max_seqlen_q) + block_rows - 1) / block_rows);
@@ -985,7 +987,7 @@ static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int
   p.tail_splits = 1;
   if (a.n_splits) return items * a.n_splits;
   const int tail = static_cast<int>(items % places);
-  const int s = tail ? min(places / tail, a.max_seqlen_k / 512) : 1;
+  const int s = tail ? min(places / tail, a.max_seqlen_k / (items < places ? 512 : 1024)) : 1;
   if (s < 2) return items;
   p.whole = static_cast<int>(items - tail);
   p.tail_splits = s;
