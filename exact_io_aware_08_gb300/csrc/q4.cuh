@@ -6,7 +6,7 @@
 // 4, so code * scale has at most 6 and lies in [2^-10, 2688]: every product is an exact fp16 number.
 #pragma once
 
-#include "sm103.cuh"
+#include "sm103_paged.cuh"
 
 namespace fa {
 
