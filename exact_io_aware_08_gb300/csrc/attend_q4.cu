@@ -33,7 +33,7 @@
 
 namespace fa {
 
-constexpr float kNone = -1e38f;                               // a reference below every score
+constexpr float kNone = -3.402823466e38f;                     // -FLT_MAX: a reference below every score
 
 template <int D, int NT>
 struct Q4Cfg {
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
             const int i = row / p.G;
             const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
             const size_t th = static_cast<size_t>(tok) * p.H + head;
-            const bool none = M == kNone;                      // a row that sees no key
+            const bool none = L == 0.f;                        // a row that sees no key (scores that are no number: L is none)
             if (x.out < 0) {
               const float inv = none ? 0.f : p.descale_v / L;
               uint32_t h[C::MT];

@@ -128,7 +128,8 @@ __device__ __forceinline__ float q4_query_row(const Q4TParams& p, bool has, size
   // the largest element goes to [2^14, 2^15); exponents such that the power and its inverse are normal
   const int ex = big == 0.f ? 14 : max(-100, static_cast<int>(__float_as_uint(big) >> 23) - 127);
   const float up = __uint_as_float(static_cast<uint32_t>(127 + 14 - ex) << 23);
-  const float c2 = p.score * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23);
+  // (a factor that vanished would make 0 * -inf of a masked score; 2^-126 leaves every weight at 1 too)
+  const float c2 = fmaxf(p.score * __uint_as_float(static_cast<uint32_t>(127 - 14 + ex) << 23), 0x1p-126f);
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     const uint32_t ww[4] = {x[i].x, x[i].y, x[i].z, x[i].w};

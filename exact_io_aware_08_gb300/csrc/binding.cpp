@@ -3,8 +3,8 @@
 //
 // These are the calls of a serving step, a few microseconds of GPU work each when the batch is small.
 // Checked and marshalled in Python a call took the host 18 us (append, 3 of them the launch) to 28 us
-// (decode: two launches, two outputs, a workspace), here 4.5 and 10.  The library's functions come from the handle of the libfa.so that the package has
-// loaded (bind()), errors go up as the package's FaError.
+// (decode: two launches, two outputs, a workspace), here 4.5 and 10.  The library's functions come from
+// the handle of the libfa.so that the package has loaded (bind()), errors go up as the package's FaError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -117,7 +117,7 @@ P* dense(const at::Tensor& t, const char* name, c10::ScalarType type, std::initi
 const fa_bf16_t* tokens(const at::Tensor& t, const char* name, std::initializer_list<int64_t> shape, int& device, long long* stride) {
   check(t, name, at::kBFloat16, shape, device);
   if (t.numel() && (t.stride(2) != 1 || (t.size(1) > 1 && t.stride(1) != t.size(2)))) refuse("%s must be dense in its last two dimensions", name);
-  *stride = t.stride(0);
+  *stride = t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);   // (a single token's is any number)
   return static_cast<const fa_bf16_t*>(t.data_ptr());
 }
 
@@ -167,19 +167,37 @@ float number(PyObject* o, const char* name) {
 
 bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
 
-// None: the device's current stream; else a stream's handle or an object that has one.
-void* stream_of(PyObject* o, int device) {
-  if (!given(o)) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
-  if (PyLong_Check(o)) return PyLong_AsVoidPtr(o);
-  PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
-  if (!h) {
-    PyErr_Clear();
-    refuse("stream must be a stream, its handle or None, is %s", Py_TYPE(o)->tp_name);
+// Where a call runs: on ``device``, and on its current stream (None) or on a stream that is given by its
+// handle or as an object that has one.  What the call allocates then belongs to that stream, as under
+// torch.cuda.stream(): a workspace freed on return is not handed to work of another stream beside it.
+struct Where {
+  c10::cuda::CUDAGuard guard;
+  c10::cuda::OptionalCUDAStreamGuard other;
+  void* stream;
+  Where(PyObject* o, int device) : guard(static_cast<c10::DeviceIndex>(device)) {
+    if (!given(o)) {
+      stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
+      return;
+    }
+    if (PyLong_Check(o)) {
+      stream = PyLong_AsVoidPtr(o);
+    } else {
+      PyObject* h = PyObject_GetAttrString(o, "cuda_stream");
+      const bool has = h && PyLong_Check(h);
+      stream = has ? PyLong_AsVoidPtr(h) : nullptr;
+      Py_XDECREF(h);
+      if (!has) {
+        PyErr_Clear();
+        refuse("stream must be a stream, its handle or None, is %s", Py_TYPE(o)->tp_name);
+      }
+    }
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      refuse("a stream's handle must be an address");
+    }
+    other.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(device)));
   }
-  void* s = PyLong_AsVoidPtr(h);
-  Py_DECREF(h);
-  return s;
-}
+};
 
 at::Tensor make(c10::IntArrayRef shape, c10::ScalarType type, int device) {
   return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device))));
@@ -234,6 +252,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   long long sq = 0, sk, sv;
   const fa_bf16_t* pk = tokens(k, "k", {total, heads, d}, device, &sk);
   const fa_bf16_t* pv = tokens(tensor(a[2], "v"), "v", {total, heads, d}, device, &sv);
+  const Where on(a[16], device);
   const fa_bf16_t* pq = nullptr;
   fa_bf16_t* po = nullptr;
   int64_t H = 0;
@@ -260,18 +279,16 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* cu = dense<int>(tensor(a[10], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, device);
   const int* lens = dense<int>(tensor(a[11], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, device);
   const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, device);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
-  void* stream = stream_of(a[16], device);
   const int ints[] = {narrow(seqs, "n_seqs"), narrow(H, "H"), narrow(heads, "H_kv"), narrow(total, "total"), narrow(table.size(1), "max_blocks"),
                       narrow(block_size, "block_size"), narrow(blocks, "num_blocks"), narrow(d, "d"), narrow(2 * half, "rotary_dim"),
                       truth(a[15]) ? 1 : 0, narrow(positions, "n_positions")};
   if (q4)
     done(lib.append_q4(pq, pk, pv, po, static_cast<fa_e2m1x2_t*>(kc), ks, static_cast<fa_e2m1x2_t*>(vc), vs, cos, sin, cu, lens, tab, ints[0],
                        ints[1], ints[2], ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10],
-                       number(a[13], "descale_k"), number(a[14], "descale_v"), stream));
+                       number(a[13], "descale_k"), number(a[14], "descale_v"), on.stream));
   else
     done(lib.append(pq, pk, pv, po, static_cast<fa_bf16_t*>(kc), static_cast<fa_bf16_t*>(vc), cos, sin, cu, lens, tab, ints[0], ints[1], ints[2],
-                    ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10], stream));
+                    ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10], on.stream));
   if (!q_out.defined()) Py_RETURN_NONE;
   if (given(a[3])) {
     Py_INCREF(a[3]);
@@ -308,6 +325,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int64_t seqs = table.size(0);
   const int64_t total = given(a[4]) ? ranked(a[4], "k", 3, "[total, H_kv, d]").size(0) : integer(a[6], "total");
   if (total < 0) refuse("total must be >= 0 (got %lld)", static_cast<long long>(total));
+  const Where on(a[12], c.device);
   const at::Tensor k = given(a[4]) ? tensor(a[4], "k") : make({total, c.heads, c.d}, at::kBFloat16, c.device);
   const at::Tensor v = given(a[5]) ? tensor(a[5], "v") : make({total, c.heads, c.d}, at::kBFloat16, c.device);
   fa_bf16_t* pk = dense<fa_bf16_t>(k, "k", at::kBFloat16, {total, c.heads, c.d}, c.device);
@@ -315,10 +333,9 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* cu = dense<int>(tensor(a[7], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, c.device);
   const int* lens = dense<int>(tensor(a[8], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
   const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device));
   done(lib.gather_q4(c.k, c.ks, c.v, c.vs, pk, pv, cu, lens, tab, narrow(seqs, "n_seqs"), narrow(c.heads, "H_kv"), narrow(total, "total"),
                      narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), narrow(c.d, "d"),
-                     number(a[10], "descale_k"), number(a[11], "descale_v"), stream_of(a[12], c.device)));
+                     number(a[10], "descale_k"), number(a[11], "descale_v"), on.stream));
   return two(k, a[4], v, a[5]);
   FA_END
 }
@@ -341,15 +358,15 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int max_k = narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k"), splits = narrow(integer(a[13], "n_splits"), "n_splits");
   const int b = narrow(B, "B"), h = narrow(H, "H"), hkv = narrow(c.heads, "H_kv"), d = narrow(c.d, "d");
   const float scale = given(a[10]) ? number(a[10], "scale") : 1.f / std::sqrt(static_cast<float>(d));
+  const Where on(a[15], c.device);
   const at::Tensor o = own && !given(a[5]) ? make({B, H, 1, c.d}, at::kBFloat16, c.device) : tensor(a[5], "o");
   const at::Tensor lse = own && !given(a[6]) ? make({B, H, 1}, at::kFloat, c.device) : tensor(a[6], "lse");
   fa_bf16_t* po = dense<fa_bf16_t>(o, "o", at::kBFloat16, {B, H, 1, c.d}, c.device);
   float* pl = dense<float>(lse, "lse", at::kFloat, {B, H, 1}, c.device);
   const at::Tensor ws = workspace(a[14], own ? lib.decode_q4_ws(b, h, hkv, max_k, d, splits) : 0, c.device, own);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device));
   done(lib.decode_q4(pq, c.k, c.ks, c.v, c.vs, po, pl, tab, lens, b, h, hkv, narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"),
                      narrow(c.blocks, "num_blocks"), max_k, d, scale, number(a[11], "descale_k"), number(a[12], "descale_v"), splits,
-                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, stream_of(a[15], c.device)));
+                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, on.stream));
   return two(o, a[5], lse, a[6]);
   FA_END
 }
@@ -373,16 +390,16 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int splits = narrow(integer(a[16], "n_splits"), "n_splits");
   const int s = narrow(seqs, "n_seqs"), t = narrow(total, "total_q"), h = narrow(H, "H"), hkv = narrow(c.heads, "H_kv"), d = narrow(c.d, "d");
   const float scale = given(a[12]) ? number(a[12], "scale") : 1.f / std::sqrt(static_cast<float>(d));
+  const Where on(a[18], c.device);
   const at::Tensor o = own && !given(a[5]) ? make({total, H, c.d}, at::kBFloat16, c.device) : tensor(a[5], "o");
   const at::Tensor lse = own && !given(a[6]) ? make({H, total}, at::kFloat, c.device) : tensor(a[6], "lse");
   fa_bf16_t* po = dense<fa_bf16_t>(o, "o", at::kBFloat16, {total, H, c.d}, c.device);
   float* pl = dense<float>(lse, "lse", at::kFloat, {H, total}, c.device);
   const at::Tensor ws = workspace(a[17], own ? lib.fwd_q4_ws(s, h, hkv, t, max_q, max_k, d, splits) : 0, c.device, own);
-  const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device));
   done(lib.fwd_q4(pq, c.k, c.ks, c.v, c.vs, po, pl, cu, lens, tab, s, h, hkv, t, max_q, narrow(table.size(1), "max_blocks"),
                   narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, d, scale, number(a[13], "descale_k"),
                   number(a[14], "descale_v"), truth(a[15]) ? 1 : 0, splits, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
-                  stream_of(a[18], c.device)));
+                  on.stream));
   return two(o, a[5], lse, a[6]);
   FA_END
 }

@@ -132,7 +132,7 @@ __device__ __forceinline__ void q4_join(F state, int n, uint16_t* o, float* lse,
     const float* st = state(i);
     if (!st) continue;
     const float2 s = *reinterpret_cast<const float2*>(st + D);
-    if (s.x == -INFINITY) continue;                            // no keys: weight 0
+    if (s.y == 0.f) continue;                                  // no keys (a sum that is no number goes on)
     const float wt = fast_exp2(s.x - M);
     L = fmaf(wt, s.y, L);
 #pragma unroll
@@ -142,7 +142,7 @@ __device__ __forceinline__ void q4_join(F state, int n, uint16_t* o, float* lse,
       acc[2 * k + 1] = fmaf(wt, v.y, acc[2 * k + 1]);
     }
   }
-  const bool none = M == -INFINITY;
+  const bool none = L == 0.f;
   const float inv = none ? 0.f : descale_v / L;
 #pragma unroll
   for (int k = 0; k < V / 2; ++k)

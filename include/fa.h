@@ -390,7 +390,9 @@ fa_status_t fa_gather_paged_q4(const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_sc
  * rounded to 16 bits for the product with the values.  block_size is a positive multiple of 16;
  * seqlens_k, block_table, max_seqlen_k, n_splits and the device-side checks as for fa_decode_paged.
  * A row with no tokens gets O = 0, lse = -inf.  ws: at least the size call's bytes, 16-byte aligned
- * (not looked at where the call runs with one split).
+ * (not looked at where the call runs with one split); calls that may run at the same time, replayed
+ * graphs among them, need one each.  A query element or a key's scale that is no number makes its rows
+ * NaN, a value's scale the elements that it scales, in rows that do not see the value too (0 NaN).
  */
 size_t fa_decode_paged_q4_workspace_size(int B, int H, int H_kv, int max_seqlen_k, int d, int n_splits);
 fa_status_t fa_decode_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales,

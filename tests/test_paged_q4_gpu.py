@@ -359,6 +359,91 @@ def test_q4_attention_is_the_same_twice_and_captured():
         assert torch.equal(o, a) and torch.equal(lse, b)
 
 
+@pytest.mark.parametrize("n", [1, 4, 40, 300])
+def test_q4_attention_with_a_vanishing_score_factor(n):
+    """Scores below fp32's range: every key weighs the same."""
+    require_gpu()
+    lens, H, d = [200], 4, 128
+    cache, table, val = fill_cache(lens, 2, d, 64, 3)
+    q = normal((n, H, d), 4) * 2.0 ** -100
+    o, lse = fa.forward_paged_q4(cuda(q), *cache, i32(table), i32([0, n]), i32(lens), n, 200, causal=False, descale_k=1e-20,
+                                 descale_v=DV)
+    fa.fa_sync_status()
+    for h in range(H):
+        want = P.attend(f64(q[:, h]), val["k"][0][:, h // 2] * (1e-20 / DK), val["v"][0][:, h // 2], d ** -0.5, [200] * n)
+        check_attention(f64(o[:, h]), f64(lse[h]), want)
+
+
+@pytest.mark.parametrize("n_splits", [0, 1, 3])
+@pytest.mark.parametrize("n", [1, 3, 40, 200])
+def test_numbers_that_are_none_stay_none(n, n_splits):
+    """A query row that holds no number, and rows that see a key or value whose scale is none, give NaN;
+    the other rows, rows without keys and the other sequences keep their results."""
+    require_gpu()
+    H, H_kv, d, lens = 4, 2, 128, [700, 700, 0, 300]
+    cu = np.arange(5) * n
+    cache, table, _ = fill_cache(lens, H_kv, d, 64, 11)
+    q = cuda(normal((4 * n, H, d), 3))
+    args = (i32(table), i32(cu), i32(lens), n, 700)
+    more = dict(causal=False, n_splits=n_splits, descale_k=DK, descale_v=DV)
+    o, lse = fa.forward_paged_q4(q, *cache, *args, **more)
+    bad = q.clone()
+    bad[0, 1, 5] = float("nan")
+    bad[2 * n + n - 1, 0, 0] = float("nan")                  # a sequence without keys: nothing to be seen
+    ks, vs = cache[1].clone(), cache[3].clone()
+    ks[int(table[1, 2]), 0, 9, 3] = 0x7F                     # sequence 1, key 137, key head 0
+    vs[int(table[3, 4]), 1, 2, 7] = 0xFF                     # sequence 3, value 258, key head 1, the last 16 elements
+    o2, lse2 = fa.forward_paged_q4(bad, cache[0], ks, cache[2], vs, *args, **more)
+    fa.fa_sync_status()
+    o, lse, o2, lse2 = (x.cpu() for x in (o, lse, o2, lse2))
+    lost = torch.zeros(4 * n, H, d, dtype=torch.bool)
+    lost[0, 1] = True
+    lost[n:2 * n, :2] = True
+    lost[3 * n:, 2:, 112:] = True
+    assert (o2.isnan() == lost).all()
+    assert torch.equal(o2[~lost], o[~lost])
+    gone = torch.zeros(H, 4 * n, dtype=torch.bool)
+    gone[1, 0] = True
+    gone[:2, n:2 * n] = True
+    assert (lse2.isnan() == gone).all()
+    assert torch.equal(lse2[~gone], lse[~gone])
+
+
+def test_outputs_belong_to_the_stream_that_is_given():
+    """What a call allocates for another stream than the current one is that stream's memory."""
+    require_gpu()
+    lens = [500, 90]
+    cache, table, _ = fill_cache(lens, 2, 128, 64, 21)
+    q = cuda(normal((2, 8, 1, 128), 6))
+    args = (*cache, i32(table), i32(lens), 500)
+    o, lse = fa.decode_paged_q4(q, *args, descale_k=DK, descale_v=DV)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        o2, lse2 = fa.decode_paged_q4(q, *args, descale_k=DK, descale_v=DV, stream=stream)
+        side.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        for t in (o2, lse2):
+            segment = [x for x in torch.cuda.memory_snapshot() if x["address"] <= t.data_ptr() < x["address"] + x["total_size"]]
+            assert [x["stream"] for x in segment] == [side.cuda_stream]
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    fa.fa_sync_status()
+
+
+def test_append_of_one_token_with_any_token_stride():
+    require_gpu()
+    nb, table = make_pages([70], 64, 0, 1)
+    x = cuda(normal((3, 2, 128), 4))
+    caches = []
+    for k in (x[:1], x.view(-1)[:256].as_strided((1, 2, 128), (3, 128, 1))):
+        kc, vc = (torch.zeros(nb, 64, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        fa.append_paged(k, k, kc, vc, i32(table), i32([0, 1]), i32([70]))
+        caches.append((kc, vc))
+    fa.fa_sync_status()
+    assert torch.equal(caches[0][0], caches[1][0]) and torch.equal(caches[0][1], caches[1][1])
+    assert torch.equal(caches[1][0][int(table[0, 1]), 5], x[0])
+
+
 def test_decode_equals_forward_of_one_token():
     require_gpu()
     lens, H, H_kv, d = [700, 64, 0, 333], 8, 4, 128
