@@ -54,9 +54,9 @@ struct Q4TCfg {
   static constexpr uint32_t T_S = 0, T_O = 256;
   static constexpr int THREADS = 512;
   static constexpr int UNPACK_WARPS = 4;
-  // launched with 128 registers a thread; 128 * 64 + 256 * 168 + 128 * 96 = 63488 = 512 * 124
-  static constexpr uint32_t REG_CTRL = 64, REG_SOFTMAX = 168, REG_UNPACK = 96;
-  static constexpr int REG_NEED = 128 * 64 + 256 * 168 + 128 * 96;
+  // launched with 128 registers a thread, all of which the split uses
+  static constexpr uint32_t REG_CTRL = 56, REG_SOFTMAX = 208, REG_UNPACK = 40;
+  static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
   static constexpr float RESCALE = 8.f;
   static constexpr uint32_t BAR_P = 3, BAR_P_THREADS = 128 + 32 + 32;
 };
@@ -142,47 +142,45 @@ __device__ __forceinline__ float q4_query_row(const Q4TParams& p, bool has, size
   return c2;
 }
 
+// A value that the compiler forms again rather than hold what follows from it in registers.
+__device__ __forceinline__ int again(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
 // One key tile of a row: S in tensor memory (columns t_s) becomes P over its first half, O (t_o) is
-// rescaled where the row's reference moves.  Keys from ``lim`` on are not the row's.
+// rescaled where the row's reference moves.  Keys from ``lim`` on are not the row's, those from
+// ``lim_low`` on not every row's of the warp.  ``far``: a reference of the warp is large.
 template <int D>
-__device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int k0, int lim, bool first, float c2, float& m, float& l) {
-  // S in four quarters of 32 columns.  The row maximum needs all four; the first two then stay in
-  // registers and the others are loaded a second time when their turn comes, so that a thread
-  // holds 96 scores at most beside P's words (all 128 made the compiler spill 450 bytes a thread:
-  // 1558 instead of 1200 us for 4x1024 tokens over 16384 keys).
-  const bool edge = __any_sync(0xffffffffu, k0 + Q4TCfg<D>::BN > lim);
-  uint32_t s0[32], s1[32], s2[32];
-  auto mask = [&](uint32_t (&v)[32], int q) {
-    if (edge) {
+__device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int k0, int lim, int lim_low, bool first, float c2,
+                                                float& m, float& l, bool& far) {
+  // The row's 128 scores stay in registers: with 208 of them a thread nothing of this spills (kept in
+  // quarters, two of them loaded twice, in 168 registers: 957 instead of 781 us for 4x1024 tokens over
+  // 16384 keys; in 168 registers all 128: 1558).
+  const bool edge = k0 + Q4TCfg<D>::BN > lim_low;
+  float s[128];
 #pragma unroll
-      for (int k = 0; k < 32; ++k)
-        if (k0 + 32 * q + k >= lim) v[k] = 0xff800000u;
-    }
-  };
-  auto top = [&](uint32_t (&v)[32]) {
-    float x = fmax3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]));
-    float y = fmax3(__uint_as_float(v[3]), __uint_as_float(v[4]), __uint_as_float(v[5]));
+  for (int k = 0; k < 4; ++k) {
+    uint32_t rr[32];
+    tmem_ld32(t_s + k * 32, rr);
 #pragma unroll
-    for (int k = 6; k < 30; k += 4) {
-      x = fmax3(x, __uint_as_float(v[k]), __uint_as_float(v[k + 1]));
-      y = fmax3(y, __uint_as_float(v[k + 2]), __uint_as_float(v[k + 3]));
-    }
-    return fmax3(fmaxf(x, y), __uint_as_float(v[30]), __uint_as_float(v[31]));
-  };
-  float mq;
-  {
-    uint32_t s3[32];
-    tmem_ld32(t_s + 64, s2);
-    tmem_ld32(t_s + 96, s3);
-    tmem_ld32(t_s, s0);
-    tmem_ld32(t_s + 32, s1);
-    tmem_wait_ld();
-    mask(s2, 2);
-    mask(s3, 3);
-    mask(s0, 0);
-    mask(s1, 1);
-    mq = fmaxf(fmaxf(top(s0), top(s1)), fmaxf(top(s2), top(s3)));
+    for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
   }
+  tmem_wait_ld();
+  if (edge) {
+#pragma unroll
+    for (int k = 0; k < 128; ++k)
+      if (k0 + k >= lim) s[k] = -INFINITY;
+  }
+  float mx[4];
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    mx[g] = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
+#pragma unroll
+    for (int k = 3; k < 31; k += 2) mx[g] = fmax3(mx[g], s[32 * g + k], s[32 * g + k + 1]);
+    mx[g] = fmaxf(mx[g], s[32 * g + 31]);
+  }
+  const float mq = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
   const float cand = fmaxf(m, mq);
   // a row that sees none of the tile's keys has nothing to move
   const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > Q4TCfg<D>::RESCALE);
@@ -192,6 +190,7 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
       l *= alpha;
       m = cand;
     }
+    far = __any_sync(0xffffffffu, fabsf(m * c2) > 4096.f && m != -INFINITY);
     if (!first) {
       // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order)
 #pragma unroll
@@ -212,38 +211,30 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
   float ms = (m == -INFINITY) ? 0.f : m * c2;
   // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
   // taken off first
-  const bool far = __any_sync(0xffffffffu, fabsf(ms) > 4096.f);
   const float ref = (m == -INFINITY) ? 0.f : m;
   if (far) ms = 0.f;
   const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
-  float2 rs[2];
-  rs[0] = rs[1] = make_float2(0.f, 0.f);
-  auto weigh = [&](uint32_t (&v)[32], int q) {            // P's columns 16 q .. 16 q + 15
-    if (far) {
+  if (far) {
 #pragma unroll
-      for (int k = 0; k < 32; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) - ref);
-    }
-    uint32_t pk[16];
+    for (int k = 0; k < 128; ++k) s[k] -= ref;
+  }
+  float2 rs[4];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float2 x = ffma2(make_float2(__uint_as_float(v[2 * k]), __uint_as_float(v[2 * k + 1])), c2v, nms);
+  for (int k = 0; k < 4; ++k) rs[k] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float2 x = ffma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2v, nms);
       const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
       pk[k] = pack_f16x2(e.x, e.y);
-      rs[k & 1] = fadd2(rs[k & 1], e);
+      rs[k & 3] = fadd2(rs[k & 3], e);
     }
-    tmem_st16(t_s + q * 16, pk);
-  };
-  tmem_ld32(t_s + 64, s2);                                // (P covers columns 0 to 63 only)
-  weigh(s0, 0);
-  weigh(s1, 1);
-  tmem_ld32(t_s + 96, s0);
-  tmem_wait_ld();
-  mask(s2, 2);
-  weigh(s2, 2);
-  mask(s0, 3);
-  weigh(s0, 3);
-  const float2 rs01 = fadd2(rs[0], rs[1]);
-  l += rs01.x + rs01.y;
+    tmem_st32(t_s + h * 32, pk);
+  }
+  const float2 sum = fadd2(fadd2(rs[0], rs[1]), fadd2(rs[2], rs[3]));
+  l += sum.x + sum.y;
 }
 
 // The row's result, or its chunk's state: O of columns t_o over l (``any``: some key tile was run).
@@ -559,20 +550,20 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     const uint32_t t_s = tbase + t_lane + C::T_S + t * 128;
     const uint32_t t_o = tbase + t_lane + C::T_O + t * 128;
     const int n = t == 0 ? n_t[0] : n_t[1];
-    const int tok = first + r / p.G, head = hkv * p.G + r % p.G;
-    const size_t th = static_cast<size_t>(tok) * p.H + head;
-    const bool has = r < rows;
-    const float c2 = q4_query_row<D>(p, has, th, sQ + t * C::TILE, row);
+    const size_t th = static_cast<size_t>(first + r / p.G) * p.H + hkv * p.G + r % p.G;
+    const float c2 = q4_query_row<D>(p, r < rows, th, sQ + t * C::TILE, row);
     fence_proxy_async_smem();
     mbar_arrive(q_full);
     const int lim = min(key_end, seen(r));                    // keys below it are this row's
+    const int lim_low = __reduce_min_sync(0xffffffffu, lim);
+    bool far = false;
     float m = -INFINITY, l = 0.f;                             // reference (raw units) and sum of the weights
     bool ok = true;
     int handed = 0;
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
       tc_fence_after();
-      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l);
+      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, lim_low, j == 0, c2, m, l, far);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -589,7 +580,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       tc_fence_after();
     }
     if (ok && row0 + t * C::BM < rows) {
-      q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, item, r - row0, c2, m, l);
+      const int x = again(r), tok = first + x / p.G, head = hkv * p.G + x % p.G;
+      q4_store_row<D>(p, t_o, n > 0, x < rows, static_cast<size_t>(tok) * p.H + head, tok, head, item, x - row0, c2, m, l);
     }
   }
   __syncwarp();
@@ -638,8 +630,8 @@ struct Q4PCfg {
   static constexpr uint32_t T_S = 0, T_O = 256;
   static constexpr int THREADS = 512;
   static constexpr int UNPACK_WARPS = 4;
-  static constexpr uint32_t REG_CTRL = 64, REG_SOFTMAX = 168, REG_UNPACK = 96;
-  static constexpr int REG_NEED = 128 * 64 + 256 * 168 + 128 * 96;
+  static constexpr uint32_t REG_CTRL = 48, REG_SOFTMAX = 208, REG_UNPACK = 48;
+  static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
 };
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Q4PCfg::THREADS, 1)
@@ -915,21 +907,21 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     const uint32_t t_s = tbase + t_lane + C::T_S + t * 128;
     const uint32_t t_o = tbase + t_lane + C::T_O + t * 128;
     const int n = t == 0 ? n_t[0] : n_t[1];
-    const int tok = first + r / p.G, head = hkv * p.G + r % p.G;
-    const size_t th = static_cast<size_t>(tok) * p.H + head;
-    const bool has = r < rows;
-    const float c2 = q4_query_row<D>(p, has, th, sQ + t * C::QTILE, row);
+    const size_t th = static_cast<size_t>(first + r / p.G) * p.H + hkv * p.G + r % p.G;
+    const float c2 = q4_query_row<D>(p, r < rows, th, sQ + t * C::QTILE, row);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive_cluster(cluster_addr(q_full, 0));
     const uint32_t hand = cluster_addr(&p_full[t], 0);
     const int lim = min(key_end, seen(r));
+    const int lim_low = __reduce_min_sync(0xffffffffu, lim);
+    bool far = false;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = 0; j < n; ++j) {
       if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;
       tc_fence_after();
-      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l);
+      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, lim_low, j == 0, c2, m, l, far);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
@@ -939,7 +931,10 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
       ok = mbar_wait_warp(&o_done[t], 0, abort_flag, 492);
       tc_fence_after();
     }
-    if (ok && row0 + t * 256 < rows) q4_store_row<D>(p, t_o, n > 0, has, th, tok, head, item, r - row0, c2, m, l);
+    if (ok && row0 + t * 256 < rows) {
+      const int x = again(r), tok = first + x / p.G, head = hkv * p.G + x % p.G;
+      q4_store_row<D>(p, t_o, n > 0, x < rows, static_cast<size_t>(tok) * p.H + head, tok, head, item, x - row0, c2, m, l);
+    }
   }
   __syncwarp();
   tc_fence_before();
