@@ -149,15 +149,16 @@ __device__ __forceinline__ int again(int x) {
 }
 
 // One key tile of a row: S in tensor memory (columns t_s) becomes P over its first half, O (t_o) is
-// rescaled where the row's reference moves.  Keys from ``lim`` on are not the row's, those from
-// ``lim_low`` on not every row's of the warp.  ``far``: a reference of the warp is large.
-template <int D>
-__device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int k0, int lim, int lim_low, bool first, float c2,
-                                                float& m, float& l, bool& far) {
+// rescaled where the row's reference moves.  Keys from ``lim`` on are not the row's.  ``far``: a
+// reference of the warp is large.  PLAIN: all keys are the rows' and none was far; written out twice
+// since the two tests stood as instructions of every element (794 instead of 758 us for 4x1024 tokens
+// over 16384 keys).
+template <int D, bool PLAIN>
+__device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int k0, int lim, bool first, float c2, float& m, float& l,
+                                                bool& far) {
   // The row's 128 scores stay in registers: with 208 of them a thread nothing of this spills (kept in
   // quarters, two of them loaded twice, in 168 registers: 957 instead of 781 us for 4x1024 tokens over
   // 16384 keys; in 168 registers all 128: 1558).
-  const bool edge = k0 + Q4TCfg<D>::BN > lim_low;
   float s[128];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -167,7 +168,7 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
     for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
   }
   tmem_wait_ld();
-  if (edge) {
+  if constexpr (!PLAIN) {
 #pragma unroll
     for (int k = 0; k < 128; ++k)
       if (k0 + k >= lim) s[k] = -INFINITY;
@@ -183,14 +184,20 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
   const float mq = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
   const float cand = fmaxf(m, mq);
   // a row that sees none of the tile's keys has nothing to move
-  const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > Q4TCfg<D>::RESCALE);
+  const bool move = (PLAIN || cand != -INFINITY) && (m == -INFINITY || (cand - m) * c2 > Q4TCfg<D>::RESCALE);
   if (__any_sync(0xffffffffu, move)) {
     const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
     if (move) {
       l *= alpha;
       m = cand;
     }
+    // s c2 - m c2 is off by the rounding of m c2: where that could matter the reference is taken off
+    // the scores first
     far = __any_sync(0xffffffffu, fabsf(m * c2) > 4096.f && m != -INFINITY);
+    if (PLAIN && far) {
+#pragma unroll
+      for (int k = 0; k < 128; ++k) s[k] -= (m == -INFINITY) ? 0.f : m;
+    }
     if (!first) {
       // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order)
 #pragma unroll
@@ -208,16 +215,12 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
       }
     }
   }
-  float ms = (m == -INFINITY) ? 0.f : m * c2;
-  // s c2 - ms is off by ms's own rounding, |ms| 2^-24: where that could matter the reference is
-  // taken off first
-  const float ref = (m == -INFINITY) ? 0.f : m;
-  if (far) ms = 0.f;
-  const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
-  if (far) {
+  if (!PLAIN && far) {
 #pragma unroll
-    for (int k = 0; k < 128; ++k) s[k] -= ref;
+    for (int k = 0; k < 128; ++k) s[k] -= (m == -INFINITY) ? 0.f : m;
   }
+  const float ms = PLAIN ? (far ? 0.f : m * c2) : far || m == -INFINITY ? 0.f : m * c2;
+  const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
   float2 rs[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) rs[k] = make_float2(0.f, 0.f);
@@ -555,23 +558,31 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     fence_proxy_async_smem();
     mbar_arrive(q_full);
     const int lim = min(key_end, seen(r));                    // keys below it are this row's
-    const int lim_low = __reduce_min_sync(0xffffffffu, lim);
+    const int lim_low = __reduce_min_sync(0xffffffffu, lim);  // keys below it are all the warp's rows'
     bool far = false;
     float m = -INFINITY, l = 0.f;                             // reference (raw units) and sum of the weights
     bool ok = true;
-    int handed = 0;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
-      tc_fence_after();
-      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, lim_low, j == 0, c2, m, l, far);
+    int j = 0;
+    auto hand_over = [&] {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       named_bar_arrive(C::BAR_P + t, C::BAR_P_THREADS);
-      ++handed;
+    };
+    for (const int plain = min(n, (lim_low - key0) / C::BN); !far && j < plain; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
+      tc_fence_after();
+      q4_softmax_tile<D, true>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l, far);
+      hand_over();
+    }
+    for (; ok && j < n; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 460))) break;
+      tc_fence_after();
+      q4_softmax_tile<D, false>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l, far);
+      hand_over();
     }
     // after an abort: keep joining (blocking) the remaining hand-offs
-    for (; handed < n; ++handed) {
+    for (; j < n; ++j) {
       __syncwarp();
       named_bar_sync(C::BAR_P + t, C::BAR_P_THREADS);
     }
@@ -914,18 +925,28 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     if (lane == 0) mbar_arrive_cluster(cluster_addr(q_full, 0));
     const uint32_t hand = cluster_addr(&p_full[t], 0);
     const int lim = min(key_end, seen(r));
-    const int lim_low = __reduce_min_sync(0xffffffffu, lim);
+    const int lim_low = __reduce_min_sync(0xffffffffu, lim);  // keys below it are all the warp's rows'
     bool far = false;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;
-      tc_fence_after();
-      q4_softmax_tile<D>(t_s, t_o, key0 + j * C::BN, lim, lim_low, j == 0, c2, m, l, far);
+    int j = 0;
+    auto hand_over = [&] {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(hand);
+    };
+    for (const int plain = min(n, (lim_low - key0) / C::BN); !far && j < plain; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;
+      tc_fence_after();
+      q4_softmax_tile<D, true>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l, far);
+      hand_over();
+    }
+    for (; ok && j < n; ++j) {
+      if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;
+      tc_fence_after();
+      q4_softmax_tile<D, false>(t_s, t_o, key0 + j * C::BN, lim, j == 0, c2, m, l, far);
+      hand_over();
     }
     if (ok && n > 0) {
       ok = mbar_wait_warp(&o_done[t], 0, abort_flag, 492);
