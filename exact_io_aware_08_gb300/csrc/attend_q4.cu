@@ -698,30 +698,28 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
   __syncthreads();
 }
 
-// Joins a row's chunks where the caller gave their count (part: [row][chunk]): one warp a row.
-template <int D>
+// Joins a row's chunks where the caller gave their count (part: [row][chunk]): WPR warps a row.
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ o,
                                                              float* __restrict__ lse, const int* __restrict__ cu_q,
                                                              int n_seqs, int H, int total_q, int n_splits, float descale_v) {
-  pdl_wait();
-  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (th >= static_cast<long long>(total_q) * H) return;
+  const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int tok = static_cast<int>(th / H), head = static_cast<int>(th - static_cast<long long>(tok) * H);
-  if (cu_q && tok >= __ldg(cu_q + n_seqs)) return;             // rows behind the last sequence stay as they are
-  const float* base = part + static_cast<size_t>(th) * n_splits * (D + 2);
-  q4_join<D>([&](int i) { return base + static_cast<size_t>(i) * (D + 2); }, n_splits, o + static_cast<size_t>(th) * D,
+  // rows behind the last sequence stay as they are
+  const bool some = th < static_cast<long long>(total_q) * H && !(cu_q && tok >= __ldg(cu_q + n_seqs));
+  pdl_wait();
+  q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0}, o + static_cast<size_t>(th) * D,
              lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
-// Joins the states of the row blocks that lie in several teams' shares: one warp a row.
+// Joins the states of the row blocks that lie in several teams' shares: a block a row.
 template <int D, int NT>
 __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int grid) {
   constexpr int ROWS = 8 * NT;
-  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const bool some = th < static_cast<long long>(p.total_q) * p.H;
-  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
+  const int th = blockIdx.x;
+  const int tok = th / p.H, head = th - tok * p.H;
   int b = tok, first, count;
-  if (p.cu_q) b = some ? owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423) : -1;
+  if (p.cu_q) b = owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423);
   int none;
   long long before = 0;
   // (the search is asked for nothing: the units before sequence b are counted here)
@@ -729,19 +727,22 @@ __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_consta
   for (int i = threadIdx.x & 31; i < b; i += 32) before += q4_seq(p, i, ROWS, false).units(p.H_kv);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+  Q4States st{p.part, 2 * ROWS * (D + 2), ROWS * (D + 2), 0};
+  if (b >= 0) {                                                // (else behind the last sequence: stays as it is)
+    const Q4Seq seq = q4_seq(p, b, ROWS, false);
+    if (seq.blocks > 0) {                                      // (else reported)
+      const int row = (tok - seq.first) * p.G + head % p.G;
+      const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
+      const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
+      if (c0 != c1) {                                          // (else its team wrote the result)
+        st.base += (static_cast<size_t>(2 * c0) * ROWS + row % ROWS) * (D + 2);
+        st.n = c1 - c0 + 1;
+      }
+    }
+  }
   pdl_wait();
-  if (!some || b < 0) return;                                  // behind the last sequence: stays as it is
-  const Q4Seq seq = q4_seq(p, b, ROWS, false);
-  if (seq.blocks == 0) return;                                 // reported
-  const int row = (tok - seq.first) * p.G + head % p.G;
-  const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
-  const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
-  if (c0 == c1) return;                                        // its team wrote the result
-  q4_join<D>([&](int i) -> const float* {
-        const int c = c0 + i;
-        return p.part + (static_cast<size_t>(2 * c + (i == 0 ? 1 : 0)) * ROWS + row % ROWS) * (D + 2);
-      }, c1 - c0 + 1, p.o + static_cast<size_t>(th) * D,
-      p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)), p.descale_v);
+  q4_join<D, 4>(st, p.o + static_cast<size_t>(th) * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)),
+             p.descale_v);
 }
 
 static int q4_sm_count() {
@@ -753,10 +754,6 @@ static int q4_sm_count() {
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 152;
   if (dev < 64) cached[dev] = n;
   return n;
-}
-
-static unsigned join_blocks(const PagedQ4Args& a) {
-  return static_cast<unsigned>((static_cast<long long>(a.total_q) * a.H + 3) / 4);
 }
 
 template <int D, int NT>
@@ -793,14 +790,16 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_splits) return e;
-  log_launch("attend_q4_join_kernel<D, NT>", join_blocks(a), 128, 0ull);
-  return launch_join(attend_q4_join_kernel<D, NT>, join_blocks(a), stream, p, C::TEAMS * grid);
+  const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.total_q) * a.H);
+  log_launch("attend_q4_join_kernel<D, NT>", blocks, 128, 0ull);
+  return launch_join(attend_q4_join_kernel<D, NT>, blocks, stream, p, C::TEAMS * grid);
 }
 
-template <int D>
+template <int D, int WPR>
 static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t stream) {
-  log_launch("attend_q4_merge_kernel<D>", join_blocks(a), 128, 0ull);
-  return launch_join(attend_q4_merge_kernel<D>, join_blocks(a), stream, static_cast<const float*>(a.part),
+  const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.total_q) * a.H * WPR + 3) / 4);
+  log_launch("attend_q4_merge_kernel<D, WPR>", blocks, 128, 0ull);
+  return launch_join(attend_q4_merge_kernel<D, WPR>, blocks, stream, static_cast<const float*>(a.part),
                      static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.n_splits, a.descale_v);
 }
 
@@ -815,7 +814,9 @@ cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
     else e = small ? launch_attend_q4_d<128, 1>(a, stream) : launch_attend_q4_d<128, 2>(a, stream);
   }
   if (e != cudaSuccess || a.n_splits <= 1) return e;
-  return a.d == 64 ? launch_attend_q4_merge<64>(a, stream) : launch_attend_q4_merge<128>(a, stream);
+  if (q4_join_warps(a.n_splits) == 1)
+    return a.d == 64 ? launch_attend_q4_merge<64, 1>(a, stream) : launch_attend_q4_merge<128, 1>(a, stream);
+  return a.d == 64 ? launch_attend_q4_merge<64, 4>(a, stream) : launch_attend_q4_merge<128, 4>(a, stream);
 }
 
 }  // namespace fa

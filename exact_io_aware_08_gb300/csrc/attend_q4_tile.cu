@@ -967,26 +967,25 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   }
 }
 
-// Joins the parts of the items from ``whole`` on: one warp a row.
-template <int D>
+// Joins the parts of the items from ``whole`` on: WPR warps a row.
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_constant__ Q4TParams p, int n_rows) {
-  pdl_wait();
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (i >= n_rows) return;
+  const int i = WPR > 1 ? blockIdx.x : blockIdx.x * 4 + (threadIdx.x >> 5);
   const int n = i / p.block_rows, row = i - n * p.block_rows;
   const Q4TItem x = q4_tile_item(p, p.whole + n * p.tail_splits);
   int first = x.b, nq = 1;
-  if (p.cu_q) {
+  if (i < n_rows && p.cu_q) {
     first = __ldg(p.cu_q + x.b);
     const int end = __ldg(p.cu_q + x.b + 1);
     nq = end - first;
-    if (first < 0 || end < first || end > p.total_q || nq > p.max_q) return;   // reported
+    if (first < 0 || end < first || end > p.total_q || nq > p.max_q) nq = 0;   // reported
   }
   const int r = x.rb * p.block_rows + row;
-  if (r >= nq * p.G) return;
+  const bool some = i < n_rows && r < nq * p.G;
   const int tok = first + r / p.G, head = x.hkv * p.G + r % p.G;
   const size_t th = static_cast<size_t>(tok) * p.H + head;
-  q4_join<D>([&](int k) { return p.part + (x.state + static_cast<size_t>(k) * p.block_rows + row) * (D + 2); }, p.tail_splits,
+  pdl_wait();
+  q4_join<D, WPR>({p.part + (x.state + row) * (D + 2), static_cast<size_t>(p.block_rows) * (D + 2), 0, some ? p.tail_splits : 0},
              p.o + th * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th), p.descale_v);
 }
 
@@ -1016,8 +1015,9 @@ template <int D>
 static cudaError_t launch_tail(const Q4TParams& p, long long grid, cudaStream_t stream) {
   if (p.tail_splits == 1) return cudaSuccess;
   const int rows = static_cast<int>((grid - p.whole) / p.tail_splits) * p.block_rows;
-  log_launch("attend_q4_tail_kernel<D>", rows / 4, 128, 0ull);
-  return launch_join(attend_q4_tail_kernel<D>, rows / 4, stream, p, rows);
+  const int warps = q4_join_warps(p.tail_splits);
+  log_launch("attend_q4_tail_kernel<D, WPR>", rows / 4 * warps, 128, 0ull);
+  return launch_join(warps == 1 ? attend_q4_tail_kernel<D, 1> : attend_q4_tail_kernel<D, 4>, rows / 4 * warps, stream, p, rows);
 }
 
 static cudaError_t launch_attend_q4_pair(Q4TParams& p, const PagedQ4Args& a, cudaStream_t stream) {

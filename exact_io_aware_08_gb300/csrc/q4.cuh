@@ -112,43 +112,78 @@ __device__ __forceinline__ bool place_of_token(const int* __restrict__ table, in
   return ok;
 }
 
-// Writes a row's result from its chunks' states, which ``state(i)`` gives for i < n: one warp.
-template <int D, typename F>
-__device__ __forceinline__ void q4_join(F state, int n, uint16_t* o, float* lse, float descale_v) {
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const float* st = state(i);
-    if (st) M = fmaxf(M, st[D]);
+// A row's states: n of them, ``stride`` floats apart, the first one ``skip`` floats further on.  n = 0: no row.
+struct Q4States {
+  const float* base;
+  size_t stride, skip;
+  int n;
+};
+
+// Writes a row's result from its states (O~ [D], then reference and sum).  WPR warps of the block, the
+// whole of it, or one share a row: every WPR-th state each, eight in flight at a time (a load takes about a
+// microsecond here, so one warp that read 63 states one after the other took 30 us).
+template <int D, int WPR>
+__device__ __forceinline__ void q4_join(const Q4States& x, uint16_t* o, float* lse, float descale_v) {
+  constexpr int V = D / 64;                                    // pairs of elements a lane
+  constexpr int AT_ONCE = 8;
+  const int lane = threadIdx.x & 31, w = WPR == 1 ? 0 : threadIdx.x >> 5;
+  float M = -INFINITY, L = 0.f;
+  float2 acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = make_float2(0.f, 0.f);
+  auto add = [&](float2 ml, const float2 (&v)[V]) {
+    if (ml.y == 0.f) return;                                   // no keys (a sum that is no number goes on)
+    const float top = fmaxf(M, ml.x);
+    const float alpha = top == M ? 1.f : fast_exp2(M - top), wt = fast_exp2(ml.x - top);
+    M = top;
+    L = fmaf(L, alpha, wt * ml.y);
+#pragma unroll
+    for (int k = 0; k < V; ++k) acc[k] = ffma2(make_float2(wt, wt), v[k], fmul2(acc[k], make_float2(alpha, alpha)));
+  };
+  for (int i0 = w; i0 < x.n; i0 += WPR * AT_ONCE) {
+    float2 ml[AT_ONCE], v[AT_ONCE][V];
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) {
+      const int i = i0 + j * WPR;
+      ml[j] = make_float2(0.f, 0.f);
+      if (i < x.n) {
+        const float* st = x.base + i * x.stride + (i == 0 ? x.skip : 0);
+        ml[j] = *reinterpret_cast<const float2*>(st + D);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[j][k] = *reinterpret_cast<const float2*>(st + 64 * k + 2 * lane);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) add(ml[j], v[j]);
   }
+  if constexpr (WPR > 1) {
+    __shared__ float2 ml_of[WPR], acc_of[WPR][V][32];
+    if (w > 0) {
+      if (lane == 0) ml_of[w] = make_float2(M, L);
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-  constexpr int V = D / 32;
-  float acc[V], L = 0.f;
+      for (int k = 0; k < V; ++k) acc_of[w][k][lane] = acc[k];
+    }
+    __syncthreads();
+    if (w > 0) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* st = state(i);
-    if (!st) continue;
-    const float2 s = *reinterpret_cast<const float2*>(st + D);
-    if (s.y == 0.f) continue;                                  // no keys (a sum that is no number goes on)
-    const float wt = fast_exp2(s.x - M);
-    L = fmaf(wt, s.y, L);
+    for (int i = 1; i < WPR; ++i) {
+      float2 v[V];
 #pragma unroll
-    for (int k = 0; k < V / 2; ++k) {
-      const float2 v = *reinterpret_cast<const float2*>(st + 64 * k + 2 * lane);
-      acc[2 * k] = fmaf(wt, v.x, acc[2 * k]);
-      acc[2 * k + 1] = fmaf(wt, v.y, acc[2 * k + 1]);
+      for (int k = 0; k < V; ++k) v[k] = acc_of[i][k][lane];
+      add(ml_of[i], v);
     }
   }
+  if (x.n == 0) return;
   const bool none = L == 0.f;
   const float inv = none ? 0.f : descale_v / L;
 #pragma unroll
-  for (int k = 0; k < V / 2; ++k)
-    *reinterpret_cast<uint32_t*>(o + 64 * k + 2 * lane) = none ? 0u : pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  for (int k = 0; k < V; ++k)
+    *reinterpret_cast<uint32_t*>(o + 64 * k + 2 * lane) = none ? 0u : pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
   if (lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
+
+// Warps a row: all four of a block where it has many states.
+__host__ __device__ constexpr int q4_join_warps(int states) { return states > 8 ? 4 : 1; }
 
 // The join runs behind the chunks on the stream, but may start while their last CTAs run
 // (programmatic dependent launch): it reads lengths and boundaries, then waits for the states.
