@@ -52,13 +52,13 @@ struct Q4Cfg {
   static constexpr int TEAMS = NT == 1 ? 4 : 3;
   static constexpr int THREADS = 128 * (TEAMS + 1);           // a warpgroup a team, and one that copies
   static constexpr int QBUF = ROWS * D * 2;
-  static constexpr int OFF_Q = NST * STAGE;                   // two items' query rows
+  static constexpr int OFF_Q = NST * STAGE;                   // an item's query rows
   static constexpr int MROW = D + 4;                          // floats of a merge row (bank spread)
-  static constexpr int OFF_MERGE = OFF_Q + 2 * QBUF;          // (WARPS - 1) x ROWS x MROW
-  static constexpr int OFF_ML = OFF_MERGE + (WARPS - 1) * ROWS * MROW * 4;   // (WARPS - 1) x ROWS x (m, l)
-  static constexpr int OFF_BAR = OFF_ML + (WARPS - 1) * ROWS * 8;
-  // full[NST], empty[NST], q_full[2], q_empty[2], merge written, merge read; then start[3], abort flag
-  static constexpr int NBAR = 2 * NST + 6;
+  static constexpr int OFF_MERGE = OFF_Q + QBUF;              // WARPS x ROWS x MROW
+  static constexpr int OFF_ML = OFF_MERGE + WARPS * ROWS * MROW * 4;   // WARPS x ROWS x (m, l)
+  static constexpr int OFF_BAR = OFF_ML + WARPS * ROWS * 8;
+  // full[NST], empty[NST], q_full, q_empty, merge written, merge read; then start[3], abort flag
+  static constexpr int NBAR = 2 * NST + 4;
   static constexpr int TEAM_BYTES = (OFF_BAR + NBAR * 8 + 16 + 1023) / 1024 * 1024;
   static constexpr int SMEM_BYTES = TEAMS * TEAM_BYTES + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NST;
   uint64_t* q_full = empty + C::NST;
-  uint64_t* q_empty = q_full + 2;
-  uint64_t* mrg = q_empty + 2;                                // [0]: warps 1 to 3 wrote, [1]: warp 0 read
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* mrg = q_empty + 1;                                // [0]: the warps' states are written, [1]: read
   int* start = reinterpret_cast<int*>(mrg + 2);               // sequence, unit in it, units of the share
   volatile int* abort_flag = start + 3;
   const int id = team * gridDim.x + blockIdx.x, teams = C::TEAMS * gridDim.x;   // few shares: one an SM first
@@ -284,12 +284,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], C::WARPS);
       }
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&q_full[s], 1);
-        mbar_init(&q_empty[s], C::WARPS);
-      }
-      mbar_init(&mrg[0], C::WARPS - 1);
-      mbar_init(&mrg[1], 1);
+      mbar_init(q_full, 1);
+      mbar_init(q_empty, C::WARPS);
+      mbar_init(&mrg[0], C::WARPS);
+      mbar_init(&mrg[1], C::WARPS);
       *abort_flag = 0;
       fence_mbarrier_init();
     }
@@ -327,16 +325,15 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
     while (!idle && ok && walk.next(x)) {
       // the item's query rows: those of a token lie side by side, lane j copies token j of the block
       {
-        const int qi = it & 1;
-        if (it >= 2 && !(ok = mbar_wait_warp(&q_empty[qi], ((it >> 1) - 1) & 1, abort_flag, 435))) break;
+        if (it >= 1 && !(ok = mbar_wait_warp(q_empty, (it - 1) & 1, abort_flag, 435))) break;
         const int row0 = x.rb * C::ROWS, row1 = min(x.nq * p.G, row0 + C::ROWS);
-        if (lane == 0) mbar_arrive_expect_tx(&q_full[qi], (row1 - row0) * D * 2);
+        if (lane == 0) mbar_arrive_expect_tx(q_full, (row1 - row0) * D * 2);
         __syncwarp();
         const int i = row0 / p.G + lane;
         const int a = max(row0, i * p.G), e = min(row1, (i + 1) * p.G);
         if (a < e)
-          bulk_load(smem + C::OFF_Q + qi * C::QBUF + (a - row0) * D * 2,
-                    p.q + (static_cast<size_t>(x.first + i) * p.H + x.hkv * p.G + (a - i * p.G)) * D, (e - a) * D * 2, &q_full[qi]);
+          bulk_load(smem + C::OFF_Q + (a - row0) * D * 2,
+                    p.q + (static_cast<size_t>(x.first + i) * p.H + x.hkv * p.G + (a - i * p.G)) * D, (e - a) * D * 2, q_full);
         ++it;
       }
       int window = -1, tab = 0;                              // 32 table entries from block ``window`` on
@@ -384,8 +381,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
       }
     }
     if (!ok) {
-      // drain the copies already issued (at most NST stages and two items' queries outstanding)
-      for (uint32_t y = (it > 2 ? it - 2 : 0); y < it; ++y) mbar_wait_warp(&q_full[y & 1], (y >> 1) & 1, nullptr, 436);
+      // drain the copies already issued (at most NST stages and an item's queries outstanding)
+      if (it > 0) mbar_wait_warp(q_full, (it - 1) & 1, nullptr, 436);
       for (uint32_t y = (g > C::NST ? g - C::NST : 0); y < g; ++y) mbar_wait_warp(&full[y % C::NST], (y / C::NST) & 1, nullptr, 431);
     }
   } else {
@@ -415,12 +412,12 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
       uint32_t qb[NT][C::KS][2];
       float2 fac[NT];
       int vis[NT][2];
-      if (!(ok = mbar_wait_warp(&q_full[it & 1], (it >> 1) & 1, abort_flag, 437))) break;
+      if (!(ok = mbar_wait_warp(q_full, it & 1, abort_flag, 437))) break;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = x.rb * C::ROWS + 8 * n + r;
         const int i = row / p.G;
-        const uint8_t* src = smem + C::OFF_Q + (it & 1) * C::QBUF + (8 * n + r) * D * 2 + c * (D / 2);
+        const uint8_t* src = smem + C::OFF_Q + (8 * n + r) * D * 2 + c * (D / 2);
         uint4 w[D / 32];
         float big = 0.f;
 #pragma unroll
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
         for (int k = 0; k < 2; ++k) vis[n][k] = min(x.key_end, __shfl_sync(0xffffffffu, seen, (2 * c + k) * 4));
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&q_empty[it & 1]);
+      if (lane == 0) mbar_arrive(q_empty);
       // m: reference, some number below every score before the first
       float2 m[NT], l[NT];
       float o[NT][C::MT][4];
@@ -609,9 +606,9 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
       }
       if (!ok) break;
 
-      // The warps' states of this stretch.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1).  Warps 1
-      // to 3 leave theirs in shared memory (position 16 t + 2 r (+1) of the merge row) and go on; warp 0
-      // adds them to its own and writes.
+      // The warps' states of this stretch.  o[n][t]: rows 2c, 2c + 1 at elements r d/8 + 2t (+1), which
+      // lie in shared memory at 16 t + 2 ((r + t) % 8) (+1) of the merge row (no bank twice, neither here
+      // nor below).  Each warp then adds up a quarter of the rows, in the order of the warps.
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -620,77 +617,69 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
           l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, off);
         }
       }
-      if (tw > 0) {
-        if (it > 0 && !(ok = mbar_wait_warp(&mrg[1], (it - 1) & 1, abort_flag, 434))) break;
+      if (it > 0 && !(ok = mbar_wait_warp(&mrg[1], (it - 1) & 1, abort_flag, 434))) break;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+      for (int n = 0; n < NT; ++n) {
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int at = (tw - 1) * C::ROWS + 8 * n + 2 * c + k;
+        for (int k = 0; k < 2; ++k) {
+          const int at = tw * C::ROWS + 8 * n + 2 * c + k;
 #pragma unroll
-            for (int t = 0; t < C::MT; ++t)
-              *reinterpret_cast<float2*>(merge + at * C::MROW + 16 * t + 2 * r) = make_float2(o[n][t][k], o[n][t][2 + k]);
-            if (r == 0) ml[at] = k ? make_float2(m[n].y, l[n].y) : make_float2(m[n].x, l[n].x);
-          }
+          for (int t = 0; t < C::MT; ++t)
+            *reinterpret_cast<float2*>(merge + at * C::MROW + 16 * t + 2 * ((r + t) & 7)) = make_float2(o[n][t][k], o[n][t][2 + k]);
+          if (r == 0) ml[at] = k ? make_float2(m[n].y, l[n].y) : make_float2(m[n].x, l[n].x);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mrg[0]);
-      } else {
-        if (!(ok = mbar_wait_warp(&mrg[0], it & 1, abort_flag, 433))) break;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int row = x.rb * C::ROWS + 8 * n + 2 * c + k;
-            float M = k ? m[n].y : m[n].x;
-            float2 st[C::WARPS - 1];
-#pragma unroll
-            for (int w = 0; w < C::WARPS - 1; ++w) {
-              st[w] = ml[w * C::ROWS + 8 * n + 2 * c + k];
-              M = fmaxf(M, st[w].x);
-            }
-            const float wt = fast_exp2((k ? m[n].y : m[n].x) - M);
-            float L = (k ? l[n].y : l[n].x) * wt;
-            float2 acc[C::MT];
-#pragma unroll
-            for (int t = 0; t < C::MT; ++t) acc[t] = make_float2(o[n][t][k] * wt, o[n][t][2 + k] * wt);
-#pragma unroll
-            for (int w = 0; w < C::WARPS - 1; ++w) {
-              const float wv = fast_exp2(st[w].x - M);
-              L = fmaf(wv, st[w].y, L);
-              const float* src = merge + (w * C::ROWS + 8 * n + 2 * c + k) * C::MROW + 2 * r;
-#pragma unroll
-              for (int t = 0; t < C::MT; ++t)
-                acc[t] = ffma2(make_float2(wv, wv), *reinterpret_cast<const float2*>(src + 16 * t), acc[t]);
-            }
-            if (row >= rows) continue;
-            const int i = row / p.G;
-            const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
-            const size_t th = static_cast<size_t>(tok) * p.H + head;
-            const bool none = L == 0.f;                        // a row that sees no key (scores that are no number: L is none)
-            if (x.out < 0) {
-              const float inv = none ? 0.f : p.descale_v / L;
-              uint32_t h[C::MT];
-#pragma unroll
-              for (int t = 0; t < C::MT; ++t) h[t] = none ? 0u : pack_bf16x2(acc[t].x * inv, acc[t].y * inv);
-              uint4* dst = reinterpret_cast<uint4*>(p.o + th * D + r * (D / 8));
-#pragma unroll
-              for (int t = 0; t < C::MT / 4; ++t) dst[t] = make_uint4(h[4 * t], h[4 * t + 1], h[4 * t + 2], h[4 * t + 3]);
-              if (r == 0)
-                p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
-                    none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-            } else {
-              const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + 8 * n + 2 * c + k;
-              float* dst = p.part + at * (D + 2);
-#pragma unroll
-              for (int t = 0; t < C::MT; ++t) *reinterpret_cast<float2*>(dst + r * (D / 8) + 2 * t) = acc[t];
-              if (r == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : M, L);
-            }
-          }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mrg[1]);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mrg[0]);
+      if (!(ok = mbar_wait_warp(&mrg[0], it & 1, abort_flag, 433))) break;
+      constexpr int QR = C::ROWS / C::WARPS;                   // a warp's rows
+      constexpr int PL = D / 64;                               // element pairs of a lane: lane + 32 i
+#pragma unroll
+      for (int y = 0; y < QR; ++y) {
+        const int rr = tw * QR + y, row = x.rb * C::ROWS + rr;
+        if (row >= rows) break;
+        float2 st[C::WARPS];
+        float M = kNone, L = 0.f;
+        float2 acc[PL];
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          st[w] = ml[w * C::ROWS + rr];
+          M = fmaxf(M, st[w].x);
+        }
+#pragma unroll
+        for (int i = 0; i < PL; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+          const float wt = fast_exp2(st[w].x - M);
+          L = fmaf(wt, st[w].y, L);
+#pragma unroll
+          for (int i = 0; i < PL; ++i) {
+            const int pr = lane + 32 * i, pt = pr % C::MT;     // (d/16 pairs of each r)
+            acc[i] = ffma2(make_float2(wt, wt), *reinterpret_cast<const float2*>(merge + (w * C::ROWS + rr) * C::MROW + 16 * pt + 2 * ((pr / C::MT + pt) & 7)), acc[i]);
+          }
+        }
+        const int i = row / p.G;
+        const int tok = x.first + i, head = x.hkv * p.G + (row - i * p.G);
+        const size_t th = static_cast<size_t>(tok) * p.H + head;
+        const bool none = L == 0.f;                            // a row that sees no key (scores that are no number: L is none)
+        if (x.out < 0) {
+          const float inv = none ? 0.f : p.descale_v / L;
+#pragma unroll
+          for (int k = 0; k < PL; ++k)
+            reinterpret_cast<uint32_t*>(p.o + th * D)[lane + 32 * k] = none ? 0u : pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
+          if (lane == 0)
+            p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
+                none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        } else {
+          const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + rr;
+          float* dst = p.part + at * (D + 2);
+#pragma unroll
+          for (int k = 0; k < PL; ++k) reinterpret_cast<float2*>(dst)[lane + 32 * k] = acc[k];
+          if (lane == 0) *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : M, L);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mrg[1]);
       ++it;
     }
   }
