@@ -136,9 +136,23 @@ constexpr int kQ4MinUnits = 1;
 struct Q4Share {
   long long total;                                            // T
   int n;                                                      // N
-  __device__ __forceinline__ long long begin(int i) const { return total * i / n; }
+  uint32_t each, rest;                                        // T / N (< 2^31: no team has more), T % N
+  __device__ __forceinline__ void set(long long t, int most) {
+    total = t;
+    n = static_cast<int>(max(1LL, min(static_cast<long long>(most), t / kQ4MinUnits)));
+    // (a 64-bit division is some hundred instructions, and this one stands before the first load of keys)
+    each = t < (1LL << 32) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(n) : static_cast<uint32_t>(t / n);
+    rest = static_cast<uint32_t>(t - static_cast<long long>(each) * n);
+  }
+  // T i / N
+  __device__ __forceinline__ long long begin(int i) const {
+    return static_cast<long long>(each) * i + rest * static_cast<uint32_t>(i) / static_cast<uint32_t>(n);
+  }
   // the team that has unit u
-  __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * n - 1) / total); }
+  __device__ __forceinline__ int owner(long long u) const {
+    const long long x = (u + 1) * n - 1;
+    return x < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(total)) : static_cast<int>(x / total);
+  }
 };
 
 // By a whole warp: the total, and the sequence that holds unit ``u_of(share)`` with the units before
@@ -148,17 +162,20 @@ __device__ __forceinline__ Q4Share q4_share(const Q4Params& p, int rows_per_bloc
                                             long long* before) {
   const int lane = threadIdx.x & 31;
   Q4Share sh;
-  long long mine = 0;
-  for (int i = lane; i < p.n_seqs; i += 32) mine += q4_seq(p, i, rows_per_block, report).units(p.H_kv);
+  long long mine = 0, own = 0;                                // of all the lane's sequences, of its first
+  for (int i = lane; i < p.n_seqs; i += 32) {
+    const long long v = q4_seq(p, i, rows_per_block, report).units(p.H_kv);
+    if (i == lane) own = v;
+    mine += v;
+  }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, off);
-  sh.total = mine;
-  sh.n = static_cast<int>(max(1LL, min(static_cast<long long>(grid), sh.total / kQ4MinUnits)));
+  sh.set(mine, grid);
   const long long u = u_of(sh);
   long long sum = 0;
   *b = -1;
   for (int base = 0; base < p.n_seqs && u >= 0; base += 32) {
-    const long long v = base + lane < p.n_seqs ? q4_seq(p, base + lane, rows_per_block, false).units(p.H_kv) : 0;
+    const long long v = base == 0 ? own : base + lane < p.n_seqs ? q4_seq(p, base + lane, rows_per_block, false).units(p.H_kv) : 0;
     long long inc = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -291,6 +308,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
       *abort_flag = 0;
       fence_mbarrier_init();
     }
+    if (lane < 2) tma_prefetch_desc(lane ? &p.tv : &p.tk);
     if (p.n_splits == 0) {
       int b;
       long long before = 0;
