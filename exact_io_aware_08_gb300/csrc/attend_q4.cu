@@ -719,14 +719,15 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
              lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
-// Joins the states of the row blocks that lie in several teams' shares: a block a row.
-template <int D, int NT>
+// Joins the states of the row blocks that lie in several teams' shares: WPR warps a row.
+template <int D, int NT, int WPR>
 __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int grid) {
   constexpr int ROWS = 8 * NT;
-  const int th = blockIdx.x;
-  const int tok = th / p.H, head = th - tok * p.H;
-  int b = tok, first, count;
-  if (p.cu_q) b = owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423);
+  const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const bool some = th < static_cast<long long>(p.total_q) * p.H;
+  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
+  int b = some ? tok : -1, first, count;
+  if (some && p.cu_q) b = owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423);
   int none;
   long long before = 0;
   // (the search is asked for nothing: the units before sequence b are counted here)
@@ -748,7 +749,7 @@ __global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_consta
     }
   }
   pdl_wait();
-  q4_join<D, 4>(st, p.o + static_cast<size_t>(th) * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)),
+  q4_join<D, WPR>(st, p.o + static_cast<size_t>(th) * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)),
              p.descale_v);
 }
 
@@ -797,9 +798,11 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_splits) return e;
-  const unsigned blocks = static_cast<unsigned>(static_cast<long long>(a.total_q) * a.H);
-  log_launch("attend_q4_join_kernel<D, NT>", blocks, 128, 0ull);
-  return launch_join(attend_q4_join_kernel<D, NT>, blocks, stream, p, C::TEAMS * grid);
+  const long long out_rows = static_cast<long long>(a.total_q) * a.H;
+  const int warps = q4_join_warps(out_rows);
+  const unsigned blocks = static_cast<unsigned>((out_rows * warps + 3) / 4);
+  log_launch("attend_q4_join_kernel<D, NT, WPR>", blocks, 128, 0ull);
+  return launch_join(warps == 1 ? attend_q4_join_kernel<D, NT, 1> : attend_q4_join_kernel<D, NT, 4>, blocks, stream, p, C::TEAMS * grid);
 }
 
 template <int D, int WPR>
@@ -821,7 +824,7 @@ cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
     else e = small ? launch_attend_q4_d<128, 1>(a, stream) : launch_attend_q4_d<128, 2>(a, stream);
   }
   if (e != cudaSuccess || a.n_splits <= 1) return e;
-  if (q4_join_warps(a.n_splits) == 1)
+  if (q4_join_warps(static_cast<long long>(a.total_q) * a.H) == 1)
     return a.d == 64 ? launch_attend_q4_merge<64, 1>(a, stream) : launch_attend_q4_merge<128, 1>(a, stream);
   return a.d == 64 ? launch_attend_q4_merge<64, 4>(a, stream) : launch_attend_q4_merge<128, 4>(a, stream);
 }

@@ -992,9 +992,10 @@ __global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_consta
 // Shares the items out to ``places`` (SMs, or pairs of them) at a time: all that fill them a whole
 // number of times run whole, what is left over is split so that it fills them once more (4x1024 tokens
 // over 16384 keys, 256 items on 76 pairs: 1010 us whole, 950 us with the last 28 in two parts).  A part
-// has at least 512 keys where nothing else runs (1x128 tokens over 8128 keys: 41 us against 45 with
-// 1024), else 1024 (8 prompts of up to 1024 tokens, 64 wide: 51 us whole, 62 us in parts of 640).
-// Returns the grid.
+// has at least 512 keys where nothing else runs (1x128 tokens over 4096 keys: 31 us, 35 with 1024), else
+// 1024 (8 prompts of up to 1024 tokens, 64 wide: 51 us whole, 62 us in parts of 640).  The states and
+// their join cost some 15 us, so that at least nine key steps have to be saved (of 64 items, 1024 keys:
+// 20 us whole, 29 in two; 2048 keys: 32 whole, 24 in four).  Returns the grid.
 static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int block_rows) {
   p.block_rows = block_rows;
   p.row_blocks = static_cast<int>((q4_rows(a.H, a.H_kv, a.max_seqlen_q) + block_rows - 1) / block_rows);
@@ -1004,7 +1005,7 @@ static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int
   if (a.n_splits) return items * a.n_splits;
   const int tail = static_cast<int>(items % places);
   const int s = tail ? min(places / tail, a.max_seqlen_k / (items < places ? 512 : 1024)) : 1;
-  if (s < 2) return items;
+  if (s < 2 || a.max_seqlen_k - a.max_seqlen_k / s < 9 * kQ4Step) return items;
   p.whole = static_cast<int>(items - tail);
   p.tail_splits = s;
   p.chunk = q4_chunk(a.max_seqlen_k, s);
@@ -1015,9 +1016,9 @@ template <int D>
 static cudaError_t launch_tail(const Q4TParams& p, long long grid, cudaStream_t stream) {
   if (p.tail_splits == 1) return cudaSuccess;
   const int rows = static_cast<int>((grid - p.whole) / p.tail_splits) * p.block_rows;
-  const int warps = q4_join_warps(p.tail_splits);
-  log_launch("attend_q4_tail_kernel<D, WPR>", rows / 4 * warps, 128, 0ull);
-  return launch_join(warps == 1 ? attend_q4_tail_kernel<D, 1> : attend_q4_tail_kernel<D, 4>, rows / 4 * warps, stream, p, rows);
+  const int warps = q4_join_warps(rows);
+  log_launch("attend_q4_tail_kernel<D, WPR>", rows * warps / 4, 128, 0ull);
+  return launch_join(warps == 1 ? attend_q4_tail_kernel<D, 1> : attend_q4_tail_kernel<D, 4>, rows * warps / 4, stream, p, rows);
 }
 
 static cudaError_t launch_attend_q4_pair(Q4TParams& p, const PagedQ4Args& a, cudaStream_t stream) {
