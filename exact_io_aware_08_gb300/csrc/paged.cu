@@ -24,7 +24,7 @@ struct AppendParams {
   const float *cos, *sin;                             // [n_positions, rotary/2]
   const int *cu, *seqlens, *table;
   long long q_stride, k_stride, v_stride;             // elements from one token to the next
-  int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, rotary, interleaved, n_positions;
+  int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, rotary, n_positions;
   int warps_per_token;
   float descale_k, descale_v;
 };
@@ -59,11 +59,12 @@ __device__ __forceinline__ void quantise16(const float (&f)[16], bool split, flo
     if (scale[h] != two >> 8) scale[h] = f32x2_to_e4m3(__fdiv_rn(a[h], six), 0.f) & 0xffu;
     const float sd = __fmul_rn(f16x2_to_f32(e4m3x2_to_f16(scale[h])).x, descale);
     const float inv = sd > 0.f ? __frcp_rn(sd) : 0.f;        // (a scale of 0: codes of 0 with x's signs)
-    const float2 up = make_float2(kUp, kUp), down = make_float2(kDown, kDown);
+    const float iu = __fmul_rn(inv, kUp), id = __fmul_rn(inv, kDown);
+    const float2 up = make_float2(iu, iu), down = make_float2(id, id);
     float y[8], z[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 q = fmul2(make_float2(f[8 * h + 2 * i], f[8 * h + 2 * i + 1]), make_float2(inv, inv));
+      const float2 q = make_float2(f[8 * h + 2 * i], f[8 * h + 2 * i + 1]);
       const float2 u = fmul2(q, up), v = fmul2(q, down);
       y[2 * i] = u.x; y[2 * i + 1] = u.y;
       z[2 * i] = v.x; z[2 * i + 1] = v.y;
@@ -77,7 +78,7 @@ __device__ __forceinline__ void quantise16(const float (&f)[16], bool split, flo
   }
 }
 
-template <int D, bool Q4, int U>
+template <int D, bool Q4, bool INTER, int U>
 __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParams p) {
   constexpr int L = D / 16;                       // lanes a head
   constexpr int SPW = 32 / L;                     // heads a warp takes at once
@@ -90,7 +91,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
   const int slots = p.H + 2 * p.H_kv;
   const int r16 = p.rotary / 16;
   const bool rotates = u < r16;
-  const bool split = rotates && !p.interleaved;
+  const bool split = rotates && !INTER;
 
   // the data does not depend on the token's place: loads first
   uint4 x0[U], x1[U];
@@ -120,16 +121,18 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
   }
   if (!place_of_token(p.table, p.max_blocks, p.block_size, p.num_blocks, b, len, pos, &page, &row, 402)) return;
 
-  float c[8], s[8];
+  float2 c[4], s[4], ns[4];                        // of the lane's pairs 2 i and 2 i + 1
   if (rotates) {
     const size_t at = static_cast<size_t>(pos) * (p.rotary / 2) + 8 * u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos + at) + i);
       const float4 e = __ldg(reinterpret_cast<const float4*>(p.sin + at) + i);
-      c[4 * i] = a.x; c[4 * i + 1] = a.y; c[4 * i + 2] = a.z; c[4 * i + 3] = a.w;
-      s[4 * i] = e.x; s[4 * i + 1] = e.y; s[4 * i + 2] = e.z; s[4 * i + 3] = e.w;
+      c[2 * i] = make_float2(a.x, a.y); c[2 * i + 1] = make_float2(a.z, a.w);
+      s[2 * i] = make_float2(e.x, e.y); s[2 * i + 1] = make_float2(e.z, e.w);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ns[i] = make_float2(-s[i].x, -s[i].y);
   }
 
 #pragma unroll
@@ -137,7 +140,7 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
     const int slot = (part * U + j) * SPW + lane / L;
     const bool is_q = slot < p.H, is_v = slot >= p.H + p.H_kv;
     const bool rot = rotates && !is_v;
-    const bool sp = rot && !p.interleaved;
+    const bool sp = rot && !INTER;
     const uint32_t in[8] = {x0[j].x, x0[j].y, x0[j].z, x0[j].w, x1[j].x, x1[j].y, x1[j].z, x1[j].w};
     float f[16];
 #pragma unroll
@@ -146,14 +149,17 @@ __global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParam
       f[2 * i + 1] = bf16_hi(in[i]);
     }
     if (rot) {
+      // two pairs at a time: their first sides A and second sides E, which lie in the lane's vectors 0
+      // and 1, or side by side
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        // pair i of the lane: vectors 0 and 1 hold its two sides, or they lie side by side
-        const float a = sp ? f[i] : f[2 * i];
-        const float e = sp ? f[8 + i] : f[2 * i + 1];
-        const float y1 = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(e, s[i]));
-        const float y2 = __fadd_rn(__fmul_rn(e, c[i]), __fmul_rn(a, s[i]));
-        if (sp) { f[i] = y1; f[8 + i] = y2; } else { f[2 * i] = y1; f[2 * i + 1] = y2; }
+      for (int i = 0; i < 4; ++i) {
+        constexpr int step = INTER ? 2 : 1;
+        const int a = INTER ? 4 * i : 2 * i, e = INTER ? 4 * i + 1 : 8 + 2 * i;
+        const float2 A = make_float2(f[a], f[a + step]), E = make_float2(f[e], f[e + step]);
+        const float2 y1 = fadd2(fmul2(A, c[i]), fmul2(E, ns[i]));
+        const float2 y2 = fadd2(fmul2(E, c[i]), fmul2(A, s[i]));
+        f[a] = y1.x; f[a + step] = y1.y;
+        f[e] = y2.x; f[e + step] = y2.y;
       }
     }
     const int v0 = sp ? u : 2 * u, v1 = sp ? u + r16 : 2 * u + 1;
@@ -259,17 +265,17 @@ __global__ void __launch_bounds__(kPagedThreads) gather_q4_kernel(const GatherPa
 // in 4 bits (with the reading back) 437, 291, 274, 354; 3 passes in 4 bits 66, 54, 83, 104.
 static bool few_passes(long long passes) { return passes < 152LL * 64; }
 
-template <int D, bool Q4, int U>
+template <int D, bool Q4, bool INTER, int U>
 static cudaError_t launch_append_u(AppendParams& p, long long passes, cudaStream_t stream) {
   p.warps_per_token = static_cast<int>((passes + U - 1) / U);
   const long long warps = static_cast<long long>(p.total) * p.warps_per_token;
   const long long grid = (warps + kPagedThreads / 32 - 1) / (kPagedThreads / 32);
-  log_launch(Q4 ? "append_kernel<D, true, U>" : "append_kernel<D, false, U>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
-  append_kernel<D, Q4, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
+  log_launch(Q4 ? "append_kernel<D, true, INTER, U>" : "append_kernel<D, false, INTER, U>", static_cast<unsigned long long>(grid), kPagedThreads, 0ull);
+  append_kernel<D, Q4, INTER, U><<<static_cast<unsigned>(grid), kPagedThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
-template <int D, bool Q4>
+template <int D, bool Q4, bool INTER>
 static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   AppendParams p{};
   p.q = static_cast<const uint16_t*>(a.q); p.k = static_cast<const uint16_t*>(a.k);
@@ -284,21 +290,26 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
   p.n_seqs = a.n_seqs; p.H = a.q ? a.H : 0; p.H_kv = a.H_kv; p.total = a.total;
   p.max_blocks = a.max_blocks; p.block_size = a.block_size; p.num_blocks = a.num_blocks;
-  p.rotary = a.rotary; p.interleaved = a.interleaved; p.n_positions = a.n_positions;
+  p.rotary = a.rotary; p.n_positions = a.n_positions;
   p.descale_k = a.descale_k; p.descale_v = a.descale_v;
   const int per_pass = 32 / (D / 16);
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;
-  if (few_passes(passes * p.total)) return launch_append_u<D, Q4, 1>(p, passes, stream);
+  if (few_passes(passes * p.total)) return launch_append_u<D, Q4, INTER, 1>(p, passes, stream);
   if constexpr (!Q4)
-    if (passes % 8 == 0) return launch_append_u<D, Q4, 8>(p, passes, stream);
-  if ((passes + 5) / 6 * 6 <= (passes + 2) / 3 * 3) return launch_append_u<D, Q4, 6>(p, passes, stream);
-  return launch_append_u<D, Q4, 3>(p, passes, stream);
+    if (passes % 8 == 0) return launch_append_u<D, Q4, INTER, 8>(p, passes, stream);
+  if ((passes + 5) / 6 * 6 <= (passes + 2) / 3 * 3) return launch_append_u<D, Q4, INTER, 6>(p, passes, stream);
+  return launch_append_u<D, Q4, INTER, 3>(p, passes, stream);
+}
+
+template <int D, bool Q4>
+static cudaError_t launch_append_q(const AppendArgs& a, cudaStream_t stream) {
+  return a.interleaved ? launch_append_d<D, Q4, true>(a, stream) : launch_append_d<D, Q4, false>(a, stream);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream) {
-  if (a.k_scales) return a.d == 64 ? launch_append_d<64, true>(a, stream) : launch_append_d<128, true>(a, stream);
-  return a.d == 64 ? launch_append_d<64, false>(a, stream) : launch_append_d<128, false>(a, stream);
+  if (a.k_scales) return a.d == 64 ? launch_append_q<64, true>(a, stream) : launch_append_q<128, true>(a, stream);
+  return a.d == 64 ? launch_append_q<64, false>(a, stream) : launch_append_q<128, false>(a, stream);
 }
 
 template <int D, int U>
