@@ -78,8 +78,9 @@ __device__ __forceinline__ void quantise16(const float (&f)[16], bool split, flo
   }
 }
 
+// (six passes in 4 bits: 124 registers without a limit, 242 against 234 us for 24 mixed sequences)
 template <int D, bool Q4, bool INTER, int U>
-__global__ void __launch_bounds__(kPagedThreads) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_kernel(const AppendParams p) {
   constexpr int L = D / 16;                       // lanes a head
   constexpr int SPW = 32 / L;                     // heads a warp takes at once
   const int lane = threadIdx.x & 31;
@@ -260,9 +261,10 @@ __global__ void __launch_bounds__(kPagedThreads) gather_q4_kernel(const GatherPa
 // A warp takes U passes of a token.  One where the passes are too few to fill the GPU twice over, so
 // that they spread (4 x 16 tokens of 96 heads: 3.3 against 4.2 us); else more, so that the search for
 // the token's place (four dependent loads) is shared and more bytes are in flight behind it.  How
-// many: 6, or 3 where that leaves fewer passes empty, or, in bf16 only, 8 where none is empty then.
-// Measured with 1, 3, 6 and 8: 4 x 4096 tokens of 24 passes in bf16 204, 141, 141, 134 us; 12 passes
-// in 4 bits (with the reading back) 437, 291, 274, 354; 3 passes in 4 bits 66, 54, 83, 104.
+// many: 6, or 3 where that leaves fewer passes empty, the one or two that there are, or, in bf16 only, 8
+// where none is empty then.  Measured: 4 x 4096 tokens of 24 passes in bf16 with 2, 3 and 8 126, 125,
+// 122 us; 12 passes in 4 bits (with the reading back) with 2, 3, 4 and 6 284, 269, 282, 242; 2 passes in
+// 4 bits with 2, 3 and 4 25, 29, 35.
 static bool few_passes(long long passes) { return passes < 152LL * 64; }
 
 template <int D, bool Q4, bool INTER, int U>
@@ -295,7 +297,8 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   const int per_pass = 32 / (D / 16);
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;
-  if (few_passes(passes * p.total)) return launch_append_u<D, Q4, INTER, 1>(p, passes, stream);
+  if (passes == 1 || few_passes(passes * p.total)) return launch_append_u<D, Q4, INTER, 1>(p, passes, stream);
+  if (passes == 2) return launch_append_u<D, Q4, INTER, 2>(p, passes, stream);
   if constexpr (!Q4)
     if (passes % 8 == 0) return launch_append_u<D, Q4, INTER, 8>(p, passes, stream);
   if ((passes + 5) / 6 * 6 <= (passes + 2) / 3 * 3) return launch_append_u<D, Q4, INTER, 6>(p, passes, stream);

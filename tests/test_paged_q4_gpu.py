@@ -54,6 +54,9 @@ APPENDS = [
     ([1] * 70, list(range(1, 71)), 16, 1, 64, 16, 64, True, 5, True),
     ([300, 1, 17], [900, 1025, 17], 7, 1, 128, 128, 96, False, 0, True),
     ([1500, 700, 3], [1500, 800, 30], 32, 8, 128, 64, 128, False, 2, True),
+    # enough tokens for several heads a warp: 1, 2, 3 and 8 rounds of them a token
+    ([9000, 801], [9000, 900], 2, 2, 64, 64, 64, True, 1, True), ([5000, 7], [5001, 7], 4, 2, 128, 32, 128, False, 0, False),
+    ([3300], [3300], 6, 3, 128, 64, 64, True, 1, True), ([1300], [1310], 16, 8, 128, 128, 128, True, 0, False),
 ]
 APPEND_IDS = [f"{len(c[0])}seqs_{sum(c[0])}tok_d{c[4]}_b{c[5]}_r{c[6]}{'i' if c[7] else ''}" for c in APPENDS]
 
