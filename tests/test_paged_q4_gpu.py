@@ -254,6 +254,9 @@ DECODES = [
     ([1000, 37, 513], 32, 8, 128, 16, 7), ([700], 5, 1, 128, 48, 0), ([257, 31], 12, 4, 64, 48, 2), ([640, 200], 9, 1, 128, 128, 0),
     ([500, 100], 16, 1, 64, 64, 4), ([333], 40, 2, 128, 32, 2), ([90, 1], 64, 1, 128, 16, 1), ([2000, 3], 8, 8, 128, 256, 64),
     ([4096, 4000], 3, 3, 64, 256, 0), ([0, 0], 4, 2, 128, 64, 2), ([1100], 200, 1, 128, 64, 0),
+    # rows of many states: few of them, and more than a thousand
+    ([9000], 8, 8, 128, 64, 0), ([6000, 0, 10], 4, 1, 64, 32, 0), ([5000] + [70, 0, 300, 1] * 9, 32, 2, 128, 16, 0),
+    ([700, 90] * 18, 32, 4, 64, 64, 20), ([3000, 17], 8, 2, 128, 64, 24),
 ]
 
 
@@ -286,7 +289,7 @@ FORWARDS = [
     ([256], [256], 4, 4, 128, 128, True, 1, 0), ([300, 20], [900, 20], 10, 2, 64, 64, True, 1, 0),
     ([1, 600], [3, 600], 4, 1, 128, 16, True, 0, 1), ([520], [1500], 8, 1, 64, 48, True, 5, 0),
     # row blocks that are split because they do not fill the SMs
-    ([300], [2500], 4, 1, 128, 64, True, 0, 1), ([200, 90], [2200, 1100], 4, 2, 64, 32, True, 0, 2), ([70, 0, 3], [3100, 40, 1030], 4, 2, 128, 48, False, 0, 0),
+    ([70], [5000], 4, 4, 128, 64, True, 0, 0), ([64], [9000], 4, 1, 64, 64, True, 0, 2), ([300], [2500], 4, 1, 128, 64, True, 0, 1), ([200, 90], [2200, 1100], 4, 2, 64, 32, True, 0, 2), ([70, 0, 3], [3100, 40, 1030], 4, 2, 128, 48, False, 0, 0),
 ]
 
 
@@ -313,22 +316,22 @@ def test_forward_q4(case):
     assert (o[cu[-1]:] == -7.25).all() and (lse[:, cu[-1]:] == -7.25).all()
 
 
-@pytest.mark.parametrize("n", [1, 40])
-def test_q4_attention_with_queries_of_any_size(n):
+@pytest.mark.parametrize("n,keys", [(1, 200), (40, 200), (1, 1500), (40, 900), (300, 900)])
+def test_q4_attention_with_queries_of_any_size(n, keys):
     """Rows of tiny, huge and zero queries beside ordinary ones: each keeps its own factor."""
     require_gpu()
-    lens, H, d, block = [200], 8, 128, 64
+    lens, H, d, block = [keys], 8, 128, 64
     cache, table, val = fill_cache(lens, 1, d, block, 3)
     q = normal((n, H, d), 4)
     for h, f in enumerate((1.0, 2.0 ** -40, 2.0 ** -120, 0.0, 2.0 ** 6, 2.0 ** 40, 2.0 ** -20, 1.0)):
         q[:, h] *= f
     q[0, 7, 3] = 300.0
-    o, lse = fa.forward_paged_q4(cuda(q), *cache, i32(table), i32([0, n]), i32(lens), n, 200, causal=False, descale_k=DK,
+    o, lse = fa.forward_paged_q4(cuda(q), *cache, i32(table), i32([0, n]), i32(lens), n, keys, causal=False, descale_k=DK,
                                  descale_v=DV)
     fa.fa_sync_status()
     rows = [0, 1, 2, 3, 4, 6, 7]
     for t in range(n):
-        want = P.attend(f64(q[t]), val["k"][0][:, 0], val["v"][0][:, 0], d ** -0.5, [200] * H)
+        want = P.attend(f64(q[t]), val["k"][0][:, 0], val["v"][0][:, 0], d ** -0.5, [keys] * H)
         check_attention(f64(o[t, rows]), f64(lse[rows, t]), [x[rows] for x in want])
         # scores of 2^40 leave one key: its value exactly, and the score itself for lse
         best = int(np.argmax(val["k"][0][:, 0] @ f64(q[t, 5])))
@@ -559,6 +562,110 @@ def test_gathered_prefix_feeds_the_varlen_forward():
 
 
 # ------------------------------------------------------------------------------------------- bad contents
+
+def test_captured_step_follows_the_lengths():
+    """A step (append, then attention) captured once and replayed as the sequences grow, beside the same
+    steps called one by one: the lengths are read on the device."""
+    require_gpu()
+    lens, H, H_kv, d, block, steps = [300, 0, 127, 900], 8, 2, 128, 64, 4
+    B, N = len(lens), 1024
+    cache, table, _ = fill_cache(lens, H_kv, d, block, 13)
+    pages = np.arange(B * 16, dtype=np.int32).reshape(B, 16)             # a pool of its own, sequence by sequence
+    pool = [torch.zeros(B * 16, H_kv, block, x.shape[3], dtype=torch.uint8, device="cuda") for x in cache]
+    for b, n in enumerate(lens):
+        for i in range(-(-n // block)):
+            for x, y in zip(pool, cache):
+                x[int(pages[b, i])] = y[int(table[b, i])]
+    other = [x.clone() for x in pool]
+    cos, sin = fa.rotary_tables(N, d, device="cuda")
+    cu, tab = i32(np.arange(B + 1)), i32(pages)
+    qkv = [cuda(normal((B, (H + 2 * H_kv) * d), 40 + i)) for i in range(steps)]
+
+    def step(x, pool, n):
+        q, k, v = (y.unflatten(1, (-1, d)) for y in x.split((H * d, H_kv * d, H_kv * d), 1))
+        q = fa.append_paged_q4(k, v, *pool, tab, cu, n, q=q, cos=cos, sin=sin, descale_k=DK, descale_v=DV)
+        return fa.decode_paged_q4(q[:, :, None], *pool, tab, n, N, descale_k=DK, descale_v=DV)
+
+    want, n = [], i32(lens)
+    for x in qkv:
+        n += 1
+        want.append(step(x, pool, n))
+    x, n = qkv[0].clone(), i32(lens)
+    step(x, [y.clone() for y in other], n + 1)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        n += 1
+        o, lse = step(x, other, n)
+    for i in range(steps):
+        x.copy_(qkv[i])
+        graph.replay()
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+    fa.fa_sync_status()
+    for y, z in zip(pool, other):
+        assert torch.equal(y, z)
+
+
+@pytest.mark.parametrize("n", [1, 4, 70])
+def test_calls_side_by_side(n):
+    """Calls on two streams at once, each with outputs and workspace of its own."""
+    require_gpu()
+    H, H_kv, d = 8, 2, 128
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls, want = [], []
+    for i in range(2):
+        lens = [3000 + 200 * i, 64, 900]
+        cache, table, _ = fill_cache(lens, H_kv, d, 64, 50 + i)
+        q = cuda(normal((3 * n, H, d), 60 + i))
+        calls.append((q, *cache, i32(table), i32(np.arange(4) * n), i32(lens), n, max(lens)))
+        want.append(fa.forward_paged_q4(*calls[i], descale_k=DK, descale_v=DV))
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got.append((i, fa.forward_paged_q4(*calls[i], descale_k=DK, descale_v=DV)))
+    torch.cuda.synchronize()
+    fa.fa_sync_status()
+    for i, (o, lse) in got:
+        assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+def test_pages_past_32_bits():
+    """The last pages of pools whose bytes and elements pass 2^32: the same as in a small pool."""
+    require_gpu()
+    H, H_kv, d, block, n, old = 16, 8, 128, 64, 70, 330
+    need = -(-(old + n) // block)
+    small, big = need, (2 ** 32 // (H_kv * block * d)) + need + 5              # bf16 elements past 2^32
+    cos, sin = fa.rotary_tables(old + n, d, device="cuda")
+    q, k, v = (cuda(normal((old + n, h, d), 70 + h)) for h in (H, H_kv, H_kv))
+    first, new = i32([0, old]), i32([0, n])
+    got = []
+    for pages in (small, big):
+        table = i32(np.arange(pages - need, pages)[None])
+        at = slice(pages - need, pages)
+        kc, vc = (torch.empty(pages, block, H_kv, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        for x, lens, part in ((first, [old], slice(0, old)), (new, [old + n], slice(old, None))):
+            fa.append_paged(k[part], v[part], kc, vc, table, x, i32(lens), q=q[part], cos=cos, sin=sin)
+        got.append([torch.cat([c[at].view(-1, H_kv, d)[:old + n] for c in (kc, vc)])])
+        del kc, vc
+    for pages in (small, 2 * big):                                             # code bytes past 2^32
+        table = i32(np.arange(pages - need, pages)[None])
+        cache = [torch.empty(pages, H_kv, block, m, dtype=torch.uint8, device="cuda") for m in (d // 2, d // 16, d // 2, d // 16)]
+        for x, lens, part in ((first, [old], slice(0, old)), (new, [old + n], slice(old, None))):
+            qo = fa.append_paged_q4(k[part], v[part], *cache, table, x, i32(lens), q=q[part], cos=cos, sin=sin, descale_k=DK, descale_v=DV)
+        more = dict(descale_k=DK, descale_v=DV)
+        out = list(fa.gather_paged_q4(*cache, table, i32([0, old + n]), i32([old + n]), old + n, **more))
+        out += fa.forward_paged_q4(qo, *cache, table, new, i32([old + n]), n, old + n, **more)
+        out += fa.forward_paged_q4(qo[:5].contiguous(), *cache, table, i32([0, 5]), i32([old + n]), 5, old + n, causal=False, **more)
+        out += fa.decode_paged_q4(qo[-1:, :, None], *cache, table, i32([old + n]), old + n, **more)
+        got.append(out)
+        del cache
+    fa.fa_sync_status()
+    for a, b in ((got[0], got[1]), (got[2], got[3])):
+        for x, y in zip(a, b):
+            assert x.isfinite().all() and torch.equal(x, y)
+
 
 @pytest.mark.parametrize("what", ["page", "minus", "short", "beyond", "position", "order", "end"])
 @pytest.mark.parametrize("q4", [False, True])
