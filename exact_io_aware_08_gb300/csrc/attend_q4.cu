@@ -26,8 +26,13 @@
 // Layout.  One CTA an SM, of three or four teams.  A team's four warps compute, 32 keys each of a
 // 128-key stage, 16 at a time; a fifth copies stages by TMA (codes, swizzled) and bulk copies (scales,
 // query rows) into a ring that runs on across work items, and its registers go to the others.  Each
-// team gets an equal share of all sequences' key steps (Q4Share), whatever their lengths; with an explicit split
-// count the items are (sequence, key head, row block, chunk).
+// team gets an equal share of all sequences' key steps (Q4Share), whatever their lengths; with an
+// explicit split count the items are (sequence, key head, row block, chunk).
+//
+// Measured: 64 x 32768 tokens, 4 query heads a key head: 384 us, 2.42 GB at 6.3 TB/s (93% of the copy
+// rate).  Short calls are bound by latencies: 4 us from the launch to the first keys (place in the work,
+// query rows, page table, stage: each waits for the last), 1.4 us a step, 1.3 to leave a row block, 3 for
+// the join behind; 1 x 1000 tokens 7.8 us.
 #include "fa_kernels.h"
 #include "q4.cuh"
 

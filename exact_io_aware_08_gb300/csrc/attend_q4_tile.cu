@@ -20,7 +20,14 @@
 // Tensor memory: S_0, S_1 (P_t over the first half of S_t), O_0, O_1.
 //
 // Unpacking costs about 1.6 instructions an element and is shared by 256 rows: some 400 issue slots of
-// each SM quarter a 128-key tile, beside some 1300 of the softmax and 2048 clocks of products.
+// each SM quarter a 128-key tile, and leaving it out (in a copy) changes no time.  What bounds the
+// kernels is each tile's chain: softmax (1250 to 1650 clocks), hand-over, 1024 clocks of its products,
+// landing of S; two tiles in flight (tensor memory is full) hide half of it.  A 128-key step of 256 rows
+// takes some 3400 clocks where its products alone take 2048.  Measured and not kept, us for 4 x 1024
+// tokens over 16384 keys with the forms of their day: two softmax threads a row 1312 against 1135; P
+// handed over in two halves 830 against 792; S in halves of 64 keys, two in flight a tile, 1434 against
+// 779 (their products issue at 91 clocks each instead of 50); part of the exponentials by polynomial 812
+// against 792.
 #include "fa_kernels.h"
 #include "q4.cuh"
 
@@ -609,7 +616,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
 // cores work on one product.  Tile t is 256 rows, 128 in each CTA, and each CTA holds half of the
 // other operand: 64 of a key tile's 128 keys for S, 64 of the 128 columns of V for O.  So each
 // unpacks half as much a row (K: its 64 keys whole, V: its half of every key), and the tensor core
-// reads half as much of it from each shared memory.
+// reads half as much of it from each shared memory.  4 x 1024 tokens over 16384 keys: 750 us, 910 by
+// CTAs of their own.
 //
 // The even CTA's warp 1 issues all products; the barriers it waits on are its own and both CTAs arrive
 // there, and a product's completion is signalled to both.

@@ -26,7 +26,7 @@ struct AppendParams {
   long long q_stride, k_stride, v_stride;             // elements from one token to the next
   int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, rotary, n_positions;
   int warps_per_token;
-  float descale_k, descale_v;
+  float descale_k, descale_v, one;
 };
 
 constexpr int kPagedThreads = 128;
@@ -122,6 +122,9 @@ __global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_ke
   }
   if (!place_of_token(p.table, p.max_blocks, p.block_size, p.num_blocks, b, len, pos, &page, &row, 402)) return;
 
+  // The sums are fma(product, 1, product) with a 1 that the compiler does not know: of mul.f32x2 and
+  // add.f32x2 it makes one fma although both carry .rn, and the product goes unrounded.
+  const float2 one = make_float2(p.one, p.one);
   float2 c[4], s[4], ns[4];                        // of the lane's pairs 2 i and 2 i + 1
   if (rotates) {
     const size_t at = static_cast<size_t>(pos) * (p.rotary / 2) + 8 * u;
@@ -157,8 +160,8 @@ __global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_ke
         constexpr int step = INTER ? 2 : 1;
         const int a = INTER ? 4 * i : 2 * i, e = INTER ? 4 * i + 1 : 8 + 2 * i;
         const float2 A = make_float2(f[a], f[a + step]), E = make_float2(f[e], f[e + step]);
-        const float2 y1 = fadd2(fmul2(A, c[i]), fmul2(E, ns[i]));
-        const float2 y2 = fadd2(fmul2(E, c[i]), fmul2(A, s[i]));
+        const float2 y1 = ffma2(fmul2(A, c[i]), one, fmul2(E, ns[i]));
+        const float2 y2 = ffma2(fmul2(E, c[i]), one, fmul2(A, s[i]));
         f[a] = y1.x; f[a + step] = y1.y;
         f[e] = y2.x; f[e + step] = y2.y;
       }
@@ -293,7 +296,7 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   p.n_seqs = a.n_seqs; p.H = a.q ? a.H : 0; p.H_kv = a.H_kv; p.total = a.total;
   p.max_blocks = a.max_blocks; p.block_size = a.block_size; p.num_blocks = a.num_blocks;
   p.rotary = a.rotary; p.n_positions = a.n_positions;
-  p.descale_k = a.descale_k; p.descale_v = a.descale_v;
+  p.descale_k = a.descale_k; p.descale_v = a.descale_v; p.one = 1.f;
   const int per_pass = 32 / (D / 16);
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;

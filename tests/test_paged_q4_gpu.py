@@ -167,6 +167,43 @@ def test_append_q4_and_gather(case):
         assert (x[c["owned"]:] == -7.25).all()
 
 
+@pytest.mark.parametrize("q4", [False, True])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("n,d,rotary", [(4000, 128, 128), (3, 128, 128), (2500, 64, 32)])
+def test_rotation_rounds_every_operation(n, d, rotary, inter, q4):
+    """The rotated queries (and bf16 keys) are those of separately rounded fp32 products and sums, bit for
+    bit: one product too few rounded would change one in some 2^16 of them."""
+    require_gpu()
+    H, H_kv, block = 16, 4, 64
+    nb, table = make_pages([n], block, 0, 5)
+    q, k, v = (cuda(normal((n, h, d), 90 + h)) for h in (H, H_kv, H_kv))
+    cos, sin = fa.rotary_tables(n, rotary, device="cuda")
+
+    def rotated(x):
+        y = x.float()
+        a, e = (slice(0, rotary, 2), slice(1, rotary, 2)) if inter else (slice(rotary // 2), slice(rotary // 2, rotary))
+        c, s = cos[:, None], sin[:, None]
+        x1, x2 = y[..., a].clone(), y[..., e].clone()
+        p, r = x1 * c, x2 * s
+        y[..., a] = p - r
+        p, r = x2 * c, x1 * s
+        y[..., e] = p + r
+        return y.to(torch.bfloat16)
+
+    args = (i32(table), i32([0, n]), i32([n]))
+    if q4:
+        cache = [torch.zeros(nb, H_kv, block, m, dtype=torch.uint8, device="cuda") for m in (d // 2, d // 16, d // 2, d // 16)]
+        qo = fa.append_paged_q4(k, v, *cache, *args, q=q, cos=cos, sin=sin, descale_k=DK, descale_v=DV, interleaved=inter)
+    else:
+        kc, vc = (torch.zeros(nb, block, H_kv, d, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        qo = fa.append_paged(k, v, kc, vc, *args, q=q, cos=cos, sin=sin, interleaved=inter)
+        pages = i32(table[0, :-(-n // block)]).long()
+        assert torch.equal(kc[pages].view(-1, H_kv, d)[:n], rotated(k))
+        assert torch.equal(vc[pages].view(-1, H_kv, d)[:n], v)
+    fa.fa_sync_status()
+    assert torch.equal(qo, rotated(q))
+
+
 def test_append_in_place_and_without_queries():
     """q_out may be q; without queries only keys and values move."""
     require_gpu()
