@@ -7,6 +7,10 @@ missing or a call is rejected, a ``FaError`` is raised.
 
 Convenience wrappers ``forward``, ``backward`` and ``decode`` allocate outputs with torch (the
 library itself never allocates).
+
+Serving over paged caches: ``append_paged`` and ``append_paged_q4`` rotate a step's queries and keys
+by position and put keys and values into the pages, ``decode_paged`` (bf16), ``decode_paged_q4`` and
+``forward_paged_q4`` (4 bits) attend over them, ``gather_paged_q4`` reads a 4-bit cache back.
 """
 from __future__ import annotations
 

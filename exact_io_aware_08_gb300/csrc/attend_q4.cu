@@ -84,7 +84,7 @@ struct Q4Params {
   const int *cu_q, *seqlens, *table;
   int n_seqs, H, H_kv, G, total_q, max_q, max_k, causal, num_blocks, block_size, max_blocks, piece;
   int n_splits, chunk, row_blocks, n_items;                   // n_splits 0: shares of equal length
-  float score, descale_v;                                     // scale * log2 e * descale_k
+  float score, descale_v, one;                                // scale * log2 e * descale_k; 1
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -563,11 +563,13 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
               o[n][i][3] *= alpha.y;
             }
           }
-          const float2 nm = make_float2(-m[n].x, -m[n].y);
+          // t - m as fma(t, 1, -m) with a 1 that the compiler does not know: t's product is not to go
+          // into an fma unrounded, where huge scores would leave their maximum's rounding in the exponent
+          const float2 nm = make_float2(-m[n].x, -m[n].y), one = make_float2(p.one, p.one);
           float2 w[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float2 y = fadd2(t[i], nm);
+            const float2 y = ffma2(t[i], one, nm);
             w[i] = make_float2(fast_exp2(y.x), fast_exp2(y.y));
             pb[i >> 1][n][i & 1] = transpose8x8(pack_f16x2(w[i].x, w[i].y));
           }
@@ -791,6 +793,7 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   p.n_items = static_cast<int>(pairs * a.n_splits);
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
+  p.one = 1.f;
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
@@ -802,7 +805,7 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   log_launch("attend_q4_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_splits) return e;
+  if (e != cudaSuccess || a.n_splits || steps <= 1) return e;   // (one unit a row block: none is divided)
   const long long out_rows = static_cast<long long>(a.total_q) * a.H;
   const int warps = q4_join_warps(out_rows);
   const unsigned blocks = static_cast<unsigned>((out_rows * warps + 3) / 4);

@@ -353,11 +353,12 @@ def test_forward_q4(case):
     assert (o[cu[-1]:] == -7.25).all() and (lse[:, cu[-1]:] == -7.25).all()
 
 
-@pytest.mark.parametrize("n,keys", [(1, 200), (40, 200), (1, 1500), (40, 900), (300, 900)])
-def test_q4_attention_with_queries_of_any_size(n, keys):
+@pytest.mark.parametrize("n,keys,d", [(1, 200, 128), (40, 200, 128), (1, 1500, 128), (4, 1500, 128), (40, 900, 128), (300, 900, 128),
+                                      (1, 1500, 64), (4, 1500, 64), (40, 900, 64)])
+def test_q4_attention_with_queries_of_any_size(n, keys, d):
     """Rows of tiny, huge and zero queries beside ordinary ones: each keeps its own factor."""
     require_gpu()
-    lens, H, d, block = [keys], 8, 128, 64
+    lens, H, block = [keys], 8, 64
     cache, table, val = fill_cache(lens, 1, d, block, 3)
     q = normal((n, H, d), 4)
     for h, f in enumerate((1.0, 2.0 ** -40, 2.0 ** -120, 0.0, 2.0 ** 6, 2.0 ** 40, 2.0 ** -20, 1.0)):
