@@ -11,6 +11,7 @@ import torch
 import exact_io_aware_08_gb300 as fa
 from oracle import paged as P
 from tests.gpu_common import cuda, poisoned, require_gpu
+from tests.test_canaries_gpu import Guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -600,6 +601,50 @@ def test_gathered_prefix_feeds_the_varlen_forward():
 
 
 # ------------------------------------------------------------------------------------------- bad contents
+
+@pytest.mark.parametrize("n_splits", [0, 1, 3, 12])
+@pytest.mark.parametrize("n,d", [(1, 128), (3, 64), (4, 128), (37, 64), (37, 128), (150, 128), (150, 64)])
+def test_everything_stays_in_bounds(n, d, n_splits):
+    """Pools, outputs and workspaces between guard bands, at sizes that fill no tile."""
+    require_gpu()
+    H, H_kv, block, lens = 10, 2, 48, [n + 700, n, n + 3001]
+    cu = np.arange(4) * n
+    total, N = 3 * n, max(lens)
+    nb, table = make_pages(lens, block, 0, 3)
+    pool = [Guarded((nb, H_kv, block, m), torch.uint8) for m in (d // 2, d // 16, d // 2, d // 16)]
+    for x in pool:
+        x.t.random_(0, 0x70)                                  # codes of any kind, scales that are numbers
+    q, k, v = (cuda(normal((total, h, d), h)) for h in (H, H_kv, H_kv))
+    cos, sin = fa.rotary_tables(N, d, device="cuda")
+    caches = [x.t for x in pool]
+    qo = Guarded((total, H, d), torch.bfloat16)
+    fa.fa_append_paged_q4(q, k, v, qo.t, *caches, cos, sin, i32(cu), i32(lens), i32(table), DK, DV)
+    ko, vo = (Guarded((total, H_kv, d), torch.bfloat16) for _ in "kv")
+    fa.fa_gather_paged_q4(*caches, ko.t, vo.t, i32(cu), i32(lens), i32(table), DK, DV)
+    o, lse = Guarded((total, H, d), torch.bfloat16), Guarded((H, total), torch.float32)
+    ws = Guarded((fa.fa_fwd_paged_q4_workspace_size(3, H, H_kv, total, n, N, d, n_splits),), torch.uint8)
+    fa.fa_fwd_paged_q4(qo.t, *caches, o.t, lse.t, i32(cu), i32(lens), i32(table), n, N, d ** -0.5, DK, DV, True, n_splits, ws.t)
+    fa.fa_sync_status()
+    for x, name in ((qo, "q"), (ko, "k"), (vo, "v"), (o, "o"), (lse, "lse")):
+        x.check(name)
+    for x in (*pool, ws):
+        x.check("pool or workspace", fully_written=False)
+    kc, vc = (Guarded((nb, block, H_kv, d), torch.bfloat16) for _ in "kv")
+    q2 = Guarded((total, H, d), torch.bfloat16)
+    fa.fa_append_paged(q, k, v, q2.t, kc.t, vc.t, cos, sin, i32(cu), i32(lens), i32(table))
+    fa.fa_sync_status()
+    q2.check("q")
+    for x in (kc, vc):
+        x.check("pool", fully_written=False)
+    if n == 1:
+        o, lse = Guarded((3, H, 1, d), torch.bfloat16), Guarded((3, H, 1), torch.float32)
+        ws = Guarded((fa.fa_decode_paged_q4_workspace_size(3, H, H_kv, N, d, n_splits),), torch.uint8)
+        fa.fa_decode_paged_q4(qo.t[:, :, None], *caches, o.t, lse.t, i32(table), i32(lens), N, d ** -0.5, DK, DV, n_splits, ws.t)
+        fa.fa_sync_status()
+        for x, name in ((o, "o"), (lse, "lse")):
+            x.check(name)
+        ws.check("workspace", fully_written=False)
+
 
 def test_captured_step_follows_the_lengths():
     """A step (append, then attention) captured once and replayed as the sequences grow, beside the same
