@@ -3,7 +3,7 @@
 //
 // These are the calls of a serving step, a few microseconds of GPU work each when the batch is small.
 // Checked and marshalled in Python a call took the host 18 us (append, 3 of them the launch) to 28 us
-// (decode: two launches, two outputs, a workspace), here 4.5 and 10.  The library's functions come from
+// (decode: two launches, two outputs, a workspace), here 4 and 8.  The library's functions come from
 // the handle of the libfa.so that the package has loaded (bind()), errors go up as the package's FaError.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
@@ -17,7 +17,8 @@
 #include <type_traits>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -199,20 +200,30 @@ struct Where {
   }
 };
 
+// (not through the dispatcher: 1.7 us a tensor)
 at::Tensor make(c10::IntArrayRef shape, c10::ScalarType type, int device) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device))));
+  return at::Tensor(at::detail::empty_cuda(shape, type, c10::Device(c10::kCUDA, static_cast<c10::DeviceIndex>(device)), std::nullopt));
 }
 
-// The caller's workspace, or one of ``need`` bytes where it has none of that size (``own``: allowed to).
-at::Tensor workspace(PyObject* o, size_t need, int device, bool own) {
-  at::Tensor ws;
-  if (given(o)) {
-    ws = tensor(o, "workspace");
-    if (!ws.is_cuda() || ws.get_device() != device || !ws.is_contiguous()) refuse("the workspace must be dense and on the cache's device");
+// The caller's workspace, or ``need`` bytes for the call where it has none of that size (``own``: allowed to).
+struct Workspace {
+  c10::DataPtr held;
+  void* ptr = nullptr;
+  size_t bytes = 0;
+  Workspace(PyObject* o, size_t need, int device, bool own) {
+    if (given(o)) {
+      const at::Tensor& t = tensor(o, "workspace");
+      if (!t.is_cuda() || t.get_device() != device || !t.is_contiguous()) refuse("the workspace must be dense and on the cache's device");
+      ptr = t.data_ptr();
+      bytes = t.nbytes();
+    }
+    if (own && need > 16 && bytes < need) {
+      held = c10::cuda::CUDACachingAllocator::get()->allocate(need);
+      ptr = held.get();
+      bytes = need;
+    }
   }
-  if (own && need > 16 && (!ws.defined() || ws.nbytes() < need)) ws = make({static_cast<int64_t>(need)}, at::kByte, device);
-  return ws;
-}
+};
 
 #define FA_BEGIN HANDLE_TH_ERRORS try {
 #define FA_END                  \
@@ -363,10 +374,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor lse = own && !given(a[6]) ? make({B, H, 1}, at::kFloat, c.device) : tensor(a[6], "lse");
   fa_bf16_t* po = dense<fa_bf16_t>(o, "o", at::kBFloat16, {B, H, 1, c.d}, c.device);
   float* pl = dense<float>(lse, "lse", at::kFloat, {B, H, 1}, c.device);
-  const at::Tensor ws = workspace(a[14], own ? lib.decode_q4_ws(b, h, hkv, max_k, d, splits) : 0, c.device, own);
+  const Workspace ws(a[14], own ? lib.decode_q4_ws(b, h, hkv, max_k, d, splits) : 0, c.device, own);
   done(lib.decode_q4(pq, c.k, c.ks, c.v, c.vs, po, pl, tab, lens, b, h, hkv, narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"),
                      narrow(c.blocks, "num_blocks"), max_k, d, scale, number(a[11], "descale_k"), number(a[12], "descale_v"), splits,
-                     ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0, on.stream));
+                     ws.ptr, ws.bytes, on.stream));
   return two(o, a[5], lse, a[6]);
   FA_END
 }
@@ -395,10 +406,10 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor lse = own && !given(a[6]) ? make({H, total}, at::kFloat, c.device) : tensor(a[6], "lse");
   fa_bf16_t* po = dense<fa_bf16_t>(o, "o", at::kBFloat16, {total, H, c.d}, c.device);
   float* pl = dense<float>(lse, "lse", at::kFloat, {H, total}, c.device);
-  const at::Tensor ws = workspace(a[17], own ? lib.fwd_q4_ws(s, h, hkv, t, max_q, max_k, d, splits) : 0, c.device, own);
+  const Workspace ws(a[17], own ? lib.fwd_q4_ws(s, h, hkv, t, max_q, max_k, d, splits) : 0, c.device, own);
   done(lib.fwd_q4(pq, c.k, c.ks, c.v, c.vs, po, pl, cu, lens, tab, s, h, hkv, t, max_q, narrow(table.size(1), "max_blocks"),
                   narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, d, scale, number(a[13], "descale_k"),
-                  number(a[14], "descale_v"), truth(a[15]) ? 1 : 0, splits, ws.defined() ? ws.data_ptr() : nullptr, ws.defined() ? ws.nbytes() : 0,
+                  number(a[14], "descale_v"), truth(a[15]) ? 1 : 0, splits, ws.ptr, ws.bytes,
                   on.stream));
   return two(o, a[5], lse, a[6]);
   FA_END
