@@ -65,7 +65,7 @@ struct Q4TCfg {
   static constexpr uint32_t REG_CTRL = 56, REG_SOFTMAX = 208, REG_UNPACK = 40;
   static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
   static constexpr float RESCALE = 8.f;
-  static constexpr uint32_t BAR_P = 3, BAR_P_THREADS = 128 + 32 + 32;
+  static constexpr uint32_t BAR_START = 1, BAR_P = 3, BAR_P_THREADS = 128 + 32 + 32;
 };
 
 struct Q4TParams {
@@ -315,6 +315,10 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
   const int lane = threadIdx.x & 31;
 
   const Q4TItem item = q4_tile_item(p, blockIdx.x);
+  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
+  // the copying warp's first 32 table entries, asked for before anything that decides which are used
+  int window = key0 / p.block_size, tab = 0;
+  if (warp == 0 && window + lane < p.max_blocks) tab = __ldg(p.table + static_cast<size_t>(item.b) * p.max_blocks + window + lane);
   const int rb = item.rb, hkv = item.hkv, b = item.b;
   int first = b, nq = 1;
   if (p.cu_q) {
@@ -337,7 +341,6 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
   // Row r of the sequence sees its first seen(r) keys; the item's keys are [key0, key_end), tile t
   // runs n_t[t] key tiles of 128.
   auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
-  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
   int n_t[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -366,11 +369,17 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
   pdl_launch_dependents();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  uint32_t tbase = 0;
+  if (warp == 0) {                                            // the copies begin at once
+    __syncwarp();
+    named_bar_arrive(C::BAR_START, C::THREADS);
+  } else {
+    if (warp == 1) tmem_alloc(tmem_slot, C::TMEM_COLS);
+    named_bar_sync(C::BAR_START, C::THREADS);
+    tc_fence_after();
+    tbase = *tmem_slot;
+  }
 
   if (warp < 4) {
     setmaxnreg_dec<C::REG_CTRL>();
@@ -378,13 +387,13 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
       // -------------------------------------------------------------- copies of codes and scales
       const int pieces = C::CKEYS / p.piece;
       bool ok = true;
-      int window = -1, tab = 0, g = 0;
+      int g = 0;
       const int n_st = 2 * n_max;                             // code stages (the last may hold no key)
       for (; ok && g < n_st; ++g) {
         const int s = g % C::NC, u = g / C::NC;
         const int kk = key0 + g * C::CKEYS;
         const int last = (min(kk + C::CKEYS, key_end) - 1) / p.block_size;
-        if (kk < key_end && (window < 0 || last >= window + 32)) {
+        if (kk < key_end && last >= window + 32) {
           window = kk / p.block_size;
           const int blk = window + lane;
           tab = blk <= (key_end - 1) / p.block_size ? __ldg(p.table + static_cast<size_t>(b) * p.max_blocks + blk) : 0;
@@ -649,6 +658,7 @@ struct Q4PCfg {
   static constexpr uint32_t T_S = 0, T_O = 256;
   static constexpr int THREADS = 512;
   static constexpr int UNPACK_WARPS = 4;
+  static constexpr uint32_t BAR_START = 1;
   static constexpr uint32_t REG_CTRL = 48, REG_SOFTMAX = 208, REG_UNPACK = 48;
   static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
 };
@@ -680,6 +690,10 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   const int rank = static_cast<int>(cluster_rank());
 
   const Q4TItem item = q4_tile_item(p, blockIdx.x >> 1);      // of 512 rows
+  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
+  // the copying warp's first 32 table entries, asked for before anything that decides which are used
+  int window = key0 / p.block_size, tab = 0;
+  if (warp == 0 && window + lane < p.max_blocks) tab = __ldg(p.table + static_cast<size_t>(item.b) * p.max_blocks + window + lane);
   const int rb = item.rb, hkv = item.hkv, b = item.b;
   int first = b, nq = 1;
   if (p.cu_q) {
@@ -700,7 +714,6 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   const int row0 = rb * 512;
   if (row0 >= rows) return;                                   // both CTAs, before any shared state
   auto seen = [&](int r) { return p.causal ? max(0, len - nq + min(r, rows - 1) / p.G + 1) : len; };
-  const int key0 = item.parts > 1 ? item.split * item.chunk : 0;
   int n_t[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -730,12 +743,19 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 1) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
   pdl_launch_dependents();
-  __syncthreads();
-  cluster_sync();                                             // barriers and tensor memory of both are there
-  tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
+  uint32_t tbase = 0;
+  if (warp == 0) {                                            // the copies, into this CTA, begin at once
+    __syncwarp();
+    named_bar_arrive(C::BAR_START, C::THREADS);
+    cluster_arrive();
+  } else {
+    if (warp == 1) tmem_alloc_pair(tmem_slot, C::TMEM_COLS);
+    named_bar_sync(C::BAR_START, C::THREADS);
+    cluster_sync();                                           // barriers and tensor memory of both are there
+    tc_fence_after();
+    tbase = *tmem_slot;
+  }
 
   if (warp < 4) {
     setmaxnreg_dec<C::REG_CTRL>();
@@ -743,12 +763,12 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
       // -------------------------------------------------------------- copies: K of this CTA's 64 keys, V of all 128
       const int kp = 64 / p.piece, vp = 128 / p.piece;        // at most 4 and 8 pieces: lanes 8 to 11, 0 to 7
       bool ok = true;
-      int window = -1, tab = 0, g = 0;
+      int g = 0;
       for (; ok && g < n_max; ++g) {
         const int s = g % C::NC, u = g / C::NC;
         const int kk = key0 + g * C::BN;                      // (< key_end)
         const int blk0 = kk / p.block_size;
-        if (window < 0 || blk0 + 8 >= window + 32) {
+        if (blk0 + 8 >= window + 32) {
           window = blk0;
           tab = window + lane <= (key_end - 1) / p.block_size
                     ? __ldg(p.table + static_cast<size_t>(b) * p.max_blocks + window + lane) : 0;
@@ -967,6 +987,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
   }
   __syncwarp();
   tc_fence_before();
+  if (warp == 0) cluster_wait();                              // (of the start)
   __syncthreads();
   cluster_sync();                                             // nothing of the other CTA reaches here any more
   if (warp == 1) {
