@@ -625,8 +625,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
 // cores work on one product.  Tile t is 256 rows, 128 in each CTA, and each CTA holds half of the
 // other operand: 64 of a key tile's 128 keys for S, 64 of the 128 columns of V for O.  So each
 // unpacks half as much a row (K: its 64 keys whole, V: its half of every key), and the tensor core
-// reads half as much of it from each shared memory.  4 x 1024 tokens over 16384 keys: 750 us, 910 by
-// CTAs of their own.
+// reads half as much of it from each shared memory.  4 x 1024 tokens over 16384 keys: 712 us, 789
+// by CTAs of their own.
 //
 // The even CTA's warp 1 issues all products; the barriers it waits on are its own and both CTAs arrive
 // there, and a product's completion is signalled to both.
@@ -659,7 +659,8 @@ struct Q4PCfg {
   static constexpr int THREADS = 512;
   static constexpr int UNPACK_WARPS = 4;
   static constexpr uint32_t BAR_START = 1;
-  static constexpr uint32_t REG_CTRL = 48, REG_SOFTMAX = 208, REG_UNPACK = 48;
+  // (4 x 1024 tokens over 16384 keys with 48, 208 and 48 719 us; with 56, 208, 40 712; with 72, 200, 40 764)
+  static constexpr uint32_t REG_CTRL = 56, REG_SOFTMAX = 208, REG_UNPACK = 40;
   static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
 };
 
