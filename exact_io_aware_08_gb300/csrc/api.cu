@@ -613,8 +613,8 @@ fa_status_t append(const void* q, const void* k, const void* v, void* q_out, voi
 }
 
 // Split count of a 4-bit attention call (0: the library shares the work out itself), or an error.
-fa_status_t q4_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int* n_splits) {
-  const long long items = fa::q4_items(n_seqs, H, H_kv, max_seqlen_q);
+fa_status_t q4_splits(int n_seqs, int H, int H_kv, int max_seqlen_q, int d, int* n_splits) {
+  const long long items = fa::q4_items(n_seqs, H, H_kv, max_seqlen_q, d);
   if (*n_splits > fa::kDecodeMaxSplits)
     return fail(FA_ERR_UNSUPPORTED, "n_splits=%d exceeds %d", *n_splits, fa::kDecodeMaxSplits);
   if (*n_splits < 0) *n_splits = 0;
@@ -631,7 +631,7 @@ size_t q4_workspace(int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q, 
   if (n_seqs < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
       (d != 64 && d != 128) || static_cast<long long>(total_q) * H >= (1LL << 31))
     return 0;
-  if (q4_splits(n_seqs, H, H_kv, max_seqlen_q, &n_splits) != FA_OK) return 0;
+  if (q4_splits(n_seqs, H, H_kv, max_seqlen_q, d, &n_splits) != FA_OK) return 0;
   return q4_part_bytes(total_q, H, H_kv, max_seqlen_q, d, n_splits);
 }
 
@@ -657,10 +657,10 @@ fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, 
   const float score = scale * 1.4426950408889634f * descale_k;
   if (!(score >= 1e-34f) || !(score <= 1e34f))
     return fail(FA_ERR_INVALID_ARG, "scale * descale_k must be in about [1e-34, 1e34] (got %g)", static_cast<double>(score));
-  if ((st = q4_splits(n_seqs, H, H_kv, max_seqlen_q, &n_splits)) != FA_OK) return st;
+  if ((st = q4_splits(n_seqs, H, H_kv, max_seqlen_q, d, &n_splits)) != FA_OK) return st;
   // key steps of a sequence are counted in an int, those of all of them over the shares too
-  if (fa::q4_items(1, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 31) ||
-      fa::q4_items(n_seqs, H, H_kv, max_seqlen_q) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 38))
+  if (fa::q4_items(1, H, H_kv, max_seqlen_q, d) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 31) ||
+      fa::q4_items(n_seqs, H, H_kv, max_seqlen_q, d) * (max_seqlen_k / fa::kQ4Step + 1) >= (1LL << 38))
     return fail(FA_ERR_UNSUPPORTED, "too many (key head, row block, key step) units");
   if (total_q == 0 || max_seqlen_q == 0) return FA_OK;
   if (!q || !k_codes || !k_scales || !v_codes || !v_scales || !o || !lse)

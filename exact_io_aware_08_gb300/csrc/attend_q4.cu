@@ -823,7 +823,7 @@ static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t str
 
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {
   cudaError_t e;
-  if (q4_use_tiles(a.H, a.H_kv, a.max_seqlen_q)) {
+  if (q4_use_tiles(a.H, a.H_kv, a.max_seqlen_q, a.d)) {
     e = launch_attend_q4_tile(a, stream);
   } else {
     // 8 rows suffice for up to 8 query heads a key head at one token; else 16 share the unpacked keys

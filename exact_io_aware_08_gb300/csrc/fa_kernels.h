@@ -243,12 +243,16 @@ inline size_t decode_part_bytes(int B, int H, int d, int n_splits) {
 // tokens) are computed 8 or 16 a CTA (attend_q4.cu), or 256 (attend_q4_tile.cu).
 constexpr int kQ4Rows = 16;
 constexpr int kQ4TileRows = 256;
-constexpr int kQ4TileMin = 64;
 inline long long q4_rows(int H, int H_kv, int max_seqlen_q) { return static_cast<long long>(H / H_kv) * max_seqlen_q; }
-inline bool q4_use_tiles(int H, int H_kv, int max_seqlen_q) { return q4_rows(H, H_kv, max_seqlen_q) >= kQ4TileMin; }
+// Tiles where there are more than two (d = 128) or three blocks of kQ4Rows rows, each of which unpacks
+// the keys anew.  16 sequences x 8 key heads, us by rows and by tiles: d = 128, 8000 keys, 32 rows 80 and 99,
+// 48 rows 116 and 99; d = 64, 4000 keys, 48 rows 45 and 49.
+inline bool q4_use_tiles(int H, int H_kv, int max_seqlen_q, int d) {
+  return q4_rows(H, H_kv, max_seqlen_q) > (d == 128 ? 2 : 3) * kQ4Rows;
+}
 // (sequence, key head, row block) items of a call
-inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q) {
-  const int per = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4TileRows : kQ4Rows;
+inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q, int d) {
+  const int per = q4_use_tiles(H, H_kv, max_seqlen_q, d) ? kQ4TileRows : kQ4Rows;
   return static_cast<long long>(n_seqs) * H_kv * ((q4_rows(H, H_kv, max_seqlen_q) + per - 1) / per);
 }
 // Without a split count (0): few rows are shared out to at most this many teams, and each keeps at most
@@ -257,7 +261,7 @@ inline long long q4_items(int n_seqs, int H, int H_kv, int max_seqlen_q) {
 constexpr int kQ4MaxShares = 4 * 152;
 constexpr int kQ4MaxTailRows = 152 * kQ4TileRows;
 inline size_t q4_auto_bytes(int H, int H_kv, int max_seqlen_q, int d) {
-  const size_t rows = q4_use_tiles(H, H_kv, max_seqlen_q) ? kQ4MaxTailRows : 2 * kQ4MaxShares * kQ4Rows;
+  const size_t rows = q4_use_tiles(H, H_kv, max_seqlen_q, d) ? kQ4MaxTailRows : 2 * kQ4MaxShares * kQ4Rows;
   return rows * (d + 2) * sizeof(float);
 }
 // Keys of a step, and of a chunk: whole steps.

@@ -326,6 +326,9 @@ FORWARDS = [
     ([129, 260], [129, 1000], 5, 1, 128, 32, True, 2, 5), ([150], [450], 12, 12, 128, 256, False, 1, 0),
     ([256], [256], 4, 4, 128, 128, True, 1, 0), ([300, 20], [900, 20], 10, 2, 64, 64, True, 1, 0),
     ([1, 600], [3, 600], 4, 1, 128, 16, True, 0, 1), ([520], [1500], 8, 1, 64, 48, True, 5, 0),
+    # on either side of the rows from which on tiles are used
+    ([8, 3], [300, 900], 8, 2, 128, 64, True, 0, 1), ([9, 2], [300, 900], 8, 2, 128, 64, True, 0, 1), ([12, 1], [700, 90], 8, 2, 64, 32, True, 0, 0),
+    ([13, 0], [700, 90], 8, 2, 64, 32, True, 3, 0),
     # row blocks that are split because they do not fill the SMs
     ([70], [5000], 4, 4, 128, 64, True, 0, 0), ([64], [9000], 4, 1, 64, 64, True, 0, 2), ([300], [2500], 4, 1, 128, 64, True, 0, 1), ([200, 90], [2200, 1100], 4, 2, 64, 32, True, 0, 2), ([70, 0, 3], [3100, 40, 1030], 4, 2, 128, 48, False, 0, 0),
 ]
@@ -603,7 +606,7 @@ def test_gathered_prefix_feeds_the_varlen_forward():
 # ------------------------------------------------------------------------------------------- bad contents
 
 @pytest.mark.parametrize("n_splits", [0, 1, 3, 12])
-@pytest.mark.parametrize("n,d", [(1, 128), (3, 64), (4, 128), (37, 64), (37, 128), (150, 128), (150, 64)])
+@pytest.mark.parametrize("n,d", [(1, 128), (3, 64), (4, 128), (8, 128), (37, 64), (37, 128), (150, 128), (150, 64)])
 def test_everything_stays_in_bounds(n, d, n_splits):
     """Pools, outputs and workspaces between guard bands, at sizes that fill no tile."""
     require_gpu()
