@@ -27,7 +27,9 @@
 // tokens over 16384 keys with the forms of their day: two softmax threads a row 1312 against 1135; P
 // handed over in two halves 830 against 792; S in halves of 64 keys, two in flight a tile, 1434 against
 // 779 (their products issue at 91 clocks each instead of 50); part of the exponentials by polynomial 812
-// against 792.
+// against 792; products of a step in one asm block 733 against 712.  And for up to 128 rows, both tiles of
+// a CTA over the same rows with the key tiles by turns: 118 against 99 us for 16 x 12 tokens over 8000
+// keys, and as fast as before at d = 64 (two K and two V tiles are too few for it).
 #include "fa_kernels.h"
 #include "q4.cuh"
 
@@ -455,7 +457,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
           tc_fence_after();
           if (n_t[0] > 0) issue_s(0, 0);
           if (n_t[1] > 0) issue_s(1, 0);
-          umma_commit_w(&k_empty[0]);
+          // (a tile is given back only where another follows in its place: no signal stays unawaited)
+          if (C::NS < n_max) umma_commit_w(&k_empty[0]);
         }
         for (int j = 0; j < n_max; ++j) {
 #pragma unroll
@@ -472,8 +475,8 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
             if (ok && j + 1 < n_t[t]) issue_s(t, j + 1);
           }
           if (ok) {
-            umma_commit_w(&v_empty[j % C::NS]);
-            if (j + 1 < n_max) umma_commit_w(&k_empty[(j + 1) % C::NS]);
+            if (j + C::NS < n_max) umma_commit_w(&v_empty[j % C::NS]);
+            if (j + 1 + C::NS < n_max) umma_commit_w(&k_empty[(j + 1) % C::NS]);
           }
         }
       }
