@@ -722,42 +722,75 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
   // rows behind the last sequence stay as they are
   const bool some = th < static_cast<long long>(total_q) * H && !(cu_q && tok >= __ldg(cu_q + n_seqs));
   pdl_wait();
-  q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0}, o + static_cast<size_t>(th) * D,
+  q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0}, WPR > 1 ? threadIdx.x >> 5 : 0, WPR, o + static_cast<size_t>(th) * D,
              lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
-// Joins the states of the row blocks that lie in several teams' shares: WPR warps a row.
-template <int D, int NT, int WPR>
-__global__ void __launch_bounds__(128) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int grid) {
+// Joins the states of the row blocks that lie in several teams' shares.  There are as many as there are
+// bounds between shares at most, so that a block looks for one: that of bound i + 1 if it is the first
+// within its row block, or, where there are fewer row blocks than that (``by_block``), row block i of
+// the most that there can be.  Its warps share the rows out.
+constexpr int kQ4JoinWarps = 16;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kQ4JoinWarps) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int teams, int by_block) {
   constexpr int ROWS = 8 * NT;
-  const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const bool some = th < static_cast<long long>(p.total_q) * p.H;
-  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
-  int b = some ? tok : -1, first, count;
-  if (some && p.cu_q) b = owner_of_token(p.cu_q, p.n_seqs, p.total_q, tok, &first, &count, 423);
-  int none;
-  long long before = 0;
-  // (the search is asked for nothing: the units before sequence b are counted here)
-  const Q4Share sh = q4_share(p, ROWS, grid, false, [](const Q4Share&) { return -1LL; }, &none, &before);
-  for (int i = threadIdx.x & 31; i < b; i += 32) before += q4_seq(p, i, ROWS, false).units(p.H_kv);
+  __shared__ Q4Item item;                                      // b, hkv, rb, first, nq; n in ``len``, first team in ``out``
+  const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (warp == 0) {
+    const int i = blockIdx.x;
+    const int want = by_block ? i / (p.H_kv * p.row_blocks) : -1;
+    int b;
+    long long before = 0;
+    const Q4Share sh = q4_share(p, ROWS, teams, false,
+                                [&](const Q4Share& y) { return !by_block && i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
+    if (by_block) {
+      // (the search was asked for nothing: the units before the sequence are counted here)
+      b = want;
+      before = 0;
+      for (int k = threadIdx.x; k < b; k += 32) before += q4_seq(p, k, ROWS, false).units(p.H_kv);
 #pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
-  Q4States st{p.part, 2 * ROWS * (D + 2), ROWS * (D + 2), 0};
-  if (b >= 0) {                                                // (else behind the last sequence: stays as it is)
-    const Q4Seq seq = q4_seq(p, b, ROWS, false);
-    if (seq.blocks > 0) {                                      // (else reported)
-      const int row = (tok - seq.first) * p.G + head % p.G;
-      const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
-      const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
-      if (c0 != c1) {                                          // (else its team wrote the result)
-        st.base += (static_cast<size_t>(2 * c0) * ROWS + row % ROWS) * (D + 2);
-        st.n = c1 - c0 + 1;
+      for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    if (threadIdx.x == 0) {
+      item.len = 0;
+      if (b >= 0) {
+        const Q4Seq seq = q4_seq(p, b, ROWS, false);
+        const long long u = by_block ? 0 : sh.begin(i + 1) - before;
+        const int pair = by_block ? i - want * p.H_kv * p.row_blocks : static_cast<int>(u / seq.steps);
+        if (pair < seq.blocks * p.H_kv) {
+          const long long u0 = before + static_cast<long long>(pair) * seq.steps;
+          const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
+          if (c0 != c1 && (by_block || c0 == i)) {             // (c0 == i: bound i + 1 is its first)
+            item.b = b;
+            item.hkv = pair % p.H_kv;
+            item.rb = pair / p.H_kv;
+            item.first = seq.first;
+            item.nq = seq.nq;
+            item.len = c1 - c0 + 1;
+            item.out = c0;
+          }
+        }
       }
     }
   }
+  __syncthreads();
   pdl_wait();
-  q4_join<D, WPR>(st, p.o + static_cast<size_t>(th) * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)),
-             p.descale_v);
+  if (item.len == 0) return;
+  const int row0 = item.rb * ROWS, rows = min(ROWS, item.nq * p.G - row0);
+  int wpr = warps;                                             // warps a row
+  while (wpr > 1 && wpr * rows > warps) wpr >>= 1;
+  const int at_once = warps / wpr;
+  for (int r0 = 0; r0 < rows; r0 += at_once) {
+    const int rr = r0 + warp / wpr;
+    const bool some = rr < rows;
+    const int row = row0 + (some ? rr : 0), i = row / p.G;
+    const int tok = item.first + i, head = item.hkv * p.G + (row - i * p.G);
+    const size_t th = static_cast<size_t>(tok) * p.H + head;
+    const Q4States st{p.part + (static_cast<size_t>(2 * item.out) * ROWS + rr) * (D + 2), 2 * ROWS * (D + 2), ROWS * (D + 2),
+                      some ? item.len : 0};
+    q4_join<D, kQ4JoinWarps>(st, warp, wpr, p.o + th * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th), p.descale_v);
+  }
 }
 
 static int q4_sm_count() {
@@ -806,18 +839,22 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_splits || steps <= 1) return e;   // (one unit a row block: none is divided)
-  const long long out_rows = static_cast<long long>(a.total_q) * a.H;
-  const int warps = q4_join_warps(out_rows);
-  const unsigned blocks = static_cast<unsigned>((out_rows * warps + 3) / 4);
-  log_launch("attend_q4_join_kernel<D, NT, WPR>", blocks, 128, 0ull);
-  return launch_join(warps == 1 ? attend_q4_join_kernel<D, NT, 1> : attend_q4_join_kernel<D, NT, 4>, blocks, stream, p, C::TEAMS * grid);
+  const int teams = C::TEAMS * grid;
+  const bool by_block = pairs < teams - 1;
+  const unsigned blocks = static_cast<unsigned>(by_block ? pairs : teams - 1);
+  // a warp a row, and many a row only where there are states for them: small blocks start sooner
+  const long long block_rows = min(static_cast<long long>(C::ROWS), q4_rows(a.H, a.H_kv, a.max_seqlen_q));
+  const bool many = block_rows > 8 || min(steps, teams / pairs) > 16;
+  const unsigned threads = 32 * (many ? kQ4JoinWarps : block_rows > 4 ? 8 : 4);
+  log_launch("attend_q4_join_kernel<D, NT>", blocks, threads, 0ull);
+  return launch_join(attend_q4_join_kernel<D, NT>, blocks, threads, stream, p, teams, by_block ? 1 : 0);
 }
 
 template <int D, int WPR>
 static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t stream) {
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.total_q) * a.H * WPR + 3) / 4);
   log_launch("attend_q4_merge_kernel<D, WPR>", blocks, 128, 0ull);
-  return launch_join(attend_q4_merge_kernel<D, WPR>, blocks, stream, static_cast<const float*>(a.part),
+  return launch_join(attend_q4_merge_kernel<D, WPR>, blocks, 128, stream, static_cast<const float*>(a.part),
                      static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.n_splits, a.descale_v);
 }
 

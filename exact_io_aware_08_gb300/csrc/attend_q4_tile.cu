@@ -1019,7 +1019,7 @@ __global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_consta
   const size_t th = static_cast<size_t>(tok) * p.H + head;
   pdl_wait();
   q4_join<D, WPR>({p.part + (x.state + row) * (D + 2), static_cast<size_t>(p.block_rows) * (D + 2), 0, some ? p.tail_splits : 0},
-             p.o + th * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th), p.descale_v);
+                  WPR > 1 ? threadIdx.x >> 5 : 0, WPR, p.o + th * D, p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th), p.descale_v);
 }
 
 // Shares the items out to ``places`` (SMs, or pairs of them) at a time: all that fill them a whole
@@ -1051,7 +1051,7 @@ static cudaError_t launch_tail(const Q4TParams& p, long long grid, cudaStream_t 
   const int rows = static_cast<int>((grid - p.whole) / p.tail_splits) * p.block_rows;
   const int warps = q4_join_warps(rows);
   log_launch("attend_q4_tail_kernel<D, WPR>", rows * warps / 4, 128, 0ull);
-  return launch_join(warps == 1 ? attend_q4_tail_kernel<D, 1> : attend_q4_tail_kernel<D, 4>, rows * warps / 4, stream, p, rows);
+  return launch_join(warps == 1 ? attend_q4_tail_kernel<D, 1> : attend_q4_tail_kernel<D, 4>, rows * warps / 4, 128, stream, p, rows);
 }
 
 static cudaError_t launch_attend_q4_pair(Q4TParams& p, const PagedQ4Args& a, cudaStream_t stream) {

@@ -119,14 +119,16 @@ struct Q4States {
   int n;
 };
 
-// Writes a row's result from its states (O~ [D], then reference and sum).  WPR warps of the block, the
-// whole of it, or one share a row: every WPR-th state each, eight in flight at a time (a load takes about a
-// microsecond here, so one warp that read 63 states one after the other took 30 us).
-template <int D, int WPR>
-__device__ __forceinline__ void q4_join(const Q4States& x, uint16_t* o, float* lse, float descale_v) {
+// Writes a row's result from its states (O~ [D], then reference and sum).  ``wpr`` warps share a row,
+// every wpr-th state each, eight in flight at a time (a load takes about a microsecond here, so one warp
+// that read 63 states one after the other took 30 us).  ``warp``: this warp in the block, of WARPS at most
+// (1: warps that have nothing to do with one another); called by all warps of the block.
+template <int D, int WARPS>
+__device__ __forceinline__ void q4_join(const Q4States& x, int warp, int wpr, uint16_t* o, float* lse, float descale_v) {
   constexpr int V = D / 64;                                    // pairs of elements a lane
   constexpr int AT_ONCE = 8;
-  const int lane = threadIdx.x & 31, w = WPR == 1 ? 0 : threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, w = WARPS == 1 ? 0 : warp % wpr;
+  if (WARPS == 1) wpr = 1;
   float M = -INFINITY, L = 0.f;
   float2 acc[V];
 #pragma unroll
@@ -140,11 +142,11 @@ __device__ __forceinline__ void q4_join(const Q4States& x, uint16_t* o, float* l
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = ffma2(make_float2(wt, wt), v[k], fmul2(acc[k], make_float2(alpha, alpha)));
   };
-  for (int i0 = w; i0 < x.n; i0 += WPR * AT_ONCE) {
+  for (int i0 = w; i0 < x.n; i0 += wpr * AT_ONCE) {
     float2 ml[AT_ONCE], v[AT_ONCE][V];
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) {
-      const int i = i0 + j * WPR;
+      const int i = i0 + j * wpr;
       ml[j] = make_float2(0.f, 0.f);
       if (i < x.n) {
         const float* st = x.base + i * x.stride + (i == 0 ? x.skip : 0);
@@ -156,21 +158,21 @@ __device__ __forceinline__ void q4_join(const Q4States& x, uint16_t* o, float* l
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) add(ml[j], v[j]);
   }
-  if constexpr (WPR > 1) {
-    __shared__ float2 ml_of[WPR], acc_of[WPR][V][32];
+  if constexpr (WARPS > 1) {
+    __shared__ float2 ml_of[WARPS], acc_of[WARPS][V][32];
+    __syncthreads();                                           // (the row before has been read)
     if (w > 0) {
-      if (lane == 0) ml_of[w] = make_float2(M, L);
+      if (lane == 0) ml_of[warp] = make_float2(M, L);
 #pragma unroll
-      for (int k = 0; k < V; ++k) acc_of[w][k][lane] = acc[k];
+      for (int k = 0; k < V; ++k) acc_of[warp][k][lane] = acc[k];
     }
     __syncthreads();
     if (w > 0) return;
-#pragma unroll
-    for (int i = 1; i < WPR; ++i) {
+    for (int i = 1; i < wpr; ++i) {
       float2 v[V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = acc_of[i][k][lane];
-      add(ml_of[i], v);
+      for (int k = 0; k < V; ++k) v[k] = acc_of[warp + i][k][lane];
+      add(ml_of[warp + i], v);
     }
   }
   if (x.n == 0) return;
@@ -189,10 +191,10 @@ inline int q4_join_warps(long long rows) { return rows <= 1024 ? 4 : 1; }
 // The join runs behind the chunks on the stream, but may start while their last CTAs run
 // (programmatic dependent launch): it reads lengths and boundaries, then waits for the states.
 template <typename... P, typename... A>
-static cudaError_t launch_join(void (*kernel)(P...), unsigned blocks, cudaStream_t stream, A... args) {
+static cudaError_t launch_join(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
