@@ -83,7 +83,8 @@ struct Q4Params {
   float *lse, *part;
   const int *cu_q, *seqlens, *table;
   int n_seqs, H, H_kv, G, total_q, max_q, max_k, causal, num_blocks, block_size, max_blocks, piece;
-  int n_splits, chunk, row_blocks, n_items;                   // n_splits 0: shares of equal length
+  int n_splits, chunk, row_blocks, n_items;                   // n_splits 0: shares of equal length,
+  int whole;                                                  // each of whole row blocks or not
   float score, descale_v, one;                                // scale * log2 e * descale_k; 1
 };
 
@@ -136,7 +137,7 @@ __device__ __forceinline__ Q4Seq q4_seq(const Q4Params& p, int b, int rows_per_b
 
 // The shares of equal length: team i of N takes units [T i / N, T (i + 1) / N) of the T units of all
 // sequences, key heads and row blocks in order, however long each sequence is.  N is all teams, or less
-// where a share would fall under kQ4MinUnits.
+// where a share would fall under kQ4MinUnits.  Of whole row blocks: those that begin in that stretch.
 constexpr int kQ4MinUnits = 1;
 struct Q4Share {
   long long total;                                            // T
@@ -257,7 +258,7 @@ struct Q4Walk {
     }
     const int pair = off / seq.steps;
     const int step0 = off - pair * seq.steps;
-    const int steps = min(left, seq.steps - step0);
+    const int steps = p.whole ? seq.steps : min(left, seq.steps - step0);
     x.b = b;
     x.hkv = pair % p.H_kv;
     x.rb = pair / p.H_kv;
@@ -333,7 +334,14 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
     walk.b = start[0];
     walk.off = start[1];
     walk.left = start[2];
-    if (walk.left > 0) walk.seq = q4_seq(p, walk.b, C::ROWS, false);
+    if (walk.left > 0) {
+      walk.seq = q4_seq(p, walk.b, C::ROWS, false);
+      if (p.whole) {
+        const int behind = walk.off % walk.seq.steps, skip = behind ? walk.seq.steps - behind : 0;
+        walk.off += skip;
+        walk.left -= skip;
+      }
+    }
   }
   Q4Item x;
 
@@ -827,18 +835,22 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   p.score = a.scale * 1.4426950408889634f * a.descale_k;
   p.descale_v = a.descale_v;
   p.one = 1.f;
+  const long long most = min(q4_sm_count(), kQ4MaxShares / C::TEAMS);
+  const long long steps = (static_cast<long long>(a.max_seqlen_k) + kQ4Step - 1) / kQ4Step;
+  // Short row blocks, and enough of them for a quarter of the teams, are not divided: the states and the
+  // join cost as much as some four steps (8 key heads, 512 tokens, 64 sequences 21 us, whole 17; 24, 18
+  // and 17; of 1000 tokens 38 sequences 21, whole 25).
+  p.whole = steps <= 1 || (steps <= 5 && 4 * pairs >= most * C::TEAMS) ? 1 : 0;
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
-  const long long most = min(q4_sm_count(), kQ4MaxShares / C::TEAMS);
-  const long long steps = (static_cast<long long>(a.max_seqlen_k) + kQ4Step - 1) / kQ4Step;
   // (a share is kQ4MinUnits long at least, and there are pairs * steps units at most)
   const long long want = a.n_splits ? p.n_items : pairs * max(1LL, steps) / kQ4MinUnits;
   const int grid = static_cast<int>(max(1LL, min(most, want)));
   log_launch("attend_q4_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_q4_kernel<D, NT><<<grid, C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.n_splits || steps <= 1) return e;   // (one unit a row block: none is divided)
+  if (e != cudaSuccess || a.n_splits || p.whole) return e;
   const int teams = C::TEAMS * grid;
   const bool by_block = pairs < teams - 1;
   const unsigned blocks = static_cast<unsigned>(by_block ? pairs : teams - 1);

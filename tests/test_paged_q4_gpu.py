@@ -295,6 +295,9 @@ DECODES = [
     # rows of many states: few of them, and more than a thousand
     ([9000], 8, 8, 128, 64, 0), ([6000, 0, 10], 4, 1, 64, 32, 0), ([5000] + [70, 0, 300, 1] * 9, 32, 2, 128, 16, 0),
     ([700, 90] * 18, 32, 4, 64, 64, 20), ([3000, 17], 8, 2, 128, 64, 24),
+    # short row blocks that are not divided, and just too long for it
+    ([640, 0, 1, 129, 500] * 10, 8, 4, 128, 64, 0), ([300, 0, 77] * 11, 40, 4, 64, 32, 0), ([641, 0, 1, 129, 500] * 10, 8, 4, 128, 64, 0),
+    ([0, 0, 0, 128] + [0] * 200, 2, 1, 128, 64, 0), ([600] + [0] * 200, 2, 1, 64, 64, 0),
 ]
 
 
@@ -329,6 +332,7 @@ FORWARDS = [
     # on either side of the rows from which on tiles are used
     ([8, 3], [300, 900], 8, 2, 128, 64, True, 0, 1), ([9, 2], [300, 900], 8, 2, 128, 64, True, 0, 1), ([12, 1], [700, 90], 8, 2, 64, 32, True, 0, 0),
     ([13, 0], [700, 90], 8, 2, 64, 32, True, 3, 0),
+    ([3, 1, 0, 4] * 20, [500, 1, 70, 4] * 20, 8, 2, 128, 64, True, 0, 3), ([1, 2] * 40, [600, 40] * 40, 4, 2, 64, 32, True, 0, 0),
     # row blocks that are split because they do not fill the SMs
     ([70], [5000], 4, 4, 128, 64, True, 0, 0), ([64], [9000], 4, 1, 64, 64, True, 0, 2), ([300], [2500], 4, 1, 128, 64, True, 0, 1), ([200, 90], [2200, 1100], 4, 2, 64, 32, True, 0, 2), ([70, 0, 3], [3100, 40, 1030], 4, 2, 128, 48, False, 0, 0),
 ]
