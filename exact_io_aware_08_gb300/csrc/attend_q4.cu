@@ -688,7 +688,8 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
 #pragma unroll
           for (int i = 0; i < PL; ++i) {
             const int pr = lane + 32 * i, pt = pr % C::MT;     // (d/16 pairs of each r)
-            acc[i] = ffma2(make_float2(wt, wt), *reinterpret_cast<const float2*>(merge + (w * C::ROWS + rr) * C::MROW + 16 * pt + 2 * ((pr / C::MT + pt) & 7)), acc[i]);
+            const float2 v = *reinterpret_cast<const float2*>(merge + (w * C::ROWS + rr) * C::MROW + 16 * pt + 2 * ((pr / C::MT + pt) & 7));
+            acc[i] = ffma2(make_float2(wt, wt), v, acc[i]);
           }
         }
         const int i = row / p.G;
@@ -730,8 +731,9 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
   // rows behind the last sequence stay as they are
   const bool some = th < static_cast<long long>(total_q) * H && !(cu_q && tok >= __ldg(cu_q + n_seqs));
   pdl_wait();
-  q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0}, WPR > 1 ? threadIdx.x >> 5 : 0, WPR, o + static_cast<size_t>(th) * D,
-             lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
+  q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0},
+                  WPR > 1 ? threadIdx.x >> 5 : 0, WPR, o + static_cast<size_t>(th) * D,
+                  lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
 // Joins the states of the row blocks that lie in several teams' shares.  There are as many as there are
