@@ -738,40 +738,46 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
 
 // Joins the states of the row blocks that lie in several teams' shares.  There are as many as there are
 // bounds between shares at most, so that a block looks for one: that of bound i + 1 if it is the first
-// within its row block, or, where there are fewer row blocks than that (``by_block``), row block i of
+// within its row block, or, where there are fewer row blocks than that (BY_BLOCK), row block i of
 // the most that there can be.  Its warps share the rows out.
 constexpr int kQ4JoinWarps = 16;
 
-template <int D, int NT>
-__global__ void __launch_bounds__(32 * kQ4JoinWarps) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int teams, int by_block) {
+template <int D, int NT, bool BY_BLOCK>
+__global__ void __launch_bounds__(32 * kQ4JoinWarps) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int teams) {
   constexpr int ROWS = 8 * NT;
   __shared__ Q4Item item;                                      // b, hkv, rb, first, nq; n in ``len``, first team in ``out``
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (warp == 0) {
     const int i = blockIdx.x;
-    const int want = by_block ? i / (p.H_kv * p.row_blocks) : -1;
-    int b;
-    long long before = 0;
-    const Q4Share sh = q4_share(p, ROWS, teams, false,
-                                [&](const Q4Share& y) { return !by_block && i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
-    if (by_block) {
-      // (the search was asked for nothing: the units before the sequence are counted here)
-      b = want;
-      before = 0;
-      for (int k = threadIdx.x; k < b; k += 32) before += q4_seq(p, k, ROWS, false).units(p.H_kv);
+    int b = BY_BLOCK ? i / (p.H_kv * p.row_blocks) : -1;
+    long long before = 0;                                      // units of the sequences before b
+    Q4Share sh;
+    if (BY_BLOCK) {
+      long long total = 0;
+      for (int k = threadIdx.x; k < p.n_seqs; k += 32) {
+        const long long v = q4_seq(p, k, ROWS, false).units(p.H_kv);
+        total += v;
+        if (k < b) before += v;
+      }
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+      for (int off = 16; off >= 1; off >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+      }
+      sh.set(total, teams);
+    } else {
+      sh = q4_share(p, ROWS, teams, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
     }
     if (threadIdx.x == 0) {
       item.len = 0;
       if (b >= 0) {
         const Q4Seq seq = q4_seq(p, b, ROWS, false);
-        const long long u = by_block ? 0 : sh.begin(i + 1) - before;
-        const int pair = by_block ? i - want * p.H_kv * p.row_blocks : static_cast<int>(u / seq.steps);
+        // (below 2^31 units a sequence)
+        const int pair = BY_BLOCK ? i - b * p.H_kv * p.row_blocks : static_cast<int>(sh.begin(i + 1) - before) / seq.steps;
         if (pair < seq.blocks * p.H_kv) {
           const long long u0 = before + static_cast<long long>(pair) * seq.steps;
           const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
-          if (c0 != c1 && (by_block || c0 == i)) {             // (c0 == i: bound i + 1 is its first)
+          if (c0 != c1 && (BY_BLOCK || c0 == i)) {             // (c0 == i: bound i + 1 is its first)
             item.b = b;
             item.hkv = pair % p.H_kv;
             item.rb = pair / p.H_kv;
@@ -860,8 +866,8 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   const long long block_rows = min(static_cast<long long>(C::ROWS), q4_rows(a.H, a.H_kv, a.max_seqlen_q));
   const bool many = block_rows > 8 || min(steps, teams / pairs) > 16;
   const unsigned threads = 32 * (many ? kQ4JoinWarps : block_rows > 4 ? 8 : 4);
-  log_launch("attend_q4_join_kernel<D, NT>", blocks, threads, 0ull);
-  return launch_join(attend_q4_join_kernel<D, NT>, blocks, threads, stream, p, teams, by_block ? 1 : 0);
+  log_launch("attend_q4_join_kernel<D, NT, BY_BLOCK>", blocks, threads, 0ull);
+  return launch_join(by_block ? attend_q4_join_kernel<D, NT, true> : attend_q4_join_kernel<D, NT, false>, blocks, threads, stream, p, teams);
 }
 
 template <int D, int WPR>
