@@ -8,9 +8,12 @@
 // operands with fp32 sums, and the descales go into the score factor and the last division.  A query
 // row is multiplied by a power of two that puts its largest element in [2^14, 2^15): in fp16 it keeps
 // bf16's 8 bits down to 2^-28 of that element, and the power goes into the row's score factor.
-// Weights are 2^(s - m) with a reference m at most 8 below the running maximum, so <= 2^8, rounded
-// to fp16 for the product with V: off by at most 2^-11 each, and independently, below the output's
-// own rounding to bf16; l sums the unrounded weights in fp32.
+// Weights are 2^(s - m) with a reference m 7 to 15 below the running maximum, so <= 2^15, rounded to
+// fp16 for the product with V: off by at most 2^-11 of themselves, and independently, or half of fp16's
+// smallest step, 2^-25, which is at most 2^-32 of the weight that the maximum has.  (A reference at the
+// maximum left fp16's upper half unused and lost what lies 2^-25 below a row's largest weight; keys that
+// many, behind one that draws most of the attention, add up.)  Bf16 weights would keep the range and
+// be off by 2^-9 each.  l sums the unrounded weights in fp32.
 //
 // What bounds it.  A key head's token is d + d/8 bytes (K and V), read once for up to kQ4Rows rows.
 // At HBM rate that is some 42 elements a clock and SM, so what counts is the work of unpacking: per
@@ -552,9 +555,10 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
             }
           }
           const float t0 = fmaxf(fmax3(t[0].x, t[1].x, t[2].x), t[3].x), t1 = fmaxf(fmax3(t[0].y, t[1].y, t[2].y), t[3].y);
-          if (__any_sync(0xffffffffu, t0 > m[n].x + 8.f || t1 > m[n].y + 8.f)) {
-            // a row's maximum grew by more than 2^8: move its reference
-            float2 top = make_float2(fmaxf(m[n].x, t0), fmaxf(m[n].y, t1));
+          if (__any_sync(0xffffffffu, t0 > m[n].x + (kQ4Lift + 8.f) || t1 > m[n].y + (kQ4Lift + 8.f))) {
+            // a row's largest weight grew past 2^15: move its reference to 7 below the maximum (for huge
+            // scores to what that rounds to, at most 8 below)
+            float2 top = make_float2(fmaxf(m[n].x, t0 - kQ4Lift), fmaxf(m[n].y, t1 - kQ4Lift));
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) {
               top.x = fmaxf(top.x, __shfl_xor_sync(0xffffffffu, top.x, off));
@@ -702,8 +706,7 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
           for (int k = 0; k < PL; ++k)
             reinterpret_cast<uint32_t*>(p.o + th * D)[lane + 32 * k] = none ? 0u : pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
           if (lane == 0)
-            p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
-                none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] = none ? -INFINITY : q4_lse(M, L);
         } else {
           const size_t at = p.n_splits ? th * p.n_splits + x.out : static_cast<size_t>(x.out) * C::ROWS + rr;
           float* dst = p.part + at * (D + 2);

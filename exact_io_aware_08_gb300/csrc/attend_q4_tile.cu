@@ -4,8 +4,8 @@
 // A CTA owns 256 rows of one key head, in two tiles of 128.  Rows are (query token, query head of the
 // group) pairs, token by token, so that a tile is full whatever the group's size, and the rows of a
 // token lie side by side in memory.  The mathematics is attend_q4.cu's: codes * scales are exact fp16
-// numbers, query rows are brought to fp16 by a power of two, weights 2^(s - m) <= 2^8 are rounded to
-// fp16, sums are fp32.
+// numbers, query rows are brought to fp16 by a power of two, weights <= 2^15 are rounded to fp16, sums
+// are fp32.  The reference m is at most 8 below the running maximum here, and weights are 2^(s - m + 7).
 //
 // Roles (512 threads, one CTA an SM):
 //   warp 0       copies codes and scales, 64 keys a stage, by bulk copies.
@@ -200,7 +200,7 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
       l *= alpha;
       m = cand;
     }
-    // s c2 - m c2 is off by the rounding of m c2: where that could matter the reference is taken off
+    // s c2 - m c2 + 7 is off by the rounding of 7 - m c2: where that could matter the reference is taken off
     // the scores first
     far = __any_sync(0xffffffffu, fabsf(m * c2) > 4096.f && m != -INFINITY);
     if (PLAIN && far) {
@@ -228,8 +228,8 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
 #pragma unroll
     for (int k = 0; k < 128; ++k) s[k] -= (m == -INFINITY) ? 0.f : m;
   }
-  const float ms = PLAIN ? (far ? 0.f : m * c2) : far || m == -INFINITY ? 0.f : m * c2;
-  const float2 c2v = make_float2(c2, c2), nms = make_float2(-ms, -ms);
+  const float up = far || (!PLAIN && m == -INFINITY) ? kQ4Lift : fmaf(-m, c2, kQ4Lift);
+  const float2 c2v = make_float2(c2, c2), nms = make_float2(up, up);
   float2 rs[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) rs[k] = make_float2(0.f, 0.f);
@@ -286,10 +286,10 @@ __device__ __forceinline__ void q4_store_row(const Q4TParams& p, uint32_t t_o, b
   }
   if (has) {
     if (dst)
-      *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : m * c2, l);
+      *reinterpret_cast<float2*>(dst + D) = make_float2(none ? -INFINITY : fmaf(m, c2, -kQ4Lift), l);
     else
       p.lse[p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : th] =
-          none ? -INFINITY : (fmaf(m, c2, log2f(l))) * 0.6931471805599453f;
+          none ? -INFINITY : fmaf(m, c2, log2f(l * 0x1p-7f)) * 0.6931471805599453f;
   }
 }
 

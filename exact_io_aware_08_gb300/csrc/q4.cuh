@@ -112,6 +112,17 @@ __device__ __forceinline__ bool place_of_token(const int* __restrict__ table, in
   return ok;
 }
 
+// Weights for the product with V are fp16.  Their reference lies so far below a row's maximum (at the last
+// time that it was moved: the maximum may since have grown by 8) that the largest is 2^7 to 2^15: a weight
+// 2^-21 of it keeps fp16's 11 bits, and what is lost of smaller ones is 2^-32 of it at most.
+constexpr float kQ4Lift = 7.f;
+
+// The log-sum-exp of a row: reference M, sum L of its weights.  (Their lift is taken off both first: the
+// logarithm of a large L has a coarse step.)
+__device__ __forceinline__ float q4_lse(float M, float L) {
+  return ((M + kQ4Lift) + log2f(L * 0x1p-7f)) * 0.6931471805599453f;
+}
+
 // A row's states: n of them, ``stride`` floats apart, the first one ``skip`` floats further on.  n = 0: no row.
 struct Q4States {
   const float* base;
@@ -181,7 +192,7 @@ __device__ __forceinline__ void q4_join(const Q4States& x, int warp, int wpr, ui
 #pragma unroll
   for (int k = 0; k < V; ++k)
     *reinterpret_cast<uint32_t*>(o + 64 * k + 2 * lane) = none ? 0u : pack_bf16x2(acc[k].x * inv, acc[k].y * inv);
-  if (lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  if (lane == 0) *lse = none ? -INFINITY : q4_lse(M, L);
 }
 
 // Warps a row: all four of a block while the rows are few enough to run side by side all the same

@@ -93,8 +93,9 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, seen):
     Returns (O [n, d], lse [n], bound_o [n, d], bound_lse [n]): the bounds on a result computed with
     fp32 scores and sums, weights rounded to fp16 and O to bf16:
       a score sums d products, each term off by at most (d + 2) 2^-24 of its size, so by e in all,
-      a weight by e^(2e) - 1 <= 2.2 e of itself, and by 2^-11 in fp16 or 2^-25 of the largest possible
-      reference weight 2^8 (fp16's smallest step), exponentials and logarithms by 2^-21 more.
+      a weight by e^(2e) - 1 <= 2.2 e of itself, and by 2^-11 in fp16 or half of fp16's smallest step,
+      2^-25, where the row's largest weight is 2^7 or more (2^-32 of that one), exponentials and
+      logarithms by 2^-21 more.
     """
     n, d = q.shape
     o, lse = np.zeros((n, d)), np.full(n, -np.inf)
@@ -111,7 +112,7 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, seen):
         lse[i] = top + np.log(l)
         err = (d + 4) * 2.0 ** -24 * scale * (np.abs(k[:m]) @ np.abs(q[i])).max() + 2.0 ** -21 + np.abs(s).max() * 2.0 ** -22
         weight = (e / l) @ np.abs(v[:m])
-        tiny = 2.0 ** -25 * np.abs(v[:m]).sum(0) / l
+        tiny = 2.0 ** -32 * np.abs(v[:m]).sum(0) / l
         bo[i] = 2.0 ** -8 * np.abs(o[i]) + (2.2 * err + 2.0 ** -11 + 2.0 ** -20) * weight + tiny + 1e-30
         bl[i] = 1.1 * err + 2.0 ** -21 + np.abs(lse[i]) * 2.0 ** -22
     return o, lse, bo, bl
