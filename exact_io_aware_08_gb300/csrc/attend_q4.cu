@@ -724,15 +724,32 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
   __syncthreads();
 }
 
-// Joins a row's chunks where the caller gave their count (part: [row][chunk]): WPR warps a row.
+// Whether packed token t is one of a sequence that the kernels above computed; by a whole warp.
+__device__ __forceinline__ bool q4_computed(const int* __restrict__ cu, int n_seqs, int total_q, int max_q, int t) {
+  auto has = [&](int b) {
+    const int first = __ldg(cu + b), end = __ldg(cu + b + 1);
+    return first >= 0 && first <= t && t < end && end <= total_q && end - first <= max_q;
+  };
+  if (has(search_owner(cu, n_seqs, t))) return true;
+  // in front of the first sequence or behind the last one, or boundaries that do not ascend, among which
+  // some sequence may be sound all the same
+  for (int b0 = 0; b0 < n_seqs; b0 += 32) {
+    const int b = b0 + (threadIdx.x & 31);
+    if (__any_sync(0xffffffffu, b < n_seqs && has(b))) return true;
+  }
+  return false;
+}
+
+// Joins a row's chunks where the caller gave their count (part: [row][chunk]): WPR warps a row.  Rows that
+// have no states stay as they are.
 template <int D, int WPR>
 __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __restrict__ part, uint16_t* __restrict__ o,
                                                              float* __restrict__ lse, const int* __restrict__ cu_q,
-                                                             int n_seqs, int H, int total_q, int n_splits, float descale_v) {
+                                                             int n_seqs, int H, int total_q, int max_q, int n_splits,
+                                                             float descale_v) {
   const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int tok = static_cast<int>(th / H), head = static_cast<int>(th - static_cast<long long>(tok) * H);
-  // rows behind the last sequence stay as they are
-  const bool some = th < static_cast<long long>(total_q) * H && !(cu_q && tok >= __ldg(cu_q + n_seqs));
+  const bool some = th < static_cast<long long>(total_q) * H && (!cu_q || q4_computed(cu_q, n_seqs, total_q, max_q, tok));
   pdl_wait();
   q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0},
                   WPR > 1 ? threadIdx.x >> 5 : 0, WPR, o + static_cast<size_t>(th) * D,
@@ -878,7 +895,8 @@ static cudaError_t launch_attend_q4_merge(const PagedQ4Args& a, cudaStream_t str
   const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.total_q) * a.H * WPR + 3) / 4);
   log_launch("attend_q4_merge_kernel<D, WPR>", blocks, 128, 0ull);
   return launch_join(attend_q4_merge_kernel<D, WPR>, blocks, 128, stream, static_cast<const float*>(a.part),
-                     static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.n_splits, a.descale_v);
+                     static_cast<uint16_t*>(a.o), a.lse, a.cu_q, a.n_seqs, a.H, a.total_q, a.max_seqlen_q,
+                     a.n_splits, a.descale_v);
 }
 
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream) {

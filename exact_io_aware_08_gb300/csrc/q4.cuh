@@ -71,14 +71,10 @@ __device__ __forceinline__ float2 f16x2_to_f32(uint32_t w) {
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
-// The sequence that owns packed token ``t``: the b with cu[b] <= t < cu[b+1], found by the whole
-// warp, 32 boundaries a step.  Returns -1 for a token at or behind cu[n_seqs] (a padding row), and
-// for boundaries that do not enclose it (which are reported).  Whatever the boundaries hold, b stays
-// in [0, n_seqs) and the search ends, since each step shrinks the range.
-__device__ __forceinline__ int owner_of_token(const int* __restrict__ cu, int n_seqs, int total, int t,
-                                              int* first, int* count, int where) {
+// The b with cu[b] <= t < cu[b+1] of ascending boundaries, found by the whole warp, 32 boundaries a
+// step.  Whatever they hold, b stays in [0, n_seqs) and the search ends, since each step shrinks the range.
+__device__ __forceinline__ int search_owner(const int* __restrict__ cu, int n_seqs, int t) {
   const int lane = threadIdx.x & 31;
-  const int end = __ldg(cu + n_seqs);
   int lo = 0, hi = n_seqs;
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
@@ -87,6 +83,16 @@ __device__ __forceinline__ int owner_of_token(const int* __restrict__ cu, int n_
     lo += __popc(__ballot_sync(0xffffffffu, before)) * step;
     hi = min(hi, lo + step);
   }
+  return lo;
+}
+
+// The sequence that owns packed token ``t``.  Returns -1 for a token at or behind cu[n_seqs] (a padding
+// row), and for boundaries that do not enclose it (which are reported).
+__device__ __forceinline__ int owner_of_token(const int* __restrict__ cu, int n_seqs, int total, int t,
+                                              int* first, int* count, int where) {
+  const int lane = threadIdx.x & 31;
+  const int end = __ldg(cu + n_seqs);
+  const int lo = search_owner(cu, n_seqs, t);
   const int a = __ldg(cu + lo), b = __ldg(cu + lo + 1);
   const bool padding = t >= end;
   if ((t == 0 && (end > total || end < 0)) || (!padding && (a > t || b <= t || a < 0 || b > total))) {

@@ -409,9 +409,10 @@ fa_status_t fa_decode_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, c
  * q, o: [total_q, H, d] packed, sequence b's n = cu_q[b+1] - cu_q[b] tokens at [cu_q[b], cu_q[b+1]);
  * lse: [H, total_q].  The keys are the sequence's seqlens_k[b] cached tokens, the step's own among them
  * (append them first).  causal: query i sees keys j <= seqlens_k[b] - n + i, that is the tokens up to
- * its own; else all.  A query that sees no key (n > seqlens_k[b]) gets O = 0, lse = -inf.  Rows at and
- * behind cu_q[n_seqs] are left as they are.  max_seqlen_q bounds the n (and sizes the launch); other
- * arguments and checks as for fa_decode_paged_q4, boundaries as for fa_fwd_varlen.
+ * its own; else all.  A query that sees no key (n > seqlens_k[b]) gets O = 0, lse = -inf.  Rows in front
+ * of cu_q[0] and rows at and behind cu_q[n_seqs] are left as they are.  max_seqlen_q bounds the n (and
+ * sizes the launch); other arguments and checks as for fa_decode_paged_q4, boundaries as for
+ * fa_fwd_varlen: the rows of a sequence whose boundaries are rejected are left as they are too.
  */
 size_t fa_fwd_paged_q4_workspace_size(int n_seqs, int H, int H_kv, int total_q, int max_seqlen_q,
                                       int max_seqlen_k, int d, int n_splits);

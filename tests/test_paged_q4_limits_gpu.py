@@ -6,7 +6,7 @@ import torch
 import exact_io_aware_08_gb300 as fa
 from oracle import paged as P
 from tests.gpu_common import cuda, require_gpu
-from tests.test_paged_q4_gpu import check_attention, f64, i32
+from tests.test_paged_q4_gpu import DK, DV, check_attention, f64, fill_cache, i32, normal
 
 pytestmark = pytest.mark.gpu
 
@@ -45,3 +45,55 @@ def test_one_key_draws_most_of_the_attention(n, d, n_splits):
     assert (np.abs(want[0]) > 2.0 ** -17).all()
     for t in range(n):
         check_attention(f64(o[t]), f64(lse[:, t]), want)
+
+
+@pytest.mark.parametrize("n_splits", [0, 1, 3])
+@pytest.mark.parametrize("what", ["front", "many", "end", "order", "sixty"])
+@pytest.mark.parametrize("n,d", [(3, 64), (4, 128), (12, 128), (70, 64), (70, 128), (200, 128)])
+def test_rows_without_a_sequence_stay_as_they_are(n, d, what, n_splits):
+    """Rows in front of the first boundary and rows of a sequence whose boundaries are rejected keep what
+    they held, whatever the split count and the workspace's contents; the other sequences get results."""
+    require_gpu()
+    H, H_kv, lens = 4, 2, [500, 900, 700]
+    if what == "sixty":                                # more boundaries than a warp looks at in one step
+        lens = [200 + i for i in range(60)]
+    B = len(lens)
+    cu, max_q = np.arange(B + 1) * n, n
+    total, sound = B * n, set(range(B))
+    if what == "front":
+        cu = cu + 5
+        total += 5
+    elif what == "many":
+        cu[2:] += 1
+        total, sound = total + 1, {0, 2}
+    elif what == "end":
+        cu[-1] += 1
+        max_q, sound = n + 1, {0, 1}
+    elif what == "order":
+        cu, sound = np.array([0, n, -5, 3 * n]), {0}
+        max_q = 3 * n
+    else:
+        cu[31:] += 1
+        total, sound = total + 1, set(range(B)) - {30}
+    cache, table, val = fill_cache(lens, H_kv, d, 64, 31)
+    q = normal((total, H, d), 32)
+    o = torch.full((total, H, d), -7.25, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((H, total), -7.25, device="cuda")
+    ws = torch.full((fa.fa_fwd_paged_q4_workspace_size(B, H, H_kv, total, max_q, 900, d, n_splits) // 4,), 3.0, device="cuda")
+    fa.fa_fwd_paged_q4(cuda(q), *cache, o, lse, i32(cu), i32(lens), i32(table), max_q, 900, d ** -0.5, DK, DV, True, n_splits, ws)
+    if what == "front":
+        fa.fa_sync_status()
+    else:
+        with pytest.raises(fa.FaError) as e:
+            fa.fa_sync_status()
+        assert e.value.status == 1
+    left = np.ones(total, bool)
+    for b in sorted(sound):
+        mine = slice(cu[b], cu[b + 1])
+        left[mine] = False
+        if b % 7 < 3:
+            m = cu[b + 1] - cu[b]
+            for h in range(H):
+                want = P.attend(f64(q[mine, h]), val["k"][b][:, h // 2], val["v"][b][:, h // 2], d ** -0.5, [lens[b] - m + i + 1 for i in range(m)])
+                check_attention(f64(o[mine, h]), f64(lse[h, mine]), want)
+    assert left.any() and (f64(o)[left] == -7.25).all() and (f64(lse)[:, left] == -7.25).all()
