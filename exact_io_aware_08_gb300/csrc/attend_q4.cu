@@ -38,6 +38,7 @@
 // the join behind; 1 x 1000 tokens 7.8 us.
 #include "fa_kernels.h"
 #include "q4.cuh"
+#include "q4_share.h"
 
 namespace fa {
 
@@ -137,32 +138,6 @@ __device__ __forceinline__ Q4Seq q4_seq(const Q4Params& p, int b, int rows_per_b
   x.steps = max(1, (x.len + kQ4Step - 1) / kQ4Step);
   return x;
 }
-
-// The shares of equal length: team i of N takes units [T i / N, T (i + 1) / N) of the T units of all
-// sequences, key heads and row blocks in order, however long each sequence is.  N is all teams, or less
-// where a share would fall under kQ4MinUnits.  Of whole row blocks: those that begin in that stretch.
-constexpr int kQ4MinUnits = 1;
-struct Q4Share {
-  long long total;                                            // T
-  int n;                                                      // N
-  uint32_t each, rest;                                        // T / N (< 2^31: no team has more), T % N
-  __device__ __forceinline__ void set(long long t, int most) {
-    total = t;
-    n = static_cast<int>(max(1LL, min(static_cast<long long>(most), t / kQ4MinUnits)));
-    // (a 64-bit division is some hundred instructions, and this one stands before the first load of keys)
-    each = t < (1LL << 32) ? static_cast<uint32_t>(t) / static_cast<uint32_t>(n) : static_cast<uint32_t>(t / n);
-    rest = static_cast<uint32_t>(t - static_cast<long long>(each) * n);
-  }
-  // T i / N
-  __device__ __forceinline__ long long begin(int i) const {
-    return static_cast<long long>(each) * i + rest * static_cast<uint32_t>(i) / static_cast<uint32_t>(n);
-  }
-  // the team that has unit u
-  __device__ __forceinline__ int owner(long long u) const {
-    const long long x = (u + 1) * n - 1;
-    return x < (1LL << 32) ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(total)) : static_cast<int>(x / total);
-  }
-};
 
 // By a whole warp: the total, and the sequence that holds unit ``u_of(share)`` with the units before
 // it (b = -1 where there is none).

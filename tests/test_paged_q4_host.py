@@ -1,6 +1,7 @@
 """Refusals of the paged-cache operators, through the C ABI and through the package: all of them
 before anything is launched, so they run without a GPU."""
 import math
+import subprocess
 
 import pytest
 import torch
@@ -156,3 +157,43 @@ def test_rotary_tables_are_exact_far_out():
     for i in (0, 1, 31):
         a = 100000 * 10000.0 ** (-2 * i / 64)
         assert abs(cos[100000, i].item() - math.cos(a)) < 2 ** -24 and abs(sin[100000, i].item() - math.sin(a)) < 2 ** -24
+
+
+SHARES = """
+#include <cstdio>
+#include <cstdlib>
+#include "q4_share.h"
+int main(int argc, char** argv) {
+  fa::Q4Share s;
+  s.set(atoll(argv[1]), atoi(argv[2]));
+  printf("%d", s.n);
+  for (int i = 0; i <= s.n; ++i) printf(" %lld", s.begin(i));
+  printf("\\n");
+  for (int a = 3; a < argc; ++a) printf("%d ", s.owner(atoll(argv[a])));
+}
+"""
+
+
+@pytest.fixture(scope="module")
+def shares(tmp_path_factory):
+    at = tmp_path_factory.mktemp("shares")
+    (at / "shares.cpp").write_text(SHARES)
+    subprocess.run(["g++", "-std=c++17", "-I" + fabuild.CSRC, "-o", str(at / "shares"), str(at / "shares.cpp")], check=True)
+    return str(at / "shares")
+
+
+@pytest.mark.parametrize("total", [1, 5, 607, 608, 609, 10 ** 6 + 7, 2 ** 32 // 608, 2 ** 31 - 1, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 1,
+                                   2 ** 33 + 12345, 2 ** 36 + 99, 2 ** 38 - 1])
+@pytest.mark.parametrize("teams", [1, 3, 456, 608])
+def test_shares_cover_every_unit_once(shares, total, teams):
+    """Team i has units [T i // N, T (i + 1) // N), whatever T is, and owner() names it."""
+    n = max(1, min(teams, total))
+    if total // n >= 2 ** 31:
+        pytest.skip("more units a team than the calls allow")
+    begin = [total * i // n for i in range(n + 1)]
+    units = sorted({min(total - 1, max(0, b + k)) for b in begin for k in (-1, 0, 1)} | {total // 3, total // 2})
+    out = subprocess.run([shares, str(total), str(teams), *map(str, units)], capture_output=True, text=True, check=True).stdout
+    first, second = out.split("\n")[:2]
+    assert [int(x) for x in first.split()] == [n, *begin]
+    want = [next(i for i in range(n) if begin[i] <= u < begin[i + 1]) for u in units]
+    assert [int(x) for x in second.split()] == want
