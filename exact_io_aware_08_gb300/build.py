@@ -3,7 +3,7 @@
 Each translation unit is compiled in parallel with nvcc, then linked into
 ``exact_io_aware_08_gb300/libfa.so`` (git-ignored); the extension module is compiled beside them with
 g++ against the installed torch's headers.  Rebuilds only when a source or header is newer than what
-it makes.  Usage: ``python -m exact_io_aware_08_gb300.build [--force] [-v]``.
+it makes.  Usage: ``python -m exact_io_aware_08_gb300.build [--force] [-v] [--no-binding]``.
 """
 from __future__ import annotations
 
@@ -76,9 +76,20 @@ def build_binding() -> str:
     return BINDING
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date() and binding_up_to_date():
-        return LIB
+def build(force: bool = False, verbose: bool = False, extra_flags=(), binding: bool = True) -> str:
+    """Build what is out of date.  ``binding=False``: libfa.so alone, which needs no torch.  A module that
+    does not compile is an error, but libfa.so is made all the same."""
+    lib_stale = force or not up_to_date()
+    with concurrent.futures.ThreadPoolExecutor(max_workers=1) as ex:
+        module = ex.submit(lambda: None if not force and binding_up_to_date() else build_binding()) if binding else None
+        if lib_stale:
+            _build_library(verbose, extra_flags)
+    if module is not None:
+        module.result()
+    return LIB
+
+
+def _build_library(verbose, extra_flags):
     nvcc = _nvcc()
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = _sources()
@@ -93,22 +104,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stderr, file=sys.stderr)
         return obj
 
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
-        binding = None if not force and binding_up_to_date() else ex.submit(build_binding)
-        objs = [] if not force and up_to_date() else list(ex.map(compile_one, srcs))
-        if binding is not None:
-            binding.result()
-    if not objs:
-        return LIB
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        objs = list(ex.map(compile_one, srcs))
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
-    build(force="--force" in sys.argv, verbose="-v" in sys.argv)
+    build(force="--force" in sys.argv, verbose="-v" in sys.argv, binding="--no-binding" not in sys.argv)
     print(LIB)
