@@ -340,11 +340,12 @@ def _binding():
     if _native is None:
         import importlib.machinery
         import importlib.util
-        import torch  # noqa: F401  (the module needs its libraries)
+        from .build import binding_path
         lib = load_library()
-        path = os.path.join(_HERE, "_binding.so")
+        path = binding_path()                        # (which has loaded torch: the module needs its libraries)
         if not os.path.exists(path):
-            raise FaError(4, f"{path} not found: build it with `python -m exact_io_aware_08_gb300.build`")
+            raise FaError(4, f"{path} not found: build it with `python -m exact_io_aware_08_gb300.build`"
+                             " (it is built for one torch and one Python)")
         loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_binding", path, loader=loader))
         loader.exec_module(module)

@@ -1,4 +1,4 @@
-"""Build libfa.so in-tree from csrc/*.cu for sm_103a, and _binding.so from csrc/binding.cpp.
+"""Build libfa.so in-tree from csrc/*.cu for sm_103a, and the extension module from csrc/binding.cpp.
 
 Each translation unit is compiled in parallel with nvcc, then linked into
 ``exact_io_aware_08_gb300/libfa.so`` (git-ignored); the extension module is compiled beside them with
@@ -19,7 +19,6 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
-BINDING = os.path.join(HERE, "_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -51,8 +50,16 @@ def up_to_date() -> bool:
     return _newer(LIB, _deps())
 
 
+def binding_path() -> str:
+    """Where the extension module lies.  It is made of torch's C++ classes and Python's: its name says of
+    which, so that another torch or Python finds none and has it built."""
+    import torch
+    made_of = f"{sys.implementation.cache_tag}-torch{torch.__version__}-abi{int(torch._C._GLIBCXX_USE_CXX11_ABI)}"
+    return os.path.join(HERE, f"_binding-{made_of}.so")
+
+
 def binding_up_to_date() -> bool:
-    return _newer(BINDING, [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.abspath(__file__)])
+    return _newer(binding_path(), [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.abspath(__file__)])
 
 
 def build_binding() -> str:
@@ -65,15 +72,16 @@ def build_binding() -> str:
     include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
     lib = os.path.join(home, "lib")
-    tmp = BINDING + ".tmp"
+    path = binding_path()
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", "-o", tmp, BINDING_SOURCE,
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + i for i in include), "-L" + lib,
            "-Wl,-rpath," + lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python", "-ldl"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr}")
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=(), binding: bool = True) -> str:

@@ -2,7 +2,9 @@
 import os
 
 import pytest
+import torch
 
+import exact_io_aware_08_gb300 as fa
 from exact_io_aware_08_gb300 import build as fabuild
 
 
@@ -33,3 +35,20 @@ def test_the_library_alone(elsewhere, monkeypatch):
     monkeypatch.setattr(fabuild, "binding_up_to_date", wanted)
     assert fabuild.build(binding=False) == str(elsewhere / "libfa.so")
     assert fabuild.up_to_date()
+
+
+def test_another_torch_finds_no_module(monkeypatch):
+    """The module is made of one torch's C++ classes: with another it is out of date, and not loaded."""
+    fabuild.build()
+    assert fabuild.binding_up_to_date()
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert not fabuild.binding_up_to_date()
+    monkeypatch.setattr(fa, "_native", None)
+    with pytest.raises(fa.FaError, match="not found"):
+        fa._binding()
+
+
+def test_another_python_finds_no_module(monkeypatch):
+    path = fabuild.binding_path()
+    monkeypatch.setattr(fabuild.sys.implementation, "cache_tag", "cpython-999")
+    assert fabuild.binding_path() != path and "cpython-999" in fabuild.binding_path()
