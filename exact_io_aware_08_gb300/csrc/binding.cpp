@@ -79,7 +79,15 @@ struct Shape {
   char text[96];
   explicit Shape(c10::IntArrayRef s) {
     int n = snprintf(text, sizeof text, "[");
-    for (size_t i = 0; i < s.size() && n < 80; ++i) n += snprintf(text + n, sizeof text - n, "%s%lld", i ? ", " : "", static_cast<long long>(s[i]));
+    // (a size has 19 digits at most: 21 characters with the comma before it, and the bracket and the 0 behind)
+    const int room = static_cast<int>(sizeof text) - 23 - 5;
+    for (size_t i = 0; i < s.size(); ++i) {
+      if (n > room) {
+        n += snprintf(text + n, sizeof text - n, ", ...");
+        break;
+      }
+      n += snprintf(text + n, sizeof text - n, "%s%lld", i ? ", " : "", static_cast<long long>(s[i]));
+    }
     snprintf(text + n, sizeof text - n, "]");
   }
 };

@@ -197,3 +197,14 @@ def test_shares_cover_every_unit_once(shares, total, teams):
     assert [int(x) for x in first.split()] == [n, *begin]
     want = [next(i for i in range(n) if begin[i] <= u < begin[i + 1]) for u in units]
     assert [int(x) for x in second.split()] == want
+
+
+def test_messages_hold_any_shape(lib):
+    """The sizes in a refusal's text end where its room does."""
+    t = tensors()
+    for lead in range(8, 17):
+        for digits in (1, 2, 5, 18):
+            shape = (0,) + (1000,) * lead + (10 ** digits,) * 3
+            wrong = torch.empty(0, dtype=torch.uint8).as_strided(shape, (0,) * len(shape))
+            with pytest.raises(fa.FaError, match=r"block_size, d/2\], is \[0, 1000, .*(\.\.\.|0)\]$"):
+                fa.decode_paged_q4(t["q"][:2, :, None], wrong, t["ks"], t["kc"], t["ks"], t["table"], t["lens"], 16)
