@@ -174,7 +174,14 @@ float number(PyObject* o, const char* name) {
   return static_cast<float>(v);
 }
 
-bool truth(PyObject* o) { return PyObject_IsTrue(o) == 1; }
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {                                                  // (several elements, say)
+    PyErr_Clear();
+    refuse("%s must be true or false, is %s", name, Py_TYPE(o)->tp_name);
+  }
+  return v == 1;
+}
 
 // Where a call runs: on ``device``, and on its current stream (None) or on a stream that is given by its
 // handle or as an object that has one.  What the call allocates then belongs to that stream, as under
@@ -300,7 +307,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, device);
   const int ints[] = {narrow(seqs, "n_seqs"), narrow(H, "H"), narrow(heads, "H_kv"), narrow(total, "total"), narrow(table.size(1), "max_blocks"),
                       narrow(block_size, "block_size"), narrow(blocks, "num_blocks"), narrow(d, "d"), narrow(2 * half, "rotary_dim"),
-                      truth(a[15]) ? 1 : 0, narrow(positions, "n_positions")};
+                      truth(a[15], "interleaved") ? 1 : 0, narrow(positions, "n_positions")};
   if (q4)
     done(lib.append_q4(pq, pk, pv, po, static_cast<fa_e2m1x2_t*>(kc), ks, static_cast<fa_e2m1x2_t*>(vc), vs, cos, sin, cu, lens, tab, ints[0],
                        ints[1], ints[2], ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10],
@@ -365,7 +372,7 @@ PyObject* gather(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_BEGIN
   count(n, 17);
-  const bool own = truth(a[16]);
+  const bool own = truth(a[16], "own");
   Cache4 c(a[1], a[2], a[3], a[4]);
   const at::Tensor& q = ranked(a[0], "q", 4, "[B, H, 1, d]");
   const at::Tensor& table = ranked(a[7], "block_table", 2, "[B, max_blocks]");
@@ -395,7 +402,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
 PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_BEGIN
   count(n, 20);
-  const bool own = truth(a[19]);
+  const bool own = truth(a[19], "own");
   Cache4 c(a[1], a[2], a[3], a[4]);
   const at::Tensor& q = ranked(a[0], "q", 3, "[total_q, H, d]");
   const at::Tensor& table = ranked(a[9], "block_table", 2, "[n_seqs, max_blocks]");
@@ -417,7 +424,7 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Workspace ws(a[17], own ? lib.fwd_q4_ws(s, h, hkv, t, max_q, max_k, d, splits) : 0, c.device, own);
   done(lib.fwd_q4(pq, c.k, c.ks, c.v, c.vs, po, pl, cu, lens, tab, s, h, hkv, t, max_q, narrow(table.size(1), "max_blocks"),
                   narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, d, scale, number(a[13], "descale_k"),
-                  number(a[14], "descale_v"), truth(a[15]) ? 1 : 0, splits, ws.ptr, ws.bytes,
+                  number(a[14], "descale_v"), truth(a[15], "causal") ? 1 : 0, splits, ws.ptr, ws.bytes,
                   on.stream));
   return two(o, a[5], lse, a[6]);
   FA_END

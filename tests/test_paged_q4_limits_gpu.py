@@ -97,3 +97,20 @@ def test_rows_without_a_sequence_stay_as_they_are(n, d, what, n_splits):
                 want = P.attend(f64(q[mine, h]), val["k"][b][:, h // 2], val["v"][b][:, h // 2], d ** -0.5, [lens[b] - m + i + 1 for i in range(m)])
                 check_attention(f64(o[mine, h]), f64(lse[h, mine]), want)
     assert left.any() and (f64(o)[left] == -7.25).all() and (f64(lse)[:, left] == -7.25).all()
+
+
+def test_flags_that_are_neither_true_nor_false():
+    """Two truth values as one: refused as an argument, with nothing launched or written."""
+    require_gpu()
+    cache, table, _ = fill_cache([40], 2, 64, 16, 5)
+    q, t, n = cuda(normal((1, 4, 64), 1)), i32(table), i32([40])
+    before = [x.clone() for x in cache]
+    for two in (torch.tensor([True, False]), np.array([1, 0])):
+        with pytest.raises(fa.FaError, match="causal must be true or false") as e:
+            fa.forward_paged_q4(q, *cache, t, i32([0, 1]), n, 1, 40, causal=two)
+        assert e.value.status == 1
+        with pytest.raises(fa.FaError, match="interleaved must be true or false") as e:
+            fa.append_paged_q4(q[:, :2], q[:, :2], *cache, t, i32([0, 1]), n, interleaved=two)
+        assert e.value.status == 1
+    fa.fa_sync_status()
+    assert all(torch.equal(x, y) for x, y in zip(cache, before))
