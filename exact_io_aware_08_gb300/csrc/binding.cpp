@@ -211,7 +211,10 @@ struct Where {
       PyErr_Clear();
       refuse("a stream's handle must be an address");
     }
-    other.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(device)));
+    // (cudaStreamLegacy is torch's default stream, whose handle is 0; of other odd handles there are none)
+    cudaStream_t handle = static_cast<cudaStream_t>(stream);
+    if (handle == cudaStreamLegacy) handle = nullptr;
+    other.reset_stream(c10::cuda::getStreamFromExternal(handle, static_cast<c10::DeviceIndex>(device)));
   }
 };
 

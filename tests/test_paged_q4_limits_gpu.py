@@ -57,7 +57,7 @@ def test_rows_without_a_sequence_stay_as_they_are(n, d, what, n_splits):
     H, H_kv, lens = 4, 2, [500, 900, 700]
     if what == "sixty":                                # more boundaries than a warp looks at in one step
         lens = [200 + i for i in range(60)]
-    B = len(lens)
+    B, N = len(lens), max(lens)
     cu, max_q = np.arange(B + 1) * n, n
     total, sound = B * n, set(range(B))
     if what == "front":
@@ -79,8 +79,8 @@ def test_rows_without_a_sequence_stay_as_they_are(n, d, what, n_splits):
     q = normal((total, H, d), 32)
     o = torch.full((total, H, d), -7.25, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((H, total), -7.25, device="cuda")
-    ws = torch.full((fa.fa_fwd_paged_q4_workspace_size(B, H, H_kv, total, max_q, 900, d, n_splits) // 4,), 3.0, device="cuda")
-    fa.fa_fwd_paged_q4(cuda(q), *cache, o, lse, i32(cu), i32(lens), i32(table), max_q, 900, d ** -0.5, DK, DV, True, n_splits, ws)
+    ws = torch.full((fa.fa_fwd_paged_q4_workspace_size(B, H, H_kv, total, max_q, N, d, n_splits) // 4,), 3.0, device="cuda")
+    fa.fa_fwd_paged_q4(cuda(q), *cache, o, lse, i32(cu), i32(lens), i32(table), max_q, N, d ** -0.5, DK, DV, True, n_splits, ws)
     if what == "front":
         fa.fa_sync_status()
     else:
@@ -114,3 +114,17 @@ def test_flags_that_are_neither_true_nor_false():
         assert e.value.status == 1
     fa.fa_sync_status()
     assert all(torch.equal(x, y) for x, y in zip(cache, before))
+
+
+def test_streams_by_their_named_handles():
+    """0 and 1 are the default stream, 2 the thread's own: as in the other calls, which take any handle."""
+    require_gpu()
+    cache, table, _ = fill_cache([500, 90], 2, 128, 64, 21)
+    q, t, n = cuda(normal((2, 8, 1, 128), 6)), i32(table), i32([500, 90])
+    o, lse = fa.decode_paged_q4(q, *cache, t, n, 500, descale_k=DK, descale_v=DV)
+    torch.cuda.synchronize()
+    for handle in (0, 1, 2):
+        o2, lse2 = fa.decode_paged_q4(q, *cache, t, n, 500, descale_k=DK, descale_v=DV, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    fa.fa_sync_status()
