@@ -890,7 +890,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     auto done = [&](uint64_t* bar) {                          // this warp's part is written: tell the issuing CTA
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cluster_addr(bar, 0));
+      if (lane == 0) mbar_arrive_cluster_release(cluster_addr(bar, 0));
     };
     bool ok = true;
     for (int j = 0; ok && j < n_max; ++j) {
@@ -954,7 +954,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
     const float c2 = q4_query_row<D>(p, r < rows, th, sQ + t * C::QTILE, row);
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(cluster_addr(q_full, 0));
+    if (lane == 0) mbar_arrive_cluster_release(cluster_addr(q_full, 0));
     const uint32_t hand = cluster_addr(&p_full[t], 0);
     const int lim = min(key_end, seen(r));
     const int lim_low = __reduce_min_sync(0xffffffffu, lim);  // keys below it are all the warp's rows'
@@ -966,7 +966,7 @@ attend_q4_pair_kernel(const __grid_constant__ Q4TParams p) {
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(hand);
+      if (lane == 0) mbar_arrive_cluster_relaxed(hand);
     };
     for (const int plain = min(n, (lim_low - key0) / C::BN); !far && j < plain; ++j) {
       if (!(ok = mbar_wait_warp(&s_full[t], j & 1, abort_flag, 491))) break;

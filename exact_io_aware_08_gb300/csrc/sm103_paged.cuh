@@ -54,12 +54,18 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   return r;
 }
 
-// Arrival on an mbarrier of another CTA of the cluster (or this one), address by cluster_addr.  Of the
-// default scope: what it announces is tensor memory, ordered by the tcgen05 fences, and shared memory
-// of the arriving CTA itself, made visible to the tensor core by a proxy fence; a release at cluster
-// scope took its warp 800 to 1400 clocks.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+// Arrivals on an mbarrier of another CTA of the cluster (or this one), address by cluster_addr.  One that
+// announces shared memory (written by the arriving warp, and made visible to the tensor core's proxy)
+// releases it to the cluster, ...
+__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
+}
+
+// ... and one that announces tensor memory only has nothing to release: what was written there is ordered
+// by the tcgen05 fences in front of the arrival and behind the wait, which go with any arrival.  (A release
+// here waits for all that the warp has under way, 800 to 1400 clocks.)
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" :: "r"(addr) : "memory");
 }
 
 // Bounded wait by a whole warp on an mbarrier that other CTAs arrive at too.

@@ -1,6 +1,8 @@
 """Refusals of the paged-cache operators, through the C ABI and through the package: all of them
 before anything is launched, so they run without a GPU."""
+import glob
 import math
+import os
 import subprocess
 
 import pytest
@@ -208,3 +210,14 @@ def test_messages_hold_any_shape(lib):
             wrong = torch.empty(0, dtype=torch.uint8).as_strided(shape, (0,) * len(shape))
             with pytest.raises(fa.FaError, match=r"block_size, d/2\], is \[0, 1000, .*(\.\.\.|0)\]$"):
                 fa.decode_paged_q4(t["q"][:2, :, None], wrong, t["ks"], t["kc"], t["ks"], t["table"], t["lens"], 16)
+
+
+def test_arrivals_in_another_cta_name_their_scope():
+    """An arrival without a scope is ordered within its own CTA only, whatever CTA its barrier lies in."""
+    found = 0
+    for path in glob.glob(os.path.join(fabuild.CSRC, "*")):
+        for line in open(path):
+            if "mbarrier.arrive" in line and "shared::cluster" in line and "tcgen05" not in line:
+                found += 1
+                assert ".release.cluster." in line or ".relaxed.cluster." in line, (path, line)
+    assert found
