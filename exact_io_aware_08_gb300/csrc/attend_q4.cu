@@ -699,20 +699,22 @@ __global__ void __launch_bounds__(Q4Cfg<D, NT>::THREADS, 1) attend_q4_kernel(con
   __syncthreads();
 }
 
-// Whether packed token t is one of a sequence that the kernels above computed; by a whole warp.
-__device__ __forceinline__ bool q4_computed(const int* __restrict__ cu, int n_seqs, int total_q, int max_q, int t) {
+// The sequence of packed token t, if it is one that the kernels above computed, else -1; by a whole warp.
+__device__ __forceinline__ int q4_owner(const int* __restrict__ cu, int n_seqs, int total_q, int max_q, int t) {
   auto has = [&](int b) {
     const int first = __ldg(cu + b), end = __ldg(cu + b + 1);
     return first >= 0 && first <= t && t < end && end <= total_q && end - first <= max_q;
   };
-  if (has(search_owner(cu, n_seqs, t))) return true;
+  const int found = search_owner(cu, n_seqs, t);
+  if (has(found)) return found;
   // in front of the first sequence or behind the last one, or boundaries that do not ascend, among which
   // some sequence may be sound all the same
   for (int b0 = 0; b0 < n_seqs; b0 += 32) {
     const int b = b0 + (threadIdx.x & 31);
-    if (__any_sync(0xffffffffu, b < n_seqs && has(b))) return true;
+    const uint32_t sound = __ballot_sync(0xffffffffu, b < n_seqs && has(b));
+    if (sound) return b0 + __ffs(sound) - 1;
   }
-  return false;
+  return -1;
 }
 
 // Joins a row's chunks where the caller gave their count (part: [row][chunk]): WPR warps a row.  Rows that
@@ -724,63 +726,80 @@ __global__ void __launch_bounds__(128) attend_q4_merge_kernel(const float* __res
                                                              float descale_v) {
   const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   const int tok = static_cast<int>(th / H), head = static_cast<int>(th - static_cast<long long>(tok) * H);
-  const bool some = th < static_cast<long long>(total_q) * H && (!cu_q || q4_computed(cu_q, n_seqs, total_q, max_q, tok));
+  const bool some = th < static_cast<long long>(total_q) * H && (!cu_q || q4_owner(cu_q, n_seqs, total_q, max_q, tok) >= 0);
   pdl_wait();
   q4_join<D, WPR>({part + static_cast<size_t>(th) * n_splits * (D + 2), D + 2, 0, some ? n_splits : 0},
                   WPR > 1 ? threadIdx.x >> 5 : 0, WPR, o + static_cast<size_t>(th) * D,
                   lse + (cu_q ? static_cast<size_t>(head) * total_q + tok : static_cast<size_t>(th)), descale_v);
 }
 
-// Joins the states of the row blocks that lie in several teams' shares.  There are as many as there are
-// bounds between shares at most, so that a block looks for one: that of bound i + 1 if it is the first
-// within its row block, or, where there are fewer row blocks than that (BY_BLOCK), row block i of
-// the most that there can be.  Its warps share the rows out.
+// Joins the states of the rows whose row block lies in several teams' shares, WPR warps a row.
+template <int D, int NT, int WPR>
+__global__ void __launch_bounds__(128) attend_q4_row_join_kernel(const __grid_constant__ Q4Params p, int teams) {
+  constexpr int ROWS = 8 * NT;
+  const long long th = WPR > 1 ? blockIdx.x : static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const bool some = th < static_cast<long long>(p.total_q) * p.H;
+  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
+  int b = some ? tok : -1;
+  if (some && p.cu_q) b = q4_owner(p.cu_q, p.n_seqs, p.total_q, p.max_q, tok);
+  long long total = 0, before = 0;                             // units of all sequences, of those before b
+  for (int k = threadIdx.x & 31; k < p.n_seqs; k += 32) {
+    const long long v = q4_seq(p, k, ROWS, false).units(p.H_kv);
+    total += v;
+    if (k < b) before += v;
+  }
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, off);
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+  }
+  Q4Share sh;
+  sh.set(total, teams);
+  Q4States st{p.part, 2 * ROWS * (D + 2), ROWS * (D + 2), 0};
+  if (b >= 0) {                                                // (else no sequence's: stays as it is)
+    const Q4Seq seq = q4_seq(p, b, ROWS, false);
+    const int row = (tok - seq.first) * p.G + head % p.G;
+    const long long u0 = before + (static_cast<long long>(row / ROWS) * p.H_kv + head / p.G) * seq.steps;
+    const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
+    if (c0 != c1) {                                            // (else its team wrote the result)
+      st.base += (static_cast<size_t>(2 * c0) * ROWS + row % ROWS) * (D + 2);
+      st.n = c1 - c0 + 1;
+    }
+  }
+  pdl_wait();
+  q4_join<D, WPR>(st, WPR > 1 ? threadIdx.x >> 5 : 0, WPR, p.o + static_cast<size_t>(th) * D,
+                  p.lse + (p.cu_q ? static_cast<size_t>(head) * p.total_q + tok : static_cast<size_t>(th)), p.descale_v);
+}
+
+// The same for many row blocks, most of which are not divided.  Those that are hold a bound between shares:
+// a block takes the row block of bound i + 1 if that is the first within it, and its warps share the rows out.
 constexpr int kQ4JoinWarps = 16;
 
-template <int D, int NT, bool BY_BLOCK>
+template <int D, int NT>
 __global__ void __launch_bounds__(32 * kQ4JoinWarps) attend_q4_join_kernel(const __grid_constant__ Q4Params p, int teams) {
   constexpr int ROWS = 8 * NT;
   __shared__ Q4Item item;                                      // b, hkv, rb, first, nq; n in ``len``, first team in ``out``
   const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   if (warp == 0) {
     const int i = blockIdx.x;
-    int b = BY_BLOCK ? i / (p.H_kv * p.row_blocks) : -1;
+    int b;
     long long before = 0;                                      // units of the sequences before b
-    Q4Share sh;
-    if (BY_BLOCK) {
-      long long total = 0;
-      for (int k = threadIdx.x; k < p.n_seqs; k += 32) {
-        const long long v = q4_seq(p, k, ROWS, false).units(p.H_kv);
-        total += v;
-        if (k < b) before += v;
-      }
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, off);
-        before += __shfl_xor_sync(0xffffffffu, before, off);
-      }
-      sh.set(total, teams);
-    } else {
-      sh = q4_share(p, ROWS, teams, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
-    }
+    const Q4Share sh = q4_share(p, ROWS, teams, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
     if (threadIdx.x == 0) {
       item.len = 0;
       if (b >= 0) {
         const Q4Seq seq = q4_seq(p, b, ROWS, false);
-        // (below 2^31 units a sequence)
-        const int pair = BY_BLOCK ? i - b * p.H_kv * p.row_blocks : static_cast<int>(sh.begin(i + 1) - before) / seq.steps;
-        if (pair < seq.blocks * p.H_kv) {
-          const long long u0 = before + static_cast<long long>(pair) * seq.steps;
-          const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
-          if (c0 != c1 && (BY_BLOCK || c0 == i)) {             // (c0 == i: bound i + 1 is its first)
-            item.b = b;
-            item.hkv = pair % p.H_kv;
-            item.rb = pair / p.H_kv;
-            item.first = seq.first;
-            item.nq = seq.nq;
-            item.len = c1 - c0 + 1;
-            item.out = c0;
-          }
+        const int pair = static_cast<int>(sh.begin(i + 1) - before) / seq.steps;   // (below 2^31 units a sequence)
+        const long long u0 = before + static_cast<long long>(pair) * seq.steps;
+        const int c0 = sh.owner(u0), c1 = sh.owner(u0 + seq.steps - 1);
+        if (c0 != c1 && c0 == i) {                             // (c0 == i: bound i + 1 is its first)
+          item.b = b;
+          item.hkv = pair % p.H_kv;
+          item.rb = pair / p.H_kv;
+          item.first = seq.first;
+          item.nq = seq.nq;
+          item.len = c1 - c0 + 1;
+          item.out = c0;
         }
       }
     }
@@ -855,14 +874,18 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   e = cudaGetLastError();
   if (e != cudaSuccess || a.n_splits || p.whole) return e;
   const int teams = C::TEAMS * grid;
-  const bool by_block = pairs < teams - 1;
-  const unsigned blocks = static_cast<unsigned>(by_block ? pairs : teams - 1);
-  // a warp a row, and many a row only where there are states for them: small blocks start sooner
-  const long long block_rows = min(static_cast<long long>(C::ROWS), q4_rows(a.H, a.H_kv, a.max_seqlen_q));
-  const bool many = block_rows > 8 || min(steps, teams / pairs) > 16;
-  const unsigned threads = 32 * (many ? kQ4JoinWarps : block_rows > 4 ? 8 : 4);
-  log_launch("attend_q4_join_kernel<D, NT, BY_BLOCK>", blocks, threads, 0ull);
-  return launch_join(by_block ? attend_q4_join_kernel<D, NT, true> : attend_q4_join_kernel<D, NT, false>, blocks, threads, stream, p, teams);
+  // By rows up to two row blocks a team, us by rows and by bounds: 16 x 4000 tokens of 16 query heads a key
+  // head 16 and 20, 48 x 8192 55 and 58, 128 x 1500 of 4 43 and 44 (1024 row blocks), 256 x 1500 76 and 73.
+  if (pairs <= 1024) {
+    const long long out_rows = static_cast<long long>(a.total_q) * a.H;
+    const int warps = q4_join_warps(out_rows);
+    const unsigned blocks = static_cast<unsigned>((out_rows * warps + 3) / 4);
+    log_launch("attend_q4_row_join_kernel<D, NT, WPR>", blocks, 128, 0ull);
+    return launch_join(warps == 1 ? attend_q4_row_join_kernel<D, NT, 1> : attend_q4_row_join_kernel<D, NT, 4>, blocks, 128, stream, p, teams);
+  }
+  const unsigned threads = NT > 1 ? 32 * kQ4JoinWarps : p.G * a.max_seqlen_q > 4 ? 256 : 128;   // a warp a row
+  log_launch("attend_q4_join_kernel<D, NT>", static_cast<unsigned long long>(teams - 1), threads, 0ull);
+  return launch_join(attend_q4_join_kernel<D, NT>, static_cast<unsigned>(teams - 1), threads, stream, p, teams);
 }
 
 template <int D, int WPR>

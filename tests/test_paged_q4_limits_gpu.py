@@ -128,3 +128,39 @@ def test_streams_by_their_named_handles():
         torch.cuda.synchronize()
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     fa.fa_sync_status()
+
+
+@pytest.mark.parametrize("H,H_kv,d,n,seqs", [(8, 4, 64, 1, 300), (32, 4, 128, 1, 270), (8, 4, 128, 3, 257), (4, 4, 128, 2, 256), (6, 3, 64, 4, 130)])
+def test_many_row_blocks(H, H_kv, d, n, seqs):
+    """More row blocks than teams, some divided between two or several of them: about as many as the rule
+    between the two ways to join them leaves to one, and more.  The same as a call that divides none."""
+    require_gpu()
+    rng = np.random.default_rng(seqs)
+    lens = np.where(rng.random(seqs) < 0.1, 0, rng.integers(0, 900, seqs)).tolist()
+    lens[seqs // 2] = 6000
+    new = [1 if n == 1 else int(x) for x in rng.integers(0, n + 1, seqs)]
+    new[3] = n
+    cu, total = np.concatenate(([0], np.cumsum(new))), sum(new) + 2
+    cache, table, val = fill_cache(lens, H_kv, d, 64, 8)
+    q = normal((total, H, d), 9)
+    got = []
+    for n_splits in (0, 1):
+        o = torch.full((total, H, d), -7.25, dtype=torch.bfloat16, device="cuda")
+        lse = torch.full((H, total), -7.25, device="cuda")
+        ws = torch.full((fa.fa_fwd_paged_q4_workspace_size(seqs, H, H_kv, total, n, 6000, d, n_splits) // 4,), float("nan"), device="cuda")
+        fa.fa_fwd_paged_q4(cuda(q), *cache, o, lse, i32(cu), i32(lens), i32(table), n, 6000, d ** -0.5, DK, DV, True, n_splits, ws)
+        fa.fa_sync_status()
+        got.append((f64(o), f64(lse)))
+    G = H // H_kv
+    for b in sorted({seqs // 2, *range(0, seqs, 9)}):
+        mine = slice(cu[b], cu[b + 1])
+        seen = [lens[b] - new[b] + i + 1 for i in range(new[b])]
+        for h in range(H if new[b] else 0):
+            want = P.attend(f64(q[mine, h]), val["k"][b][:, h // G], val["v"][b][:, h // G], d ** -0.5, seen)
+            for o, lse in got:
+                check_attention(o[mine, h], lse[h, mine], want)
+    (o, lse), (o1, lse1) = got
+    # two results within half a bf16 step and the weights' own 2^-11 each of one another's value
+    top = np.abs(val["v"][seqs // 2]).max()
+    assert (np.abs(o - o1) <= 2.0 ** -7 * np.abs(o1) + 2.0 ** -9 * top).all()
+    assert (np.isneginf(lse) == np.isneginf(lse1)).all() and (o[cu[-1]:] == -7.25).all() and (lse[:, cu[-1]:] == -7.25).all()
