@@ -23,20 +23,18 @@ __device__ __forceinline__ void report_device_error(unsigned int code, int where
 
 }  // namespace fa
 
-// Host accessor: copy this TU's status word out (after synchronising ``stream``) and clear it.
+// Host accessor: copy this TU's status word out (after synchronising ``stream``) and clear it.  Each copy is
+// a round trip to the device (some 9 us), so that a clean word, the usual one, is all that is read.
 #define FA_DEFINE_STATUS_FETCH(NAME)                                                         \
   namespace fa {                                                                             \
   cudaError_t NAME(cudaStream_t stream, unsigned int* code, int* where) {                    \
     cudaError_t e = cudaStreamSynchronize(stream);                                           \
     if (e != cudaSuccess) return e;                                                          \
     e = cudaMemcpyFromSymbol(code, g_dev_status, sizeof(unsigned int));                      \
-    if (e != cudaSuccess) return e;                                                          \
+    if (e != cudaSuccess || !*code) return e;                                                \
     e = cudaMemcpyFromSymbol(where, g_dev_where, sizeof(int));                               \
     if (e != cudaSuccess) return e;                                                          \
-    if (*code) {                                                                             \
-      const unsigned int zero = 0;                                                           \
-      e = cudaMemcpyToSymbol(g_dev_status, &zero, sizeof(unsigned int));                     \
-    }                                                                                        \
-    return e;                                                                                \
+    const unsigned int zero = 0;                                                             \
+    return cudaMemcpyToSymbol(g_dev_status, &zero, sizeof(unsigned int));                    \
   }                                                                                          \
   }

@@ -183,3 +183,12 @@ def test_block_sparse_entry_points_validate_before_launching(lib):
     assert bwd(*args, FAKE, need - 1, 1, 2, 256, 256, 128, 0.1, 0, FAKE, 0, None) == WORKSPACE
     assert bwd(*args, FAKE, need, 1, 2, 256, 256, 128, 0.1, 0, None, 0, None) == INVALID
     assert bwd(*args, FAKE, need, 1, 2, 256, 256, 64, 0.1, 1, FAKE, 3, None) == INVALID
+
+
+def test_a_clean_status_is_one_read_a_unit():
+    """fa_sync_status asks every unit that launches kernels; a clean one costs it one copy from the
+    device, so that units of their own for other calls do not double what a check costs."""
+    text = open(os.path.join(fabuild.CSRC, "fa_status.cuh")).read()
+    body = text[text.index("#define FA_DEFINE_STATUS_FETCH"):]
+    clean = body[:body.index("!*code) return e;")]
+    assert clean.count("cudaMemcpyFromSymbol") == 1 and body.count("cudaMemcpyFromSymbol") == 2
