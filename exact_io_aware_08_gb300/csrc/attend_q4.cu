@@ -32,10 +32,10 @@
 // team gets an equal share of all sequences' key steps (Q4Share), whatever their lengths; with an
 // explicit split count the items are (sequence, key head, row block, chunk).
 //
-// Measured: 64 x 32768 tokens, 4 query heads a key head: 384 us, 2.42 GB at 6.3 TB/s (93% of the copy
-// rate).  Short calls are bound by latencies: 4 us from the launch to the first keys (place in the work,
-// query rows, page table, stage: each waits for the last), 1.4 us a step, 1.3 to leave a row block, 3 for
-// the join behind; 1 x 1000 tokens 7.8 us.
+// Measured on the GPU, without the call's host time: 64 x 32768 tokens, 4 query heads a key head: 384 us,
+// 2.42 GB at 6.3 TB/s (93% of the copy rate).  Short calls are bound by latencies: 4 us from the launch to
+// the first keys (place in the work, query rows, page table, stage: each waits for the last), 1.4 us a step,
+// 1.3 to leave a row block, 3 for the join behind; 1 x 1000 tokens 7.7 us.
 #include "fa_kernels.h"
 #include "q4.cuh"
 #include "q4_share.h"
@@ -860,8 +860,8 @@ static cudaError_t launch_attend_q4_d(const PagedQ4Args& a, cudaStream_t stream)
   const long long most = min(q4_sm_count(), kQ4MaxShares / C::TEAMS);
   const long long steps = (static_cast<long long>(a.max_seqlen_k) + kQ4Step - 1) / kQ4Step;
   // Short row blocks, and enough of them for a quarter of the teams, are not divided: the states and the
-  // join cost as much as some four steps (8 key heads, 512 tokens, 64 sequences 21 us, whole 17; 24, 18
-  // and 17; of 1000 tokens 38 sequences 21, whole 25).
+  // join cost as much as some four steps (8 key heads, 512 tokens, 64 sequences 18.6 us, whole 14.4; 24, 14.5
+  // and 13.7, though 38, 13.8 and 14.4; of 1000 tokens 38 sequences 17.2, whole 21.2).
   p.whole = steps <= 1 || (steps <= 5 && 4 * pairs >= most * C::TEAMS) ? 1 : 0;
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_q4_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);

@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(Q4TCfg<D>::THREADS, 1) attend_q4_tile_kernel(c
 // cores work on one product.  Tile t is 256 rows, 128 in each CTA, and each CTA holds half of the
 // other operand: 64 of a key tile's 128 keys for S, 64 of the 128 columns of V for O.  So each
 // unpacks half as much a row (K: its 64 keys whole, V: its half of every key), and the tensor core
-// reads half as much of it from each shared memory.  4 x 1024 tokens over 16384 keys: 712 us, 789
+// reads half as much of it from each shared memory.  4 x 1024 tokens over 16384 keys: 717 us, 809
 // by CTAs of their own.
 //
 // The even CTA's warp 1 issues all products; the barriers it waits on are its own and both CTAs arrive
@@ -662,7 +662,7 @@ struct Q4PCfg {
   static constexpr int THREADS = 512;
   static constexpr int UNPACK_WARPS = 4;
   static constexpr uint32_t BAR_START = 1;
-  // (4 x 1024 tokens over 16384 keys with 48, 208 and 48 719 us; with 56, 208, 40 712; with 72, 200, 40 764)
+  // (4 x 1024 tokens over 16384 keys with 48, 208 and 48 721 us; with 56, 208, 40 717; with 72, 200, 40 794)
   static constexpr uint32_t REG_CTRL = 56, REG_SOFTMAX = 208, REG_UNPACK = 40;
   static constexpr int REG_NEED = 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX) + static_cast<int>(REG_UNPACK));
 };
@@ -1024,11 +1024,12 @@ __global__ void __launch_bounds__(128) attend_q4_tail_kernel(const __grid_consta
 
 // Shares the items out to ``places`` (SMs, or pairs of them) at a time: all that fill them a whole
 // number of times run whole, what is left over is split so that it fills them once more (4x1024 tokens
-// over 16384 keys, 256 items on 76 pairs: 1010 us whole, 950 us with the last 28 in two parts).  A part
-// has at least 512 keys where nothing else runs (1x128 tokens over 4096 keys: 31 us, 35 with 1024), else
-// 1024 (8 prompts of up to 1024 tokens, 64 wide: 51 us whole, 62 us in parts of 640).  The states and
-// their join cost some 15 us, so that at least nine key steps have to be saved (of 64 items, 1024 keys:
-// 20 us whole, 29 in two; 2048 keys: 32 whole, 24 in four).  Returns the grid.
+// over 16384 keys, 256 items on 76 pairs: 785 us whole, 717 us with the last 28 in two parts).  A part
+// has at least 512 keys where nothing else runs (1x128 tokens over 4096 keys: 30 us, 59 whole; 35 with 1024
+// keys a part against 31 at the time), else 1024 (8 prompts of up to 1024 tokens, 64 wide: 51 us whole, 62 us
+// in parts of 640 at the time).  The states and their join cost some 15 us, so that at least nine key steps
+// have to be saved (64 items over 1024 keys: 19 us whole, 28 in two; over 2048: 31 and 34; 16 items over
+// 2048: 31 whole, 20 in four).  Returns the grid.
 static long long share_tiles(Q4TParams& p, const PagedQ4Args& a, int places, int block_rows) {
   p.block_rows = block_rows;
   p.row_blocks = static_cast<int>((q4_rows(a.H, a.H_kv, a.max_seqlen_q) + block_rows - 1) / block_rows);

@@ -174,7 +174,9 @@ struct PagedQ4Args {
   const uint8_t *k_codes, *k_scales, *v_codes, *v_scales;
   void* o;
   float* lse;
-  float* part;                  // [total_q * H, n_splits, d + 2], used when n_splits > 1
+  // States of parts of rows, d + 2 floats each: [total_q * H, n_splits] with a split count above 1; without
+  // one (0) two a team of 8 or 16 rows each, or, of tiles, [row block that is split, part, row].
+  float* part;
   const int *cu_q, *seqlens, *block_table;
   int n_seqs, H, H_kv, total_q, max_seqlen_q, d, num_blocks, block_size, max_blocks, max_seqlen_k, causal;
   float scale, descale_k, descale_v;
@@ -240,13 +242,14 @@ inline size_t decode_part_bytes(int B, int H, int d, int n_splits) {
 }
 
 // 4-bit attention: query rows of a key head (the query heads that share it, times a sequence's query
-// tokens) are computed 8 or 16 a CTA (attend_q4.cu), or 256 (attend_q4_tile.cu).
+// tokens) are computed 8 or 16 by a team of warps, three or four teams a CTA (attend_q4.cu), or 256 a CTA
+// and 512 a pair (attend_q4_tile.cu).
 constexpr int kQ4Rows = 16;
 constexpr int kQ4TileRows = 256;
 inline long long q4_rows(int H, int H_kv, int max_seqlen_q) { return static_cast<long long>(H / H_kv) * max_seqlen_q; }
 // Tiles where there are more than two (d = 128) or three blocks of kQ4Rows rows, each of which unpacks
-// the keys anew.  16 sequences x 8 key heads, us by rows and by tiles: d = 128, 8000 keys, 32 rows 80 and 99,
-// 48 rows 116 and 99; d = 64, 4000 keys, 48 rows 45 and 49.
+// the keys anew.  16 sequences x 8 key heads, us by rows and by tiles: d = 128, 8000 keys, 32 rows 80 and 101,
+// 48 rows 116 and 102; d = 64, 4000 keys, 48 rows 44 and 48, 64 rows 57 and 48.
 inline bool q4_use_tiles(int H, int H_kv, int max_seqlen_q, int d) {
   return q4_rows(H, H_kv, max_seqlen_q) > (d == 128 ? 2 : 3) * kQ4Rows;
 }

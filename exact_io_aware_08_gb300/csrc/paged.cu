@@ -78,7 +78,7 @@ __device__ __forceinline__ void quantise16(const float (&f)[16], bool split, flo
   }
 }
 
-// (six passes in 4 bits: 124 registers without a limit, 242 against 234 us for 24 mixed sequences)
+// (six passes in 4 bits: 124 registers without a limit, 200 against 194 us for 24 mixed sequences)
 template <int D, bool Q4, bool INTER, int U>
 __global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_kernel(const AppendParams p) {
   constexpr int L = D / 16;                       // lanes a head
@@ -262,12 +262,12 @@ __global__ void __launch_bounds__(kPagedThreads) gather_q4_kernel(const GatherPa
 }
 
 // A warp takes U passes of a token.  One where the passes are too few to fill the GPU twice over, so
-// that they spread (4 x 16 tokens of 96 heads: 3.3 against 4.2 us); else more, so that the search for
+// that they spread (4 x 16 tokens of 96 heads: 3.0 us, 4.0 with eight passes a warp); else more, so that the search for
 // the token's place (four dependent loads) is shared and more bytes are in flight behind it.  How
 // many: 6, or 3 where that leaves fewer passes empty, the one or two that there are, or, in bf16 only, 8
-// where none is empty then.  Measured: 4 x 4096 tokens of 24 passes in bf16 with 2, 3 and 8 126, 125,
-// 122 us; 12 passes in 4 bits (with the reading back) with 2, 3, 4 and 6 284, 269, 282, 242; 2 passes in
-// 4 bits with 2, 3 and 4 25, 29, 35.
+// where none is empty then.  Measured on the GPU: 4 x 4096 tokens of 24 passes in bf16 with 2, 3, 6 and 8
+// 142, 133, 129, 124 us; 24 mixed sequences of 12 passes in 4 bits with 2, 3, 4 and 6 239, 258, 237, 194; of
+// 2 passes in 4 bits with 2, 3 and 4 44, 59, 68.
 static bool few_passes(long long passes) { return passes < 152LL * 64; }
 
 template <int D, bool Q4, bool INTER, int U>
@@ -339,7 +339,7 @@ static cudaError_t launch_gather_d(const GatherArgs& a, cudaStream_t stream) {
   p.descale_k = a.descale_k; p.descale_v = a.descale_v;
   const int per_pass = 32 / (D / 16);
   const long long passes = (2LL * p.H_kv + per_pass - 1) / per_pass;
-  // two passes a warp where there are (8 x 16384 tokens of 4 passes, with 1, 2 and 4: 146, 124, 174 us)
+  // two passes a warp where there are (8 x 16384 tokens of 4 passes, with 1, 2 and 4: 140, 123, 167 us)
   if (passes == 1 || few_passes(passes * p.total)) return launch_gather_u<D, 1>(p, passes, stream);
   return launch_gather_u<D, 2>(p, passes, stream);
 }

@@ -336,7 +336,9 @@ fa_status_t fa_decode_splitkv_noalloc(const fa_bf16_t* q, const fa_bf16_t* k, co
  * is dense and may be q itself where q is dense.
  *
  * bf16 cache: k_cache, v_cache [num_blocks, block_size, H_kv, d], rounded to nearest, as
- * fa_decode_paged reads them (which wants block_size a multiple of 64; any will do here).
+ * fa_decode_paged reads them.  That one takes single query tokens, as many key heads as query heads
+ * and block_size a multiple of 64 (any will do here); it is the only call that reads these pages.  For
+ * grouped heads, or several query tokens a sequence over what is cached, use the 4-bit cache.
  *
  * 4-bit cache: codes [num_blocks, H_kv, block_size, d/2], scales [num_blocks, H_kv, block_size, d/16]:
  * a head's rows of a block are consecutive, so that the attention reads them in long runs.
@@ -344,7 +346,9 @@ fa_status_t fa_decode_splitkv_noalloc(const fa_bf16_t* q, const fa_bf16_t* k, co
  *   scale = e4m3(max |x| / (6 descale)),  code_i = e2m1(x_i / (scale descale)),
  * both to nearest, ties to even, saturating at 448 and 6; a scale of 0 gives codes of 0.  The value
  * is code * scale * descale (descale_k for keys, descale_v for values, in [1e-30, 1e30]; commonly
- * the largest magnitude expected over 6 * 448).  What is not finite is held as some finite value.
+ * the largest magnitude expected over 6 * 448).  What is not finite is held as some finite value: an
+ * infinity as the largest one of its scale, and so is NaN, which the cache does not show (queries keep
+ * it, and the bf16 cache does).
  *
  * Device-side checks: boundaries outside [0, total] or not ascending, seqlens_k[b] below the step's
  * tokens of b, a position outside the block table or the cos/sin tables, or a block id outside
@@ -386,8 +390,10 @@ fa_status_t fa_gather_paged_q4(const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_sc
  *
  *   O, lse = attention of q over the first seqlens_k[b] cached tokens       q, o: [B,H,1,d], lse: [B,H,1]
  *
- * Scores accumulate in fp32 from exact products of codes and scales with q; the attention weights are
- * rounded to 16 bits for the product with the values.  block_size is a positive multiple of 16;
+ * Scores accumulate in fp32 from exact products of codes and scales with q, of which elements below
+ * 2^-28 of the (query, head)'s largest lose bits (it is held in fp16 times a power of two); exponentials
+ * are good to 2^-22.  The attention weights are rounded to fp16 for the product with the values, by 2^-11
+ * of themselves and 2^-32 of the row's largest at most.  block_size is a positive multiple of 16;
  * seqlens_k, block_table, max_seqlen_k, n_splits and the device-side checks as for fa_decode_paged.
  * A row with no tokens gets O = 0, lse = -inf.  ws: at least the size call's bytes, 16-byte aligned
  * (not looked at where the call runs with one split); calls that may run at the same time, replayed
