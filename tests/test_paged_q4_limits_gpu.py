@@ -130,7 +130,8 @@ def test_streams_by_their_named_handles():
     fa.fa_sync_status()
 
 
-@pytest.mark.parametrize("H,H_kv,d,n,seqs", [(8, 4, 64, 1, 300), (32, 4, 128, 1, 270), (8, 4, 128, 3, 257), (4, 4, 128, 2, 256), (6, 3, 64, 4, 130)])
+@pytest.mark.parametrize("H,H_kv,d,n,seqs", [(8, 4, 64, 1, 300), (32, 4, 128, 1, 270), (8, 4, 128, 3, 257), (4, 4, 128, 2, 256), (6, 3, 64, 4, 130),
+                                              (16, 4, 128, 4, 270), (32, 4, 64, 4, 140)])
 def test_many_row_blocks(H, H_kv, d, n, seqs):
     """More row blocks than teams, some divided between two or several of them: about as many as the rule
     between the two ways to join them leaves to one, and more.  The same as a call that divides none."""
