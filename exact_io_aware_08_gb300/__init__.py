@@ -10,7 +10,10 @@ library itself never allocates).
 
 Serving over paged caches: ``append_paged`` and ``append_paged_q4`` rotate a step's queries and keys
 by position and put keys and values into the pages, ``decode_paged`` (bf16), ``decode_paged_q4`` and
-``forward_paged_q4`` (4 bits) attend over them, ``gather_paged_q4`` reads a 4-bit cache back.
+``forward_paged_q4`` (4 bits) attend over them, ``gather_paged_q4`` reads a 4-bit cache back.  Over the
+bf16 cache ``forward_paged_tree`` attends for grouped heads and any number of tokens, drafted trees among
+them, ``accept_paged`` keeps a tree's accepted path, ``weigh_paged`` adds up the attention that each cached
+token draws, and ``evict_paged`` keeps those that draw the most.
 """
 from __future__ import annotations
 
@@ -30,6 +33,9 @@ __all__ = [
     "fa_append_paged", "fa_append_paged_q4", "fa_gather_paged_q4", "fa_decode_paged_q4", "fa_fwd_paged_q4",
     "fa_decode_paged_q4_workspace_size", "fa_fwd_paged_q4_workspace_size",
     "append_paged", "append_paged_q4", "gather_paged_q4", "decode_paged_q4", "forward_paged_q4", "rotary_tables",
+    "fa_append_paged_at", "fa_append_paged_q4_at", "fa_fwd_paged_tree", "fa_fwd_paged_tree_workspace_size",
+    "fa_accept_paged", "fa_weigh_paged", "fa_evict_paged",
+    "forward_paged_tree", "accept_paged", "weigh_paged", "evict_paged", "tree_bits",
 ]
 
 BLOCK_SIZE = 128   # block-sparse attention: blocks of 128 queries x 128 keys
@@ -88,6 +94,13 @@ _SIGNATURES = {
     "fa_decode_paged_q4": (_I, [_P] * 9 + [_I] * 8 + [_F] * 3 + [_I, _P, _S, _P]),
     "fa_fwd_paged_q4_workspace_size": (_S, [_I] * 8),
     "fa_fwd_paged_q4": (_I, [_P] * 10 + [_I] * 10 + [_F] * 3 + [_I] * 2 + [_P, _S, _P]),
+    "fa_append_paged_at": (_I, [_P] * 12 + [_I] * 4 + [_L] * 3 + [_I] * 7 + [_P]),
+    "fa_append_paged_q4_at": (_I, [_P] * 14 + [_I] * 4 + [_L] * 3 + [_I] * 7 + [_F] * 2 + [_P]),
+    "fa_fwd_paged_tree_workspace_size": (_S, [_I] * 4),
+    "fa_fwd_paged_tree": (_I, [_P] * 6 + [_I] + [_P] * 3 + [_I] * 10 + [_F, _P, _S, _P]),
+    "fa_accept_paged": (_I, [_P] * 8 + [_I] * 7 + [_P]),
+    "fa_weigh_paged": (_I, [_P] * 8 + [_I] * 10 + [_F] * 2 + [_P]),
+    "fa_evict_paged": (_I, [_P] * 9 + [_I] * 11 + [_P]),
     "fa_sync_status": (_I, [_P]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
     "fa_debug_counters": (_I, [_P]),
@@ -362,7 +375,7 @@ def fa_append_paged(q, k, v, q_out, k_cache, v_cache, cos, sin, cu_seqlens, seql
     if q is not None and q_out is None:
         raise FaError(1, "q and q_out go together")
     (_native or _binding()).append(q, k, v, q_out, k_cache, None, v_cache, None, cos, sin, cu_seqlens, seqlens_k, block_table,
-                                   1.0, 1.0, interleaved, stream)
+                                   1.0, 1.0, interleaved, stream, None)
 
 
 def fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
@@ -374,7 +387,27 @@ def fa_append_paged_q4(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos
     if k_scales is None:
         raise FaError(1, "k_scales must be a tensor")
     (_native or _binding()).append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
-                                   block_table, descale_k, descale_v, interleaved, stream)
+                                   block_table, descale_k, descale_v, interleaved, stream, None)
+
+
+def fa_append_paged_at(q, k, v, q_out, k_cache, v_cache, cos, sin, positions, cu_seqlens, seqlens_k, block_table,
+                       interleaved: bool = False, stream=None):
+    """As fa_append_paged, with the positions of the rotation (int32 [total], None: the places in the cache)."""
+    if q is not None and q_out is None:
+        raise FaError(1, "q and q_out go together")
+    (_native or _binding()).append(q, k, v, q_out, k_cache, None, v_cache, None, cos, sin, cu_seqlens, seqlens_k, block_table,
+                                   1.0, 1.0, interleaved, stream, positions)
+
+
+def fa_append_paged_q4_at(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, positions, cu_seqlens, seqlens_k,
+                          block_table, descale_k: float, descale_v: float, interleaved: bool = False, stream=None):
+    """As fa_append_paged_q4, with the positions of the rotation (int32 [total], None: the places in the cache)."""
+    if q is not None and q_out is None:
+        raise FaError(1, "q and q_out go together")
+    if k_scales is None:
+        raise FaError(1, "k_scales must be a tensor")
+    (_native or _binding()).append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens, seqlens_k,
+                                   block_table, descale_k, descale_v, interleaved, stream, positions)
 
 
 def fa_gather_paged_q4(k_codes, k_scales, v_codes, v_scales, k, v, cu_seqlens, seqlens_k, block_table,
@@ -411,6 +444,45 @@ def fa_fwd_paged_q4(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_
     (_native or _binding()).forward(q, k_codes, k_scales, v_codes, v_scales, o, lse, cu_seqlens_q, seqlens_k, block_table,
                                     max_seqlen_q, max_seqlen_k, scale, descale_k, descale_v, causal, n_splits, ws, stream,
                                     False)
+
+
+def fa_fwd_paged_tree_workspace_size(H: int, H_kv: int, max_seqlen_q: int, d: int) -> int:
+    return load_library().fa_fwd_paged_tree_workspace_size(H, H_kv, max_seqlen_q, d)
+
+
+def fa_fwd_paged_tree(q, k_cache, v_cache, o, lse, tree, cu_seqlens, seqlens_k, block_table, max_seqlen_q: int,
+                      max_seqlen_k: int, scale: float, ws, stream=None):
+    """q, o [total, H, d]; k/v cache [num_blocks, block_size, H_kv, d] bf16; lse [H, total]; tree int32 [total, words]
+    or None; cu_seqlens [n_seqs + 1], seqlens_k [n_seqs], block_table [n_seqs, max_blocks] int32."""
+    (_native or _binding()).tree(q, k_cache, v_cache, o, lse, tree, cu_seqlens, seqlens_k, block_table, max_seqlen_q,
+                                 max_seqlen_k, scale, ws, stream, False)
+
+
+def fa_accept_paged(k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seqlens, seqlens_k, block_table,
+                    stream=None):
+    """accepted int32 [n_seqs, max_accepted], n_accepted [n_seqs]; seqlens_out [n_seqs] is written."""
+    if seqlens_out is None:
+        raise FaError(1, "seqlens_out must be a tensor")
+    (_native or _binding()).accept(k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seqlens, seqlens_k, block_table,
+                                   stream)
+
+
+def fa_weigh_paged(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q: int,
+                   max_seqlen_k: int, scale: float, decay: float, stream=None):
+    """q [total, H, d]; lse [H, total]; weights fp32 [num_blocks, H_kv, block_size] are brought up to the step;
+    weighed int32 [n_seqs] or None."""
+    (_native or _binding()).weigh(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q,
+                                  max_seqlen_k, scale, decay, stream)
+
+
+def fa_evict_paged(k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table,
+                   max_seqlen_k: int, max_kept: int, keep_first: int, keep_last: int, stream=None):
+    """kept int32 [n_seqs, H_kv, max_kept] and seqlens_out [n_seqs] are written; budgets [n_seqs]; new_table
+    [n_seqs, new_max_blocks] int32."""
+    if kept is None or seqlens_out is None:
+        raise FaError(1, "kept and seqlens_out must be tensors")
+    (_native or _binding()).evict(k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table,
+                                  max_seqlen_k, max_kept, keep_first, keep_last, stream)
 
 
 def fa_debug_counters(counters):
@@ -571,21 +643,22 @@ def rotary_tables(n_positions: int, rotary_dim: int, base: float = 10000.0, devi
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, q=None, cos=None, sin=None,
-                 interleaved: bool = False, q_out=None, stream=None):
+                 interleaved: bool = False, q_out=None, stream=None, positions=None):
     """Rotates a step's packed keys by their positions, puts keys and values into the bf16 paged cache
-    that decode_paged reads, and returns the rotated queries (None without q)."""
+    that decode_paged and forward_paged_tree read, and returns the rotated queries (None without q).
+    ``positions`` (int32 [total]): where those of the rotation are not the places in the cache."""
     return (_native or _binding()).append(q, k, v, q_out, k_cache, None, v_cache, None, cos, sin, cu_seqlens, seqlens_k,
-                                          block_table, 1.0, 1.0, interleaved, stream)
+                                          block_table, 1.0, 1.0, interleaved, stream, positions)
 
 
 def append_paged_q4(k, v, k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, q=None, cos=None,
                     sin=None, descale_k: float = 1.0, descale_v: float = 1.0, interleaved: bool = False, q_out=None,
-                    stream=None):
+                    stream=None, positions=None):
     """append_paged into a 4-bit cache (see fa_append_paged_q4)."""
     if k_scales is None:
         raise FaError(1, "k_scales must be a tensor")
     return (_native or _binding()).append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, cu_seqlens,
-                                          seqlens_k, block_table, descale_k, descale_v, interleaved, stream)
+                                          seqlens_k, block_table, descale_k, descale_v, interleaved, stream, positions)
 
 
 def gather_paged_q4(k_codes, k_scales, v_codes, v_scales, block_table, cu_seqlens, seqlens_k, total: int,
@@ -612,3 +685,57 @@ def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
     return (_native or _binding()).forward(q, k_codes, k_scales, v_codes, v_scales, None, None, cu_seqlens_q, seqlens_k,
                                            block_table, max_seqlen_q, max_seqlen_k, scale, descale_k, descale_v, causal,
                                            n_splits, workspace, stream, True)
+
+
+def tree_bits(parents, cu_seqlens, max_seqlen_q: int):
+    """(tree, depth) of packed drafted tokens: ``parents`` int32 [total] names each token's parent within its
+    sequence (an earlier token, or -1 for a root).  tree int32 [total, words]: a token sees itself and its
+    ancestors; depth int32 [total]: 0 for a root.  A few torch operations, on the tensors' device: for trees that
+    stay, made once."""
+    import torch
+    n, words, dev = parents.shape[0], max(1, -(-max_seqlen_q // 32)), parents.device
+    t = torch.arange(n, device=dev)
+    cu = cu_seqlens.long()
+    first = cu[torch.searchsorted(cu[1:].contiguous(), t, right=True).clamp(max=cu.numel() - 2)]
+    up = torch.cat((torch.where(parents < 0, n, first + parents.long()), cu.new_tensor([n])))    # (n: no token)
+    bits = torch.zeros((n + 1, 32 * words), dtype=torch.bool, device=dev)
+    bits[t, (t - first).clamp(max=32 * words - 1)] = True
+    depth = torch.ones(n + 1, dtype=torch.int32, device=dev)
+    depth[n] = 0
+    for _ in range(max(1, max_seqlen_q).bit_length()):           # twice as many ancestors each time
+        bits, depth, up = bits | bits[up], depth + depth[up], up[up]
+    power = torch.ones(32, dtype=torch.int64, device=dev) << torch.arange(32, device=dev)
+    word = (bits[:n].unflatten(1, (words, 32)).long() * power).sum(-1)
+    return torch.where(word >= 1 << 31, word - (1 << 32), word).to(torch.int32), depth[:n] - 1
+
+
+def forward_paged_tree(q, k_cache, v_cache, block_table, cu_seqlens, seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
+                       tree=None, scale: float | None = None, stream=None, workspace=None):
+    """Packed queries [total, H, d] over the bf16 paged cache, grouped heads: every token sees what is cached in
+    front of the step, and of the step's tokens those that ``tree`` names (see fa_fwd_paged_tree; None: those up to
+    its own) -> (O [total, H, d], lse [H, total])."""
+    return (_native or _binding()).tree(q, k_cache, v_cache, None, None, tree, cu_seqlens, seqlens_k, block_table,
+                                        max_seqlen_q, max_seqlen_k, scale, workspace, stream, True)
+
+
+def accept_paged(k_cache, v_cache, block_table, cu_seqlens, seqlens_k, accepted, n_accepted, stream=None):
+    """Keeps the tokens accepted[b, :n_accepted[b]] (ascending) of each sequence's step in the bf16 cache, at the
+    front of the step's places -> the sequences' new lengths."""
+    return (_native or _binding()).accept(k_cache, v_cache, None, accepted, n_accepted, cu_seqlens, seqlens_k, block_table,
+                                          stream)
+
+
+def weigh_paged(q, lse, k_cache, weights, block_table, cu_seqlens, seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
+                weighed=None, decay: float = 1.0, scale: float | None = None, stream=None):
+    """Adds to ``weights`` [num_blocks, H_kv, block_size] the attention that each cached token draws from a step's
+    queries (see fa_weigh_paged)."""
+    (_native or _binding()).weigh(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q,
+                                  max_seqlen_k, scale, decay, stream)
+
+
+def evict_paged(k_cache, v_cache, weights, block_table, new_table, seqlens_k, budgets, max_seqlen_k: int, max_kept: int,
+                keep_first: int = 0, keep_last: int = 0, stream=None):
+    """Cuts sequences down to budgets[b] tokens a key head, by weight, into the pages of ``new_table`` (see
+    fa_evict_paged) -> (kept [n_seqs, H_kv, max_kept], the sequences' new lengths)."""
+    return (_native or _binding()).evict(k_cache, v_cache, weights, None, None, budgets, seqlens_k, block_table, new_table,
+                                         max_seqlen_k, max_kept, keep_first, keep_last, stream)

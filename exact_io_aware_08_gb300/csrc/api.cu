@@ -564,8 +564,8 @@ fa_status_t check_index_arrays(const int* a, const int* b, const int* c) {
 }
 
 fa_status_t append(const void* q, const void* k, const void* v, void* q_out, void* k_cache, void* k_scales,
-                   void* v_cache, void* v_scales, bool q4, const float* cos, const float* sin, const int* cu,
-                   const int* seqlens, const int* table, int n_seqs, int H, int H_kv, int total,
+                   void* v_cache, void* v_scales, bool q4, const float* cos, const float* sin, const int* positions,
+                   const int* cu, const int* seqlens, const int* table, int n_seqs, int H, int H_kv, int total,
                    long long q_stride, long long k_stride, long long v_stride, int max_blocks, int block_size,
                    int num_blocks, int d, int rotary, int interleaved, int n_positions, float descale_k,
                    float descale_v, void* stream, const char* name) {
@@ -589,6 +589,7 @@ fa_status_t append(const void* q, const void* k, const void* v, void* q_out, voi
       (rotary > 0 && (!cos || !sin)))
     return fail(FA_ERR_INVALID_ARG, "null pointer argument");
   if ((st = check_index_arrays(cu, seqlens, table)) != FA_OK) return st;
+  if (positions && !aligned4(positions)) return fail(FA_ERR_INVALID_ARG, "positions must be 4-byte aligned");
   if (rotary > 0 && n_positions < 1) return fail(FA_ERR_INVALID_ARG, "n_positions must be >= 1 (got %d)", n_positions);
   for (const void* x : {q, k, v, static_cast<const void*>(q_out), static_cast<const void*>(k_cache),
                         static_cast<const void*>(v_cache), static_cast<const void*>(k_scales),
@@ -608,6 +609,7 @@ fa_status_t append(const void* q, const void* k, const void* v, void* q_out, voi
   a.n_seqs = n_seqs; a.H = H; a.H_kv = H_kv; a.total = total; a.max_blocks = max_blocks;
   a.block_size = block_size; a.num_blocks = num_blocks; a.d = d; a.rotary = rotary;
   a.interleaved = interleaved; a.n_positions = n_positions; a.descale_k = descale_k; a.descale_v = descale_v;
+  a.positions = rotary > 0 ? positions : nullptr;
   cudaError_t e = fa::launch_append(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
 }
@@ -687,9 +689,52 @@ fa_status_t attend_q4(const void* q, const void* k_codes, const void* k_scales, 
   return e == cudaSuccess ? FA_OK : cuda_fail(e, name);
 }
 
+// Shape checks of the calls that attend over a bf16 paged cache.
+fa_status_t check_step(int n_seqs, int H, int H_kv, int total, int max_seqlen_q, int max_blocks, int block_size,
+                       int num_blocks, int max_seqlen_k, int d, float scale) {
+  fa_status_t st = check_paged(n_seqs, H, H_kv, d, max_blocks, block_size, num_blocks, 16);
+  if (st != FA_OK) return st;
+  if (H < 1 || H % H_kv != 0) return fail(FA_ERR_INVALID_ARG, "H must be a positive multiple of H_kv (got %d, %d)", H, H_kv);
+  if (total < 0 || max_seqlen_q < 0 || max_seqlen_k < 0)
+    return fail(FA_ERR_INVALID_ARG, "totals and max sequence lengths must be >= 0");
+  if (max_seqlen_q > total) return fail(FA_ERR_INVALID_ARG, "max_seqlen exceeds the total token count");
+  if (static_cast<long long>(max_seqlen_k) > static_cast<long long>(max_blocks) * block_size)
+    return fail(FA_ERR_INVALID_ARG, "max_seqlen_k=%d exceeds max_blocks_per_seq * block_size", max_seqlen_k);
+  if (max_seqlen_k >= (1LL << 31) / d) return fail(FA_ERR_UNSUPPORTED, "max_seqlen_k too large for d=%d", d);
+  if (static_cast<long long>(total) * H >= (1LL << 31)) return fail(FA_ERR_UNSUPPORTED, "total * H must be < 2^31");
+  if (!std::isfinite(scale) || !(scale >= 1e-34f) || !(scale <= 1e34f))
+    return fail(FA_ERR_INVALID_ARG, "scale must be in [1e-34, 1e34] (got %g)", static_cast<double>(scale));
+  // work items are counted in an int: (sequence, key head) pairs times their key tiles and row blocks
+  const long long pairs = static_cast<long long>(n_seqs) * H_kv, steps = max_seqlen_k / 128 + 1;
+  const long long blocks = (static_cast<long long>(H / H_kv) * max_seqlen_q + 255) / 256;
+  if (pairs * steps >= (1LL << 31) || pairs * blocks >= (1LL << 30))
+    return fail(FA_ERR_UNSUPPORTED, "too many (sequence, key head) pairs for these lengths");
+  return FA_OK;
+}
+
+// Pools whose rows are moved.
+fa_status_t check_pool(int n_seqs, int H_kv, int d, int max_blocks, int block_size, int num_blocks) {
+  fa_status_t st = check_paged(n_seqs, 0, H_kv, d, max_blocks, block_size, num_blocks, 1);
+  if (st != FA_OK) return st;
+  if (n_seqs > 65535) return fail(FA_ERR_UNSUPPORTED, "n_seqs must be <= 65535 (got %d)", n_seqs);
+  return FA_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+fa_status_t fa_append_paged_at(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                               fa_bf16_t* k_cache, fa_bf16_t* v_cache, const float* cos, const float* sin,
+                               const int* positions, const int* cu_seqlens, const int* seqlens_k,
+                               const int* block_table, int n_seqs, int H, int H_kv, int total, long long q_stride,
+                               long long k_stride, long long v_stride, int max_blocks_per_seq, int block_size,
+                               int num_blocks, int d, int rotary_dim, int interleaved, int n_positions, void* stream) {
+  return append(q, k, v, q_out, k_cache, nullptr, v_cache, nullptr, false, cos, sin, positions, cu_seqlens, seqlens_k,
+                block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq,
+                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, 1.f, 1.f, stream,
+                "fa_append_paged launch");
+}
 
 fa_status_t fa_append_paged(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
                             fa_bf16_t* k_cache, fa_bf16_t* v_cache, const float* cos, const float* sin,
@@ -697,10 +742,23 @@ fa_status_t fa_append_paged(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf1
                             int H, int H_kv, int total, long long q_stride, long long k_stride,
                             long long v_stride, int max_blocks_per_seq, int block_size, int num_blocks, int d,
                             int rotary_dim, int interleaved, int n_positions, void* stream) {
-  return append(q, k, v, q_out, k_cache, nullptr, v_cache, nullptr, false, cos, sin, cu_seqlens, seqlens_k,
+  return fa_append_paged_at(q, k, v, q_out, k_cache, v_cache, cos, sin, nullptr, cu_seqlens, seqlens_k, block_table,
+                            n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq, block_size,
+                            num_blocks, d, rotary_dim, interleaved, n_positions, stream);
+}
+
+fa_status_t fa_append_paged_q4_at(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                                  fa_e2m1x2_t* k_codes, fa_e4m3_t* k_scales, fa_e2m1x2_t* v_codes,
+                                  fa_e4m3_t* v_scales, const float* cos, const float* sin, const int* positions,
+                                  const int* cu_seqlens, const int* seqlens_k, const int* block_table, int n_seqs,
+                                  int H, int H_kv, int total, long long q_stride, long long k_stride,
+                                  long long v_stride, int max_blocks_per_seq, int block_size, int num_blocks, int d,
+                                  int rotary_dim, int interleaved, int n_positions, float descale_k, float descale_v,
+                                  void* stream) {
+  return append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, true, cos, sin, positions, cu_seqlens, seqlens_k,
                 block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq,
-                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, 1.f, 1.f, stream,
-                "fa_append_paged launch");
+                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, descale_k, descale_v, stream,
+                "fa_append_paged_q4 launch");
 }
 
 fa_status_t fa_append_paged_q4(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
@@ -710,10 +768,10 @@ fa_status_t fa_append_paged_q4(const fa_bf16_t* q, const fa_bf16_t* k, const fa_
                                int total, long long q_stride, long long k_stride, long long v_stride,
                                int max_blocks_per_seq, int block_size, int num_blocks, int d, int rotary_dim,
                                int interleaved, int n_positions, float descale_k, float descale_v, void* stream) {
-  return append(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, true, cos, sin, cu_seqlens, seqlens_k,
-                block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride, max_blocks_per_seq,
-                block_size, num_blocks, d, rotary_dim, interleaved, n_positions, descale_k, descale_v, stream,
-                "fa_append_paged_q4 launch");
+  return fa_append_paged_q4_at(q, k, v, q_out, k_codes, k_scales, v_codes, v_scales, cos, sin, nullptr, cu_seqlens,
+                               seqlens_k, block_table, n_seqs, H, H_kv, total, q_stride, k_stride, v_stride,
+                               max_blocks_per_seq, block_size, num_blocks, d, rotary_dim, interleaved, n_positions,
+                               descale_k, descale_v, stream);
 }
 
 fa_status_t fa_gather_paged_q4(const fa_e2m1x2_t* k_codes, const fa_e4m3_t* k_scales, const fa_e2m1x2_t* v_codes,
@@ -772,6 +830,106 @@ fa_status_t fa_fwd_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, cons
                    scale, descale_k, descale_v, causal, n_splits, ws, ws_bytes, stream, "fa_fwd_paged_q4 launch");
 }
 
+size_t fa_fwd_paged_tree_workspace_size(int H, int H_kv, int max_seqlen_q, int d) {
+  if (H < 1 || H_kv < 1 || H % H_kv != 0 || max_seqlen_q < 0 || (d != 64 && d != 128)) return 0;
+  return fa::tree_part_bytes(H, H_kv, max_seqlen_q, d);
+}
+
+fa_status_t fa_fwd_paged_tree(const fa_bf16_t* q, const fa_bf16_t* k_cache, const fa_bf16_t* v_cache, fa_bf16_t* o,
+                              float* lse, const int* tree, int tree_words, const int* cu_seqlens, const int* seqlens_k,
+                              const int* block_table, int n_seqs, int H, int H_kv, int total, int max_seqlen_q,
+                              int max_blocks_per_seq, int block_size, int num_blocks, int max_seqlen_k, int d,
+                              float scale, void* ws, size_t ws_bytes, void* stream) {
+  fa_status_t st = check_step(n_seqs, H, H_kv, total, max_seqlen_q, max_blocks_per_seq, block_size, num_blocks, max_seqlen_k, d, scale);
+  if (st != FA_OK) return st;
+  if (tree && (tree_words < 1 || 32LL * tree_words < max_seqlen_q))
+    return fail(FA_ERR_INVALID_ARG, "a tree of %d words a token does not cover max_seqlen_q=%d", tree_words, max_seqlen_q);
+  if (total == 0 || max_seqlen_q == 0) return FA_OK;
+  if (!q || !k_cache || !v_cache || !o || !lse) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  for (const void* x : {static_cast<const void*>(q), static_cast<const void*>(k_cache), static_cast<const void*>(v_cache),
+                        static_cast<const void*>(o), static_cast<const void*>(lse)})
+    if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  if (tree && !aligned4(tree)) return fail(FA_ERR_INVALID_ARG, "tree must be 4-byte aligned");
+  if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
+  const size_t need = fa::tree_part_bytes(H, H_kv, max_seqlen_q, d);
+  if (!ws || ws_bytes < need || !aligned16(ws))
+    return fail(FA_ERR_WORKSPACE, "workspace must be >= %zu bytes and 16-byte aligned (got %zu)", need, ws_bytes);
+  fa::PagedTreeArgs a{q, k_cache, v_cache, o, lse, static_cast<float*>(ws), tree, cu_seqlens, seqlens_k, block_table,
+                      tree_words, n_seqs, H, H_kv, total, max_seqlen_q, max_seqlen_k, d, num_blocks, block_size,
+                      max_blocks_per_seq, scale};
+  cudaError_t e = fa::launch_attend_tree(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_fwd_paged_tree launch");
+}
+
+fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens_out, const int* accepted,
+                            const int* n_accepted, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
+                            int n_seqs, int H_kv, int max_accepted, int max_blocks_per_seq, int block_size,
+                            int num_blocks, int d, void* stream) {
+  fa_status_t st = check_pool(n_seqs, H_kv, d, max_blocks_per_seq, block_size, num_blocks);
+  if (st != FA_OK) return st;
+  if (max_accepted < 0) return fail(FA_ERR_INVALID_ARG, "max_accepted must be >= 0 (got %d)", max_accepted);
+  if (!k_cache || !v_cache || !seqlens_out || !n_accepted || (max_accepted > 0 && !accepted))
+    return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
+  if (!aligned4(seqlens_out) || !aligned4(accepted) || !aligned4(n_accepted))
+    return fail(FA_ERR_INVALID_ARG, "accepted, n_accepted and the new lengths must be 4-byte aligned");
+  if (seqlens_out == seqlens_k) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  fa::AcceptArgs a{k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seqlens, seqlens_k, block_table,
+                   n_seqs, H_kv, max_accepted, max_blocks_per_seq, block_size, num_blocks, d};
+  cudaError_t e = fa::launch_accept(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_accept_paged launch");
+}
+
+fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t* k_cache, float* weights,
+                           const int* weighed, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
+                           int n_seqs, int H, int H_kv, int total, int max_seqlen_q, int max_blocks_per_seq,
+                           int block_size, int num_blocks, int max_seqlen_k, int d, float scale, float decay, void* stream) {
+  fa_status_t st = check_step(n_seqs, H, H_kv, total, max_seqlen_q, max_blocks_per_seq, block_size, num_blocks, max_seqlen_k, d, scale);
+  if (st != FA_OK) return st;
+  if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads a key head (got %d)", H / H_kv);
+  if (!(decay >= 0.f) || !(decay <= 1.f)) return fail(FA_ERR_INVALID_ARG, "decay must be in [0, 1] (got %g)", static_cast<double>(decay));
+  if (total == 0 || max_seqlen_q == 0) return FA_OK;
+  if (!q || !lse || !k_cache || !weights) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  for (const void* x : {static_cast<const void*>(q), static_cast<const void*>(lse), static_cast<const void*>(k_cache), static_cast<const void*>(weights)})
+    if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
+  if (weighed && !aligned4(weighed)) return fail(FA_ERR_INVALID_ARG, "weighed must be 4-byte aligned");
+  fa::WeighArgs a{q, k_cache, lse, weights, cu_seqlens, seqlens_k, weighed, block_table, n_seqs, H, H_kv, total,
+                  max_seqlen_q, max_seqlen_k, d, num_blocks, block_size, max_blocks_per_seq, scale, decay};
+  cudaError_t e = fa::launch_weigh(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_weigh_paged launch");
+}
+
+fa_status_t fa_evict_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, float* weights, int* kept, int* seqlens_out,
+                           const int* budgets, const int* seqlens_k, const int* block_table, const int* new_table,
+                           int n_seqs, int H_kv, int max_seqlen_k, int max_kept, int keep_first, int keep_last,
+                           int max_blocks_per_seq, int new_max_blocks_per_seq, int block_size, int num_blocks, int d,
+                           void* stream) {
+  fa_status_t st = check_pool(n_seqs, H_kv, d, max_blocks_per_seq, block_size, num_blocks);
+  if (st != FA_OK) return st;
+  if (max_seqlen_k < 0 || max_kept < 0 || keep_first < 0 || keep_last < 0 || new_max_blocks_per_seq < 0)
+    return fail(FA_ERR_INVALID_ARG, "lengths and counts must be >= 0");
+  if (static_cast<long long>(max_seqlen_k) > static_cast<long long>(max_blocks_per_seq) * block_size)
+    return fail(FA_ERR_INVALID_ARG, "max_seqlen_k=%d exceeds max_blocks_per_seq * block_size", max_seqlen_k);
+  if (static_cast<long long>(max_kept) > static_cast<long long>(new_max_blocks_per_seq) * block_size)
+    return fail(FA_ERR_INVALID_ARG, "max_kept=%d exceeds new_max_blocks_per_seq * block_size", max_kept);
+  if (static_cast<long long>(new_max_blocks_per_seq) * block_size >= (1LL << 31) ||
+      static_cast<long long>(n_seqs) * H_kv * (static_cast<long long>(max_kept) / 16 + 1) >= (1LL << 31))
+    return fail(FA_ERR_UNSUPPORTED, "n_seqs * H_kv * max_kept too large");
+  if (!k_cache || !v_cache || !weights || !seqlens_out || (max_kept > 0 && (!kept || !new_table)))
+    return fail(FA_ERR_INVALID_ARG, "null pointer argument");
+  if ((st = check_index_arrays(budgets, seqlens_k, block_table)) != FA_OK) return st;
+  if (!aligned4(new_table) || !aligned4(kept) || !aligned4(seqlens_out))
+    return fail(FA_ERR_INVALID_ARG, "new_table, kept and the new lengths must be 4-byte aligned");
+  if (seqlens_out == seqlens_k || seqlens_out == budgets) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
+  fa::EvictArgs a{k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table, n_seqs, H_kv,
+                  max_seqlen_k, max_kept, keep_first, keep_last, max_blocks_per_seq, new_max_blocks_per_seq, block_size, num_blocks, d};
+  cudaError_t e = fa::launch_evict(a, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_evict_paged launch");
+}
+
 fa_status_t fa_debug_counters(unsigned long long* device_counters) {
   fa::g_debug_counters = device_counters;
   return FA_OK;
@@ -793,7 +951,8 @@ fa_status_t fa_sync_status(void* stream) {
   cudaError_t (*fetch[])(cudaStream_t, unsigned int*, int*) = {
       fa::status_fetch_fwd, fa::status_fetch_bwd, fa::status_fetch_decode,
       fa::status_fetch_selftest, fa::status_fetch_paged, fa::status_fetch_attend_q4,
-      fa::status_fetch_attend_q4_tile};
+      fa::status_fetch_attend_q4_tile, fa::status_fetch_attend_tree, fa::status_fetch_weigh,
+      fa::status_fetch_evict};
   for (auto f : fetch) {
     cudaError_t e = f(s, &c, &w);
     if (e != cudaSuccess) return cuda_fail(e, "fa_sync_status");

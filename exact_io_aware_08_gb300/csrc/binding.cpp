@@ -29,13 +29,18 @@
 namespace {
 
 struct Library {
-  decltype(&fa_append_paged) append = nullptr;
-  decltype(&fa_append_paged_q4) append_q4 = nullptr;
+  decltype(&fa_append_paged_at) append = nullptr;
+  decltype(&fa_append_paged_q4_at) append_q4 = nullptr;
   decltype(&fa_gather_paged_q4) gather_q4 = nullptr;
   decltype(&fa_decode_paged_q4) decode_q4 = nullptr;
   decltype(&fa_decode_paged_q4_workspace_size) decode_q4_ws = nullptr;
   decltype(&fa_fwd_paged_q4) fwd_q4 = nullptr;
   decltype(&fa_fwd_paged_q4_workspace_size) fwd_q4_ws = nullptr;
+  decltype(&fa_fwd_paged_tree) tree = nullptr;
+  decltype(&fa_fwd_paged_tree_workspace_size) tree_ws = nullptr;
+  decltype(&fa_accept_paged) accept = nullptr;
+  decltype(&fa_weigh_paged) weigh = nullptr;
+  decltype(&fa_evict_paged) evict = nullptr;
   decltype(&fa_last_error_message) message = nullptr;
 };
 Library lib;
@@ -129,6 +134,21 @@ const fa_bf16_t* tokens(const at::Tensor& t, const char* name, std::initializer_
   *stride = t.size(0) > 1 ? t.stride(0) : t.size(1) * t.size(2);   // (a single token's is any number)
   return static_cast<const fa_bf16_t*>(t.data_ptr());
 }
+
+struct Cache16 {
+  int device = -1;
+  int64_t blocks, block_size, heads, d;
+  fa_bf16_t *k, *v = nullptr;
+  Cache16(PyObject* k_cache, PyObject* v_cache) {                // (v_cache null: the keys alone)
+    const at::Tensor& c = ranked(k_cache, "k_cache", 4, "[num_blocks, block_size, H_kv, d]");
+    blocks = c.size(0);
+    block_size = c.size(1);
+    heads = c.size(2);
+    d = c.size(3);
+    k = dense<fa_bf16_t>(c, "k_cache", at::kBFloat16, {blocks, block_size, heads, d}, device);
+    if (v_cache) v = dense<fa_bf16_t>(tensor(v_cache, "v_cache"), "v_cache", at::kBFloat16, {blocks, block_size, heads, d}, device);
+  }
+};
 
 struct Cache4 {
   int device = -1;
@@ -256,10 +276,10 @@ void count(Py_ssize_t n, Py_ssize_t want) {
 }
 
 // (q, k, v, q_out, k_cache, k_scales, v_cache, v_scales, cos, sin, cu_seqlens, seqlens_k, block_table,
-//  descale_k, descale_v, interleaved, stream): k_scales None for the bf16 cache; q_out None with q: made.
+//  descale_k, descale_v, interleaved, stream, positions): k_scales None for the bf16 cache; q_out None with q: made.
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_BEGIN
-  count(n, 17);
+  count(n, 18);
   const bool q4 = given(a[5]);
   int device = -1;
   int64_t blocks, heads, block_size, d;
@@ -270,10 +290,9 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     device = c.device; blocks = c.blocks; heads = c.heads; block_size = c.block_size; d = c.d;
     kc = c.k; vc = c.v; ks = c.ks; vs = c.vs;
   } else {
-    const at::Tensor& c = ranked(a[4], "k_cache", 4, "[num_blocks, block_size, H_kv, d]");
-    blocks = c.size(0); block_size = c.size(1); heads = c.size(2); d = c.size(3);
-    kc = dense<void>(c, "k_cache", at::kBFloat16, {blocks, block_size, heads, d}, device);
-    vc = dense<void>(tensor(a[6], "v_cache"), "v_cache", at::kBFloat16, {blocks, block_size, heads, d}, device);
+    const Cache16 c(a[4], a[6]);
+    device = c.device; blocks = c.blocks; heads = c.heads; block_size = c.block_size; d = c.d;
+    kc = c.k; vc = c.v;
   }
   const at::Tensor& k = ranked(a[1], "k", 3, "[total, H_kv, d]");
   const at::Tensor& table = ranked(a[12], "block_table", 2, "[n_seqs, max_blocks]");
@@ -311,12 +330,13 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int ints[] = {narrow(seqs, "n_seqs"), narrow(H, "H"), narrow(heads, "H_kv"), narrow(total, "total"), narrow(table.size(1), "max_blocks"),
                       narrow(block_size, "block_size"), narrow(blocks, "num_blocks"), narrow(d, "d"), narrow(2 * half, "rotary_dim"),
                       truth(a[15], "interleaved") ? 1 : 0, narrow(positions, "n_positions")};
+  const int* at = given(a[17]) ? dense<int>(tensor(a[17], "positions"), "positions", at::kInt, {total}, device) : nullptr;
   if (q4)
-    done(lib.append_q4(pq, pk, pv, po, static_cast<fa_e2m1x2_t*>(kc), ks, static_cast<fa_e2m1x2_t*>(vc), vs, cos, sin, cu, lens, tab, ints[0],
+    done(lib.append_q4(pq, pk, pv, po, static_cast<fa_e2m1x2_t*>(kc), ks, static_cast<fa_e2m1x2_t*>(vc), vs, cos, sin, at, cu, lens, tab, ints[0],
                        ints[1], ints[2], ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10],
                        number(a[13], "descale_k"), number(a[14], "descale_v"), on.stream));
   else
-    done(lib.append(pq, pk, pv, po, static_cast<fa_bf16_t*>(kc), static_cast<fa_bf16_t*>(vc), cos, sin, cu, lens, tab, ints[0], ints[1], ints[2],
+    done(lib.append(pq, pk, pv, po, static_cast<fa_bf16_t*>(kc), static_cast<fa_bf16_t*>(vc), cos, sin, at, cu, lens, tab, ints[0], ints[1], ints[2],
                     ints[3], sq, sk, sv, ints[4], ints[5], ints[6], ints[7], ints[8], ints[9], ints[10], on.stream));
   if (!q_out.defined()) Py_RETURN_NONE;
   if (given(a[3])) {
@@ -433,6 +453,128 @@ PyObject* forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_END
 }
 
+// A scale that is given, or 1 / sqrt(d).
+float scale_of(PyObject* o, int64_t d) { return given(o) ? number(o, "scale") : 1.f / std::sqrt(static_cast<float>(d)); }
+
+// (q, k_cache, v_cache, o, lse, tree, cu_seqlens, seqlens_k, block_table, max_seqlen_q, max_seqlen_k, scale, ws,
+//  stream, own): as decode(); tree may be None.
+PyObject* tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FA_BEGIN
+  count(n, 15);
+  const bool own = truth(a[14], "own");
+  Cache16 c(a[1], a[2]);
+  const at::Tensor& q = ranked(a[0], "q", 3, "[total, H, d]");
+  const at::Tensor& table = ranked(a[8], "block_table", 2, "[n_seqs, max_blocks]");
+  const int64_t total = q.size(0), H = q.size(1), seqs = table.size(0);
+  const fa_bf16_t* pq = dense<fa_bf16_t>(q, "q", at::kBFloat16, {total, H, c.d}, c.device);
+  const int* bits = nullptr;
+  int words = 0;
+  if (given(a[5])) {
+    const at::Tensor& t = ranked(a[5], "tree", 2, "[total, words]");
+    words = narrow(t.size(1), "words");
+    bits = dense<int>(t, "tree", at::kInt, {total, t.size(1)}, c.device);
+    if (words == 0 && total > 0) refuse("tree must have a word for 32 tokens, has none");
+  }
+  const int* cu = dense<int>(tensor(a[6], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, c.device);
+  const int* lens = dense<int>(tensor(a[7], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
+  const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
+  const int max_q = narrow(integer(a[9], "max_seqlen_q"), "max_seqlen_q"), max_k = narrow(integer(a[10], "max_seqlen_k"), "max_seqlen_k");
+  const int h = narrow(H, "H"), hkv = narrow(c.heads, "H_kv"), d = narrow(c.d, "d");
+  const Where on(a[13], c.device);
+  const at::Tensor o = own && !given(a[3]) ? make({total, H, c.d}, at::kBFloat16, c.device) : tensor(a[3], "o");
+  const at::Tensor lse = own && !given(a[4]) ? make({H, total}, at::kFloat, c.device) : tensor(a[4], "lse");
+  fa_bf16_t* po = dense<fa_bf16_t>(o, "o", at::kBFloat16, {total, H, c.d}, c.device);
+  float* pl = dense<float>(lse, "lse", at::kFloat, {H, total}, c.device);
+  const Workspace ws(a[12], own ? lib.tree_ws(h, hkv, max_q, d) : 0, c.device, own);
+  done(lib.tree(pq, c.k, c.v, po, pl, bits, words, cu, lens, tab, narrow(seqs, "n_seqs"), h, hkv, narrow(total, "total"), max_q,
+                narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, d,
+                scale_of(a[11], c.d), ws.ptr, ws.bytes, on.stream));
+  return two(o, a[3], lse, a[4]);
+  FA_END
+}
+
+PyObject* one(const at::Tensor& x, PyObject* had) {
+  if (!given(had)) return THPVariable_Wrap(x);
+  Py_INCREF(had);
+  return had;
+}
+
+// (k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seqlens, seqlens_k, block_table, stream): seqlens_out None: made.
+PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FA_BEGIN
+  count(n, 9);
+  Cache16 c(a[0], a[1]);
+  const at::Tensor& table = ranked(a[7], "block_table", 2, "[n_seqs, max_blocks]");
+  const at::Tensor& path = ranked(a[3], "accepted", 2, "[n_seqs, max_accepted]");
+  const int64_t seqs = table.size(0), deep = path.size(1);
+  const int* pa = dense<int>(path, "accepted", at::kInt, {seqs, deep}, c.device);
+  const int* pn = dense<int>(tensor(a[4], "n_accepted"), "n_accepted", at::kInt, {seqs}, c.device);
+  const int* cu = dense<int>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, c.device);
+  const int* lens = dense<int>(tensor(a[6], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
+  const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
+  const Where on(a[8], c.device);
+  const at::Tensor out = given(a[2]) ? tensor(a[2], "seqlens_out") : make({seqs}, at::kInt, c.device);
+  int* po = dense<int>(out, "seqlens_out", at::kInt, {seqs}, c.device);
+  done(lib.accept(c.k, c.v, po, pa, pn, cu, lens, tab, narrow(seqs, "n_seqs"), narrow(c.heads, "H_kv"), narrow(deep, "max_accepted"),
+                  narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), narrow(c.d, "d"),
+                  on.stream));
+  return one(out, a[2]);
+  FA_END
+}
+
+// (q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q, max_seqlen_k, scale, decay, stream)
+PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FA_BEGIN
+  count(n, 13);
+  Cache16 c(a[2], nullptr);
+  const at::Tensor& q = ranked(a[0], "q", 3, "[total, H, d]");
+  const at::Tensor& table = ranked(a[7], "block_table", 2, "[n_seqs, max_blocks]");
+  const int64_t total = q.size(0), H = q.size(1), seqs = table.size(0);
+  const fa_bf16_t* pq = dense<fa_bf16_t>(q, "q", at::kBFloat16, {total, H, c.d}, c.device);
+  const float* pl = dense<float>(tensor(a[1], "lse"), "lse", at::kFloat, {H, total}, c.device);
+  float* pw = dense<float>(tensor(a[3], "weights"), "weights", at::kFloat, {c.blocks, c.heads, c.block_size}, c.device);
+  const int* had = given(a[4]) ? dense<int>(tensor(a[4], "weighed"), "weighed", at::kInt, {seqs}, c.device) : nullptr;
+  const int* cu = dense<int>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, c.device);
+  const int* lens = dense<int>(tensor(a[6], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
+  const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
+  const Where on(a[12], c.device);
+  done(lib.weigh(pq, pl, c.k, pw, had, cu, lens, tab, narrow(seqs, "n_seqs"), narrow(H, "H"), narrow(c.heads, "H_kv"), narrow(total, "total"),
+                 narrow(integer(a[8], "max_seqlen_q"), "max_seqlen_q"), narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"),
+                 narrow(c.blocks, "num_blocks"), narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k"), narrow(c.d, "d"), scale_of(a[10], c.d),
+                 number(a[11], "decay"), on.stream));
+  Py_RETURN_NONE;
+  FA_END
+}
+
+// (k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table, max_seqlen_k, max_kept, keep_first,
+//  keep_last, stream): kept and seqlens_out None: made.
+PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  FA_BEGIN
+  count(n, 14);
+  Cache16 c(a[0], a[1]);
+  const at::Tensor& table = ranked(a[7], "block_table", 2, "[n_seqs, max_blocks]");
+  const at::Tensor& fresh = ranked(a[8], "new_table", 2, "[n_seqs, max_blocks]");
+  const int64_t seqs = table.size(0);
+  float* pw = dense<float>(tensor(a[2], "weights"), "weights", at::kFloat, {c.blocks, c.heads, c.block_size}, c.device);
+  const int* bud = dense<int>(tensor(a[5], "budgets"), "budgets", at::kInt, {seqs}, c.device);
+  const int* lens = dense<int>(tensor(a[6], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
+  const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
+  const int* to = dense<int>(fresh, "new_table", at::kInt, {seqs, fresh.size(1)}, c.device);
+  const int max_kept = narrow(integer(a[10], "max_kept"), "max_kept");
+  if (max_kept < 0) refuse("max_kept must be >= 0 (got %d)", max_kept);
+  const Where on(a[13], c.device);
+  const at::Tensor kept = given(a[3]) ? tensor(a[3], "kept") : make({seqs, c.heads, max_kept}, at::kInt, c.device);
+  const at::Tensor out = given(a[4]) ? tensor(a[4], "seqlens_out") : make({seqs}, at::kInt, c.device);
+  int* pk = dense<int>(kept, "kept", at::kInt, {seqs, c.heads, max_kept}, c.device);
+  int* po = dense<int>(out, "seqlens_out", at::kInt, {seqs}, c.device);
+  done(lib.evict(c.k, c.v, pw, pk, po, bud, lens, tab, to, narrow(seqs, "n_seqs"), narrow(c.heads, "H_kv"), narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k"),
+                 max_kept, narrow(integer(a[11], "keep_first"), "keep_first"), narrow(integer(a[12], "keep_last"), "keep_last"),
+                 narrow(table.size(1), "max_blocks"), narrow(fresh.size(1), "new_max_blocks"), narrow(c.block_size, "block_size"),
+                 narrow(c.blocks, "num_blocks"), narrow(c.d, "d"), on.stream));
+  return two(kept, a[3], out, a[4]);
+  FA_END
+}
+
 // (FaError, handle of libfa.so)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 2) return PyErr_Format(PyExc_TypeError, "bind(FaError, handle)");
@@ -443,13 +585,18 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     f = reinterpret_cast<std::remove_reference_t<decltype(f)>>(dlsym(h, name));
     ok = ok && f;
   };
-  find(lib.append, "fa_append_paged");
-  find(lib.append_q4, "fa_append_paged_q4");
+  find(lib.append, "fa_append_paged_at");
+  find(lib.append_q4, "fa_append_paged_q4_at");
   find(lib.gather_q4, "fa_gather_paged_q4");
   find(lib.decode_q4, "fa_decode_paged_q4");
   find(lib.decode_q4_ws, "fa_decode_paged_q4_workspace_size");
   find(lib.fwd_q4, "fa_fwd_paged_q4");
   find(lib.fwd_q4_ws, "fa_fwd_paged_q4_workspace_size");
+  find(lib.tree, "fa_fwd_paged_tree");
+  find(lib.tree_ws, "fa_fwd_paged_tree_workspace_size");
+  find(lib.accept, "fa_accept_paged");
+  find(lib.weigh, "fa_weigh_paged");
+  find(lib.evict, "fa_evict_paged");
   find(lib.message, "fa_last_error_message");
   if (!ok) return PyErr_Format(PyExc_RuntimeError, "libfa.so lacks a paged-cache function");
   Py_INCREF(a[0]);
@@ -464,7 +611,9 @@ PyCFunction fast() {
 
 PyMethodDef methods[] = {{"bind", fast<bind>(), METH_FASTCALL, nullptr},     {"append", fast<append>(), METH_FASTCALL, nullptr},
                          {"gather", fast<gather>(), METH_FASTCALL, nullptr}, {"decode", fast<decode>(), METH_FASTCALL, nullptr},
-                         {"forward", fast<forward>(), METH_FASTCALL, nullptr}, {nullptr, nullptr, 0, nullptr}};
+                         {"forward", fast<forward>(), METH_FASTCALL, nullptr}, {"tree", fast<tree>(), METH_FASTCALL, nullptr},
+                         {"accept", fast<accept>(), METH_FASTCALL, nullptr}, {"weigh", fast<weigh>(), METH_FASTCALL, nullptr},
+                         {"evict", fast<evict>(), METH_FASTCALL, nullptr},     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

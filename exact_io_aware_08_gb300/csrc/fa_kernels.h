@@ -157,6 +157,7 @@ struct AppendArgs {
   long long q_stride, k_stride, v_stride;
   int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, d, rotary, interleaved, n_positions;
   float descale_k, descale_v;
+  const int* positions;         // [total] for the rotation, or null: a token's place in its sequence
 };
 
 struct GatherArgs {
@@ -182,6 +183,61 @@ struct PagedQ4Args {
   float scale, descale_k, descale_v;
   int n_splits, chunk;
 };
+
+// Attention of packed queries [total, H, d] over the bf16 paged cache [num_blocks, block_size, H_kv, d].
+struct PagedTreeArgs {
+  const void *q, *k_cache, *v_cache;
+  void* o;
+  float *lse, *part;            // [H, total]; states of cut row blocks, d + 4 floats a row
+  const int *tree, *cu, *seqlens, *block_table;               // tree [total, words] or null
+  int words, n_seqs, H, H_kv, total, max_q, max_k, d, num_blocks, block_size, max_blocks;
+  float scale;
+};
+
+// Weights of cached tokens [num_blocks, H_kv, block_size], brought up to a step's queries.
+struct WeighArgs {
+  const void *q, *k_cache;
+  const float* lse;
+  float* weights;
+  const int *cu, *seqlens, *weighed, *block_table;            // weighed [n_seqs] or null
+  int n_seqs, H, H_kv, total, max_q, max_k, d, num_blocks, block_size, max_blocks;
+  float scale, decay;
+};
+
+// Tokens of the heaviest weights into new pages.
+struct EvictArgs {
+  void *k_cache, *v_cache;
+  float* weights;
+  int *kept, *seqlens_out;      // [n_seqs, H_kv, max_kept], [n_seqs]
+  const int *budgets, *seqlens, *block_table, *new_table;
+  int n_seqs, H_kv, max_k, max_kept, keep_first, keep_last, max_blocks, new_max_blocks, block_size, num_blocks, d;
+};
+
+// Some of a step's tokens to the front of its places.
+struct AcceptArgs {
+  void *k_cache, *v_cache;
+  int* seqlens_out;
+  const int *accepted, *n_accepted, *cu, *seqlens, *block_table;   // accepted [n_seqs, max_accepted]
+  int n_seqs, H_kv, max_accepted, max_blocks, block_size, num_blocks, d;
+};
+
+cudaError_t launch_attend_tree(const PagedTreeArgs& a, cudaStream_t stream);
+cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream);
+cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
+cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
+cudaError_t status_fetch_attend_tree(cudaStream_t, unsigned int*, int*);
+cudaError_t status_fetch_weigh(cudaStream_t, unsigned int*, int*);
+cudaError_t status_fetch_evict(cudaStream_t, unsigned int*, int*);
+
+// Attention over the bf16 paged cache: up to 128 or 256 rows of a key head (its query heads times a sequence's
+// query tokens) are a row block.  Where that is all of them the work is shared out to at most kTreeMaxCtas CTAs
+// that keep at most two states each; else the last row blocks are split, into as many parts as there are CTAs.
+constexpr int kTreeMaxCtas = 152;
+inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
+  const long long rows = static_cast<long long>(H / H_kv) * max_q;
+  const size_t states = rows <= 256 ? 2 * kTreeMaxCtas * static_cast<size_t>(rows) : kTreeMaxCtas * size_t(256);
+  return states * (d + 4) * sizeof(float);
+}
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream);

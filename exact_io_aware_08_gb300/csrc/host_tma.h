@@ -92,6 +92,22 @@ inline bool make_map_bf16_tok(CUtensorMap* map, const void* base, uint64_t d, ui
   return r == CUDA_SUCCESS;
 }
 
+// Packed token-major bf16 tensor [total, groups * per_group, d] as {d, per_group, groups, total}: box
+// {box_inner, box_group, 1, box_rows} covers box_rows consecutive tokens of one group's heads, token by token.
+inline bool make_map_bf16_group(CUtensorMap* map, const void* base, uint64_t d, uint64_t per_group, uint64_t groups,
+                                uint64_t total, uint32_t box_inner, uint32_t box_group, uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[4] = {d, per_group, groups, total};
+  const cuuint64_t strides[3] = {d * 2, d * per_group * 2, d * per_group * groups * 2};
+  const cuuint32_t box[4] = {box_inner, box_group, 1, box_rows};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
 // fp32 tensor {d0, d1, d2} with byte strides (stride1, stride2) for dims 1 and 2; box
 // {b0, b1, b2}; no swizzle (a row-major box in shared memory).
 // ``sw128``: the shared-memory box uses the 128-byte swizzle (inner box extent 32 floats).

@@ -1,6 +1,7 @@
 // Filling a paged key/value cache and reading a 4-bit one back.
 //
-// Append: each packed token's query and key heads are rotated by the token's position, keys and
+// Append: each packed token's query and key heads are rotated by the token's position (its place in the
+// sequence, or one that is given: a drafted token's depth, places behind evicted tokens), keys and
 // values go to the token's row of its page, in bf16 or rounded to the 4-bit format (q4.cuh).
 // Pairs (x1, x2) become (x1 c - x2 s, x2 c + x1 s) in fp32, every product and sum rounded by itself.
 // 4 bits: of 16 consecutive elements, scale = e4m3(max |x| / (6 descale)) and
@@ -27,6 +28,7 @@ struct AppendParams {
   int n_seqs, H, H_kv, total, max_blocks, block_size, num_blocks, rotary, n_positions;
   int warps_per_token;
   float descale_k, descale_v, one;
+  const int* positions;                               // [total] or null
 };
 
 constexpr int kPagedThreads = 128;
@@ -111,12 +113,14 @@ __global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_ke
     }
   }
 
+  const int given = p.positions ? __ldg(p.positions + t) : 0;
   int first, count, page, row;
   const int b = owner_of_token(p.cu, p.n_seqs, p.total, t, &first, &count, 400);
   if (b < 0) return;
   const int len = __ldg(p.seqlens + b);
   const int pos = len - count + (t - first);
-  if (len < count || (p.rotary > 0 && pos >= p.n_positions)) {
+  const int turn = p.positions ? given : pos;     // where the tables are read
+  if (len < count || (p.rotary > 0 && (turn < 0 || turn >= p.n_positions))) {
     if (lane == 0) report_device_error(FA_DEV_BAD_CONFIG, 401);
     return;
   }
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kPagedThreads, Q4 && U == 6 ? 5 : 1) append_ke
   const float2 one = make_float2(p.one, p.one);
   float2 c[4], s[4], ns[4];                        // of the lane's pairs 2 i and 2 i + 1
   if (rotates) {
-    const size_t at = static_cast<size_t>(pos) * (p.rotary / 2) + 8 * u;
+    const size_t at = static_cast<size_t>(turn) * (p.rotary / 2) + 8 * u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float4 a = __ldg(reinterpret_cast<const float4*>(p.cos + at) + i);
@@ -297,6 +301,7 @@ static cudaError_t launch_append_d(const AppendArgs& a, cudaStream_t stream) {
   p.max_blocks = a.max_blocks; p.block_size = a.block_size; p.num_blocks = a.num_blocks;
   p.rotary = a.rotary; p.n_positions = a.n_positions;
   p.descale_k = a.descale_k; p.descale_v = a.descale_v; p.one = 1.f;
+  p.positions = a.positions;
   const int per_pass = 32 / (D / 16);
   const int slots = p.H + 2 * p.H_kv;
   const long long passes = (slots + per_pass - 1) / per_pass;

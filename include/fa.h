@@ -336,9 +336,9 @@ fa_status_t fa_decode_splitkv_noalloc(const fa_bf16_t* q, const fa_bf16_t* k, co
  * is dense and may be q itself where q is dense.
  *
  * bf16 cache: k_cache, v_cache [num_blocks, block_size, H_kv, d], rounded to nearest, as
- * fa_decode_paged reads them.  That one takes single query tokens, as many key heads as query heads
- * and block_size a multiple of 64 (any will do here); it is the only call that reads these pages.  For
- * grouped heads, or several query tokens a sequence over what is cached, use the 4-bit cache.
+ * fa_decode_paged and fa_fwd_paged_tree read them.  fa_decode_paged takes single query tokens, as many key
+ * heads as query heads and block_size a multiple of 64; fa_fwd_paged_tree grouped heads, any number of query
+ * tokens and block_size a multiple of 16 (any will do here).
  *
  * 4-bit cache: codes [num_blocks, H_kv, block_size, d/2], scales [num_blocks, H_kv, block_size, d/16]:
  * a head's rows of a block are consecutive, so that the attention reads them in long runs.
@@ -369,6 +369,27 @@ fa_status_t fa_append_paged_q4(const fa_bf16_t* q, const fa_bf16_t* k, const fa_
                                int total, long long q_stride, long long k_stride, long long v_stride,
                                int max_blocks_per_seq, int block_size, int num_blocks, int d, int rotary_dim,
                                int interleaved, int n_positions, float descale_k, float descale_v, void* stream);
+
+/*
+ * fa_append_paged_at / fa_append_paged_q4_at -- the same with the positions that the rotation goes by, which are
+ * not the tokens' places in the cache where drafted tokens form a tree (a token's position is its depth) or tokens
+ * have been evicted (positions run on, places do not): positions [total] int32, row positions[t] of cos and sin for
+ * token t.  The places stay those above.  A position outside the tables is handled as above.  Null: the places.
+ */
+fa_status_t fa_append_paged_at(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                               fa_bf16_t* k_cache, fa_bf16_t* v_cache, const float* cos, const float* sin,
+                               const int* positions, const int* cu_seqlens, const int* seqlens_k,
+                               const int* block_table, int n_seqs, int H, int H_kv, int total, long long q_stride,
+                               long long k_stride, long long v_stride, int max_blocks_per_seq, int block_size,
+                               int num_blocks, int d, int rotary_dim, int interleaved, int n_positions, void* stream);
+fa_status_t fa_append_paged_q4_at(const fa_bf16_t* q, const fa_bf16_t* k, const fa_bf16_t* v, fa_bf16_t* q_out,
+                                  fa_e2m1x2_t* k_codes, fa_e4m3_t* k_scales, fa_e2m1x2_t* v_codes,
+                                  fa_e4m3_t* v_scales, const float* cos, const float* sin, const int* positions,
+                                  const int* cu_seqlens, const int* seqlens_k, const int* block_table, int n_seqs,
+                                  int H, int H_kv, int total, long long q_stride, long long k_stride,
+                                  long long v_stride, int max_blocks_per_seq, int block_size, int num_blocks, int d,
+                                  int rotary_dim, int interleaved, int n_positions, float descale_k, float descale_v,
+                                  void* stream);
 
 /*
  * fa_gather_paged_q4 -- read tokens of a 4-bit paged cache back as packed bf16: k, v [total, H_kv, d]
@@ -429,6 +450,88 @@ fa_status_t fa_fwd_paged_q4(const fa_bf16_t* q, const fa_e2m1x2_t* k_codes, cons
                             int block_size, int num_blocks, int max_seqlen_k, int d, float scale,
                             float descale_k, float descale_v, int causal, int n_splits, void* ws,
                             size_t ws_bytes, void* stream);
+
+/*
+ * fa_fwd_paged_tree -- attention of a step's packed queries over the bf16 paged cache that fa_append_paged filled,
+ * grouped heads (query head h reads key head h / (H / H_kv)), one token a sequence or many, with a mask among the
+ * step's own tokens: trees of drafted tokens are checked in one step.
+ *
+ *   q, o [total, H, d] bf16; lse [H, total] fp32; k_cache, v_cache [num_blocks, block_size, H_kv, d];
+ *   cu_seqlens [n_seqs + 1], seqlens_k [n_seqs], block_table [n_seqs, max_blocks_per_seq] as for fa_append_paged:
+ *   sequence b's n = cu[b+1] - cu[b] tokens are the last of its seqlens_k[b] cached ones.
+ *
+ * Query token i sees every cached token in front of the step's, and of the step's the tokens j whose bit is set in
+ * its row of tree [total, tree_words]: bit j % 32 of word j / 32, 32 * tree_words >= max_seqlen_q (bits from n on
+ * are not looked at).  tree null: the tokens j <= i.  A token that sees nothing has O = 0 and lse = -inf.  What is
+ * not seen does not count, whatever it holds.
+ *
+ * Scores and sums are fp32; weights are rounded to bf16 for the product with V, and O is divided by the sum of the
+ * rounded ones.  block_size is a positive multiple of 16; scale in [1e-34, 1e34].  The workspace (size by the query,
+ * whose arguments are the call's) does not grow with the lengths; a call uses it until its work on the stream has
+ * ended.  Rows at and behind cu[n_seqs], and those of a sequence that is rejected, are left as they are.
+ *
+ * Device-side checks: boundaries outside [0, total] or not ascending, more than max_seqlen_q tokens, a length below
+ * n or above max_seqlen_k, a block id outside [0, num_blocks): fa_sync_status reports FA_ERR_INVALID_ARG.
+ */
+size_t fa_fwd_paged_tree_workspace_size(int H, int H_kv, int max_seqlen_q, int d);
+fa_status_t fa_fwd_paged_tree(const fa_bf16_t* q, const fa_bf16_t* k_cache, const fa_bf16_t* v_cache, fa_bf16_t* o,
+                              float* lse, const int* tree, int tree_words, const int* cu_seqlens, const int* seqlens_k,
+                              const int* block_table, int n_seqs, int H, int H_kv, int total, int max_seqlen_q,
+                              int max_blocks_per_seq, int block_size, int num_blocks, int max_seqlen_k, int d,
+                              float scale, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * fa_accept_paged -- keep the accepted ones of a step's tokens in the bf16 cache: of sequence b's n tokens of the step
+ * those at accepted[b * max_accepted + i], i < n_accepted[b], which ascend, become the step's first ones (keys and
+ * values of all heads move within the step's places), and seqlens_out[b] = seqlens_k[b] - n + n_accepted[b].
+ * seqlens_out is not seqlens_k.  A sequence whose boundaries, path or blocks are not sound (indices that do not
+ * ascend or lie outside [0, n), n_accepted above n or max_accepted) is left as it is, with its length, and reported
+ * by fa_sync_status.  block_size is any; n_seqs at most 65535.
+ */
+fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens_out, const int* accepted,
+                            const int* n_accepted, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
+                            int n_seqs, int H_kv, int max_accepted, int max_blocks_per_seq, int block_size,
+                            int num_blocks, int d, void* stream);
+
+/*
+ * fa_weigh_paged -- add up the attention that each cached token draws: weights [num_blocks, H_kv, block_size] fp32,
+ * beside the pages of the bf16 cache.  For each sequence with n > 0 query tokens in the step, key head and cached
+ * token p < seqlens_k[b]:
+ *
+ *   w[p] = decay w[p] (p < weighed[b]; else 0) + sum of exp(scale q_r . k[p] - lse_r)
+ *
+ * over the query tokens r that see p (their own place and those in front of it) and the query heads that share the key
+ * head.  q [total, H, d], lse [H, total] as fa_fwd_paged_tree takes and gives them without a tree; rows with an lse of
+ * -inf weigh nothing.  weighed [n_seqs]: the tokens that have a weight (what others held is not read); null: those in
+ * front of the step's.  After a whole prompt, or with its last tokens as queries and weighed of 0, all weights are set.
+ * Sums are fp32, in a fixed order.  H / H_kv <= 128; decay in [0, 1]; the rest and the device-side checks as for
+ * fa_fwd_paged_tree.  Two sequences that share a page race.
+ */
+fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t* k_cache, float* weights,
+                           const int* weighed, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
+                           int n_seqs, int H, int H_kv, int total, int max_seqlen_q, int max_blocks_per_seq,
+                           int block_size, int num_blocks, int max_seqlen_k, int d, float scale, float decay, void* stream);
+
+/*
+ * fa_evict_paged -- cut sequences of the bf16 cache down to budgets[b] tokens, by weight.  Of a sequence with more, each
+ * key head keeps the first keep_first, the last keep_last, and of those between them the ones with the largest
+ * weights, of equal ones those in front (a weight that is no number counts as the lowest).  Keys, values and weights of
+ * what is kept go in order to the pages of new_table [n_seqs, new_max_blocks_per_seq], of the same pool; sequences
+ * within their budget go there whole.  kept [n_seqs, H_kv, max_kept] gets the positions they had, ascending, and -1
+ * behind them; seqlens_out[b] = min(seqlens_k[b], budgets[b]) (an array of its own).  Rotation stays: later tokens
+ * are appended by fa_append_paged_at.
+ *
+ * No new page may be one that a sequence of the call is read from; pages of block_table that sequences share are fine.
+ * Device-side checks (fa_sync_status): a length outside [0, max_seqlen_k], a budget below 0, min(seqlens_k[b],
+ * budgets[b]) above max_kept, or a budget below keep_first + keep_last of a sequence that exceeds it leave the
+ * sequence as it is, with its length and a kept of -1; a block id outside [0, num_blocks) leaves out its tokens.
+ * block_size is any; n_seqs at most 65535.
+ */
+fa_status_t fa_evict_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, float* weights, int* kept, int* seqlens_out,
+                           const int* budgets, const int* seqlens_k, const int* block_table, const int* new_table,
+                           int n_seqs, int H_kv, int max_seqlen_k, int max_kept, int keep_first, int keep_last,
+                           int max_blocks_per_seq, int new_max_blocks_per_seq, int block_size, int num_blocks, int d,
+                           void* stream);
 
 /*
  * fa_sync_status -- synchronise ``stream`` and report device-side failures recorded by any

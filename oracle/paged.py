@@ -116,3 +116,86 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, seen):
         bo[i] = 2.0 ** -8 * np.abs(o[i]) + (2.2 * err + 2.0 ** -11 + 2.0 ** -20) * weight + tiny + 1e-30
         bl[i] = 1.1 * err + 2.0 ** -21 + np.abs(lse[i]) * 2.0 ** -22
     return o, lse, bo, bl
+
+
+def tree_mask(parents) -> np.ndarray:
+    """seen [n, n] of one sequence's drafted tokens: itself and its ancestors."""
+    n = len(parents)
+    seen = np.zeros((n, n), bool)
+    for i in range(n):
+        j = i
+        while j >= 0:
+            seen[i, j] = True
+            j = parents[j]
+    return seen
+
+
+def pack_bits(seen: np.ndarray, words: int) -> np.ndarray:
+    """int32 [n, words]: bit j % 32 of word j // 32."""
+    n, m = seen.shape
+    wide = np.zeros((n, 32 * words), np.uint64)
+    wide[:, :m] = seen
+    return (wide.reshape(n, words, 32) << np.arange(32, dtype=np.uint64)).sum(-1).astype(np.uint32).view(np.int32)
+
+
+def attend_seen(q: np.ndarray, k: np.ndarray, v: np.ndarray, scale: float, seen: np.ndarray):
+    """Query rows q [n, d] over k, v [len, d] in fp64, row i over the keys with seen[i, j].
+
+    Returns (O, lse, bound_o, bound_lse): the bounds on fp32 scores and sums, weights rounded to bf16, O divided by
+    the sum of the rounded ones and rounded to bf16:
+      a score is off by at most e = (d + 4) 2^-24 of its terms' sum and 2^-22 of itself, and where the reference
+      that is taken off it has 2^12 by 2^-12 (in base 2) of rounding, which all weights of a row share,
+      exponentials by 2^-21;
+      a rounded weight by 2^-8 of itself: O by 2^-8 sum p |v - O| (what all share cancels), to first order,
+      of which the second order, 2^-8 of it, is allowed for too.
+    """
+    n, d = q.shape
+    o, lse = np.zeros((n, d)), np.full(n, -np.inf)
+    bo, bl = np.zeros((n, d)), np.zeros(n)
+    for i in range(n):
+        at = np.flatnonzero(seen[i])
+        if not len(at):
+            continue
+        K, V = k[at], v[at]
+        s = (K @ q[i]) * scale
+        top = s.max()
+        e = np.exp(s - top)
+        l = e.sum()
+        p = e / l
+        o[i] = p @ V
+        lse[i] = top + np.log(l)
+        err = (d + 4) * 2.0 ** -24 * scale * (np.abs(K) @ np.abs(q[i])).max() + 2.0 ** -21 + np.abs(s).max() * 2.0 ** -22
+        spread = p @ np.abs(V - o[i])
+        bo[i] = 2.0 ** -8 * np.abs(o[i]) + (2.2 * err + 2.0 ** -20) * (p @ np.abs(V)) + 1.01 * 2.0 ** -8 * spread + 1e-30
+        bl[i] = 1.1 * err + 2.0 ** -21 + np.abs(lse[i]) * 2.0 ** -22
+    return o, lse, bo, bl
+
+
+def weigh(q: np.ndarray, lse: np.ndarray, k: np.ndarray, scale: float, at):
+    """(sums, bounds) [len]: what each key draws from the rows q [n, d] with lse [n], row i seeing keys j <= at[i].
+
+    The bound: a weight p by p times its score's error (as above, without a reference) and 2^-21 of the exponential and
+    of the difference to lse, and sums of n terms by n 2^-24 of what they add up to."""
+    n, d = q.shape
+    w, b = np.zeros(len(k)), np.zeros(len(k))
+    for i in range(n):
+        if lse[i] == -np.inf:
+            continue
+        K = k[:at[i] + 1]
+        s = (K @ q[i]) * scale
+        p = np.exp(s - lse[i])
+        err = (d + 4) * 2.0 ** -24 * scale * (np.abs(K) @ np.abs(q[i])) + 2.0 ** -21 + np.abs(s) * 2.0 ** -23
+        w[:at[i] + 1] += p
+        b[:at[i] + 1] += 1.1 * p * err
+    return w, b + w * (n + 4) * 2.0 ** -24
+
+
+def evict(weights: np.ndarray, budget: int, first: int, last: int):
+    """Positions that one key head keeps of a sequence whose tokens have these weights."""
+    n = len(weights)
+    if n <= budget:
+        return list(range(n))
+    w = np.where(np.isnan(weights), -np.inf, weights.astype(np.float64))
+    sure = list(range(first)) + list(range(n - last, n))
+    rest = sorted(range(first, n - last), key=lambda j: (-w[j], j))
+    return sorted(sure + rest[:budget - len(sure)])
