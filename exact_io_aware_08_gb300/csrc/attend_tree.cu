@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   uint64_t* empty = full + C::NST;
   uint64_t* q_full = empty + C::NST;
   uint64_t* s_full = q_full + 2;
-  uint64_t* pv_done = s_full + 2;                             // NT = 2: a row block's last product; NT = 1: each
+  uint64_t* pv_done = s_full + 2;                             // NT = 2: a row tile's last product; NT = 1: each, by turns
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
   int* start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
             if (ok) {
               tc_fence_after();
               issue_pv(0, hc & 1, at_v(g, j, n), j == 0);
-              umma_commit_w(&pv_done[0]);
+              umma_commit_w(&pv_done[hc & 1]);
               umma_commit_w(&empty[at_v(g, j, n) % C::NST]);
             }
             if (j + 2 < n) {
@@ -614,7 +614,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
             uint32_t w[4] = {0u, 0u, 0u, 0u};
             auto settle = [&] {
               if (NT == 2) return true;                       // S came behind the tile's last product
-              const bool done = mbar_wait_warp(&pv_done[0], (hc - 1) & 1, abort_flag, 541);
+              const bool done = mbar_wait_warp(&pv_done[(hc - 1) & 1], (hc - 1) >> 1 & 1, abort_flag, 541);
               tc_fence_after();
               return done;
             };
@@ -636,9 +636,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           }
         }
         if (ok) {
-          // (one row tile: the last S came behind the last product but two, so that two phases may be open)
-          if (NT == 1 && hc >= 2) ok = mbar_wait_warp(&pv_done[0], (hc - 2) & 1, abort_flag, 543);
-          ok = ok && mbar_wait_warp(&pv_done[t], (NT == 2 ? mine - 1 : hc - 1) & 1, abort_flag, 542);
+          // (one row tile: the product before the last one with this barrier was done when the last S was)
+          const int done = NT == 2 ? t : (hc - 1) & 1;
+          ok = mbar_wait_warp(&pv_done[done], (NT == 2 ? mine - 1 : (hc - 1) >> 1) & 1, abort_flag, 542);
           tc_fence_after();
         }
       }

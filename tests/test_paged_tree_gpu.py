@@ -86,7 +86,9 @@ class Step:
     def check(self, o, lse, sequences=None, most=24):
         G = self.H // self.H_kv
         og, lg = f64(o), f64(lse)
-        for b in range(len(self.new)) if sequences is None else sequences:
+        if sequences is None:
+            sequences = sorted({*range(min(12, len(self.new))), *range(0, len(self.new), 5), len(self.new) - 1})
+        for b in sequences:
             n = self.new[b]
             if n == 0:
                 continue
@@ -126,6 +128,7 @@ STEPS = [
     ([1] * 70, list(range(1, 1401, 20)), 8, 4, 128, 32, None, 0),
     ([4] * 40, [4] * 40, 4, 2, 64, 16, "bits", 0),
     ([0, 0, 1], [9, 0, 1], 3, 3, 64, 16, None, 4),
+    ([8] * 64, [1000] * 64, 32, 8, 128, 64, "tree", 0),
     # one and two tiles of rows by turns, several sequences a CTA
     ([60, 1, 1, 33, 2, 40, 1, 64, 31, 32] * 7, [20 * i + 70 for i in range(70)], 16, 4, 128, 64, "tree", 0),
     ([1, 1, 250, 3, 129, 1, 128] * 9, [17 * i + 260 for i in range(63)], 8, 8, 64, 16, None, 0),
