@@ -12,19 +12,25 @@
 // What bounds it.  4 d flops a (row, key) and 4 d bytes a key of a key head: up to some 278 rows the reading
 // of the cache, above it the tensor core.
 //
-// Layout.  A CTA an SM takes NT tiles of 128 rows of one key head, and runs over keys 128 at a time:
+// Layout.  A CTA an SM takes NT tiles of up to 128 rows of one key head (whole tokens, so that TMA brings them), and
+// runs over keys 128 at a time:
 //   warp 0       copies K and V tiles by TMA into one ring, in the order in which they are used.
 //   warp 1       issues the products (the whole warp converged, one elected lane): S = Q K^T from shared
 //                memory, O += P V with P from tensor memory.
 //   warp 2       joins the hand-off of P once V is there, and cleans V's tile: rows behind the last key hold
 //                anything, and 0 * NaN is NaN.
-//   warps 4 on   softmax, thread = row; they bring the rows of Q in and write those of O out.
+//   warp 3       brings Q in, the next item's as soon as the last S of one is done.
+//   warps 4-11   softmax.  NT = 2: thread = row, a warpgroup a row tile.  NT = 1: two threads a row, 64 keys each,
+//                which exchange their maxima in tensor memory; they write O out, or states, a state's rows side by side.
 // Two S buffers are in flight: of the two row tiles (NT = 2, more than 128 rows), or of two key tiles in a
 // row (NT = 1).
 //
 // Where one row block holds all rows of a sequence and key head, each CTA gets an equal share of all key steps,
 // whatever the sequences' lengths, and what is cut is joined from states (Q4Share).  With more row blocks a
 // CTA takes one, all row blocks of a key head side by side so that its keys are read from memory once.
+//
+// Short calls are bound by latencies, of fetching instructions among them (a first pass over unrolled code that
+// streamed caches have driven out of L2 takes microseconds): the rarer paths are loops.
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
 #include "q4_share.h"
@@ -37,35 +43,38 @@ struct TreeCfg {
   static constexpr int CH = D / 64;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int TILE = 128 * D * 2;
-  static constexpr int ROWS = NT * 128;
   static constexpr int NST = D == 128 ? (NT == 1 ? 6 : 5) : 11;   // K and V tiles of the ring
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_KV = NT * TILE;
   static constexpr int OFF_BAR = OFF_KV + NST * TILE;
-  // full[NST], empty[NST], q_full[2], s_full[2], pv_done[2]; then the TMEM slot, abort flag, start[3], spoilt[4]
+  // full[NST], empty[NST], q_full, q_empty, s_full[2], pv_done[2]; then the TMEM slot, abort flag, start[3], spoilt[4]
   static constexpr int NBAR = 2 * NST + 6;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
   static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t T_S = 0, T_O = 256;
-  static constexpr int THREADS = 128 + NT * 128;
+  static constexpr uint32_t T_S = 0, T_O = 256, T_X = 384;    // T_X: exchanged maxima and sums (NT = 1)
+  static constexpr int THREADS = 384;
   // NT = 2: launched with 168 registers a thread, moved from the control warps
   static constexpr uint32_t REG_CTRL = 80, REG_SOFTMAX = 208;
   static constexpr int REG_NEED = NT == 2 ? 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX)) : 0;
-  static constexpr float RESCALE = 8.f;
-  static constexpr uint32_t BAR_P = 2, BAR_P_THREADS = 128 + 32 + 32;
-  static constexpr int STATE = D + 4;                         // O~, then reference, sum, rounded sum
+  // named barriers: start, hand-off of P by S buffer, pairs of warps (NT = 1)
+  static constexpr uint32_t BAR_START = 1, BAR_P = 2, BAR_PAIR = 4;
+  static constexpr uint32_t BAR_P_THREADS = (NT == 1 ? 256 : 128) + 32 + 32;
 };
+constexpr float kTreeRescale = 8.f;
 
 struct TreeParams {
-  CUtensorMap tk, tv;
+  CUtensorMap tk, tv, tq;
   PagedCache cache;
-  const uint16_t *q, *v;
+  const uint16_t* v;
   uint16_t* o;
   float *lse, *part;
   const int *tree, *cu, *seqlens;
-  int words, n_seqs, H, G, total, max_q, max_k;
+  // A key head's G query heads are taken ``group`` at a time (all of them where a tile holds them): heads of
+  // that kind are called key heads below, ``heads`` of them, ``per_kv`` to a key head of the cache.
+  int group, heads, per_kv, tokens;                           // tokens of a row tile
+  int words, n_seqs, H, total, max_q, max_k;
   int shares, whole;                                          // equal shares of key steps (of whole row blocks or not)
   int row_blocks, full_items, tail_splits, chunk, state_rows; // else: items from full_items on in tail_splits parts
   float c2;
@@ -73,11 +82,13 @@ struct TreeParams {
 
 // One stretch of work: row block rb of a key head of a sequence over keys [key0, key_end).
 struct TreeItem {
-  int b, hkv, rb, key0, key_end, slot;                        // slot: -1 results, else the state's place
+  int b, head, rb, key0, key_end, slot;                       // slot: -1 results, else the state's place
   PagedSeq seq;
 };
 
-template <int ROWS>
+__device__ __forceinline__ int tree_steps(const PagedSeq& s) { return s.nq ? max(1, (s.len + kPagedTile - 1) / kPagedTile) : 0; }
+
+template <int NT>
 struct TreeWalk {
   const TreeParams& p;
   int b, off, left;                                           // shares: sequence, unit in it, units left
@@ -85,11 +96,24 @@ struct TreeWalk {
   PagedSeq seq;
   int steps;
 
-  __device__ __forceinline__ int seq_steps(const PagedSeq& s) const { return s.nq ? max(1, (s.len + kPagedTile - 1) / kPagedTile) : 0; }
+  // Tokens up to ``token`` of the sequence see keys below this.
+  __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int token) {
+    return p.tree ? s.len : s.base() + min(token, s.nq - 1) + 1;
+  }
 
-  // Rows up to ``row`` of the sequence see keys below this.
-  __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int row) {
-    return p.tree ? s.len : s.base() + min(row, s.nq * p.G - 1) / p.G + 1;
+  // The share: whose first unit is unit ``u`` of sequence ``at``.
+  __device__ __forceinline__ void begin(int at, int u, int n) {
+    b = at;
+    off = u;
+    left = n;
+    if (left <= 0) return;
+    seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
+    steps = tree_steps(seq);
+    if (p.whole) {                                            // the row blocks that begin in it
+      const int behind = off % steps, skip = behind ? steps - behind : 0;
+      off += skip;
+      left -= skip;
+    }
   }
 
   __device__ __forceinline__ bool next(TreeItem& x) {
@@ -107,31 +131,30 @@ struct TreeWalk {
       }
       x.rb = p.row_blocks - 1 - item % p.row_blocks;
       const int w = item / p.row_blocks;
-      x.hkv = w % p.cache.H_kv;
-      x.b = w / p.cache.H_kv;
-      x.seq = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, x.rb == 0 && x.hkv == 0 && threadIdx.x == 0, 500);
-      const int row0 = x.rb * ROWS;
-      if (row0 >= x.seq.nq * p.G) return false;
+      x.head = w % p.heads;
+      x.b = w / p.heads;
+      x.seq = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, x.rb == 0 && x.head == 0 && threadIdx.x == 0, 500);
+      if (x.rb * NT * p.tokens >= x.seq.nq) return false;
       x.key0 = split * p.chunk;
-      x.key_end = min(seen(p, x.seq, row0 + ROWS - 1), parts > 1 ? x.key0 + p.chunk : 1 << 30);
+      x.key_end = min(seen(p, x.seq, (x.rb + 1) * NT * p.tokens - 1), parts > 1 ? x.key0 + p.chunk : 1 << 30);
       return true;
     }
     if (left <= 0) return false;
-    while (off >= steps * p.cache.H_kv) {                     // (a sequence with work follows: left > 0)
+    while (off >= steps * p.heads) {                          // (a sequence with work follows: left > 0)
       if (++b >= p.n_seqs) return false;
       off = 0;
       seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-      steps = seq_steps(seq);
+      steps = tree_steps(seq);
     }
     x.b = b;
     x.seq = seq;
     x.rb = 0;
-    x.hkv = off / steps;
-    const int step0 = off - x.hkv * steps;
+    x.head = off / steps;
+    const int step0 = off - x.head * steps;
     const int n = p.whole ? steps : min(left, steps - step0);
     x.key0 = step0 * kPagedTile;
     x.key_end = min(x.key0 + n * kPagedTile, seq.len);
-    x.slot = n == steps ? -1 : 2 * blockIdx.x + (step0 == 0 ? 1 : 0);
+    x.slot = n == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
     off += n;
     left -= n;
     return true;
@@ -142,9 +165,8 @@ struct TreeWalk {
 template <typename F>
 __device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, bool report, F u_of, int* b, long long* before) {
   const int lane = threadIdx.x & 31;
-  auto units = [&](int i, bool rep) -> long long {
-    const PagedSeq s = paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501);
-    return s.nq ? static_cast<long long>(max(1, (s.len + kPagedTile - 1) / kPagedTile)) * p.cache.H_kv : 0;
+  auto units = [&](int i, bool rep) {
+    return static_cast<long long>(tree_steps(paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501))) * p.heads;
   };
   Q4Share sh;
   long long mine = 0, own = 0;
@@ -180,33 +202,124 @@ __device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, boo
 }
 
 // Bit k of word w: the row's token sees key k0 + 32 w + k.
-__device__ __forceinline__ void tree_mask(const TreeParams& p, const PagedSeq& s, int token, int k0, uint32_t (&w)[4]) {
-  // below the first n bits of a word
+template <int W>
+__device__ __forceinline__ void tree_mask(const TreeParams& p, const PagedSeq& s, int token, int k0, uint32_t (&w)[W]) {
   auto first_bits = [](int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; };
   const int end = p.tree ? s.len : s.base() + token + 1;
 #pragma unroll
-  for (int m = 0; m < 4; ++m) w[m] = first_bits(end - (k0 + 32 * m));
+  for (int m = 0; m < W; ++m) w[m] = first_bits(end - (k0 + 32 * m));
   if (!p.tree) return;
   const int* row = p.tree + static_cast<size_t>(s.first + token) * p.words;
   auto word = [&](int i) { return i >= 0 && i < p.words ? static_cast<uint32_t>(__ldg(row + i)) : 0u; };
 #pragma unroll
-  for (int m = 0; m < 4; ++m) {
+  for (int m = 0; m < W; ++m) {
     const int x = k0 + 32 * m - s.base();                     // the step's token of bit 0
     uint32_t bits = first_bits(-x);                           // tokens in front of the step's
     if (x > -32 && w[m]) {
-      const int i = x >> 5, sh = x & 31;
-      bits |= __funnelshift_r(word(i), word(i + 1), sh);
+      const int i = x >> 5;
+      bits |= __funnelshift_r(word(i), word(i + 1), x & 31);
     }
     w[m] &= bits;
   }
 }
 
-// One key tile of a row: S in tensor memory (columns t_s) becomes P over its first half, O (t_o) is
-// rescaled where the row's reference moves, once ``settle`` says that its last product is done.  PLAIN: the
-// row sees all keys of the tile, and no reference is large (``far``); else w says which.
-template <int D, bool PLAIN, typename F>
-__device__ __forceinline__ bool tree_softmax(uint32_t t_s, uint32_t t_o, const uint32_t (&w)[4], bool first, float c2, float& m, float& l,
-                                             float& lh, bool& far, F settle) {
+__device__ __forceinline__ float max32(const float* s) {
+  float a = fmax3(s[0], s[1], s[2]);
+#pragma unroll
+  for (int k = 3; k < 31; k += 2) a = fmax3(a, s[k], s[k + 1]);
+  return fmaxf(a, s[31]);
+}
+
+// Multiplies COLS columns of a row of O.
+template <int COLS>
+__device__ __forceinline__ void tree_rescale(uint32_t t_o, float alpha) {
+#pragma unroll 1
+  for (int k = 0; k < COLS; k += 32) {
+    uint32_t rr[32];
+    tmem_ld32(t_o + k, rr);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      const float2 v = fmul2(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), make_float2(alpha, alpha));
+      rr[i] = __float_as_uint(v.x);
+      rr[i + 1] = __float_as_uint(v.y);
+    }
+    tmem_st32(t_o + k, rr);
+  }
+}
+
+// Reference and sums of a row (or of one thread's half of it).
+struct TreeRow {
+  float m = -INFINITY, l = 0.f, lh = 0.f;
+
+  // The reference follows ``cand`` (the largest score so far) where that is far above it: the factor of what has been
+  // added up.  ``any``: some row of the warp moves.
+  __device__ __forceinline__ float follow(float cand, float c2, bool valid, bool* any) {
+    // a row that sees none of the keys so far has nothing to move
+    const bool move = valid && cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > kTreeRescale);
+    *any = __any_sync(0xffffffffu, move);
+    const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
+    if (move) {
+      l *= alpha;
+      lh *= alpha;
+      m = cand;
+    }
+    return alpha;
+  }
+};
+
+// Weights of 32 scores, as 16 words of bf16 pairs; x = (s - ref) c2.
+__device__ __forceinline__ void tree_weights(const float* s, float ref, float c2, TreeRow& r, uint32_t* pk) {
+  float2 rs = make_float2(0.f, 0.f), hs = rs;
+  const float2 nr = make_float2(-ref, -ref), c = make_float2(c2, c2);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float2 x = fmul2(fadd2(make_float2(s[2 * k], s[2 * k + 1]), nr), c);
+    const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
+    pk[k] = pack_bf16x2(e.x, e.y);
+    rs = fadd2(rs, e);
+    hs = add_bf16x2_f32(hs, pk[k]);
+  }
+  r.l += rs.x + rs.y;
+  r.lh += hs.x + hs.y;
+}
+
+// One key tile of a row, thread = row, where some keys are not seen or the reference is large: S in tensor memory
+// (columns t_s) becomes P over its first half, O (t_o) is rescaled where the row's reference moves.
+template <int D>
+__device__ __forceinline__ void tree_softmax_masked(uint32_t t_s, uint32_t t_o, const uint32_t (&w)[4], bool first, bool valid, float c2, TreeRow& r) {
+  float s[32];
+  auto load = [&](int k) {
+    uint32_t rr[32];
+    tmem_ld32(t_s + k * 32, rr);
+    tmem_wait_ld();
+    const uint32_t bits = k < 2 ? (k == 0 ? w[0] : w[1]) : (k == 2 ? w[2] : w[3]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? __uint_as_float(rr[i]) : -INFINITY;
+  };
+  float cand = r.m;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {
+    load(k);
+    cand = fmaxf(cand, max32(s));
+  }
+  bool any;
+  const float alpha = r.follow(cand, c2, valid, &any);
+  if (any && !first) tree_rescale<D>(t_o, alpha);
+  const float ref = r.m == -INFINITY ? 0.f : r.m;
+#pragma unroll 1
+  for (int k = 0; k < 4; ++k) {                               // (P of a quarter lies over S of quarters that were read)
+    load(k);
+    uint32_t pk[16];
+    tree_weights(s, ref, c2, r, pk);
+    tmem_st16(t_s + k * 16, pk);
+  }
+}
+
+// The same where the row sees all keys, and c s - c m may be formed at once: false where c m has become so large that
+// its rounding could matter (the tile is then done by the form above).
+template <int D>
+__device__ __forceinline__ bool tree_softmax_plain(uint32_t t_s, uint32_t t_o, bool first, bool valid, float c2, TreeRow& r) {
   float s[128];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -216,53 +329,14 @@ __device__ __forceinline__ bool tree_softmax(uint32_t t_s, uint32_t t_o, const u
     for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
   }
   tmem_wait_ld();
-  if constexpr (!PLAIN) {
-#pragma unroll
-    for (int k = 0; k < 128; ++k)
-      if (!(w[k >> 5] >> (k & 31) & 1u)) s[k] = -INFINITY;
+  const float cand = fmaxf(r.m, fmaxf(fmax3(max32(s), max32(s + 32), max32(s + 64)), max32(s + 96)));
+  bool any;
+  const float alpha = r.follow(cand, c2, valid, &any);
+  if (any) {
+    if (!first) tree_rescale<D>(t_o, alpha);
+    if (__any_sync(0xffffffffu, valid && fabsf(r.m * c2) > 4096.f && r.m != -INFINITY)) return false;
   }
-  float mx[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    mx[g] = fmax3(s[32 * g], s[32 * g + 1], s[32 * g + 2]);
-#pragma unroll
-    for (int k = 3; k < 31; k += 2) mx[g] = fmax3(mx[g], s[32 * g + k], s[32 * g + k + 1]);
-    mx[g] = fmaxf(mx[g], s[32 * g + 31]);
-  }
-  const float cand = fmaxf(m, fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]));
-  // a row that sees none of the tile's keys has nothing to move
-  const bool move = cand != -INFINITY && (m == -INFINITY || (cand - m) * c2 > TreeCfg<D, 1>::RESCALE);
-  if (__any_sync(0xffffffffu, move)) {
-    const float alpha = move ? fast_exp2((m - cand) * c2) : 1.f;
-    if (move) {
-      l *= alpha;
-      lh *= alpha;
-      m = cand;
-    }
-    // c s - c m is off by the rounding of c m: where that could matter the reference is taken off first
-    far = __any_sync(0xffffffffu, fabsf(m * c2) > 4096.f && m != -INFINITY);
-    if (!first) {
-      if (!settle()) return false;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
-        uint32_t rr[32];
-        tmem_ld32(t_o + k * 32, rr);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          const float2 v = fmul2(make_float2(__uint_as_float(rr[i]), __uint_as_float(rr[i + 1])), make_float2(alpha, alpha));
-          rr[i] = __float_as_uint(v.x);
-          rr[i + 1] = __float_as_uint(v.y);
-        }
-        tmem_st32(t_o + k * 32, rr);
-      }
-    }
-  }
-  if (far) {
-#pragma unroll
-    for (int k = 0; k < 128; ++k) s[k] -= (m == -INFINITY) ? 0.f : m;
-  }
-  const float up = far || m == -INFINITY ? 0.f : -m * c2;
+  const float up = r.m == -INFINITY ? 0.f : -r.m * c2;
   const float2 c2v = make_float2(c2, c2), nms = make_float2(up, up);
   float2 rs[2], hs[2];
 #pragma unroll
@@ -281,8 +355,8 @@ __device__ __forceinline__ bool tree_softmax(uint32_t t_s, uint32_t t_o, const u
     tmem_st32(t_s + h * 32, pk);
   }
   const float2 sum = fadd2(rs[0], rs[1]), sumh = fadd2(hs[0], hs[1]);
-  l += sum.x + sum.y;
-  lh += sumh.x + sumh.y;
+  r.l += sum.x + sum.y;
+  r.lh += sumh.x + sumh.y;
   return true;
 }
 
@@ -298,8 +372,7 @@ __device__ __forceinline__ void tree_spoil(const TreeParams& p, const TreeItem& 
     const int blk = k / p.cache.block_size;
     const int page = __ldg(p.cache.table + static_cast<size_t>(x.b) * p.cache.max_blocks + blk);
     if (page < 0 || page >= p.cache.num_blocks) continue;
-    const uint16_t* v = p.v + ((static_cast<size_t>(page) * p.cache.block_size + (k - blk * p.cache.block_size)) * p.cache.H_kv + x.hkv) * D + col;
-#pragma unroll
+    const uint16_t* v = p.v + ((static_cast<size_t>(page) * p.cache.block_size + (k - blk * p.cache.block_size)) * p.cache.H_kv + x.head / p.per_kv) * D + col;
     for (int i = 0; i < 32; ++i) {
       const uint32_t bits = __ldg(v + i);
       if ((bits & 0x7f80u) == 0x7f80u) acc[i] += __uint_as_float(bits << 16);
@@ -317,7 +390,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
   uint64_t* empty = full + C::NST;
   uint64_t* q_full = empty + C::NST;
-  uint64_t* s_full = q_full + 2;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_empty + 1;
   uint64_t* pv_done = s_full + 2;                             // NT = 2: a row tile's last product; NT = 1: each, by turns
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
@@ -326,6 +400,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   volatile int* spoilt = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 20);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  TreeWalk<NT> walk{p, 0, 0, 0, false, {}, 0};
+  uint32_t tbase = 0;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -333,8 +409,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
         mbar_init(&full[s], 1);
         mbar_init(&empty[s], 1);
       }
+      mbar_init(q_full, 1);
+      mbar_init(q_empty, 1);
       for (int t = 0; t < 2; ++t) {
-        mbar_init(&q_full[t], 128);
         mbar_init(&s_full[t], 1);
         mbar_init(&pv_done[t], 1);
       }
@@ -342,52 +419,47 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       for (int i = 0; i < 4; ++i) spoilt[i] = 0;
       fence_mbarrier_init();
     }
-    if (lane < 2) tma_prefetch_desc(lane ? &p.tv : &p.tk);
+    if (lane < 3) tma_prefetch_desc(lane == 0 ? &p.tk : lane == 1 ? &p.tv : &p.tq);
     if (p.shares) {
       int b;
       long long before = 0;
       const Q4Share sh = tree_share(p, gridDim.x, blockIdx.x == 0,
                                     [&](const Q4Share& y) { return static_cast<int>(blockIdx.x) < y.n && y.total > 0 ? y.begin(blockIdx.x) : -1LL; },
                                     &b, &before);
+      const int u = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x) - before);
+      const int n = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x + 1) - sh.begin(blockIdx.x));
       if (lane == 0) {
         start[0] = b;
-        start[1] = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x) - before);
-        start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x + 1) - sh.begin(blockIdx.x));
+        start[1] = u;
+        start[2] = n;
       }
+      walk.begin(b, u, n);
     }
-  } else if (warp == 1) {
-    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    __syncwarp();
+    named_bar_arrive(C::BAR_START, C::THREADS);               // the copies begin at once
+  } else {
+    if (warp == 1) {
+      tmem_alloc(tmem_slot, C::TMEM_COLS);
+      __syncwarp();
+      tc_fence_before();
+    }
+    pdl_launch_dependents();
+    named_bar_sync(C::BAR_START, C::THREADS);
+    tc_fence_after();
+    tbase = *tmem_slot;
+    if (p.shares) walk.begin(start[0], start[1], start[2]);
   }
-  pdl_launch_dependents();
-  __syncwarp();
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tbase = *tmem_slot;
 
-  TreeWalk<C::ROWS> walk{p, 0, 0, 0, false, {}, 0};
-  if (p.shares) {
-    walk.b = start[0];
-    walk.off = start[1];
-    walk.left = start[2];
-    if (walk.left > 0) {
-      walk.seq = paged_seq(p.cu, p.seqlens, walk.b, p.total, p.max_q, p.max_k, false, 0);
-      walk.steps = walk.seq_steps(walk.seq);
-      if (p.whole) {                                          // the row blocks that begin in the share
-        const int behind = walk.off % walk.steps, skip = behind ? walk.steps - behind : 0;
-        walk.off += skip;
-        walk.left -= skip;
-      }
-    }
-  }
-  TreeItem x;
+  TreeItem x{};
   // Key tiles of row tile t: those that some row of it sees.
   auto tiles = [&](int t) {
-    const int row0 = x.rb * C::ROWS + t * 128;
-    if (row0 >= x.seq.nq * p.G) return 0;
-    const int end = min(x.key_end, TreeWalk<C::ROWS>::seen(p, x.seq, row0 + 127));
+    const int token0 = (x.rb * NT + t) * p.tokens;
+    if (token0 >= x.seq.nq) return 0;
+    const int end = min(x.key_end, TreeWalk<NT>::seen(p, x.seq, token0 + p.tokens - 1));
     return end <= x.key0 ? 0 : (end - x.key0 + C::BN - 1) / C::BN;
   };
+  // Keys from here on are not seen by every row of the block.
+  auto common = [&] { return p.tree ? x.seq.base() : x.seq.base() + x.rb * NT * p.tokens + 1; };
   // Ring places of an item's tiles, from its first one, g: K_0 V_0 K_1 V_1 ... for two row tiles, and
   // K_0 K_1 V_0 K_2 V_1 ... for one.
   auto at_k = [&](int g, int j) { return NT == 2 ? g + 2 * j : g + (j == 0 ? 0 : 2 * j - 1); };
@@ -403,23 +475,20 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       auto load = [&](const CUtensorMap* map, int j) {
         const int s = g % C::NST, u = g / C::NST;
         if (u > 0 && !(ok = mbar_wait_warp(&empty[s], (u - 1) & 1, abort_flag, 510))) return;
-        load_paged_tile<D>(p.cache, win, map, sKV + s * C::TILE, &full[s], x.b, x.hkv, x.key0 + j * C::BN, x.key_end, 502);
+        load_paged_tile<D>(p.cache, win, map, sKV + s * C::TILE, &full[s], x.b, x.head / p.per_kv, x.key0 + j * C::BN, x.key_end, 502);
         ++g;
       };
       while (ok && walk.next(x)) {
         const int n = NT == 2 ? max(tiles(0), tiles(1)) : tiles(0);
-        if (n == 0) continue;
-        load(&p.tk, 0);
-        for (int j = 0; ok && j < n; ++j) {
-          if (NT == 1 && j + 1 < n) load(&p.tk, j + 1);
-          if (ok) load(&p.tv, j);
-          if (NT == 2 && ok && j + 1 < n) load(&p.tk, j + 1);
+        // K_0 V_0 K_1 V_1 ..., or K_0 K_1 V_0 K_2 V_1 ...
+        for (int i = 0; ok && i < 2 * n; ++i) {
+          const bool is_k = NT == 2 ? (i & 1) == 0 : i == 0 || ((i & 1) && i + 1 < 2 * n);
+          const int j = NT == 2 ? i >> 1 : is_k ? (i + 1) >> 1 : i + 1 < 2 * n ? (i >> 1) - 1 : n - 1;
+          load(is_k ? &p.tk : &p.tv, j);
         }
       }
       // every signal is awaited; after an abort: every copy that was started lands
-      if (ok) {
-        for (int i = max(0, g - C::NST); ok && i < g; ++i) ok = mbar_wait_warp(&empty[i % C::NST], (i / C::NST) & 1, abort_flag, 511);
-      }
+      for (int i = max(0, g - C::NST); ok && i < g; ++i) ok = mbar_wait_warp(&empty[i % C::NST], (i / C::NST) & 1, abort_flag, 511);
       if (!ok)
         for (int i = max(0, g - C::NST); i < g; ++i) mbar_wait_warp(&full[i % C::NST], (i / C::NST) & 1, nullptr, 512);
     } else if (warp == 1) {
@@ -431,7 +500,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       const uint64_t dk0 = smem_desc_sw128(smem_u32(sKV), 0, 1024);
       const uint64_t dv0 = smem_desc_sw128(smem_u32(sKV), C::CHUNK, 1024);
       bool ok = true;
-      int g = 0, c0 = 0, c1 = 0, hc = 0;                      // items of the row tiles, hand-offs so far (NT = 1)
+      int g = 0, items = 0, hc = 0;                           // hc: hand-offs so far (NT = 1)
       auto wait_tile = [&](int at) {
         ok = ok && mbar_wait_warp(&full[at % C::NST], (at / C::NST) & 1, abort_flag, 520);
         tc_fence_after();
@@ -456,14 +525,15 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       while (walk.next(x)) {
         const int n0 = tiles(0), n1 = NT == 2 ? tiles(1) : 0, n = max(n0, n1);
         if (n == 0) continue;
-        if (n0 > 0) ok = ok && mbar_wait_warp(&q_full[0], c0++ & 1, abort_flag, 521);
-        if (n1 > 0) ok = ok && mbar_wait_warp(&q_full[1], c1++ & 1, abort_flag, 522);
+        ok = ok && mbar_wait_warp(q_full, items & 1, abort_flag, 521);
+        ++items;
         if constexpr (NT == 2) {
           wait_tile(at_k(g, 0));
           if (ok) {
             if (n0 > 0) issue_s(0, 0, at_k(g, 0));
             if (n1 > 0) issue_s(1, 1, at_k(g, 0));
             umma_commit_w(&empty[at_k(g, 0) % C::NST]);
+            if (n == 1) umma_commit_w(q_empty);
           }
           for (int j = 0; j < n; ++j) {
 #pragma unroll
@@ -483,32 +553,31 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
             if (ok) {
               umma_commit_w(&empty[at_v(g, j, n) % C::NST]);
               if (j + 1 < n) umma_commit_w(&empty[at_k(g, j + 1) % C::NST]);
+              if (j + 2 == n) umma_commit_w(q_empty);
             }
           }
         } else {
-          for (int j = 0; j < min(2, n); ++j) {
-            wait_tile(at_k(g, j));
-            if (ok) {
-              issue_s(0, (hc + j) & 1, at_k(g, j));
-              umma_commit_w(&empty[at_k(g, j) % C::NST]);
-            }
-          }
-          for (int j = 0; j < n; ++j, ++hc) {
-            __syncwarp();
-            named_bar_sync(C::BAR_P + (hc & 1), C::BAR_P_THREADS);
-            if (ok) {
-              tc_fence_after();
-              issue_pv(0, hc & 1, at_v(g, j, n), j == 0);
-              umma_commit_w(&pv_done[hc & 1]);
-              umma_commit_w(&empty[at_v(g, j, n) % C::NST]);
-            }
-            if (j + 2 < n) {
-              wait_tile(at_k(g, j + 2));
+          // S of tiles 0 and 1; then, j by j, O += P_j V_j and S of tile j + 2 over P_j
+          for (int i = -2; i < n; ++i) {
+            if (i >= 0) {
+              __syncwarp();
+              named_bar_sync(C::BAR_P + (hc & 1), C::BAR_P_THREADS);
               if (ok) {
-                issue_s(0, hc & 1, at_k(g, j + 2));
-                umma_commit_w(&empty[at_k(g, j + 2) % C::NST]);
+                tc_fence_after();
+                issue_pv(0, hc & 1, at_v(g, i, n), i == 0);
+                umma_commit_w(&pv_done[hc & 1]);
+                umma_commit_w(&empty[at_v(g, i, n) % C::NST]);
               }
             }
+            if (i + 2 < n) {
+              wait_tile(at_k(g, i + 2));
+              if (ok) {
+                issue_s(0, (hc + (i < 0 ? i + 2 : 0)) & 1, at_k(g, i + 2));
+                umma_commit_w(&empty[at_k(g, i + 2) % C::NST]);
+                if (i + 3 == n) umma_commit_w(q_empty);
+              }
+            }
+            if (i >= 0) ++hc;
           }
         }
         g += 2 * n;
@@ -522,8 +591,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
         if (n == 0) continue;
         if (n0 > 0) ++c0;
         if (n1 > 0) ++c1;
-        // keys from ``from`` on are not seen by every row of the block
-        const int from = p.tree ? x.seq.base() : x.seq.base() + x.rb * C::ROWS / p.G + 1;
+        const int from = common();
         for (int j = 0; j < n; ++j) {
           const int at = at_v(g, j, n);
           if (ok) ok = mbar_wait_warp(&full[at % C::NST], (at / C::NST) & 1, abort_flag, 530);
@@ -532,15 +600,15 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           const int k0 = x.key0 + j * C::BN;
           if (ok && (k0 + C::BN > x.key_end || k0 + C::BN > from)) {
             uint8_t* tile = sKV + (at % C::NST) * C::TILE;
-            bool found = false;
-            for (int i = max(0, min(from, x.key_end) - k0) * (D / 8) + lane; i < C::BN * (D / 8); i += 32) {
+            const int live = min(C::BN, x.key_end - k0);
+            auto vec = [&](int i) {                           // 16-byte vector i of the tile, row by row
               const int row = i / (D / 8), c = i % (D / 8);
-              uint4* at16 = reinterpret_cast<uint4*>(tile + (c >> 3) * C::CHUNK + sw128_offset(row, (c & 7) * 8));
-              if (k0 + row >= x.key_end) {
-                *at16 = make_uint4(0u, 0u, 0u, 0u);
-                continue;
-              }
-              uint4 v = *at16;
+              return reinterpret_cast<uint4*>(tile + (c >> 3) * C::CHUNK + sw128_offset(row, (c & 7) * 8));
+            };
+            bool found = false;
+#pragma unroll 4
+            for (int i = max(0, min(from - k0, live)) * (D / 8) + lane; i < live * (D / 8); i += 32) {
+              uint4 v = *vec(i);
               uint32_t* e = reinterpret_cast<uint32_t*>(&v);
               bool bad = false;
 #pragma unroll
@@ -550,9 +618,11 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
                 if (lo) e[y] &= 0xffff0000u;
                 if (hi) e[y] &= 0xffffu;
               }
-              if (bad) *at16 = v;
+              if (bad) *vec(i) = v;
               found |= bad;
             }
+#pragma unroll 4
+            for (int i = live * (D / 8) + lane; i < C::BN * (D / 8); i += 32) *vec(i) = make_uint4(0u, 0u, 0u, 0u);
             if (found && n0 > 0) spoilt[c0 & 1] = c0;
             if (found && n1 > 0) spoilt[2 + (c1 & 1)] = c1;
             __threadfence_block();
@@ -568,61 +638,119 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
         }
         g += 2 * n;
       }
+    } else {
+      // -------------------------------------------------------------- Q
+      bool ok = true;
+      int items = 0;
+      while (ok && walk.next(x)) {
+        const int n0 = tiles(0), n1 = NT == 2 ? tiles(1) : 0;
+        if (max(n0, n1) == 0) continue;
+        if (items > 0 && !(ok = mbar_wait_warp(q_empty, (items - 1) & 1, abort_flag, 535))) break;
+        const bool two = NT == 2 && (x.rb * NT + 1) * p.tokens < x.seq.nq;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, (two ? 2 : 1) * p.tokens * p.group * D * 2);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (t == 0 || two)
+#pragma unroll
+              for (int ch = 0; ch < C::CH; ++ch)
+                tma_load_4d(sQ + t * C::TILE + ch * C::CHUNK, &p.tq, q_full, ch * 64, 0, x.head, x.seq.first + (x.rb * NT + t) * p.tokens);
+        }
+        __syncwarp();
+        ++items;
+      }
+      if (ok && items > 0) ok = mbar_wait_warp(q_empty, (items - 1) & 1, abort_flag, 536);
+      if (!ok && items > 0) mbar_wait_warp(q_full, (items - 1) & 1, nullptr, 537);
     }
   } else {
-    // ---------------------------------------------------------------- softmax, thread = row
+    // ---------------------------------------------------------------- softmax
     if constexpr (NT == 2) setmaxnreg_inc<C::REG_SOFTMAX>();
-    const int t = NT == 2 ? (warp - 4) >> 2 : 0;
+    const int wg = (warp - 4) >> 2;                           // NT = 2: row tile; NT = 1: half of the keys, and of O's columns
+    const int t = NT == 2 ? wg : 0, half = NT == 1 ? wg : 0;
+    constexpr int COLS = NT == 2 ? D : D / 2;                 // columns of O that a thread writes
     const int sub = warp & 3;                                 // TMEM lane quarter this warp may access
     const int row = sub * 32 + lane;
-    const uint32_t t_lane = static_cast<uint32_t>(sub * 32) << 16;
-    const uint32_t t_o = tbase + t_lane + C::T_O + t * 128;
+    const uint32_t t_lane = tbase + (static_cast<uint32_t>(sub * 32) << 16);
+    const uint32_t t_o = t_lane + C::T_O + t * 128 + half * COLS;
     bool ok = true;
     int mine = 0, hc = 0;                                     // items that this row tile has keys in, key tiles so far
     const float c2 = p.c2;
+    const int row_token = row / p.group, row_head = row - row_token * p.group;
     while (walk.next(x)) {
       const int n = tiles(t);
-      const int rows = x.seq.nq * p.G, r = x.rb * C::ROWS + t * 128 + row;
-      const int token = min(r, rows - 1) / p.G, head = x.hkv * p.G + r % p.G;
-      const size_t th = static_cast<size_t>(x.seq.first + token) * p.H + head;
-      float m = -INFINITY, l = 0.f, lh = 0.f;
+      const int token = (x.rb * NT + t) * p.tokens + row_token, head = x.head * p.group + row_head;
+      const bool valid = row_token < p.tokens && token < x.seq.nq;
+      const bool idle = !__any_sync(0xffffffffu, valid);
+      TreeRow r;
       if (n > 0) {
         ++mine;
-        // (this tile's products of the item before are done: their S has been read)
-        uint4 q[D / 8];
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          q[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < rows) q[i] = __ldg(reinterpret_cast<const uint4*>(p.q + th * D) + i);
-        }
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4*>(sQ + t * C::TILE + (i >> 3) * C::CHUNK + sw128_offset(row, (i & 7) * 8)) = q[i];
-        fence_proxy_async_smem();
-        mbar_arrive(&q_full[t]);
+        if (p.tree && valid)                                  // (the words are wanted at the last key tiles)
+          asm volatile("prefetch.global.L1 [%0];" :: "l"(p.tree + static_cast<size_t>(x.seq.first + token) * p.words));
         bool far = false;
         // keys below it are all the warp's rows'
-        const int full_end = __reduce_min_sync(0xffffffffu, r >= rows ? 1 << 30 : p.tree ? x.seq.base() : x.seq.base() + token + 1);
-        const bool idle = __all_sync(0xffffffffu, r >= rows);
+        const int full_end = min(x.key_end, __reduce_min_sync(0xffffffffu, !valid ? 1 << 30 : p.tree ? x.seq.base() : x.seq.base() + token + 1));
         for (int j = 0; j < n; ++j, ++hc) {
           const int buf = NT == 2 ? t : hc & 1;
-          const uint32_t t_s = tbase + t_lane + C::T_S + buf * 128;
+          const uint32_t t_s = t_lane + C::T_S + buf * 128;
           if (ok) ok = mbar_wait_warp(&s_full[buf], (NT == 2 ? hc : hc >> 1) & 1, abort_flag, 540);
-          if (ok && !idle) {
-            tc_fence_after();
-            const int k0 = x.key0 + j * C::BN;
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-            auto settle = [&] {
-              if (NT == 2) return true;                       // S came behind the tile's last product
-              const bool done = mbar_wait_warp(&pv_done[(hc - 1) & 1], (hc - 1) >> 1 & 1, abort_flag, 541);
+          tc_fence_after();
+          const int k0 = x.key0 + j * C::BN;
+          const bool plain = k0 + C::BN <= full_end;
+          if constexpr (NT == 2) {
+            if (ok && !idle) {
+              bool done = false;
+              if (plain && !far) {
+                done = tree_softmax_plain<D>(t_s, t_o, j == 0, valid, c2, r);
+                far = !done;
+              }
+              if (!done) {
+                uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+                if (!plain && valid) tree_mask<4>(p, x.seq, token, k0, w);
+                tree_softmax_masked<D>(t_s, t_o, w, j == 0, valid, c2, r);
+              }
+            }
+          } else if (!idle) {
+            // two threads a row: both read their half of S, exchange its maximum, and then write P over the first half
+            float s[64];
+            float top = -INFINITY;
+            if (ok) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                uint32_t rr[32];
+                tmem_ld32(t_s + half * 64 + k * 32, rr);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
+              }
+              tmem_wait_ld();
+              if (!plain) {
+                uint32_t w[2] = {0u, 0u};
+                if (valid) tree_mask<2>(p, x.seq, token, k0 + half * 64, w);
+#pragma unroll
+                for (int k = 0; k < 64; ++k)
+                  if (!(w[k >> 5] >> (k & 31) & 1u)) s[k] = -INFINITY;
+              }
+              top = fmaxf(max32(s), max32(s + 32));
+              tmem_st1(t_lane + C::T_X + 2 * (hc & 1) + half, __float_as_uint(top));
+              tmem_wait_st();
+              tc_fence_before();
+            }
+            named_bar_sync(C::BAR_PAIR + sub, 64);            // (joined whatever became of a wait)
+            if (ok) {
               tc_fence_after();
-              return done;
-            };
-            if (!far && k0 + C::BN <= min(full_end, x.key_end)) {
-              ok = tree_softmax<D, true>(t_s, t_o, w, j == 0, c2, m, l, lh, far, settle);
-            } else {
-              if (r < rows) tree_mask(p, x.seq, token, k0, w);
-              ok = tree_softmax<D, false>(t_s, t_o, w, j == 0, c2, m, l, lh, far, settle);
+              const uint32_t other = tmem_ld1(t_lane + C::T_X + 2 * (hc & 1) + (half ^ 1));
+              tmem_wait_ld();
+              bool any;
+              const float alpha = r.follow(fmaxf(r.m, fmaxf(top, __uint_as_float(other))), c2, valid, &any);
+              if (any && j > 0) {
+                ok = mbar_wait_warp(&pv_done[(hc - 1) & 1], (hc - 1) >> 1 & 1, abort_flag, 541);
+                tc_fence_after();
+                if (ok) tree_rescale<COLS>(t_o, alpha);
+              }
+              const float ref = r.m == -INFINITY ? 0.f : r.m;
+              uint32_t pk[32];
+              tree_weights(s, ref, c2, r, pk);
+              tree_weights(s + 32, ref, c2, r, pk + 16);
+              tmem_st32(t_s + half * 32, pk);
             }
           }
           if (ok) {
@@ -635,6 +763,21 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
             named_bar_sync(C::BAR_P + buf, C::BAR_P_THREADS);
           }
         }
+        if constexpr (NT == 1) {
+          if (!idle) {                                        // the halves' sums
+            tmem_st1(t_lane + C::T_X + 4 + half, __float_as_uint(r.l));
+            tmem_st1(t_lane + C::T_X + 6 + half, __float_as_uint(r.lh));
+            tmem_wait_st();
+            tc_fence_before();
+            named_bar_sync(C::BAR_PAIR + sub, 64);
+            tc_fence_after();
+            const uint32_t l0 = tmem_ld1(t_lane + C::T_X + 4), l1 = tmem_ld1(t_lane + C::T_X + 5);
+            const uint32_t h0 = tmem_ld1(t_lane + C::T_X + 6), h1 = tmem_ld1(t_lane + C::T_X + 7);
+            tmem_wait_ld();
+            r.l = __uint_as_float(l0) + __uint_as_float(l1);
+            r.lh = __uint_as_float(h0) + __uint_as_float(h1);
+          }
+        }
         if (ok) {
           // (one row tile: the product before the last one with this barrier was done when the last S was)
           const int done = NT == 2 ? t : (hc - 1) & 1;
@@ -642,46 +785,52 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           tc_fence_after();
         }
       }
-      if (!ok || __all_sync(0xffffffffu, r >= rows)) continue;
+      if (!ok || idle) continue;
       // the row's result, or its stretch's state
-      const bool none = l == 0.f;
-      const float inv = none ? 0.f : 1.f / lh;
+      const bool none = r.l == 0.f;
+      const float inv = none ? 0.f : 1.f / r.lh;
       const bool spoil = n > 0 && spoilt[2 * t + (mine & 1)] == mine;
-      float* dst = x.slot < 0 ? nullptr : p.part + (static_cast<size_t>(x.slot) * p.state_rows + (t * 128 + row)) * C::STATE;
-#pragma unroll
-      for (int k = 0; k < D / 32; ++k) {
+      const size_t th = static_cast<size_t>(x.seq.first + token) * p.H + head;
+      float* dst = x.slot < 0 ? nullptr : p.part + static_cast<size_t>(x.slot) * (D + 3) * p.state_rows + t * 128 + row;
+#pragma unroll 1
+      for (int k = 0; k < COLS; k += 32) {
+        const int col = half * COLS + k;
         float acc[32];
+        uint32_t rr[32];
         if (n > 0) {
-          uint32_t rr[32];
-          tmem_ld32(t_o + k * 32, rr);
+          tmem_ld32(t_o + k, rr);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(rr[i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
         }
-        if (r < rows) {
-          if (spoil) tree_spoil<D>(p, x, p.tree ? x.seq.base() : x.seq.base() + x.rb * C::ROWS / p.G + 1, token, k * 32, acc);
-          if (dst) {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + k * 32 + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+        for (int i = 0; i < 32; ++i) acc[i] = n > 0 ? __uint_as_float(rr[i]) : 0.f;
+        if (valid) {
+          if (spoil) tree_spoil<D>(p, x, common(), token, col, acc);
+          if (dst) {
+            float* at = dst + col * p.state_rows;
+#pragma unroll
+            for (int i = 0; i < 32; ++i, at += p.state_rows) *at = acc[i];
           } else {
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               uint32_t h[4];
 #pragma unroll
               for (int e = 0; e < 4; ++e) h[e] = none ? 0u : pack_bf16x2(acc[i + 2 * e] * inv, acc[i + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(p.o + th * D + k * 32 + i) = make_uint4(h[0], h[1], h[2], h[3]);
+              *reinterpret_cast<uint4*>(p.o + th * D + col + i) = make_uint4(h[0], h[1], h[2], h[3]);
             }
           }
         }
       }
-      if (r < rows) {
-        if (dst) *reinterpret_cast<float4*>(dst + D) = make_float4(none ? -INFINITY : m * c2, l, lh, 0.f);
-        else
-          p.lse[static_cast<size_t>(head) * p.total + x.seq.first + token] = none ? -INFINITY : fmaf(m, c2, log2f(l)) * 0.6931471805599453f;
+      if (valid && half == 0) {
+        if (dst) {
+          dst[D * p.state_rows] = none ? -INFINITY : r.m * c2;
+          dst[(D + 1) * p.state_rows] = r.l;
+          dst[(D + 2) * p.state_rows] = r.lh;
+        } else {
+          p.lse[static_cast<size_t>(head) * p.total + x.seq.first + token] = none ? -INFINITY : fmaf(r.m, c2, log2f(r.l)) * 0.6931471805599453f;
+        }
       }
+      // (what was read of O comes before the next item's first product, which the next hand-off lets go)
+      tc_fence_before();
     }
   }
   __syncwarp();
@@ -693,148 +842,177 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   }
 }
 
-// Joins the n states of a row, ``stride`` floats apart (the first one ``skip`` further on), by one warp.
-template <int D>
-__device__ __forceinline__ void tree_join(const float* base, size_t stride, size_t skip, int n, uint16_t* o, float* lse) {
-  constexpr int V = D / 32;                                   // consecutive elements a lane
-  constexpr int AT_ONCE = 8;
-  const int lane = threadIdx.x & 31;
-  float M = -INFINITY, L = 0.f, LH = 0.f, acc[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
-  for (int i0 = 0; i0 < n; i0 += AT_ONCE) {
-    float4 ml[AT_ONCE];
-    float v[AT_ONCE][V];
-#pragma unroll
-    for (int j = 0; j < AT_ONCE; ++j) {
-      ml[j] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
-      if (i0 + j < n) {
-        const float* st = base + (i0 + j) * stride + (i0 + j == 0 ? skip : 0);
-        ml[j] = *reinterpret_cast<const float4*>(st + D);
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 y = *reinterpret_cast<const float2*>(st + V * lane + k);
-          v[j][k] = y.x;
-          v[j][k + 1] = y.y;
+// Joins the states of row blocks that are cut.  A block takes RB rows and 2048 / RB columns (D at most) of one row
+// block; a state's rows lie side by side, so that a lane has one row and every (32 / RB)th column, and the warps share
+// the states out.  SHARES: row block of bound i + 1 between the CTAs' shares, if that is the first within it; else of
+// the i-th item that was split.
+constexpr int kTreeJoinWarps = 4;
+
+template <int D, int RB>
+struct TreeJoinCfg {
+  static constexpr int COLS = 2048 / RB < D ? 2048 / RB : D;
+  static constexpr int STEP = 32 / RB;                        // columns side by side in a warp
+  static constexpr int PER = COLS / STEP;                     // columns of a lane
+};
+
+template <int D, int RB, bool SHARES>
+__global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas, int chunks) {
+  using J = TreeJoinCfg<D, RB>;
+  __shared__ int found[7];                                    // first token, tokens, key head, token of row 0, states, first slot, -
+  __shared__ float sums[kTreeJoinWarps][J::COLS][RB + 1];
+  __shared__ float parts[3][kTreeJoinWarps][RB], weights[kTreeJoinWarps][RB];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col0 = blockIdx.y * J::COLS, chunk = blockIdx.x % chunks, i = blockIdx.x / chunks;
+  if (warp == 0) {
+    int n = 0, slot = 0, head = 0, token0 = 0;
+    PagedSeq s{0, 0, 0};
+    if constexpr (SHARES) {
+      int b;
+      long long before = 0;
+      const Q4Share sh = tree_share(p, ctas, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
+      if (b >= 0) {
+        s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
+        const int steps = tree_steps(s);
+        head = static_cast<int>(sh.begin(i + 1) - before) / steps;
+        const long long u0 = before + static_cast<long long>(head) * steps;
+        const int c0 = sh.owner(u0), c1 = sh.owner(u0 + steps - 1);
+        if (c0 != c1 && c0 == i) {                            // (c0 == i: bound i + 1 is its first)
+          n = c1 - c0 + 1;
+          slot = 2 * c0;
         }
       }
+    } else {
+      const int item = p.full_items + i, w = item / p.row_blocks;
+      head = w % p.heads;
+      s = paged_seq(p.cu, p.seqlens, w / p.heads, p.total, p.max_q, p.max_k, false, 0);
+      token0 = (p.row_blocks - 1 - item % p.row_blocks) * 2 * p.tokens;
+      n = p.tail_splits;
+      slot = i * p.tail_splits;
     }
-#pragma unroll
-    for (int j = 0; j < AT_ONCE; ++j) {
-      if (ml[j].y == 0.f) continue;                           // no keys (a sum that is no number goes on)
-      const float top = fmaxf(M, ml[j].x);
-      const float alpha = top == M ? 1.f : fast_exp2(M - top), wt = fast_exp2(ml[j].x - top);
-      M = top;
-      L = fmaf(L, alpha, wt * ml[j].y);
-      LH = fmaf(LH, alpha, wt * ml[j].z);
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] = fmaf(acc[k], alpha, wt * v[j][k]);
+    if (lane == 0) {
+      found[0] = s.first; found[1] = s.nq; found[2] = head; found[3] = token0; found[4] = token0 < s.nq ? n : 0; found[5] = slot;
     }
   }
-  const bool none = L == 0.f;
-  const float inv = none ? 0.f : 1.f / LH;
+  __syncthreads();
+  pdl_wait();
+  const int n = found[4];
+  if (n == 0) return;
+  // token of a row of the state, or -1
+  auto token_of = [&](int r) {
+    const int in_tile = (r & 127) / p.group, token = found[3] + (r >> 7) * p.tokens + in_tile;
+    return in_tile < p.tokens && token < found[1] ? token : -1;
+  };
+  const int rr = lane % RB, sub = lane / RB;
+  // this warp's states, then all warps' (what they hold is asked for at once: each round of loads is a microsecond)
+  float m = -INFINITY, l = 0.f, lh = 0.f, acc[J::PER];
 #pragma unroll
-  for (int k = 0; k < V; k += 2)
-    *reinterpret_cast<uint32_t*>(o + V * lane + k) = none ? 0u : pack_bf16x2(acc[k] * inv, acc[k + 1] * inv);
-  if (lane == 0) *lse = none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  for (int c = 0; c < J::PER; ++c) acc[c] = 0.f;
+  for (int k = warp; k < n; k += kTreeJoinWarps) {
+    // state k: SHARES: the first CTA's second place, the others' first one
+    const int slot = SHARES ? found[5] + 2 * k + (k == 0 ? 1 : 0) : found[5] + k;
+    const float* st = p.part + static_cast<size_t>(slot) * (D + 3) * p.state_rows + chunk * RB + rr;
+    const float mk = st[D * p.state_rows], lk = st[(D + 1) * p.state_rows], lhk = st[(D + 2) * p.state_rows];
+    float v[J::PER];
+    const float* at = st + (col0 + sub) * p.state_rows;
+#pragma unroll
+    for (int c = 0; c < J::PER; ++c, at += J::STEP * p.state_rows) v[c] = *at;
+    if (lk == 0.f) continue;                                  // no keys (a sum that is no number goes on)
+    const float top = fmaxf(m, mk);
+    const float alpha = top == m ? 1.f : fast_exp2(m - top), wt = fast_exp2(mk - top);
+    m = top;
+    l = fmaf(l, alpha, wt * lk);
+    lh = fmaf(lh, alpha, wt * lhk);
+#pragma unroll
+    for (int c = 0; c < J::PER; ++c) acc[c] = fmaf(acc[c], alpha, wt * v[c]);
+  }
+#pragma unroll
+  for (int c = 0; c < J::PER; ++c) sums[warp][sub + J::STEP * c][rr] = acc[c];
+  if (sub == 0) {
+    parts[0][warp][rr] = m;
+    parts[1][warp][rr] = l;
+    parts[2][warp][rr] = lh;
+  }
+  __syncthreads();
+  if (threadIdx.x < RB) {
+    const int r = chunk * RB + rr, token = token_of(r);
+    float M = -INFINITY, L = 0.f, LH = 0.f;
+#pragma unroll
+    for (int w = 0; w < kTreeJoinWarps; ++w) M = fmaxf(M, parts[0][w][rr]);
+    float wt[kTreeJoinWarps];
+#pragma unroll
+    for (int w = 0; w < kTreeJoinWarps; ++w) {
+      wt[w] = parts[1][w][rr] == 0.f ? 0.f : fast_exp2(parts[0][w][rr] - M);
+      L = fmaf(wt[w], parts[1][w][rr], L);
+      LH = fmaf(wt[w], parts[2][w][rr], LH);
+    }
+    const bool none = L == 0.f;
+    const float inv = none ? 0.f : 1.f / LH;
+#pragma unroll
+    for (int w = 0; w < kTreeJoinWarps; ++w) weights[w][rr] = wt[w] * inv;
+    if (token >= 0 && blockIdx.y == 0)
+      p.lse[static_cast<size_t>(found[2] * p.group + (r & 127) % p.group) * p.total + found[0] + token] =
+          none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  // a warp writes every fourth row, a lane two columns at a time
+  for (int y = warp; y < RB; y += kTreeJoinWarps) {
+    const int r = chunk * RB + y, token = token_of(r);
+    if (token < 0) continue;
+    uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (static_cast<size_t>(found[0] + token) * p.H + found[2] * p.group + (r & 127) % p.group) * D + col0);
+#pragma unroll
+    for (int c = lane; c < J::COLS / 2; c += 32) {
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kTreeJoinWarps; ++w) {
+        v.x = fmaf(weights[w][y], sums[w][2 * c][y], v.x);
+        v.y = fmaf(weights[w][y], sums[w][2 * c + 1][y], v.y);
+      }
+      out[c] = pack_bf16x2(v.x, v.y);
+    }
+  }
 }
 
-// Rows whose row block lies in several CTAs' shares, a warp a row.
-template <int D>
-__global__ void __launch_bounds__(128) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas) {
-  constexpr int STATE = TreeCfg<D, 1>::STATE;
-  const long long th = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const bool some = th < static_cast<long long>(p.total) * p.H;
-  const int tok = some ? static_cast<int>(th / p.H) : 0, head = static_cast<int>(th - static_cast<long long>(tok) * p.H);
-  // (every sequence whose boundaries are sound has its rows, also where those of others are not)
-  int b = -1;
-  long long total = 0, before = 0;
-  for (int i = threadIdx.x & 31; i < p.n_seqs; i += 32) {
-    const PagedSeq s = paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, false, 0);
-    total += s.nq ? static_cast<long long>(max(1, (s.len + kPagedTile - 1) / kPagedTile)) * p.cache.H_kv : 0;
-    if (some && s.first <= tok && tok < s.first + s.nq && b < 0) b = i;
-  }
-  const uint32_t has = __ballot_sync(0xffffffffu, b >= 0);
-  if (has) b = static_cast<int>(__reduce_min_sync(0xffffffffu, static_cast<unsigned>(b < 0 ? 0x7fffffff : b)));
-  for (int i = threadIdx.x & 31; i < b; i += 32) {
-    const PagedSeq s = paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, false, 0);
-    before += s.nq ? static_cast<long long>(max(1, (s.len + kPagedTile - 1) / kPagedTile)) * p.cache.H_kv : 0;
-  }
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
-  int n = 0;
-  size_t base = 0;
-  if (b >= 0) {
-    const PagedSeq s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-    const int steps = max(1, (s.len + kPagedTile - 1) / kPagedTile);
-    Q4Share sh;
-    sh.set(total, ctas);
-    const long long u0 = before + static_cast<long long>(head / p.G) * steps;
-    const int c0 = sh.owner(u0), c1 = sh.owner(u0 + steps - 1);
-    if (c0 != c1) {                                           // (else its CTA wrote the result)
-      n = c1 - c0 + 1;
-      base = (static_cast<size_t>(2 * c0) * p.state_rows + (tok - s.first) * p.G + head % p.G) * STATE;
-    }
-  }
-  pdl_wait();
-  if (n > 0)
-    tree_join<D>(p.part + base, 2 * static_cast<size_t>(p.state_rows) * STATE, static_cast<size_t>(p.state_rows) * STATE, n,
-                 p.o + static_cast<size_t>(th) * D, p.lse + static_cast<size_t>(head) * p.total + tok);
-}
-
-// Rows of the row blocks whose keys were split, a warp a row.
-template <int D>
-__global__ void __launch_bounds__(128) attend_tree_tail_kernel(const __grid_constant__ TreeParams p, int n_rows) {
-  constexpr int STATE = TreeCfg<D, 2>::STATE, ROWS = TreeCfg<D, 2>::ROWS;
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int it = i / ROWS, row = i - it * ROWS, item = p.full_items + it;
-  const int rb = p.row_blocks - 1 - item % p.row_blocks, w = item / p.row_blocks;
-  const int hkv = w % p.cache.H_kv, b = w / p.cache.H_kv;
-  bool some = i < n_rows;
-  PagedSeq s{0, 0, 0};
-  if (some) s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-  const int r = rb * ROWS + row;
-  some = some && r < s.nq * p.G;
-  pdl_wait();
-  if (!some) return;
-  const int tok = s.first + r / p.G, head = hkv * p.G + r % p.G;
-  tree_join<D>(p.part + (static_cast<size_t>(it) * p.tail_splits * p.state_rows + row) * STATE, static_cast<size_t>(p.state_rows) * STATE, 0,
-               p.tail_splits, p.o + (static_cast<size_t>(tok) * p.H + head) * D, p.lse + static_cast<size_t>(head) * p.total + tok);
+template <int D, int RB>
+static cudaError_t launch_tree_join(const TreeParams& p, long long grid, long long cut, cudaStream_t stream) {
+  const int chunks = p.state_rows / RB;
+  const dim3 blocks(static_cast<unsigned>(cut * chunks), D / TreeJoinCfg<D, RB>::COLS);
+  log_launch("attend_tree_join_kernel<D, RB, SHARES>", static_cast<unsigned long long>(blocks.x) * blocks.y, 32 * kTreeJoinWarps, 0ull);
+  if constexpr (RB == 32)
+    if (!p.shares)
+      return launch_join(attend_tree_join_kernel<D, RB, false>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks);
+  return launch_join(attend_tree_join_kernel<D, RB, true>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks);
 }
 
 template <int D, int NT>
-static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, cudaStream_t stream) {
+static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& t, cudaStream_t stream) {
   using C = TreeCfg<D, NT>;
   TreeParams p{};
   const int piece = paged_piece(a.block_size);
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.block_size;
-  if (!make_map_bf16_tok(&p.tk, a.k_cache, D, a.H_kv, rows, 64, piece) || !make_map_bf16_tok(&p.tv, a.v_cache, D, a.H_kv, rows, 64, piece))
+  if (!make_map_bf16_tok(&p.tk, a.k_cache, D, a.H_kv, rows, 64, piece) || !make_map_bf16_tok(&p.tv, a.v_cache, D, a.H_kv, rows, 64, piece) ||
+      !make_map_bf16_group(&p.tq, a.q, D, t.group, a.H / t.group, a.total, 64, t.group, t.tokens))
     return cudaErrorInvalidValue;
   p.cache = {a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks, piece};
-  p.q = static_cast<const uint16_t*>(a.q); p.v = static_cast<const uint16_t*>(a.v_cache);
+  p.v = static_cast<const uint16_t*>(a.v_cache);
   p.o = static_cast<uint16_t*>(a.o); p.lse = a.lse; p.part = a.part;
   p.tree = a.tree; p.words = a.words; p.cu = a.cu; p.seqlens = a.seqlens;
-  p.n_seqs = a.n_seqs; p.H = a.H; p.G = a.H / a.H_kv; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
+  p.group = t.group; p.heads = a.H / t.group; p.per_kv = p.heads / a.H_kv; p.tokens = t.tokens;
+  p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
   p.c2 = a.scale * 1.4426950408889634f;
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(attend_tree_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
   if (e != cudaSuccess) return e;
-  const long long all_rows = static_cast<long long>(p.G) * a.max_q;
   const int sms = min(paged_sm_count(), kTreeMaxCtas);
-  const long long pairs = static_cast<long long>(a.n_seqs) * a.H_kv;
+  const long long pairs = static_cast<long long>(a.n_seqs) * p.heads;
   const long long steps = max(1, (a.max_k + kPagedTile - 1) / kPagedTile);
   long long grid;
-  p.shares = all_rows <= C::ROWS;
+  p.shares = t.tiles <= 2;
+  p.state_rows = t.state_rows;
   if (p.shares) {
     p.whole = steps <= 1;
-    p.state_rows = static_cast<int>(all_rows);
     grid = min(static_cast<long long>(sms), pairs * steps);
   } else {
-    p.state_rows = C::ROWS;
-    p.row_blocks = static_cast<int>((all_rows + C::ROWS - 1) / C::ROWS);
+    p.row_blocks = (t.tiles + 1) / 2;
     const long long items = pairs * p.row_blocks;
     const int tail = static_cast<int>(items % sms);
     const int s = tail ? static_cast<int>(min(static_cast<long long>(sms / tail), steps / 4)) : 1;
@@ -852,22 +1030,16 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, cudaStream_t str
   attend_tree_kernel<D, NT><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (p.shares) {
-    if (p.whole) return cudaSuccess;
-    const unsigned blocks = static_cast<unsigned>((static_cast<long long>(a.total) * a.H + 3) / 4);
-    log_launch("attend_tree_join_kernel<D>", blocks, 128, 0ull);
-    return launch_join(attend_tree_join_kernel<D>, blocks, 128, stream, p, static_cast<int>(grid));
-  }
-  if (p.tail_splits == 1) return cudaSuccess;
-  const int n_rows = static_cast<int>((grid - p.full_items) / p.tail_splits) * C::ROWS;
-  log_launch("attend_tree_tail_kernel<D>", n_rows / 4, 128, 0ull);
-  return launch_join(attend_tree_tail_kernel<D>, static_cast<unsigned>(n_rows / 4), 128, stream, p, n_rows);
+  // the row blocks that a bound cuts, or that were split
+  const long long cut = p.shares ? (p.whole ? 0 : grid - 1) : p.tail_splits == 1 ? 0 : (grid - p.full_items) / p.tail_splits;
+  if (cut == 0) return cudaSuccess;
+  return p.state_rows % 32 ? launch_tree_join<D, 8>(p, grid, cut, stream) : launch_tree_join<D, 32>(p, grid, cut, stream);
 }
 
 cudaError_t launch_attend_tree(const PagedTreeArgs& a, cudaStream_t stream) {
-  const bool one = static_cast<long long>(a.H / a.H_kv) * a.max_q <= 128;
-  if (a.d == 64) return one ? launch_attend_tree_d<64, 1>(a, stream) : launch_attend_tree_d<64, 2>(a, stream);
-  return one ? launch_attend_tree_d<128, 1>(a, stream) : launch_attend_tree_d<128, 2>(a, stream);
+  const TreeRows t = tree_rows(a.H, a.H_kv, a.max_q);
+  if (a.d == 64) return t.tiles == 1 ? launch_attend_tree_d<64, 1>(a, t, stream) : launch_attend_tree_d<64, 2>(a, t, stream);
+  return t.tiles == 1 ? launch_attend_tree_d<128, 1>(a, t, stream) : launch_attend_tree_d<128, 2>(a, t, stream);
 }
 
 }  // namespace fa

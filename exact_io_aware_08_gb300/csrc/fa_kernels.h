@@ -188,7 +188,7 @@ struct PagedQ4Args {
 struct PagedTreeArgs {
   const void *q, *k_cache, *v_cache;
   void* o;
-  float *lse, *part;            // [H, total]; states of cut row blocks, d + 4 floats a row
+  float *lse, *part;            // [H, total]; states of cut row blocks, d + 3 floats a row
   const int *tree, *cu, *seqlens, *block_table;               // tree [total, words] or null
   int words, n_seqs, H, H_kv, total, max_q, max_k, d, num_blocks, block_size, max_blocks;
   float scale;
@@ -229,14 +229,28 @@ cudaError_t status_fetch_attend_tree(cudaStream_t, unsigned int*, int*);
 cudaError_t status_fetch_weigh(cudaStream_t, unsigned int*, int*);
 cudaError_t status_fetch_evict(cudaStream_t, unsigned int*, int*);
 
-// Attention over the bf16 paged cache: up to 128 or 256 rows of a key head (its query heads times a sequence's
-// query tokens) are a row block.  Where that is all of them the work is shared out to at most kTreeMaxCtas CTAs
-// that keep at most two states each; else the last row blocks are split, into as many parts as there are CTAs.
+// Attention over the bf16 paged cache: rows of a key head are its query heads times a sequence's query tokens, in
+// tiles of whole tokens, up to 128 rows each.  (Of more than 128 query heads a key head, some at a time: the largest
+// divisor that fits.)  Where one or two tiles hold all rows the work is shared out to at most kTreeMaxCtas CTAs that
+// keep at most two states each; else the last row blocks, of two tiles, are split into as many parts as there are CTAs.
 constexpr int kTreeMaxCtas = 152;
+struct TreeRows {
+  int group, tokens, tiles, state_rows;                       // heads taken at a time, tokens of a tile
+};
+inline TreeRows tree_rows(int H, int H_kv, int max_q) {
+  TreeRows t;
+  const int G = H / H_kv;
+  t.group = G < 128 ? G : 128;
+  while (G % t.group) --t.group;
+  t.tokens = 128 / t.group < max_q ? 128 / t.group : max_q < 1 ? 1 : max_q;
+  t.tiles = (max_q + t.tokens - 1) / t.tokens;
+  const int last = (max_q - (t.tiles - 1) * t.tokens) * t.group;
+  t.state_rows = t.tiles > 2 ? 256 : t.tiles == 2 ? 128 + (last + 31) / 32 * 32 : last <= 8 ? 8 : (last + 31) / 32 * 32;
+  return t;
+}
 inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
-  const long long rows = static_cast<long long>(H / H_kv) * max_q;
-  const size_t states = rows <= 256 ? 2 * kTreeMaxCtas * static_cast<size_t>(rows) : kTreeMaxCtas * size_t(256);
-  return states * (d + 4) * sizeof(float);
+  const TreeRows t = tree_rows(H, H_kv, max_q);
+  return (t.tiles <= 2 ? 2 : 1) * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) * sizeof(float);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);

@@ -209,9 +209,9 @@ inline int q4_join_warps(long long rows) { return rows <= 1024 ? 4 : 1; }
 // The join runs behind the chunks on the stream, but may start while their last CTAs run
 // (programmatic dependent launch): it reads lengths and boundaries, then waits for the states.
 template <typename... P, typename... A>
-static cudaError_t launch_join(void (*kernel)(P...), unsigned blocks, unsigned threads, cudaStream_t stream, A... args) {
+static cudaError_t launch_join(void (*kernel)(P...), dim3 blocks, unsigned threads, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = blocks;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
