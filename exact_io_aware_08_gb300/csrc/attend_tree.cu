@@ -55,6 +55,7 @@ struct TreeCfg {
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t T_S = 0, T_O = 256, T_X = 384;    // T_X: exchanged maxima and sums (NT = 1)
   static constexpr int THREADS = 384;
+  static constexpr int STATE = 32 * (D + 3);                  // of 32 rows: each column, reference, sum, rounded sum
   // NT = 2: launched with 168 registers a thread, moved from the control warps
   static constexpr uint32_t REG_CTRL = 80, REG_SOFTMAX = 208;
   static constexpr int REG_NEED = NT == 2 ? 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX)) : 0;
@@ -161,9 +162,10 @@ struct TreeWalk {
   }
 };
 
-// By a whole warp: the shares, and the sequence that holds unit ``u_of(shares)`` with the units before it.
+// By a whole warp: the shares, and the sequence that holds unit ``u_of(shares)`` (b = -1 where there is none), or
+// sequence ``at`` where that is given, with the units before it.
 template <typename F>
-__device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, bool report, F u_of, int* b, long long* before) {
+__device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, bool report, F u_of, int at, int* b, long long* before) {
   const int lane = threadIdx.x & 31;
   auto units = [&](int i, bool rep) {
     return static_cast<long long>(tree_steps(paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501))) * p.heads;
@@ -178,7 +180,7 @@ __device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, boo
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   sh.set(mine, grid);
-  const long long u = u_of(sh);
+  const long long u = at >= 0 ? 1LL << 62 : u_of(sh);
   long long sum = 0;
   *b = -1;
   for (int base = 0; base < p.n_seqs && u >= 0; base += 32) {
@@ -189,7 +191,7 @@ __device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, boo
       const long long x = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += x;
     }
-    const uint32_t beyond = __ballot_sync(0xffffffffu, sum + inc > u);
+    const uint32_t beyond = __ballot_sync(0xffffffffu, at >= 0 ? base + lane >= at : sum + inc > u);
     if (beyond) {
       const int l = __ffs(beyond) - 1;
       *b = base + l;
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       long long before = 0;
       const Q4Share sh = tree_share(p, gridDim.x, blockIdx.x == 0,
                                     [&](const Q4Share& y) { return static_cast<int>(blockIdx.x) < y.n && y.total > 0 ? y.begin(blockIdx.x) : -1LL; },
-                                    &b, &before);
+                                    -1, &b, &before);
       const int u = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x) - before);
       const int n = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x + 1) - sh.begin(blockIdx.x));
       if (lane == 0) {
@@ -600,29 +602,38 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           const int k0 = x.key0 + j * C::BN;
           if (ok && (k0 + C::BN > x.key_end || k0 + C::BN > from)) {
             uint8_t* tile = sKV + (at % C::NST) * C::TILE;
-            const int live = min(C::BN, x.key_end - k0);
-            auto vec = [&](int i) {                           // 16-byte vector i of the tile, row by row
-              const int row = i / (D / 8), c = i % (D / 8);
-              return reinterpret_cast<uint4*>(tile + (c >> 3) * C::CHUNK + sw128_offset(row, (c & 7) * 8));
-            };
+            const int live = min(C::BN, x.key_end - k0), lo = max(0, min(from - k0, live));
+            // lane: 16 bytes of every RS-th row, eight rows (one period of the swizzle) at a time
+            constexpr int L = D / 8, RS = 32 / L;
+            const int c = lane % L, r0 = lane / L;
             bool found = false;
-#pragma unroll 4
-            for (int i = max(0, min(from - k0, live)) * (D / 8) + lane; i < live * (D / 8); i += 32) {
-              uint4 v = *vec(i);
-              uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-              bool bad = false;
+#pragma unroll 1
+            for (int r8 = lo & ~7; r8 < C::BN; r8 += 8) {
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const bool lo = (e[y] & 0x7f80u) == 0x7f80u, hi = (e[y] & 0x7f800000u) == 0x7f800000u;
-                bad |= lo || hi;
-                if (lo) e[y] &= 0xffff0000u;
-                if (hi) e[y] &= 0xffffu;
+              for (int u = 0; u < 8 / RS; ++u) {
+                const int row = r8 + r0 + u * RS;
+                uint4* at16 = reinterpret_cast<uint4*>(tile + r8 * 128 + (c >> 3) * C::CHUNK + sw128_offset(r0 + u * RS, (c & 7) * 8));
+                if (row >= live) {
+                  *at16 = make_uint4(0u, 0u, 0u, 0u);
+                } else if (row >= lo) {
+                  uint4 v = *at16;
+                  uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+                  // an exponent of all ones carries into the sign's place
+                  uint32_t carry = 0;
+#pragma unroll
+                  for (int y = 0; y < 4; ++y) carry |= ((e[y] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+                  if (carry) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                      if ((e[y] & 0x7f80u) == 0x7f80u) e[y] &= 0xffff0000u;
+                      if ((e[y] & 0x7f800000u) == 0x7f800000u) e[y] &= 0xffffu;
+                    }
+                    *at16 = v;
+                    found = true;
+                  }
+                }
               }
-              if (bad) *vec(i) = v;
-              found |= bad;
             }
-#pragma unroll 4
-            for (int i = live * (D / 8) + lane; i < C::BN * (D / 8); i += 32) *vec(i) = make_uint4(0u, 0u, 0u, 0u);
             if (found && n0 > 0) spoilt[c0 & 1] = c0;
             if (found && n1 > 0) spoilt[2 + (c1 & 1)] = c1;
             __threadfence_block();
@@ -791,40 +802,40 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       const float inv = none ? 0.f : 1.f / r.lh;
       const bool spoil = n > 0 && spoilt[2 * t + (mine & 1)] == mine;
       const size_t th = static_cast<size_t>(x.seq.first + token) * p.H + head;
-      float* dst = x.slot < 0 ? nullptr : p.part + static_cast<size_t>(x.slot) * (D + 3) * p.state_rows + t * 128 + row;
+      float* dst = x.slot < 0 ? nullptr : p.part + (static_cast<size_t>(x.slot) * (p.state_rows / 32) + t * 4 + sub) * C::STATE + lane;
 #pragma unroll 1
       for (int k = 0; k < COLS; k += 32) {
         const int col = half * COLS + k;
-        float acc[32];
         uint32_t rr[32];
+        float acc[32];
         if (n > 0) {
           tmem_ld32(t_o + k, rr);
           tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[i] = __uint_as_float(rr[i]);
+          if (spoil && valid) tree_spoil<D>(p, x, common(), token, col, acc);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) acc[i] = 0.f;
         }
+        if (!valid) continue;
+        if (dst) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i) acc[i] = n > 0 ? __uint_as_float(rr[i]) : 0.f;
-        if (valid) {
-          if (spoil) tree_spoil<D>(p, x, common(), token, col, acc);
-          if (dst) {
-            float* at = dst + col * p.state_rows;
+          for (int i = 0; i < 32; ++i) dst[(col + i) * 32] = acc[i];
+        } else {
+          // (a row that sees nothing has sums of 0, and 0 here)
+          uint4* out = reinterpret_cast<uint4*>(p.o + th * D + col);
 #pragma unroll
-            for (int i = 0; i < 32; ++i, at += p.state_rows) *at = acc[i];
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-              uint32_t h[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) h[e] = none ? 0u : pack_bf16x2(acc[i + 2 * e] * inv, acc[i + 2 * e + 1] * inv);
-              *reinterpret_cast<uint4*>(p.o + th * D + col + i) = make_uint4(h[0], h[1], h[2], h[3]);
-            }
-          }
+          for (int i = 0; i < 32; i += 8)
+            out[i / 8] = make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
+                                    pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
         }
       }
       if (valid && half == 0) {
         if (dst) {
-          dst[D * p.state_rows] = none ? -INFINITY : r.m * c2;
-          dst[(D + 1) * p.state_rows] = r.l;
-          dst[(D + 2) * p.state_rows] = r.lh;
+          dst[D * 32] = none ? -INFINITY : r.m * c2;
+          dst[(D + 1) * 32] = r.l;
+          dst[(D + 2) * 32] = r.lh;
         } else {
           p.lse[static_cast<size_t>(head) * p.total + x.seq.first + token] = none ? -INFINITY : fmaf(r.m, c2, log2f(r.l)) * 0.6931471805599453f;
         }
@@ -842,41 +853,43 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   }
 }
 
-// Joins the states of row blocks that are cut.  A block takes RB rows and 2048 / RB columns (D at most) of one row
-// block; a state's rows lie side by side, so that a lane has one row and every (32 / RB)th column, and the warps share
-// the states out.  SHARES: row block of bound i + 1 between the CTAs' shares, if that is the first within it; else of
-// the i-th item that was split.
-constexpr int kTreeJoinWarps = 4;
+// Joins the states of row blocks that are cut.  A block takes RB rows of one row block: a lane has one row and eight
+// columns (a state's rows lie side by side), S warps share the states of those out, and where that leaves warps for
+// less than D columns, blockIdx.y tells which.  SHARES: row block of bound i + 1 between the CTAs' shares, if that is
+// the first within it, or, BY_PAIR, i-th row block of the call; else the i-th item that was split.  Little code: each part of it runs once, and is fetched
+// while nothing else happens (64 columns a lane, in straight lines: 7.6 us behind 1 x 8 tokens over 1000).
+constexpr int kTreeJoinWarps = 16;
 
-template <int D, int RB>
+template <int D, int RB, int S>
 struct TreeJoinCfg {
-  static constexpr int COLS = 2048 / RB < D ? 2048 / RB : D;
-  static constexpr int STEP = 32 / RB;                        // columns side by side in a warp
-  static constexpr int PER = COLS / STEP;                     // columns of a lane
+  static constexpr int STEP = 32 / RB;                        // lanes of a row
+  static constexpr int COLS = kTreeJoinWarps / S * STEP * 8;  // columns of a block
+  static_assert(COLS <= D, "columns of a block");
 };
 
-template <int D, int RB, bool SHARES>
-__global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas, int chunks) {
-  using J = TreeJoinCfg<D, RB>;
-  __shared__ int found[7];                                    // first token, tokens, key head, token of row 0, states, first slot, -
-  __shared__ float sums[kTreeJoinWarps][J::COLS][RB + 1];
-  __shared__ float parts[3][kTreeJoinWarps][RB], weights[kTreeJoinWarps][RB];
+template <int D, int RB, int S, bool SHARES>
+__global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas, int chunks, int by_pair) {
+  using J = TreeJoinCfg<D, RB, S>;
+  __shared__ int found[6];                                    // first token, tokens, key head, token of row 0, states, first slot
+  __shared__ float merge[S > 1 ? kTreeJoinWarps : 1][11][32]; // a lane's columns, reference, sum, rounded sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int col0 = blockIdx.y * J::COLS, chunk = blockIdx.x % chunks, i = blockIdx.x / chunks;
+  const int chunk = blockIdx.x % chunks, i = blockIdx.x / chunks;
   if (warp == 0) {
     int n = 0, slot = 0, head = 0, token0 = 0;
     PagedSeq s{0, 0, 0};
     if constexpr (SHARES) {
+      // with fewer row blocks than bounds a block of this kernel takes one of those, else one of these
+      const int at = by_pair ? i / p.heads : -1;
       int b;
       long long before = 0;
-      const Q4Share sh = tree_share(p, ctas, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
+      const Q4Share sh = tree_share(p, ctas, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, at, &b, &before);
       if (b >= 0) {
         s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-        const int steps = tree_steps(s);
-        head = static_cast<int>(sh.begin(i + 1) - before) / steps;
+        const int steps = max(1, tree_steps(s));
+        head = by_pair ? i - b * p.heads : static_cast<int>(sh.begin(i + 1) - before) / steps;
         const long long u0 = before + static_cast<long long>(head) * steps;
         const int c0 = sh.owner(u0), c1 = sh.owner(u0 + steps - 1);
-        if (c0 != c1 && c0 == i) {                            // (c0 == i: bound i + 1 is its first)
+        if (s.nq && c0 != c1 && (by_pair || c0 == i)) {       // (c0 == i: bound i + 1 is its first)
           n = c1 - c0 + 1;
           slot = 2 * c0;
         }
@@ -894,93 +907,85 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(c
     }
   }
   __syncthreads();
+  const int n = found[4], r = chunk * RB + lane % RB;
+  const int in_tile = (r & 127) / p.group, token = found[3] + (r >> 7) * p.tokens + in_tile;
+  const bool some = in_tile < p.tokens && token < found[1];
+  const int col = (blockIdx.y * (kTreeJoinWarps / S) + warp / S) * J::STEP * 8 + (lane / RB) * 8;
   pdl_wait();
-  const int n = found[4];
-  if (n == 0) return;
-  // token of a row of the state, or -1
-  auto token_of = [&](int r) {
-    const int in_tile = (r & 127) / p.group, token = found[3] + (r >> 7) * p.tokens + in_tile;
-    return in_tile < p.tokens && token < found[1] ? token : -1;
-  };
-  const int rr = lane % RB, sub = lane / RB;
-  // this warp's states, then all warps' (what they hold is asked for at once: each round of loads is a microsecond)
-  float m = -INFINITY, l = 0.f, lh = 0.f, acc[J::PER];
+  if (n == 0 || !__any_sync(0xffffffffu, some)) return;       // (the same for the whole block: its warps have the same rows)
+  float m = -INFINITY, l = 0.f, lh = 0.f, acc[8];
 #pragma unroll
-  for (int c = 0; c < J::PER; ++c) acc[c] = 0.f;
-  for (int k = warp; k < n; k += kTreeJoinWarps) {
-    // state k: SHARES: the first CTA's second place, the others' first one
-    const int slot = SHARES ? found[5] + 2 * k + (k == 0 ? 1 : 0) : found[5] + k;
-    const float* st = p.part + static_cast<size_t>(slot) * (D + 3) * p.state_rows + chunk * RB + rr;
-    const float mk = st[D * p.state_rows], lk = st[(D + 1) * p.state_rows], lhk = st[(D + 2) * p.state_rows];
-    float v[J::PER];
-    const float* at = st + (col0 + sub) * p.state_rows;
-#pragma unroll
-    for (int c = 0; c < J::PER; ++c, at += J::STEP * p.state_rows) v[c] = *at;
-    if (lk == 0.f) continue;                                  // no keys (a sum that is no number goes on)
+  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  // a state's, or a warp's, share of the row (sum 0: no keys, and a reference of -inf; a sum that is no number goes on)
+  auto add = [&](float mk, float lk, float lhk, const float (&v)[8]) {
     const float top = fmaxf(m, mk);
-    const float alpha = top == m ? 1.f : fast_exp2(m - top), wt = fast_exp2(mk - top);
+    const float alpha = top == m ? 1.f : fast_exp2(m - top), wt = lk == 0.f ? 0.f : fast_exp2(mk - top);
     m = top;
     l = fmaf(l, alpha, wt * lk);
     lh = fmaf(lh, alpha, wt * lhk);
 #pragma unroll
-    for (int c = 0; c < J::PER; ++c) acc[c] = fmaf(acc[c], alpha, wt * v[c]);
-  }
+    for (int c = 0; c < 8; ++c) acc[c] = fmaf(acc[c], alpha, wt * v[c]);
+  };
+  constexpr int AT_ONCE = S > 4 ? 4 : 2;                      // states whose loads are under way together
+  for (int k0 = warp % S; k0 < n; k0 += S * AT_ONCE) {
+    float v[AT_ONCE][8], mk[AT_ONCE], lk[AT_ONCE], lhk[AT_ONCE];
 #pragma unroll
-  for (int c = 0; c < J::PER; ++c) sums[warp][sub + J::STEP * c][rr] = acc[c];
-  if (sub == 0) {
-    parts[0][warp][rr] = m;
-    parts[1][warp][rr] = l;
-    parts[2][warp][rr] = lh;
-  }
-  __syncthreads();
-  if (threadIdx.x < RB) {
-    const int r = chunk * RB + rr, token = token_of(r);
-    float M = -INFINITY, L = 0.f, LH = 0.f;
+    for (int j = 0; j < AT_ONCE; ++j) {
+      // state k: SHARES: the first CTA's second place, the others' first one
+      const int k = k0 + j * S;
+      const int slot = SHARES ? found[5] + 2 * k + (k == 0 ? 1 : 0) : found[5] + k;
+      const float* st = p.part + (static_cast<size_t>(slot) * (p.state_rows / 32) + (r >> 5)) * (32 * (D + 3)) + (r & 31);
+      mk[j] = -INFINITY;
+      lk[j] = lhk[j] = 0.f;
 #pragma unroll
-    for (int w = 0; w < kTreeJoinWarps; ++w) M = fmaxf(M, parts[0][w][rr]);
-    float wt[kTreeJoinWarps];
-#pragma unroll
-    for (int w = 0; w < kTreeJoinWarps; ++w) {
-      wt[w] = parts[1][w][rr] == 0.f ? 0.f : fast_exp2(parts[0][w][rr] - M);
-      L = fmaf(wt[w], parts[1][w][rr], L);
-      LH = fmaf(wt[w], parts[2][w][rr], LH);
-    }
-    const bool none = L == 0.f;
-    const float inv = none ? 0.f : 1.f / LH;
-#pragma unroll
-    for (int w = 0; w < kTreeJoinWarps; ++w) weights[w][rr] = wt[w] * inv;
-    if (token >= 0 && blockIdx.y == 0)
-      p.lse[static_cast<size_t>(found[2] * p.group + (r & 127) % p.group) * p.total + found[0] + token] =
-          none ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-  }
-  __syncthreads();
-  // a warp writes every fourth row, a lane two columns at a time
-  for (int y = warp; y < RB; y += kTreeJoinWarps) {
-    const int r = chunk * RB + y, token = token_of(r);
-    if (token < 0) continue;
-    uint32_t* out = reinterpret_cast<uint32_t*>(p.o + (static_cast<size_t>(found[0] + token) * p.H + found[2] * p.group + (r & 127) % p.group) * D + col0);
-#pragma unroll
-    for (int c = lane; c < J::COLS / 2; c += 32) {
-      float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kTreeJoinWarps; ++w) {
-        v.x = fmaf(weights[w][y], sums[w][2 * c][y], v.x);
-        v.y = fmaf(weights[w][y], sums[w][2 * c + 1][y], v.y);
+      for (int c = 0; c < 8; ++c) v[j][c] = k < n ? st[(col + c) * 32] : 0.f;
+      if (k < n) {
+        mk[j] = st[D * 32];
+        lk[j] = st[(D + 1) * 32];
+        lhk[j] = st[(D + 2) * 32];
       }
-      out[c] = pack_bf16x2(v.x, v.y);
+    }
+#pragma unroll
+    for (int j = 0; j < AT_ONCE; ++j) add(mk[j], lk[j], lhk[j], v[j]);
+  }
+  if constexpr (S > 1) {
+    if (warp % S) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) merge[warp][c][lane] = acc[c];
+      merge[warp][8][lane] = m;
+      merge[warp][9][lane] = l;
+      merge[warp][10][lane] = lh;
+    }
+    __syncthreads();
+    if (warp % S) return;
+#pragma unroll 1
+    for (int w = warp + 1; w < warp + S; ++w) {
+      float v[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] = merge[w][c][lane];
+      add(merge[w][8][lane], merge[w][9][lane], merge[w][10][lane], v);
     }
   }
+  if (!some) return;
+  const bool none = l == 0.f;
+  const float inv = none ? 0.f : 1.f / lh;
+  const int head = found[2] * p.group + (r & 127) - in_tile * p.group;
+  uint32_t h[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) h[c] = none ? 0u : pack_bf16x2(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  *reinterpret_cast<uint4*>(p.o + (static_cast<size_t>(found[0] + token) * p.H + head) * D + col) = make_uint4(h[0], h[1], h[2], h[3]);
+  if (col == 0) p.lse[static_cast<size_t>(head) * p.total + found[0] + token] = none ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-template <int D, int RB>
-static cudaError_t launch_tree_join(const TreeParams& p, long long grid, long long cut, cudaStream_t stream) {
-  const int chunks = p.state_rows / RB;
-  const dim3 blocks(static_cast<unsigned>(cut * chunks), D / TreeJoinCfg<D, RB>::COLS);
-  log_launch("attend_tree_join_kernel<D, RB, SHARES>", static_cast<unsigned long long>(blocks.x) * blocks.y, 32 * kTreeJoinWarps, 0ull);
-  if constexpr (RB == 32)
+template <int D, int RB, int S>
+static cudaError_t launch_tree_join(const TreeParams& p, long long grid, long long cut, int by_pair, cudaStream_t stream) {
+  const int chunks = RB == 8 ? 1 : p.state_rows / RB;
+  const dim3 blocks(static_cast<unsigned>(cut * chunks), D / TreeJoinCfg<D, RB, S>::COLS);
+  log_launch("attend_tree_join_kernel<D, RB, S, SHARES>", static_cast<unsigned long long>(blocks.x) * blocks.y, 32 * kTreeJoinWarps, 0ull);
+  if constexpr (RB == 32 && S < 8)
     if (!p.shares)
-      return launch_join(attend_tree_join_kernel<D, RB, false>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks);
-  return launch_join(attend_tree_join_kernel<D, RB, true>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks);
+      return launch_join(attend_tree_join_kernel<D, RB, S, false>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks, 0);
+  return launch_join(attend_tree_join_kernel<D, RB, S, true>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks, by_pair);
 }
 
 template <int D, int NT>
@@ -1030,10 +1035,16 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   attend_tree_kernel<D, NT><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // the row blocks that a bound cuts, or that were split
-  const long long cut = p.shares ? (p.whole ? 0 : grid - 1) : p.tail_splits == 1 ? 0 : (grid - p.full_items) / p.tail_splits;
+  // the row blocks that a bound cuts (of all of them, or of all bounds), or that were split
+  const int by_pair = p.shares && pairs < grid;
+  const long long cut = p.shares ? (p.whole ? 0 : by_pair ? pairs : grid - 1) : p.tail_splits == 1 ? 0 : (grid - p.full_items) / p.tail_splits;
   if (cut == 0) return cudaSuccess;
-  return p.state_rows % 32 ? launch_tree_join<D, 8>(p, grid, cut, stream) : launch_tree_join<D, 32>(p, grid, cut, stream);
+  // A row block has some grid / pairs states where the sequences are alike: with few of them a block has all columns,
+  // with many each warp of eight has an eighth of them.
+  const bool many = p.shares && grid > 8 * pairs;
+  if (t.rows <= 8)
+    return many && D == 128 ? launch_tree_join<D, 8, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 8, 512 / D>(p, grid, cut, by_pair, stream);
+  return many ? launch_tree_join<D, 32, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 32, 128 / D>(p, grid, cut, by_pair, stream);
 }
 
 cudaError_t launch_attend_tree(const PagedTreeArgs& a, cudaStream_t stream) {

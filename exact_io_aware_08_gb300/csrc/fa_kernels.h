@@ -235,7 +235,7 @@ cudaError_t status_fetch_evict(cudaStream_t, unsigned int*, int*);
 // keep at most two states each; else the last row blocks, of two tiles, are split into as many parts as there are CTAs.
 constexpr int kTreeMaxCtas = 152;
 struct TreeRows {
-  int group, tokens, tiles, state_rows;                       // heads taken at a time, tokens of a tile
+  int group, tokens, tiles, rows, state_rows;                 // heads taken at a time, tokens of a tile, rows of a tile
 };
 inline TreeRows tree_rows(int H, int H_kv, int max_q) {
   TreeRows t;
@@ -245,7 +245,8 @@ inline TreeRows tree_rows(int H, int H_kv, int max_q) {
   t.tokens = 128 / t.group < max_q ? 128 / t.group : max_q < 1 ? 1 : max_q;
   t.tiles = (max_q + t.tokens - 1) / t.tokens;
   const int last = (max_q - (t.tiles - 1) * t.tokens) * t.group;
-  t.state_rows = t.tiles > 2 ? 256 : t.tiles == 2 ? 128 + (last + 31) / 32 * 32 : last <= 8 ? 8 : (last + 31) / 32 * 32;
+  t.rows = t.tokens * t.group;
+  t.state_rows = t.tiles > 2 ? 256 : (t.tiles - 1) * 128 + (last + 31) / 32 * 32;
   return t;
 }
 inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
