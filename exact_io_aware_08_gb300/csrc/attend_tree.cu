@@ -17,17 +17,19 @@
 //   warp 0       copies K and V tiles by TMA into one ring, in the order in which they are used.
 //   warp 1       issues the products (the whole warp converged, one elected lane): S = Q K^T from shared
 //                memory, O += P V with P from tensor memory.
-//   warp 2       joins the hand-off of P once V is there, and cleans V's tile: rows behind the last key hold
-//                anything, and 0 * NaN is NaN.
+//   warp 2       joins the hand-off of P once V is there.
 //   warp 3       brings Q in, the next item's as soon as the last S of one is done.
 //   warps 4-11   softmax.  NT = 2: thread = row, a warpgroup a row tile.  NT = 1: two threads a row, 64 keys each,
-//                which exchange their maxima in tensor memory; they write O out, or states, a state's rows side by side.
+//                which exchange their maxima in tensor memory.  They write O out, or states, a state's rows side by
+//                side, and clean V's tile where some row does not see all of it: 0 * NaN is NaN.
 // Two S buffers are in flight: of the two row tiles (NT = 2, more than 128 rows), or of two key tiles in a
 // row (NT = 1).
 //
 // Where one row block holds all rows of a sequence and key head, each CTA gets an equal share of all key steps,
 // whatever the sequences' lengths, and what is cut is joined from states (Q4Share).  With more row blocks a
-// CTA takes one, all row blocks of a key head side by side so that its keys are read from memory once.
+// CTA takes whole ones, all row blocks of a key head side by side so that its keys are read from memory once, as
+// many rounds as all CTAs can; the key steps of the rest are shared out equally (4 x 512 tokens over 16384 keys, 256 row
+// blocks: 451 us in two rounds).
 //
 // Short calls are bound by latencies, of fetching instructions among them (a first pass over unrolled code that
 // streamed caches have driven out of L2 takes microseconds): the rarer paths are loops.
@@ -50,7 +52,8 @@ struct TreeCfg {
   // full[NST], empty[NST], q_full, q_empty, s_full[2], pv_done[2]; then the TMEM slot, abort flag, start[3], spoilt[4]
   static constexpr int NBAR = 2 * NST + 6;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;
+  static constexpr int OFF_TAIL = OFF_MISC + 48;              // kTreeMaxCtas + 1 running counts (rests)
+  static constexpr int SMEM_BYTES = OFF_TAIL + (NT == 2 ? (kTreeMaxCtas + 1) * 4 : 0) + 1024;
   static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t T_S = 0, T_O = 256, T_X = 384;    // T_X: exchanged maxima and sums (NT = 1)
@@ -77,7 +80,7 @@ struct TreeParams {
   int group, heads, per_kv, tokens;                           // tokens of a row tile
   int words, n_seqs, H, total, max_q, max_k;
   int shares, whole;                                          // equal shares of key steps (of whole row blocks or not)
-  int row_blocks, full_items, tail_splits, chunk, state_rows; // else: items from full_items on in tail_splits parts
+  int row_blocks, rounds, rest, state_rows;                   // else: rounds of whole row blocks, and the rest in shares
   float c2;
 };
 
@@ -89,17 +92,80 @@ struct TreeItem {
 
 __device__ __forceinline__ int tree_steps(const PagedSeq& s) { return s.nq ? max(1, (s.len + kPagedTile - 1) / kPagedTile) : 0; }
 
+// Row block ``index`` of those that are taken whole or rest: (sequence, key head) pairs, and within one the last rows,
+// which see the most, first.
+template <int NT>
+struct TreeBlock {
+  int b, head, rb;
+  __device__ __forceinline__ TreeBlock(const TreeParams& p, int index) {
+    rb = p.row_blocks - 1 - index % p.row_blocks;
+    const int w = index / p.row_blocks;
+    head = w % p.heads;
+    b = w / p.heads;
+  }
+  __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int token) {
+    return p.tree ? s.len : s.base() + min(token, s.nq - 1) + 1;
+  }
+  // Its keys (0: no rows).
+  __device__ __forceinline__ int keys(const TreeParams& p, const PagedSeq& s) const {
+    return rb * NT * p.tokens >= s.nq ? 0 : seen(p, s, (rb + 1) * NT * p.tokens - 1);
+  }
+};
+
+// By a whole warp: running counts of the rest's key steps, counts[0] = 0 to counts[p.rest].
+__device__ __forceinline__ void tree_rest(const TreeParams& p, int ctas, bool report, int* counts) {
+  const int lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int base = 0; base < p.rest; base += 32) {
+    int steps = 0;
+    if (base + lane < p.rest) {
+      const TreeBlock<2> x(p, p.rounds * ctas + base + lane);
+      const PagedSeq s = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, report, 503);
+      steps = (x.keys(p, s) + kPagedTile - 1) / kPagedTile;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, steps, o);
+      if (lane >= o) steps += y;
+    }
+    if (base + lane < p.rest) counts[base + lane + 1] = sum + steps;
+    sum += __shfl_sync(0xffffffffu, steps, 31);
+  }
+  if (lane == 0) counts[0] = 0;
+  __syncwarp();
+}
+
+// The rest's shares: CTA c's first unit of ``units``, and the CTA that has unit u (no share is empty: of few units
+// each of the first CTAs has one).
+__device__ __forceinline__ int rest_begin(int units, int c, int ctas) {
+  const int n = min(ctas, units);
+  return c >= n ? units : static_cast<int>(static_cast<long long>(units) * c / n);
+}
+__device__ __forceinline__ int rest_owner(int units, int u, int ctas) {
+  return static_cast<int>((static_cast<long long>(u + 1) * min(ctas, units) - 1) / units);
+}
+
 template <int NT>
 struct TreeWalk {
   const TreeParams& p;
+  const int* counts;                                          // (rests)
   int b, off, left;                                           // shares: sequence, unit in it, units left
-  bool once;
+  int round;                                                  // else: round; of the rest row block b, first unit off
   PagedSeq seq;
   int steps;
 
   // Tokens up to ``token`` of the sequence see keys below this.
-  __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int token) {
-    return p.tree ? s.len : s.base() + min(token, s.nq - 1) + 1;
+  __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int token) { return TreeBlock<NT>::seen(p, s, token); }
+
+  __device__ __forceinline__ void block(TreeItem& x, int index) const {
+    const TreeBlock<NT> y(p, index);
+    x.b = y.b;
+    x.head = y.head;
+    x.rb = y.rb;
+    x.seq = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, x.rb == 0 && x.head == 0 && threadIdx.x == 0, 500);
+    x.key0 = 0;
+    x.key_end = y.keys(p, x.seq);
+    x.slot = -1;
   }
 
   // The share: whose first unit is unit ``u`` of sequence ``at``.
@@ -118,26 +184,29 @@ struct TreeWalk {
   }
 
   __device__ __forceinline__ bool next(TreeItem& x) {
-    if (!p.shares) {
-      if (once) return false;
-      once = true;
-      int item = blockIdx.x, split = 0, parts = 1;
-      x.slot = -1;
-      if (item >= p.full_items) {
-        const int i = item - p.full_items;
-        item = p.full_items + i / p.tail_splits;
-        split = i % p.tail_splits;
-        parts = p.tail_splits;
-        x.slot = i;
+    if (NT == 2 && !p.shares) {
+      const int ctas = gridDim.x;
+      for (; round < p.rounds; ++round) {
+        block(x, pers_item(round, ctas));
+        if (x.key_end == 0) continue;
+        ++round;
+        return true;
       }
-      x.rb = p.row_blocks - 1 - item % p.row_blocks;
-      const int w = item / p.row_blocks;
-      x.head = w % p.heads;
-      x.b = w / p.heads;
-      x.seq = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, x.rb == 0 && x.head == 0 && threadIdx.x == 0, 500);
-      if (x.rb * NT * p.tokens >= x.seq.nq) return false;
-      x.key0 = split * p.chunk;
-      x.key_end = min(seen(p, x.seq, (x.rb + 1) * NT * p.tokens - 1), parts > 1 ? x.key0 + p.chunk : 1 << 30);
+      if (round == p.rounds) {                                // the share of the rest
+        ++round;
+        off = rest_begin(counts[p.rest], blockIdx.x, ctas);
+        left = rest_begin(counts[p.rest], blockIdx.x + 1, ctas) - off;
+        b = 0;
+      }
+      if (left <= 0) return false;
+      while (counts[b + 1] <= off) ++b;
+      block(x, p.rounds * ctas + b);
+      const int step0 = off - counts[b], all = counts[b + 1] - counts[b], n = min(left, all - step0);
+      x.key0 = step0 * kPagedTile;
+      x.key_end = min(x.key_end, x.key0 + n * kPagedTile);
+      x.slot = n == all ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
+      off += n;
+      left -= n;
       return true;
     }
     if (left <= 0) return false;
@@ -382,6 +451,41 @@ __device__ __forceinline__ void tree_spoil(const TreeParams& p, const TreeItem& 
   }
 }
 
+// By THREADS threads: of a tile of V rows from ``live`` on become 0, and of those from ``lo`` on what is no finite number.
+// Whether this thread found any.
+template <int D, int THREADS>
+__device__ __forceinline__ bool clean_values(uint8_t* tile, int thread, int lo, int live) {
+  constexpr int L = D / 8, RS = THREADS / L;                  // threads of a row, rows at a time (whole periods of the swizzle)
+  static_assert(RS % 8 == 0, "rows of a thread share their swizzle");
+  const int c = thread % L, r0 = thread / L;
+  uint8_t* mine = tile + (c >> 3) * 128 * 128 + sw128_offset(r0, (c & 7) * 8);
+  bool found = false;
+#pragma unroll 4
+  for (int r = r0; r < 128; r += RS, mine += RS * 128) {
+    uint4* at = reinterpret_cast<uint4*>(mine);
+    if (r >= live) {
+      *at = make_uint4(0u, 0u, 0u, 0u);
+    } else if (r >= lo) {
+      uint4 v = *at;
+      uint32_t* e = reinterpret_cast<uint32_t*>(&v);
+      // an exponent of all ones carries into the sign's place
+      uint32_t carry = 0;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) carry |= ((e[y] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
+      if (carry) {
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          if ((e[y] & 0x7f80u) == 0x7f80u) e[y] &= 0xffff0000u;
+          if ((e[y] & 0x7f800000u) == 0x7f800000u) e[y] &= 0xffffu;
+        }
+        *at = v;
+        found = true;
+      }
+    }
+  }
+  return found;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel(const __grid_constant__ TreeParams p) {
   using C = TreeCfg<D, NT>;
@@ -402,7 +506,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   volatile int* spoilt = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 20);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  TreeWalk<NT> walk{p, 0, 0, 0, false, {}, 0};
+  int* counts = reinterpret_cast<int*>(smem + C::OFF_TAIL);
+  TreeWalk<NT> walk{p, counts, 0, 0, 0, 0, {}, 0};
   uint32_t tbase = 0;
 
   if (warp == 0) {
@@ -436,6 +541,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
         start[2] = n;
       }
       walk.begin(b, u, n);
+    } else if (NT == 2) {
+      tree_rest(p, gridDim.x, blockIdx.x == 0, counts);
     }
     __syncwarp();
     named_bar_arrive(C::BAR_START, C::THREADS);               // the copies begin at once
@@ -587,58 +694,15 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
     } else if (warp == 2) {
       // -------------------------------------------------------------- joins P's hand-off once V is there
       bool ok = true;
-      int g = 0, c0 = 0, c1 = 0, hc = 0;
+      int g = 0, hc = 0;
       while (walk.next(x)) {
         const int n0 = tiles(0), n1 = NT == 2 ? tiles(1) : 0, n = max(n0, n1);
         if (n == 0) continue;
-        if (n0 > 0) ++c0;
-        if (n1 > 0) ++c1;
-        const int from = common();
         for (int j = 0; j < n; ++j) {
           const int at = at_v(g, j, n);
           if (ok) ok = mbar_wait_warp(&full[at % C::NST], (at / C::NST) & 1, abort_flag, 530);
           if (NT == 2 && ok && j + 1 < n)
             ok = mbar_wait_warp(&full[at_k(g, j + 1) % C::NST], (at_k(g, j + 1) / C::NST) & 1, abort_flag, 531);
-          const int k0 = x.key0 + j * C::BN;
-          if (ok && (k0 + C::BN > x.key_end || k0 + C::BN > from)) {
-            uint8_t* tile = sKV + (at % C::NST) * C::TILE;
-            const int live = min(C::BN, x.key_end - k0), lo = max(0, min(from - k0, live));
-            // lane: 16 bytes of every RS-th row, eight rows (one period of the swizzle) at a time
-            constexpr int L = D / 8, RS = 32 / L;
-            const int c = lane % L, r0 = lane / L;
-            bool found = false;
-#pragma unroll 1
-            for (int r8 = lo & ~7; r8 < C::BN; r8 += 8) {
-#pragma unroll
-              for (int u = 0; u < 8 / RS; ++u) {
-                const int row = r8 + r0 + u * RS;
-                uint4* at16 = reinterpret_cast<uint4*>(tile + r8 * 128 + (c >> 3) * C::CHUNK + sw128_offset(r0 + u * RS, (c & 7) * 8));
-                if (row >= live) {
-                  *at16 = make_uint4(0u, 0u, 0u, 0u);
-                } else if (row >= lo) {
-                  uint4 v = *at16;
-                  uint32_t* e = reinterpret_cast<uint32_t*>(&v);
-                  // an exponent of all ones carries into the sign's place
-                  uint32_t carry = 0;
-#pragma unroll
-                  for (int y = 0; y < 4; ++y) carry |= ((e[y] & 0x7fff7fffu) + 0x00800080u) & 0x80008000u;
-                  if (carry) {
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                      if ((e[y] & 0x7f80u) == 0x7f80u) e[y] &= 0xffff0000u;
-                      if ((e[y] & 0x7f800000u) == 0x7f800000u) e[y] &= 0xffffu;
-                    }
-                    *at16 = v;
-                    found = true;
-                  }
-                }
-              }
-            }
-            if (found && n0 > 0) spoilt[c0 & 1] = c0;
-            if (found && n1 > 0) spoilt[2 + (c1 & 1)] = c1;
-            __threadfence_block();
-            fence_proxy_async_smem();
-          }
 #pragma unroll
           for (int t = 0; t < NT; ++t)
             if (NT == 1 || j < (t ? n1 : n0)) {
@@ -685,10 +749,12 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
     const uint32_t t_o = t_lane + C::T_O + t * 128 + half * COLS;
     bool ok = true;
     int mine = 0, hc = 0;                                     // items that this row tile has keys in, key tiles so far
+    int g = 0, others = 0;                                    // ring tiles so far; items that the other row tile has keys in
     const float c2 = p.c2;
     const int row_token = row / p.group, row_head = row - row_token * p.group;
     while (walk.next(x)) {
-      const int n = tiles(t);
+      const int n = tiles(t), n_other = NT == 2 ? tiles(t ^ 1) : 0, n_all = max(n, n_other);
+      if (n_other > 0) ++others;
       const int token = (x.rb * NT + t) * p.tokens + row_token, head = x.head * p.group + row_head;
       const bool valid = row_token < p.tokens && token < x.seq.nq;
       const bool idle = !__any_sync(0xffffffffu, valid);
@@ -699,6 +765,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           asm volatile("prefetch.global.L1 [%0];" :: "l"(p.tree + static_cast<size_t>(x.seq.first + token) * p.words));
         bool far = false;
         // keys below it are all the warp's rows'
+        const int from = common();
         const int full_end = min(x.key_end, __reduce_min_sync(0xffffffffu, !valid ? 1 << 30 : p.tree ? x.seq.base() : x.seq.base() + token + 1));
         for (int j = 0; j < n; ++j, ++hc) {
           const int buf = NT == 2 ? t : hc & 1;
@@ -707,6 +774,18 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           tc_fence_after();
           const int k0 = x.key0 + j * C::BN;
           const bool plain = k0 + C::BN <= full_end;
+          // the first row tile that has the key tile cleans V, before its hand-off of P lets the product go
+          if (ok && k0 + C::BN > min(from, x.key_end) && (t == 0 || j >= n_other)) {
+            const int at = at_v(g, j, n_all);
+            ok = mbar_wait_warp(&full[at % C::NST], (at / C::NST) & 1, abort_flag, 543);
+            if (ok && clean_values<D, NT == 1 ? 256 : 128>(sKV + (at % C::NST) * C::TILE, NT == 1 ? threadIdx.x - 128 : row,
+                                                            max(0, from - k0), min(C::BN, x.key_end - k0))) {
+              spoilt[2 * t + (mine & 1)] = mine;
+              if (j < n_other) spoilt[2 * (t ^ 1) + (others & 1)] = others;
+              __threadfence_block();
+            }
+            fence_proxy_async_smem();
+          }
           if constexpr (NT == 2) {
             if (ok && !idle) {
               bool done = false;
@@ -796,6 +875,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
           tc_fence_after();
         }
       }
+      g += 2 * n_all;
       if (!ok || idle) continue;
       // the row's result, or its stretch's state
       const bool none = r.l == 0.f;
@@ -856,8 +936,9 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
 // Joins the states of row blocks that are cut.  A block takes RB rows of one row block: a lane has one row and eight
 // columns (a state's rows lie side by side), S warps share the states of those out, and where that leaves warps for
 // less than D columns, blockIdx.y tells which.  SHARES: row block of bound i + 1 between the CTAs' shares, if that is
-// the first within it, or, BY_PAIR, i-th row block of the call; else the i-th item that was split.  Little code: each part of it runs once, and is fetched
-// while nothing else happens (64 columns a lane, in straight lines: 7.6 us behind 1 x 8 tokens over 1000).
+// the first within it, or, by_pair, the i-th row block of all; else the i-th row block of the rest.  Little code:
+// each part of it runs once, and is fetched while nothing else happens (64 columns a lane, in straight lines: 7.6 us
+// behind 1 x 8 tokens over 1000).
 constexpr int kTreeJoinWarps = 16;
 
 template <int D, int RB, int S>
@@ -870,6 +951,7 @@ struct TreeJoinCfg {
 template <int D, int RB, int S, bool SHARES>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas, int chunks, int by_pair) {
   using J = TreeJoinCfg<D, RB, S>;
+  __shared__ int counts[SHARES ? 1 : kTreeMaxCtas + 1];
   __shared__ int found[6];                                    // first token, tokens, key head, token of row 0, states, first slot
   __shared__ float merge[S > 1 ? kTreeJoinWarps : 1][11][32]; // a lane's columns, reference, sum, rounded sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -895,12 +977,19 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(c
         }
       }
     } else {
-      const int item = p.full_items + i, w = item / p.row_blocks;
-      head = w % p.heads;
-      s = paged_seq(p.cu, p.seqlens, w / p.heads, p.total, p.max_q, p.max_k, false, 0);
-      token0 = (p.row_blocks - 1 - item % p.row_blocks) * 2 * p.tokens;
-      n = p.tail_splits;
-      slot = i * p.tail_splits;
+      tree_rest(p, ctas, false, counts);
+      const TreeBlock<2> x(p, p.rounds * ctas + i);
+      s = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, false, 0);
+      head = x.head;
+      token0 = x.rb * 2 * p.tokens;
+      const int units = counts[p.rest], u0 = counts[i], u1 = counts[i + 1] - 1;
+      if (u1 >= u0) {
+        const int c0 = rest_owner(units, u0, ctas), c1 = rest_owner(units, u1, ctas);
+        if (c0 != c1) {
+          n = c1 - c0 + 1;
+          slot = 2 * c0;
+        }
+      }
     }
     if (lane == 0) {
       found[0] = s.first; found[1] = s.nq; found[2] = head; found[3] = token0; found[4] = token0 < s.nq ? n : 0; found[5] = slot;
@@ -931,9 +1020,8 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(c
     float v[AT_ONCE][8], mk[AT_ONCE], lk[AT_ONCE], lhk[AT_ONCE];
 #pragma unroll
     for (int j = 0; j < AT_ONCE; ++j) {
-      // state k: SHARES: the first CTA's second place, the others' first one
-      const int k = k0 + j * S;
-      const int slot = SHARES ? found[5] + 2 * k + (k == 0 ? 1 : 0) : found[5] + k;
+      // state k: the first CTA's second place, the others' first one
+      const int k = k0 + j * S, slot = found[5] + 2 * k + (k == 0 ? 1 : 0);
       const float* st = p.part + (static_cast<size_t>(slot) * (p.state_rows / 32) + (r >> 5)) * (32 * (D + 3)) + (r & 31);
       mk[j] = -INFINITY;
       lk[j] = lhk[j] = 0.f;
@@ -982,7 +1070,7 @@ static cudaError_t launch_tree_join(const TreeParams& p, long long grid, long lo
   const int chunks = RB == 8 ? 1 : p.state_rows / RB;
   const dim3 blocks(static_cast<unsigned>(cut * chunks), D / TreeJoinCfg<D, RB, S>::COLS);
   log_launch("attend_tree_join_kernel<D, RB, S, SHARES>", static_cast<unsigned long long>(blocks.x) * blocks.y, 32 * kTreeJoinWarps, 0ull);
-  if constexpr (RB == 32 && S < 8)
+  if constexpr (RB == 32)
     if (!p.shares)
       return launch_join(attend_tree_join_kernel<D, RB, S, false>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks, 0);
   return launch_join(attend_tree_join_kernel<D, RB, S, true>, blocks, 32 * kTreeJoinWarps, stream, p, static_cast<int>(grid), chunks, by_pair);
@@ -1019,29 +1107,21 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   } else {
     p.row_blocks = (t.tiles + 1) / 2;
     const long long items = pairs * p.row_blocks;
-    const int tail = static_cast<int>(items % sms);
-    const int s = tail ? static_cast<int>(min(static_cast<long long>(sms / tail), steps / 4)) : 1;
-    p.full_items = static_cast<int>(items);
-    p.tail_splits = 1;
-    grid = items;
-    if (s >= 2) {
-      p.full_items = static_cast<int>(items - tail);
-      p.tail_splits = s;
-      p.chunk = static_cast<int>((steps + s - 1) / s) * kPagedTile;
-      grid = p.full_items + static_cast<long long>(tail) * s;
-    }
+    grid = min(static_cast<long long>(sms), items * steps);
+    p.rounds = static_cast<int>(items / grid);
+    p.rest = static_cast<int>(items - p.rounds * grid);
   }
   log_launch("attend_tree_kernel<D, NT>", static_cast<unsigned long long>(grid), C::THREADS, static_cast<unsigned long long>(C::SMEM_BYTES));
   attend_tree_kernel<D, NT><<<static_cast<unsigned>(grid), C::THREADS, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // the row blocks that a bound cuts (of all of them, or of all bounds), or that were split
+  // the row blocks that a bound may cut: all, or one for each bound, or the rest
   const int by_pair = p.shares && pairs < grid;
-  const long long cut = p.shares ? (p.whole ? 0 : by_pair ? pairs : grid - 1) : p.tail_splits == 1 ? 0 : (grid - p.full_items) / p.tail_splits;
+  const long long cut = p.shares ? (p.whole ? 0 : by_pair ? pairs : grid - 1) : p.rest;
   if (cut == 0) return cudaSuccess;
-  // A row block has some grid / pairs states where the sequences are alike: with few of them a block has all columns,
+  // A row block has some grid / pairs (or rest) states where the sequences are alike: with few of them a block has all columns,
   // with many each warp of eight has an eighth of them.
-  const bool many = p.shares && grid > 8 * pairs;
+  const bool many = grid > 8 * (p.shares ? pairs : p.rest);
   if (t.rows <= 8)
     return many && D == 128 ? launch_tree_join<D, 8, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 8, 512 / D>(p, grid, cut, by_pair, stream);
   return many ? launch_tree_join<D, 32, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 32, 128 / D>(p, grid, cut, by_pair, stream);

@@ -210,6 +210,12 @@ def test_long_caches_and_many_shares():
     s.check(*s.attend())
     s = Step([90], [30000], 4, 1, 64, 256, "tree")
     s.check(*s.attend(), most=6)
+    s = Step([100, 7, 300], [30000, 9, 2300], 8, 2, 128, 64, None)          # whole row blocks and a rest
+    s.check(*s.attend(), most=6)
+    s = Step([700, 1, 50, 650], [700, 5, 3000, 9000], 16, 4, 64, 64, None)
+    s.check(*s.attend(), most=6)
+    s = Step([600] * 10, [600 + 10 * i for i in range(10)], 8, 8, 128, 64, "tree")
+    s.check(*s.attend(), most=6)
 
 
 def test_pages_past_32_bits():
