@@ -80,6 +80,7 @@ struct TreeParams {
   int group, heads, per_kv, tokens;                           // tokens of a row tile
   int words, n_seqs, H, total, max_q, max_k;
   int shares, whole;                                          // equal shares of key steps (of whole row blocks or not)
+  int leave;                                                  // what a row block costs beside its steps
   int row_blocks, rounds, rest, state_rows;                   // else: rounds of whole row blocks, and the rest in shares
   float c2;
 };
@@ -90,7 +91,10 @@ struct TreeItem {
   PagedSeq seq;
 };
 
-__device__ __forceinline__ int tree_steps(const PagedSeq& s) { return s.nq ? max(1, (s.len + kPagedTile - 1) / kPagedTile) : 0; }
+// Units of a (sequence, key head) in equal shares: its key steps, and in front of them what leaving one row block for
+// the next costs, in steps.
+__device__ __forceinline__ int tree_steps(const PagedSeq& s) { return (s.len + kPagedTile - 1) / kPagedTile; }
+__device__ __forceinline__ int tree_units(const TreeParams& p, const PagedSeq& s) { return s.nq ? p.leave + tree_steps(s) : 0; }
 
 // Row block ``index`` of those that are taken whole or rest: (sequence, key head) pairs, and within one the last rows,
 // which see the most, first.
@@ -135,6 +139,9 @@ __device__ __forceinline__ void tree_rest(const TreeParams& p, int ctas, bool re
   __syncwarp();
 }
 
+// Their place in the workspace, for the join: in front of the states.
+__device__ __forceinline__ int* tree_counts(const TreeParams& p) { return reinterpret_cast<int*>(p.part) - (kTreeMaxCtas + 8); }
+
 // The rest's shares: CTA c's first unit of ``units``, and the CTA that has unit u (no share is empty: of few units
 // each of the first CTAs has one).
 __device__ __forceinline__ int rest_begin(int units, int c, int ctas) {
@@ -152,7 +159,7 @@ struct TreeWalk {
   int b, off, left;                                           // shares: sequence, unit in it, units left
   int round;                                                  // else: round; of the rest row block b, first unit off
   PagedSeq seq;
-  int steps;
+  int units;                                                  // of a key head of it
 
   // Tokens up to ``token`` of the sequence see keys below this.
   __device__ __forceinline__ static int seen(const TreeParams& p, const PagedSeq& s, int token) { return TreeBlock<NT>::seen(p, s, token); }
@@ -175,9 +182,9 @@ struct TreeWalk {
     left = n;
     if (left <= 0) return;
     seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-    steps = tree_steps(seq);
+    units = tree_units(p, seq);
     if (p.whole) {                                            // the row blocks that begin in it
-      const int behind = off % steps, skip = behind ? steps - behind : 0;
+      const int behind = off % units, skip = behind ? units - behind : 0;
       off += skip;
       left -= skip;
     }
@@ -209,25 +216,28 @@ struct TreeWalk {
       left -= n;
       return true;
     }
-    if (left <= 0) return false;
-    while (off >= steps * p.heads) {                          // (a sequence with work follows: left > 0)
-      if (++b >= p.n_seqs) return false;
-      off = 0;
-      seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-      steps = tree_steps(seq);
+    while (left > 0) {
+      while (off >= units * p.heads) {                        // (a sequence with work follows: left > 0)
+        if (++b >= p.n_seqs) return false;
+        off = 0;
+        seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
+        units = tree_units(p, seq);
+      }
+      x.head = off / units;
+      const int u0 = off - x.head * units, n = p.whole ? units : min(left, units - u0);
+      off += n;
+      left -= n;
+      const int step0 = max(0, u0 - p.leave), step1 = u0 + n - p.leave;
+      if (step1 <= step0) continue;
+      x.b = b;
+      x.seq = seq;
+      x.rb = 0;
+      x.key0 = step0 * kPagedTile;
+      x.key_end = min(step1 * kPagedTile, seq.len);
+      x.slot = step1 - step0 == units - p.leave ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
+      return true;
     }
-    x.b = b;
-    x.seq = seq;
-    x.rb = 0;
-    x.head = off / steps;
-    const int step0 = off - x.head * steps;
-    const int n = p.whole ? steps : min(left, steps - step0);
-    x.key0 = step0 * kPagedTile;
-    x.key_end = min(x.key0 + n * kPagedTile, seq.len);
-    x.slot = n == steps ? -1 : 2 * static_cast<int>(blockIdx.x) + (step0 == 0 ? 1 : 0);
-    off += n;
-    left -= n;
-    return true;
+    return false;
   }
 };
 
@@ -237,7 +247,7 @@ template <typename F>
 __device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, bool report, F u_of, int at, int* b, long long* before) {
   const int lane = threadIdx.x & 31;
   auto units = [&](int i, bool rep) {
-    return static_cast<long long>(tree_steps(paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501))) * p.heads;
+    return static_cast<long long>(tree_units(p, paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501))) * p.heads;
   };
   Q4Share sh;
   long long mine = 0, own = 0;
@@ -356,21 +366,27 @@ __device__ __forceinline__ void tree_weights(const float* s, float ref, float c2
 }
 
 // One key tile of a row, thread = row, where some keys are not seen or the reference is large: S in tensor memory
-// (columns t_s) becomes P over its first half, O (t_o) is rescaled where the row's reference moves.
+// (columns t_s) becomes P over its first half, O (t_o) is rescaled where the row's reference moves.  All rows of the
+// warp see columns below ``all``, and none those from ``end`` on.
 template <int D>
-__device__ __forceinline__ void tree_softmax_masked(uint32_t t_s, uint32_t t_o, const uint32_t (&w)[4], bool first, bool valid, float c2, TreeRow& r) {
+__device__ __forceinline__ void tree_softmax_masked(uint32_t t_s, uint32_t t_o, const uint32_t (&w)[4], int all, int end, bool first, bool valid,
+                                                    float c2, TreeRow& r) {
   float s[32];
   auto load = [&](int k) {
     uint32_t rr[32];
     tmem_ld32(t_s + k * 32, rr);
     tmem_wait_ld();
-    const uint32_t bits = k < 2 ? (k == 0 ? w[0] : w[1]) : (k == 2 ? w[2] : w[3]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? __uint_as_float(rr[i]) : -INFINITY;
+    for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(rr[i]);
+    if (k * 32 + 32 > all) {
+      const uint32_t bits = k < 2 ? (k == 0 ? w[0] : w[1]) : (k == 2 ? w[2] : w[3]);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = bits >> i & 1u ? s[i] : -INFINITY;
+    }
   };
   float cand = r.m;
 #pragma unroll 1
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 4 && k * 32 < end; ++k) {
     load(k);
     cand = fmaxf(cand, max32(s));
   }
@@ -380,9 +396,14 @@ __device__ __forceinline__ void tree_softmax_masked(uint32_t t_s, uint32_t t_o, 
   const float ref = r.m == -INFINITY ? 0.f : r.m;
 #pragma unroll 1
   for (int k = 0; k < 4; ++k) {                               // (P of a quarter lies over S of quarters that were read)
-    load(k);
     uint32_t pk[16];
-    tree_weights(s, ref, c2, r, pk);
+    if (k * 32 < end) {
+      load(k);
+      tree_weights(s, ref, c2, r, pk);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) pk[i] = 0u;
+    }
     tmem_st16(t_s + k * 16, pk);
   }
 }
@@ -458,10 +479,11 @@ __device__ __forceinline__ bool clean_values(uint8_t* tile, int thread, int lo, 
   constexpr int L = D / 8, RS = THREADS / L;                  // threads of a row, rows at a time (whole periods of the swizzle)
   static_assert(RS % 8 == 0, "rows of a thread share their swizzle");
   const int c = thread % L, r0 = thread / L;
-  uint8_t* mine = tile + (c >> 3) * 128 * 128 + sw128_offset(r0, (c & 7) * 8);
+  const int skip = min(lo, live) / RS * RS;
+  uint8_t* mine = tile + (c >> 3) * 128 * 128 + sw128_offset(r0, (c & 7) * 8) + skip * 128;
   bool found = false;
 #pragma unroll 4
-  for (int r = r0; r < 128; r += RS, mine += RS * 128) {
+  for (int r = r0 + skip; r < 128; r += RS, mine += RS * 128) {
     uint4* at = reinterpret_cast<uint4*>(mine);
     if (r >= live) {
       *at = make_uint4(0u, 0u, 0u, 0u);
@@ -543,6 +565,8 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       walk.begin(b, u, n);
     } else if (NT == 2) {
       tree_rest(p, gridDim.x, blockIdx.x == 0, counts);
+      if (blockIdx.x == 0)
+        for (int i = lane; i <= p.rest; i += 32) tree_counts(p)[i] = counts[i];
     }
     __syncwarp();
     named_bar_arrive(C::BAR_START, C::THREADS);               // the copies begin at once
@@ -796,7 +820,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
               if (!done) {
                 uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 if (!plain && valid) tree_mask<4>(p, x.seq, token, k0, w);
-                tree_softmax_masked<D>(t_s, t_o, w, j == 0, valid, c2, r);
+                tree_softmax_masked<D>(t_s, t_o, w, full_end - k0, x.key_end - k0, j == 0, valid, c2, r);
               }
             }
           } else if (!idle) {
@@ -951,7 +975,6 @@ struct TreeJoinCfg {
 template <int D, int RB, int S, bool SHARES>
 __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(const __grid_constant__ TreeParams p, int ctas, int chunks, int by_pair) {
   using J = TreeJoinCfg<D, RB, S>;
-  __shared__ int counts[SHARES ? 1 : kTreeMaxCtas + 1];
   __shared__ int found[6];                                    // first token, tokens, key head, token of row 0, states, first slot
   __shared__ float merge[S > 1 ? kTreeJoinWarps : 1][11][32]; // a lane's columns, reference, sum, rounded sum
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -967,17 +990,18 @@ __global__ void __launch_bounds__(32 * kTreeJoinWarps) attend_tree_join_kernel(c
       const Q4Share sh = tree_share(p, ctas, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, at, &b, &before);
       if (b >= 0) {
         s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-        const int steps = max(1, tree_steps(s));
-        head = by_pair ? i - b * p.heads : static_cast<int>(sh.begin(i + 1) - before) / steps;
-        const long long u0 = before + static_cast<long long>(head) * steps;
-        const int c0 = sh.owner(u0), c1 = sh.owner(u0 + steps - 1);
+        const int units = max(1, tree_units(p, s));
+        head = by_pair ? i - b * p.heads : static_cast<int>(sh.begin(i + 1) - before) / units;
+        const long long u0 = before + static_cast<long long>(head) * units;
+        const int c0 = sh.owner(u0 + p.leave), c1 = sh.owner(u0 + units - 1);
         if (s.nq && c0 != c1 && (by_pair || c0 == i)) {       // (c0 == i: bound i + 1 is its first)
           n = c1 - c0 + 1;
           slot = 2 * c0;
         }
       }
     } else {
-      tree_rest(p, ctas, false, counts);
+      pdl_wait();
+      const int* counts = tree_counts(p);                     // (written by the first CTA)
       const TreeBlock<2> x(p, p.rounds * ctas + i);
       s = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, false, 0);
       head = x.head;
@@ -1087,7 +1111,7 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
     return cudaErrorInvalidValue;
   p.cache = {a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks, piece};
   p.v = static_cast<const uint16_t*>(a.v_cache);
-  p.o = static_cast<uint16_t*>(a.o); p.lse = a.lse; p.part = a.part;
+  p.o = static_cast<uint16_t*>(a.o); p.lse = a.lse; p.part = a.part + kTreeMaxCtas + 8;
   p.tree = a.tree; p.words = a.words; p.cu = a.cu; p.seqlens = a.seqlens;
   p.group = t.group; p.heads = a.H / t.group; p.per_kv = p.heads / a.H_kv; p.tokens = t.tokens;
   p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
@@ -1103,6 +1127,9 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   p.state_rows = t.state_rows;
   if (p.shares) {
     p.whole = steps <= 1;
+    // 16 mixed sequences of up to 60 tokens, four query heads: 120 us without, 95 with 4, 98 with 6 (their slowest CTA had
+    // five short row blocks); 64 sequences of one token, up to 8192 keys, 233 us without, 227 with 1, 228 with 2
+    p.leave = pairs * steps <= sms ? 0 : NT == 2 ? 4 : 1;
     grid = min(static_cast<long long>(sms), pairs * steps);
   } else {
     p.row_blocks = (t.tiles + 1) / 2;
@@ -1121,7 +1148,7 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   if (cut == 0) return cudaSuccess;
   // A row block has some grid / pairs (or rest) states where the sequences are alike: with few of them a block has all columns,
   // with many each warp of eight has an eighth of them.
-  const bool many = grid > 8 * (p.shares ? pairs : p.rest);
+  const bool many = grid >= 4 * (p.shares ? pairs : p.rest);
   if (t.rows <= 8)
     return many && D == 128 ? launch_tree_join<D, 8, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 8, 512 / D>(p, grid, cut, by_pair, stream);
   return many ? launch_tree_join<D, 32, 8>(p, grid, cut, by_pair, stream) : launch_tree_join<D, 32, 128 / D>(p, grid, cut, by_pair, stream);

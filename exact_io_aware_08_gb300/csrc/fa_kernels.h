@@ -232,7 +232,7 @@ cudaError_t status_fetch_evict(cudaStream_t, unsigned int*, int*);
 // Attention over the bf16 paged cache: rows of a key head are its query heads times a sequence's query tokens, in
 // tiles of whole tokens, up to 128 rows each.  (Of more than 128 query heads a key head, some at a time: the largest
 // divisor that fits.)  A row block is one tile or two.  Of the key steps that are shared out (all of them where a row
-// block holds all rows) each of at most kTreeMaxCtas CTAs keeps at most two states.
+// block holds all rows) each of at most kTreeMaxCtas CTAs keeps at most two states, behind kTreeMaxCtas + 8 counts.
 constexpr int kTreeMaxCtas = 152;
 struct TreeRows {
   int group, tokens, tiles, rows, state_rows;                 // heads taken at a time, tokens of a tile, rows of a tile
@@ -251,7 +251,7 @@ inline TreeRows tree_rows(int H, int H_kv, int max_q) {
 }
 inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
   const TreeRows t = tree_rows(H, H_kv, max_q);
-  return 2 * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) * sizeof(float);
+  return (2 * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) + kTreeMaxCtas + 8) * sizeof(float);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);

@@ -68,8 +68,8 @@ def test_weigh_refuses_more(lib, kw, code):
 
 def test_tree_workspace_size(lib):
     size = lib.fa_fwd_paged_tree_workspace_size
-    assert size(8, 2, 1, 128) == size(8, 2, 8, 128) == 2 * 152 * 32 * 131 * 4
-    assert size(8, 2, 100, 64) == size(8, 2, 100000, 64) == 2 * 152 * 256 * 67 * 4
+    assert size(8, 2, 1, 128) == size(8, 2, 8, 128) == 2 * 152 * 32 * 131 * 4 + 640
+    assert size(8, 2, 100, 64) == size(8, 2, 100000, 64) == 2 * 152 * 256 * 67 * 4 + 640
     assert size(8, 3, 1, 128) == size(8, 2, -1, 128) == size(8, 2, 1, 96) == size(0, 1, 1, 64) == 0
 
 
