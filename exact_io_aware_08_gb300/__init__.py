@@ -34,7 +34,7 @@ __all__ = [
     "fa_decode_paged_q4_workspace_size", "fa_fwd_paged_q4_workspace_size",
     "append_paged", "append_paged_q4", "gather_paged_q4", "decode_paged_q4", "forward_paged_q4", "rotary_tables",
     "fa_append_paged_at", "fa_append_paged_q4_at", "fa_fwd_paged_tree", "fa_fwd_paged_tree_workspace_size",
-    "fa_accept_paged", "fa_weigh_paged", "fa_evict_paged",
+    "fa_accept_paged", "fa_weigh_paged", "fa_weigh_paged_workspace_size", "fa_evict_paged",
     "forward_paged_tree", "accept_paged", "weigh_paged", "evict_paged", "tree_bits",
 ]
 
@@ -99,7 +99,8 @@ _SIGNATURES = {
     "fa_fwd_paged_tree_workspace_size": (_S, [_I] * 4),
     "fa_fwd_paged_tree": (_I, [_P] * 6 + [_I] + [_P] * 3 + [_I] * 10 + [_F, _P, _S, _P]),
     "fa_accept_paged": (_I, [_P] * 8 + [_I] * 7 + [_P]),
-    "fa_weigh_paged": (_I, [_P] * 8 + [_I] * 10 + [_F] * 2 + [_P]),
+    "fa_weigh_paged_workspace_size": (_S, [_I] * 5),
+    "fa_weigh_paged": (_I, [_P] * 8 + [_I] * 10 + [_F] * 2 + [_P, _S, _P]),
     "fa_evict_paged": (_I, [_P] * 9 + [_I] * 11 + [_P]),
     "fa_sync_status": (_I, [_P]),
     "fa_selftest_wait_timeout": (_I, [ctypes.c_uint, _P]),
@@ -468,11 +469,15 @@ def fa_accept_paged(k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seql
 
 
 def fa_weigh_paged(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q: int,
-                   max_seqlen_k: int, scale: float, decay: float, stream=None):
+                   max_seqlen_k: int, scale: float, decay: float, ws=None, stream=None):
     """q [total, H, d]; lse [H, total]; weights fp32 [num_blocks, H_kv, block_size] are brought up to the step;
     weighed int32 [n_seqs] or None."""
     (_native or _binding()).weigh(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q,
-                                  max_seqlen_k, scale, decay, stream)
+                                  max_seqlen_k, scale, decay, ws, stream, False)
+
+
+def fa_weigh_paged_workspace_size(n_seqs: int, H: int, H_kv: int, max_seqlen_q: int, max_seqlen_k: int) -> int:
+    return load_library().fa_weigh_paged_workspace_size(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k)
 
 
 def fa_evict_paged(k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table,
@@ -726,11 +731,11 @@ def accept_paged(k_cache, v_cache, block_table, cu_seqlens, seqlens_k, accepted,
 
 
 def weigh_paged(q, lse, k_cache, weights, block_table, cu_seqlens, seqlens_k, max_seqlen_q: int, max_seqlen_k: int,
-                weighed=None, decay: float = 1.0, scale: float | None = None, stream=None):
+                weighed=None, decay: float = 1.0, scale: float | None = None, stream=None, workspace=None):
     """Adds to ``weights`` [num_blocks, H_kv, block_size] the attention that each cached token draws from a step's
     queries (see fa_weigh_paged)."""
     (_native or _binding()).weigh(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q,
-                                  max_seqlen_k, scale, decay, stream)
+                                  max_seqlen_k, scale, decay, workspace, stream, True)
 
 
 def evict_paged(k_cache, v_cache, weights, block_table, new_table, seqlens_k, budgets, max_seqlen_k: int, max_kept: int,

@@ -40,6 +40,7 @@ struct Library {
   decltype(&fa_fwd_paged_tree_workspace_size) tree_ws = nullptr;
   decltype(&fa_accept_paged) accept = nullptr;
   decltype(&fa_weigh_paged) weigh = nullptr;
+  decltype(&fa_weigh_paged_workspace_size) weigh_ws = nullptr;
   decltype(&fa_evict_paged) evict = nullptr;
   decltype(&fa_last_error_message) message = nullptr;
 };
@@ -522,10 +523,12 @@ PyObject* accept(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_END
 }
 
-// (q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q, max_seqlen_k, scale, decay, stream)
+// (q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, block_table, max_seqlen_q, max_seqlen_k, scale, decay, ws,
+//  stream, own): as decode().
 PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
   FA_BEGIN
-  count(n, 13);
+  count(n, 15);
+  const bool own = truth(a[14], "own");
   Cache16 c(a[2], nullptr);
   const at::Tensor& q = ranked(a[0], "q", 3, "[total, H, d]");
   const at::Tensor& table = ranked(a[7], "block_table", 2, "[n_seqs, max_blocks]");
@@ -537,11 +540,13 @@ PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int* cu = dense<int>(tensor(a[5], "cu_seqlens"), "cu_seqlens", at::kInt, {seqs + 1}, c.device);
   const int* lens = dense<int>(tensor(a[6], "seqlens_k"), "seqlens_k", at::kInt, {seqs}, c.device);
   const int* tab = dense<int>(table, "block_table", at::kInt, {seqs, table.size(1)}, c.device);
-  const Where on(a[12], c.device);
-  done(lib.weigh(pq, pl, c.k, pw, had, cu, lens, tab, narrow(seqs, "n_seqs"), narrow(H, "H"), narrow(c.heads, "H_kv"), narrow(total, "total"),
-                 narrow(integer(a[8], "max_seqlen_q"), "max_seqlen_q"), narrow(table.size(1), "max_blocks"), narrow(c.block_size, "block_size"),
-                 narrow(c.blocks, "num_blocks"), narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k"), narrow(c.d, "d"), scale_of(a[10], c.d),
-                 number(a[11], "decay"), on.stream));
+  const int max_q = narrow(integer(a[8], "max_seqlen_q"), "max_seqlen_q"), max_k = narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k");
+  const int s = narrow(seqs, "n_seqs"), h = narrow(H, "H"), hkv = narrow(c.heads, "H_kv");
+  const Where on(a[13], c.device);
+  const Workspace ws(a[12], own ? lib.weigh_ws(s, h, hkv, max_q, max_k) : 0, c.device, own);
+  done(lib.weigh(pq, pl, c.k, pw, had, cu, lens, tab, s, h, hkv, narrow(total, "total"), max_q, narrow(table.size(1), "max_blocks"),
+                 narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, narrow(c.d, "d"), scale_of(a[10], c.d),
+                 number(a[11], "decay"), ws.ptr, ws.bytes, on.stream));
   Py_RETURN_NONE;
   FA_END
 }
@@ -596,6 +601,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   find(lib.tree_ws, "fa_fwd_paged_tree_workspace_size");
   find(lib.accept, "fa_accept_paged");
   find(lib.weigh, "fa_weigh_paged");
+  find(lib.weigh_ws, "fa_weigh_paged_workspace_size");
   find(lib.evict, "fa_evict_paged");
   find(lib.message, "fa_last_error_message");
   if (!ok) return PyErr_Format(PyExc_RuntimeError, "libfa.so lacks a paged-cache function");

@@ -504,13 +504,16 @@ fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens
  * head.  q [total, H, d], lse [H, total] as fa_fwd_paged_tree takes and gives them without a tree; rows with an lse of
  * -inf weigh nothing.  weighed [n_seqs]: the tokens that have a weight (what others held is not read); null: those in
  * front of the step's.  After a whole prompt, or with its last tokens as queries and weighed of 0, all weights are set.
- * Sums are fp32, in a fixed order.  H / H_kv <= 128; decay in [0, 1]; the rest and the device-side checks as for
+ * Sums are fp32, in a fixed order.  H / H_kv <= 128; decay in [0, 1].  The workspace may be null where its size by the
+ * query (whose arguments are the call's) is 16 bytes or less.  The rest and the device-side checks as for
  * fa_fwd_paged_tree.  Two sequences that share a page race.
  */
+size_t fa_weigh_paged_workspace_size(int n_seqs, int H, int H_kv, int max_seqlen_q, int max_seqlen_k);
 fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t* k_cache, float* weights,
                            const int* weighed, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
                            int n_seqs, int H, int H_kv, int total, int max_seqlen_q, int max_blocks_per_seq,
-                           int block_size, int num_blocks, int max_seqlen_k, int d, float scale, float decay, void* stream);
+                           int block_size, int num_blocks, int max_seqlen_k, int d, float scale, float decay, void* ws,
+                           size_t ws_bytes, void* stream);
 
 /*
  * fa_evict_paged -- cut sequences of the bf16 cache down to budgets[b] tokens, by weight.  Of a sequence with more, each

@@ -319,6 +319,9 @@ WEIGHS = [
     ([700], [700], 5, 1, 128, 16, None, 1.0),
     ([1] * 70, list(range(1, 1401, 20)), 8, 8, 64, 32, None, 0.7),
     ([520, 2, 511], [1040, 5, 511], 3, 3, 128, 32, None, 0.25),
+    ([1000, 3, 0, 600], [1000, 9, 50, 4000], 8, 2, 128, 64, [0, 9, 5, 100], 0.5),      # ranges of rows
+    ([1100], [1300], 2, 2, 64, 64, None, 1.0),
+    ([700, 650], [1400, 650], 100, 1, 64, 16, None, 1.0),                             # a token a tile
 ]
 
 

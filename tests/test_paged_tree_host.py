@@ -28,7 +28,7 @@ STEP = dict(q=FAKE, kc=FAKE, vc=FAKE, o=FAKE, lse=FAKE, tree=FAKE, words=1, cu=F
             total=6, max_q=4, max_blocks=8, block=64, num_blocks=16, max_k=500, d=128, scale=0.1, ws=FAKE, ws_bytes=1 << 40,
             weights=FAKE, weighed=None, decay=1.0)
 TREE = ("q kc vc o lse tree words cu lens table n_seqs H H_kv total max_q max_blocks block num_blocks max_k d scale ws ws_bytes")
-WEIGH = "q lse kc weights weighed cu lens table n_seqs H H_kv total max_q max_blocks block num_blocks max_k d scale decay"
+WEIGH = "q lse kc weights weighed cu lens table n_seqs H H_kv total max_q max_blocks block num_blocks max_k d scale decay ws ws_bytes"
 
 
 @pytest.mark.parametrize("what", ["tree", "weigh"])
@@ -60,7 +60,8 @@ def test_tree_refuses_more(lib, kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(weights=None), INVALID), (dict(weights=FAKE + 4), INVALID), (dict(weighed=FAKE + 1), INVALID), (dict(decay=-0.1), INVALID),
-    (dict(decay=1.5), INVALID), (dict(decay=NAN), INVALID), (dict(H=258), UNSUPPORTED), (dict(total=0, max_q=0, weights=None), OK),
+    (dict(total=4000, max_q=2000, ws=None), WORKSPACE), (dict(total=4000, max_q=2000, ws_bytes=1000), WORKSPACE),
+    (dict(total=4000, max_q=2000, ws=FAKE + 4), WORKSPACE), (dict(decay=1.5), INVALID), (dict(decay=NAN), INVALID), (dict(H=258), UNSUPPORTED), (dict(total=0, max_q=0, weights=None), OK),
 ])
 def test_weigh_refuses_more(lib, kw, code):
     assert call(lib.fa_weigh_paged, WEIGH, STEP, kw) == code
@@ -71,6 +72,13 @@ def test_tree_workspace_size(lib):
     assert size(8, 2, 1, 128) == size(8, 2, 8, 128) == 2 * 152 * 32 * 131 * 4 + 640
     assert size(8, 2, 100, 64) == size(8, 2, 100000, 64) == 2 * 152 * 256 * 67 * 4 + 640
     assert size(8, 3, 1, 128) == size(8, 2, -1, 128) == size(8, 2, 1, 96) == size(0, 1, 1, 64) == 0
+
+
+def test_weigh_workspace_size(lib):
+    size = lib.fa_weigh_paged_workspace_size
+    assert size(4, 8, 2, 1, 1000) == size(64, 32, 8, 300, 30000) == 16          # one tile of rows; enough pieces without ranges
+    assert size(1, 32, 8, 4096, 4096) == 10 * 8 * 16 * 256 * 4
+    assert size(0, 8, 2, 1, 1) == size(1, 8, 3, 1, 1) == size(1, 130, 1, 1, 1) == size(1, 8, 2, -1, 1) == 0
 
 
 ACCEPT = dict(kc=FAKE, vc=FAKE, out=FAKE, path=FAKE, n=FAKE, cu=FAKE, lens=FAKE + 64, table=FAKE, n_seqs=2, H_kv=2, deep=4, max_blocks=8,
