@@ -254,10 +254,10 @@ inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
   return (2 * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) + kTreeMaxCtas + 8) * sizeof(float);
 }
 
-// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each, against 256 keys at a time.  Several
-// tiles are divided into ranges of at least four where the (sequence, key head, 256 keys) pieces alone would leave a CTA
-// fewer than eight to take (two prompts of 4096 tokens with 8 key heads: 512 pieces, of which the first sees 16 times as
-// many rows as the last).
+// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each.  Several tiles go against 512 keys at a
+// time, and are divided into ranges of at least four where the (sequence, key head, 512 keys) pieces alone would leave a
+// CTA fewer than six to take (two prompts of 4096 tokens with 8 key heads: 128 pieces, of which the first sees eight times
+// as many rows as the last).
 struct WeighSplit {
   int tokens, ranges, range;                                  // of a tile; ranges of ``range`` tiles
 };
@@ -266,8 +266,8 @@ inline WeighSplit weigh_split(int n_seqs, int H, int H_kv, int max_q, int max_k)
   const int G = H / H_kv;
   t.tokens = 128 / G < max_q ? 128 / G : max_q < 1 ? 1 : max_q;
   const long long tiles = (max_q + t.tokens - 1) / t.tokens;
-  const long long pieces = static_cast<long long>(n_seqs) * H_kv * ((max_k + 255) / 256);
-  long long r = pieces > 0 ? (8 * 152 + pieces - 1) / pieces : 1;
+  const long long pieces = static_cast<long long>(n_seqs) * H_kv * ((max_k + 511) / 512);
+  long long r = pieces > 0 ? (6 * 152 + pieces - 1) / pieces : 1;
   if (r > tiles / 4) r = tiles / 4;
   if (r < 1) r = 1;
   t.range = static_cast<int>((tiles + r - 1) / r);
@@ -276,7 +276,7 @@ inline WeighSplit weigh_split(int n_seqs, int H, int H_kv, int max_q, int max_k)
 }
 inline size_t weigh_part_bytes(int n_seqs, int H, int H_kv, int max_q, int max_k) {
   const WeighSplit t = weigh_split(n_seqs, H, H_kv, max_q, max_k);
-  return t.ranges <= 1 ? 16 : static_cast<size_t>(t.ranges) * n_seqs * H_kv * ((max_k + 255) / 256) * 256 * sizeof(float);
+  return t.ranges <= 1 ? 16 : static_cast<size_t>(t.ranges) * n_seqs * H_kv * ((max_k + 511) / 512) * 512 * sizeof(float);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
