@@ -99,7 +99,7 @@ _SIGNATURES = {
     "fa_fwd_paged_tree_workspace_size": (_S, [_I] * 4),
     "fa_fwd_paged_tree": (_I, [_P] * 6 + [_I] + [_P] * 3 + [_I] * 10 + [_F, _P, _S, _P]),
     "fa_accept_paged": (_I, [_P] * 8 + [_I] * 7 + [_P]),
-    "fa_weigh_paged_workspace_size": (_S, [_I] * 5),
+    "fa_weigh_paged_workspace_size": (_S, [_I] * 3),
     "fa_weigh_paged": (_I, [_P] * 8 + [_I] * 10 + [_F] * 2 + [_P, _S, _P]),
     "fa_evict_paged": (_I, [_P] * 9 + [_I] * 11 + [_P]),
     "fa_sync_status": (_I, [_P]),
@@ -476,8 +476,8 @@ def fa_weigh_paged(q, lse, k_cache, weights, weighed, cu_seqlens, seqlens_k, blo
                                   max_seqlen_k, scale, decay, ws, stream, False)
 
 
-def fa_weigh_paged_workspace_size(n_seqs: int, H: int, H_kv: int, max_seqlen_q: int, max_seqlen_k: int) -> int:
-    return load_library().fa_weigh_paged_workspace_size(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k)
+def fa_weigh_paged_workspace_size(H: int, H_kv: int, max_seqlen_q: int) -> int:
+    return load_library().fa_weigh_paged_workspace_size(H, H_kv, max_seqlen_q)
 
 
 def fa_evict_paged(k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table,

@@ -881,11 +881,9 @@ fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens
   return e == cudaSuccess ? FA_OK : cuda_fail(e, "fa_accept_paged launch");
 }
 
-size_t fa_weigh_paged_workspace_size(int n_seqs, int H, int H_kv, int max_seqlen_q, int max_seqlen_k) {
-  if (n_seqs < 1 || H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
-      static_cast<long long>(n_seqs) * H_kv * (max_seqlen_k / 256 + 1) >= (1LL << 30))
-    return 0;
-  return fa::weigh_part_bytes(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k);
+size_t fa_weigh_paged_workspace_size(int H, int H_kv, int max_seqlen_q) {
+  if (H < 1 || H_kv < 1 || H % H_kv != 0 || H / H_kv > 128 || max_seqlen_q < 0) return 0;
+  return fa::weigh_part_bytes(H, H_kv, max_seqlen_q);
 }
 
 fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t* k_cache, float* weights,
@@ -896,8 +894,9 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
   fa_status_t st = check_step(n_seqs, H, H_kv, total, max_seqlen_q, max_blocks_per_seq, block_size, num_blocks, max_seqlen_k, d, scale);
   if (st != FA_OK) return st;
   if (H / H_kv > 128) return fail(FA_ERR_UNSUPPORTED, "more than 128 query heads a key head (got %d)", H / H_kv);
-  if (static_cast<long long>(n_seqs) * H_kv > 65535 && fa::weigh_split(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k).ranges > 1)
-    return fail(FA_ERR_UNSUPPORTED, "n_seqs * H_kv must be <= 65535 for these lengths");
+  // (512 keys, row tile) units are counted in an int
+  if (static_cast<long long>(n_seqs) * H_kv * (max_seqlen_k / 512 + 1) * (max_seqlen_q / fa::weigh_tokens(H, H_kv, max_seqlen_q) + 2) >= (1LL << 31))
+    return fail(FA_ERR_UNSUPPORTED, "too many (key head, 512 keys, row tile) units");
   if (!(decay >= 0.f) || !(decay <= 1.f)) return fail(FA_ERR_INVALID_ARG, "decay must be in [0, 1] (got %g)", static_cast<double>(decay));
   if (total == 0 || max_seqlen_q == 0) return FA_OK;
   if (!q || !lse || !k_cache || !weights) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
@@ -905,7 +904,7 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
     if (!aligned16(x)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
   if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
   if (weighed && !aligned4(weighed)) return fail(FA_ERR_INVALID_ARG, "weighed must be 4-byte aligned");
-  const size_t need = fa::weigh_part_bytes(n_seqs, H, H_kv, max_seqlen_q, max_seqlen_k);
+  const size_t need = fa::weigh_part_bytes(H, H_kv, max_seqlen_q);
   if (need > 16 && (!ws || ws_bytes < need || !aligned16(ws)))
     return fail(FA_ERR_WORKSPACE, "workspace must be >= %zu bytes and 16-byte aligned (got %zu)", need, ws_bytes);
   fa::WeighArgs a{q, k_cache, lse, weights, static_cast<float*>(ws), cu_seqlens, seqlens_k, weighed, block_table, n_seqs, H, H_kv, total,

@@ -35,7 +35,6 @@
 // streamed caches have driven out of L2 takes microseconds): the rarer paths are loops.
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
-#include "q4_share.h"
 
 namespace fa {
 
@@ -241,45 +240,11 @@ struct TreeWalk {
   }
 };
 
-// By a whole warp: the shares, and the sequence that holds unit ``u_of(shares)`` (b = -1 where there is none), or
-// sequence ``at`` where that is given, with the units before it.
 template <typename F>
-__device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int grid, bool report, F u_of, int at, int* b, long long* before) {
-  const int lane = threadIdx.x & 31;
-  auto units = [&](int i, bool rep) {
-    return static_cast<long long>(tree_units(p, paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, rep, 501))) * p.heads;
-  };
-  Q4Share sh;
-  long long mine = 0, own = 0;
-  for (int i = lane; i < p.n_seqs; i += 32) {
-    const long long v = units(i, report);
-    if (i == lane) own = v;
-    mine += v;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  sh.set(mine, grid);
-  const long long u = at >= 0 ? 1LL << 62 : u_of(sh);
-  long long sum = 0;
-  *b = -1;
-  for (int base = 0; base < p.n_seqs && u >= 0; base += 32) {
-    const long long v = base == 0 ? own : base + lane < p.n_seqs ? units(base + lane, false) : 0;
-    long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += x;
-    }
-    const uint32_t beyond = __ballot_sync(0xffffffffu, at >= 0 ? base + lane >= at : sum + inc > u);
-    if (beyond) {
-      const int l = __ffs(beyond) - 1;
-      *b = base + l;
-      *before = sum + __shfl_sync(0xffffffffu, inc - v, l);
-      break;
-    }
-    sum += __shfl_sync(0xffffffffu, inc, 31);
-  }
-  return sh;
+__device__ __forceinline__ Q4Share tree_share(const TreeParams& p, int ctas, bool report, F u_of, int at, int* b, long long* before) {
+  return paged_share(p.n_seqs, ctas, [&](int i, bool first) {
+    return static_cast<long long>(tree_units(p, paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, report && first, 501))) * p.heads;
+  }, u_of, at, b, before);
 }
 
 // Bit k of word w: the row's token sees key k0 + 32 w + k.

@@ -543,7 +543,7 @@ PyObject* weigh(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int max_q = narrow(integer(a[8], "max_seqlen_q"), "max_seqlen_q"), max_k = narrow(integer(a[9], "max_seqlen_k"), "max_seqlen_k");
   const int s = narrow(seqs, "n_seqs"), h = narrow(H, "H"), hkv = narrow(c.heads, "H_kv");
   const Where on(a[13], c.device);
-  const Workspace ws(a[12], own ? lib.weigh_ws(s, h, hkv, max_q, max_k) : 0, c.device, own);
+  const Workspace ws(a[12], own ? lib.weigh_ws(h, hkv, max_q) : 0, c.device, own);
   done(lib.weigh(pq, pl, c.k, pw, had, cu, lens, tab, s, h, hkv, narrow(total, "total"), max_q, narrow(table.size(1), "max_blocks"),
                  narrow(c.block_size, "block_size"), narrow(c.blocks, "num_blocks"), max_k, narrow(c.d, "d"), scale_of(a[10], c.d),
                  number(a[11], "decay"), ws.ptr, ws.bytes, on.stream));

@@ -198,7 +198,7 @@ struct PagedTreeArgs {
 struct WeighArgs {
   const void *q, *k_cache;
   const float* lse;
-  float *weights, *part;        // part: sums of ranges of rows
+  float *weights, *part;        // part: sums of cut pieces
   const int *cu, *seqlens, *weighed, *block_table;            // weighed [n_seqs] or null
   int n_seqs, H, H_kv, total, max_q, max_k, d, num_blocks, block_size, max_blocks;
   float scale, decay;
@@ -254,29 +254,15 @@ inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
   return (2 * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) + kTreeMaxCtas + 8) * sizeof(float);
 }
 
-// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each.  Several tiles go against 512 keys at a
-// time, and are divided into ranges of at least four where the (sequence, key head, 512 keys) pieces alone would leave a
-// CTA fewer than six to take (two prompts of 4096 tokens with 8 key heads: 128 pieces, of which the first sees eight times
-// as many rows as the last).
-struct WeighSplit {
-  int tokens, ranges, range;                                  // of a tile; ranges of ``range`` tiles
-};
-inline WeighSplit weigh_split(int n_seqs, int H, int H_kv, int max_q, int max_k) {
-  WeighSplit t;
-  const int G = H / H_kv;
-  t.tokens = 128 / G < max_q ? 128 / G : max_q < 1 ? 1 : max_q;
-  const long long tiles = (max_q + t.tokens - 1) / t.tokens;
-  const long long pieces = static_cast<long long>(n_seqs) * H_kv * ((max_k + 511) / 512);
-  long long r = pieces > 0 ? (6 * 152 + pieces - 1) / pieces : 1;
-  if (r > tiles / 4) r = tiles / 4;
-  if (r < 1) r = 1;
-  t.range = static_cast<int>((tiles + r - 1) / r);
-  t.ranges = t.range > 0 ? static_cast<int>((tiles + t.range - 1) / t.range) : 1;
-  return t;
+// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each.  Several tiles are shared out to at most
+// kWeighMaxCtas CTAs, 512 keys at a time, which keep the sums of at most two cut pieces each.
+constexpr int kWeighMaxCtas = 152;
+inline int weigh_tokens(int H, int H_kv, int max_q) {
+  const int t = 128 / (H / H_kv);
+  return t < max_q ? t : max_q < 1 ? 1 : max_q;
 }
-inline size_t weigh_part_bytes(int n_seqs, int H, int H_kv, int max_q, int max_k) {
-  const WeighSplit t = weigh_split(n_seqs, H, H_kv, max_q, max_k);
-  return t.ranges <= 1 ? 16 : static_cast<size_t>(t.ranges) * n_seqs * H_kv * ((max_k + 511) / 512) * 512 * sizeof(float);
+inline size_t weigh_part_bytes(int H, int H_kv, int max_q) {
+  return weigh_tokens(H, H_kv, max_q) >= max_q ? 16 : 2 * kWeighMaxCtas * size_t(512) * sizeof(float);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);

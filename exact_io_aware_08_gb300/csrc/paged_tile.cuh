@@ -3,6 +3,7 @@
 #pragma once
 
 #include "q4.cuh"
+#include "q4_share.h"
 
 namespace fa {
 
@@ -27,6 +28,45 @@ __device__ __forceinline__ PagedSeq paged_seq(const int* __restrict__ cu, const 
     x.first = x.nq = x.len = 0;
   }
   return x;
+}
+
+// By a whole warp: equal shares of all sequences' units (``units(i, first)``, ``first``: asked for the first time), and the
+// sequence that holds unit ``u_of(shares)`` (b = -1 where there is none), or sequence ``at`` where that is given, with the
+// units before it.
+template <typename U, typename F>
+__device__ __forceinline__ Q4Share paged_share(int n_seqs, int ctas, U units, F u_of, int at, int* b, long long* before) {
+  const int lane = threadIdx.x & 31;
+  Q4Share sh;
+  long long mine = 0, own = 0;
+  for (int i = lane; i < n_seqs; i += 32) {
+    const long long v = units(i, true);
+    if (i == lane) own = v;
+    mine += v;
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  sh.set(mine, ctas);
+  const long long u = at >= 0 ? 1LL << 62 : u_of(sh);
+  long long sum = 0;
+  *b = -1;
+  for (int base = 0; base < n_seqs && u >= 0; base += 32) {
+    const long long v = base == 0 ? own : base + lane < n_seqs ? units(base + lane, false) : 0;
+    long long inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const uint32_t beyond = __ballot_sync(0xffffffffu, at >= 0 ? base + lane >= at : sum + inc > u);
+    if (beyond) {
+      const int l = __ffs(beyond) - 1;
+      *b = base + l;
+      *before = sum + __shfl_sync(0xffffffffu, inc - v, l);
+      break;
+    }
+    sum += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return sh;
 }
 
 // The bf16 cache as the copying warp sees it.  ``piece``: the rows of a copy, which never cross a page.

@@ -16,13 +16,12 @@
 //   warp 1       issues the products.
 //   warps 4 on   the sums, thread = key.
 // Few rows (one tile of them): Q stays, each CTA gets an equal share of all keys (Q4Share), 256 at a time with two S
-// buffers for each half.  Else a CTA keeps 512 keys and runs over a range of the rows that see them, four tiles of keys
-// by turns; where there are too few pieces for the SMs the rows are divided into ranges whose sums a second kernel adds
-// up, in order.  512 keys, since tiles of Q come from L2, at some 5 TB/s in all: with 256 of them that alone took 122 us of
-// 170 for 2 x 4096 tokens.
+// buffers for each half.  Else a CTA keeps 512 keys and runs over the rows that see them, four tiles of keys by turns, so
+// that a tile of Q is brought for 512 keys and the sums of one key tile run beside the products of the others.  The (512
+// keys, row tile) units are shared out equally too; the sums of 512 keys that lie in several shares are added up, in
+// order, by a second kernel.  (2 x 4096 tokens in whole ranges of row tiles, dealt out in rounds: 152 us.)
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
-#include "q4_share.h"
 
 namespace fa {
 
@@ -39,10 +38,11 @@ struct WeighCfg {
   // k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NQ], l_empty[NQ], s_full[4], s_empty[4]
   static constexpr int NBAR = 2 * NK + 4 * NQ + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;
+  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;      // (TMEM slot, abort flag, start[5])
   static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
   static constexpr int PAIRS = NK / 2;                        // few rows: pairs of K tiles in flight
   static constexpr int FEW_THREADS = 384, MANY_THREADS = 640;
+  static constexpr uint32_t BAR_S = 1, BAR_S_THREADS = 128 + 32;   // many rows: S of key tile a has been read
 };
 constexpr int kWeighKeys = 512;                               // of a piece with many rows
 
@@ -50,16 +50,12 @@ struct WeighParams {
   CUtensorMap tk, tq;
   PagedCache cache;
   const float* lse;
-  float *weights, *part;                                      // part: sums of ranges [range][sequence][key head][pieces * 512]
+  float *weights, *part;                                      // part: sums of cut pieces, two of 512 keys a CTA
   const int *cu, *seqlens, *weighed;
   int n_seqs, H, G, total, max_q, max_k;
   int tokens, rows;                                           // rows of a tile: ``tokens`` whole tokens
-  int pieces, ranges, range;                                  // pieces of 512 keys that max_k has; ranges of ``range`` row tiles
   float c2, decay;                                            // scale * log2 e
 };
-
-// First row tile whose tokens see a key of piece kt.
-__device__ __forceinline__ int weigh_first(const WeighParams& p, const PagedSeq& s, int kt) { return max(0, kt * kWeighKeys - s.base()) / p.tokens; }
 
 // Where a weight lies, or null (a page that is not there is reported by the copying warp).
 __device__ __forceinline__ float* weigh_place(const WeighParams& p, int b, int hkv, int key) {
@@ -102,42 +98,91 @@ struct WeighWalk {
   }
 };
 
-// Many rows: piece kt of a key head of a sequence against row tiles [q0, q1).
+// Many rows: pieces of 512 keys of a sequence against its row tiles.  Piece j has units(j) units: one for bringing its
+// keys, and as many as row tiles see them, or nearly (whole multiples of 512 keys are taken for so many whole row tiles,
+// which makes their sum a closed form); its row tiles [first, tiles) are shared out in proportion to units.
+struct WeighPieces {
+  int pieces, tiles, step, skip, base, tokens;                // row tiles; of 512 keys; that begin before the step's tokens end
+  __device__ __forceinline__ WeighPieces(const WeighParams& p, const PagedSeq& s) {
+    pieces = s.nq ? (s.len + kWeighKeys - 1) / kWeighKeys : 0;
+    tokens = p.tokens;
+    tiles = (s.nq + tokens - 1) / tokens;
+    step = kWeighKeys / tokens;
+    base = s.base();
+    skip = (base + tokens - 1) / tokens;
+  }
+  __device__ __forceinline__ int units(int j) const { return tiles - max(0, j * step - skip) + 1; }
+  __device__ __forceinline__ long long total() const {        // of a key head
+    const long long from = skip / step + 1, n = max(0LL, pieces - from);
+    return static_cast<long long>(pieces) * (tiles + 1) - (step * (from + pieces - 1) * n / 2 - skip * n);
+  }
+  // First row tile behind the first k units of piece j.
+  __device__ __forceinline__ int row_tile(int j, int k) const {
+    const int first = max(0, j * kWeighKeys - base) / tokens;
+    return first + static_cast<int>(static_cast<long long>(max(0, k - 1)) * (tiles - first) / (units(j) - 1));
+  }
+};
+
+template <typename F>
+__device__ __forceinline__ Q4Share weigh_share(const WeighParams& p, int ctas, bool report, F u_of, int* b, long long* before) {
+  return paged_share(p.n_seqs, ctas, [&](int i, bool first) {
+    return WeighPieces(p, paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, report && first, 600)).total() * p.cache.H_kv;
+  }, u_of, -1, b, before);
+}
+
+// Key head and piece of unit u of sequence ``x``; u becomes the unit in the piece.
+__device__ __forceinline__ void weigh_piece_of(const WeighPieces& x, long long* u, int* hkv, int* j) {
+  const long long all = x.total();
+  *hkv = static_cast<int>(*u / all);
+  *u -= *hkv * all;
+  *j = 0;
+  while (*u >= x.units(*j)) *u -= x.units((*j)++);
+}
+
+// Piece kt of a key head of a sequence against row tiles [q0, q1).  slot: -1 all of them, else the place of their sums.
 struct WeighPiece {
-  int b, hkv, kt, q0, q1, range;
+  int b, hkv, kt, q0, q1, slot;
   PagedSeq seq;
 };
-struct WeighRounds {
+struct WeighParts {
   const WeighParams& p;
-  int round;
+  int b, hkv, kt, k;                                          // next unit: sequence, key head, piece, unit in it
+  long long left;
 
   __device__ __forceinline__ bool next(WeighPiece& x) {
-    // (range, piece) by (range, piece) over all sequences and heads, the last rows, which see the most, first; dealt out
-    // in rounds
-    const int per = p.n_seqs * p.cache.H_kv, n = per * p.pieces * p.ranges;
-    for (; round * static_cast<int>(gridDim.x) < n; ++round) {
-      const int item = pers_item(round, gridDim.x);
-      if (item >= n) continue;
-      const int i = item / per, w = item - i * per;
-      x.hkv = w % p.cache.H_kv;
-      x.b = w / p.cache.H_kv;
-      x.range = p.ranges - 1 - i / p.pieces;
-      x.kt = i % p.pieces;
-      x.seq = paged_seq(p.cu, p.seqlens, x.b, p.total, p.max_q, p.max_k, threadIdx.x == 0 && i == 0 && x.hkv == 0, 600);
-      if (x.seq.nq == 0 || x.kt * kWeighKeys >= x.seq.len) continue;
-      x.q0 = max(x.range * p.range, weigh_first(p, x.seq, x.kt));
-      x.q1 = min((x.range + 1) * p.range, (x.seq.nq + p.tokens - 1) / p.tokens);
-      if (x.q0 >= x.q1) continue;
-      ++round;
-      return true;
+    while (left > 0) {
+      x.seq = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
+      const WeighPieces y(p, x.seq);
+      if (kt >= y.pieces) {
+        kt = k = 0;
+        if (++hkv >= p.cache.H_kv || y.pieces == 0) {
+          hkv = 0;
+          if (++b >= p.n_seqs) return false;
+        }
+        continue;
+      }
+      const int units = y.units(kt), n = static_cast<int>(min(left, static_cast<long long>(units - k)));
+      x.b = b;
+      x.hkv = hkv;
+      x.kt = kt;
+      x.q0 = y.row_tile(kt, k);
+      x.q1 = y.row_tile(kt, k + n);
+      x.slot = n == units ? -1 : 2 * static_cast<int>(blockIdx.x) + (k == 0 ? 1 : 0);
+      left -= n;
+      k += n;
+      if (k == units) {
+        k = 0;
+        ++kt;
+      }
+      if (x.q0 < x.q1) return true;
     }
     return false;
   }
 
-  // Key tiles of the piece that hold keys, and whether row tile qt sees any of tile a.
+  // Key tiles of the piece that hold keys, and of these the first ones that row tile qt sees (one at least).
   __device__ __forceinline__ int tiles(const WeighPiece& x) const { return min(4, (x.seq.len - x.kt * kWeighKeys + 127) / 128); }
-  __device__ __forceinline__ bool sees(const WeighPiece& x, int qt, int a) const {
-    return min(x.seq.nq, (qt + 1) * p.tokens) - 1 >= x.kt * kWeighKeys + a * 128 - x.seq.base();
+  __device__ __forceinline__ int seen(const WeighPiece& x, int qt, int n) const {
+    return min(n, ((min(x.seq.nq, (qt + 1) * p.tokens) - 1 + x.seq.base() - x.kt * kWeighKeys) >> 7) + 1);
   }
 };
 
@@ -250,9 +295,10 @@ struct WeighSpan {
   }
 };
 
-// Adds up the weights of a tile's columns, 32 from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e.  What has
-// been read is given back at ``read`` before the last of it is added up.
-__device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restrict__ nl, int cols, const WeighSpan& x, float c2, uint64_t* read) {
+// Adds up the weights of a tile's columns, 32 from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e.  ``read`` is
+// called when all has been read, before the last of it is added up.
+template <typename F>
+__device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restrict__ nl, int cols, const WeighSpan& x, float c2, F read) {
   float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
   const float2 c = make_float2(c2, c2);
 #pragma unroll 1
@@ -263,7 +309,7 @@ __device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restric
     if (c0 + 32 >= cols) {
       tc_fence_before();
       __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(read);
+      read();
     }
     if (c0 + 32 <= x.lo_min || c0 >= x.hi) continue;
     if (c0 < x.lo_max || c0 + 32 > x.hi) {
@@ -300,40 +346,16 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
     if (lane == 0) m.init(2, 8);                              // (a slot of K: a pair of tiles)
     if (lane < 2) tma_prefetch_desc(lane ? &p.tq : &p.tk);
     // this CTA's share of the key pairs
-    auto units = [&](int i, bool report) {
-      return static_cast<long long>(weigh_pairs(paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, report, 601))) * p.cache.H_kv;
-    };
-    long long mine = 0;
-    for (int i = lane; i < p.n_seqs; i += 32) mine += units(i, blockIdx.x == 0);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-    Q4Share sh;
-    sh.set(mine, gridDim.x);
-    const bool some = static_cast<int>(blockIdx.x) < sh.n && sh.total > 0;
-    const long long u = some ? sh.begin(blockIdx.x) : -1;
-    long long sum = 0, before = 0;
-    int b = -1;
-    for (int base = 0; base < p.n_seqs && u >= 0; base += 32) {
-      const long long v = base + lane < p.n_seqs ? units(base + lane, false) : 0;
-      long long inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
-      }
-      const uint32_t beyond = __ballot_sync(0xffffffffu, sum + inc > u);
-      if (beyond) {
-        const int l = __ffs(beyond) - 1;
-        b = base + l;
-        before = sum + __shfl_sync(0xffffffffu, inc - v, l);
-        break;
-      }
-      sum += __shfl_sync(0xffffffffu, inc, 31);
-    }
+    int b;
+    long long before = 0;
+    const int c = blockIdx.x;
+    const Q4Share sh = paged_share(p.n_seqs, gridDim.x, [&](int i, bool first) {
+      return static_cast<long long>(weigh_pairs(paged_seq(p.cu, p.seqlens, i, p.total, p.max_q, p.max_k, c == 0 && first, 601))) * p.cache.H_kv;
+    }, [&](const Q4Share& y) { return c < y.n && y.total > 0 ? y.begin(c) : -1LL; }, -1, &b, &before);
     if (lane == 0) {
       m.start[0] = b;
-      m.start[1] = b < 0 ? 0 : static_cast<int>(u - before);
-      m.start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(blockIdx.x + 1) - u);
+      m.start[1] = b < 0 ? 0 : static_cast<int>(sh.begin(c) - before);
+      m.start[2] = b < 0 ? 0 : static_cast<int>(sh.begin(c + 1) - sh.begin(c));
     }
   } else if (warp == 1) {
     tmem_alloc(m.tmem_slot, 512);
@@ -433,7 +455,9 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
         const float old = at && key < weighed ? *at * p.decay : 0.f;
         if (!(ok = mbar_wait_warp(&m.s_full[buf], (kc >> 1) & 1, abort_flag, 631))) break;
         tc_fence_after();
-        const float sum = weigh_tile(t_lane + buf * 128, lse, cols, WeighSpan(p, x.seq, key, 0, x.seq.nq * p.G), p.c2, &m.s_empty[buf]);
+        const float sum = weigh_tile(t_lane + buf * 128, lse, cols, WeighSpan(p, x.seq, key, 0, x.seq.nq * p.G), p.c2, [&] {
+          if (lane == 0) mbar_arrive(&m.s_empty[buf]);
+        });
         if (at) *at = old + sum;
       }
       __syncwarp();
@@ -461,6 +485,22 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
   if (warp == 0) {
     if (lane == 0) m.init(1, 16);
     if (lane < 2) tma_prefetch_desc(lane ? &p.tq : &p.tk);
+    int b, hkv = 0, kt = 0;
+    long long before = 0, u = 0, left = 0;
+    const int c = blockIdx.x;
+    const Q4Share sh = weigh_share(p, gridDim.x, c == 0, [&](const Q4Share& y) { return c < y.n && y.total > 0 ? y.begin(c) : -1LL; }, &b, &before);
+    if (b >= 0) {
+      u = sh.begin(c) - before;
+      left = sh.begin(c + 1) - sh.begin(c);
+      weigh_piece_of(WeighPieces(p, paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0)), &u, &hkv, &kt);
+    }
+    if (lane == 0) {
+      m.start[0] = b;
+      m.start[1] = hkv;
+      m.start[2] = kt;
+      m.start[3] = static_cast<int>(u);
+      m.start[4] = static_cast<int>(left);                    // (below 2^31: launch)
+    }
   } else if (warp == 1) {
     tmem_alloc(m.tmem_slot, 512);
   }
@@ -471,7 +511,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
   tc_fence_after();
   const uint32_t tbase = *m.tmem_slot;
 
-  WeighRounds walk{p, 0};
+  WeighParts walk{p, m.start[0], m.start[1], m.start[2], m.start[3], m.start[4]};
   WeighPiece x;
   bool ok = true;
   int kc = 0, qc = 0;                                         // pieces, row tiles so far
@@ -535,61 +575,77 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
     const uint32_t idesc = idesc_bf16_f32(128, (p.rows + 15) / 16 * 16, 0, 0);
     const uint64_t dk0 = smem_desc_sw128(smem_u32(m.k), 0, 1024);
     const uint64_t dq0 = smem_desc_sw128(smem_u32(m.q), 0, 1024);
-    uint32_t k_parity = 0, s_used = 0, s_parity = 0;          // by slot of K, by S buffer
-    while (ok && walk.next(x)) {
+    // After a failed wait the warp goes on joining every hand-back, issuing nothing.
+    uint32_t k_parity = 0, s_used = 0;                        // by slot of K, by S buffer
+    while (walk.next(x)) {
       const int n = walk.tiles(x), set = 4 * (kc % SETS);
-      for (int qt = x.q0; ok && qt < x.q1; ++qt, ++qc) {
-        ok = mbar_wait_warp(&m.q_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 621);
-        for (int a = 0; ok && a < n; ++a) {
-          if (qt == x.q0) {
-            ok = mbar_wait_warp(&m.k_full[set + a], k_parity >> (set + a) & 1u, abort_flag, 620);
+      for (int qt = x.q0; qt < x.q1; ++qt, ++qc) {
+        ok = ok && mbar_wait_warp(&m.q_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 621);
+        const uint64_t dq = desc_advance(dq0, (qc % C::NQ) * C::TILE);
+        if (qt == x.q0)
+          for (int a = 0; a < n; ++a) {
+            ok = ok && mbar_wait_warp(&m.k_full[set + a], k_parity >> (set + a) & 1u, abort_flag, 620);
             k_parity ^= 1u << (set + a);
           }
-          if (!ok || !walk.sees(x, qt, a)) continue;
-          if (s_used >> a & 1u) {
-            if (!(ok = mbar_wait_warp(&m.s_empty[a], s_parity >> a & 1u, abort_flag, 622))) break;
-            s_parity ^= 1u << a;
-          }
+        const int seen = walk.seen(x, qt, n);
+        const uint64_t dk = desc_advance(dk0, set * C::TILE);
+        // (unrolled: what the warp does between two products has to fit into the few that the tensor core has queued)
+#pragma unroll
+        for (int a = 0; a < 4; ++a) {
+          if (a >= seen) break;
+          if (s_used & (1u << a)) named_bar_sync(C::BAR_S + a, C::BAR_S_THREADS);
           s_used |= 1u << a;
-          tc_fence_after();
-          weigh_product<D>(tbase + a * 128, desc_advance(dk0, (set + a) * C::TILE), desc_advance(dq0, (qc % C::NQ) * C::TILE), idesc, &m.s_full[a]);
+          if (ok) {
+            tc_fence_after();
+            weigh_product<D>(tbase + a * 128, desc_advance(dk, a * C::TILE), dq, idesc, &m.s_full[a]);
+            if (qt + 1 == x.q1) umma_commit_w(&m.k_empty[set + a]);   // (the last row tile sees all that any sees)
+          }
         }
         if (ok) umma_commit_w(&m.q_empty[qc % C::NQ]);
       }
-      for (int a = 0; ok && a < n; ++a) umma_commit_w(&m.k_empty[set + a]);
+      for (int a = walk.seen(x, x.q1 - 1, n); ok && a < n; ++a) umma_commit_w(&m.k_empty[set + a]);
       ++kc;
+    }
+    for (int a = 0; a < 4; ++a) {
+      __syncwarp();
+      if (s_used >> a & 1u) named_bar_sync(C::BAR_S + a, C::BAR_S_THREADS);
     }
   } else {
     // ---------------------------------------------------------------- sums, a warpgroup a key tile
+    // (S is given back by a named barrier, which costs the issuing warp some 30 clocks where an mbarrier costs it 175)
     const int a = (warp - 4) >> 2, sub = warp & 3;
     const uint32_t t_s = tbase + (static_cast<uint32_t>(sub * 32) << 16) + a * 128;
     const int cols = (p.rows + 31) / 32 * 32;
     int sc = 0;                                               // products so far
-    while (ok && walk.next(x)) {
-      const int key = x.kt * kWeighKeys + a * 128 + sub * 32 + lane;
-      const bool mine = a < walk.tiles(x);
+    while (walk.next(x)) {
+      const int key = x.kt * kWeighKeys + a * 128 + sub * 32 + lane, tiles = walk.tiles(x);
       float sum = 0.f;
-      for (int qt = x.q0; ok && qt < x.q1; ++qt, ++qc) {
-        if (mine && walk.sees(x, qt, a)) {
+      for (int qt = x.q0; qt < x.q1; ++qt, ++qc) {
+        if (a < walk.seen(x, qt, tiles)) {
           // (both at once: most of the time neither is waited for)
           uint64_t* bars[2] = {&m.l_full[qc % C::NQ], &m.s_full[a]};
           const uint32_t there = mbar_try_wait(smem_u32(bars[0]), (qc / C::NQ) & 1), done = mbar_try_wait(smem_u32(bars[1]), sc & 1);
           if (!__all_sync(0xffffffffu, there && done))
-            ok = mbar_wait_warp(bars[0], (qc / C::NQ) & 1, abort_flag, 630) && mbar_wait_warp(bars[1], sc & 1, abort_flag, 631);
-          if (!ok) break;
-          tc_fence_after();
-          const int r0 = qt * p.tokens * p.G, n = min(p.tokens, x.seq.nq - qt * p.tokens) * p.G;
-          sum += weigh_tile(t_s, m.lse + (qc % C::NQ) * 128, cols, WeighSpan(p, x.seq, key, r0, n), p.c2, &m.s_empty[a]);
+            ok = ok && mbar_wait_warp(bars[0], (qc / C::NQ) & 1, abort_flag, 630) && mbar_wait_warp(bars[1], sc & 1, abort_flag, 631);
           ++sc;
-        } else if (!(ok = mbar_wait_warp(&m.l_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 632))) {
-          break;                                              // (lse is given back once for each time that it was there)
+          if (!ok) {                                          // after an abort: keep joining, blocking
+            __syncwarp();
+            named_bar_sync(C::BAR_S + a, C::BAR_S_THREADS);
+            continue;
+          }
+          tc_fence_after();
+          const int r0 = qt * p.tokens * p.G, rows = min(p.tokens, x.seq.nq - qt * p.tokens) * p.G;
+          sum += weigh_tile(t_s, m.lse + (qc % C::NQ) * 128, cols, WeighSpan(p, x.seq, key, r0, rows), p.c2,
+                            [&] { named_bar_arrive(C::BAR_S + a, C::BAR_S_THREADS); });
+        } else {
+          ok = ok && mbar_wait_warp(&m.l_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 632);
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&m.l_empty[qc % C::NQ]);
+        if (lane == 0 && ok) mbar_arrive(&m.l_empty[qc % C::NQ]);   // (once for each time that it was there)
       }
-      if (!ok || !mine || key >= x.seq.len) continue;
-      if (p.ranges > 1) {
-        p.part[(((static_cast<size_t>(x.range) * p.n_seqs + x.b) * p.cache.H_kv + x.hkv) * p.pieces) * kWeighKeys + key] = sum;
+      if (!ok || a >= tiles || key >= x.seq.len) continue;
+      if (x.slot >= 0) {
+        p.part[static_cast<size_t>(x.slot) * kWeighKeys + key - x.kt * kWeighKeys] = sum;
       } else {
         float* at = weigh_place(p, x.b, x.hkv, key);
         const int weighed = p.weighed ? __ldg(p.weighed + x.b) : x.seq.base();
@@ -606,22 +662,58 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
   }
 }
 
-// Adds up the ranges' sums, thread = key.
-__global__ void __launch_bounds__(256) weigh_join_kernel(const __grid_constant__ WeighParams p) {
-  const int hkv = blockIdx.y % p.cache.H_kv, b = blockIdx.y / p.cache.H_kv;
-  const PagedSeq s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
-  const int key = blockIdx.x * 256 + threadIdx.x;
-  const int weighed = p.weighed ? __ldg(p.weighed + b) : s.base();
-  float* at = s.nq && key < s.len ? weigh_place(p, b, hkv, key) : nullptr;
-  pdl_wait();
-  if (!at) return;
-  const int tiles = (s.nq + p.tokens - 1) / p.tokens;
-  const float* part = p.part + (static_cast<size_t>(b) * p.cache.H_kv + hkv) * p.pieces * kWeighKeys + key;
-  const size_t stride = static_cast<size_t>(p.n_seqs) * p.cache.H_kv * p.pieces * kWeighKeys;
-  const float old = key < weighed ? *at * p.decay : 0.f;
-  float drawn = 0.f;
-  for (int r = weigh_first(p, s, key / kWeighKeys) / p.range; r * p.range < tiles; ++r) drawn += part[r * stride];
-  *at = old + drawn;
+// Adds up the sums of a piece that a bound between shares cuts, if bound i + 1 is the first within it; thread = key.
+__global__ void __launch_bounds__(kWeighKeys) weigh_join_kernel(const __grid_constant__ WeighParams p, int ctas) {
+  __shared__ int found[4];                                    // sequence, key head, piece, CTAs
+  __shared__ uint32_t has[8];                                 // by CTA of the piece: whether it has any row tiles
+  const int i = blockIdx.x, lane = threadIdx.x & 31;
+  if (threadIdx.x < 32) {
+    int b;
+    long long before = 0;
+    const Q4Share sh = weigh_share(p, ctas, false, [&](const Q4Share& y) { return i + 1 < y.n ? y.begin(i + 1) : -1LL; }, &b, &before);
+    int n = 0, hkv = 0, kt = 0;
+    if (b >= 0) {
+      const WeighPieces y(p, paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0));
+      long long k = sh.begin(i + 1) - before;
+      weigh_piece_of(y, &k, &hkv, &kt);
+      // the bound lies k units into the piece: within it, and the first that does
+      const long long u0 = sh.begin(i + 1) - k;
+      if (k > 0 && sh.begin(i) <= u0) {
+        const int units = y.units(kt);
+        n = sh.owner(u0 + units - 1) - i + 1;
+        for (int base = 0; base < n; base += 32) {
+          const int c = i + base + lane;
+          bool some = false;
+          if (base + lane < n) {
+            const int k0 = static_cast<int>(max(0LL, sh.begin(c) - u0)), k1 = static_cast<int>(min(static_cast<long long>(units), sh.begin(c + 1) - u0));
+            some = y.row_tile(kt, k0) < y.row_tile(kt, k1);
+          }
+          const uint32_t bits = __ballot_sync(0xffffffffu, some);
+          if (lane == 0) has[base / 32] = bits;
+        }
+      }
+    }
+    if (lane == 0) {
+      found[0] = b; found[1] = hkv; found[2] = kt; found[3] = n;
+    }
+  }
+  __syncthreads();
+  const int n = found[3], b = found[0];
+  if (n > 0) {
+    const PagedSeq s = paged_seq(p.cu, p.seqlens, b, p.total, p.max_q, p.max_k, false, 0);
+    const int key = found[2] * kWeighKeys + threadIdx.x;
+    const int weighed = p.weighed ? __ldg(p.weighed + b) : s.base();
+    float* at = key < s.len ? weigh_place(p, b, found[1], key) : nullptr;
+    pdl_wait();
+    if (!at) return;
+    const float old = key < weighed ? *at * p.decay : 0.f;
+    float drawn = 0.f;
+    for (int c = 0; c < n; ++c)                               // (the first CTA's second place, the others' first one)
+      if (has[c >> 5] >> (c & 31) & 1u) drawn += p.part[static_cast<size_t>(2 * (i + c) + (c == 0 ? 1 : 0)) * kWeighKeys + threadIdx.x];
+    *at = old + drawn;
+  } else {
+    pdl_wait();
+  }
 }
 
 template <int D>
@@ -630,9 +722,8 @@ static cudaError_t launch_weigh_d(const WeighArgs& a, cudaStream_t stream) {
   WeighParams p{};
   const int piece = paged_piece(a.block_size);
   const uint64_t rows = static_cast<uint64_t>(a.num_blocks) * a.block_size;
-  const WeighSplit t = weigh_split(a.n_seqs, a.H, a.H_kv, a.max_q, a.max_k);
   p.G = a.H / a.H_kv;
-  p.tokens = t.tokens;
+  p.tokens = weigh_tokens(a.H, a.H_kv, a.max_q);
   p.rows = p.tokens * p.G;
   if (!make_map_bf16_tok(&p.tk, a.k_cache, D, a.H_kv, rows, 64, piece) ||
       !make_map_bf16_group(&p.tq, a.q, D, p.G, a.H_kv, a.total, 64, p.G, p.tokens))
@@ -641,25 +732,22 @@ static cudaError_t launch_weigh_d(const WeighArgs& a, cudaStream_t stream) {
   p.lse = a.lse; p.weights = a.weights; p.part = a.part; p.cu = a.cu; p.seqlens = a.seqlens; p.weighed = a.weighed;
   p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
   p.c2 = a.scale * 1.4426950408889634f; p.decay = a.decay;
-  p.pieces = (a.max_k + kWeighKeys - 1) / kWeighKeys;
-  p.ranges = t.ranges;
-  p.range = t.range;
   const bool few = p.tokens >= a.max_q;
   static int few_done[64] = {0}, many_done[64] = {0};
   cudaError_t e = few ? ensure_smem_attr(weigh_few_kernel<D>, C::SMEM_BYTES, few_done) : ensure_smem_attr(weigh_many_kernel<D>, C::SMEM_BYTES, many_done);
   if (e != cudaSuccess) return e;
   const long long heads = static_cast<long long>(a.n_seqs) * a.H_kv;
-  const long long items = few ? heads * ((a.max_k + 255) / 256) : heads * p.pieces * p.ranges;
-  const long long grid = min(static_cast<long long>(paged_sm_count()), items);
+  const long long items = few ? heads * ((a.max_k + 255) / 256)
+                              : heads * ((a.max_k + kWeighKeys - 1) / kWeighKeys) * ((a.max_q + p.tokens - 1) / p.tokens);
+  const long long grid = min(static_cast<long long>(min(paged_sm_count(), kWeighMaxCtas)), items);
   const unsigned threads = few ? C::FEW_THREADS : C::MANY_THREADS;
   log_launch(few ? "weigh_few_kernel<D>" : "weigh_many_kernel<D>", static_cast<unsigned long long>(grid), threads, static_cast<unsigned long long>(C::SMEM_BYTES));
   if (few) weigh_few_kernel<D><<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(p);
   else weigh_many_kernel<D><<<static_cast<unsigned>(grid), threads, C::SMEM_BYTES, stream>>>(p);
   e = cudaGetLastError();
-  if (e != cudaSuccess || p.ranges == 1) return e;
-  const dim3 blocks(static_cast<unsigned>((a.max_k + 255) / 256), static_cast<unsigned>(heads));
-  log_launch("weigh_join_kernel", static_cast<unsigned long long>(blocks.x) * blocks.y, 256, 0ull);
-  return launch_join(weigh_join_kernel, blocks, 256, stream, p);
+  if (e != cudaSuccess || few || grid == 1) return e;
+  log_launch("weigh_join_kernel", static_cast<unsigned long long>(grid - 1), kWeighKeys, 0ull);
+  return launch_join(weigh_join_kernel, static_cast<unsigned>(grid - 1), kWeighKeys, stream, p, static_cast<int>(grid));
 }
 
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream) {

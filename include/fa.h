@@ -508,7 +508,7 @@ fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens
  * query (whose arguments are the call's) is 16 bytes or less.  The rest and the device-side checks as for
  * fa_fwd_paged_tree.  Two sequences that share a page race.
  */
-size_t fa_weigh_paged_workspace_size(int n_seqs, int H, int H_kv, int max_seqlen_q, int max_seqlen_k);
+size_t fa_weigh_paged_workspace_size(int H, int H_kv, int max_seqlen_q);
 fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t* k_cache, float* weights,
                            const int* weighed, const int* cu_seqlens, const int* seqlens_k, const int* block_table,
                            int n_seqs, int H, int H_kv, int total, int max_seqlen_q, int max_blocks_per_seq,

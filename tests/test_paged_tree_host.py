@@ -76,9 +76,9 @@ def test_tree_workspace_size(lib):
 
 def test_weigh_workspace_size(lib):
     size = lib.fa_weigh_paged_workspace_size
-    assert size(4, 8, 2, 1, 1000) == size(64, 32, 8, 300, 30000) == 16          # one tile of rows; enough pieces without ranges
-    assert size(1, 32, 8, 4096, 4096) == 15 * 8 * 8 * 512 * 4
-    assert size(0, 8, 2, 1, 1) == size(1, 8, 3, 1, 1) == size(1, 130, 1, 1, 1) == size(1, 8, 2, -1, 1) == 0
+    assert size(8, 2, 1) == size(8, 2, 32) == 16                 # one tile of rows
+    assert size(8, 2, 33) == size(32, 8, 4096) == 2 * 152 * 512 * 4
+    assert size(8, 3, 1) == size(130, 1, 1) == size(8, 2, -1) == size(0, 1, 1) == 0
 
 
 ACCEPT = dict(kc=FAKE, vc=FAKE, out=FAKE, path=FAKE, n=FAKE, cu=FAKE, lens=FAKE + 64, table=FAKE, n_seqs=2, H_kv=2, deep=4, max_blocks=8,
