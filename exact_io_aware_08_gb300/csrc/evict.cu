@@ -8,8 +8,11 @@
 // (above the border; at it), so that the order stays and nothing depends on the order of atomics.  Rows are copied
 // by lanes of 16 bytes.
 //
-// What bounds it: the copy is bound by HBM; the selection, 4 bytes a token, by latencies: four passes over the keys
-// (from shared memory, up to kHeld of them), each with a scan of 256 counts.
+// What bounds it: the copy is bound by HBM (16 sequences of 10000 to 16384 tokens, 8 heads of 128, 1024 to 4096 of them
+// kept: 61 us for about 330 MB read and written); the selection, 4 bytes a token, by latencies: four passes over the keys (from shared memory, up
+// to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 29 for 16384).  Three passes of 11, 11 and 10
+// bits with equal digits of a warp counted together were no faster (13 and 33 us), and choosing in every block that copies,
+// without the list between them, was slower as a whole (123 us for that batch, 91 this way).
 //
 // Accept.  Rows move down: token i of the path, at place a_i >= i of the step's, comes to place i.  A thread takes 16
 // bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.
@@ -148,7 +151,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 }
 
 constexpr int kCopyThreads = 256;
-constexpr int kCopyRows = 64;                                 // kept tokens of a block
+constexpr int kCopyRows = 32;                                 // kept tokens of a block (64: 240 us for 16 x 9000 of 8 heads, 32: 230)
 
 // Copies kept rows of a key head: 16 bytes a lane, D / 8 lanes a row, K and V.
 template <int D>
