@@ -569,20 +569,26 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       // -------------------------------------------------------------- copies
       bool ok = true;
       int g = 0;
-      PageWindow win;
-      auto load = [&](const CUtensorMap* map, int j) {
-        const int s = g % C::NST, u = g / C::NST;
-        if (u > 0 && !(ok = mbar_wait_warp(&empty[s], (u - 1) & 1, abort_flag, 510))) return;
-        load_paged_tile<D>(p.cache, win, map, sKV + s * C::TILE, &full[s], x.b, x.head / p.per_kv, x.key0 + j * C::BN, x.key_end, 502);
-        ++g;
-      };
+      PagedStream<D> keys(p.cache);
+      int slot = 0, laps = 0;                                 // of the next tile
       while (ok && walk.next(x)) {
-        const int n = NT == 2 ? max(tiles(0), tiles(1)) : tiles(0);
+        const int n = NT == 2 ? max(tiles(0), tiles(1)) : tiles(0), hkv = x.head / p.per_kv;
+        keys.begin(p.cache, x.b, x.key0, x.key_end);
+        int at = -1, before = -1;                             // of the last K tile, and of the one before it
         // K_0 V_0 K_1 V_1 ..., or K_0 K_1 V_0 K_2 V_1 ...
-        for (int i = 0; ok && i < 2 * n; ++i) {
-          const bool is_k = NT == 2 ? (i & 1) == 0 : i == 0 || ((i & 1) && i + 1 < 2 * n);
-          const int j = NT == 2 ? i >> 1 : is_k ? (i + 1) >> 1 : i + 1 < 2 * n ? (i >> 1) - 1 : n - 1;
-          load(is_k ? &p.tk : &p.tv, j);
+        for (int i = 0; i < 2 * n; ++i) {
+          const bool last = i + 1 == 2 * n, is_k = !last && (NT == 2 ? (i & 1) == 0 : i == 0 || (i & 1));
+          if (is_k) {
+            before = at;
+            at = keys.next(p.cache, 502);
+          }
+          if (laps > 0 && !(ok = mbar_wait_warp(&empty[slot], (laps - 1) & 1, abort_flag, 510))) break;
+          keys.load(p.cache, is_k ? &p.tk : &p.tv, sKV + slot * C::TILE, &full[slot], hkv, NT == 2 || is_k || last ? at : before);
+          ++g;
+          if (++slot == C::NST) {
+            slot = 0;
+            ++laps;
+          }
         }
       }
       // every signal is awaited; after an abort: every copy that was started lands
@@ -1074,7 +1080,7 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   if (!make_map_bf16_tok(&p.tk, a.k_cache, D, a.H_kv, rows, 64, piece) || !make_map_bf16_tok(&p.tv, a.v_cache, D, a.H_kv, rows, 64, piece) ||
       !make_map_bf16_group(&p.tq, a.q, D, t.group, a.H / t.group, a.total, 64, t.group, t.tokens))
     return cudaErrorInvalidValue;
-  p.cache = {a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks, piece};
+  p.cache = paged_cache(a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks);
   p.v = static_cast<const uint16_t*>(a.v_cache);
   p.o = static_cast<uint16_t*>(a.o); p.lse = a.lse; p.part = a.part + kTreeMaxCtas + 8;
   p.tree = a.tree; p.words = a.words; p.cu = a.cu; p.seqlens = a.seqlens;

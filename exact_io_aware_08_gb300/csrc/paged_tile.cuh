@@ -69,60 +69,84 @@ __device__ __forceinline__ Q4Share paged_share(int n_seqs, int ctas, U units, F 
   return sh;
 }
 
-// The bf16 cache as the copying warp sees it.  ``piece``: the rows of a copy, which never cross a page.
+// The bf16 cache as the copying warp sees it.
 struct PagedCache {
   const int* table;
-  int H_kv, num_blocks, block_size, max_blocks, piece;
+  int H_kv, num_blocks, block_size, max_blocks;
+  int shift;                                                  // a copy takes 2^shift rows, which never cross a page
+  int step_blocks, step_rows;                                 // a tile on: whole blocks, and rows
 };
 
-// The copying warp's window of 32 entries of a sequence's block table, one a lane.
-struct PageWindow {
-  int b = -1, at = 0, entry = 0;
-
-  // Page of block ``blk`` of sequence ``seq``, for a warp whose lanes ask for blocks in [lo, hi], hi - lo < 32.
-  __device__ __forceinline__ int page(const PagedCache& c, int seq, int lo, int hi, int blk, int where) {
-    const int lane = threadIdx.x & 31;
-    if (seq != b || lo < at || hi >= at + 32) {
-      b = seq;
-      at = lo;
-      entry = lo + lane < c.max_blocks ? __ldg(c.table + static_cast<size_t>(seq) * c.max_blocks + lo + lane) : -1;
-    }
-    int p = __shfl_sync(0xffffffffu, entry, (blk - at) & 31);
-    if (blk <= hi && (p < 0 || p >= c.num_blocks)) {
-      report_device_error(FA_DEV_BAD_CONFIG, where);
-      p = 0;                                                  // stays in bounds; the result is reported invalid
-    }
-    return p;
-  }
-};
-
-// Brings keys [key, min(key + 128, end)) of key head ``hkv`` as a 128-byte-swizzled tile [D / 64][128][64]:
-// by the whole warp, counted on ``bar``.  Rows behind ``end`` that share no copy with one before it keep what
-// they held.
+// A sequence's tiles of 128 keys in a row, by the whole warp: a lane holds one piece of a tile (and one 64-column half).
+// Tiles are counted on, without divisions, and the page of the next one is asked for ahead: a warp by itself takes 4 to 5
+// clocks an instruction, and 200 of them a tile bound the long reads (16 x 32768 keys of 4 heads: 186 us).
 template <int D>
-__device__ __forceinline__ void load_paged_tile(const PagedCache& c, PageWindow& w, const CUtensorMap* map, uint8_t* dst, uint64_t* bar,
-                                                int seq, int hkv, int key, int end, int where) {
-  constexpr int CH = D / 64;
-  const int lane = threadIdx.x & 31;
-  const int pieces = kPagedTile / c.piece, pi = lane % pieces;
-  const int k = key + pi * c.piece;
-  const bool mine = lane < pieces * CH && k < end;
-  const int lo = key / c.block_size, hi = (min(key + kPagedTile, end) - 1) / c.block_size;
-  const int blk = mine ? k / c.block_size : lo;
-  const int page = w.page(c, seq, lo, hi, blk, where);
-  const int live = __popc(__ballot_sync(0xffffffffu, mine));
-  if (lane == 0) mbar_arrive_expect_tx(bar, live * c.piece * 128);
-  __syncwarp();
-  if (mine) {
-    const int ch = lane / pieces;
-    tma_load_3d(dst + ch * kPagedTile * 128 + pi * c.piece * 128, map, bar, ch * 64, hkv, page * c.block_size + (k - blk * c.block_size));
+struct PagedStream {
+  static constexpr int HALVES = D / 64;
+  const int* table;
+  int key, end, blk, row, page;                               // of the lane's piece of the next tile
+  int copies;                                                 // whether the lane has one
+  int offset;                                                 // in the tile, bytes
+
+  __device__ __forceinline__ explicit PagedStream(const PagedCache& c) {
+    const int lane = threadIdx.x & 31, pieces_log2 = 7 - c.shift, half = lane >> pieces_log2, pi = lane & ((1 << pieces_log2) - 1);
+    copies = half < HALVES;
+    offset = half * kPagedTile * 128 + (pi << (c.shift + 7));
   }
-  __syncwarp();
-}
+
+  __device__ __forceinline__ int entry() const { return copies && key < end ? __ldg(table + blk) : 0; }
+
+  // Keys [key0, end0) of sequence b, which lie within its table.
+  __device__ __forceinline__ void begin(const PagedCache& c, int b, int key0, int end0) {
+    table = c.table + static_cast<size_t>(b) * c.max_blocks;
+    key = key0 + ((offset & (kPagedTile * 128 - 1)) >> 7);
+    end = end0;
+    blk = key / c.block_size;
+    row = key - blk * c.block_size;
+    page = entry();
+  }
+
+  // The cache row of the lane's piece of the next tile, or -1.
+  __device__ __forceinline__ int next(const PagedCache& c, int where) {
+    int at = -1;
+    if (copies && key < end) {
+      if (static_cast<unsigned>(page) >= static_cast<unsigned>(c.num_blocks)) {
+        report_device_error(FA_DEV_BAD_CONFIG, where);
+        page = 0;                                             // stays in bounds; the result is reported invalid
+      }
+      at = page * c.block_size + row;
+    }
+    key += kPagedTile;
+    blk += c.step_blocks;
+    row += c.step_rows;
+    if (row >= c.block_size) {
+      row -= c.block_size;
+      ++blk;
+    }
+    page = entry();
+    return at;
+  }
+
+  // Brings the tile whose pieces are at ``at`` as a 128-byte-swizzled one, [D / 64][128][64], counted on ``bar``.  Rows
+  // behind the last key that share no copy with one before it keep what they held.
+  __device__ __forceinline__ void load(const PagedCache& c, const CUtensorMap* map, uint8_t* dst, uint64_t* bar, int hkv, int at) const {
+    const int live = __popc(__ballot_sync(0xffffffffu, at >= 0));
+    if ((threadIdx.x & 31) == 0) mbar_arrive_expect_tx(bar, live << (c.shift + 7));
+    __syncwarp();
+    if (at >= 0) tma_load_3d(dst + offset, map, bar, offset >> 14 << 6, hkv, at);
+    __syncwarp();
+  }
+};
 
 // Rows of a copy for a block size that is a multiple of 16.
 inline int paged_piece(int block_size) {
   return block_size % 128 == 0 ? 128 : block_size % 64 == 0 ? 64 : block_size % 32 == 0 ? 32 : 16;
+}
+
+inline PagedCache paged_cache(const int* table, int H_kv, int num_blocks, int block_size, int max_blocks) {
+  const int piece = paged_piece(block_size);
+  return {table, H_kv, num_blocks, block_size, max_blocks, piece == 128 ? 7 : piece == 64 ? 6 : piece == 32 ? 5 : 4,
+          kPagedTile / block_size, kPagedTile % block_size};
 }
 
 inline int paged_sm_count() {

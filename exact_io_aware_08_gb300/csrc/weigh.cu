@@ -377,17 +377,16 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies of K
-    PageWindow win;
+    PagedStream<D> keys(p.cache);
     while (ok && walk.next(x)) {
+      keys.begin(p.cache, x.b, x.kt0 * 256, x.seq.len);
       for (int kt = x.kt0; ok && kt < x.kt1; ++kt, ++kc) {
         const int s = kc % C::PAIRS, u = kc / C::PAIRS;
         if (u > 0 && !(ok = mbar_wait_warp(&m.k_empty[s], (u - 1) & 1, abort_flag, 610))) break;
         uint8_t* dst = m.k + s * 2 * C::TILE;
-        load_paged_tile<D>(p.cache, win, &p.tk, dst, &m.k_full[s], x.b, x.hkv, kt * 256, x.seq.len, 602);
-        if (kt * 256 + 128 < x.seq.len)
-          load_paged_tile<D>(p.cache, win, &p.tk, dst + C::TILE, &m.k_full[s], x.b, x.hkv, kt * 256 + 128, x.seq.len, 602);
-        else if (lane == 0)
-          mbar_arrive(&m.k_full[s]);
+        // (a tile behind the last key brings nothing)
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) keys.load(p.cache, &p.tk, dst + i * C::TILE, &m.k_full[s], x.hkv, keys.next(p.cache, 602));
       }
     }
     for (int i = max(0, kc - C::PAIRS); ok && i < kc; ++i) ok = mbar_wait_warp(&m.k_empty[i % C::PAIRS], (i / C::PAIRS) & 1, abort_flag, 611);
@@ -519,11 +518,12 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
 
   if (warp == 0) {
     // ---------------------------------------------------------------- copies of K: slot 4 (piece % SETS) + tile
-    PageWindow win;
+    PagedStream<D> keys(p.cache);
     uint32_t used = 0;                                        // slots that were filled before
     uint32_t parity = 0;                                      // of the next wait for them
     while (ok && walk.next(x)) {
       const int n = walk.tiles(x);
+      keys.begin(p.cache, x.b, x.kt * kWeighKeys, x.seq.len);
       for (int a = 0; ok && a < n; ++a) {
         const int s = 4 * (kc % SETS) + a;
         if (used >> s & 1u) {
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
           parity ^= 1u << s;
         }
         used |= 1u << s;
-        load_paged_tile<D>(p.cache, win, &p.tk, m.k + s * C::TILE, &m.k_full[s], x.b, x.hkv, x.kt * kWeighKeys + a * 128, x.seq.len, 602);
+        keys.load(p.cache, &p.tk, m.k + s * C::TILE, &m.k_full[s], x.hkv, keys.next(p.cache, 602));
       }
       ++kc;
     }
@@ -728,7 +728,7 @@ static cudaError_t launch_weigh_d(const WeighArgs& a, cudaStream_t stream) {
   if (!make_map_bf16_tok(&p.tk, a.k_cache, D, a.H_kv, rows, 64, piece) ||
       !make_map_bf16_group(&p.tq, a.q, D, p.G, a.H_kv, a.total, 64, p.G, p.tokens))
     return cudaErrorInvalidValue;
-  p.cache = {a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks, piece};
+  p.cache = paged_cache(a.block_table, a.H_kv, a.num_blocks, a.block_size, a.max_blocks);
   p.lse = a.lse; p.weights = a.weights; p.part = a.part; p.cu = a.cu; p.seqlens = a.seqlens; p.weighed = a.weighed;
   p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
   p.c2 = a.scale * 1.4426950408889634f; p.decay = a.decay;
