@@ -844,6 +844,11 @@ fa_status_t fa_fwd_paged_tree(const fa_bf16_t* q, const fa_bf16_t* k_cache, cons
   if (st != FA_OK) return st;
   if (tree && (tree_words < 1 || 32LL * tree_words < max_seqlen_q))
     return fail(FA_ERR_INVALID_ARG, "a tree of %d words a token does not cover max_seqlen_q=%d", tree_words, max_seqlen_q);
+  // (groups of more heads than a row tile has rows count as more key heads)
+  const fa::TreeRows rows = fa::tree_rows(H, H_kv, max_seqlen_q);
+  const long long pairs = static_cast<long long>(n_seqs) * (H / rows.group);
+  if (pairs * (max_seqlen_k / 128 + 8) >= (1LL << 31) || pairs * ((rows.tiles + 1) / 2) >= (1LL << 30))
+    return fail(FA_ERR_UNSUPPORTED, "too many (sequence, heads of a row tile) pairs for these lengths");
   if (total == 0 || max_seqlen_q == 0) return FA_OK;
   if (!q || !k_cache || !v_cache || !o || !lse) return fail(FA_ERR_INVALID_ARG, "null pointer argument");
   for (const void* x : {static_cast<const void*>(q), static_cast<const void*>(k_cache), static_cast<const void*>(v_cache),
@@ -935,6 +940,7 @@ fa_status_t fa_evict_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, float* weight
   if (!aligned4(new_table) || !aligned4(kept) || !aligned4(seqlens_out))
     return fail(FA_ERR_INVALID_ARG, "new_table, kept and the new lengths must be 4-byte aligned");
   if (seqlens_out == seqlens_k || seqlens_out == budgets) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+  if (new_table == block_table) return fail(FA_ERR_INVALID_ARG, "the new pages need a table of their own, and must not be read from");
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
   fa::EvictArgs a{k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table, n_seqs, H_kv,
                   max_seqlen_k, max_kept, keep_first, keep_last, max_blocks_per_seq, new_max_blocks_per_seq, block_size, num_blocks, d};

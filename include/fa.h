@@ -524,7 +524,8 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
  * behind them; seqlens_out[b] = min(seqlens_k[b], budgets[b]) (an array of its own).  Rotation stays: later tokens
  * are appended by fa_append_paged_at.
  *
- * No new page may be one that a sequence of the call is read from; pages of block_table that sequences share are fine.
+ * No new page may be one that a sequence of the call is read from (new_table is not block_table); pages of block_table
+ * that sequences share are fine.
  * Device-side checks (fa_sync_status): a length outside [0, max_seqlen_k], a budget below 0, min(seqlens_k[b],
  * budgets[b]) above max_kept, or a budget below keep_first + keep_last of a sequence that exceeds it leave the
  * sequence as it is, with its length and a kept of -1; a block id outside [0, num_blocks) leaves out its tokens.

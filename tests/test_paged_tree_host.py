@@ -52,7 +52,7 @@ def test_a_step_refuses(lib, what, kw, code):
     (dict(words=0), INVALID), (dict(total=40, max_q=33), INVALID), (dict(tree=FAKE + 2), INVALID), (dict(o=None), INVALID),
     (dict(vc=None), INVALID), (dict(vc=FAKE + 4), INVALID), (dict(o=FAKE + 8), INVALID), (dict(ws=None), WORKSPACE),
     (dict(ws=FAKE + 8), WORKSPACE), (dict(ws_bytes=100), WORKSPACE), (dict(total=0, max_q=0, q=None, ws=None), OK),
-    (dict(max_q=0, o=None), OK),
+    (dict(max_q=0, o=None), OK), (dict(H=1031, H_kv=1, n_seqs=200000), UNSUPPORTED),
 ])
 def test_tree_refuses_more(lib, kw, code):
     assert call(lib.fa_fwd_paged_tree, TREE, STEP, kw) == code
@@ -95,7 +95,7 @@ def test_accept_refuses(lib, kw, code):
     assert call(lib.fa_accept_paged, "kc vc out path n cu lens table n_seqs H_kv deep max_blocks block num_blocks d", ACCEPT, kw) == code
 
 
-EVICT = dict(kc=FAKE, vc=FAKE, weights=FAKE, kept=FAKE, out=FAKE, budgets=FAKE + 128, lens=FAKE + 64, table=FAKE, new=FAKE, n_seqs=2, H_kv=2,
+EVICT = dict(kc=FAKE, vc=FAKE, weights=FAKE, kept=FAKE, out=FAKE, budgets=FAKE + 128, lens=FAKE + 64, table=FAKE, new=FAKE + 256, n_seqs=2, H_kv=2,
              max_k=500, max_kept=100, first=4, last=10, max_blocks=8, new_blocks=2, block=64, num_blocks=16, d=64)
 
 
@@ -105,7 +105,7 @@ EVICT = dict(kc=FAKE, vc=FAKE, weights=FAKE, kept=FAKE, out=FAKE, budgets=FAKE +
     (dict(new_blocks=-1), INVALID), (dict(new_blocks=1 << 26), UNSUPPORTED), (dict(d=100), UNSUPPORTED), (dict(weights=None), INVALID),
     (dict(weights=FAKE + 8), INVALID), (dict(kept=None), INVALID), (dict(new=None), INVALID), (dict(new=FAKE + 2), INVALID),
     (dict(out=None), INVALID), (dict(out=FAKE + 64), INVALID), (dict(out=FAKE + 128), INVALID), (dict(budgets=None), INVALID),
-    (dict(kc=FAKE + 2), INVALID), (dict(num_blocks=1 << 26), UNSUPPORTED),
+    (dict(kc=FAKE + 2), INVALID), (dict(num_blocks=1 << 26), UNSUPPORTED), (dict(new=FAKE), INVALID),
 ])
 def test_evict_refuses(lib, kw, code):
     order = "kc vc weights kept out budgets lens table new n_seqs H_kv max_k max_kept first last max_blocks new_blocks block num_blocks d"
