@@ -58,9 +58,6 @@ struct TreeCfg {
   static constexpr uint32_t T_S = 0, T_O = 256, T_X = 384;    // T_X: exchanged maxima and sums (NT = 1)
   static constexpr int THREADS = 384;
   static constexpr int STATE = 32 * (D + 3);                  // of 32 rows: each column, reference, sum, rounded sum
-  // NT = 2: launched with 168 registers a thread, moved from the control warps
-  static constexpr uint32_t REG_CTRL = 80, REG_SOFTMAX = 208;
-  static constexpr int REG_NEED = NT == 2 ? 128 * (static_cast<int>(REG_CTRL) + 2 * static_cast<int>(REG_SOFTMAX)) : 0;
   // named barriers: start, hand-off of P by S buffer, pairs of warps (NT = 1)
   static constexpr uint32_t BAR_START = 1, BAR_P = 2, BAR_PAIR = 4;
   static constexpr uint32_t BAR_P_THREADS = (NT == 1 ? 256 : 128) + 32 + 32;
@@ -377,16 +374,27 @@ __device__ __forceinline__ void tree_softmax_masked(uint32_t t_s, uint32_t t_o, 
 // its rounding could matter (the tile is then done by the form above).
 template <int D>
 __device__ __forceinline__ bool tree_softmax_plain(uint32_t t_s, uint32_t t_o, bool first, bool valid, float c2, TreeRow& r) {
-  float s[128];
+  // Weights are formed by a loop of two halves, the second one read again: less code (16 sequences of 1 to 60 tokens over
+  // 500 to 8188, all 128 scores held and no loop: 92.8 us, this way 89; 4 x 512 tokens over 16384: 398 and 396), and no registers have to be moved to
+  // these warps, which left the others too few (then 85 and 385).
+  float s[64];
+  auto load = [&](int k) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    uint32_t rr[32];
-    tmem_ld32(t_s + k * 32, rr);
+    for (int y = 0; y < 2; ++y) {
+      uint32_t rr[32];
+      tmem_ld32(t_s + 64 * k + 32 * y, rr);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) s[k * 32 + i] = __uint_as_float(rr[i]);
+      for (int i = 0; i < 32; ++i) s[32 * y + i] = __uint_as_float(rr[i]);
+    }
+    tmem_wait_ld();
+  };
+  float cand = r.m;
+#pragma unroll
+  for (int k = 1; k >= 0; --k) {                              // (half 0 stays)
+    load(k);
+#pragma unroll
+    for (int y = 0; y < 2; ++y) cand = fmaxf(cand, max32(s + 32 * y));
   }
-  tmem_wait_ld();
-  const float cand = fmaxf(r.m, fmaxf(fmax3(max32(s), max32(s + 32), max32(s + 64)), max32(s + 96)));
   bool any;
   const float alpha = r.follow(cand, c2, valid, &any);
   if (any) {
@@ -398,18 +406,19 @@ __device__ __forceinline__ bool tree_softmax_plain(uint32_t t_s, uint32_t t_o, b
   float2 rs[2], hs[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) rs[k] = hs[k] = make_float2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
   for (int h = 0; h < 2; ++h) {
+    if (h) load(h);
     uint32_t pk[32];
 #pragma unroll
     for (int k = 0; k < 32; ++k) {
-      const float2 x = ffma2(make_float2(s[64 * h + 2 * k], s[64 * h + 2 * k + 1]), c2v, nms);
+      const float2 x = ffma2(make_float2(s[2 * k], s[2 * k + 1]), c2v, nms);
       const float2 e = make_float2(fast_exp2(x.x), fast_exp2(x.y));
       pk[k] = pack_bf16x2(e.x, e.y);
       rs[k & 1] = fadd2(rs[k & 1], e);
       hs[k & 1] = add_bf16x2_f32(hs[k & 1], pk[k]);
     }
-    tmem_st32(t_s + h * 32, pk);
+    tmem_st32(t_s + 32 * h, pk);
   }
   const float2 sum = fadd2(rs[0], rs[1]), sumh = fadd2(hs[0], hs[1]);
   r.l += sum.x + sum.y;
@@ -564,7 +573,6 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
   auto at_v = [&](int g, int j, int n) { return NT == 2 ? g + 2 * j + 1 : j + 1 < n ? g + 2 * j + 2 : g + 2 * n - 1; };
 
   if (warp < 4) {
-    if constexpr (NT == 2) setmaxnreg_dec<C::REG_CTRL>();
     if (warp == 0) {
       // -------------------------------------------------------------- copies
       bool ok = true;
@@ -734,7 +742,6 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
     }
   } else {
     // ---------------------------------------------------------------- softmax
-    if constexpr (NT == 2) setmaxnreg_inc<C::REG_SOFTMAX>();
     const int wg = (warp - 4) >> 2;                           // NT = 2: row tile; NT = 1: half of the keys, and of O's columns
     const int t = NT == 2 ? wg : 0, half = NT == 1 ? wg : 0;
     constexpr int COLS = NT == 2 ? D : D / 2;                 // columns of O that a thread writes
@@ -1088,7 +1095,7 @@ static cudaError_t launch_attend_tree_d(const PagedTreeArgs& a, const TreeRows& 
   p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
   p.c2 = a.scale * 1.4426950408889634f;
   static int attr_done[64] = {0};
-  cudaError_t e = ensure_smem_attr(attend_tree_kernel<D, NT>, C::SMEM_BYTES, attr_done, C::THREADS, C::REG_NEED);
+  cudaError_t e = ensure_smem_attr(attend_tree_kernel<D, NT>, C::SMEM_BYTES, attr_done);
   if (e != cudaSuccess) return e;
   const int sms = min(paged_sm_count(), kTreeMaxCtas);
   const long long pairs = static_cast<long long>(a.n_seqs) * p.heads;
