@@ -15,7 +15,8 @@
 // without the list between them, was slower as a whole (123 us for that batch, 91 this way).
 //
 // Accept.  Rows move down: token i of the path, at place a_i >= i of the step's, comes to place i.  A thread takes 16
-// bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.
+// bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.  It is bound by the chain
+// of path, page and row: 4 trees of 26 tokens 3.7 us, 128 of 64 5.7.
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
 

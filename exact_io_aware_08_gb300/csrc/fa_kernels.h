@@ -254,15 +254,17 @@ inline size_t tree_part_bytes(int H, int H_kv, int max_q, int d) {
   return (2 * kTreeMaxCtas * static_cast<size_t>(t.state_rows) * (d + 3) + kTreeMaxCtas + 8) * sizeof(float);
 }
 
-// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each.  Several tiles are shared out to at most
-// kWeighMaxCtas CTAs, 512 keys at a time, which keep the sums of at most two cut pieces each.
+// Weights of cached tokens: rows in tiles of whole tokens, up to 128 rows each.  More than kWeighFewTiles are shared out
+// to at most kWeighMaxCtas CTAs, 512 keys at a time, which keep the sums of at most two cut pieces each.
 constexpr int kWeighMaxCtas = 152;
 inline int weigh_tokens(int H, int H_kv, int max_q) {
   const int t = 128 / (H / H_kv);
   return t < max_q ? t : max_q < 1 ? 1 : max_q;
 }
+constexpr int kWeighFewTiles = 3;
+inline bool weigh_few(int tokens, int max_q) { return max_q <= kWeighFewTiles * tokens; }
 inline size_t weigh_part_bytes(int H, int H_kv, int max_q) {
-  return weigh_tokens(H, H_kv, max_q) >= max_q ? 16 : 2 * kWeighMaxCtas * size_t(512) * sizeof(float);
+  return weigh_few(weigh_tokens(H, H_kv, max_q), max_q) ? 16 : 2 * kWeighMaxCtas * size_t(512) * sizeof(float);
 }
 
 cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);

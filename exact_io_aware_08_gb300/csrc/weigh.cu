@@ -15,11 +15,16 @@
 //                Q is given back when its products are done, its lse when it has been added up.
 //   warp 1       issues the products.
 //   warps 4 on   the sums, thread = key.
-// Few rows (one tile of them): Q stays, each CTA gets an equal share of all keys (Q4Share), 256 at a time with two S
-// buffers for each half.  Else a CTA keeps 512 keys and runs over the rows that see them, four tiles of keys by turns, so
-// that a tile of Q is brought for 512 keys and the sums of one key tile run beside the products of the others.  The (512
-// keys, row tile) units are shared out equally too; the sums of 512 keys that lie in several shares are added up, in
-// order, by a second kernel.  (2 x 4096 tokens in whole ranges of row tiles, dealt out in rounds: 152 us.)
+// Few rows (up to three tiles of them): Q stays, each CTA gets an equal share of all keys (Q4Share), 256 at a time with two
+// S buffers for each half.  (By the kernel for many rows: two tiles, 32 x 64 tokens over 500 keys 31 us, this way 23; three,
+// 4 x 90 over 1000 18 and 15, but 16 x 96 over 8000 both 110.)  Else a CTA keeps 512 keys and runs over the rows that see
+// them, four tiles of keys by turns, so that a tile of Q is brought for 512 keys and the sums of one key tile run beside
+// the products of the others.  The (512 keys, row tile) units are shared out equally too; the sums of 512 keys that lie in
+// several shares are added up, in order, by a second kernel.  (2 x 4096 tokens in whole ranges of row tiles, dealt out in
+// rounds: 152 us.)
+//
+// Measured, 32 heads over 8, d = 128: 32 single tokens over 100 to 8191 61 us (5.5 TB/s of keys and weights), 16 x 64
+// tokens over 8000 82, 2 prompts of 4096 115 (1.2 PFLOP/s; 95 without the sums).
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
 
@@ -30,7 +35,7 @@ struct WeighCfg {
   static constexpr int TILE = 128 * D * 2;
   static constexpr int CHUNK = 128 * 128;
   static constexpr int NK = D == 128 ? 4 : 8;                 // K tiles
-  static constexpr int NQ = 3;                                // tiles of Q
+  static constexpr int NQ = kWeighFewTiles;                   // tiles of Q
   static constexpr int OFF_K = 0;
   static constexpr int OFF_Q = NK * TILE;
   static constexpr int OFF_LSE = OFF_Q + NQ * TILE;
@@ -69,7 +74,7 @@ __device__ __forceinline__ int weigh_pairs(const PagedSeq& s) { return s.nq ? (s
 
 // Few rows: a stretch of key pairs [kt0, kt1) of a key head of a sequence.
 struct WeighStretch {
-  int b, hkv, kt0, kt1, weighed;
+  int b, hkv, kt0, kt1, tiles;                                // (row tiles)
   PagedSeq seq;
 };
 struct WeighWalk {
@@ -88,6 +93,7 @@ struct WeighWalk {
     }
     x.b = b;
     x.seq = seq;
+    x.tiles = (seq.nq + p.tokens - 1) / p.tokens;
     x.hkv = off / pairs;
     x.kt0 = off - x.hkv * pairs;
     const int n = min(left, pairs - x.kt0);
@@ -295,42 +301,49 @@ struct WeighSpan {
   }
 };
 
-// Adds up the weights of a tile's columns, 32 from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e.  ``read`` is
+// Adds up the weights of a tile's columns, W from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e.  ``read`` is
 // called when all has been read, before the last of it is added up.
-template <typename F>
+template <int W, typename F>
 __device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restrict__ nl, int cols, const WeighSpan& x, float c2, F read) {
-  float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  float2 sum[W / 16];
+#pragma unroll
+  for (int i = 0; i < W / 16; ++i) sum[i] = make_float2(0.f, 0.f);
   const float2 c = make_float2(c2, c2);
 #pragma unroll 1
-  for (int c0 = 0; c0 < cols; c0 += 32) {
-    uint32_t s[32];
-    tmem_ld32(t_s + c0, s);
+  for (int c0 = 0; c0 < cols; c0 += W) {
+    uint32_t s[W / 32][32];
+#pragma unroll
+    for (int y = 0; y < W / 32; ++y) tmem_ld32(t_s + c0 + 32 * y, s[y]);
     tmem_wait_ld();
-    if (c0 + 32 >= cols) {
+    if (c0 + W >= cols) {
       tc_fence_before();
       __syncwarp();
       read();
     }
-    if (c0 + 32 <= x.lo_min || c0 >= x.hi) continue;
-    if (c0 < x.lo_max || c0 + 32 > x.hi) {
+    if (c0 + W <= x.lo_min || c0 >= x.hi) continue;
+    if (c0 < x.lo_max || c0 + W > x.hi) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float e = fast_exp2(fmaf(__uint_as_float(s[i]), c2, nl[c0 + i]));
-        sum[i & 1].x += c0 + i >= x.lo && c0 + i < x.hi ? e : 0.f;
+      for (int i = 0; i < W; ++i) {
+        const float e = fast_exp2(fmaf(__uint_as_float(s[i / 32][i % 32]), c2, nl[c0 + i]));
+        sum[i % (W / 16)].x += c0 + i >= x.lo && c0 + i < x.hi ? e : 0.f;
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; i += 4) {
+      for (int i = 0; i < W; i += 4) {
         const float4 n = *reinterpret_cast<const float4*>(nl + c0 + i);
-        const float2 u = ffma2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c, make_float2(n.x, n.y));
-        const float2 v = ffma2(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), c, make_float2(n.z, n.w));
-        sum[0] = fadd2(sum[0], make_float2(fast_exp2(u.x), fast_exp2(u.y)));
-        sum[1] = fadd2(sum[1], make_float2(fast_exp2(v.x), fast_exp2(v.y)));
+        const uint32_t* v4 = &s[i / 32][i % 32];
+        const float2 u = ffma2(make_float2(__uint_as_float(v4[0]), __uint_as_float(v4[1])), c, make_float2(n.x, n.y));
+        const float2 v = ffma2(make_float2(__uint_as_float(v4[2]), __uint_as_float(v4[3])), c, make_float2(n.z, n.w));
+        sum[i / 2 % (W / 16)] = fadd2(sum[i / 2 % (W / 16)], make_float2(fast_exp2(u.x), fast_exp2(u.y)));
+        sum[(i / 2 + 1) % (W / 16)] = fadd2(sum[(i / 2 + 1) % (W / 16)], make_float2(fast_exp2(v.x), fast_exp2(v.y)));
       }
     }
   }
-  const float2 t = fadd2(sum[0], sum[1]);
-  return t.x + t.y;
+#pragma unroll
+  for (int i = W / 32; i >= 1; i /= 2)
+#pragma unroll
+    for (int y = 0; y < i; ++y) sum[y] = fadd2(sum[y], sum[y + i]);
+  return sum[0].x + sum[0].y;
 }
 
 template <int D>
@@ -394,74 +407,87 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
       for (int i = max(0, kc - C::PAIRS); i < kc; ++i) mbar_wait_warp(&m.k_full[i % C::PAIRS], (i / C::PAIRS) & 1, nullptr, 612);
   } else if (warp == 2) {
     // ---------------------------------------------------------------- copies of Q
-    while (ok && walk.next(x)) {
-      const int s = qc % C::NQ, u = qc / C::NQ;
-      if (u > 0 && !(ok = mbar_wait_warp(&m.q_empty[s], (u - 1) & 1, abort_flag, 613))) break;
-      if (lane == 0) weigh_load_q<D>(p, m, s, x.hkv, x.seq.first);
-      __syncwarp();
-      ++qc;
-    }
+    while (ok && walk.next(x))
+      for (int r = 0; r < x.tiles; ++r, ++qc) {
+        const int s = qc % C::NQ, u = qc / C::NQ;
+        if (u > 0 && !(ok = mbar_wait_warp(&m.q_empty[s], (u - 1) & 1, abort_flag, 613))) break;
+        if (lane == 0) weigh_load_q<D>(p, m, s, x.hkv, x.seq.first + r * p.tokens);
+        __syncwarp();
+      }
     for (int i = max(0, qc - C::NQ); ok && i < qc; ++i) ok = mbar_wait_warp(&m.q_empty[i % C::NQ], (i / C::NQ) & 1, abort_flag, 614);
     if (!ok)
       for (int i = max(0, qc - C::NQ); i < qc; ++i) mbar_wait_warp(&m.q_full[i % C::NQ], (i / C::NQ) & 1, nullptr, 615);
   } else if (warp == 3) {
     // ---------------------------------------------------------------- lse
     WeighLse lse(p);
-    while (ok && walk.next(x)) {
-      const int s = qc % C::NQ, u = qc / C::NQ;
-      lse.ask(x.seq, x.hkv, 0, lse.e);
-      if (u > 0 && !(ok = mbar_wait_warp(&m.l_empty[s], (u - 1) & 1, abort_flag, 616))) break;
-      lse.write(m.lse + s * 128);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&m.l_full[s]);
-      ++qc;
-    }
+    while (ok && walk.next(x))
+      for (int r = 0; r < x.tiles; ++r, ++qc) {
+        const int s = qc % C::NQ, u = qc / C::NQ;
+        lse.ask(x.seq, x.hkv, r, lse.e);
+        if (u > 0 && !(ok = mbar_wait_warp(&m.l_empty[s], (u - 1) & 1, abort_flag, 616))) break;
+        lse.write(m.lse + s * 128);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.l_full[s]);
+      }
   } else if (warp == 1) {
     // ---------------------------------------------------------------- products
     const uint32_t idesc = idesc_bf16_f32(128, (p.rows + 15) / 16 * 16, 0, 0);
     const uint64_t dk0 = smem_desc_sw128(smem_u32(m.k), 0, 1024);
     const uint64_t dq0 = smem_desc_sw128(smem_u32(m.q), 0, 1024);
+    int sc = 0;                                               // products of each tile of a pair so far
     while (ok && walk.next(x)) {
-      ok = mbar_wait_warp(&m.q_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 621);
+      for (int r = 0; ok && r < x.tiles; ++r) ok = mbar_wait_warp(&m.q_full[(qc + r) % C::NQ], ((qc + r) / C::NQ) & 1, abort_flag, 621);
       for (int kt = x.kt0; ok && kt < x.kt1; ++kt, ++kc) {
         ok = mbar_wait_warp(&m.k_full[kc % C::PAIRS], (kc / C::PAIRS) & 1, abort_flag, 620);
+        for (int r = 0; ok && r < x.tiles; ++r, ++sc) {
 #pragma unroll
-        for (int a = 0; a < 2; ++a) {
-          const int buf = 2 * a + (kc & 1);
-          if (ok && kc >= 2) ok = mbar_wait_warp(&m.s_empty[buf], ((kc >> 1) - 1) & 1, abort_flag, 622);
-          if (!ok) break;
-          tc_fence_after();
-          weigh_product<D>(tbase + buf * 128, desc_advance(dk0, ((kc % C::PAIRS) * 2 + a) * C::TILE), desc_advance(dq0, (qc % C::NQ) * C::TILE),
-                           idesc, &m.s_full[buf]);
+          for (int a = 0; a < 2; ++a) {
+            const int buf = 2 * a + (sc & 1);
+            if (ok && sc >= 2) ok = mbar_wait_warp(&m.s_empty[buf], ((sc >> 1) - 1) & 1, abort_flag, 622);
+            if (!ok) break;
+            tc_fence_after();
+            weigh_product<D>(tbase + buf * 128, desc_advance(dk0, ((kc % C::PAIRS) * 2 + a) * C::TILE),
+                             desc_advance(dq0, ((qc + r) % C::NQ) * C::TILE), idesc, &m.s_full[buf]);
+          }
         }
         if (ok) umma_commit_w(&m.k_empty[kc % C::PAIRS]);
       }
-      if (ok) umma_commit_w(&m.q_empty[qc % C::NQ]);
-      ++qc;
+      for (int r = 0; r < x.tiles; ++r, ++qc)
+        if (ok) umma_commit_w(&m.q_empty[qc % C::NQ]);
     }
   } else {
     // ---------------------------------------------------------------- sums
     const int a = (warp - 4) >> 2, sub = warp & 3;
     const uint32_t t_lane = tbase + (static_cast<uint32_t>(sub * 32) << 16);
     const int cols = (p.rows + 31) / 32 * 32;
+    int sc = 0;
     while (ok && walk.next(x)) {
       const int weighed = p.weighed ? __ldg(p.weighed + x.b) : x.seq.base();
-      const float* lse = m.lse + (qc % C::NQ) * 128;
-      if (!(ok = mbar_wait_warp(&m.l_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 630))) break;
-      for (int kt = x.kt0; ok && kt < x.kt1; ++kt, ++kc) {
-        const int key = kt * 256 + a * 128 + sub * 32 + lane, buf = 2 * a + (kc & 1);
+      for (int r = 0; ok && r < x.tiles; ++r) ok = mbar_wait_warp(&m.l_full[(qc + r) % C::NQ], ((qc + r) / C::NQ) & 1, abort_flag, 630);
+      for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
+        const int key = kt * 256 + a * 128 + sub * 32 + lane;
         float* at = key < x.seq.len ? weigh_place(p, x.b, x.hkv, key) : nullptr;
         const float old = at && key < weighed ? *at * p.decay : 0.f;
-        if (!(ok = mbar_wait_warp(&m.s_full[buf], (kc >> 1) & 1, abort_flag, 631))) break;
-        tc_fence_after();
-        const float sum = weigh_tile(t_lane + buf * 128, lse, cols, WeighSpan(p, x.seq, key, 0, x.seq.nq * p.G), p.c2, [&] {
-          if (lane == 0) mbar_arrive(&m.s_empty[buf]);
-        });
-        if (at) *at = old + sum;
+        float sum = 0.f;
+        for (int r = 0; r < x.tiles; ++r, ++sc) {
+          const int buf = 2 * a + (sc & 1);
+          if (!(ok = mbar_wait_warp(&m.s_full[buf], (sc >> 1) & 1, abort_flag, 631))) break;
+          tc_fence_after();
+          const int r0 = r * p.rows;
+          const float* nl = m.lse + ((qc + r) % C::NQ) * 128;
+          const WeighSpan span(p, x.seq, key, r0, min(p.rows, x.seq.nq * p.G - r0));
+          auto read = [&] {
+            if (lane == 0) mbar_arrive(&m.s_empty[buf]);
+          };
+          // (64 columns at a time where there are as many: 16 x 64 tokens over 8000 87 us with 32, 82 with 64, 140 with 128;
+          // 32 single tokens, four columns, 62 with 32 and 68 with 64)
+          sum += cols > 32 ? weigh_tile<64>(t_lane + buf * 128, nl, cols, span, p.c2, read) : weigh_tile<32>(t_lane + buf * 128, nl, cols, span, p.c2, read);
+        }
+        if (at && ok) *at = old + sum;
       }
       __syncwarp();
-      if (lane == 0 && ok) mbar_arrive(&m.l_empty[qc % C::NQ]);
-      ++qc;
+      for (int r = 0; r < x.tiles; ++r, ++qc)
+        if (lane == 0 && ok) mbar_arrive(&m.l_empty[qc % C::NQ]);
     }
   }
   __syncwarp();
@@ -635,7 +661,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
           }
           tc_fence_after();
           const int r0 = qt * p.tokens * p.G, rows = min(p.tokens, x.seq.nq - qt * p.tokens) * p.G;
-          sum += weigh_tile(t_s, m.lse + (qc % C::NQ) * 128, cols, WeighSpan(p, x.seq, key, r0, rows), p.c2,
+          sum += weigh_tile<32>(t_s, m.lse + (qc % C::NQ) * 128, cols, WeighSpan(p, x.seq, key, r0, rows), p.c2,
                             [&] { named_bar_arrive(C::BAR_S + a, C::BAR_S_THREADS); });
         } else {
           ok = ok && mbar_wait_warp(&m.l_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 632);
@@ -732,7 +758,7 @@ static cudaError_t launch_weigh_d(const WeighArgs& a, cudaStream_t stream) {
   p.lse = a.lse; p.weights = a.weights; p.part = a.part; p.cu = a.cu; p.seqlens = a.seqlens; p.weighed = a.weighed;
   p.n_seqs = a.n_seqs; p.H = a.H; p.total = a.total; p.max_q = a.max_q; p.max_k = a.max_k;
   p.c2 = a.scale * 1.4426950408889634f; p.decay = a.decay;
-  const bool few = p.tokens >= a.max_q;
+  const bool few = weigh_few(p.tokens, a.max_q);
   static int few_done[64] = {0}, many_done[64] = {0};
   cudaError_t e = few ? ensure_smem_attr(weigh_few_kernel<D>, C::SMEM_BYTES, few_done) : ensure_smem_attr(weigh_many_kernel<D>, C::SMEM_BYTES, many_done);
   if (e != cudaSuccess) return e;

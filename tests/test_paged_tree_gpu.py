@@ -322,6 +322,9 @@ WEIGHS = [
     ([1000, 3, 0, 600], [1000, 9, 50, 4000], 8, 2, 128, 64, [0, 9, 5, 100], 0.5),      # ranges of rows
     ([1100], [1300], 2, 2, 64, 64, None, 1.0),
     ([700, 650], [1400, 650], 100, 1, 64, 16, None, 1.0),                             # a token a tile
+    ([96, 1, 33, 0, 64, 32] * 12, [31 * i + 96 for i in range(72)], 16, 4, 128, 64, None, 0.98),   # up to three tiles of rows
+    ([90, 7], [9000, 4000], 8, 2, 64, 32, [0, 1000], 0.5),
+    ([97, 1], [3000, 1], 8, 2, 128, 64, None, 1.0),                                   # one more
 ]
 
 

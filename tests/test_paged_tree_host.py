@@ -76,8 +76,8 @@ def test_tree_workspace_size(lib):
 
 def test_weigh_workspace_size(lib):
     size = lib.fa_weigh_paged_workspace_size
-    assert size(8, 2, 1) == size(8, 2, 32) == 16                 # one tile of rows
-    assert size(8, 2, 33) == size(32, 8, 4096) == 2 * 152 * 512 * 4
+    assert size(8, 2, 1) == size(8, 2, 96) == 16                 # up to three tiles of rows
+    assert size(8, 2, 97) == size(32, 8, 4096) == 2 * 152 * 512 * 4
     assert size(8, 3, 1) == size(130, 1, 1) == size(8, 2, -1) == size(0, 1, 1) == 0
 
 
