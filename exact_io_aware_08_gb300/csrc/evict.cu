@@ -10,9 +10,9 @@
 //
 // What bounds it: the copy is bound by HBM (16 sequences of 10000 to 16384 tokens, 8 heads of 128, 1024 to 4096 of them
 // kept: 61 us for about 330 MB read and written); the selection, 4 bytes a token, by latencies: four passes over the keys (from shared memory, up
-// to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 29 for 16384).  Three passes of 11, 11 and 10
-// bits with equal digits of a warp counted together were no faster (13 and 33 us), and choosing in every block that copies,
-// without the list between them, was slower as a whole (123 us for that batch, 91 this way).
+// to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 25 for 16384).  Counts of each lane's own, or three
+// passes of 11, 11 and 10 bits with equal digits of a warp counted together, were no faster, and choosing in every block
+// that copies, without the list between them, was slower as a whole (123 us for that batch, 91 with the list at the time).
 //
 // Accept.  Rows move down: token i of the path, at place a_i >= i of the step's, comes to place i.  A thread takes 16
 // bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.  It is bound by the chain
@@ -93,11 +93,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
   }
   // candidates are tokens [keep_first, keep_first + c), of which k stay
   const int c = len - p.keep_first - p.keep_last, k = n - p.keep_first - p.keep_last;
+  // Candidate i's key: the lowest where there is no page (reported where the row is copied).
   auto weight = [&](int i) {
     const int pos = p.keep_first + i, blk = pos / p.block_size;
     const int page = __ldg(p.table + static_cast<size_t>(b) * p.max_blocks + blk);
-    if (page < 0 || page >= p.num_blocks) return 0u;          // (reported where the row is copied)
-    return weight_key(p.weights[(static_cast<size_t>(page) * p.H_kv + h) * p.block_size + (pos - blk * p.block_size)]);
+    if (page < 0 || page >= p.num_blocks) return 0u;
+    return weight_key(p.weights[(page * p.H_kv + h) * p.block_size + (pos - blk * p.block_size)]);   // (below 2^31)
   };
   const bool hold = c <= p.held;
   if (hold)
@@ -128,11 +129,12 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     border |= static_cast<uint32_t>(digit[0]) << shift;
     want -= digit[1];
   }
-  // ``want`` of those at the border stay, the first ones.  A thread takes consecutive candidates.
+  // ``want`` of those at the border stay, the first ones.  A thread takes consecutive candidates, an odd number of them
+  // (an even one met in few banks of shared memory: 32768 tokens 65 us, this way 40).
   for (int i = threadIdx.x; i < p.keep_first; i += kSelectThreads) kept[i] = i;
   for (int i = threadIdx.x; i < p.keep_last; i += kSelectThreads) kept[n - p.keep_last + i] = len - p.keep_last + i;
   if (k == 0) return;
-  const int per = (c + kSelectThreads - 1) / kSelectThreads;
+  const int per = (c + kSelectThreads - 1) / kSelectThreads | 1;
   const int i0 = min(c, static_cast<int>(threadIdx.x) * per), i1 = min(c, i0 + per);
   int over = 0, at = 0;
   for (int i = i0; i < i1; ++i) {
