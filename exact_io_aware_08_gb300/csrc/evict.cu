@@ -9,10 +9,11 @@
 // by lanes of 16 bytes.
 //
 // What bounds it: the copy is bound by HBM (16 sequences of 10000 to 16384 tokens, 8 heads of 128, 1024 to 4096 of them
-// kept: 61 us for about 330 MB read and written); the selection, 4 bytes a token, by latencies: four passes over the keys (from shared memory, up
-// to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 25 for 16384).  Counts of each lane's own, or three
-// passes of 11, 11 and 10 bits with equal digits of a warp counted together, were no faster, and choosing in every block
-// that copies, without the list between them, was slower as a whole (123 us for that batch, 91 with the list at the time).
+// kept: 61 us for about 330 MB read and written); the selection, 4 bytes a token, by latencies: four passes over the keys
+// (from shared memory, up to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 25 for 16384).  Counts
+// of each lane's own, or three passes of 11, 11 and 10 bits with equal digits of a warp counted together, were no faster,
+// and choosing in every block that copies, without the list between them, was slower as a whole (123 us for that batch,
+// 91 with the list at the time).
 //
 // Accept.  Rows move down: token i of the path, at place a_i >= i of the step's, comes to place i.  A thread takes 16
 // bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.  It is bound by the chain

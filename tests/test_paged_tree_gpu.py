@@ -204,6 +204,42 @@ def test_values_that_are_no_numbers_in_many_sequences():
         np.testing.assert_array_equal(np.delete(o[at][sees], 100, -1), np.delete(clean[at][sees], 100, -1))
 
 
+@pytest.mark.parametrize("case,more", [(STEPS[2], 40), (STEPS[7], 300), (STEPS[12], 500), (STEPS[16], 1000)], ids=lambda x: str(x)[:8])
+def test_loose_maxima_and_guards(case, more):
+    """Maxima above the lengths (other tile counts, empty row blocks), and bytes around the outputs and the workspaces."""
+    require_gpu()
+    new, lens, H, H_kv, d, block, kind, _ = case
+    s = Step(new, lens, H, H_kv, d, block, kind, more)
+    s.max_q, s.max_k = min(s.total, s.max_q + more), min(s.max_k + more, s.table.shape[1] * block)
+    if s.tree is not None:
+        s.tree = np.pad(s.tree, ((0, 0), (0, -(-s.max_q // 32) - s.tree.shape[1])))
+    o, lse = s.attend()
+    s.check(o, lse)
+    q, k, v, table, cu, ln = s.gpu()
+    size = fa.fa_fwd_paged_tree_workspace_size(H, H_kv, s.max_q, d)
+    room, pad = [size, o.numel() * 2, lse.numel() * 4], 256
+    held = [torch.full((pad + -(-n // 16) * 16 + pad,), 0xA5, dtype=torch.uint8, device="cuda") for n in room]
+    ws, og, lg = (x[pad:pad + n] for x, n in zip(held, room))
+    fa.fa_fwd_paged_tree(q, k, v, og.view(torch.bfloat16).view(o.shape), lg.view(torch.float32).view(lse.shape), None if s.tree is None else i32(s.tree),
+                         cu, ln, table, s.max_q, s.max_k, s.scale, ws)
+    size = fa.fa_weigh_paged_workspace_size(H, H_kv, s.max_q)
+    held.append(torch.full((pad + size + pad,), 0xA5, dtype=torch.uint8, device="cuda"))
+    room.append(size)
+    rows = lse.clone()
+    rows[:, s.cu[-1]:] = 0
+    w = torch.zeros((s.nb, H_kv, block), device="cuda")
+    fa.fa_weigh_paged(q, rows, k, w, None, cu, ln, table, s.max_q, s.max_k, s.scale, 1.0, held[3][pad:pad + size])
+    fa.fa_sync_status()
+    n = s.cu[-1]
+    assert torch.equal(og.view(torch.int16).view(o.shape)[:n], o.view(torch.int16)[:n])
+    assert torch.equal(lg.view(torch.int32).view(lse.shape)[:, :n], lse.view(torch.int32)[:, :n])
+    for x, y in zip(held, room):
+        assert (x[:pad] == 0xA5).all() and (x[pad + y:] == 0xA5).all()
+    assert (og.view(o.shape[0], -1)[n:] == 0xA5).all()
+    if kind is None:                                              # (a row's weights sum to 1: each is off by some 2^-18 of itself at most)
+        assert abs(f64(w).sum() - n * H) <= n * H * 1e-4
+
+
 def test_long_caches_and_many_shares():
     require_gpu()
     s = Step([1, 3, 2], [70001, 5, 40000], 8, 2, 128, 64, "tree")
