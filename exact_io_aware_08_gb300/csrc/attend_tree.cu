@@ -311,6 +311,7 @@ struct TreeRow {
       lh *= alpha;
       m = cand;
     }
+    __syncwarp();                                             // (tensor memory is accessed by the whole warp at once)
     return alpha;
   }
 };
@@ -791,6 +792,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
               __threadfence_block();
             }
             fence_proxy_async_smem();
+            __syncwarp();
           }
           if constexpr (NT == 2) {
             if (ok && !idle) {
@@ -802,6 +804,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
               if (!done) {
                 uint32_t w[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
                 if (!plain && valid) tree_mask<4>(p, x.seq, token, k0, w);
+                __syncwarp();
                 tree_softmax_masked<D>(t_s, t_o, w, full_end - k0, x.key_end - k0, j == 0, valid, c2, r);
               }
             }
@@ -824,6 +827,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
 #pragma unroll
                 for (int k = 0; k < 64; ++k)
                   if (!(w[k >> 5] >> (k & 31) & 1u)) s[k] = -INFINITY;
+                __syncwarp();
               }
               top = fmaxf(max32(s), max32(s + 32));
               tmem_st1(t_lane + C::T_X + 2 * (hc & 1) + half, __float_as_uint(top));
@@ -889,6 +893,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
       const bool spoil = n > 0 && spoilt[2 * t + (mine & 1)] == mine;
       const size_t th = static_cast<size_t>(x.seq.first + token) * p.H + head;
       float* dst = x.slot < 0 ? nullptr : p.part + (static_cast<size_t>(x.slot) * (p.state_rows / 32) + t * 4 + sub) * C::STATE + lane;
+      // (lanes without a row write nothing, but come back for the next columns: all of a warp read tensor memory together)
 #pragma unroll 1
       for (int k = 0; k < COLS; k += 32) {
         const int col = half * COLS + k;
@@ -904,11 +909,10 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
 #pragma unroll
           for (int i = 0; i < 32; ++i) acc[i] = 0.f;
         }
-        if (!valid) continue;
-        if (dst) {
+        if (valid && dst) {
 #pragma unroll
           for (int i = 0; i < 32; ++i) dst[(col + i) * 32] = acc[i];
-        } else {
+        } else if (valid) {
           // (a row that sees nothing has sums of 0, and 0 here)
           uint4* out = reinterpret_cast<uint4*>(p.o + th * D + col);
 #pragma unroll
@@ -916,6 +920,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
             out[i / 8] = make_uint4(pack_bf16x2(acc[i] * inv, acc[i + 1] * inv), pack_bf16x2(acc[i + 2] * inv, acc[i + 3] * inv),
                                     pack_bf16x2(acc[i + 4] * inv, acc[i + 5] * inv), pack_bf16x2(acc[i + 6] * inv, acc[i + 7] * inv));
         }
+        __syncwarp();
       }
       if (valid && half == 0) {
         if (dst) {
@@ -927,6 +932,7 @@ __global__ void __launch_bounds__(TreeCfg<D, NT>::THREADS, 1) attend_tree_kernel
         }
       }
       // (what was read of O comes before the next item's first product, which the next hand-off lets go)
+      __syncwarp();
       tc_fence_before();
     }
   }

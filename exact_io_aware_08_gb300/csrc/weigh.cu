@@ -327,6 +327,7 @@ __device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restric
         const float e = fast_exp2(fmaf(__uint_as_float(s[i / 32][i % 32]), c2, nl[c0 + i]));
         sum[i % (W / 16)].x += c0 + i >= x.lo && c0 + i < x.hi ? e : 0.f;
       }
+      __syncwarp();                                           // (tensor memory is read by the whole warp at once)
     } else {
 #pragma unroll
       for (int i = 0; i < W; i += 4) {

@@ -187,6 +187,46 @@ def test_what_is_not_seen_does_not_count(case, where, value):
         assert (np.abs(got - want) <= bo).all() and (gl[none] == -np.inf).all() and (np.abs(gl[~none] - l[~none]) <= bl[~none]).all()
 
 
+@pytest.mark.parametrize("case", [
+    ([7, 9, 1], [700, 9, 257], 5, 1, 128, 16, "tree", 0),                  # 35, 45 and 5 rows: warps that rows fill in part
+    ([9, 30], [1009, 4000], 4, 1, 64, 64, "bits", 2),
+    ([21, 33, 5], [300, 2033, 5], 8, 1, 128, 64, "tree", 0),               # 168, 264 (shares) and 40 rows
+    ([77, 130, 3], [177, 1130, 259], 7, 1, 128, 48, None, 1),              # row blocks
+], ids=lambda c: f"{sum(c[0])}tok_{c[6]}")
+def test_values_that_are_no_numbers_beside_lanes_without_a_row(case):
+    """Warps in which some lanes have no row, some see a value that is no finite number and some do not, in every
+    block of columns: each row has what it sees, and every other result stays bit for bit."""
+    require_gpu()
+    s = Step(*case)
+    clean = [x.clone() for x in s.attend()]
+    G, d = s.H // s.H_kv, s.d
+    planted = []
+    for b, n in enumerate(s.new):
+        for i, c in enumerate(range(1, d, 15)):
+            j, value = (i * 5) % n, (NAN, float("inf"), -float("inf"))[i % 3]
+            p = s.lens[b] - n + j
+            s.v[s.table[b][p // s.block], p % s.block, :, c] = value
+            planted.append((b, j, c, value))
+    j = s.new[1] // 2                                                      # and two that meet in one column
+    for k, value in ((0, float("inf")), (j, -float("inf"))):
+        p = s.lens[1] - s.new[1] + k
+        s.v[s.table[1][p // s.block], p % s.block, :, d - 2] = value
+        planted.append((1, k, d - 2, value))
+    want = f64(clean[0])
+    for b, n in enumerate(s.new):
+        for c in {x[2] for x in planted}:
+            sums = np.zeros(n)
+            with np.errstate(invalid="ignore"):
+                for _, j, _, value in (x for x in planted if x[0] == b and x[2] == c):
+                    sums += np.where(s.seen[b][:, j], value, 0.0)
+            hit = ~np.isfinite(sums)
+            want[s.cu[b]:s.cu[b + 1], :, c][hit] = sums[hit, None]
+    for _ in range(2):
+        o, lse = s.attend()
+        np.testing.assert_array_equal(f64(o), want)
+        assert torch.equal(lse.view(torch.int32), clean[1].view(torch.int32))
+
+
 def test_values_that_are_no_numbers_in_many_sequences():
     """Every second sequence has one, with one and two tiles of rows by turns and several sequences a CTA."""
     require_gpu()
