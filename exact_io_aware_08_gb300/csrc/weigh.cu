@@ -764,8 +764,9 @@ static cudaError_t launch_weigh_d(const WeighArgs& a, cudaStream_t stream) {
   cudaError_t e = few ? ensure_smem_attr(weigh_few_kernel<D>, C::SMEM_BYTES, few_done) : ensure_smem_attr(weigh_many_kernel<D>, C::SMEM_BYTES, many_done);
   if (e != cudaSuccess) return e;
   const long long heads = static_cast<long long>(a.n_seqs) * a.H_kv;
-  const long long items = few ? heads * ((a.max_k + 255) / 256)
-                              : heads * ((a.max_k + kWeighKeys - 1) / kWeighKeys) * ((a.max_q + p.tokens - 1) / p.tokens);
+  // (of no keys one CTA: it checks lengths and boundaries)
+  const int pieces = few ? (a.max_k + 255) / 256 : (a.max_k + kWeighKeys - 1) / kWeighKeys;
+  const long long items = heads * max(1, pieces) * (few ? 1 : (a.max_q + p.tokens - 1) / p.tokens);
   const long long grid = min(static_cast<long long>(min(paged_sm_count(), kWeighMaxCtas)), items);
   const unsigned threads = few ? C::FEW_THREADS : C::MANY_THREADS;
   log_launch(few ? "weigh_few_kernel<D>" : "weigh_many_kernel<D>", static_cast<unsigned long long>(grid), threads, static_cast<unsigned long long>(C::SMEM_BYTES));

@@ -377,6 +377,30 @@ def test_bad_sequences_are_reported_and_left(what):
             assert (f64(w)[pages] == 7).all()
 
 
+@pytest.mark.parametrize("what", ["tree", "weigh"])
+def test_a_step_over_caches_of_no_tokens(what):
+    """max_seqlen_k of 0: nothing is written where all sequences are empty, and one that is not is reported."""
+    require_gpu()
+    q, c = cuda(normal((3, 8, 64), 1)), torch.full((2, 16, 2, 64), NAN, dtype=torch.bfloat16, device="cuda")
+    o, lse = poisoned((3, 8, 64), torch.bfloat16), poisoned((8, 3), torch.float32)
+    w = torch.full((2, 2, 16), 7.0, device="cuda")
+    ws = torch.empty(max(fa.fa_fwd_paged_tree_workspace_size(8, 2, 3, 64), fa.fa_weigh_paged_workspace_size(8, 2, 3)), dtype=torch.uint8, device="cuda")
+
+    def call(cu, lens, max_k, max_q=2):
+        if what == "tree":
+            fa.fa_fwd_paged_tree(q, c, c, o, lse, None, i32(cu), i32(lens), i32([[0], [1]]), max_q, max_k, 0.125, ws)
+        else:
+            fa.fa_weigh_paged(q, lse, c, w, None, i32(cu), i32(lens), i32([[0], [1]]), max_q, max_k, 0.125, 1.0, ws)
+        fa.fa_sync_status()
+
+    call([0, 0, 0], [0, 0], 0)                                   # padding rows alone
+    for cu, lens in (([0, 2, 2], [2, 0]), ([0, 0, 0], [0, 1]), ([0, 1, 1], [0, 0])):
+        with pytest.raises(fa.FaError, match="invalid sequence boundaries"):
+            call(cu, lens, 0)
+    call([0, 0, 0], [0, 0], 0, 3)
+    assert torch.isnan(o).all() and torch.isnan(lse).all() and (w == 7).all()
+
+
 # --------------------------------------------------------------------------------------------
 # weights
 # --------------------------------------------------------------------------------------------
@@ -461,6 +485,18 @@ def test_rows_that_see_nothing_weigh_nothing():
     p = np.arange(200)
     got = f64(w)[s.table[0][p // 64], :, p % 64]
     assert (got[:196] == 0.5).all() and (got[196:] == 0).all()
+
+
+def test_weights_of_many_rows_over_caches_of_no_tokens():
+    require_gpu()
+    q, c = cuda(normal((300, 4, 128), 1)), torch.zeros((2, 16, 1, 128), dtype=torch.bfloat16, device="cuda")
+    lse, w = torch.zeros((4, 300), device="cuda"), torch.full((2, 1, 16), 7.0, device="cuda")
+    fa.weigh_paged(q, lse, c, w, i32([[0], [1]]), i32([0, 0, 0]), i32([0, 0]), 300, 0)
+    fa.fa_sync_status()
+    fa.weigh_paged(q, lse, c, w, i32([[0], [1]]), i32([0, 300, 300]), i32([300, 0]), 300, 0)
+    with pytest.raises(fa.FaError, match="invalid sequence boundaries"):
+        fa.fa_sync_status()
+    assert (w == 7).all()
 
 
 # --------------------------------------------------------------------------------------------
