@@ -712,6 +712,16 @@ fa_status_t check_step(int n_seqs, int H, int H_kv, int total, int max_seqlen_q,
   return FA_OK;
 }
 
+// An array of ints that a call has, and whether two of them share memory.
+struct Ints {
+  const int* at;
+  long long n;
+};
+bool meet(const Ints& a, const Ints& b) {
+  const auto x = reinterpret_cast<uintptr_t>(a.at), y = reinterpret_cast<uintptr_t>(b.at);
+  return a.at && b.at && a.n > 0 && b.n > 0 && x < y + 4 * static_cast<unsigned long long>(b.n) && y < x + 4 * static_cast<unsigned long long>(a.n);
+}
+
 // Pools whose rows are moved.
 fa_status_t check_pool(int n_seqs, int H_kv, int d, int max_blocks, int block_size, int num_blocks) {
   fa_status_t st = check_paged(n_seqs, 0, H_kv, d, max_blocks, block_size, num_blocks, 1);
@@ -878,7 +888,12 @@ fa_status_t fa_accept_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, int* seqlens
   if ((st = check_index_arrays(cu_seqlens, seqlens_k, block_table)) != FA_OK) return st;
   if (!aligned4(seqlens_out) || !aligned4(accepted) || !aligned4(n_accepted))
     return fail(FA_ERR_INVALID_ARG, "accepted, n_accepted and the new lengths must be 4-byte aligned");
-  if (seqlens_out == seqlens_k) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+  // (the blocks of a sequence read these while one of them writes its new length)
+  const Ints lens{seqlens_out, n_seqs};
+  for (const Ints& x : {Ints{seqlens_k, n_seqs}, Ints{n_accepted, n_seqs}, Ints{cu_seqlens, n_seqs + 1LL},
+                        Ints{accepted, static_cast<long long>(n_seqs) * max_accepted},
+                        Ints{block_table, static_cast<long long>(n_seqs) * max_blocks_per_seq}})
+    if (meet(lens, x)) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
   if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
   fa::AcceptArgs a{k_cache, v_cache, seqlens_out, accepted, n_accepted, cu_seqlens, seqlens_k, block_table,
                    n_seqs, H_kv, max_accepted, max_blocks_per_seq, block_size, num_blocks, d};
@@ -939,7 +954,13 @@ fa_status_t fa_evict_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, float* weight
   if ((st = check_index_arrays(budgets, seqlens_k, block_table)) != FA_OK) return st;
   if (!aligned4(new_table) || !aligned4(kept) || !aligned4(seqlens_out))
     return fail(FA_ERR_INVALID_ARG, "new_table, kept and the new lengths must be 4-byte aligned");
-  if (seqlens_out == seqlens_k || seqlens_out == budgets) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+  const Ints lens{seqlens_out, n_seqs}, positions{kept, static_cast<long long>(n_seqs) * H_kv * max_kept};
+  for (const Ints& x : {Ints{seqlens_k, n_seqs}, Ints{budgets, n_seqs}, Ints{block_table, static_cast<long long>(n_seqs) * max_blocks_per_seq},
+                        Ints{new_table, static_cast<long long>(n_seqs) * new_max_blocks_per_seq}}) {
+    if (meet(lens, x)) return fail(FA_ERR_INVALID_ARG, "the new lengths need an array of their own");
+    if (meet(positions, x)) return fail(FA_ERR_INVALID_ARG, "kept needs an array of its own");
+  }
+  if (meet(lens, positions)) return fail(FA_ERR_INVALID_ARG, "kept and the new lengths need arrays of their own");
   if (new_table == block_table) return fail(FA_ERR_INVALID_ARG, "the new pages need a table of their own, and must not be read from");
   if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned16(weights)) return fail(FA_ERR_INVALID_ARG, "arrays must be 16-byte aligned");
   fa::EvictArgs a{k_cache, v_cache, weights, kept, seqlens_out, budgets, seqlens_k, block_table, new_table, n_seqs, H_kv,

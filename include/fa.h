@@ -484,7 +484,7 @@ fa_status_t fa_fwd_paged_tree(const fa_bf16_t* q, const fa_bf16_t* k_cache, cons
  * fa_accept_paged -- keep the accepted ones of a step's tokens in the bf16 cache: of sequence b's n tokens of the step
  * those at accepted[b * max_accepted + i], i < n_accepted[b], which ascend, become the step's first ones (keys and
  * values of all heads move within the step's places), and seqlens_out[b] = seqlens_k[b] - n + n_accepted[b].
- * seqlens_out is not seqlens_k.  A sequence whose boundaries, path or blocks are not sound (indices that do not
+ * seqlens_out shares no memory with the arrays that are read.  A sequence whose boundaries, path or blocks are not sound (indices that do not
  * ascend or lie outside [0, n), n_accepted above n or max_accepted) is left as it is, with its length, and reported
  * by fa_sync_status.  block_size is any; n_seqs at most 65535.
  */
@@ -521,8 +521,8 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
  * weights, of equal ones those in front (a weight that is no number counts as the lowest).  Keys, values and weights of
  * what is kept go in order to the pages of new_table [n_seqs, new_max_blocks_per_seq], of the same pool; sequences
  * within their budget go there whole.  kept [n_seqs, H_kv, max_kept] gets the positions they had, ascending, and -1
- * behind them; seqlens_out[b] = min(seqlens_k[b], budgets[b]) (an array of its own).  Rotation stays: later tokens
- * are appended by fa_append_paged_at.
+ * behind them; seqlens_out[b] = min(seqlens_k[b], budgets[b]).  kept and seqlens_out share no memory with each other
+ * or with the arrays that are read.  Rotation stays: later tokens are appended by fa_append_paged_at.
  *
  * No new page may be one that a sequence of the call is read from (new_table is not block_table); pages of block_table
  * that sequences share are fine.

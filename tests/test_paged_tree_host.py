@@ -112,6 +112,33 @@ def test_evict_refuses(lib, kw, code):
     assert call(lib.fa_evict_paged, order, EVICT, kw) == code
 
 
+# Arrays of their own, far apart; every entry of the two tables below makes an output share memory with one that is read.
+APART = {x: (i + 1) << 24 for i, x in enumerate("kc vc weights out kept path n cu lens table new budgets".split())}
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=APART["lens"]), dict(out=APART["n"]), dict(out=APART["cu"]), dict(out=APART["path"]), dict(out=APART["table"]),
+    dict(out=APART["lens"] + 4), dict(out=APART["lens"] - 4), dict(out=APART["cu"] + 8), dict(out=APART["path"] + 4 * 2 * 4 - 4),
+    dict(out=APART["table"] + 4 * 2 * 8 - 4), dict(n=APART["out"] + 4), dict(cu=APART["out"] - 8),
+], ids=str)
+def test_accept_refuses_lengths_in_an_array_that_is_read(lib, kw):
+    order = "kc vc out path n cu lens table n_seqs H_kv deep max_blocks block num_blocks d"
+    assert call(lib.fa_accept_paged, order, dict(ACCEPT, **{x: APART[x] for x in order.split() if x in APART}), kw) == INVALID
+    assert b"array of their own" in lib.fa_last_error_message()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=APART["lens"]), dict(out=APART["budgets"]), dict(out=APART["table"]), dict(out=APART["new"]), dict(out=APART["kept"]),
+    dict(kept=APART["lens"]), dict(kept=APART["budgets"]), dict(kept=APART["table"]), dict(kept=APART["new"]),
+    dict(out=APART["budgets"] + 4), dict(out=APART["kept"] + 4 * 2 * 2 * 100 - 4), dict(kept=APART["out"] + 4), dict(new=APART["out"] - 4 * 2 * 2 + 4),
+    dict(lens=APART["kept"] + 4 * 2 * 2 * 100 - 8),
+], ids=str)
+def test_evict_refuses_outputs_in_an_array_that_is_read(lib, kw):
+    order = "kc vc weights kept out budgets lens table new n_seqs H_kv max_k max_kept first last max_blocks new_blocks block num_blocks d"
+    assert call(lib.fa_evict_paged, order, dict(EVICT, **{x: APART[x] for x in order.split() if x in APART}), kw) == INVALID
+    assert b"of their own" in lib.fa_last_error_message() or b"of its own" in lib.fa_last_error_message()
+
+
 def test_append_at_refuses(lib):
     def append(positions):
         return lib.fa_append_paged_at(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, positions, FAKE, FAKE, FAKE, 2, 8, 2, 4, 1024, 256, 256,
