@@ -694,17 +694,20 @@ def forward_paged_q4(q, k_codes, k_scales, v_codes, v_scales, block_table, cu_se
 
 def tree_bits(parents, cu_seqlens, max_seqlen_q: int):
     """(tree, depth) of packed drafted tokens: ``parents`` int32 [total] names each token's parent within its
-    sequence (an earlier token, or -1 for a root).  tree int32 [total, words]: a token sees itself and its
-    ancestors; depth int32 [total]: 0 for a root.  A few torch operations, on the tensors' device: for trees that
-    stay, made once."""
+    sequence, an earlier token; anything else, -1 say, makes it a root.  tree int32 [total, words]: a token sees itself
+    and its ancestors; depth int32 [total]: 0 for a root.  Rows that no sequence owns see nothing, whatever their parents
+    hold.  A few torch operations, on the tensors' device: for trees that stay, made once."""
     import torch
     n, words, dev = parents.shape[0], max(1, -(-max_seqlen_q // 32)), parents.device
     t = torch.arange(n, device=dev)
-    cu = cu_seqlens.long()
-    first = cu[torch.searchsorted(cu[1:].contiguous(), t, right=True).clamp(max=cu.numel() - 2)]
-    up = torch.cat((torch.where(parents < 0, n, first + parents.long()), cu.new_tensor([n])))    # (n: no token)
+    cu, p = cu_seqlens.long(), parents.long()
+    first = cu[torch.searchsorted(cu[1:].contiguous(), t, right=True).clamp(max=max(0, cu.numel() - 2))]
+    place = t - first
+    owned = (first >= 0) & (place >= 0) & (t < cu[-1])
+    # (an index is used only where it is sound: one out of range would end the process's use of the GPU)
+    up = torch.cat((torch.where(owned & (p >= 0) & (p < place), first + p, n), cu.new_tensor([n])))    # (n: no token)
     bits = torch.zeros((n + 1, 32 * words), dtype=torch.bool, device=dev)
-    bits[t, (t - first).clamp(max=32 * words - 1)] = True
+    bits[:n] = owned[:, None] & (place[:, None] == torch.arange(32 * words, device=dev))
     depth = torch.ones(n + 1, dtype=torch.int32, device=dev)
     depth[n] = 0
     for _ in range(max(1, max_seqlen_q).bit_length()):           # twice as many ancestors each time

@@ -179,6 +179,48 @@ def test_tree_bits(sizes):
     np.testing.assert_array_equal(depth.numpy(), np.concatenate([m.sum(1) - 1 for m in masks if len(m)]))
 
 
+@pytest.mark.parametrize("kind", ["padding", "outside", "behind", "uninitialised"])
+def test_tree_bits_of_parents_that_are_none(kind):
+    """Whatever stands in the parents, behind the last sequence's tokens too: what is no token in front of the own one, of
+    the same sequence, makes a root, and the others keep their ancestors."""
+    r = np.random.default_rng(len(kind))
+    sizes, pad = [40, 0, 7, 33], 9
+    trees = [[-1 if i == 0 else int(r.integers(0, i)) for i in range(n)] for n in sizes]
+    parents = np.array(sum(trees, []) + [-1] * pad, np.int64)
+    cu = np.concatenate(([0], np.cumsum(sizes)))
+    first = np.repeat(cu[:-1], sizes)
+    big = np.iinfo(np.int32)
+    if kind in ("padding", "uninitialised"):
+        parents[cu[-1]:] = r.choice([0, 1, 89, 1 << 30, big.max, big.min, -2], pad)
+    if kind == "outside":
+        parents[r.choice(cu[-1], 20, replace=False)] = r.choice([big.max, big.min, -7, 80, 1000, 1 << 24], 20)
+    if kind == "behind":
+        at = r.choice(cu[-1], 25, replace=False)
+        parents[at] = (at - first[at]) + r.integers(0, 30, 25)             # itself, a later one, the next sequence's
+    if kind == "uninitialised":
+        parents[:] = r.integers(big.min, big.max, len(parents))
+        parents[::3] = r.integers(-3, 90, len(parents[::3]))
+    bits, depth = fa.tree_bits(torch.tensor(parents, dtype=torch.int32), torch.tensor(cu, dtype=torch.int32), 40)
+    sound = [[p if 0 <= p < i else -1 for i, p in enumerate(parents[a:b].tolist())] for a, b in zip(cu[:-1], cu[1:])]
+    masks = [P.tree_mask(p) for p in sound]
+    np.testing.assert_array_equal(bits.numpy()[:cu[-1]], np.concatenate([P.pack_bits(m, 2) for m in masks]))
+    np.testing.assert_array_equal(depth.numpy()[:cu[-1]], np.concatenate([m.sum(1) - 1 for m in masks if len(m)]))
+    assert (bits.numpy()[cu[-1]:] == 0).all() and (depth.numpy()[cu[-1]:] == 0).all()
+
+
+def test_tree_bits_of_more_tokens_than_there_is_room_for():
+    """Tokens behind max_seqlen_q have no bits (the attention refuses their sequence); odd boundaries index nothing."""
+    parents = torch.tensor([-1, 0, 1, 2] * 12, dtype=torch.int32)
+    bits, depth = fa.tree_bits(parents, torch.tensor([0, 48], dtype=torch.int32), 32)
+    seen = P.tree_mask([p if p < i else -1 for i, p in enumerate(parents.tolist())])
+    np.testing.assert_array_equal(bits.numpy(), P.pack_bits(seen[:, :32], 1))
+    for cu in ([0, 0], [7, 48], [0, 1 << 30], [40, 9], [-5, 20], [-(1 << 20), 48], [48]):
+        bits, depth = fa.tree_bits(parents, torch.tensor(cu, dtype=torch.int32), 32)
+        assert bits.shape == (48, 1) and depth.shape == (48,)
+    bits, depth = fa.tree_bits(parents[:0], torch.tensor([0, 0], dtype=torch.int32), 0)
+    assert bits.shape == (0, 1) and depth.shape == (0,)
+
+
 def test_oracle_agrees_with_torch():
     """The oracle's masked attention, weights and eviction against other ways to say them."""
     r = np.random.default_rng(5)
