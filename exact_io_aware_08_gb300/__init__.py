@@ -705,11 +705,10 @@ def tree_bits(parents, cu_seqlens, max_seqlen_q: int):
     place = t - first
     owned = (first >= 0) & (place >= 0) & (t < cu[-1])
     # (an index is used only where it is sound: one out of range would end the process's use of the GPU)
-    up = torch.cat((torch.where(owned & (p >= 0) & (p < place), first + p, n), cu.new_tensor([n])))    # (n: no token)
+    up = torch.cat(((first + p).masked_fill(~(owned & (p >= 0) & (p < place)), n), torch.full((1,), n, device=dev)))    # (n: no token)
     bits = torch.zeros((n + 1, 32 * words), dtype=torch.bool, device=dev)
     bits[:n] = owned[:, None] & (place[:, None] == torch.arange(32 * words, device=dev))
-    depth = torch.ones(n + 1, dtype=torch.int32, device=dev)
-    depth[n] = 0
+    depth = (torch.arange(n + 1, device=dev) < n).int()
     for _ in range(max(1, max_seqlen_q).bit_length()):           # twice as many ancestors each time
         bits, depth, up = bits | bits[up], depth + depth[up], up[up]
     power = torch.ones(32, dtype=torch.int64, device=dev) << torch.arange(32, device=dev)

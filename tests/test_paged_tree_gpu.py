@@ -756,6 +756,27 @@ def test_captured_steps_with_new_contents():
             assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
 
 
+def test_masks_and_depths_on_the_device():
+    """The masks that the host's make, with padding rows of any contents, and a step captured and replayed with other trees."""
+    require_gpu()
+    r = np.random.default_rng(3)
+    sizes, pad = [26, 0, 33, 5], 6
+    cu = np.concatenate(([0], np.cumsum(sizes)))
+    parents, graph = i32(np.zeros(cu[-1] + pad)), torch.cuda.CUDAGraph()
+    cug = i32(cu)
+    fa.tree_bits(parents, cug, 33)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        held = fa.tree_bits(parents, cug, 33)
+    for _ in range(3):
+        new = np.concatenate([random_tree(r, n) for n in sizes] + [r.integers(-(1 << 31), 1 << 31, pad)])
+        parents.copy_(i32(new))
+        graph.replay()
+        want = fa.tree_bits(torch.tensor(new, dtype=torch.int32), torch.tensor(cu, dtype=torch.int32), 33)
+        for x, y, z in zip(want, held, fa.tree_bits(parents, cug, 33)):
+            assert torch.equal(x, y.cpu()) and torch.equal(x, z.cpu())
+
+
 def test_serving_with_drafts_and_a_short_cache():
     """A prompt, its weights, its eviction, a drafted tree at its true positions, the accepted path, and its weights:
     every call's result against the oracle on what the cache holds."""
