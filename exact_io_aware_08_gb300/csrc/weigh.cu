@@ -43,7 +43,7 @@ struct WeighCfg {
   // k_full[NK], k_empty[NK], q_full[NQ], q_empty[NQ], l_full[NQ], l_empty[NQ], s_full[4], s_empty[4]
   static constexpr int NBAR = 2 * NK + 4 * NQ + 8;
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
-  static constexpr int SMEM_BYTES = OFF_MISC + 32 + 1024;      // (TMEM slot, abort flag, start[5])
+  static constexpr int SMEM_BYTES = OFF_MISC + 48 + 1024;      // (TMEM slot, abort flag, start[5], out[NQ])
   static_assert(SMEM_BYTES <= 232448, "shared memory budget (227 KB per CTA)");
   static constexpr int PAIRS = NK / 2;                        // few rows: pairs of K tiles in flight
   static constexpr int FEW_THREADS = 384, MANY_THREADS = 640;
@@ -201,7 +201,7 @@ struct WeighShared {
   uint64_t *k_full, *k_empty, *q_full, *q_empty, *l_full, *l_empty, *s_full, *s_empty;
   uint32_t* tmem_slot;
   volatile int* abort_flag;
-  int* start;
+  int *start, *out;                                           // out: whether some row of a tile's lse is -inf
   __device__ __forceinline__ explicit WeighShared(uint8_t* smem) {
     k = smem + C::OFF_K;
     q = smem + C::OFF_Q;
@@ -217,6 +217,7 @@ struct WeighShared {
     tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     start = reinterpret_cast<int*>(smem + C::OFF_MISC + 8);
+    out = start + 5;
   }
   // By one thread: ``k_arrivals`` copies make a K slot full, ``sum_warps`` give lse back, four warps an S buffer.
   __device__ __forceinline__ void init(int k_arrivals, int sum_warps) const {
@@ -271,9 +272,17 @@ struct WeighLse {
       v[i] = token_of[i] < n ? __ldg(p.lse + static_cast<size_t>(hkv * p.G + head_of[i]) * p.total + s.first + qt * p.tokens + token_of[i])
                              : -INFINITY;
   }
-  __device__ __forceinline__ void write(float* to) const {    // (rows that see nothing weigh nothing)
+  // ``n``: tokens of the tile.  (Rows that see nothing weigh nothing, and ``out`` is set: -inf and a score that is no
+  // finite number would not add up to -inf.)
+  __device__ __forceinline__ void write(int n, float* to, int* out) const {
+    bool some = false;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) to[i * 32 + (threadIdx.x & 31)] = e[i] == -INFINITY ? -INFINITY : e[i] * -1.4426950408889634f;
+    for (int i = 0; i < 4; ++i) {
+      some |= token_of[i] < n && e[i] == -INFINITY;
+      to[i * 32 + (threadIdx.x & 31)] = e[i] == -INFINITY ? -INFINITY : e[i] * -1.4426950408889634f;
+    }
+    some = __any_sync(0xffffffffu, some);
+    if ((threadIdx.x & 31) == 0) *out = some;
   }
 };
 
@@ -301,10 +310,10 @@ struct WeighSpan {
   }
 };
 
-// Adds up the weights of a tile's columns, W from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e.  ``read`` is
-// called when all has been read, before the last of it is added up.
+// Adds up the weights of a tile's columns, W from tensor memory at a time up to ``cols``; ``nl``: -lse log2 e, -inf among
+// them where ``out``.  ``read`` is called when all has been read, before the last of it is added up.
 template <int W, typename F>
-__device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restrict__ nl, int cols, const WeighSpan& x, float c2, F read) {
+__device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restrict__ nl, bool out, int cols, const WeighSpan& x, float c2, F read) {
   float2 sum[W / 16];
 #pragma unroll
   for (int i = 0; i < W / 16; ++i) sum[i] = make_float2(0.f, 0.f);
@@ -321,6 +330,11 @@ __device__ __forceinline__ float weigh_tile(uint32_t t_s, const float* __restric
       read();
     }
     if (c0 + W <= x.lo_min || c0 >= x.hi) continue;
+    if (out) {                                                // (a pass of its own: 32 single tokens 62 us, a test of each weight 64)
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (nl[c0 + i] == -INFINITY) s[i / 32][i % 32] = 0u;
+    }
     if (c0 < x.lo_max || c0 + W > x.hi) {
 #pragma unroll
       for (int i = 0; i < W; ++i) {
@@ -426,7 +440,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
         const int s = qc % C::NQ, u = qc / C::NQ;
         lse.ask(x.seq, x.hkv, r, lse.e);
         if (u > 0 && !(ok = mbar_wait_warp(&m.l_empty[s], (u - 1) & 1, abort_flag, 616))) break;
-        lse.write(m.lse + s * 128);
+        lse.write(x.seq.nq - r * p.tokens, m.lse + s * 128, m.out + s);
         __syncwarp();
         if (lane == 0) mbar_arrive(&m.l_full[s]);
       }
@@ -464,7 +478,11 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
     int sc = 0;
     while (ok && walk.next(x)) {
       const int weighed = p.weighed ? __ldg(p.weighed + x.b) : x.seq.base();
-      for (int r = 0; ok && r < x.tiles; ++r) ok = mbar_wait_warp(&m.l_full[(qc + r) % C::NQ], ((qc + r) / C::NQ) & 1, abort_flag, 630);
+      uint32_t out = 0;                                       // by row tile
+      for (int r = 0; ok && r < x.tiles; ++r) {
+        ok = mbar_wait_warp(&m.l_full[(qc + r) % C::NQ], ((qc + r) / C::NQ) & 1, abort_flag, 630);
+        out |= static_cast<uint32_t>(m.out[(qc + r) % C::NQ]) << r;
+      }
       for (int kt = x.kt0; ok && kt < x.kt1; ++kt) {
         const int key = kt * 256 + a * 128 + sub * 32 + lane;
         float* at = key < x.seq.len ? weigh_place(p, x.b, x.hkv, key) : nullptr;
@@ -482,7 +500,8 @@ __global__ void __launch_bounds__(WeighCfg<D>::FEW_THREADS, 1) weigh_few_kernel(
           };
           // (64 columns at a time where there are as many: 16 x 64 tokens over 8000 87 us with 32, 82 with 64, 140 with 128;
           // 32 single tokens, four columns, 62 with 32 and 68 with 64)
-          sum += cols > 32 ? weigh_tile<64>(t_lane + buf * 128, nl, cols, span, p.c2, read) : weigh_tile<32>(t_lane + buf * 128, nl, cols, span, p.c2, read);
+          sum += cols > 32 ? weigh_tile<64>(t_lane + buf * 128, nl, out >> r & 1u, cols, span, p.c2, read) 
+                            : weigh_tile<32>(t_lane + buf * 128, nl, out >> r & 1u, cols, span, p.c2, read);
         }
         if (at && ok) *at = old + sum;
       }
@@ -590,7 +609,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
         float next[4] = {0.f, 0.f, 0.f, 0.f};
         if (qt + 1 < x.q1) lse.ask(x.seq, x.hkv, qt + 1, next);
         if (u > 0 && !(ok = mbar_wait_warp(&m.l_empty[s], (u - 1) & 1, abort_flag, 616))) break;
-        lse.write(m.lse + s * 128);
+        lse.write(x.seq.nq - qt * p.tokens, m.lse + s * 128, m.out + s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) lse.e[i] = next[i];
         __syncwarp();
@@ -662,7 +681,7 @@ __global__ void __launch_bounds__(WeighCfg<D>::MANY_THREADS, 1) weigh_many_kerne
           }
           tc_fence_after();
           const int r0 = qt * p.tokens * p.G, rows = min(p.tokens, x.seq.nq - qt * p.tokens) * p.G;
-          sum += weigh_tile<32>(t_s, m.lse + (qc % C::NQ) * 128, cols, WeighSpan(p, x.seq, key, r0, rows), p.c2,
+          sum += weigh_tile<32>(t_s, m.lse + (qc % C::NQ) * 128, m.out[qc % C::NQ], cols, WeighSpan(p, x.seq, key, r0, rows), p.c2,
                             [&] { named_bar_arrive(C::BAR_S + a, C::BAR_S_THREADS); });
         } else {
           ok = ok && mbar_wait_warp(&m.l_full[qc % C::NQ], (qc / C::NQ) & 1, abort_flag, 632);

@@ -499,6 +499,44 @@ def test_weights_of_many_rows_over_caches_of_no_tokens():
     assert (w == 7).all()
 
 
+@pytest.mark.parametrize("case", [
+    ([1, 3], [300, 257], 8, 2, 128, 64), ([40, 90], [40, 1090], 4, 1, 64, 16), ([9, 31], [700, 231], 12, 4, 128, 48),     # few rows
+    ([300, 1, 520], [300, 900, 1520], 4, 2, 128, 64), ([700], [700], 5, 1, 64, 32), ([530], [531], 2, 2, 128, 16),         # many
+], ids=lambda c: f"{sum(c[0])}tok_H{c[2]}x{c[3]}")
+@pytest.mark.parametrize("what", ["queries", "keys"])
+def test_rows_that_see_nothing_weigh_nothing_whatever_they_hold(case, what):
+    """An lse of -inf takes a row out, also where its queries, or keys that it would meet, are no finite numbers; the
+    other rows' weights are those of a step with finite numbers there, bit for bit."""
+    require_gpu()
+    s = Step(*case, None)
+    r = np.random.default_rng(s.total)
+    q, k, v, table, cu, lens = s.gpu()
+    lse = torch.tensor(r.normal(size=(s.H, s.total)) + 3, dtype=torch.float32, device="cuda")
+    out = torch.tensor(r.random((s.total, s.H)) < (0.3 if s.total > 20 else 0.5), device="cuda")
+    out[0, 0], out[-1, -1] = True, True
+    if what == "keys":                                           # of the last token: its own row alone would see it
+        out[s.cu[1:] - 1] = True
+    lse[out.T] = -float("inf")
+
+    def weights(q, k):
+        w = torch.full((s.nb, s.H_kv, s.block), 0.5, device="cuda")
+        fa.weigh_paged(q, lse, k, w, table, cu, lens, s.max_q, s.max_k)
+        fa.fa_sync_status()
+        return w
+
+    want = weights(q, k)
+    assert torch.isfinite(want).all()
+    for value in (NAN, float("inf"), -float("inf")):
+        q2, k2 = q.clone(), k.clone()
+        if what == "queries":
+            q2[out] = value
+        else:
+            for b, m in enumerate(s.lens):
+                k2[int(s.table[b][(m - 1) // s.block]), (m - 1) % s.block] = value
+        got = weights(q2, k2)
+        assert torch.equal(got.view(torch.int32), want.view(torch.int32))
+
+
 # --------------------------------------------------------------------------------------------
 # eviction, accepted paths
 # --------------------------------------------------------------------------------------------
