@@ -46,10 +46,9 @@ __device__ __forceinline__ int evict_count(const EvictParams& p, int b, int* len
   return bad ? -1 : n;
 }
 
-// Order of weights as unsigned numbers; one that is no number is the lowest.
+// Order of weights as unsigned numbers, from 1 on; one that is no number counts as -inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0u;
-  const uint32_t u = __float_as_uint(w + 0.f);                // (-0 + 0 = 0)
+  const uint32_t u = __float_as_uint((w != w ? -INFINITY : w) + 0.f);   // (-0 + 0 = 0)
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 

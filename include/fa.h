@@ -518,7 +518,7 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
 /*
  * fa_evict_paged -- cut sequences of the bf16 cache down to budgets[b] tokens, by weight.  Of a sequence with more, each
  * key head keeps the first keep_first, the last keep_last, and of those between them the ones with the largest
- * weights, of equal ones those in front (a weight that is no number counts as the lowest).  Keys, values and weights of
+ * weights, of equal ones those in front (a weight that is no number counts as -inf).  Keys, values and weights of
  * what is kept go in order to the pages of new_table [n_seqs, new_max_blocks_per_seq], of the same pool; sequences
  * within their budget go there whole.  kept [n_seqs, H_kv, max_kept] gets the positions they had, ascending, and -1
  * behind them; seqlens_out[b] = min(seqlens_k[b], budgets[b]).  kept and seqlens_out share no memory with each other

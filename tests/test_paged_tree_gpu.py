@@ -619,6 +619,21 @@ def test_bad_evictions_are_reported_and_left():
     fa.fa_sync_status()
 
 
+def test_weights_that_are_no_numbers_rank_with_the_lowest():
+    """NaN counts as -inf: of equal ones the front stays, in either order, on chip and beyond it."""
+    require_gpu()
+    r = np.random.default_rng(8)
+    for n, budget in ((200, 70), (200, 199), (60000, 20000)):
+        nb, both = make_pages([n, budget], 64, 0, n)
+        table, new = both[:1], both[1:, :-(-budget // 64)]
+        w = r.choice([NAN, -np.inf, 1.0], (nb, 1, 64), p=[0.4, 0.4, 0.2]).astype(np.float32)
+        c = torch.zeros((nb, 64, 1, 64), dtype=torch.bfloat16, device="cuda")
+        kept, _ = fa.evict_paged(c, c.clone(), torch.tensor(w, device="cuda"), i32(table), i32(new), i32([n]), i32([budget]), n, budget, keep_last=3)
+        fa.fa_sync_status()
+        p = np.arange(n)
+        np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), P.evict(w[table[0][p // 64], 0, p % 64], budget, 0, 3))
+
+
 def test_accept():
     require_gpu()
     new = [26, 1, 0, 7, 100, 5]
