@@ -528,7 +528,8 @@ fa_status_t fa_weigh_paged(const fa_bf16_t* q, const float* lse, const fa_bf16_t
  * that sequences share are fine.
  * Device-side checks (fa_sync_status): a length outside [0, max_seqlen_k], a budget below 0, min(seqlens_k[b],
  * budgets[b]) above max_kept, or a budget below keep_first + keep_last of a sequence that exceeds it leave the
- * sequence as it is, with its length and a kept of -1; a block id outside [0, num_blocks) leaves out its tokens.
+ * sequence as it is, with its length and a kept of -1; tokens of a block id outside [0, num_blocks) rank behind all
+ * others, and are not copied where they are kept all the same, nor is what would go to such a block.
  * block_size is any; n_seqs at most 65535.
  */
 fa_status_t fa_evict_paged(fa_bf16_t* k_cache, fa_bf16_t* v_cache, float* weights, int* kept, int* seqlens_out,

@@ -634,6 +634,48 @@ def test_weights_that_are_no_numbers_rank_with_the_lowest():
         np.testing.assert_array_equal(kept[0, 0].cpu().numpy(), P.evict(w[table[0][p // 64], 0, p % 64], budget, 0, 3))
 
 
+def test_evictions_without_a_block_leave_out_its_tokens():
+    """Tokens of a block that is not there rank behind all others and are not copied, nor is what would go to one; what is
+    sound is moved, and nothing else changes."""
+    require_gpu()
+    lens, budgets, block, H_kv = [150, 40, 130], [60, 40, 100], 16, 2
+    r = np.random.default_rng(4)
+    nb, both = make_pages(lens + budgets, block, 3, 5)
+    table, new = both[:3].copy(), both[3:, :7].copy()
+    k, v = pool(nb, block, H_kv, 64, 6)
+    w = r.normal(size=(nb, H_kv, block)).astype(np.float32)
+    w[table[0][5]] = -np.inf                             # the lowest of those that have a block
+    gone = {0: [2, 9], 1: [1], 2: [0, 1, 2, 3]}          # more than sequence 2 drops: some of them are kept in name
+    for b, blocks in gone.items():
+        table[b, blocks] = [nb, -1, nb + 7, -9][:len(blocks)]
+    new[0, 1], new[2, 6] = -5, nb
+    kg, vg, wg = cuda(k), cuda(v), torch.tensor(w, device="cuda")
+    kept, out = fa.evict_paged(kg.view(torch.bfloat16), vg.view(torch.bfloat16), wg, i32(table), i32(new), i32(lens), i32(budgets), 150, 100,
+                               keep_first=3, keep_last=4)
+    with pytest.raises(fa.FaError, match="invalid"):
+        fa.fa_sync_status()
+    assert out.tolist() == budgets
+    kept, kw, vw, ww = kept.cpu().numpy(), k.numpy().copy(), v.numpy().copy(), w.copy()
+    for b, n in enumerate(lens):
+        p = np.arange(n)
+        there = (table[b][p // block] >= 0) & (table[b][p // block] < nb)
+        for h in range(H_kv):
+            # ranks in place of weights: 0 for tokens without a block, then the weights' order
+            own = np.where(there, w[np.where(there, table[b][p // block], 0), h, p % block], 0)
+            levels = np.unique(own[there])
+            want = np.array(P.evict(np.where(there, 1.0 + np.searchsorted(levels, own), 0.0), budgets[b], 3, 4), int)
+            np.testing.assert_array_equal(kept[b, h], np.concatenate((want, np.full(100 - len(want), -1))))
+            for i, j in enumerate(want):
+                to = new[b][i // block]
+                if there[j] and 0 <= to < nb:
+                    kw[to, i % block, h], vw[to, i % block, h] = k.numpy()[table[b][j // block], j % block, h], v.numpy()[table[b][j // block], j % block, h]
+                    ww[to, h, i % block] = w[table[b][j // block], h, j % block]
+    assert (kept[2, :, :100] // block == 1).any()     # (tokens without a block that are kept in name)
+    np.testing.assert_array_equal(kg.cpu().numpy(), kw)
+    np.testing.assert_array_equal(vg.cpu().numpy(), vw)
+    np.testing.assert_array_equal(wg.cpu().numpy().view(np.int32), ww.view(np.int32))
+
+
 def test_accept():
     require_gpu()
     new = [26, 1, 0, 7, 100, 5]
