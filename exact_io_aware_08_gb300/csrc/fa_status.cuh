@@ -3,8 +3,9 @@
 // and clears the word in fa_sync_status().
 //
 // The library is built without relocatable device code, so every translation unit that
-// launches kernels owns its own status word; FA_DEFINE_STATUS_FETCH gives each one a host
-// accessor that fa_sync_status() calls in turn.
+// launches kernels owns its own status word; FA_DEFINE_STATUS_FETCH gives each one host
+// accessors: where the word is, so that fa_sync_status() looks at all of them in one go, and
+// what it holds, for the units in turn once one of them has something to say.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -25,6 +26,7 @@ __device__ __forceinline__ void report_device_error(unsigned int code, int where
 
 // Host accessor: copy this TU's status word out (after synchronising ``stream``) and clear it.  Each copy is
 // a round trip to the device (some 9 us), so that a clean word, the usual one, is all that is read.
+// NAME_word: the word's address.
 #define FA_DEFINE_STATUS_FETCH(NAME)                                                         \
   namespace fa {                                                                             \
   cudaError_t NAME(cudaStream_t stream, unsigned int* code, int* where) {                    \
@@ -36,5 +38,11 @@ __device__ __forceinline__ void report_device_error(unsigned int code, int where
     if (e != cudaSuccess) return e;                                                          \
     const unsigned int zero = 0;                                                             \
     return cudaMemcpyToSymbol(g_dev_status, &zero, sizeof(unsigned int));                    \
+  }                                                                                          \
+  cudaError_t NAME##_word(const unsigned int** at) {                                         \
+    void* p = nullptr;                                                                       \
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_dev_status);                            \
+    *at = static_cast<const unsigned int*>(p);                                               \
+    return e;                                                                                \
   }                                                                                          \
   }

@@ -192,3 +192,15 @@ def test_a_clean_status_is_one_read_a_unit():
     body = text[text.index("#define FA_DEFINE_STATUS_FETCH"):]
     clean = body[:body.index("!*code) return e;")]
     assert clean.count("cudaMemcpyFromSymbol") == 1 and body.count("cudaMemcpyFromSymbol") == 2
+
+
+def test_every_unit_with_a_status_is_asked():
+    """A unit that launches kernels defines its status word once, and the list of what is asked names them all."""
+    import glob
+    import re
+    defined = [n for p in glob.glob(os.path.join(fabuild.CSRC, "*.cu")) for n in re.findall(r"^FA_DEFINE_STATUS_FETCH\((\w+)\)", open(p).read(), re.M)]
+    text = open(os.path.join(fabuild.CSRC, "fa_kernels.h")).read()
+    body = text[text.index("#define FA_STATUS_UNITS(X)"):text.index("#define FA_DECLARE_STATUS")]
+    assert sorted(defined) == sorted(re.findall(r"X\((status_fetch_\w+)\)", body)) and len(set(defined)) == len(defined)
+    reports = [p for p in glob.glob(os.path.join(fabuild.CSRC, "*.cu")) if "report_device_error" in open(p).read() or "mbar_wait" in open(p).read()]
+    assert len(reports) <= len(defined)

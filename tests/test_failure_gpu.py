@@ -1,5 +1,7 @@
 """Failure detection on the GPU without a fault: a bounded pipeline wait that can never complete
 times out, is reported by fa_sync_status, is cleared, and the context keeps computing correctly."""
+import time
+
 import pytest
 import torch
 
@@ -39,6 +41,26 @@ def test_timeout_on_a_side_stream_is_seen_by_sync_status_of_that_stream():
         fa.fa_sync_status(stream=s)
     assert e.value.status == TIMEOUT
     fa.fa_sync_status(stream=s)
+
+
+def test_a_clean_status_takes_few_round_trips():
+    """fa_sync_status does not make a round trip to the device for each part of the library."""
+    require_gpu()
+    x, y = torch.zeros(1, device="cuda"), torch.zeros(1)
+
+    def median(f):
+        times = []
+        for _ in range(60):
+            t = time.perf_counter()
+            f()
+            times.append(time.perf_counter() - t)
+        return sorted(times)[30]
+
+    fa.fa_sync_status()
+    trip = median(lambda: y.copy_(x))                    # a synchronous copy from the device
+    status = median(fa.fa_sync_status)
+    print(f"fa_sync_status {status * 1e6:.1f} us, a copy {trip * 1e6:.1f} us")
+    assert status < 4 * trip
 
 
 def test_fa_log_writes_one_line_per_launch():
