@@ -200,6 +200,7 @@ __device__ __forceinline__ void q4_softmax_tile(uint32_t t_s, uint32_t t_o, int 
       l *= alpha;
       m = cand;
     }
+    __syncwarp();                             // (tensor memory is accessed by the whole warp at once)
     // s c2 - m c2 + 7 is off by the rounding of 7 - m c2: where that could matter the reference is taken off
     // the scores first
     far = __any_sync(0xffffffffu, fabsf(m * c2) > 4096.f && m != -INFINITY);
@@ -283,6 +284,7 @@ __device__ __forceinline__ void q4_store_row(const Q4TParams& p, uint32_t t_o, b
         }
       }
     }
+    __syncwarp();
   }
   if (has) {
     if (dst)

@@ -585,6 +585,7 @@ bwd_main_kernel(const __grid_constant__ BwdParams p) {
               *reinterpret_cast<uint4*>(dst + (col >> 6) * C::KV_CHUNK + sw128_offset(r, col & 63)) = v4;
             }
           }
+          if constexpr (VL) __syncwarp();      // (tensor memory is read by the whole warp at once)
         }
       }
       fence_proxy_async_smem();
@@ -1202,6 +1203,7 @@ bwd_persistent_kernel64(const __grid_constant__ BwdParams p) {
             for (int u = 0; u < 4; ++u)
               dst[cc * 4 + u] = make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
           }
+          __syncwarp();                        // (tensor memory is read by the whole warp at once)
         }
       }
     };

@@ -682,6 +682,7 @@ fwd_kernel(const __grid_constant__ FwdParams p) {
           lb *= alpha;
           m = cand;
         }
+        __syncwarp();                          // (tensor memory is accessed by the whole warp at once)
         if (j > 0) {
           // O_t is settled: PV_t(j-1) completed before S_t(j) (same issuing thread, in order).
 #pragma unroll
@@ -815,6 +816,7 @@ fwd_kernel(const __grid_constant__ FwdParams p) {
             *reinterpret_cast<uint4*>(stage + (col >> 6) * C::CHUNK + sw128_offset(row, col & 63)) = v4;
           }
         }
+        if constexpr (VL) __syncwarp();
       }
       if (q_idx < n_q) {
         const size_t li = VL ? static_cast<size_t>(head) * p.total_q + q_beg + q_idx
@@ -1175,6 +1177,7 @@ fwd_persistent_kernel(const __grid_constant__ FwdParams p) {
             lb *= alpha;
             m = cand;
           }
+          __syncwarp();
           if (j > 0) {                          // O_t settled: PV_t(j-1) preceded S_t(j)
 #pragma unroll
             for (int kk = 0; kk < C::DO / 16; ++kk) {  // 16 columns at a time (s[] is live here)
