@@ -10,14 +10,15 @@
 //
 // What bounds it: the copy is bound by HBM (16 sequences of 10000 to 16384 tokens, 8 heads of 128, 1024 to 4096 of them
 // kept: 61 us for about 330 MB read and written); the selection, 4 bytes a token, by latencies: four passes over the keys
-// (from shared memory, up to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 25 for 16384).  Counts
+// (from shared memory, up to kHeld of them), each with a scan of 256 counts (12 us for 4160 tokens, 22 for 16384).  Counts
 // of each lane's own, or three passes of 11, 11 and 10 bits with equal digits of a warp counted together, were no faster,
 // and choosing in every block that copies, without the list between them, was slower as a whole (123 us for that batch,
-// 91 with the list at the time).
+// 91 with the list at the time).  Candidates beyond kHeld are looked up again in every pass, through the table: 131072
+// tokens of 8 heads 448 us, of which 8192 are kept (32768 tokens: 44).
 //
 // Accept.  Rows move down: token i of the path, at place a_i >= i of the step's, comes to place i.  A thread takes 16
 // bytes of every row of a sequence, in ascending order, so that what it overwrites it has read.  It is bound by the chain
-// of path, page and row: 4 trees of 26 tokens 3.7 us, 128 of 64 5.7.
+// of path, page and row: 4 trees of 26 tokens 3.7 us, with flushed caches 4.9; 128 of 64 5.7 and 7.1.
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
 
@@ -27,12 +28,11 @@ constexpr int kSelectThreads = 1024;
 constexpr int kHeld = 48 * 1024;                              // keys held in shared memory
 
 struct EvictParams {
-  const uint16_t *k, *v;
-  uint16_t *k_out, *v_out;
+  uint16_t *k, *v;
   float* weights;
   int *kept, *seqlens_out;
   const int *budgets, *seqlens, *table, *new_table;
-  int H_kv, max_k, max_kept, keep_first, keep_last, max_blocks, new_max_blocks, block_size, num_blocks, n_seqs;
+  int H_kv, max_k, max_kept, keep_first, keep_last, max_blocks, new_max_blocks, block_size, num_blocks;
   int held;                                                   // keys that fit
 };
 
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     want -= digit[1];
   }
   // ``want`` of those at the border stay, the first ones.  A thread takes consecutive candidates, an odd number of them
-  // (an even one met in few banks of shared memory: 32768 tokens 65 us, this way 40).
+  // (an even one met in few banks of shared memory: 32768 tokens 65 us, this way 38).
   for (int i = threadIdx.x; i < p.keep_first; i += kSelectThreads) kept[i] = i;
   for (int i = threadIdx.x; i < p.keep_last; i += kSelectThreads) kept[n - p.keep_last + i] = len - p.keep_last + i;
   if (k == 0) return;
@@ -204,20 +204,18 @@ __global__ void __launch_bounds__(kCopyThreads) evict_copy_kernel(const EvictPar
 #pragma unroll
   for (int j = 0; j < U; ++j)
     if (ok[j]) {
-      reinterpret_cast<uint4*>(p.k_out + (to[j] * p.H_kv + h) * D)[u] = x[j];
-      reinterpret_cast<uint4*>(p.v_out + (to[j] * p.H_kv + h) * D)[u] = y[j];
+      reinterpret_cast<uint4*>(p.k + (to[j] * p.H_kv + h) * D)[u] = x[j];
+      reinterpret_cast<uint4*>(p.v + (to[j] * p.H_kv + h) * D)[u] = y[j];
     }
 }
 
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   EvictParams p{};
-  p.k = static_cast<const uint16_t*>(a.k_cache); p.v = static_cast<const uint16_t*>(a.v_cache);
-  p.k_out = static_cast<uint16_t*>(a.k_cache); p.v_out = static_cast<uint16_t*>(a.v_cache);
+  p.k = static_cast<uint16_t*>(a.k_cache); p.v = static_cast<uint16_t*>(a.v_cache);
   p.weights = a.weights; p.kept = a.kept; p.seqlens_out = a.seqlens_out;
   p.budgets = a.budgets; p.seqlens = a.seqlens; p.table = a.block_table; p.new_table = a.new_table;
   p.H_kv = a.H_kv; p.max_k = a.max_k; p.max_kept = a.max_kept; p.keep_first = a.keep_first; p.keep_last = a.keep_last;
   p.max_blocks = a.max_blocks; p.new_max_blocks = a.new_max_blocks; p.block_size = a.block_size; p.num_blocks = a.num_blocks;
-  p.n_seqs = a.n_seqs;
   p.held = min(a.max_k, kHeld);
   static int attr_done[64] = {0};
   cudaError_t e = ensure_smem_attr(evict_select_kernel, kHeld * 4, attr_done);
