@@ -31,9 +31,13 @@
 // many rounds as all CTAs can; the key steps of the rest are shared out equally (4 x 512 tokens over 16384 keys, 256 row
 // blocks: 451 us in two rounds).
 //
-// Measured, d = 128: 16 single tokens over 32768 keys, 32 heads over 4, 180 us (6.0 TB/s; the fastest CTA has its equal
-// share done after 142); 16 trees of 1 to 60 tokens over 500 to 8188, 32 over 8, 85; 4 x 512 tokens over 16384 385 (1.4
-// PFLOP/s); one tree of 8 over 1000 13.
+// Measured, d = 128, caches flushed before each call: 16 single tokens over 32768 keys, 32 heads over 4, 180 us (6.0 TB/s;
+// the fastest CTA has its equal share done after 142); 16 trees of 1 to 60 tokens over 500 to 8188, 32 over 8, 84; 4 x 512
+// tokens over 16384 407 (1.33 PFLOP/s; not flushed 388); one tree of 8 over 1000 12.3.
+//
+// A sequence of more than two row tiles beside short ones: row blocks are counted for the longest, and the only one that a
+// single token has falls to the same few CTAs and is not cut (63 single tokens and 512 in one call, all over 8192 keys: 1.4
+// ms, the single tokens alone 0.35; 64 single tokens with max_seqlen_q of 512: 1.3).  Two calls are the faster way.
 //
 // Short calls are bound by latencies, of fetching instructions among them (a first pass over unrolled code that
 // streamed caches have driven out of L2 takes microseconds): the rarer paths are loops.

@@ -16,15 +16,15 @@
 //   warp 1       issues the products.
 //   warps 4 on   the sums, thread = key.
 // Few rows (up to three tiles of them): Q stays, each CTA gets an equal share of all keys (Q4Share), 256 at a time with two
-// S buffers for each half.  (By the kernel for many rows: two tiles, 32 x 64 tokens over 500 keys 31 us, this way 23; three,
-// 4 x 90 over 1000 18 and 15, but 16 x 96 over 8000 both 110.)  Else a CTA keeps 512 keys and runs over the rows that see
-// them, four tiles of keys by turns, so that a tile of Q is brought for 512 keys and the sums of one key tile run beside
+// S buffers for each half.  (By the kernel for many rows, caches not flushed: two tiles, 32 x 64 tokens over 500 keys 31 us,
+// this way 23; three, 4 x 90 over 1000 18 and 15, but 16 x 96 over 8000 both 110.)  Else a CTA keeps 512 keys and runs over
+// the rows that see them, four tiles of keys by turns, so that a tile of Q is brought for 512 keys and the sums of one key tile run beside
 // the products of the others.  The (512 keys, row tile) units are shared out equally too; the sums of 512 keys that lie in
 // several shares are added up, in order, by a second kernel.  (2 x 4096 tokens in whole ranges of row tiles, dealt out in
 // rounds: 152 us.)
 //
-// Measured, 32 heads over 8, d = 128: 32 single tokens over 100 to 8191 61 us (5.5 TB/s of keys and weights), 16 x 64
-// tokens over 8000 82, 2 prompts of 4096 115 (1.2 PFLOP/s; 95 without the sums).
+// Measured, 32 heads over 8, d = 128, caches flushed before each call: 32 single tokens over 100 to 8191 62 us (5.4 TB/s of
+// keys and weights), 16 x 64 tokens over 8000 88, 2 prompts of 4096 121 (1.13 PFLOP/s; without the sums 95).
 #include "fa_kernels.h"
 #include "paged_tile.cuh"
 
